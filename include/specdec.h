@@ -91,6 +91,7 @@ extern "C" {
 #define SPECDEC_ROW_BAD_TREE 16  /* parent[0] != -1, parent[n] not in [0, n), or depth > max_depth */
 #define SPECDEC_ROW_INTERNAL 32  /* a kernel's bounded wait ran out: for a copy of its own, or (tree walk)
                                     for another CTA of the request's cluster */
+#define SPECDEC_ROW_BAD_CACHE 64 /* a cache length, token count or block id out of range */
 
 /* Limits. */
 #define SPECDEC_MAX_GAMMA 32       /* linear: drafted positions per request */
@@ -424,6 +425,152 @@ int specdec_row_alpha(const void *logits, const void *q, int dtype, const float 
 int specdec_philox_uniforms(const uint64_t *key, const uint64_t *counter,
                             unsigned long long first_word, long long n, float *out,
                             void *stream);
+
+/*
+ * The attention side of the step.  The target's logits over the drafted
+ * positions ("Chapter 15: Decoding acceleration", section 15.1.2 step 2, the
+ * parallel verification pass) come from a forward pass of the drafted tokens
+ * over the request's cached tokens.  Three calls cover what that pass needs
+ * beside dense products: rotary positions, attention of a drafted chain or
+ * tree over an 8-bit cache, and the append of the accepted tokens once
+ * specdec_verify_linear / specdec_verify_tree has named them.  Drafted tokens
+ * enter the cache only after they were accepted, so a rejection undoes nothing.
+ *
+ * One request's pass takes N tokens: node 0 is its last emitted token, the
+ * others are the drafted ones (N = gamma + 1 in the linear form).
+ *
+ * The cache is paged and held in 8 bits: e4m3 codes (1 sign, 4 exponent, 3
+ * fraction bits; 448 the largest value, no infinities) with one float32 scale
+ * for each block of tokens and head, of k and of v; value = code * scale.
+ * Token j of request b is slot j % block of block block_table[b, j / block].
+ * Table entries past the request's length are not read.  The arrays are
+ * device memory; the struct is host memory, read before the call returns.
+ * Scales are finite and >= 0; any such value is read, the append writes powers
+ * of two.  Blocks may be shared by requests that only read them.
+ */
+typedef struct specdec_kv_cache {
+  void *k, *v;                 /* e4m3 [n_blocks, Hkv, block, D], 16-byte aligned */
+  float *k_scale, *v_scale;    /* [n_blocks, Hkv] */
+  const int32_t *block_table;  /* [B, max_blocks] */
+  const int32_t *length;       /* [B] tokens held, 0 .. max_blocks * block */
+  int n_blocks, max_blocks;
+  int block;                   /* tokens a block: a multiple of 16, <= SPECDEC_MAX_KV_BLOCK */
+  int Hkv, D;                  /* heads, and elements a head: a multiple of 16, <= SPECDEC_MAX_HEAD_DIM */
+} specdec_kv_cache;
+
+#define SPECDEC_MAX_KV_BLOCK 1024
+#define SPECDEC_MAX_HEAD_DIM 256
+#define SPECDEC_MAX_HEADS 1024      /* query heads */
+
+/*
+ * Rotary positions of q and k, out of place or in place.
+ *
+ * For a token at position p, pair i < rot/2 of every head turns by the angle
+ * a = 2 pi p freq[i] / 2^64: freq[i] is the pair's frequency in units of
+ * 2^-64 turns a position, so that p * freq[i] mod 2^64 is the exact phase at
+ * any position (frequencies scaled for long contexts are put into freq).
+ *     y1 = magnitude * (x1 cos a - x2 sin a)
+ *     y2 = magnitude * (x2 cos a + x1 sin a)
+ * Pair i is elements (i, i + rot/2), or (2i, 2i + 1) with
+ * SPECDEC_ROPE_INTERLEAVED; elements rot .. D-1 are copied.  The gradient of
+ * the map (its transpose) is the same call with SPECDEC_ROPE_BACKWARD: dy in,
+ * dx out.
+ *
+ *   q, k          [B, N, Hq, D] and [B, N, Hk, D], float32 or bfloat16 (dtype);
+ *                 consecutive tokens q_stride / k_stride elements apart (slices
+ *                 of a fused projection), heads and elements contiguous.
+ *                 k may be NULL with Hk = 0
+ *   freq          uint64 [rot/2]; rot even, 2 <= rot <= D
+ *   positions     int32 [B, N], or NULL: base[b] + depth of node n
+ *   base          int32 [B] or NULL (0); only without positions
+ *   parent        int32 [B, N] (as in specdec_verify_tree) or NULL: a chain,
+ *                 depth n; only without positions.  A parent index that is not
+ *                 below its node ends the walk up, as the root does
+ *   q_out, k_out  [B, N, Hq, D] and [B, N, Hk, D], contiguous; may be q and k
+ *                 themselves where those are contiguous, must not overlap them
+ *                 otherwise
+ * Limits: D <= SPECDEC_MAX_HEAD_DIM, Hq + Hk <= 2 * SPECDEC_MAX_HEADS.
+ * B = 0 and N = 0 are no-ops.
+ */
+#define SPECDEC_ROPE_INTERLEAVED 1u
+#define SPECDEC_ROPE_BACKWARD 2u
+int specdec_rope(const void *q, const void *k, int dtype, long long q_stride, long long k_stride,
+                 const uint64_t *freq, const int32_t *positions, const int32_t *base,
+                 const int32_t *parent, int B, int N, int Hq, int Hk, int D, int rot,
+                 unsigned flags, float magnitude, void *q_out, void *k_out, void *stream);
+
+/*
+ * Append tokens to the cache.
+ *
+ * Request b appends n = (count ? count[b] : N) + extra tokens: nodes
+ * path[b, 0 .. n-1], or nodes 0 .. n-1 without a path.  After a verify step:
+ * count = its n_accepted, extra = 1 (node 0 is the token before the drafts),
+ * path = its path_nodes in the tree form.
+ * Each block of tokens and head is scaled by the smallest power of two s
+ * (2^-100 at least) with |x| <= 448 s over its new finite values, or by the
+ * block's present scale where tokens stand before them and that is larger;
+ * codes are round-to-nearest-even of x / s.  Where a block's scale grows, the
+ * codes of the tokens before are rounded anew (a power-of-two scale loses only
+ * bits below the new smallest step, 2^-9 s).  Non-finite values are stored as
+ * NaN codes.
+ *
+ *   k, v        [B, N, Hkv, D] float32 or bfloat16, tokens k_stride / v_stride
+ *               elements apart
+ *   count       int32 [B] or NULL
+ *   path        int32 [B, path_len] or NULL
+ *   cache       codes and scales are updated; block_table holds the blocks that
+ *               the new tokens go to, which no other request may share.
+ *               length is read, not written
+ *   new_length  int32 [B]: length + n.  Not cache->length itself
+ *   row_status  int32 [B]: SPECDEC_ROW_BAD_CACHE for a length, n or block id out
+ *               of range (n in [0, N], at most path_len with a path),
+ *               SPECDEC_ROW_BAD_TREE for a path node outside [0, N).  Such a
+ *               request appends nothing and new_length is its length
+ * The call may run twice on the same state with the same result.
+ */
+int specdec_kv_append(const void *k, const void *v, int dtype, long long k_stride,
+                      long long v_stride, const int32_t *count, int extra, const int32_t *path,
+                      int path_len, const specdec_kv_cache *cache, int B, int N,
+                      int32_t *new_length, int32_t *row_status, void *stream);
+
+/*
+ * Attention of N drafted tokens over their request's cached tokens and over
+ * one another.
+ *
+ * Node n of request b stands at position length[b] + depth(n) and sees every
+ * cached token, its ancestors and itself (a chain without parent: nodes 0 ..
+ * n), less those `window` or more positions before it (window = 0: no limit).
+ * With G = Hq / Hkv, query head h reads head h / G of k and v:
+ *     s = scale * q . k;   softcap > 0:  s = softcap * tanh(s / softcap)
+ *     s -= slopes[h] * (position of n - position of the token)      (slopes given)
+ *     out = sum softmax(s) v,   lse = ln sum exp(s)
+ * Masked tokens have no influence whatever they hold.  A node that sees
+ * nothing, or only scores of -infinity, gets out = 0 and lse = -infinity.
+ *
+ *   q             [B, N, Hq, D]; k_new, v_new [B, N, Hkv, D], float32 or bfloat16
+ *                 (dtype), consecutive tokens *_stride elements apart
+ *   parent        int32 [B, N] as in specdec_verify_tree, or NULL: a chain
+ *   n_nodes       int32 [B] in [0, N] or NULL (N): nodes past it see nothing and
+ *                 nothing sees them; their q, k_new, v_new are not read
+ *   slopes        float32 [Hq] or NULL
+ *   out           [B, N, Hq, D] in dtype, contiguous
+ *   lse           float32 [B, N, Hq] or NULL
+ *   row_status    int32 [B]: SPECDEC_ROW_BAD_TREE, SPECDEC_ROW_BAD_CACHE (length
+ *                 or a block id that is read), SPECDEC_ROW_INTERNAL; such a request
+ *                 gets out = 0, lse = -infinity
+ *   workspace     >= specdec_attend_workspace_size(...) bytes, 16-byte aligned;
+ *                 0 bytes (NULL) where that is 0
+ * Limits: N <= SPECDEC_MAX_TREE_NODES, Hq a multiple of Hkv, Hq <=
+ * SPECDEC_MAX_HEADS, scale finite, softcap >= 0, window >= 0.
+ * B = 0 and N = 0 are no-ops.
+ */
+size_t specdec_attend_workspace_size(int B, int N, int Hq, int Hkv, int D, int dtype);
+int specdec_attend(const void *q, const void *k_new, const void *v_new, int dtype,
+                   long long q_stride, long long k_stride, long long v_stride,
+                   const int32_t *parent, const int32_t *n_nodes, const specdec_kv_cache *cache,
+                   int B, int N, int Hq, float scale, float softcap, const float *slopes,
+                   int window, void *out, float *lse, int32_t *row_status, void *workspace,
+                   size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -27,6 +27,7 @@ ROW_NONFINITE = 4
 ROW_BAD_TEMP = 8
 ROW_BAD_TREE = 16
 ROW_INTERNAL = 32
+ROW_BAD_CACHE = 64
 
 _lib = None
 
@@ -93,6 +94,18 @@ _EXPORTS = {
                               [ctypes.c_void_p] * 4 + [ctypes.c_int] * 4 +
                               [ctypes.c_void_p] * 8 + [ctypes.c_size_t, ctypes.c_void_p],
                               ctypes.c_int),
+    "specdec_rope": ([ctypes.c_void_p] * 2 + [ctypes.c_int] + [ctypes.c_longlong] * 2 +
+                     [ctypes.c_void_p] * 4 + [ctypes.c_int] * 6 +
+                     [ctypes.c_uint, ctypes.c_float] + [ctypes.c_void_p] * 3, ctypes.c_int),
+    "specdec_kv_append": ([ctypes.c_void_p] * 2 + [ctypes.c_int] + [ctypes.c_longlong] * 2 +
+                          [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_int,
+                           ctypes.c_void_p, ctypes.c_int, ctypes.c_int] + [ctypes.c_void_p] * 3,
+                          ctypes.c_int),
+    "specdec_attend_workspace_size": ([ctypes.c_int] * 6, ctypes.c_size_t),
+    "specdec_attend": ([ctypes.c_void_p] * 3 + [ctypes.c_int] + [ctypes.c_longlong] * 3 +
+                       [ctypes.c_void_p] * 3 + [ctypes.c_int] * 3 + [ctypes.c_float] * 2 +
+                       [ctypes.c_void_p, ctypes.c_int] + [ctypes.c_void_p] * 4 +
+                       [ctypes.c_size_t, ctypes.c_void_p], ctypes.c_int),
 }
 
 
@@ -603,4 +616,278 @@ def path_logprob(logits: torch.Tensor, temperature: torch.Tensor, out_tokens: to
         _ptr(path_nodes), _ptr(row_status), B, R, V, out_tokens.shape[1], _ptr(workspace),
         workspace.numel(), _ptr(out), _stream_ptr(stream))
     _check(rc, "specdec_path_logprob")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# the attention side of the step: rotary positions, the 8-bit cache, attention
+# ---------------------------------------------------------------------------
+
+ROPE_INTERLEAVED, ROPE_BACKWARD = 1, 2
+
+
+class _CacheStruct(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale", "block_table",
+                                                "length")] +
+                [(n, ctypes.c_int) for n in ("n_blocks", "max_blocks", "block", "Hkv", "D")])
+
+
+@dataclasses.dataclass
+class KVCache:
+    """A paged cache in 8 bits (``specdec_kv_cache``): token j of request b is slot
+    j % block of block ``block_table[b, j // block]``; value = code * scale."""
+    k: torch.Tensor            # float8_e4m3fn [n_blocks, Hkv, block, D]
+    v: torch.Tensor            # float8_e4m3fn [n_blocks, Hkv, block, D]
+    k_scale: torch.Tensor      # float32 [n_blocks, Hkv]
+    v_scale: torch.Tensor      # float32 [n_blocks, Hkv]
+    block_table: torch.Tensor  # int32 [B, max_blocks]
+    length: torch.Tensor       # int32 [B]
+
+    @staticmethod
+    def empty(B: int, max_blocks: int, n_blocks: int, block: int, Hkv: int, D: int,
+              device="cuda") -> "KVCache":
+        """An empty cache: no request holds a token and no table entry a block (-1)."""
+        f8 = torch.float8_e4m3fn
+        shape = (n_blocks, Hkv, block, D)
+        return KVCache(torch.empty(shape, dtype=torch.uint8, device=device).view(f8),
+                       torch.empty(shape, dtype=torch.uint8, device=device).view(f8),
+                       torch.zeros(n_blocks, Hkv, device=device),
+                       torch.zeros(n_blocks, Hkv, device=device),
+                       torch.full((B, max_blocks), -1, dtype=torch.int32, device=device),
+                       torch.zeros(B, dtype=torch.int32, device=device))
+
+
+@dataclasses.dataclass
+class AppendOut:
+    length: torch.Tensor      # int32 [B]: the cache's length with the new tokens
+    row_status: torch.Tensor  # int32 [B]
+
+
+@dataclasses.dataclass
+class AttendOut:
+    out: torch.Tensor            # [B, N, Hq, D] in q's dtype
+    lse: Optional[torch.Tensor]  # float32 [B, N, Hq]
+    row_status: torch.Tensor     # int32 [B]
+
+
+def _raw(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream) -> int:
+    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+
+
+def _named(prefix: str, holder) -> dict:
+    """A holder's tensors under names of its own for ``_cuda`` (none for None)."""
+    return {} if holder is None else {f"{prefix}.{k}": t for k, t in vars(holder).items()}
+
+
+def _token_stride(t: torch.Tensor, name: str, dtype, B: int, N: int) -> int:
+    """Elements between consecutive tokens of a [B, N, H, D] tensor whose heads and
+    elements are contiguous (a whole tensor, or heads of a fused projection)."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 4 or t.shape[0] != B or t.shape[1] != N:
+        raise ValueError(f"{name} must have shape [{B}, {N}, heads, D], got {tuple(t.shape)}")
+    H, D = t.shape[2], t.shape[3]
+    s = t.stride()
+    at = s[1] if N > 1 else s[0] if B > 1 else H * D
+    if (s[3] != 1 and D > 1) or (s[2] != D and H > 1) or (B > 1 and N > 1 and s[0] != N * at):
+        raise ValueError(f"{name}: heads and elements must be contiguous and tokens one stride "
+                         f"apart, got strides {s}")
+    return at
+
+
+def _cache_struct(c: KVCache, B: int) -> _CacheStruct:
+    dev = c.k.device
+    if c.k.dim() != 4:
+        raise ValueError(f"cache.k must be [n_blocks, Hkv, block, D], got {tuple(c.k.shape)}")
+    nb, Hkv, block, D = c.k.shape
+    for t, name, dtype, shape in ((c.k, "cache.k", torch.float8_e4m3fn, (nb, Hkv, block, D)),
+                                  (c.v, "cache.v", torch.float8_e4m3fn, (nb, Hkv, block, D)),
+                                  (c.k_scale, "cache.k_scale", torch.float32, (nb, Hkv)),
+                                  (c.v_scale, "cache.v_scale", torch.float32, (nb, Hkv)),
+                                  (c.block_table, "cache.block_table", torch.int32,
+                                   (B, c.block_table.shape[-1])),
+                                  (c.length, "cache.length", torch.int32, (B,))):
+        _req(t, name, dtype, shape, dev)
+    return _CacheStruct(c.k.data_ptr(), c.v.data_ptr(), c.k_scale.data_ptr(),
+                        c.v_scale.data_ptr(), c.block_table.data_ptr(), c.length.data_ptr(),
+                        nb, c.block_table.shape[1], block, Hkv, D)
+
+
+def rope_frequencies(rot: int, theta: float = 10000.0, factor: float = 1.0,
+                     original_length: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                     device="cuda") -> torch.Tensor:
+    """Frequencies of ``rope`` in units of 2^-64 turns a position, int64 [rot / 2]: pair i
+    turns by theta^(-2i/rot) radians a position.  ``factor`` > 1 stretches them for a
+    context ``factor`` times longer: all pairs alike (position interpolation), or, given
+    the ``original_length`` that a model was trained on, only those that turn fewer than
+    ``beta_slow`` times over it, with a linear ramp up to ``beta_fast`` turns
+    (interpolation by frequency band)."""
+    import math
+    if rot < 2 or rot % 2:
+        raise ValueError(f"rot must be even and positive, got {rot}")
+    words = []
+    for i in range(rot // 2):
+        turns = theta ** (-2.0 * i / rot) / (2.0 * math.pi)
+        if factor != 1.0:
+            keep = 0.0
+            if original_length > 0:
+                # the ramp is linear in the pair's index, from where a pair turns
+                # beta_fast times over the original length to where it turns beta_slow times
+                def at(n):
+                    return rot * math.log(original_length / (n * 2.0 * math.pi)) / \
+                        (2.0 * math.log(theta))
+                low = max(math.floor(at(beta_fast)), 0)
+                high = min(math.ceil(at(beta_slow)), rot // 2 - 1)
+                keep = 1.0 - min(1.0, max(0.0, (i - low) / max(high - low, 1e-3)))
+            turns = turns * keep + turns / factor * (1.0 - keep)
+        word = int(math.ldexp(turns, 64)) % 2 ** 64
+        words.append(word - 2 ** 64 if word >= 2 ** 63 else word)
+    return torch.tensor(words, dtype=torch.int64, device=device)
+
+
+def rope(q: torch.Tensor, k: Optional[torch.Tensor], freq: torch.Tensor,
+         positions: Optional[torch.Tensor] = None, base: Optional[torch.Tensor] = None,
+         parent: Optional[torch.Tensor] = None, interleaved: bool = False,
+         backward: bool = False, magnitude: float = 1.0, q_out: Optional[torch.Tensor] = None,
+         k_out: Optional[torch.Tensor] = None, stream=None):
+    """Rotary positions (``specdec_rope``) of q [B, N, Hq, D] and k [B, N, Hk, D] (or None):
+    returns the turned (q, k).  Positions are ``positions`` [B, N], or ``base`` [B] plus the
+    depth of each node of ``parent`` [B, N] (a chain without it).  ``backward``: the
+    gradient, from dq and dk."""
+    _cuda(q=q, k=k, freq=freq, positions=positions, base=base, parent=parent, q_out=q_out,
+          k_out=k_out)
+    dt, dev = dtype_code(q), q.device
+    if q.dim() != 4:
+        raise ValueError(f"q must be [B, N, Hq, D], got {tuple(q.shape)}")
+    B, N, Hq, D = q.shape
+    q_at = _token_stride(q, "q", q.dtype, B, N)
+    Hk = k_at = 0
+    if k is not None:
+        k_at, Hk = _token_stride(k, "k", q.dtype, B, N), k.shape[2]
+        if k.shape[3] != D:
+            raise ValueError(f"k must have heads of {D} elements, got {k.shape[3]}")
+    _req(freq, "freq", torch.int64, (freq.numel(),), dev)
+    for t, name, shape in ((positions, "positions", (B, N)), (base, "base", (B,)),
+                           (parent, "parent", (B, N))):
+        if t is not None:
+            _req(t, name, torch.int32, shape, dev)
+    if q_out is None:
+        q_out = torch.empty((B, N, Hq, D), dtype=q.dtype, device=dev)
+    else:
+        _req(q_out, "q_out", q.dtype, (B, N, Hq, D), dev)
+    if k is None:
+        k_out = None
+    elif k_out is None:
+        k_out = torch.empty((B, N, Hk, D), dtype=q.dtype, device=dev)
+    else:
+        _req(k_out, "k_out", q.dtype, (B, N, Hk, D), dev)
+    rc = load_library().specdec_rope(
+        q.data_ptr(), _raw(k), dt, q_at, k_at, freq.data_ptr(), _raw(positions), _raw(base),
+        _raw(parent), B, N, Hq, Hk, D, 2 * freq.numel(),
+        (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_BACKWARD if backward else 0), magnitude,
+        q_out.data_ptr(), _raw(k_out), _raw_stream(stream))
+    _check(rc, "specdec_rope")
+    return q_out, k_out
+
+
+def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache,
+              count: Optional[torch.Tensor] = None, extra: int = 0,
+              path: Optional[torch.Tensor] = None, out: Optional[AppendOut] = None,
+              stream=None) -> AppendOut:
+    """Append tokens of k, v [B, N, Hkv, D] to the cache (``specdec_kv_append``): of request b
+    the first ``count[b] + extra`` nodes (N + extra without count) of ``path`` [B, path_len]
+    or of 0 .. N-1.  After a verify step: ``count=r.n_accepted, extra=1`` and, for a tree,
+    ``path=r.path_nodes``.  ``cache.length`` is left alone: set it to the result's
+    ``length`` for the next step."""
+    _cuda(k=k, v=v, count=count, path=path,
+          **_named("cache", cache), **_named("out", out))
+    dt, dev = dtype_code(k), k.device
+    if k.dim() != 4:
+        raise ValueError(f"k must be [B, N, Hkv, D], got {tuple(k.shape)}")
+    B, N = k.shape[:2]
+    k_at, v_at = _token_stride(k, "k", k.dtype, B, N), _token_stride(v, "v", k.dtype, B, N)
+    c = _cache_struct(cache, B)
+    for t, name in ((k, "k"), (v, "v")):
+        if t.shape[2] != c.Hkv or t.shape[3] != c.D:
+            raise ValueError(f"{name} must have {c.Hkv} heads of {c.D} elements, as the cache, "
+                             f"got {tuple(t.shape)}")
+    if count is not None:
+        _req(count, "count", torch.int32, (B,), dev)
+    if path is not None:
+        _req(path, "path", torch.int32, (B, path.shape[-1]), dev)
+    if out is None:
+        both = torch.empty((2, B), dtype=torch.int32, device=dev)
+        out = AppendOut(both[0], both[1])
+    else:
+        _req(out.length, "out.length", torch.int32, (B,), dev)
+        _req(out.row_status, "out.row_status", torch.int32, (B,), dev)
+    rc = load_library().specdec_kv_append(
+        k.data_ptr(), v.data_ptr(), dt, k_at, v_at, _raw(count), extra, _raw(path),
+        path.shape[1] if path is not None else 0, ctypes.addressof(c), B, N,
+        out.length.data_ptr(), out.row_status.data_ptr(), _raw_stream(stream))
+    _check(rc, "specdec_kv_append")
+    return out
+
+
+def attend_workspace_size(B: int, N: int, Hq: int, Hkv: int, D: int, dtype: int) -> int:
+    return int(load_library().specdec_attend_workspace_size(B, N, Hq, Hkv, D, dtype))
+
+
+def alloc_attend_workspace(q: torch.Tensor, cache: KVCache) -> torch.Tensor:
+    """The workspace of ``attend`` for queries of q's shape on this cache."""
+    B, N, Hq, D = q.shape
+    n = attend_workspace_size(B, N, Hq, cache.k.shape[1], D, dtype_code(q))
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
+
+
+def attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: KVCache,
+           parent: Optional[torch.Tensor] = None, n_nodes: Optional[torch.Tensor] = None,
+           scale: Optional[float] = None, softcap: float = 0.0,
+           slopes: Optional[torch.Tensor] = None, window: int = 0,
+           out: Optional[AttendOut] = None, workspace: Optional[torch.Tensor] = None,
+           stream=None) -> AttendOut:
+    """Attention of drafted tokens (``specdec_attend``): q [B, N, Hq, D] over the request's
+    cached tokens and, by the chain or the tree ``parent`` [B, N], over the drafted tokens'
+    own k, v [B, N, Hkv, D].  ``scale`` defaults to D ** -0.5."""
+    _cuda(q=q, k=k, v=v, parent=parent, n_nodes=n_nodes, slopes=slopes, workspace=workspace,
+          **_named("cache", cache), **_named("out", out))
+    dt, dev = dtype_code(q), q.device
+    if q.dim() != 4:
+        raise ValueError(f"q must be [B, N, Hq, D], got {tuple(q.shape)}")
+    B, N, Hq, D = q.shape
+    q_at = _token_stride(q, "q", q.dtype, B, N)
+    k_at, v_at = _token_stride(k, "k", q.dtype, B, N), _token_stride(v, "v", q.dtype, B, N)
+    c = _cache_struct(cache, B)
+    for t, name in ((k, "k"), (v, "v")):
+        if t.shape[2] != c.Hkv or t.shape[3] != c.D:
+            raise ValueError(f"{name} must have {c.Hkv} heads of {c.D} elements, as the cache, "
+                             f"got {tuple(t.shape)}")
+    if D != c.D:
+        raise ValueError(f"q has heads of {D} elements, the cache of {c.D}")
+    for t, name, dtype, shape in ((parent, "parent", torch.int32, (B, N)),
+                                  (n_nodes, "n_nodes", torch.int32, (B,)),
+                                  (slopes, "slopes", torch.float32, (Hq,))):
+        if t is not None:
+            _req(t, name, dtype, shape, dev)
+    if out is None:
+        out = AttendOut(torch.empty((B, N, Hq, D), dtype=q.dtype, device=dev),
+                        torch.empty((B, N, Hq), dtype=torch.float32, device=dev),
+                        torch.empty(B, dtype=torch.int32, device=dev))
+    else:
+        _req(out.out, "out.out", q.dtype, (B, N, Hq, D), dev)
+        if out.lse is not None:
+            _req(out.lse, "out.lse", torch.float32, (B, N, Hq), dev)
+        _req(out.row_status, "out.row_status", torch.int32, (B,), dev)
+    if workspace is None:
+        workspace = alloc_attend_workspace(q, cache)
+    rc = load_library().specdec_attend(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), dt, q_at, k_at, v_at, _raw(parent),
+        _raw(n_nodes), ctypes.addressof(c), B, N, Hq, D ** -0.5 if scale is None else scale,
+        softcap, _raw(slopes), window, out.out.data_ptr(), _raw(out.lse),
+        out.row_status.data_ptr(), workspace.data_ptr(), workspace.numel(), _raw_stream(stream))
+    _check(rc, "specdec_attend")
     return out

@@ -1,0 +1,935 @@
+// Attention of drafted tokens over the 8-bit paged cache (specdec_attend).
+//
+// For one request and one head of k and v the R = N * G rows (node n, query
+// head g of the group) all read the same cached tokens:
+//     s = scale q . k (capped, biased), out = sum 2^(s' - m) v / sum 2^(s' - m),
+// s' = s log2(e), with the running maximum m and sum of one pass.  Each cached
+// byte is read once for 16 rows; with few rows the pass is bound by HBM.
+//
+// Streaming kernel.  A CTA of four warps takes one request, one k/v head, 16
+// rows and one split of the tokens; a warp takes every fourth granule of 16
+// tokens, with statistics of its own, so nothing waits on another warp until
+// the four are joined at the end.  Codes go from global memory straight into
+// the operand registers of m16n8k16 products, no shared memory between:
+//   * the products' inner order is free, so for q k^T lane c of a quad owns 16
+//     consecutive elements of a head instead of scattered pairs: one 16-byte
+//     load fills the operand of four products;
+//   * for p v the order of the output columns is free too: lane group g owns
+//     D/8 consecutive elements of a head for its four tokens, and a byte
+//     permute pairs neighbouring tokens.
+// e4m3 codes widen to fp16 exactly.  q is scaled by a power of two per row, so
+// that its largest element is in [2^10, 2^11): a bfloat16 is then exact in fp16
+// but for elements below 2^-24 of that.  p goes into
+// the products in fp16 (11 bits; bfloat16 would add as much error as the
+// rounding of a bfloat16 result) around 2^6, so that weights down to 2^-20 of
+// the largest keep all of them.  Float32 activations are split into two fp16
+// terms each (22 bits) and the products repeated.  Maximum, sum and the
+// accumulators are float32.  The accumulators are in units of the largest
+// v scale so far; p carries the ratio of a block's scale to it.
+//
+// The drafted tokens' own k and v take the same path as granules of 16 nodes,
+// scaled to fp16 by a power of two per node.  Where a mask hides part of a
+// granule, non-finite v are taken out of the products (0 * NaN would reach rows
+// that do not see them) and added to the rows that do.
+//
+// With several splits a second kernel joins their partials in split order.
+#include "attention_common.cuh"
+
+namespace specdec {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kRows = 16;       // rows of one CTA
+constexpr int kGran = 16;       // tokens of one granule
+constexpr float kRaise = 8.0f;  // the maximum moves when a score passes it by this much
+constexpr float kLift = 6.0f;   // p = 2^(s' - m + kLift) <= 2^14: inside fp16
+constexpr unsigned kAll = 0xffffffffu;
+
+// A partial: m[16], l[16], then O[16][D]; a row's flags ride in l (< 0).
+__host__ __device__ inline size_t partial_floats(int D) { return (size_t)kRows * (D + 2); }
+
+__device__ __forceinline__ void mma16816(float *c, const uint32_t *a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// 2^k, k in [-126, 127].
+__device__ __forceinline__ float pow2i(int k) { return __uint_as_float((uint32_t)(k + 127) << 23); }
+
+// The exponent k of the unit that values of size up to `top` are carried in:
+// top / 2^k is in [2^10, 2^11), clear of fp16's subnormals at both terms.
+__device__ __forceinline__ int unit_exponent(float top) {
+  return min(max((int)(__float_as_uint(top) >> 23) - 127 - 10, -126), 126);
+}
+
+__device__ __forceinline__ uint4 ldg_stream(const uint8_t *p) {
+  uint4 r;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
+  return r;
+}
+__device__ __forceinline__ uint2 ldg_stream8(const uint8_t *p) {
+  uint2 r;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];"
+               : "=r"(r.x), "=r"(r.y)
+               : "l"(p));
+  return r;
+}
+
+template <int DP, bool kF32>
+struct Kernel {
+  static constexpr int KC = DP / 64;  // 16-byte pieces of a token that a lane takes for q k^T
+  static constexpr int VB = DP / 8;   // consecutive elements that a lane takes for p v
+  static constexpr int NT = DP / 8;   // 8-column tiles of the output
+  static constexpr int KS = DP / 16;  // inner steps of q k^T
+  static constexpr int U = DP > 128 || kF32 ? 1 : 2;  // granules a warp has in flight
+
+  struct Smem {
+    uint4 q[KS][32];                    // A operands, in register order
+    uint4 q_lo[kF32 ? KS : 1][32];      // the low terms of float32 activations
+    float q_exp[kRows];                 // 2^e taken out of each row
+    float o[2][kRows][DP + 4];          // joining of the warps
+    float m[kWarps][kRows], l[kWarps][kRows], vref[kWarps];
+    int bad[kWarps];
+  };
+
+  const AttendParams &p;
+  Smem &sm;
+  const int lane, warp, g, c;
+  int b, h, tile, split;
+  int len, nodes, max_depth;
+  // the thread's two rows (g and g + 8 of the CTA's 16)
+  int node[2], pos[2];
+  bool live[2];
+  float rf[2], slope[2];
+  float m[2], l[2], vref;
+  float o[NT][4];
+
+  __device__ Kernel(const AttendParams &p_, Smem &s_)
+      : p(p_), sm(s_), lane(threadIdx.x & 31), warp(threadIdx.x >> 5), g((threadIdx.x & 31) >> 2),
+        c(threadIdx.x & 3) {
+    // row tiles of one split are neighbours: they read the same tokens
+    int i = blockIdx.x;
+    tile = i % p.row_tiles;
+    i /= p.row_tiles;
+    split = i % p.splits;
+    i /= p.splits;
+    h = i % p.cache.Hkv;
+    b = i / p.cache.Hkv;
+  }
+
+  __device__ __forceinline__ float act(const void *base, long long i) const {
+    return load_elem(base, kF32 ? SPECDEC_F32 : SPECDEC_BF16, i);
+  }
+
+  // -------------------------------------------------------------------------
+  // scores: products -> base-2 exponents, masked where hidden
+  // -------------------------------------------------------------------------
+  __device__ __forceinline__ float score(float dot, float k_unit, int i, int dist) const {
+    float s = dot * (k_unit * rf[i]);  // natural units
+    if (p.softcap > 0.0f) {
+      const float y = s / p.softcap;
+      float t;
+      if (kF32) {
+        t = tanhf(y);
+      } else {  // 1 - 2 / (1 + e^2y): absolute error below 2^-22
+        t = 1.0f - __fdividef(2.0f, 1.0f + ex2_approx(y * (2.0f * kLog2e)));
+      }
+      s = t * p.softcap;
+    }
+    if (p.slopes) s -= slope[i] * (float)dist;
+    return s * kLog2e;
+  }
+
+  // One granule's softmax: x[nt][0..3] are base-2 scores (hidden ones -inf);
+  // returns p as A operands, scaled by v_unit (per own token, over vref), and
+  // adds to l.  Lanes of a quad share rows.
+  template <int kU>
+  __device__ __forceinline__ void raise(const float (*x)[2][4]) {
+    float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          top[i] = fmaxf(top[i], fmaxf(x[u][nt][2 * i], x[u][nt][2 * i + 1]));
+    bool need = false;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      top[i] = fmaxf(top[i], __shfl_xor_sync(kAll, top[i], 1));
+      top[i] = fmaxf(top[i], __shfl_xor_sync(kAll, top[i], 2));
+      need |= top[i] > m[i] + kRaise;  // also the first time: m = -inf
+    }
+    if (__any_sync(kAll, need)) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float to = fmaxf(m[i], top[i]);
+        const float f = m[i] == -INFINITY ? 0.0f : ex2_approx(m[i] - to);
+        l[i] *= f;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          o[j][2 * i] *= f;
+          o[j][2 * i + 1] *= f;
+        }
+        m[i] = to;
+      }
+    }
+  }
+
+  __device__ __forceinline__ void raise_unit(float unit) {
+    if (unit > vref) {  // the same in all lanes
+      const float f = __fdividef(vref, unit);
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[j][e] *= f;
+      vref = unit;
+    }
+  }
+
+  // p of one granule; unit[0..3]: v units over vref of tokens 2c, 2c+1, 2c+8, 2c+9.
+  __device__ __forceinline__ void weights(const float (*x)[4], const float *unit, uint32_t *a,
+                                          uint32_t *a_lo) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float at = m[i] == -INFINITY ? 0.0f : m[i] - kLift;
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        const float p0 = ex2_approx(x[nt][2 * i] - at), p1 = ex2_approx(x[nt][2 * i + 1] - at);
+        l[i] += p0 + p1;
+        const float w0 = p0 * unit[2 * nt], w1 = p1 * unit[2 * nt + 1];
+        const uint32_t w = pack_half2(w0, w1);
+        a[2 * nt + i] = w;
+        if (kF32)
+          a_lo[2 * nt + i] = pack_half2(w0 - half_bits_to_float(w & 0xFFFFu),
+                                        w1 - half_bits_to_float(w >> 16));
+      }
+    }
+  }
+
+  // -------------------------------------------------------------------------
+  // cached tokens
+  // -------------------------------------------------------------------------
+  struct Codes {
+    uint4 k[2][KC];
+    uint32_t v[4][VB / 4];
+    float ks, vs;
+  };
+
+  // The block of token t and its slot there; ok = a block id in range.
+  __device__ __forceinline__ int block_id(int t) const {
+    return __ldg(p.cache.block_table + (long long)b * p.cache.max_blocks + t / p.cache.block);
+  }
+
+  __device__ __forceinline__ void load(Codes &w, int t0, int id) const {
+    const specdec_kv_cache &kv = p.cache;
+    const long long cell = (long long)id * kv.Hkv + h;
+    const int slot = t0 % kv.block;
+    const uint8_t *k = reinterpret_cast<const uint8_t *>(kv.k) +
+                       (cell * kv.block + slot) * kv.D;
+    const uint8_t *v = reinterpret_cast<const uint8_t *>(kv.v) +
+                       (cell * kv.block + slot) * kv.D;
+    const int held = len - t0;  // tokens of this granule that exist
+    w.ks = __ldg(kv.k_scale + cell);
+    w.vs = __ldg(kv.v_scale + cell);
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+      for (int i = 0; i < KC; ++i) {
+        const int t = nt * 8 + g, e = (c + 4 * i) * 16;
+        w.k[nt][i] = (t < held && e < kv.D) ? ldg_stream(k + t * kv.D + e)
+                                            : make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int t = (j >> 1) * 8 + 2 * c + (j & 1), e = g * VB;
+      if (VB == 8) {
+        const uint2 x = (t < held && e < kv.D) ? ldg_stream8(v + t * kv.D + e) : make_uint2(0u, 0u);
+        w.v[j][0] = x.x;
+        w.v[j][1] = x.y;
+      } else {
+#pragma unroll
+        for (int i = 0; i < VB / 16; ++i) {
+          const uint4 x = (t < held && e + 16 * i < kv.D) ? ldg_stream(v + t * kv.D + e + 16 * i)
+                                                          : make_uint4(0u, 0u, 0u, 0u);
+          w.v[j][4 * i] = x.x;
+          w.v[j][4 * i + 1] = x.y;
+          w.v[j][4 * i + 2] = x.z;
+          w.v[j][4 * i + 3] = x.w;
+        }
+      }
+    }
+  }
+
+  __device__ __forceinline__ void dots(const Codes &w, float (*s)[4]) const {
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[nt][e] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < KC; ++i)
+#pragma unroll
+      for (int sub = 0; sub < 4; ++sub) {
+        const uint4 qa = sm.q[i * 4 + sub][lane];
+        const uint32_t a[4] = {qa.x, qa.y, qa.z, qa.w};
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          const uint32_t word = sub == 0 ? w.k[nt][i].x : sub == 1 ? w.k[nt][i].y
+                                : sub == 2 ? w.k[nt][i].z : w.k[nt][i].w;
+          const uint32_t b0 = e4m3x2_to_half2(word & 0xFFFFu), b1 = e4m3x2_to_half2(word >> 16);
+          mma16816(s[nt], a, b0, b1);
+          if (kF32) {
+            const uint4 ql = sm.q_lo[i * 4 + sub][lane];
+            const uint32_t al[4] = {ql.x, ql.y, ql.z, ql.w};
+            mma16816(s[nt], al, b0, b1);
+          }
+        }
+      }
+  }
+
+  // Scores of the granule at t0 from its dots, hidden ones -inf.
+  __device__ __forceinline__ void scores(float (*s)[4], float ks, int t0, bool partial) const {
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = e >> 1, t = t0 + nt * 8 + 2 * c + (e & 1);
+        const float x = score(s[nt][e], ks, i, pos[i] - t);
+        s[nt][e] = (partial && !sees(i, t)) ? -INFINITY : x;
+      }
+  }
+
+  __device__ __forceinline__ bool sees(int i, int t) const {
+    return live[i] && t < len && (p.window == 0 || pos[i] - t < p.window);
+  }
+
+  __device__ __forceinline__ void values(Codes &w, const uint32_t *a, const uint32_t *a_lo) {
+#pragma unroll
+    for (int q4 = 0; q4 < VB / 4; ++q4) {
+      uint32_t b0[4], b1[4];
+      const uint32_t x01 = __byte_perm(w.v[0][q4], w.v[1][q4], 0x5140);
+      const uint32_t x23 = __byte_perm(w.v[0][q4], w.v[1][q4], 0x7362);
+      const uint32_t y01 = __byte_perm(w.v[2][q4], w.v[3][q4], 0x5140);
+      const uint32_t y23 = __byte_perm(w.v[2][q4], w.v[3][q4], 0x7362);
+      b0[0] = e4m3x2_to_half2(x01 & 0xFFFFu);
+      b0[1] = e4m3x2_to_half2(x01 >> 16);
+      b0[2] = e4m3x2_to_half2(x23 & 0xFFFFu);
+      b0[3] = e4m3x2_to_half2(x23 >> 16);
+      b1[0] = e4m3x2_to_half2(y01 & 0xFFFFu);
+      b1[1] = e4m3x2_to_half2(y01 >> 16);
+      b1[2] = e4m3x2_to_half2(y23 & 0xFFFFu);
+      b1[3] = e4m3x2_to_half2(y23 >> 16);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        mma16816(o[q4 * 4 + k], a, b0[k], b1[k]);
+        if (kF32) mma16816(o[q4 * 4 + k], a_lo, b0[k], b1[k]);
+      }
+    }
+  }
+
+  // Element of the thread's output column: tile j, value e of its four.
+  __device__ __forceinline__ int column(int j, int e) const { return (2 * c + (e & 1)) * VB + j; }
+
+  // NaN codes of a partly hidden granule: out of the products, into the rows
+  // that see their token.
+  __device__ __forceinline__ void sift(Codes &w, int t0, int id) {
+    unsigned hit = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int q4 = 0; q4 < VB / 4; ++q4) {
+        uint32_t keep = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (((w.v[j][q4] >> (8 * k)) & 0x7Fu) != 0x7Fu) keep |= 0xFFu << (8 * k);
+        if (keep != kAll) hit |= 1u << ((j >> 1) * 8 + 2 * c + (j & 1));
+        w.v[j][q4] &= keep;
+      }
+    hit = __reduce_or_sync(kAll, hit);
+    const specdec_kv_cache &kv = p.cache;
+    const uint8_t *v = reinterpret_cast<const uint8_t *>(kv.v) +
+                       (((long long)id * kv.Hkv + h) * kv.block + t0 % kv.block) * kv.D;
+    while (hit) {
+      const int t = __ffs(hit) - 1;
+      hit &= hit - 1;
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int d = column(j, e);
+          if (d < kv.D && (v[t * kv.D + d] & 0x7Fu) == 0x7Fu && sees(e >> 1, t0 + t))
+            o[j][e] = __int_as_float(0x7fc00000);
+        }
+    }
+  }
+
+  // Cached tokens [from, to): the warp's granules.  Returns false on a bad id.
+  __device__ __forceinline__ bool cached(int from, int to) {
+    constexpr int kStep = kGran * kWarps;
+    int t0 = from + kGran * warp;
+    int id[U];
+    bool ok = true;
+    auto fetch = [&](int t) {
+      int i = t < to ? block_id(t) : 0;
+      if (i < 0 || i >= p.cache.n_blocks) {
+        ok = false;
+        i = 0;
+      }
+      return i;
+    };
+#pragma unroll
+    for (int u = 0; u < U; ++u) id[u] = fetch(t0 + u * kStep);
+    Codes w[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (t0 + u * kStep < to) load(w[u], t0 + u * kStep, id[u]);
+    for (; t0 < to; t0 += U * kStep) {
+      int next[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) next[u] = fetch(t0 + (U + u) * kStep);
+      // the window's and the length's edges; with a tree's depth unknown, any
+      // granule that the deepest possible node may not see whole
+      float s[U][2][4];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int t = t0 + u * kStep;
+        if (t < to) {
+          const bool partial =
+              t + kGran > len || (p.window > 0 && t <= len + p.N - 1 - p.window);
+          dots(w[u], s[u]);
+          scores(s[u], w[u].ks, t, partial);
+          if (partial && p.window > 0) sift(w[u], t, id[u]);
+        } else {
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[u][nt][e] = -INFINITY;
+        }
+      }
+      raise<U>(s);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (t0 + u * kStep < to) {
+          raise_unit(w[u].vs);
+          const float r = __fdividef(w[u].vs, vref);
+          const float unit[4] = {r, r, r, r};
+          uint32_t a[4], a_lo[4];
+          weights(s[u], unit, a, a_lo);
+          values(w[u], a, a_lo);
+        }
+        if (t0 + (U + u) * kStep < to) load(w[u], t0 + (U + u) * kStep, next[u]);
+        id[u] = next[u];
+      }
+    }
+    return ok;
+  }
+
+  // -------------------------------------------------------------------------
+  // the drafted tokens themselves
+  // -------------------------------------------------------------------------
+  // Nodes of [j0, j0 + 16) that node n sees, as bits.
+  __device__ __forceinline__ unsigned above(int n, int depth, int j0) const {
+    unsigned bits = 0;
+    int a = n, at = depth;
+    while (a >= j0) {
+      if (a < j0 + kGran && (p.window == 0 || depth - at < p.window)) bits |= 1u << (a - j0);
+      int up = a - 1;
+      if (p.parent && a > 0) {
+        up = p.parent[(long long)b * p.N + a];
+        if (up >= a) up = -1;
+      }
+      a = up;
+      --at;
+    }
+    return bits;
+  }
+
+  __device__ __forceinline__ void drafted(int j0) {
+    const specdec_kv_cache &kv = p.cache;
+    const long long first = (long long)b * p.N + j0;
+    const int held = min(nodes - j0, kGran);
+    unsigned see[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) see[i] = live[i] ? above(node[i], pos[i] - len, j0) : 0u;
+
+    // q k^T, the node's k in units of its size
+    float s[1][2][4], unit_k[2];
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+      const int t = nt * 8 + g;
+      const long long at = (first + t) * p.k_stride + (long long)h * kv.D;
+      float top = 0.0f;
+      if (t < held)
+        for (int i = 0; i < KC; ++i)
+          for (int e = (c + 4 * i) * 16; e < (c + 4 * i) * 16 + 16 && e < kv.D; ++e) {
+            const float x = fabsf(act(p.k_new, at + e));
+            if (x < INFINITY) top = fmaxf(top, x);
+          }
+      top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
+      const int ex = unit_exponent(top);
+      unit_k[nt] = pow2i(ex);
+      const float inv = pow2i(-ex);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[0][nt][e] = 0.0f;
+      for (int i = 0; i < KC; ++i)
+        for (int sub = 0; sub < 4; ++sub) {
+          const int e = (c + 4 * i) * 16 + sub * 4;
+          float x[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            x[k] = (t < held && e < kv.D) ? act(p.k_new, at + e + k) * inv : 0.0f;
+          const uint32_t b0 = pack_half2(x[0], x[1]), b1 = pack_half2(x[2], x[3]);
+          const uint4 qa = sm.q[i * 4 + sub][lane];
+          const uint32_t a[4] = {qa.x, qa.y, qa.z, qa.w};
+          mma16816(s[0][nt], a, b0, b1);
+          if (kF32) {
+            const uint32_t l0 = low_half2(x[0], x[1], b0), l1 = low_half2(x[2], x[3], b1);
+            const uint4 ql = sm.q_lo[i * 4 + sub][lane];
+            const uint32_t al[4] = {ql.x, ql.y, ql.z, ql.w};
+            mma16816(s[0][nt], al, b0, b1);
+            mma16816(s[0][nt], a, l0, l1);
+          }
+        }
+    }
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = e >> 1, t = nt * 8 + 2 * c + (e & 1);
+        // column t's unit is with the lanes of group t % 8
+        const float unit = __shfl_sync(kAll, unit_k[nt], (2 * c + (e & 1)) * 4);
+        const bool seen = (see[i] >> t) & 1u;
+        const int dist = p.slopes && seen ? pos[i] - len - depth_of(j0 + t) : 0;
+        s[0][nt][e] = seen ? score(s[0][nt][e], unit, i, dist) : -INFINITY;
+      }
+    raise<1>(s);
+
+    // p v, the node's v in units of its size
+    float unit_v[4], inv_v[4];
+    float top_unit = 0.0f;
+    unsigned hit = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int t = (j >> 1) * 8 + 2 * c + (j & 1);
+      const long long at = (first + t) * p.v_stride + (long long)h * kv.D;
+      float top = 0.0f;
+      if (t < held)
+        for (int e = g * VB; e < (g + 1) * VB && e < kv.D; ++e) {
+          const float x = fabsf(act(p.v_new, at + e));
+          if (x < INFINITY)
+            top = fmaxf(top, x);
+          else
+            hit |= 1u << t;
+        }
+#pragma unroll
+      for (int d = 4; d <= 16; d <<= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
+      const int ex = unit_exponent(top);
+      unit_v[j] = pow2i(ex);
+      inv_v[j] = pow2i(-ex);
+      top_unit = fmaxf(top_unit, unit_v[j]);
+    }
+    hit = __reduce_or_sync(kAll, hit);
+    top_unit = fmaxf(top_unit, __shfl_xor_sync(kAll, top_unit, 1));
+    top_unit = fmaxf(top_unit, __shfl_xor_sync(kAll, top_unit, 2));
+    raise_unit(top_unit);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) unit_v[j] = __fdividef(unit_v[j], vref);
+    uint32_t a[4], a_lo[4];
+    weights(s[0], unit_v, a, a_lo);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int t = (j >> 1) * 8 + 2 * c + (j & 1), e = g * VB + n;
+        x[j] = 0.0f;
+        if (t < held && e < kv.D) {
+          const float y = act(p.v_new, (first + t) * p.v_stride + (long long)h * kv.D + e);
+          if (finite(y)) x[j] = y * inv_v[j];
+        }
+      }
+      const uint32_t b0 = pack_half2(x[0], x[1]), b1 = pack_half2(x[2], x[3]);
+      mma16816(o[n], a, b0, b1);
+      if (kF32) {
+        mma16816(o[n], a_lo, b0, b1);
+        mma16816(o[n], a, low_half2(x[0], x[1], b0), low_half2(x[2], x[3], b1));
+      }
+    }
+    while (hit) {  // infinities and NaN reach the rows that see their node, no others
+      const int t = __ffs(hit) - 1;
+      hit &= hit - 1;
+      for (int n = 0; n < NT; ++n)
+        for (int e = 0; e < 4; ++e) {
+          const int d = column(n, e);
+          if (d < kv.D && ((see[e >> 1] >> t) & 1u)) {
+            const float y = act(p.v_new, (first + t) * p.v_stride + (long long)h * kv.D + d);
+            if (!finite(y)) add_to(n, e, y);
+          }
+        }
+    }
+  }
+
+  // o[n][e] += y with n, e known only at run time (o stays in registers)
+  __device__ __forceinline__ void add_to(int n, int e, float y) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (j == n && k == e) o[j][k] += y;
+  }
+
+  // what fp16 left of (x0, x1); nothing where they are not finite
+  __device__ __forceinline__ uint32_t low_half2(float x0, float x1, uint32_t hi) const {
+    const float l0 = x0 - half_bits_to_float(hi & 0xFFFFu), l1 = x1 - half_bits_to_float(hi >> 16);
+    return pack_half2(finite(l0) ? l0 : 0.0f, finite(l1) ? l1 : 0.0f);
+  }
+
+  __device__ __forceinline__ int depth_of(int n) const {
+    if (!p.parent) return n;
+    int depth = 0;
+    for (int a = n; a > 0; ++depth) {
+      const int up = p.parent[(long long)b * p.N + a];
+      if (up < 0 || up >= a) break;
+      a = up;
+    }
+    return depth;
+  }
+
+  // -------------------------------------------------------------------------
+  __device__ __forceinline__ void run() {
+    const int row0 = tile * kRows, R = p.N * p.G;
+    const specdec_kv_cache &kv = p.cache;
+    int bad = 0;
+    len = kv.length[b];
+    if (len < 0 || (long long)len > (long long)kv.max_blocks * kv.block) {
+      bad = SPECDEC_ROW_BAD_CACHE;
+      len = 0;
+    }
+    nodes = p.N;
+    if (p.n_nodes) {
+      nodes = p.n_nodes[b];
+      if (nodes < 0 || nodes > p.N) {
+        bad |= SPECDEC_ROW_BAD_TREE;
+        nodes = 0;
+      }
+    }
+    if (p.parent) {
+      bool wrong = false;
+      for (int n = threadIdx.x; n < nodes; n += kThreads) {
+        const int up = p.parent[(long long)b * p.N + n];
+        wrong |= n == 0 ? up != -1 : (up < 0 || up >= n);
+      }
+      if (__syncthreads_or(wrong)) bad |= SPECDEC_ROW_BAD_TREE;
+    }
+
+    // q: rows to fp16 by a power of two each, in operand order
+    for (int r = warp; r < kRows; r += kWarps) {
+      const int row = row0 + r, n = row / p.G;
+      const bool in = row < R && n < nodes;
+      const long long at = in ? ((long long)b * p.N + n) * p.q_stride +
+                                    (long long)(h * p.G + row - n * p.G) * kv.D
+                              : 0;
+      float top = 0.0f;
+      for (int e = lane; in && e < kv.D; e += 32) {
+        const float x = fabsf(act(p.q, at + e));
+        if (x < INFINITY) top = fmaxf(top, x);
+      }
+#pragma unroll
+      for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
+      const int ex = unit_exponent(top);
+      const float inv = pow2i(-ex);
+      if (lane == 0) sm.q_exp[r] = pow2i(ex);
+      // elements 4 w .. 4 w + 3 are one lane's part of one step
+      for (int w = lane; w < DP / 4; w += 32) {
+        float x[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          x[k] = (in && 4 * w < kv.D) ? act(p.q, at + 4 * w + k) * inv : 0.0f;
+        const int piece = w >> 2, sub = w & 3;           // 16-element piece, step in it
+        const int cc = piece & 3, ks = (piece >> 2) * 4 + sub;
+        uint32_t *dst = reinterpret_cast<uint32_t *>(&sm.q[ks][(r & 7) * 4 + cc]);
+        const uint32_t x01 = pack_half2(x[0], x[1]), x23 = pack_half2(x[2], x[3]);
+        dst[r >> 3] = x01;
+        dst[2 + (r >> 3)] = x23;
+        if (kF32) {
+          dst = reinterpret_cast<uint32_t *>(&sm.q_lo[ks][(r & 7) * 4 + cc]);
+          dst[r >> 3] = low_half2(x[0], x[1], x01);
+          dst[2 + (r >> 3)] = low_half2(x[2], x[3], x23);
+        }
+      }
+    }
+    __syncthreads();
+
+    vref = 0x1p-126f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = g + 8 * i, row = row0 + r;
+      node[i] = row / p.G;
+      live[i] = row < R && node[i] < nodes;
+      pos[i] = len + (live[i] ? depth_of(node[i]) : 0);
+      rf[i] = p.scale * sm.q_exp[r];
+      slope[i] = (p.slopes && live[i]) ? p.slopes[h * p.G + row - node[i] * p.G] : 0.0f;
+      m[i] = -INFINITY;
+      l[i] = 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[j][e] = 0.0f;
+
+    if (nodes > 0) {
+      // the split's share of the tokens that the window leaves
+      int from = p.window > 0 ? max(0, len - p.window + 1) : 0;
+      from = from / kGran * kGran;
+      const int unit = kGran * kWarps;
+      const int share = ((len - from + p.splits - 1) / p.splits + unit - 1) / unit * unit;
+      const int lo = (int)min((long long)len, from + (long long)split * share);
+      const int hi = (int)min((long long)len, lo + (long long)share);
+      if (lo < hi && !cached(lo, hi)) bad |= SPECDEC_ROW_BAD_CACHE;
+      // drafted tokens: the last split's, that has the fewest cached ones
+      if (split == p.splits - 1)
+        for (int j0 = kGran * warp; j0 < nodes; j0 += kGran * kWarps) drafted(j0);
+    }
+
+    // quads hold parts of l; rows past the request's nodes took part unmasked
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (!live[i]) {
+        m[i] = -INFINITY;
+        l[i] = 0.0f;
+      }
+      l[i] += __shfl_xor_sync(kAll, l[i], 1);
+      l[i] += __shfl_xor_sync(kAll, l[i], 2);
+    }
+    bad = __reduce_or_sync(kAll, bad);
+    if (c == 0) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        sm.m[warp][g + 8 * i] = m[i];
+        sm.l[warp][g + 8 * i] = l[i];
+      }
+    }
+    if (lane == 0) sm.bad[warp] = bad;
+    __syncthreads();
+    // every warp moves to the common maximum and to true units
+    float all[2], sum[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = g + 8 * i;
+      all[i] = -INFINITY;
+      for (int w = 0; w < kWarps; ++w) all[i] = fmaxf(all[i], sm.m[w][r]);
+      sum[i] = 0.0f;
+      for (int w = 0; w < kWarps; ++w)
+        if (sm.m[w][r] > -INFINITY) sum[i] += sm.l[w][r] * ex2_approx(sm.m[w][r] - all[i]);
+      const float f = m[i] > -INFINITY ? ex2_approx(m[i] - all[i]) * vref : 0.0f;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        o[j][2 * i] = m[i] > -INFINITY ? o[j][2 * i] * f : 0.0f;
+        o[j][2 * i + 1] = m[i] > -INFINITY ? o[j][2 * i + 1] * f : 0.0f;
+      }
+    }
+    bad = 0;
+    for (int w = 0; w < kWarps; ++w) bad |= sm.bad[w];
+#pragma unroll
+    for (int step = kWarps / 2; step >= 1; step >>= 1) {
+      if (warp >= step && warp < 2 * step) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            sm.o[warp - step][g + 8 * (e >> 1)][column(j, e)] = o[j][e];
+      }
+      __syncthreads();
+      if (warp < step) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            o[j][e] += sm.o[warp][g + 8 * (e >> 1)][column(j, e)];
+      }
+      __syncthreads();
+    }
+    if (warp != 0) return;
+
+    if (p.splits > 1) {
+      float *part = p.part + ((((long long)b * kv.Hkv + h) * p.row_tiles + tile) * p.splits +
+                              split) * partial_floats(kv.D);
+      if (c == 0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          part[g + 8 * i] = all[i];
+          part[kRows + g + 8 * i] = bad ? -(float)bad : sum[i];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            const int d = column(j, k);
+            if (d < kv.D) part[2 * kRows + (g + 8 * i) * kv.D + d] = o[j][2 * i + k];
+          }
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int row = row0 + g + 8 * i;
+      if (row >= R) continue;
+      const int n = row / p.G;
+      const long long at = ((long long)b * p.N + n) * p.Hq + h * p.G + row - n * p.G;
+      const bool empty = bad || !live[i] || all[i] == -INFINITY;
+      const float inv = empty ? 0.0f : 1.0f / sum[i];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const int d = column(j, k);
+          if (d < kv.D) store_out(at * kv.D + d, empty ? 0.0f : o[j][2 * i + k] * inv);
+        }
+      if (c == 0 && p.lse)
+        p.lse[at] = empty ? -INFINITY : (all[i] - kLift + log2f(sum[i])) * 0.6931471805599453f;
+    }
+    if (tile == 0 && h == 0 && lane == 0) p.row_status[b] = bad;
+  }
+
+  __device__ __forceinline__ void store_out(long long i, float x) const {
+    if (kF32)
+      reinterpret_cast<float *>(p.out)[i] = x;
+    else
+      reinterpret_cast<unsigned short *>(p.out)[i] = (unsigned short)pack_bf16x2(x, 0.0f);
+  }
+};
+
+template <int DP, bool kF32>
+__global__ void __launch_bounds__(kThreads) attend_stream_kernel(const AttendParams p) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  pdl_wait();
+  pdl_launch_dependents();
+  using K = Kernel<DP, kF32>;
+  K k(p, *reinterpret_cast<typename K::Smem *>(raw));
+  k.run();
+}
+
+// Joins the splits of one row: a warp each.
+__global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, D = p.cache.D, Hkv = p.cache.Hkv;
+  const long long at = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);  // (b, n, query head)
+  if (at >= (long long)p.B * p.N * p.Hq) return;
+  const int hq = (int)(at % p.Hq), n = (int)(at / p.Hq % p.N), h = hq / p.G;
+  const long long b = at / p.Hq / p.N;
+  const int row = n * p.G + hq - h * p.G;
+  const size_t stride = partial_floats(D);
+  const float *part = p.part + (((b * Hkv + h) * p.row_tiles + row / kRows) * p.splits) * stride;
+  const int r = row % kRows;
+  // lane s holds split s and s + 32
+  float m[2], l[2];
+  int bad = 0;
+  float all = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int s = lane + 32 * i;
+    m[i] = s < p.splits ? part[s * stride + r] : -INFINITY;
+    l[i] = s < p.splits ? part[s * stride + kRows + r] : 0.0f;
+    if (l[i] < 0.0f) bad |= (int)-l[i];
+    all = fmaxf(all, m[i]);
+  }
+  bad = __reduce_or_sync(kAll, bad);
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) all = fmaxf(all, __shfl_xor_sync(kAll, all, d));
+  float f[2], sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    f[i] = m[i] > -INFINITY ? ex2_approx(m[i] - all) : 0.0f;
+    sum += l[i] * f[i];
+  }
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
+  const bool empty = bad != 0 || all == -INFINITY;
+  float acc[SPECDEC_MAX_HEAD_DIM / 32];
+#pragma unroll
+  for (int i = 0; i < SPECDEC_MAX_HEAD_DIM / 32; ++i) acc[i] = 0.0f;
+  for (int s = 0; s < p.splits; ++s) {
+    const float w = __shfl_sync(kAll, s < 32 ? f[0] : f[1], s & 31);
+    const float ms = __shfl_sync(kAll, s < 32 ? m[0] : m[1], s & 31);
+    if (ms == -INFINITY) continue;
+#pragma unroll
+    for (int i = 0; i < SPECDEC_MAX_HEAD_DIM / 32; ++i) {
+      const int d = lane + 32 * i;
+      if (d < D) acc[i] += w * part[s * stride + 2 * kRows + r * D + d];
+    }
+  }
+  const float inv = empty ? 0.0f : 1.0f / sum;
+#pragma unroll
+  for (int i = 0; i < SPECDEC_MAX_HEAD_DIM / 32; ++i) {
+    const int d = lane + 32 * i;
+    if (d >= D) continue;
+    const float x = empty ? 0.0f : acc[i] * inv;
+    if (p.dtype == SPECDEC_F32)
+      reinterpret_cast<float *>(p.out)[at * D + d] = x;
+    else
+      reinterpret_cast<unsigned short *>(p.out)[at * D + d] = (unsigned short)pack_bf16x2(x, 0.0f);
+  }
+  if (lane == 0) {
+    if (p.lse) p.lse[at] = empty ? -INFINITY : (all - kLift + log2f(sum)) * 0.6931471805599453f;
+    if (n == 0 && hq == 0) p.row_status[b] = bad;
+  }
+}
+
+int row_tiles_of(int N, int G) { return (N * G + kRows - 1) / kRows; }
+
+// Splits of the tokens: as many as give the device's SMs a few CTAs each.  A
+// function of the sizes alone, so that the workspace is too.
+int splits_of(long long B, int N, int Hkv, int G) {
+  const long long ctas = B * Hkv * row_tiles_of(N, G);
+  const long long s = 608 / ctas;  // 4 for each of 152 SMs
+  return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
+}
+
+template <int DP, bool kF32>
+cudaError_t launch_stream(const AttendParams &p, cudaStream_t stream) {
+  static DeviceOnce once;
+  const int smem = (int)sizeof(typename Kernel<DP, kF32>::Smem);
+  const cudaError_t err = smem_opt_in_once(once, attend_stream_kernel<DP, kF32>, smem);
+  if (err != cudaSuccess) return err;
+  return launch_pdl(attend_stream_kernel<DP, kF32>,
+                    dim3((unsigned)(p.splits * p.row_tiles * p.B * p.cache.Hkv)),
+                    dim3(kThreads), (size_t)smem, stream, p);
+}
+
+template <bool kF32>
+cudaError_t launch_type(const AttendParams &p, cudaStream_t stream) {
+  if (p.cache.D <= 64) return launch_stream<64, kF32>(p, stream);
+  if (p.cache.D <= 128) return launch_stream<128, kF32>(p, stream);
+  return launch_stream<256, kF32>(p, stream);
+}
+
+}  // namespace
+
+size_t attend_workspace_bytes(long long B, int N, int Hq, int Hkv, int D, int dtype) {
+  (void)dtype;
+  const int G = Hq / Hkv, s = splits_of(B, N, Hkv, G);
+  if (s == 1) return 0;
+  return (size_t)B * Hkv * row_tiles_of(N, G) * s * partial_floats(D) * sizeof(float);
+}
+
+cudaError_t launch_attend(AttendParams p, cudaStream_t stream) {
+  p.splits = splits_of(p.B, p.N, p.cache.Hkv, p.G);
+  p.row_tiles = row_tiles_of(p.N, p.G);
+  cudaError_t err = p.dtype == SPECDEC_F32 ? launch_type<true>(p, stream)
+                                           : launch_type<false>(p, stream);
+  if (err != cudaSuccess || p.splits == 1) return err;
+  const long long rows = (long long)p.B * p.N * p.Hq;
+  return launch_pdl(attend_join_kernel, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, stream, p);
+}
+
+}  // namespace specdec

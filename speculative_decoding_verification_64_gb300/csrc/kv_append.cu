@@ -1,0 +1,231 @@
+// Append of accepted tokens to the 8-bit paged cache (specdec_kv_append).
+//
+// For each block of tokens and head that gets tokens, with x the new values:
+//     s = max(2^ceil(log2(max |x| / 448)), 2^-100, s_old if tokens stand before),
+//     code = e4m3(x / s), and old codes c -> e4m3(c s_old / s) where s grew.
+// A power of two as the scale makes x / s exact, so a code is one rounding of
+// its value, and a grown scale only rounds off bits below the new smallest
+// step; e4m3's own exponent covers the factor of two that a finer scale would
+// give.
+//
+// One task is one block of tokens, of one head, of k or of v: its values are
+// read for their maximum and again (from L1 or L2) for their codes, 16 elements
+// a thread.  Bound by HBM for prompts; a verify step's few tokens are bound by
+// latency: there a task is one warp, for many tokens it is a CTA.
+#include "attention_common.cuh"
+
+namespace specdec {
+namespace {
+
+// The smallest power of two s >= 2^-100 with a <= 448 s (a finite, >= 0), from
+// a's exponent field: 448 = 1.75 * 2^8.
+__device__ __forceinline__ float scale_for(float a) {
+  if (!(a > 448.0f * 0x1p-100f)) return 0x1p-100f;
+  const uint32_t u = __float_as_uint(a);
+  const int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+// 16 consecutive elements as float32 values.
+template <int DT, bool kVec>
+__device__ __forceinline__ void load16(const char *in, float *x) {
+  if (!kVec) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = load_elem(in, DT, i);
+  } else if (DT == SPECDEC_F32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 w = __ldg(reinterpret_cast<const float4 *>(in) + i);
+      x[4 * i] = w.x;
+      x[4 * i + 1] = w.y;
+      x[4 * i + 2] = w.z;
+      x[4 * i + 3] = w.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint4 w = __ldg(reinterpret_cast<const uint4 *>(in) + i);
+      const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        x[8 * i + 2 * k] = bf16_lo(a[k]);
+        x[8 * i + 2 * k + 1] = bf16_hi(a[k]);
+      }
+    }
+  }
+}
+
+// kT threads work on one task: 32 (a warp) or the whole CTA.
+template <int kT>
+__device__ __forceinline__ void task_sync() {
+  if (kT == 32)
+    __syncwarp();
+  else
+    __syncthreads();
+}
+
+template <int kT>
+__device__ __forceinline__ bool task_any(bool x) {
+  if (kT == 32) return __any_sync(0xffffffffu, x);
+  return __syncthreads_or(x) != 0;
+}
+
+template <int DT, bool kVec, int kT>
+__global__ void __launch_bounds__(256) kv_append_kernel(const AppendParams p) {
+  __shared__ float red[8];
+  pdl_wait();
+  pdl_launch_dependents();
+  constexpr int es = DT == SPECDEC_F32 ? 4 : 2;
+  const specdec_kv_cache &c = p.cache;
+  const int t = kT == 32 ? threadIdx.x & 31 : threadIdx.x;
+  // task = ((b * blocks + m) * 2 + side) * Hkv + h
+  long long task = blockIdx.x;
+  if (kT == 32) {
+    task = task * 8 + (threadIdx.x >> 5);
+    if (task >= (long long)p.B * p.blocks * 2 * c.Hkv) return;
+  }
+  const int h = (int)(task % c.Hkv);
+  task /= c.Hkv;
+  const int side = (int)(task & 1);
+  task >>= 1;
+  const int m = (int)(task % p.blocks);
+  const long long b = task / p.blocks;
+
+  const int len = c.length[b];
+  const long long count = (long long)(p.count ? p.count[b] : p.N) + p.extra;
+  const long long most = (long long)c.max_blocks * c.block;
+  int status = 0;
+  if (len < 0 || len > most || count < 0 || count > (p.path ? min(p.path_len, p.N) : p.N) ||
+      len + count > most)
+    status = SPECDEC_ROW_BAD_CACHE;
+  const int first = status ? 0 : len / c.block;
+  if (!status && count > 0) {
+    // every task of a request checks all that the request touches, so that a
+    // request is appended whole or not at all
+    const int last = (int)((len + count - 1) / c.block);
+    bool bad_id = false, bad_node = false;
+    for (int i = first + t; i <= last; i += kT) {
+      const int id = c.block_table[b * c.max_blocks + i];
+      bad_id |= id < 0 || id >= c.n_blocks;
+    }
+    if (p.path)
+      for (int i = t; i < count; i += kT) {
+        const int n = p.path[b * p.path_len + i];
+        bad_node |= n < 0 || n >= p.N;
+      }
+    if (task_any<kT>(bad_id)) status = SPECDEC_ROW_BAD_CACHE;
+    if (task_any<kT>(bad_node)) status |= SPECDEC_ROW_BAD_TREE;
+  }
+  if (m == 0 && side == 0 && h == 0 && t == 0) {
+    p.new_length[b] = len + (status ? 0 : (int)count);
+    p.row_status[b] = status;
+  }
+  if (status || count == 0) return;
+
+  // this task's tokens: slots [off, off + take) of the block, tokens j0 ...
+  const long long start = (long long)(first + m) * c.block;
+  const int off = m == 0 ? len - first * c.block : 0;
+  const long long j0 = start + off - len;
+  if (j0 >= count) return;
+  const int take = (int)min((long long)(c.block - off), count - j0);
+  const int id = c.block_table[b * c.max_blocks + first + m];
+  const long long cell = (long long)id * c.Hkv + h;
+  uint8_t *codes = reinterpret_cast<uint8_t *>(side ? c.v : c.k) + cell * c.block * c.D;
+  float *scale = (side ? c.v_scale : c.k_scale) + cell;
+  const char *src = reinterpret_cast<const char *>(side ? p.v : p.k) + (long long)h * c.D * es;
+  const long long stride = (side ? p.v_stride : p.k_stride) * es;
+  const int per = c.D / 16, vecs = take * per;
+
+  float top = 0.0f;
+  for (int i = t; i < vecs; i += kT) {
+    const int j = i / per, e = (i - j * per) * 16;
+    const long long n = p.path ? p.path[b * p.path_len + j0 + j] : j0 + j;
+    float x[16];
+    load16<DT, kVec>(src + (b * p.N + n) * stride + e * es, x);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const float a = fabsf(x[k]);
+      if (a < INFINITY) top = fmaxf(top, a);
+    }
+  }
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  if (kT > 32) {
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 8; ++w) top = fmaxf(top, red[w]);
+  }
+  float s = scale_for(top);
+  if (off > 0) {
+    const float was = *scale;
+    task_sync<kT>();  // read by all before one of them writes it
+    if (was >= s) {
+      s = was;
+    } else {
+      // the tokens that stand before: 16 codes a thread, each thread its own
+      const float ratio = __fdiv_rn(was, s);
+      for (int i = t; i < off * per; i += kT) {
+        uint4 w = reinterpret_cast<uint4 *>(codes)[i];
+        uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t lo = e4m3x2_to_half2(a[k] & 0xFFFFu), hi = e4m3x2_to_half2(a[k] >> 16);
+          a[k] = pack_e4m3x2(half_bits_to_float(lo & 0xFFFFu) * ratio,
+                             half_bits_to_float(lo >> 16) * ratio) |
+                 pack_e4m3x2(half_bits_to_float(hi & 0xFFFFu) * ratio,
+                             half_bits_to_float(hi >> 16) * ratio)
+                     << 16;
+        }
+        reinterpret_cast<uint4 *>(codes)[i] = make_uint4(a[0], a[1], a[2], a[3]);
+      }
+    }
+  }
+  if (t == 0) *scale = s;
+  // x / s is exact for a power of two; an old scale of another kind needs the division
+  const bool pow2 = (__float_as_uint(s) & 0x7FFFFFu) == 0;
+  const float inv = pow2 ? __fdiv_rn(1.0f, s) : 0.0f;
+  for (int i = t; i < vecs; i += kT) {
+    const int j = i / per, e = (i - j * per) * 16;
+    const long long n = p.path ? p.path[b * p.path_len + j0 + j] : j0 + j;
+    float x[16];
+    load16<DT, kVec>(src + (b * p.N + n) * stride + e * es, x);
+    uint32_t a[4];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const float y = pow2 ? x[k] * inv : __fdiv_rn(x[k], s);
+      x[k] = finite(x[k]) ? y : __int_as_float(0x7fc00000);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      a[k] = pack_e4m3x2(x[4 * k], x[4 * k + 1]) | pack_e4m3x2(x[4 * k + 2], x[4 * k + 3]) << 16;
+    *reinterpret_cast<uint4 *>(codes + (long long)(off + j) * c.D + e) =
+        make_uint4(a[0], a[1], a[2], a[3]);
+  }
+}
+
+template <int DT, bool kVec>
+cudaError_t launch_vec(const AppendParams &p, cudaStream_t stream) {
+  const long long tasks = (long long)p.B * p.blocks * 2 * p.cache.Hkv;
+  if (p.N <= 64)
+    return launch_pdl(kv_append_kernel<DT, kVec, 32>, dim3((unsigned)((tasks + 7) / 8)), dim3(256),
+                      0, stream, p);
+  return launch_pdl(kv_append_kernel<DT, kVec, 256>, dim3((unsigned)tasks), dim3(256), 0, stream,
+                    p);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append(const AppendParams &p, cudaStream_t stream) {
+  const int es = p.dtype == SPECDEC_F32 ? 4 : 2;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p.k) | reinterpret_cast<uintptr_t>(p.v) |
+                       (uintptr_t)(p.k_stride * es) | (uintptr_t)(p.v_stride * es);
+  const bool vec = (at & 15) == 0;  // heads start on multiples of 16 elements
+  if (p.dtype == SPECDEC_F32)
+    return vec ? launch_vec<SPECDEC_F32, true>(p, stream)
+               : launch_vec<SPECDEC_F32, false>(p, stream);
+  return vec ? launch_vec<SPECDEC_BF16, true>(p, stream)
+             : launch_vec<SPECDEC_BF16, false>(p, stream);
+}
+
+}  // namespace specdec
