@@ -916,13 +916,16 @@ cudaError_t launch_type(const AttendParams &p, cudaStream_t stream) {
 }  // namespace
 
 size_t attend_workspace_bytes(long long B, int N, int Hq, int Hkv, int D, int dtype) {
-  (void)dtype;
   const int G = Hq / Hkv, s = splits_of(B, N, Hkv, G);
-  if (s == 1) return 0;
-  return (size_t)B * Hkv * row_tiles_of(N, G) * s * partial_floats(D) * sizeof(float);
+  const size_t stream =
+      s == 1 ? 0 : (size_t)B * Hkv * row_tiles_of(N, G) * s * partial_floats(D) * sizeof(float);
+  // which kernel a call takes depends on the pool too, which the sizes here do not name
+  const size_t tile = dtype == SPECDEC_BF16 && D <= 128 ? attend_tile_workspace_bytes(N, G, D) : 0;
+  return stream > tile ? stream : tile;
 }
 
 cudaError_t launch_attend(AttendParams p, cudaStream_t stream) {
+  if (attend_tile_applies(p)) return launch_attend_tile(p, stream);
   p.splits = splits_of(p.B, p.N, p.cache.Hkv, p.G);
   p.row_tiles = row_tiles_of(p.N, p.G);
   cudaError_t err = p.dtype == SPECDEC_F32 ? launch_type<true>(p, stream)

@@ -1,0 +1,1448 @@
+// Attention of drafted tokens over the 8-bit cache on the tensor cores
+// (specdec_attend, bfloat16 activations, heads of at most 128 elements).
+//
+// Per request, k/v head and up to RN rows (node n, query head g of the group),
+// tiles of 128 tokens go through
+//     S^T = K Q^T          [128 tokens, rows]     tcgen05.mma, e4m3
+//     P^T = 2^(S^T - m)    by one thread per token and half of the rows
+//     O^T += V^T P^T       [128 elements, rows]   tcgen05.mma, fp16
+// with m a running maximum per row.  Tokens stand on the 128 lanes of the
+// accumulators and rows on their columns, so that a product costs what its
+// rows need: with few rows (one token, G = 4) the pass stays bound by HBM, and
+// with many (a tree's 64 nodes, G = 4) it runs at the tensor cores' rate.
+//
+//   * K goes from the cache into the products as it is, e4m3.  A bfloat16 q has
+//     8 significant bits: scaled by a power of two per row it is the sum of two
+//     e4m3 values of 4 bits each, exactly for elements above 2^-10 of the row's
+//     largest (below, to 2^-19 of that).  Two products with K give q k^T.
+//   * V widens to fp16 exactly, in shared memory, four warps' work; P is fp16
+//     around 2^6 (11 bits, down to 2^-20 of the largest).  P in e4m3 would lose
+//     the many small weights under one large one.
+//   * the drafted tokens' own k and v are one more kind of tile: k in two e4m3
+//     terms as q, v in fp16, each scaled by a power of two per node.
+//   * m moves only when a score passes it by 2^8: the threads of a tile vote,
+//     and mostly nothing is reduced or rescaled.  Sums stay per thread and are
+//     reduced once, at the end.
+//   * V's block scales ride on P, over a running unit (of the largest so far).
+//
+// A persistent grid, one CTA per SM.  All tiles of all requests, heads and row
+// tiles form one line that is cut into equal parts, one per CTA, from the
+// lengths on the device: any mix of lengths keeps all SMs busy to the end.
+// What a cut divides is joined by a second kernel, in order.
+// Roles: warp 0 copies (TMA), warp 1 issues products, warps 2-5 widen V, stage
+// q and build drafted tiles, warps 6-13 take the softmax and write results.
+// Every wait is bounded in time.
+#include <cstddef>
+
+#include <cuda.h>
+
+#include "attention_common.cuh"
+
+namespace specdec {
+namespace {
+
+constexpr int kTok = 128;
+constexpr int kThreads = 448;
+constexpr int kRow = 128;              // bytes of a shared-memory row: one swizzle span
+constexpr int kTileBytes = kTok * kRow;
+constexpr int kMaxCtas = 160;
+constexpr long long kWaitCycles = 4000000000ll;  // about 2 s
+constexpr float kRaise = 8.0f;
+constexpr float kLift = 6.0f;
+constexpr float kUnseen = 1e30f;       // minus the maximum of a row that has seen nothing
+constexpr unsigned kAll = 0xffffffffu;
+
+template <int RN>
+struct Cfg {
+  static constexpr int kK = RN == 64 ? 3 : 2;  // stages of K codes
+  static constexpr int kV = RN == 64 ? 3 : 1;  // stages of V codes
+  static constexpr int kCols = RN == 64 ? 256 : 512;
+};
+
+// one CTA's part of the line of tiles
+struct Plan {
+  long long total, first, count;  // tiles in all, the part's first, the part's
+  int b, off;                     // first request, first tile of it
+};
+
+// The part that tile x belongs to, of n that split `total` tiles (part i begins
+// at tile total * i / n).
+// (Out of line: one copy of a 64-bit division.  The kernels' code has to stay
+// small, as five roles' loops share an SM's instruction cache.)
+__device__ __noinline__ long long divide(long long a, long long b) { return a / b; }
+__device__ __forceinline__ int part_of(long long x, long long total, int n) {
+  return (int)divide((x + 1) * n - 1, total);
+}
+
+struct Request {
+  int len, nodes, from;  // cached tokens, drafted ones, first token that the window leaves
+  int cached, tiles;     // tiles of cached tokens, and in all
+  int bad;
+};
+
+// A run of tiles of one unit (request, head, row tile).
+struct Segment {
+  int b, h, rt, t0, t1;  // b < 0: the end
+  Request r;
+  int whole;
+};
+
+template <int RN>
+struct Smem {
+  uint8_t k[Cfg<RN>::kK][kTileBytes];   // K codes [token][128 B], 128-byte swizzle
+  uint8_t v[Cfg<RN>::kV][kTileBytes];   // V codes, the same (drafted tiles: the low terms of k)
+  uint8_t vh[2][2][kTileBytes];         // V in fp16, [64 elements][token][128 B]
+  uint8_t pt[2][RN / 64][kTileBytes];   // P^T in fp16, [64 rows][token][128 B]
+  uint8_t q[2][RN * kRow];              // q: high and low terms [row][128 B]
+  float2 boxes[8][8];                   // k and v scales of a tile's pieces
+  float2 unit[2][kTok];                 // the same per token (k below 0: it is not finite)
+  uint32_t see[2][kTok][4];             // drafted tiles: the nodes that a node of the rows sees
+  alignas(16) float rf[4][RN];
+  float slope[4][RN];
+  int pos[4][RN];
+  alignas(16) float nm[RN];             // kLift - m
+  alignas(16) float fac[2][RN];         // factors of l and O when m or the unit moves
+  float red[4][RN];
+  float vred[2][4];
+  int vote[2][4];
+  alignas(16) float ones[RN / 2];
+  uint8_t node[4][RN];                  // of the nodes that the rows have
+  Segment seg[8];
+  int bad[8], dirty[8];
+  uint64_t k_full[Cfg<RN>::kK], k_empty[Cfg<RN>::kK], v_full[Cfg<RN>::kV], v_empty[Cfg<RN>::kV];
+  uint64_t seg_full[8], q_full, q_empty, s_full[2], s_empty[2], p_full[2], vh_full[2], pv_done[2];
+  uint64_t group[2], fin;
+  uint32_t tmem;
+  int give_up;
+  int done[2];                          // segments that a half of the softmax warps finished
+  long long scan[kThreads / 32 + 1];
+  Plan plan;
+};
+
+// ---------------------------------------------------------------------------
+// PTX
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void tma_rows(void *dst, const CUtensorMap *map, int row, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+      "%3}], [%4];" ::"r"(smem_addr(dst)),
+      "l"(map), "r"(0), "r"(row), "r"(smem_addr(bar))
+      : "memory");
+}
+__device__ __forceinline__ void mbar_expect_tx(uint64_t *bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)),
+               "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void fence_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ void fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t *bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+          smem_addr(bar))
+      : "memory");
+}
+template <bool kF8>
+__device__ __forceinline__ void mma_issue(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                          bool add) {
+  if (kF8)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+// Shared-memory operand, 128-byte swizzle.  group: bytes between groups of 8
+// rows; span: bytes between 64-element groups of an operand whose rows run
+// along the inner dimension.
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t group, uint32_t span) {
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(span >> 4) << 16 |
+         (uint64_t)(group >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+// float32 accumulators, M = 128, N = n; `outer`: both operands have their outer
+// dimension contiguous
+__device__ __forceinline__ uint32_t shape(int n, bool outer) {
+  return 1u << 4 | (outer ? 3u << 15 : 0u) | (uint32_t)(n >> 3) << 17 | 8u << 24;
+}
+__device__ __forceinline__ void tmem_load8(uint32_t at, float *x) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                 "=r"(r[7])
+               : "r"(at)
+               : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(r[i]);
+}
+// The wait names the registers, so that nothing reads them before it.
+__device__ __forceinline__ void tmem_wait8(float *x) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(x[0]), "+f"(x[1]), "+f"(x[2]), "+f"(x[3]), "+f"(x[4]), "+f"(x[5]),
+                 "+f"(x[6]), "+f"(x[7])::"memory");
+}
+__device__ __forceinline__ void tmem_store8(uint32_t at, const float *x) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at),
+               "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]),
+               "f"(x[7])
+               : "memory");
+}
+__device__ __forceinline__ float tmem_load1(uint32_t at) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;"
+               : "=r"(r)
+               : "r"(at)
+               : "memory");
+  return __uint_as_float(r);
+}
+__device__ __forceinline__ void tmem_store1(uint32_t at, float x) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(at), "f"(x) : "memory");
+}
+__device__ __forceinline__ void tmem_stored() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+using f2 = unsigned long long;  // two float32 values in one register pair
+__device__ __forceinline__ f2 pair(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(f2 v, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// float order as int order (NaN above everything or below)
+__device__ __forceinline__ int ordered(float x) {
+  const int i = __float_as_int(x);
+  return i >= 0 ? i : i ^ 0x7FFFFFFF;
+}
+__device__ __forceinline__ float unordered(int i) {
+  return __int_as_float(i >= 0 ? i : i ^ 0x7FFFFFFF);
+}
+
+// 2^k, k in [-126, 127].
+__device__ __forceinline__ float pow2i(int k) { return __uint_as_float((uint32_t)(k + 127) << 23); }
+// k with top / 2^k in [2^at, 2^(at + 1)), inside the range of pow2i(+-k)
+__device__ __forceinline__ int unit_exponent(float top, int at) {
+  return min(max((int)(__float_as_uint(top) >> 23) - 127 - at, -126), 126);
+}
+
+// ---------------------------------------------------------------------------
+// the line of tiles
+// ---------------------------------------------------------------------------
+__device__ __noinline__ Request request_of(const AttendParams &p, int b, int box) {
+  Request r;
+  r.bad = 0;
+  r.len = p.cache.length[b];
+  r.nodes = p.n_nodes ? p.n_nodes[b] : p.N;
+  if (r.len < 0 || (long long)r.len > (long long)p.cache.max_blocks * p.cache.block)
+    r.bad = SPECDEC_ROW_BAD_CACHE;
+  if (r.nodes < 0 || r.nodes > p.N) r.bad |= SPECDEC_ROW_BAD_TREE;
+  if (r.bad) r.len = r.nodes = 0;
+  r.from = p.window > 0 ? max(0, r.len - p.window + 1) / box * box : 0;
+  r.cached = r.nodes > 0 ? (r.len - r.from + kTok - 1) / kTok : 0;
+  // a request without tokens still has its rows to write
+  r.tiles = max(1, r.cached + (r.nodes + kTok - 1) / kTok);
+  return r;
+}
+
+// The part of CTA `i` of `n`; all threads of the CTA, `scan` shared.
+__device__ Plan make_plan(const AttendParams &p, int box, int i, int n, long long *scan,
+                          Plan *shared) {
+  const int t = threadIdx.x, threads = blockDim.x;
+  const int units = p.cache.Hkv * p.row_tiles;
+  const int per = (p.B + threads - 1) / threads;
+  long long mine = 0;
+#pragma unroll 1
+  for (int b = t * per; b < min(p.B, (t + 1) * per); ++b)
+    mine += (long long)request_of(p, b, box).tiles * units;
+  long long upto = mine;  // inclusive scan
+#pragma unroll 1
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long o = __shfl_up_sync(kAll, upto, d);
+    if ((t & 31) >= d) upto += o;
+  }
+  if ((t & 31) == 31) scan[t >> 5] = upto;
+  __syncthreads();
+  long long before = 0, total = 0;
+#pragma unroll 1
+  for (int w = 0; w < threads / 32; ++w) {
+    if (w < (t >> 5)) before += scan[w];
+    total += scan[w];
+  }
+  upto += before;
+  const long long first = divide(total * i, n), last = divide(total * (i + 1), n);
+  if (t == 0) {
+    shared->total = total;
+    shared->first = first;
+    shared->count = last - first;
+  }
+  if (first >= upto - mine && first < upto) {
+    long long at = upto - mine;
+    for (int b = t * per;; ++b) {
+      const long long here = (long long)request_of(p, b, box).tiles * units;
+      if (first < at + here) {
+        shared->b = b;
+        shared->off = (int)(first - at);
+        break;
+      }
+      at += here;
+    }
+  }
+  __syncthreads();
+  const Plan r = *shared;
+  __syncthreads();
+  return r;
+}
+
+// Segments of a CTA's part: runs of tiles of one unit (request, head, row tile).
+// Warp 0 walks them and publishes each in shared memory for the other roles.
+struct Walk {
+  long long left;
+  int b, off;
+  Request r;
+
+  __device__ Walk(const AttendParams &p, int box, const Plan &plan)
+      : left(plan.count), b(plan.b), off(plan.off) {
+    if (left > 0) r = request_of(p, b, box);
+  }
+  __device__ __forceinline__ bool next(const AttendParams &p, int box, Segment &s) {
+    s.b = -1;
+    if (left <= 0) return false;
+    const int units = p.cache.Hkv * p.row_tiles;
+    if (off >= r.tiles * units) {
+      ++b;
+      off = 0;
+      r = request_of(p, b, box);
+    }
+    const int unit = off / r.tiles;
+    s.b = b;
+    s.t0 = off - unit * r.tiles;
+    s.h = unit / p.row_tiles;
+    s.rt = unit - s.h * p.row_tiles;
+    s.t1 = (int)min((long long)r.tiles, s.t0 + left);
+    s.r = r;
+    s.whole = s.t0 == 0 && s.t1 == r.tiles;
+    left -= s.t1 - s.t0;
+    off += s.t1 - s.t0;
+    return true;
+  }
+};
+
+__device__ __noinline__ bool wait_on(uint64_t *bar, uint32_t parity, volatile int *give_up) {
+  const long long t0 = clock64();
+  bool ok;
+  while (!(ok = mbar_try_wait(bar, parity))) {
+    if (*give_up) break;
+    if (clock64() - t0 > kWaitCycles) {
+      *give_up = 1;
+      break;
+    }
+  }
+  return __all_sync(kAll, ok);
+}
+
+// 8 bfloat16 values from an address that is not a multiple of 16 bytes
+__device__ __noinline__ uint4 load8_narrow(const unsigned short *s) {
+  uint32_t a[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a[i] = (uint32_t)__ldg(s + 2 * i) | (uint32_t)__ldg(s + 2 * i + 1) << 16;
+  return make_uint4(a[0], a[1], a[2], a[3]);
+}
+
+// Whether a window hides part of cached tile t from some row.
+__device__ __forceinline__ bool partly_hidden(const AttendParams &p, const Request &r, int t) {
+  return p.window > 0 && r.from + t * kTok <= r.len + p.N - 1 - p.window;
+}
+
+// q . k of one row and one drafted token, from global memory, term by term.
+__device__ __noinline__ float plain_dot(const AttendParams &p, int b, int h, int row, int node) {
+  const int D = p.cache.D, n = row / p.G, hq = h * p.G + row - n * p.G;
+  float s = 0.0f;
+  for (int e = 0; e < D; ++e)
+    s += load_elem(p.q, SPECDEC_BF16, ((long long)b * p.N + n) * p.q_stride + (long long)hq * D + e) *
+         load_elem(p.k_new, SPECDEC_BF16,
+                   ((long long)b * p.N + node) * p.k_stride + (long long)h * D + e);
+  return s;
+}
+
+// The sum of what is not finite among the v that a node sees in tiles [t0, t1),
+// at element d: drafted tokens', and cached ones' at the window's edge.
+__device__ __noinline__ float stray(const AttendParams &p, int box, int b, int h, int t0, int t1,
+                                    int n, int pos, int d) {
+  const specdec_kv_cache &kv = p.cache;
+  const Request r = request_of(p, b, box);
+  float sum = 0.0f;
+  const int j0 = max(0, t0 - r.cached) * kTok, j1 = (t1 - r.cached) * kTok;
+  int a = n;
+  for (int step = 0; a >= 0 && (p.window == 0 || step < p.window); ++step) {
+    if (a >= j0 && a < j1) {
+      const float y = load_elem(p.v_new, SPECDEC_BF16,
+                                ((long long)b * p.N + a) * p.v_stride + (long long)h * kv.D + d);
+      if (!finite(y)) sum += y;
+    }
+    int up = a - 1;
+    if (p.parent && a > 0) {
+      up = p.parent[(long long)b * p.N + a];
+      if (up >= a) up = -1;
+    }
+    a = up;
+  }
+  for (int t = t0; t < min(t1, r.cached) && partly_hidden(p, r, t); ++t)
+    for (int i = 0; i < kTok; ++i) {
+      const int at = r.from + t * kTok + i;
+      if (at >= r.len || pos - at >= p.window) continue;
+      const int id = kv.block_table[(long long)b * kv.max_blocks + at / kv.block];
+      if (id < 0 || id >= kv.n_blocks) continue;
+      const uint8_t code = reinterpret_cast<const uint8_t *>(
+          kv.v)[(((long long)id * kv.Hkv + h) * kv.block + at % kv.block) * kv.D + d];
+      if ((code & 0x7Fu) == 0x7Fu) sum = __int_as_float(0x7fc00000);
+    }
+  return sum;
+}
+
+// A partial: for each row m, l, then its D elements; flags as l < 0.
+__host__ __device__ inline size_t partial_floats(int RN, int D) { return (size_t)RN * (D + 2); }
+
+// ---------------------------------------------------------------------------
+// the kernel
+// ---------------------------------------------------------------------------
+template <int RN, bool kPlain>
+struct Tile {
+  using S = Smem<RN>;
+  static constexpr int kK = Cfg<RN>::kK, kV = Cfg<RN>::kV;
+  const AttendParams &p;
+  S &sm;
+  const CUtensorMap *k_map, *v_map;
+  const int box, lane, warp;
+  int columns;  // rows of a tile, a multiple of 16
+
+  __device__ Tile(const AttendParams &p_, S &s_, const CUtensorMap *k_, const CUtensorMap *v_,
+                  int box_)
+      : p(p_), sm(s_), k_map(k_), v_map(v_), box(box_), lane(threadIdx.x & 31),
+        warp(threadIdx.x >> 5) {
+    columns = (min(RN, p.N * p.G) + 15) / 16 * 16;
+  }
+
+  // Bounded wait of a whole warp; false when it, or another, gave up.
+  __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity) {
+    if (__all_sync(kAll, mbar_try_wait(bar, parity))) return true;
+    return wait_on(bar, parity, &sm.give_up);
+  }
+  // Slot and parities of tile c in a ring of n: full is waited on with the
+  // first, empty (of the slot's last use) with the second.
+  static __device__ __forceinline__ uint32_t full_par(uint32_t c, int n) { return (c / n) & 1; }
+  static __device__ __forceinline__ uint32_t empty_par(uint32_t c, int n) { return ((c / n) & 1) ^ 1; }
+
+  // Segment i, published by warp 0 (a ring of eight is enough, since it is at
+  // most six tiles ahead of the softmax); false at the end or on giving up.
+  __device__ __forceinline__ bool segment(uint32_t i, bool &ok) {
+    ok = wait(&sm.seg_full[i & 7], (i >> 3) & 1);
+    return ok && sm.seg[i & 7].b >= 0;
+  }
+
+  // ------------------------------------------------------------ warp 0: copies
+  __device__ __forceinline__ void copies(const Plan &plan) {
+    const specdec_kv_cache &kv = p.cache;
+    uint32_t c = 0, index = 0;
+    Walk walk(p, box, plan);
+    bool ok = true;
+    for (; ok; ++index) {
+      Segment w;
+      const bool more = walk.next(p, box, w);
+      if (lane == 0) {
+        sm.seg[index & 7] = w;
+        mbar_arrive(&sm.seg_full[index & 7]);
+      }
+      if (!more) break;
+#pragma unroll 1
+      for (int t = w.t0; ok && t < w.t1; ++t, ++c) {
+        const int ks = c % kK, vs = c % kV;
+        if (t >= w.r.cached) {
+          // nothing to copy, but a phase missed here would make the slot's next
+          // wait take an old phase of the same parity for its own
+          if (!(ok = wait(&sm.k_empty[ks], empty_par(c, kK)))) break;
+          if (!(ok = wait(&sm.v_empty[vs], empty_par(c, kV)))) break;
+          continue;
+        }
+        const int token = w.r.from + t * kTok;
+        const int pieces = min(kTok, w.r.len - token + box - 1) / box;
+        int row = 0;
+        long long cell = 0;
+        const bool mine = lane < pieces;
+        if (mine) {
+          const int tok = token + lane * box;
+          int id = kv.block_table[(long long)w.b * kv.max_blocks + tok / kv.block];
+          if (id < 0 || id >= kv.n_blocks) {
+            id = 0;
+            sm.bad[index & 7] = SPECDEC_ROW_BAD_CACHE;
+          }
+          cell = (long long)id * kv.Hkv + w.h;
+          row = (int)(cell * kv.block + tok % kv.block);
+        }
+        const uint32_t bytes = (uint32_t)pieces * box * kRow;
+        if (!(ok = wait(&sm.k_empty[ks], empty_par(c, kK)))) break;
+        if (lane == 0) mbar_expect_tx(&sm.k_full[ks], bytes);
+        __syncwarp();
+        if (mine) tma_rows(sm.k[ks] + lane * box * kRow, k_map, row, &sm.k_full[ks]);
+        if (mine) sm.boxes[c & 7][lane] = make_float2(kv.k_scale[cell], kv.v_scale[cell]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.k_full[ks]);
+        if (!(ok = wait(&sm.v_empty[vs], empty_par(c, kV)))) break;
+        if (lane == 0) mbar_arrive_expect_tx(&sm.v_full[vs], bytes);
+        __syncwarp();
+        if (mine) tma_rows(sm.v[vs] + lane * box * kRow, v_map, row, &sm.v_full[vs]);
+      }
+    }
+    // Every copy has been waited on by its reader, unless somebody gave up: then
+    // copies in flight get time to land before the CTA may leave.
+    copied = c;
+  }
+
+  uint32_t copied;
+  __device__ void drain() {
+    for (uint32_t i = copied > kK ? copied - kK : 0; i < copied; ++i)
+      mbar_wait_bounded(&sm.k_full[i % kK], full_par(i, kK));
+    for (uint32_t i = copied > kV ? copied - kV : 0; i < copied; ++i)
+      mbar_wait_bounded(&sm.v_full[i % kV], full_par(i, kV));
+  }
+
+  // ------------------------------------------------------------ warp 1: products
+  __device__ __forceinline__ void scores(uint32_t c, bool drafted) {
+    if (lane == 0) {
+      const uint32_t d = sm.tmem + (c & 1) * RN, idesc = shape(columns, false);
+      const uint32_t k = smem_addr(sm.k[c % kK]), lo = smem_addr(sm.v[c % kV]);
+      const uint32_t qh = smem_addr(sm.q[0]), ql = smem_addr(sm.q[1]);
+      const int steps = (p.cache.D + 31) / 32;
+      // 32 elements a step: 32 bytes, 2 units of the descriptor's address
+      uint64_t ka = operand(k, 1024, 16), kl = operand(lo, 1024, 16);
+      uint64_t qa = operand(qh, 1024, 16), qb = operand(ql, 1024, 16);
+#pragma unroll 1
+      for (int i = 0; i < steps; ++i, ka += 2, kl += 2, qa += 2, qb += 2) {
+        mma_issue<true>(d, ka, qa, idesc, i > 0);
+        mma_issue<true>(d, ka, qb, idesc, true);
+        if (drafted) {
+          mma_issue<true>(d, kl, qa, idesc, true);
+          mma_issue<true>(d, kl, qb, idesc, true);
+        }
+      }
+      mma_commit(&sm.s_full[c & 1]);
+      mma_commit(&sm.k_empty[c % kK]);
+      if (drafted) {  // the low terms stood in a V slot, which four arrivals free
+        mbar_arrive(&sm.v_empty[c % kV]);
+        mbar_arrive(&sm.v_empty[c % kV]);
+        mbar_arrive(&sm.v_empty[c % kV]);
+        mma_commit(&sm.v_empty[c % kV]);
+      }
+    }
+    __syncwarp();
+  }
+
+  __device__ __forceinline__ bool outputs(uint32_t c, bool first) {
+    if (!wait(&sm.vh_full[c & 1], (c >> 1) & 1) || !wait(&sm.p_full[c & 1], (c >> 1) & 1))
+      return false;
+    fence_after();
+    if (lane == 0) {
+      const uint32_t d = sm.tmem + 2 * RN, idesc = shape(columns, true);
+      const uint32_t v = smem_addr(sm.vh[c & 1][0]), pt = smem_addr(sm.pt[c & 1][0]);
+      uint64_t va = operand(v, 1024, kTileBytes), pb = operand(pt, 1024, kTileBytes);
+#pragma unroll 1
+      for (int i = 0; i < kTok / 16; ++i, va += 128, pb += 128)
+        mma_issue<false>(d, va, pb, idesc, !first || i > 0);
+      mma_commit(&sm.pv_done[c & 1]);
+    }
+    __syncwarp();
+    return true;
+  }
+
+  __device__ __forceinline__ void products() {
+    uint32_t c = 0;
+    bool ok = true, pending = false, pending_first = false;
+    for (uint32_t index = 0; segment(index, ok); ++index) {
+      const int t0 = sm.seg[index & 7].t0, t1 = sm.seg[index & 7].t1;
+      const int cached = sm.seg[index & 7].r.cached;
+#pragma unroll 1
+      for (int t = t0; ok && t < t1; ++t, ++c) {
+        const bool first = t == t0, drafted = t >= cached;
+        // at a segment's start the products of the one before come first: q is
+        // staged meanwhile
+        if (first && pending) {
+          if (!(ok = outputs(c - 1, pending_first))) break;
+          pending = false;
+        }
+        if (first && !(ok = wait(&sm.q_full, index & 1))) break;
+        if (drafted) {
+          if (!(ok = wait(&sm.vh_full[c & 1], (c >> 1) & 1))) break;
+          if (lane == 0) {  // nobody copies into this tile's slots
+            mbar_arrive(&sm.k_full[c % kK]);
+            mbar_arrive(&sm.v_full[c % kV]);
+          }
+        } else if (!(ok = wait(&sm.k_full[c % kK], full_par(c, kK)))) {
+          break;
+        }
+        if (!(ok = wait(&sm.s_empty[c & 1], ((c >> 1) & 1) ^ 1))) break;
+        fence_after();
+        scores(c, drafted);
+        if (t == t1 - 1 && lane == 0) mma_commit(&sm.q_empty);
+        if (pending && !(ok = outputs(c - 1, pending_first))) break;
+        pending = true;
+        pending_first = first;
+      }
+      if (!ok) break;
+    }
+    if (ok && pending) outputs(c - 1, pending_first);
+    // products in flight end before the CTA may leave
+    if (lane == 0) mma_commit(&sm.fin);
+    __syncwarp();
+    mbar_wait_bounded(&sm.fin, 0);
+  }
+
+  // ------------------------------------------------------------ warps 2-5: operands
+  __device__ __forceinline__ int depth_of(int b, int n) const {
+    if (!p.parent) return n;
+    int depth = 0;
+    for (int a = n; a > 0; ++depth) {
+      const int up = p.parent[(long long)b * p.N + a];
+      if (up < 0 || up >= a) break;
+      a = up;
+    }
+    return depth;
+  }
+
+  // 8 consecutive bfloat16 values; `wide`: 16-byte aligned
+  __device__ __forceinline__ void load8(const void *base, long long at, bool wide, float *x) const {
+    const unsigned short *s = reinterpret_cast<const unsigned short *>(base) + at;
+    const uint4 w = wide ? __ldg(reinterpret_cast<const uint4 *>(s)) : load8_narrow(s);
+    const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = bf16_lo(a[i]);
+      x[2 * i + 1] = bf16_hi(a[i]);
+    }
+  }
+
+  // Largest finite size among the 16 lanes of a row, and whether all are finite.
+  __device__ __forceinline__ float row_top(const float *x, bool &all) const {
+    float top = 0.0f;
+    all = true;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float a = fabsf(x[i]);
+      if (a < INFINITY)
+        top = fmaxf(top, a);
+      else
+        all = false;
+    }
+#pragma unroll
+    for (int d = 8; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
+    all = ((__ballot_sync(kAll, all) >> (lane & 16)) & 0xFFFFu) == 0xFFFFu;
+    return top;
+  }
+
+  // x * inv as the sum of two e4m3 terms: 8 bytes each at element e of row r.
+  __device__ __forceinline__ void split(uint8_t *hi, uint8_t *lo, int r, int e, const float *x,
+                                        float inv) const {
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float a = x[2 * i] * inv, b = x[2 * i + 1] * inv;
+      h[i] = pack_e4m3x2(finite(a) ? a : __int_as_float(0x7fc00000),
+                         finite(b) ? b : __int_as_float(0x7fc00000));
+      const uint32_t w = e4m3x2_to_half2(h[i]);
+      l[i] = pack_e4m3x2(a - half_bits_to_float(w & 0xFFFFu), b - half_bits_to_float(w >> 16));
+    }
+    const int at = r * kRow + ((((e >> 4) ^ (r & 7)) << 4) | (e & 8));
+    *reinterpret_cast<uint2 *>(hi + at) = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+    *reinterpret_cast<uint2 *>(lo + at) = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
+  }
+
+  __device__ __forceinline__ void stage_q(const Segment &w, uint32_t index, int worker) {
+    const int D = p.cache.D, ring = index & 3, e = (lane & 15) * 8;
+    const bool wide = ((reinterpret_cast<uintptr_t>(p.q) | (uintptr_t)(p.q_stride * 2)) & 15) == 0;
+#pragma unroll 1
+    for (int r = worker * 2 + (lane >> 4); r < columns; r += 8) {
+      const int row = w.rt * RN + r, n = row / p.G;
+      const bool in = row < p.N * p.G && n < w.r.nodes;
+      const int hq = w.h * p.G + row - n * p.G;
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = 0.0f;
+      if (in && e < D)
+        load8(p.q, ((long long)w.b * p.N + n) * p.q_stride + (long long)hq * D + e, wide, x);
+      bool all;
+      const int ex = unit_exponent(row_top(x, all), 7);
+      split(sm.q[0], sm.q[1], r, e, x, pow2i(-ex));
+      if ((lane & 15) == 0) {
+        sm.node[ring][r] = (uint8_t)(n - w.rt * RN / p.G);
+        sm.rf[ring][r] = in ? p.scale * kLog2e * pow2i(ex) : 0.0f;
+        sm.pos[ring][r] = in ? w.r.len + ((p.window > 0 || p.slopes) ? depth_of(w.b, n) : 0) : -1;
+        sm.slope[ring][r] = (in && p.slopes) ? p.slopes[hq] * kLog2e : 0.0f;
+      }
+    }
+  }
+
+  // NaN codes of a tile that a window hides in part: out of the products, as
+  // they must not reach rows that do not see them (the results add them).
+  __device__ __noinline__ static bool sift(uint8_t *codes, int tid) {
+    bool odd = false;
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i) {  // the thread's own pieces, as widen reads them
+      const int at = (i >> 2) * 128 + tid, tok = at >> 3;
+      uint32_t *w = reinterpret_cast<uint32_t *>(codes + tok * kRow +
+                                                 (((at & 7) ^ (tok & 7)) << 4)) + (i & 3);
+      uint32_t keep = 0;
+      for (int s = 0; s < 32; s += 8)
+        if (((*w >> s) & 0x7Fu) != 0x7Fu) keep |= 0xFFu << s;
+      odd |= keep != kAll;
+      *w &= keep;
+    }
+    return odd;
+  }
+
+  // V codes of a cached tile to fp16; tokens past the length as zeros.
+  __device__ __forceinline__ void widen(const Segment &w, uint32_t index, int t, uint32_t c,
+                                        int worker) {
+    const int held = w.r.len - (w.r.from + t * kTok), tid = worker * 32 + lane;
+    uint8_t *src = sm.v[c % kV];
+    if (partly_hidden(p, w.r, t) && sift(src, tid)) sm.dirty[index & 7] = 1;
+    // a thread's pieces are 16 tokens apart: the same place in the swizzle
+    const int tok0 = tid >> 3, j = tid & 7, x7 = tok0 & 7, side = j >> 2, piece = (j & 3) * 2;
+    src += tok0 * kRow + ((j ^ x7) << 4);
+    // lanes of the two 64-element groups write odd and even pieces in turn:
+    // eight lanes cover eight different 16-byte banks
+    uint8_t *dst = sm.vh[c & 1][side] + tok0 * kRow;
+    uint8_t *d0 = dst + (((piece + side) ^ x7) << 4), *d1 = dst + (((piece + 1 - side) ^ x7) << 4);
+#pragma unroll 2
+    for (int i = 0; i < 8; ++i) {
+      uint4 x = *reinterpret_cast<const uint4 *>(src + i * 16 * kRow);
+      if (tok0 + 16 * i >= held) x = make_uint4(0u, 0u, 0u, 0u);
+      const uint4 lo = make_uint4(e4m3x2_to_half2(x.x & 0xFFFFu), e4m3x2_to_half2(x.x >> 16),
+                                  e4m3x2_to_half2(x.y & 0xFFFFu), e4m3x2_to_half2(x.y >> 16));
+      const uint4 hi = make_uint4(e4m3x2_to_half2(x.z & 0xFFFFu), e4m3x2_to_half2(x.z >> 16),
+                                  e4m3x2_to_half2(x.w & 0xFFFFu), e4m3x2_to_half2(x.w >> 16));
+      *reinterpret_cast<uint4 *>(d0 + i * 16 * kRow) = side ? hi : lo;
+      *reinterpret_cast<uint4 *>(d1 + i * 16 * kRow) = side ? lo : hi;
+    }
+    sm.unit[c & 1][tid] = sm.boxes[c & 7][tid / box];
+  }
+
+  // A tile of drafted tokens: nodes [j0, j0 + 128).
+  __device__ __forceinline__ void build(const Segment &w, uint32_t index, int t, uint32_t c,
+                                        int worker) {
+    const int D = p.cache.D, j0 = (t - w.r.cached) * kTok, e = (lane & 15) * 8;
+    const long long first = (long long)w.b * p.N;
+    const bool k_wide =
+        ((reinterpret_cast<uintptr_t>(p.k_new) | (uintptr_t)(p.k_stride * 2)) & 15) == 0;
+    const bool v_wide =
+        ((reinterpret_cast<uintptr_t>(p.v_new) | (uintptr_t)(p.v_stride * 2)) & 15) == 0;
+#pragma unroll 1
+    for (int r = worker * 2 + (lane >> 4); r < kTok; r += 8) {
+      const bool in = j0 + r < w.r.nodes;
+      float x[8], y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = y[i] = 0.0f;
+      if (in && e < D) {
+        load8(p.k_new, (first + j0 + r) * p.k_stride + (long long)w.h * D + e, k_wide, x);
+        load8(p.v_new, (first + j0 + r) * p.v_stride + (long long)w.h * D + e, v_wide, y);
+      }
+      bool all;
+      const int ek = unit_exponent(row_top(x, all), 7);
+      split(sm.k[c % kK], sm.v[c % kV], r, e, x, pow2i(-ek));
+      const float k_unit = all ? pow2i(ek) : -1.0f;
+      const int ev = unit_exponent(row_top(y, all), 10);
+      const float inv = pow2i(-ev);
+      if (!all) sm.dirty[index & 7] = 1;
+      uint32_t a[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        a[i] = pack_half2(finite(y[2 * i]) ? y[2 * i] * inv : 0.0f,
+                          finite(y[2 * i + 1]) ? y[2 * i + 1] * inv : 0.0f);
+      *reinterpret_cast<uint4 *>(sm.vh[c & 1][e >> 6] + r * kRow +
+                                 ((((e & 63) >> 3) ^ (r & 7)) << 4)) =
+          make_uint4(a[0], a[1], a[2], a[3]);
+      if ((lane & 15) == 0) sm.unit[c & 1][r] = make_float2(k_unit, pow2i(ev));
+    }
+    // what each node of the rows sees of this tile
+    const int tid = worker * 32 + lane, n0 = w.rt * RN / p.G;
+    const int n = n0 + tid;
+    uint32_t bits[4] = {0u, 0u, 0u, 0u};
+    if (tid <= (columns - 1) / p.G + 1 && n < w.r.nodes) {
+      int a = n;
+      for (int step = 0; a >= j0; ++step) {
+        if (a < j0 + kTok && (p.window == 0 || step < p.window))
+          bits[(a - j0) >> 5] |= 1u << ((a - j0) & 31);
+        int up = a - 1;
+        if (p.parent && a > 0) {
+          up = p.parent[first + a];
+          if (up >= a) up = -1;
+        }
+        a = up;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sm.see[c & 1][tid][i] = bits[i];
+    if (p.parent) {
+      bool wrong = false;
+#pragma unroll 1
+      for (int i = tid; i < w.r.nodes; i += 128) {
+        const int up = p.parent[first + i];
+        wrong |= i == 0 ? up != -1 : (up < 0 || up >= i);
+      }
+      if (wrong) atomicOr(&sm.bad[index & 7], SPECDEC_ROW_BAD_TREE);
+    }
+  }
+
+  __device__ __forceinline__ void operands() {
+    const int worker = warp - 2;
+    uint32_t c = 0;
+    bool ok = true;
+    for (uint32_t index = 0; segment(index, ok); ++index) {
+      const Segment &w = sm.seg[index & 7];
+      const int t0 = w.t0, t1 = w.t1, cached = w.r.cached;
+      if (!(ok = wait(&sm.q_empty, (index & 1) ^ 1))) break;
+      stage_q(w, index, worker);
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.q_full);
+#pragma unroll 1
+      for (int t = t0; ok && t < t1; ++t, ++c) {
+        const bool drafted = t >= cached;
+        if (drafted) {
+          if (!(ok = wait(&sm.k_empty[c % kK], empty_par(c, kK)))) break;
+          if (!(ok = wait(&sm.v_empty[c % kV], empty_par(c, kV)))) break;
+        } else if (!(ok = wait(&sm.v_full[c % kV], full_par(c, kV)))) {
+          break;
+        }
+        if (!(ok = wait(&sm.pv_done[c & 1], ((c >> 1) & 1) ^ 1))) break;
+        if (drafted)
+          build(w, index, t, c, worker);
+        else
+          widen(w, index, t, c, worker);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (!drafted) mbar_arrive(&sm.v_empty[c % kV]);
+          mbar_arrive(&sm.vh_full[c & 1]);
+        }
+        // as the copying warp: every phase of v_full is waited on
+        if (drafted) ok = wait(&sm.v_full[c % kV], full_par(c, kV));
+      }
+      if (!ok) break;
+    }
+  }
+
+  // ------------------------------------------------------------ warps 6-13: softmax
+  uint32_t group_phase;
+  // The four warps of one half of the rows.
+  __device__ __forceinline__ bool meet(int half) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.group[half]);
+    const bool ok = wait(&sm.group[half], group_phase);
+    group_phase ^= 1;
+    return ok;
+  }
+
+  __device__ __forceinline__ float bent(float y, int ring, int col, int token_pos) const {
+    if (p.softcap > 0.0f) {
+      // 1 - 2 / (1 + e^2u): absolute error below 2^-22
+      const float cap = p.softcap * kLog2e;
+      const float u = __fdividef(y, p.softcap);  // = 2u log2(e) / 2 of the natural argument
+      y = cap * (1.0f - __fdividef(2.0f, 1.0f + ex2_approx(2.0f * u)));
+    }
+    if (p.slopes) y -= sm.slope[ring][col] * (float)(sm.pos[ring][col] - token_pos);
+    return y;
+  }
+
+  // Scores of a tile that needs more than a factor, in place: bent, biased and
+  // masked, in base-2 units.  tok: the thread's token; drafted: a drafted tile.
+  __device__ __forceinline__ void bend(const Segment &w, int ring, int t, uint32_t c, bool drafted,
+                                       int tok, int c0, int mine, uint32_t s_at) {
+    const float2 unit = sm.unit[c & 1][tok];
+    const int at = w.r.from + t * kTok + tok, j = (t - w.r.cached) * kTok + tok;
+    const bool exists = drafted || at < w.r.len, special = drafted && unit.x < 0.0f;
+    const int position = !drafted ? at : p.slopes ? w.r.len + depth_of(w.b, min(j, p.N - 1)) : 0;
+    if (__any_sync(kAll, special))  // k is not finite: its products term by term
+#pragma unroll 1
+      for (int i = 0; i < mine; ++i) {
+        float s = tmem_load1(s_at + i);
+        const float rf = sm.rf[ring][c0 + i];
+        if (special && rf != 0.0f && j < w.r.nodes)
+          s = -plain_dot(p, w.b, w.h, w.rt * RN + c0 + i, j) * (p.scale * kLog2e / rf);
+        __syncwarp();
+        tmem_store1(s_at + i, s);
+        tmem_stored();
+      }
+#pragma unroll 1
+    for (int ch = 0; ch * 8 < mine; ++ch) {
+      float s[8];
+      tmem_load8(s_at + ch * 8, s);
+      tmem_wait8(s);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int col = c0 + ch * 8 + k, pos = sm.pos[ring][col];
+        bool seen = pos >= 0 && exists;
+        if (drafted)
+          seen = seen && ((sm.see[c & 1][sm.node[ring][col]][tok >> 5] >> (tok & 31)) & 1u);
+        else if (p.window > 0)
+          seen = seen && pos - at < p.window;
+        float y = s[k] * (unit.x * sm.rf[ring][col]);
+        if (!kPlain) y = bent(y, ring, col, position);
+        s[k] = seen ? y : -INFINITY;
+      }
+      tmem_store8(s_at + ch * 8, s);
+    }
+    tmem_stored();
+  }
+
+  // Sums of 8 values over a warp's lanes: lane 4 i holds that of value i.
+  __device__ __forceinline__ float sum8(const float *v) const {
+    float a[4], b[2];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const bool up = lane & 16;
+      a[k] = (up ? v[k + 4] : v[k]) + __shfl_xor_sync(kAll, up ? v[k] : v[k + 4], 16);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const bool up = lane & 8;
+      b[k] = (up ? a[k + 2] : a[k]) + __shfl_xor_sync(kAll, up ? a[k] : a[k + 2], 8);
+    }
+    const bool up = lane & 4;
+    float x = (up ? b[1] : b[0]) + __shfl_xor_sync(kAll, up ? b[0] : b[1], 4);
+    x += __shfl_xor_sync(kAll, x, 2);
+    return x + __shfl_xor_sync(kAll, x, 1);
+  }
+
+  __device__ __forceinline__ void softmax() {
+    constexpr int kCh = RN / 16;         // most chunks of 8 columns of a half
+    constexpr bool kHold = RN == 64;     // a thread's scores fit its registers
+    const int half = warp >= 10, quarter = warp & 3, tok = quarter * 32 + lane;
+    const int mine = columns / 2, c0 = half * mine;  // columns of this half, a multiple of 8
+    const bool leader = lane == 0 && quarter == 0;
+    const uint32_t lanes = sm.tmem + ((uint32_t)quarter << 21);  // TMEM lanes of this warp
+    const uint32_t o_at = lanes + 2 * RN + c0;
+    const specdec_kv_cache &kv = p.cache;
+    uint32_t c = 0;
+    group_phase = 0;
+    f2 l[RN / 4];
+    bool ok = true;
+    for (uint32_t index = 0; segment(index, ok); ++index) {
+      const Segment &w = sm.seg[index & 7];
+      const int ring = index & 3, t0 = w.t0, t1 = w.t1;
+      float vref = 0.0f;
+#pragma unroll
+      for (int i = 0; i < RN / 4; ++i) l[i] = 0ull;
+      // the rows have seen nothing yet
+      if (tok < mine) sm.nm[c0 + tok] = kUnseen;
+#pragma unroll 1
+      for (int t = t0; ok && t < t1; ++t, ++c) {
+        const bool drafted = t >= w.r.cached;
+        const uint32_t s_at = lanes + (c & 1) * RN + c0;
+        if (!(ok = wait(&sm.vh_full[c & 1], (c >> 1) & 1))) break;
+        if (!(ok = wait(&sm.s_full[c & 1], (c >> 1) & 1))) break;
+        fence_after();
+        const float2 unit = sm.unit[c & 1][tok];
+        // a plain tile's scores are a factor away; the others are written back
+        const int past = w.r.from + t * kTok + kTok - w.r.len;
+        const bool kept = !kPlain || drafted || past > 0 || partly_hidden(p, w.r, t);
+        if (kept) bend(w, ring, t, c, drafted, tok, c0, mine, s_at);
+        const float v_unit = drafted || past + tok < kTok ? unit.y : 0.0f;
+        const float k_unit = kept ? 1.0f : unit.x;
+        const f2 ks = pair(k_unit, k_unit);
+        const float *factor = kept ? sm.ones : sm.rf[ring] + c0;
+        const float *minus = sm.nm + c0;
+        float x[kHold ? RN / 2 : 8];
+        bool moved = false;
+        for (;;) {
+          float top = -INFINITY;
+          if (kHold) {
+#pragma unroll
+            for (int ch = 0; ch < kCh; ++ch)
+              if (ch * 8 < mine) tmem_load8(s_at + ch * 8, x + ch * 8);
+          }
+#pragma unroll
+          for (int ch = 0; ch < kCh; ++ch) {
+            if (ch * 8 >= mine) break;
+            float *s = x + (kHold ? ch * 8 : 0);
+            if (!kHold) tmem_load8(s_at + ch * 8, s);
+            tmem_wait8(s);
+#pragma unroll
+            for (int k = 0; k < 8; k += 4) {
+              const ulonglong2 r = *reinterpret_cast<const ulonglong2 *>(factor + ch * 8 + k);
+              const ulonglong2 n = *reinterpret_cast<const ulonglong2 *>(minus + ch * 8 + k);
+              unpair(fma2(pair(s[k], s[k + 1]), mul2(r.x, ks), n.x), s[k], s[k + 1]);
+              unpair(fma2(pair(s[k + 2], s[k + 3]), mul2(r.y, ks), n.y), s[k + 2], s[k + 3]);
+              top = fmaxf(fmaxf(top, fmaxf(s[k], s[k + 1])), fmaxf(s[k + 2], s[k + 3]));
+            }
+          }
+          if (moved) break;
+          // scores far above a maximum, or a larger unit of v: all four warps move
+          const bool first = t == t0;
+          if (__any_sync(kAll, top > kRaise + kLift || v_unit > vref) && lane == 0)
+            sm.vote[half][c & 3] = 1;
+          if (!(ok = meet(half))) break;
+          if (!first && !*(volatile int *)&sm.vote[half][c & 3]) break;
+          // maxima of the tile: a warp's by column, then the four warps'
+#pragma unroll 1
+          for (int ch = 0; ch * 8 < mine; ++ch) {
+            float y[8];
+            __syncwarp();
+            tmem_load8(s_at + ch * 8, y);
+            tmem_wait8(y);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              float z = y[k] * (k_unit * factor[ch * 8 + k]);
+              if (!(z == z)) z = INFINITY;  // its row becomes NaN
+              const int best = __reduce_max_sync(kAll, ordered(z));
+              if (lane == 0) sm.red[quarter][c0 + ch * 8 + k] = unordered(best);
+            }
+          }
+          const int vmax = __reduce_max_sync(kAll, __float_as_int(v_unit));  // units are >= 0
+          if (lane == 0) sm.vred[half][quarter] = __int_as_float(vmax);
+          if (!(ok = meet(half))) break;
+          const float unit_max = fmaxf(fmaxf(sm.vred[half][0], sm.vred[half][1]),
+                                       fmaxf(sm.vred[half][2], sm.vred[half][3]));
+          // headroom of 4, so that units of one size move once
+          const float to = unit_max > vref ? fminf(unit_max * 4.0f, 0x1p126f) : vref;
+          const float v_fac = to > 0.0f ? __fdividef(vref, to) : 1.0f;
+          vref = to;
+          if (tok < mine) {
+            const int col = c0 + tok;
+            const float best = fmaxf(fmaxf(sm.red[0][col], sm.red[1][col]),
+                                     fmaxf(sm.red[2][col], sm.red[3][col]));
+            const float nm = sm.nm[col];
+            float f = 1.0f;
+            if (best > -INFINITY && (nm == kUnseen || kLift - best < nm)) {
+              f = nm == kUnseen ? 0.0f : ex2_approx(kLift - best - nm);
+              sm.nm[col] = kLift - best;
+            }
+            sm.fac[0][col] = f;
+            sm.fac[1][col] = f * v_fac;
+          }
+          if (!first && !(ok = wait(&sm.pv_done[(c - 1) & 1], ((c - 1) >> 1) & 1))) break;
+          fence_after();
+          if (!(ok = meet(half))) break;
+          if (!first) {
+#pragma unroll 1
+            for (int ch = 0; ch * 8 < mine; ++ch) {
+              float o[8];
+              tmem_load8(o_at + ch * 8, o);
+              tmem_wait8(o);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) o[k] *= sm.fac[1][c0 + ch * 8 + k];
+              tmem_store8(o_at + ch * 8, o);
+            }
+            tmem_stored();
+#pragma unroll
+            for (int i = 0; i < RN / 4; ++i)
+              if (2 * i < mine)
+                l[i] = mul2(l[i], *reinterpret_cast<const f2 *>(&sm.fac[0][c0 + 2 * i]));
+          }
+          if (!kHold) break;
+          moved = true;  // once more, under the new maxima
+        }
+        if (!ok) break;
+        if (leader) sm.vote[half][(c + 2) & 3] = 0;
+        // P^T of two tiles ago has been read
+        if (!(ok = wait(&sm.pv_done[c & 1], ((c >> 1) & 1) ^ 1))) break;
+        const float ratio = vref > 0.0f ? __fdividef(v_unit, vref) : 0.0f;
+        const f2 r2 = pair(ratio, ratio);
+        uint8_t *pt = sm.pt[c & 1][0] + tok * kRow;
+#pragma unroll
+        for (int ch = 0; ch < kCh; ++ch) {
+          if (ch * 8 >= mine) break;
+          float *s = x + (kHold ? ch * 8 : 0);
+          if (!kHold) {
+            tmem_load8(s_at + ch * 8, s);
+            tmem_wait8(s);
+#pragma unroll
+            for (int k = 0; k < 8; k += 4) {
+              const ulonglong2 r = *reinterpret_cast<const ulonglong2 *>(factor + ch * 8 + k);
+              const ulonglong2 n = *reinterpret_cast<const ulonglong2 *>(minus + ch * 8 + k);
+              unpair(fma2(pair(s[k], s[k + 1]), mul2(r.x, ks), n.x), s[k], s[k + 1]);
+              unpair(fma2(pair(s[k + 2], s[k + 3]), mul2(r.y, ks), n.y), s[k + 2], s[k + 3]);
+            }
+          }
+          uint32_t out[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const f2 e = pair(ex2_approx(s[2 * k]), ex2_approx(s[2 * k + 1]));
+            l[ch * 4 + k] = add2(l[ch * 4 + k], e);
+            float a, b;
+            unpair(mul2(e, r2), a, b);
+            out[k] = pack_half2(a, b);
+          }
+          const int col = c0 + ch * 8;
+          *reinterpret_cast<uint4 *>(pt + (col >> 6) * kTileBytes +
+                                     ((((col & 63) >> 3) ^ (tok & 7)) << 4)) =
+              make_uint4(out[0], out[1], out[2], out[3]);
+        }
+        fence_async_smem();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sm.s_empty[c & 1]);
+          mbar_arrive(&sm.p_full[c & 1]);
+        }
+      }
+      if (!ok) break;
+
+      // the segment's sums, by column
+#pragma unroll
+      for (int ch = 0; ch < kCh; ++ch) {
+        if (ch * 8 >= mine) break;
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) unpair(l[ch * 4 + k], v[2 * k], v[2 * k + 1]);
+        const float sum = sum8(v);
+        if ((lane & 3) == 0) sm.red[quarter][c0 + ch * 8 + (lane >> 2)] = sum;
+      }
+      if (!(ok = wait(&sm.pv_done[(c - 1) & 1], ((c - 1) >> 1) & 1))) break;
+      fence_after();
+      if (!(ok = meet(half))) break;
+      // both halves are past the segment before; nobody is seven ahead
+      if (leader && half == 0) sm.bad[(index + 7) & 7] = sm.dirty[(index + 7) & 7] = 0;
+      const int bad = w.r.bad | *(volatile int *)&sm.bad[index & 7];
+      const bool dirty = *(volatile int *)&sm.dirty[index & 7] != 0, whole = w.whole;
+      float *part = p.part + (size_t)(2 * blockIdx.x + (t0 == 0)) * partial_floats(RN, kv.D);
+      if (tok < mine) {  // a thread for each row: its factor and its statistics
+        const int col = c0 + tok, row = w.rt * RN + col, n = row / p.G;
+        const float sum = (sm.red[0][col] + sm.red[1][col]) + (sm.red[2][col] + sm.red[3][col]);
+        const float nm = sm.nm[col];
+        const bool empty = bad || n >= w.r.nodes || (nm == kUnseen && sum == 0.0f);
+        const int at = (w.b * p.N + n) * p.Hq + w.h * p.G + row - n * p.G;
+        const bool in = row < p.N * p.G;
+        sm.red[0][col] = __int_as_float(in ? at : -1);  // nobody else reads this column
+        sm.fac[0][col] = empty ? 0.0f : whole ? __fdividef(vref, sum) : vref;
+        if (in && whole && p.lse)
+          p.lse[at] = empty ? -INFINITY : (log2f(sum) - nm) * 0.6931471805599453f;
+        if (in && !whole) {
+          part[(size_t)col * (kv.D + 2)] = empty ? -INFINITY : -nm;
+          part[(size_t)col * (kv.D + 2) + 1] = bad ? -(float)bad : empty ? 0.0f : sum;
+        }
+      }
+      if (!(ok = meet(half))) break;
+      if (dirty)  // what the products left out because it is not finite
+#pragma unroll 1
+        for (int i = 0; i < mine; ++i) {
+          float o = tmem_load1(o_at + i);
+          if (sm.fac[0][c0 + i] != 0.0f && __float_as_int(sm.red[0][c0 + i]) >= 0 && tok < kv.D)
+            o += stray(p, box, w.b, w.h, t0, t1, sm.node[ring][c0 + i] + w.rt * RN / p.G,
+                       sm.pos[ring][c0 + i], tok);
+          __syncwarp();
+          tmem_store1(o_at + i, o);
+          tmem_stored();
+        }
+#pragma unroll 1
+      for (int ch = 0; ch * 8 < mine; ++ch) {
+        float o[8];
+        __syncwarp();
+        tmem_load8(o_at + ch * 8, o);
+        tmem_wait8(o);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int col = c0 + ch * 8 + k, at = __float_as_int(sm.red[0][col]);
+          const float f = sm.fac[0][col];
+          if (at < 0 || tok >= kv.D) continue;
+          const float y = f != 0.0f ? o[k] * f : 0.0f;
+          if (whole)
+            reinterpret_cast<unsigned short *>(p.out)[(long long)at * kv.D + tok] =
+                (unsigned short)pack_bf16x2(y, 0.0f);
+          else
+            part[(size_t)col * (kv.D + 2) + 2 + tok] = y;
+        }
+      }
+      if (whole && leader && half == 0 && w.h == 0 && w.rt == 0) p.row_status[w.b] = bad;
+      fence_before();
+      if (leader) sm.done[half] = index + 1;
+      if (!(ok = meet(half))) break;
+    }
+  }
+
+  // After a wait ran out: the segments that were not finished get no result.
+  __device__ __noinline__ static void give_up_results(const AttendParams &p, int box,
+                                                      const Plan &plan, int finished, int columns) {
+    const specdec_kv_cache &kv = p.cache;
+    Walk walk(p, box, plan);
+    Segment w;
+    for (int index = 0; walk.next(p, box, w); ++index) {
+      if (index < finished) continue;
+      float *part = p.part + (size_t)(2 * blockIdx.x + (w.t0 == 0)) * partial_floats(RN, kv.D);
+      for (int col = threadIdx.x; col < columns; col += kThreads) {
+        const int row = w.rt * RN + col, n = row / p.G;
+        if (row >= p.N * p.G) continue;
+        const long long at = ((long long)w.b * p.N + n) * p.Hq + w.h * p.G + row - n * p.G;
+        if (w.whole) {
+#pragma unroll 1
+          for (int d = 0; d < kv.D; ++d) reinterpret_cast<unsigned short *>(p.out)[at * kv.D + d] = 0;
+          if (p.lse) p.lse[at] = -INFINITY;
+        } else {
+          part[(size_t)col * (kv.D + 2)] = -INFINITY;
+          part[(size_t)col * (kv.D + 2) + 1] = -(float)SPECDEC_ROW_INTERNAL;
+        }
+      }
+      if (threadIdx.x == 0) p.row_status[w.b] = SPECDEC_ROW_INTERNAL;
+    }
+  }
+};
+
+template <int RN, bool kPlain>
+__global__ void __launch_bounds__(kThreads, 1)
+    attend_tile_kernel(const __grid_constant__ AttendParams p,
+                       const __grid_constant__ CUtensorMap k_map,
+                       const __grid_constant__ CUtensorMap v_map, int box) {
+  extern __shared__ __align__(1024) uint8_t raw[];
+  using S = Smem<RN>;
+  S &sm = *reinterpret_cast<S *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  const int tid = threadIdx.x, warp = tid >> 5;
+  if (tid == 0) {
+    for (int i = 0; i < Cfg<RN>::kK; ++i) {
+      mbar_init(&sm.k_full[i], 1);
+      mbar_init(&sm.k_empty[i], 1);
+    }
+    for (int i = 0; i < Cfg<RN>::kV; ++i) {
+      mbar_init(&sm.v_full[i], 1);
+      mbar_init(&sm.v_empty[i], 4);
+    }
+    mbar_init(&sm.q_full, 4);
+    mbar_init(&sm.q_empty, 1);
+    mbar_init(&sm.fin, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.s_empty[i], 8);
+      mbar_init(&sm.p_full[i], 8);
+      mbar_init(&sm.vh_full[i], 4);
+      mbar_init(&sm.pv_done[i], 1);
+      mbar_init(&sm.group[i], 4);
+      sm.done[i] = 0;
+      for (int k = 0; k < 4; ++k) sm.vote[i][k] = 0;
+    }
+    for (int i = 0; i < 8; ++i) {
+      sm.bad[i] = sm.dirty[i] = 0;
+      mbar_init(&sm.seg_full[i], 1);
+    }
+    sm.give_up = 0;
+    fence_mbar_init();
+    fence_async_smem();
+  }
+  if (tid < RN / 2) sm.ones[tid] = 1.0f;
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(&sm.tmem)),
+                 "r"(Cfg<RN>::kCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const Plan plan = make_plan(p, box, blockIdx.x, gridDim.x, sm.scan, &sm.plan);
+  Tile<RN, kPlain> tile(p, sm, &k_map, &v_map, box);
+  if (warp == 0)
+    tile.copies(plan);
+  else if (warp == 1)
+    tile.products();
+  else if (warp < 6)
+    tile.operands();
+  else
+    tile.softmax();
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (sm.give_up) {
+    if (warp == 0) tile.drain();
+    tile.give_up_results(p, box, plan, min(sm.done[0], sm.done[1]), tile.columns);
+    __syncthreads();
+  }
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(sm.tmem),
+                 "r"(Cfg<RN>::kCols));
+}
+
+// Joins the units that the cuts between CTAs divide.  Block (i, part): the unit
+// that CTA i - 1 began and CTA i goes on with, an eighth of its rows.
+constexpr int kJoinParts = 8;
+__global__ void __launch_bounds__(256)
+    attend_tile_join_kernel(const AttendParams p, int box, int ctas, int RN) {
+  __shared__ long long scan[33];
+  __shared__ Plan shared;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int i = blockIdx.x + 1, D = p.cache.D;
+  const Plan plan = make_plan(p, box, i, ctas, scan, &shared);
+  if (plan.count == 0) return;
+  Walk walk(p, box, plan);
+  Segment w;
+  walk.next(p, box, w);
+  if (w.t0 == 0) return;  // a unit begins here
+  const long long u0 = plan.first - w.t0;
+  const int begun = part_of(u0, plan.total, ctas);
+  if (part_of(plan.first - 1, plan.total, ctas) != begun) return;  // another CTA was here before
+  // the beginning is in slot 1 of its CTA, what follows in slot 0 of theirs; with
+  // fewer tiles than CTAs some have none, and each other has one
+  const long long u1 = u0 + w.r.tiles;
+  const bool few = plan.total < ctas;
+  const int parts = few ? (int)(u1 - plan.first) : part_of(u1 - 1, plan.total, ctas) - i + 1;
+  const size_t size = partial_floats(RN, D);
+  const float *head = p.part + (size_t)(2 * begun + 1) * size;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int any_bad = 0;
+  for (int col = blockIdx.y * 8 + warp; col < RN; col += 8 * kJoinParts) {
+    const int row = w.rt * RN + col, n = row / p.G;
+    if (row >= p.N * p.G) break;
+    auto record = [&](int s) {
+      const int at = few && s > 0 ? part_of(plan.first + s - 1, plan.total, ctas) : i + s - 1;
+      return (s == 0 ? head : p.part + (size_t)(2 * at) * size) + (size_t)col * (D + 2);
+    };
+    float all = -INFINITY, sum = 0.0f;
+    int bad = 0;
+    for (int s = lane; s <= parts; s += 32) {
+      const float *rec = record(s);
+      all = fmaxf(all, rec[0]);
+      if (rec[1] < 0.0f) bad |= (int)-rec[1];
+    }
+    bad = __reduce_or_sync(kAll, bad);
+    any_bad |= bad;
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) all = fmaxf(all, __shfl_xor_sync(kAll, all, d));
+    const bool empty = bad || all == -INFINITY;
+    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s = 0; !empty && s <= parts; ++s) {
+      const float *rec = record(s);
+      const float m = rec[0];
+      if (m == -INFINITY) continue;
+      const float f = ex2_approx(m - all);
+      sum += rec[1] * f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (lane + 32 * k < D) acc[k] += f * rec[2 + lane + 32 * k];
+    }
+    const float inv = empty ? 0.0f : 1.0f / sum;
+    const long long at = ((long long)w.b * p.N + n) * p.Hq + w.h * p.G + row - n * p.G;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (lane + 32 * k < D)
+        reinterpret_cast<unsigned short *>(p.out)[at * D + lane + 32 * k] =
+            (unsigned short)pack_bf16x2(empty ? 0.0f : acc[k] * inv, 0.0f);
+    if (p.lse && lane == 0)
+      p.lse[at] = empty ? -INFINITY : (all + log2f(sum)) * 0.6931471805599453f;
+  }
+  if (w.h == 0 && w.rt == 0 && blockIdx.y == 0 && threadIdx.x == 0) p.row_status[w.b] = any_bad;
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                              const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                              const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+  static std::atomic<EncodeFn> cached{nullptr};
+  EncodeFn f = cached.load(std::memory_order_acquire);
+  if (f) return f;
+  void *sym = nullptr;
+  cudaDriverEntryPointQueryResult found;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &sym, 12000, cudaEnableDefault,
+                                       &found) !=
+          cudaSuccess ||
+      found != cudaDriverEntryPointSuccess)
+    return nullptr;
+  f = reinterpret_cast<EncodeFn>(sym);
+  cached.store(f, std::memory_order_release);
+  return f;
+}
+
+// The pool as rows of D bytes (a token of a head each); boxes of `box` rows and
+// 128 bytes, what lies past D read as zeros.
+bool encode(CUtensorMap *map, void *codes, const specdec_kv_cache &kv, int box) {
+  const EncodeFn f = encode_fn();
+  if (!f) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)kv.D, (cuuint64_t)kv.n_blocks * kv.Hkv * kv.block};
+  const cuuint64_t strides[1] = {(cuuint64_t)kv.D};
+  const cuuint32_t size[2] = {(cuuint32_t)kRow, (cuuint32_t)box}, step[2] = {1, 1};
+  return f(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, codes, dims, strides, size, step,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int box_rows(int block) {  // the largest power of two that divides the block and the tile
+  int box = 16;
+  while (box < kTok && block % (2 * box) == 0) box *= 2;
+  return box;
+}
+
+int rows_of(int N, int G) { return N * G <= 64 ? 64 : 128; }
+
+template <int RN, bool kPlain>
+cudaError_t launch_rn(AttendParams p, cudaStream_t stream) {
+  static DeviceOnce once;
+  const int smem = (int)sizeof(Smem<RN>) + 1024;
+  static_assert(offsetof(Smem<RN>, rf) % 16 == 0 && offsetof(Smem<RN>, nm) % 16 == 0 &&
+                    offsetof(Smem<RN>, ones) % 16 == 0 && offsetof(Smem<RN>, fac) % 16 == 0,
+                "read in 16-byte vectors");
+  static_assert(sizeof(Smem<RN>) + 1024 <= 232448, "shared memory of a CTA");
+  cudaError_t err = smem_opt_in_once(once, attend_tile_kernel<RN, kPlain>, smem);
+  if (err != cudaSuccess) return err;
+  CUtensorMap k_map, v_map;
+  const int box = box_rows(p.cache.block);
+  if (!encode(&k_map, p.cache.k, p.cache, box) || !encode(&v_map, p.cache.v, p.cache, box))
+    return cudaErrorInvalidValue;
+  p.row_tiles = (p.N * p.G + RN - 1) / RN;
+  const int sms = device_sm_count();
+  const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
+  err = launch_pdl(attend_tile_kernel<RN, kPlain>, dim3((unsigned)ctas), dim3(kThreads),
+                   (size_t)smem, stream, p, k_map, v_map, box);
+  if (err != cudaSuccess) return err;
+  return launch_pdl(attend_tile_join_kernel, dim3((unsigned)(ctas - 1), kJoinParts), dim3(256), 0,
+                    stream, p, box, ctas, RN);
+}
+
+}  // namespace
+
+size_t attend_tile_workspace_bytes(int N, int G, int D) {
+  return (size_t)2 * kMaxCtas * partial_floats(rows_of(N, G), D) * sizeof(float);
+}
+
+bool attend_tile_applies(const AttendParams &p) {
+  const specdec_kv_cache &kv = p.cache;
+  return p.dtype == SPECDEC_BF16 && kv.D <= kRow &&
+         (long long)kv.n_blocks * kv.Hkv * kv.block < (1ll << 31) - kTok;
+}
+
+cudaError_t launch_attend_tile(const AttendParams &p, cudaStream_t stream) {
+  const bool plain = p.softcap == 0.0f && !p.slopes;
+  if (rows_of(p.N, p.G) == 64)
+    return plain ? launch_rn<64, true>(p, stream) : launch_rn<64, false>(p, stream);
+  return plain ? launch_rn<128, true>(p, stream) : launch_rn<128, false>(p, stream);
+}
+
+}  // namespace specdec

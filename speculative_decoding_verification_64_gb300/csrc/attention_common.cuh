@@ -48,6 +48,10 @@ struct AttendParams {
 cudaError_t launch_rope(const RopeParams &p, cudaStream_t stream);
 cudaError_t launch_kv_append(const AppendParams &p, cudaStream_t stream);
 cudaError_t launch_attend(AttendParams p, cudaStream_t stream);
+// attend_tile.cu: the tensor-core kernel, for the calls that it takes
+bool attend_tile_applies(const AttendParams &p);
+size_t attend_tile_workspace_bytes(int N, int G, int D);
+cudaError_t launch_attend_tile(const AttendParams &p, cudaStream_t stream);
 size_t attend_workspace_bytes(long long B, int N, int Hq, int Hkv, int D, int dtype);
 
 #ifdef __CUDACC__

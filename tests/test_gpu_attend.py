@@ -94,6 +94,25 @@ def test_chains(sd, dtype, lens, N, Hq, Hkv, D, block, pad):
     assert torch.equal(r.out, again.out) and torch.equal(r.lse, again.lse)
 
 
+@pytest.mark.parametrize("B,N,Hq,Hkv,most,window", [(100, 3, 16, 8, 900, 0), (48, 17, 32, 8, 600, 0),
+                                                    (90, 2, 8, 8, 700, 300), (300, 1, 2, 2, 400, 0)])
+def test_many_requests(sd, B, N, Hq, Hkv, most, window):
+    """More requests and heads than the device has SMs, of every length: a CTA works through
+    several of them, whole and in part, and tiles of cached and of drafted tokens alternate."""
+    rng = np.random.default_rng(B)
+    D, block = 64, 32
+    lens = [int(n) for n in rng.integers(0, most, B)]
+    lens[::7] = [0] * len(lens[::7])
+    nodes = [int(n) for n in rng.integers(0, N + 1, B)]
+    q, k, v = tokens(rng, B, N, Hq, Hkv, D, torch.bfloat16)
+    cache = ref.make_cache(rng, lens, [0] * B, block, Hkv, D)
+    n_nodes = torch.tensor(nodes, dtype=torch.int32).cuda()
+    r = sd.attend(q, k, v, ref.on_gpu(cache), n_nodes=n_nodes, window=window)
+    check(r, q, k, v, cache, block, None, nodes, D ** -0.5, window=window)
+    again = sd.attend(q, k, v, ref.on_gpu(cache), n_nodes=n_nodes, window=window)
+    assert torch.equal(r.out, again.out) and torch.equal(r.lse, again.lse)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("softcap,bias,window", [(0.0, False, 0), (30.0, False, 0), (0.0, True, 0),
                                                  (0.0, False, 50), (20.0, True, 7), (0.0, True, 1)])
