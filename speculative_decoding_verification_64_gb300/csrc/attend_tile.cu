@@ -46,7 +46,7 @@ constexpr int kThreads = 448;
 constexpr int kRow = 128;              // bytes of a shared-memory row: one swizzle span
 constexpr int kTileBytes = kTok * kRow;
 constexpr int kMaxCtas = 160;
-constexpr long long kWaitCycles = 4000000000ll;  // about 2 s
+constexpr int kWaitTries = 1000000;
 constexpr float kRaise = 8.0f;
 constexpr float kLift = 6.0f;
 constexpr float kUnseen = 1e30f;       // minus the maximum of a row that has seen nothing
@@ -54,9 +54,19 @@ constexpr unsigned kAll = 0xffffffffu;
 
 template <int RN>
 struct Cfg {
-  static constexpr int kK = RN == 64 ? 3 : 2;  // stages of K codes
-  static constexpr int kV = RN == 64 ? 3 : 1;  // stages of V codes
-  static constexpr int kCols = RN == 64 ? 256 : 512;
+  // Up to 64 rows the two softmax groups take the tiles in turn, each with an
+  // output accumulator, maxima and sums of its own, joined at a segment's end; a
+  // tile's fixed costs (waits, votes, fences) then overlap.  With 128 rows a
+  // thread could not hold the sums: the groups take half of the rows each.
+  static constexpr bool kTurns = RN <= 64;
+  static constexpr int kCols = kTurns ? RN : RN / 2;  // most columns of a softmax thread
+  static constexpr bool kHold = RN == 32;             // its scores stay in registers
+  static constexpr int kK = RN <= 64 ? 3 : 2;         // stages of K codes
+  static constexpr int kV = RN == 32 ? 3 : RN == 64 ? 2 : 1;  // stages of V codes
+  static constexpr int kQ = kTurns ? 2 : 1;           // stages of q: the next segment's ahead
+  static constexpr int kLag = kTurns ? 2 : 1;         // tiles whose outputs follow their scores
+  static constexpr int kTmem = RN == 32 ? 128 : RN == 64 ? 256 : 512;
+  static constexpr int kSpans = RN <= 64 ? 1 : 2;     // 64-row groups of P^T
 };
 
 // one CTA's part of the line of tiles
@@ -92,26 +102,29 @@ struct Smem {
   uint8_t k[Cfg<RN>::kK][kTileBytes];   // K codes [token][128 B], 128-byte swizzle
   uint8_t v[Cfg<RN>::kV][kTileBytes];   // V codes, the same (drafted tiles: the low terms of k)
   uint8_t vh[2][2][kTileBytes];         // V in fp16, [64 elements][token][128 B]
-  uint8_t pt[2][RN / 64][kTileBytes];   // P^T in fp16, [64 rows][token][128 B]
-  uint8_t q[2][RN * kRow];              // q: high and low terms [row][128 B]
+  uint8_t pt[2][Cfg<RN>::kSpans][kTileBytes];  // P^T in fp16, [64 rows][token][128 B]
+  uint8_t q[Cfg<RN>::kQ][2][RN * kRow];  // q: high and low terms [row][128 B]
   float2 boxes[8][8];                   // k and v scales of a tile's pieces
   float2 unit[2][kTok];                 // the same per token (k below 0: it is not finite)
-  uint32_t see[2][kTok][4];             // drafted tiles: the nodes that a node of the rows sees
+  alignas(16) uint32_t see[2][4][RN];   // drafted tiles: bits of the nodes that a row sees
   alignas(16) float rf[4][RN];
   float slope[4][RN];
   int pos[4][RN];
-  alignas(16) float nm[RN];             // kLift - m
-  alignas(16) float fac[2][RN];         // factors of l and O when m or the unit moves
-  float red[4][RN];
+  // per softmax group, by column
+  alignas(16) float nm[2][Cfg<RN>::kCols];      // kLift - m
+  alignas(16) float fac[2][2][Cfg<RN>::kCols];  // factors of l and O when m or the unit moves
+  float red[2][4][Cfg<RN>::kCols];
+  float vlast[2];
   float vred[2][4];
   int vote[2][4];
-  alignas(16) float ones[RN / 2];
+  alignas(16) float ones[Cfg<RN>::kCols];
   uint8_t node[4][RN];                  // of the nodes that the rows have
   Segment seg[8];
   int bad[8], dirty[8];
   uint64_t k_full[Cfg<RN>::kK], k_empty[Cfg<RN>::kK], v_full[Cfg<RN>::kV], v_empty[Cfg<RN>::kV];
-  uint64_t seg_full[8], q_full, q_empty, s_full[2], s_empty[2], p_full[2], vh_full[2], pv_done[2];
-  uint64_t group[2], fin;
+  uint64_t seg_full[8], box_full[8], q_full[Cfg<RN>::kQ], q_empty[Cfg<RN>::kQ];
+  uint64_t s_full[2], s_empty[2], p_full[2], vh_full[2], pv_done[2];
+  uint64_t group[2], both, fin;
   uint32_t tmem;
   int give_up;
   int done[2];                          // segments that a half of the softmax warps finished
@@ -129,11 +142,6 @@ __device__ __forceinline__ void tma_rows(void *dst, const CUtensorMap *map, int 
       "l"(map), "r"(0), "r"(row), "r"(smem_addr(bar))
       : "memory");
 }
-__device__ __forceinline__ void mbar_expect_tx(uint64_t *bar, uint32_t bytes) {
-  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)),
-               "r"(bytes)
-               : "memory");
-}
 __device__ __forceinline__ void fence_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
@@ -142,6 +150,13 @@ __device__ __forceinline__ void fence_before() {
 }
 __device__ __forceinline__ void fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ bool elected() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r));
+  return r != 0;
 }
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
   asm volatile(
@@ -198,6 +213,19 @@ __device__ __forceinline__ void tmem_store8(uint32_t at, const float *x) {
                "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]),
                "f"(x[7])
                : "memory");
+}
+__device__ __forceinline__ void tmem_load4(uint32_t at, float *x) {
+  uint32_t r[4];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_wait4(float *x) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(x[0]), "+f"(x[1]), "+f"(x[2]), "+f"(x[3])::"memory");
 }
 __device__ __forceinline__ float tmem_load1(uint32_t at) {
   uint32_t r;
@@ -357,17 +385,59 @@ struct Walk {
   }
 };
 
-__device__ __noinline__ bool wait_on(uint64_t *bar, uint32_t parity, volatile int *give_up) {
-  const long long t0 = clock64();
-  bool ok;
-  while (!(ok = mbar_try_wait(bar, parity))) {
-    if (*give_up) break;
-    if (clock64() - t0 > kWaitCycles) {
-      *give_up = 1;
-      break;
-    }
+// Waits until the phase of `parity` is complete.  Gives up after kWaitTries
+// tries of up to about 2 us each (at least a few 10 ms in all, where no wait of
+// a working kernel takes 1 ms), and says so in shared memory at `give_up`.
+__device__ __forceinline__ bool wait_lane(uint32_t bar, uint32_t parity, uint32_t give_up) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+      "mov.u32 n, %4;\n\t"
+      "AGAIN:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 2000;\n\t"
+      "@p bra DONE;\n\t"
+      "sub.u32 n, n, 1;\n\t"
+      "setp.ne.u32 q, n, 0;\n\t"
+      "@q bra AGAIN;\n\t"
+      "st.volatile.shared.u32 [%3], 1;\n\t"
+      "DONE:\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(give_up), "n"(kWaitTries)
+      : "memory");
+  return ok != 0;
+}
+
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {  // of unsigned 16-bit halves
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t half2_to_e4m3x2(uint32_t h) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f16x2 t, %1;\n\tcvt.u32.u16 %0, t;\n\t}"
+      : "=r"(r)
+      : "r"(h));
+  return r;
+}
+__device__ __forceinline__ uint32_t sub_half2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// The largest finite size (bfloat16 bits) among the 16 lanes of a row.
+__device__ __noinline__ uint32_t finite_top(uint4 w) {
+  const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+  uint32_t m = 0;
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t x = (i < 2 ? a[0] : i < 4 ? a[1] : i < 6 ? a[2] : a[3]) >> (16 * (i & 1)) & 0x7FFFu;
+    if (x < 0x7F80u) m = max(m, x);
   }
-  return __all_sync(kAll, ok);
+#pragma unroll 1
+  for (int d = 8; d >= 1; d >>= 1) m = max(m, __shfl_xor_sync(kAll, m, d));
+  return m;
 }
 
 // 8 bfloat16 values from an address that is not a multiple of 16 bytes
@@ -443,19 +513,21 @@ struct Tile {
   S &sm;
   const CUtensorMap *k_map, *v_map;
   const int box, lane, warp;
+  const int box_shift;
+  const uint32_t g_magic;  // ceil(2^32 / G): row / G for rows below 2^16 * G
   int columns;  // rows of a tile, a multiple of 16
 
   __device__ Tile(const AttendParams &p_, S &s_, const CUtensorMap *k_, const CUtensorMap *v_,
                   int box_)
       : p(p_), sm(s_), k_map(k_), v_map(v_), box(box_), lane(threadIdx.x & 31),
-        warp(threadIdx.x >> 5) {
+        warp(threadIdx.x >> 5), box_shift(box_ == 128 ? 7 : box_ == 64 ? 6 : box_ == 32 ? 5 : 4),
+        g_magic((uint32_t)(0xFFFFFFFFu / (uint32_t)p_.G) + 1u) {
     columns = (min(RN, p.N * p.G) + 15) / 16 * 16;
   }
 
   // Bounded wait of a whole warp; false when it, or another, gave up.
   __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity) {
-    if (__all_sync(kAll, mbar_try_wait(bar, parity))) return true;
-    return wait_on(bar, parity, &sm.give_up);
+    return __all_sync(kAll, wait_lane(smem_addr(bar), parity, smem_addr(&sm.give_up)));
   }
   // Slot and parities of tile c in a ring of n: full is waited on with the
   // first, empty (of the slot's last use) with the second.
@@ -463,63 +535,80 @@ struct Tile {
   static __device__ __forceinline__ uint32_t empty_par(uint32_t c, int n) { return ((c / n) & 1) ^ 1; }
 
   // Segment i, published by warp 0 (a ring of eight is enough, since it is at
-  // most six tiles ahead of the softmax); false at the end or on giving up.
+  // most seven ahead of the softmax); false at the end or on giving up.
   __device__ __forceinline__ bool segment(uint32_t i, bool &ok) {
     ok = wait(&sm.seg_full[i & 7], (i >> 3) & 1);
     return ok && sm.seg[i & 7].b >= 0;
   }
 
   // ------------------------------------------------------------ warp 0: copies
+  // A lane's piece of a tile: its block id in flight.
+  struct Piece {
+    int id, tok;
+    bool mine;
+  };
+  __device__ __forceinline__ Piece piece_of(const Segment &w, int t) const {
+    const specdec_kv_cache &kv = p.cache;
+    Piece x;
+    x.tok = w.r.from + t * kTok + lane * box;
+    x.mine = lane * box < kTok && x.tok < w.r.len && t < w.r.cached;
+    x.id = x.mine ? __ldg(kv.block_table + (long long)w.b * kv.max_blocks + x.tok / kv.block) : 0;
+    return x;
+  }
+  __device__ __forceinline__ bool publish(Walk &walk, uint32_t index, Segment &w) {
+    const bool more = walk.next(p, box, w);
+    if (lane == 0) {
+      sm.seg[index & 7] = w;
+      mbar_arrive(&sm.seg_full[index & 7]);
+    }
+    return more;
+  }
+
   __device__ __forceinline__ void copies(const Plan &plan) {
     const specdec_kv_cache &kv = p.cache;
     uint32_t c = 0, index = 0;
     Walk walk(p, box, plan);
-    bool ok = true;
-    for (; ok; ++index) {
-      Segment w;
-      const bool more = walk.next(p, box, w);
-      if (lane == 0) {
-        sm.seg[index & 7] = w;
-        mbar_arrive(&sm.seg_full[index & 7]);
-      }
-      if (!more) break;
+    Segment w, ahead;
+    bool ok = true, more = publish(walk, 0, ahead);
 #pragma unroll 1
-      for (int t = w.t0; ok && t < w.t1; ++t, ++c) {
+    for (; ok && more; ++index) {
+      w = ahead;
+      more = publish(walk, index + 1, ahead);  // the others prepare the next one
+      Piece next = piece_of(w, w.t0);
+#pragma unroll 1
+      for (int t = w.t0; t < w.t1; ++t, ++c) {
         const int ks = c % kK, vs = c % kV;
-        if (t >= w.r.cached) {
-          // nothing to copy, but a phase missed here would make the slot's next
-          // wait take an old phase of the same parity for its own
-          if (!(ok = wait(&sm.k_empty[ks], empty_par(c, kK)))) break;
-          if (!(ok = wait(&sm.v_empty[vs], empty_par(c, kV)))) break;
-          continue;
+        Piece x = next;
+        if (t + 1 < w.t1) next = piece_of(w, t + 1);  // the next tile's ids load meanwhile
+        const bool cached = t < w.r.cached;
+        if (x.id < 0 || x.id >= kv.n_blocks) {
+          x.id = 0;
+          sm.bad[index & 7] = SPECDEC_ROW_BAD_CACHE;
         }
-        const int token = w.r.from + t * kTok;
-        const int pieces = min(kTok, w.r.len - token + box - 1) / box;
-        int row = 0;
-        long long cell = 0;
-        const bool mine = lane < pieces;
-        if (mine) {
-          const int tok = token + lane * box;
-          int id = kv.block_table[(long long)w.b * kv.max_blocks + tok / kv.block];
-          if (id < 0 || id >= kv.n_blocks) {
-            id = 0;
-            sm.bad[index & 7] = SPECDEC_ROW_BAD_CACHE;
-          }
-          cell = (long long)id * kv.Hkv + w.h;
-          row = (int)(cell * kv.block + tok % kv.block);
-        }
-        const uint32_t bytes = (uint32_t)pieces * box * kRow;
+        const long long cell = (long long)x.id * kv.Hkv + w.h;
+        const int row = (int)(cell * kv.block + x.tok % kv.block);
+        const uint32_t bytes = (uint32_t)__popc(__ballot_sync(kAll, x.mine)) * box * kRow;
+        float2 unit = make_float2(0.0f, 0.0f);
+        if (x.mine) unit = make_float2(__ldg(kv.k_scale + cell), __ldg(kv.v_scale + cell));
+        // drafted tiles have nothing to copy, but a phase missed here would make
+        // the slot's next wait take an old phase of the same parity for its own
         if (!(ok = wait(&sm.k_empty[ks], empty_par(c, kK)))) break;
-        if (lane == 0) mbar_expect_tx(&sm.k_full[ks], bytes);
-        __syncwarp();
-        if (mine) tma_rows(sm.k[ks] + lane * box * kRow, k_map, row, &sm.k_full[ks]);
-        if (mine) sm.boxes[c & 7][lane] = make_float2(kv.k_scale[cell], kv.v_scale[cell]);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.k_full[ks]);
+        if (cached) {
+          if (lane == 0) mbar_arrive_expect_tx(&sm.k_full[ks], bytes);
+          __syncwarp();
+          if (x.mine) tma_rows(sm.k[ks] + lane * box * kRow, k_map, row, &sm.k_full[ks]);
+        }
         if (!(ok = wait(&sm.v_empty[vs], empty_par(c, kV)))) break;
-        if (lane == 0) mbar_arrive_expect_tx(&sm.v_full[vs], bytes);
-        __syncwarp();
-        if (mine) tma_rows(sm.v[vs] + lane * box * kRow, v_map, row, &sm.v_full[vs]);
+        if (cached) {
+          if (lane == 0) mbar_arrive_expect_tx(&sm.v_full[vs], bytes);
+          __syncwarp();
+          if (x.mine) {
+            tma_rows(sm.v[vs] + lane * box * kRow, v_map, row, &sm.v_full[vs]);
+            sm.boxes[c & 7][lane] = unit;
+          }
+          __syncwarp();
+          if (lane < 4) mbar_arrive(&sm.box_full[c & 7]);
+        }
       }
     }
     // Every copy has been waited on by its reader, unless somebody gave up: then
@@ -536,22 +625,26 @@ struct Tile {
   }
 
   // ------------------------------------------------------------ warp 1: products
-  __device__ __forceinline__ void scores(uint32_t c, bool drafted) {
-    if (lane == 0) {
-      const uint32_t d = sm.tmem + (c & 1) * RN, idesc = shape(columns, false);
-      const uint32_t k = smem_addr(sm.k[c % kK]), lo = smem_addr(sm.v[c % kV]);
-      const uint32_t qh = smem_addr(sm.q[0]), ql = smem_addr(sm.q[1]);
+  __device__ __forceinline__ void scores(uint32_t c, bool drafted, int q, bool ends) {
+    if (elected()) {
+      const uint32_t d = sm_tmem + (c & 1) * RN, idesc = shape(columns, false);
       const int steps = (p.cache.D + 31) / 32;
       // 32 elements a step: 32 bytes, 2 units of the descriptor's address
-      uint64_t ka = operand(k, 1024, 16), kl = operand(lo, 1024, 16);
-      uint64_t qa = operand(qh, 1024, 16), qb = operand(ql, 1024, 16);
+      const uint64_t ka = operand(smem_addr(sm.k[c % kK]), 1024, 16);
+      const uint64_t qa = operand(smem_addr(sm.q[q][0]), 1024, 16);
+      const uint64_t qb = operand(smem_addr(sm.q[q][1]), 1024, 16);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i >= steps) continue;
+        mma_issue<true>(d, ka + 2 * i, qa + 2 * i, idesc, i > 0);
+        mma_issue<true>(d, ka + 2 * i, qb + 2 * i, idesc, true);
+      }
+      if (drafted) {
+        const uint64_t kl = operand(smem_addr(sm.v[c % kV]), 1024, 16);
 #pragma unroll 1
-      for (int i = 0; i < steps; ++i, ka += 2, kl += 2, qa += 2, qb += 2) {
-        mma_issue<true>(d, ka, qa, idesc, i > 0);
-        mma_issue<true>(d, ka, qb, idesc, true);
-        if (drafted) {
-          mma_issue<true>(d, kl, qa, idesc, true);
-          mma_issue<true>(d, kl, qb, idesc, true);
+        for (int i = 0; i < steps; ++i) {
+          mma_issue<true>(d, kl + 2 * i, qa + 2 * i, idesc, true);
+          mma_issue<true>(d, kl + 2 * i, qb + 2 * i, idesc, true);
         }
       }
       mma_commit(&sm.s_full[c & 1]);
@@ -562,6 +655,7 @@ struct Tile {
         mbar_arrive(&sm.v_empty[c % kV]);
         mma_commit(&sm.v_empty[c % kV]);
       }
+      if (ends) mma_commit(&sm.q_empty[q]);
     }
     __syncwarp();
   }
@@ -570,37 +664,45 @@ struct Tile {
     if (!wait(&sm.vh_full[c & 1], (c >> 1) & 1) || !wait(&sm.p_full[c & 1], (c >> 1) & 1))
       return false;
     fence_after();
-    if (lane == 0) {
-      const uint32_t d = sm.tmem + 2 * RN, idesc = shape(columns, true);
-      const uint32_t v = smem_addr(sm.vh[c & 1][0]), pt = smem_addr(sm.pt[c & 1][0]);
-      uint64_t va = operand(v, 1024, kTileBytes), pb = operand(pt, 1024, kTileBytes);
-#pragma unroll 1
-      for (int i = 0; i < kTok / 16; ++i, va += 128, pb += 128)
-        mma_issue<false>(d, va, pb, idesc, !first || i > 0);
+    if (elected()) {
+      const uint32_t d = sm_tmem + (Cfg<RN>::kTurns ? 2 + (c & 1) : 2) * RN;
+      const uint32_t idesc = shape(columns, true);
+      const uint64_t va = operand(smem_addr(sm.vh[c & 1][0]), 1024, kTileBytes);
+      const uint64_t pb = operand(smem_addr(sm.pt[c & 1][0]), 1024, kTileBytes);
+#pragma unroll
+      for (int i = 0; i < kTok / 16; ++i)  // 16 tokens a step: 2048 bytes
+        mma_issue<false>(d, va + 128 * i, pb + 128 * i, idesc, !first || i > 0);
       mma_commit(&sm.pv_done[c & 1]);
     }
     __syncwarp();
     return true;
   }
 
+  uint32_t sm_tmem;
   __device__ __forceinline__ void products() {
-    uint32_t c = 0;
-    bool ok = true, pending = false, pending_first = false;
+    constexpr int kLag = Cfg<RN>::kLag, kQ = Cfg<RN>::kQ;
+    uint32_t c = 0, done = 0;  // tiles whose scores, and whose outputs were issued
+    uint32_t firsts = 0;       // bit k: tile c - 1 - k is its accumulator's first
+    bool ok = true;
+    sm_tmem = sm.tmem;
+#pragma unroll 1
     for (uint32_t index = 0; segment(index, ok); ++index) {
       const int t0 = sm.seg[index & 7].t0, t1 = sm.seg[index & 7].t1;
       const int cached = sm.seg[index & 7].r.cached;
 #pragma unroll 1
-      for (int t = t0; ok && t < t1; ++t, ++c) {
-        const bool first = t == t0, drafted = t >= cached;
-        // at a segment's start the products of the one before come first: q is
-        // staged meanwhile
-        if (first && pending) {
-          if (!(ok = outputs(c - 1, pending_first))) break;
-          pending = false;
-        }
-        if (first && !(ok = wait(&sm.q_full, index & 1))) break;
+      for (int t = t0; t < t1; ++t, ++c) {
+        const bool drafted = t >= cached;
+        // Outputs of the tiles before: up to kLag stay behind, so that scores run
+        // ahead of the softmax.  Before a drafted tile fewer: its operands wait for
+        // room that those outputs free.  And where q has one place only, none
+        // before a segment: the next q waits for the softmax of the last.
+        const uint32_t behind = kQ == 1 && t == t0 ? 0 : drafted ? 1 : kLag;
+#pragma unroll 1
+        for (; ok && c - done > behind; ++done) ok = outputs(done, (firsts >> (c - 1 - done)) & 1);
+        if (!ok) break;
+        if (t == t0 && !(ok = wait(&sm.q_full[index % kQ], (index / kQ) & 1))) break;
+        if (!(ok = wait(&sm.box_full[c & 7], (c >> 3) & 1))) break;
         if (drafted) {
-          if (!(ok = wait(&sm.vh_full[c & 1], (c >> 1) & 1))) break;
           if (lane == 0) {  // nobody copies into this tile's slots
             mbar_arrive(&sm.k_full[c % kK]);
             mbar_arrive(&sm.v_full[c % kV]);
@@ -610,103 +712,110 @@ struct Tile {
         }
         if (!(ok = wait(&sm.s_empty[c & 1], ((c >> 1) & 1) ^ 1))) break;
         fence_after();
-        scores(c, drafted);
-        if (t == t1 - 1 && lane == 0) mma_commit(&sm.q_empty);
-        if (pending && !(ok = outputs(c - 1, pending_first))) break;
-        pending = true;
-        pending_first = first;
+        scores(c, drafted, index % kQ, t == t1 - 1);
+        firsts = firsts << 1 | (t - t0 < (Cfg<RN>::kTurns ? 2 : 1));
       }
       if (!ok) break;
     }
-    if (ok && pending) outputs(c - 1, pending_first);
+#pragma unroll 1
+    for (; ok && done < c; ++done) ok = outputs(done, (firsts >> (c - 1 - done)) & 1);
     // products in flight end before the CTA may leave
-    if (lane == 0) mma_commit(&sm.fin);
+    if (elected()) mma_commit(&sm.fin);
     __syncwarp();
     mbar_wait_bounded(&sm.fin, 0);
   }
 
   // ------------------------------------------------------------ warps 2-5: operands
+  __device__ __forceinline__ int node_of(int row) const {  // row / G
+    return p.G == 1 ? row : (int)__umulhi((uint32_t)row, g_magic);
+  }
+  // The node above a, -1 above a root; `first`: the request's first node.
+  __device__ __forceinline__ int above(long long first, int a) const {
+    if (!p.parent || a == 0) return a - 1;
+    const int up = __ldg(p.parent + first + a);
+    return up < a ? max(up, -1) : -1;
+  }
   __device__ __forceinline__ int depth_of(int b, int n) const {
     if (!p.parent) return n;
     int depth = 0;
-    for (int a = n; a > 0; ++depth) {
-      const int up = p.parent[(long long)b * p.N + a];
-      if (up < 0 || up >= a) break;
-      a = up;
-    }
+#pragma unroll 1
+    for (int a = above((long long)b * p.N, n); a >= 0; a = above((long long)b * p.N, a)) ++depth;
     return depth;
   }
 
-  // 8 consecutive bfloat16 values; `wide`: 16-byte aligned
-  __device__ __forceinline__ void load8(const void *base, long long at, bool wide, float *x) const {
+  // Rows are staged by 16 lanes each, 8 elements a lane, two rows a warp at once.
+  // The lane's elements of a row, as packed bfloat16; `wide`: 16-byte aligned.
+  __device__ __forceinline__ uint4 load8(const void *base, long long at, bool wide) const {
     const unsigned short *s = reinterpret_cast<const unsigned short *>(base) + at;
-    const uint4 w = wide ? __ldg(reinterpret_cast<const uint4 *>(s)) : load8_narrow(s);
+    return wide ? __ldg(reinterpret_cast<const uint4 *>(s)) : load8_narrow(s);
+  }
+
+  // The row's largest finite size, and whether all are finite.
+  __device__ __forceinline__ float row_top(const uint4 &w, bool &all) const {
+    uint32_t m = max2(max2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
+                      max2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
+    m = max(m >> 16, m & 0xFFFFu);
+#pragma unroll
+    for (int d = 8; d >= 1; d >>= 1) m = max(m, __shfl_xor_sync(kAll, m, d));
+    all = m < 0x7F80u;
+    if (__any_sync(kAll, !all)) m = finite_top(w);
+    return __uint_as_float(m << 16);
+  }
+
+  // The row in units of 2^ex as the sum of two e4m3 terms: 8 bytes of each at
+  // element e of row r.  (In fp16 between: bfloat16's bits fit, and so does what
+  // the first term leaves.)
+  __device__ __forceinline__ void split(uint8_t *hi, uint8_t *lo, int r, int e, const uint4 &w,
+                                        int ex) const {
     const uint32_t a[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = bf16_lo(a[i]);
-      x[2 * i + 1] = bf16_hi(a[i]);
-    }
-  }
-
-  // Largest finite size among the 16 lanes of a row, and whether all are finite.
-  __device__ __forceinline__ float row_top(const float *x, bool &all) const {
-    float top = 0.0f;
-    all = true;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float a = fabsf(x[i]);
-      if (a < INFINITY)
-        top = fmaxf(top, a);
-      else
-        all = false;
-    }
-#pragma unroll
-    for (int d = 8; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
-    all = ((__ballot_sync(kAll, all) >> (lane & 16)) & 0xFFFFu) == 0xFFFFu;
-    return top;
-  }
-
-  // x * inv as the sum of two e4m3 terms: 8 bytes each at element e of row r.
-  __device__ __forceinline__ void split(uint8_t *hi, uint8_t *lo, int r, int e, const float *x,
-                                        float inv) const {
+    const float inv = pow2i(-ex);
     uint32_t h[4], l[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float a = x[2 * i] * inv, b = x[2 * i + 1] * inv;
-      h[i] = pack_e4m3x2(finite(a) ? a : __int_as_float(0x7fc00000),
-                         finite(b) ? b : __int_as_float(0x7fc00000));
-      const uint32_t w = e4m3x2_to_half2(h[i]);
-      l[i] = pack_e4m3x2(a - half_bits_to_float(w & 0xFFFFu), b - half_bits_to_float(w >> 16));
+      const uint32_t x = pack_half2(bf16_lo(a[i]) * inv, bf16_hi(a[i]) * inv);
+      h[i] = half2_to_e4m3x2(x);
+      l[i] = half2_to_e4m3x2(sub_half2(x, e4m3x2_to_half2(h[i])));
     }
     const int at = r * kRow + ((((e >> 4) ^ (r & 7)) << 4) | (e & 8));
     *reinterpret_cast<uint2 *>(hi + at) = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
     *reinterpret_cast<uint2 *>(lo + at) = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
   }
 
-  __device__ __forceinline__ void stage_q(const Segment &w, uint32_t index, int worker) {
-    const int D = p.cache.D, ring = index & 3, e = (lane & 15) * 8;
+  __device__ __forceinline__ void stage_q(uint32_t index, int worker) {
+    const Segment &w = sm.seg[index & 7];
+    const int D = p.cache.D, ring = index & 3, e = (lane & 15) * 8, q = index % Cfg<RN>::kQ;
+    const int nodes = w.r.nodes, row0 = w.rt * RN;
     const bool wide = ((reinterpret_cast<uintptr_t>(p.q) | (uintptr_t)(p.q_stride * 2)) & 15) == 0;
+    const long long first = (long long)w.b * p.N;
+    auto load = [&](int r) {
+      const int row = row0 + r, n = node_of(row);
+      if (r >= columns || row >= p.N * p.G || n >= nodes || e >= D) return make_uint4(0u, 0u, 0u, 0u);
+      return load8(p.q, (first + n) * p.q_stride + (long long)(w.h * p.G + row - n * p.G) * D + e,
+                   wide);
+    };
+    uint4 next = load(worker * 2 + (lane >> 4));
 #pragma unroll 1
     for (int r = worker * 2 + (lane >> 4); r < columns; r += 8) {
-      const int row = w.rt * RN + r, n = row / p.G;
-      const bool in = row < p.N * p.G && n < w.r.nodes;
-      const int hq = w.h * p.G + row - n * p.G;
-      float x[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = 0.0f;
-      if (in && e < D)
-        load8(p.q, ((long long)w.b * p.N + n) * p.q_stride + (long long)hq * D + e, wide, x);
+      const uint4 x = next;
+      next = load(r + 8);
       bool all;
       const int ex = unit_exponent(row_top(x, all), 7);
-      split(sm.q[0], sm.q[1], r, e, x, pow2i(-ex));
+      split(sm.q[q][0], sm.q[q][1], r, e, x, ex);
       if ((lane & 15) == 0) {
-        sm.node[ring][r] = (uint8_t)(n - w.rt * RN / p.G);
-        sm.rf[ring][r] = in ? p.scale * kLog2e * pow2i(ex) : 0.0f;
+        const int row = row0 + r, n = node_of(row);
+        const bool in = row < p.N * p.G && n < nodes;
+        sm.node[ring][r] = (uint8_t)(n - node_of(row0));
+        // a q that is not finite makes its row NaN
+        sm.rf[ring][r] = in ? (all ? p.scale * kLog2e * pow2i(ex) : __int_as_float(0x7fc00000)) : 0.0f;
         sm.pos[ring][r] = in ? w.r.len + ((p.window > 0 || p.slopes) ? depth_of(w.b, n) : 0) : -1;
-        sm.slope[ring][r] = (in && p.slopes) ? p.slopes[hq] * kLog2e : 0.0f;
+        if (!kPlain)
+          sm.slope[ring][r] =
+              (in && p.slopes) ? p.slopes[w.h * p.G + row - n * p.G] * kLog2e : 0.0f;
       }
     }
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.q_full[q]);
   }
 
   // NaN codes of a tile that a window hides in part: out of the products, as
@@ -740,7 +849,7 @@ struct Tile {
     // eight lanes cover eight different 16-byte banks
     uint8_t *dst = sm.vh[c & 1][side] + tok0 * kRow;
     uint8_t *d0 = dst + (((piece + side) ^ x7) << 4), *d1 = dst + (((piece + 1 - side) ^ x7) << 4);
-#pragma unroll 2
+#pragma unroll 4
     for (int i = 0; i < 8; ++i) {
       uint4 x = *reinterpret_cast<const uint4 *>(src + i * 16 * kRow);
       if (tok0 + 16 * i >= held) x = make_uint4(0u, 0u, 0u, 0u);
@@ -751,69 +860,77 @@ struct Tile {
       *reinterpret_cast<uint4 *>(d0 + i * 16 * kRow) = side ? hi : lo;
       *reinterpret_cast<uint4 *>(d1 + i * 16 * kRow) = side ? lo : hi;
     }
-    sm.unit[c & 1][tid] = sm.boxes[c & 7][tid / box];
   }
 
   // A tile of drafted tokens: nodes [j0, j0 + 128).
   __device__ __forceinline__ void build(const Segment &w, uint32_t index, int t, uint32_t c,
                                         int worker) {
     const int D = p.cache.D, j0 = (t - w.r.cached) * kTok, e = (lane & 15) * 8;
+    const int nodes = w.r.nodes, held = min(nodes - j0, kTok);
     const long long first = (long long)w.b * p.N;
     const bool k_wide =
         ((reinterpret_cast<uintptr_t>(p.k_new) | (uintptr_t)(p.k_stride * 2)) & 15) == 0;
     const bool v_wide =
         ((reinterpret_cast<uintptr_t>(p.v_new) | (uintptr_t)(p.v_stride * 2)) & 15) == 0;
 #pragma unroll 1
-    for (int r = worker * 2 + (lane >> 4); r < kTok; r += 8) {
-      const bool in = j0 + r < w.r.nodes;
-      float x[8], y[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = y[i] = 0.0f;
-      if (in && e < D) {
-        load8(p.k_new, (first + j0 + r) * p.k_stride + (long long)w.h * D + e, k_wide, x);
-        load8(p.v_new, (first + j0 + r) * p.v_stride + (long long)w.h * D + e, v_wide, y);
-      }
+    for (int r = worker * 2 + (lane >> 4); r - (lane >> 4) < held; r += 8) {
+      const bool in = r < held && e < D;
+      const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+      const uint4 x = in ? load8(p.k_new, (first + j0 + r) * p.k_stride + (long long)w.h * D + e, k_wide)
+                         : zero;
+      const uint4 y = in ? load8(p.v_new, (first + j0 + r) * p.v_stride + (long long)w.h * D + e, v_wide)
+                         : zero;
       bool all;
       const int ek = unit_exponent(row_top(x, all), 7);
-      split(sm.k[c % kK], sm.v[c % kV], r, e, x, pow2i(-ek));
+      split(sm.k[c % kK], sm.v[c % kV], r, e, x, ek);
       const float k_unit = all ? pow2i(ek) : -1.0f;
       const int ev = unit_exponent(row_top(y, all), 10);
       const float inv = pow2i(-ev);
       if (!all) sm.dirty[index & 7] = 1;
+      const uint32_t b[4] = {y.x, y.y, y.z, y.w};
       uint32_t a[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        a[i] = pack_half2(finite(y[2 * i]) ? y[2 * i] * inv : 0.0f,
-                          finite(y[2 * i + 1]) ? y[2 * i + 1] * inv : 0.0f);
+      for (int i = 0; i < 4; ++i) {
+        const float v0 = bf16_lo(b[i]), v1 = bf16_hi(b[i]);
+        a[i] = pack_half2(finite(v0) ? v0 * inv : 0.0f, finite(v1) ? v1 * inv : 0.0f);
+      }
       *reinterpret_cast<uint4 *>(sm.vh[c & 1][e >> 6] + r * kRow +
                                  ((((e & 63) >> 3) ^ (r & 7)) << 4)) =
           make_uint4(a[0], a[1], a[2], a[3]);
       if ((lane & 15) == 0) sm.unit[c & 1][r] = make_float2(k_unit, pow2i(ev));
     }
-    // what each node of the rows sees of this tile
-    const int tid = worker * 32 + lane, n0 = w.rt * RN / p.G;
-    const int n = n0 + tid;
+    // past the last node: weights there are 0, but V must not be NaN
+    const int tid = worker * 32 + lane;
+#pragma unroll 1
+    for (int i = max(held, 0) * 8 + tid; i < kTok * 8; i += 128) {
+      const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+      reinterpret_cast<uint4 *>(sm.vh[c & 1][0])[i] = zero;
+      reinterpret_cast<uint4 *>(sm.vh[c & 1][1])[i] = zero;
+    }
+    // what each row sees of this tile: its node's ancestors, as bits
+    const int n = node_of(w.rt * RN + tid);
     uint32_t bits[4] = {0u, 0u, 0u, 0u};
-    if (tid <= (columns - 1) / p.G + 1 && n < w.r.nodes) {
+    if (tid < columns && n < nodes) {
       int a = n;
+#pragma unroll 1
       for (int step = 0; a >= j0; ++step) {
-        if (a < j0 + kTok && (p.window == 0 || step < p.window))
-          bits[(a - j0) >> 5] |= 1u << ((a - j0) & 31);
-        int up = a - 1;
-        if (p.parent && a > 0) {
-          up = p.parent[first + a];
-          if (up >= a) up = -1;
+        if (a < j0 + kTok && (p.window == 0 || step < p.window)) {
+          const uint32_t bit = 1u << ((a - j0) & 31);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if ((a - j0) >> 5 == i) bits[i] |= bit;
         }
-        a = up;
+        a = above(first, a);
       }
     }
+    if (tid < columns)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sm.see[c & 1][tid][i] = bits[i];
+      for (int i = 0; i < 4; ++i) sm.see[c & 1][i][tid] = bits[i];
     if (p.parent) {
       bool wrong = false;
 #pragma unroll 1
-      for (int i = tid; i < w.r.nodes; i += 128) {
-        const int up = p.parent[first + i];
+      for (int i = tid; i < nodes; i += 128) {
+        const int up = __ldg(p.parent + first + i);
         wrong |= i == 0 ? up != -1 : (up < 0 || up >= i);
       }
       if (wrong) atomicOr(&sm.bad[index & 7], SPECDEC_ROW_BAD_TREE);
@@ -824,16 +941,22 @@ struct Tile {
     const int worker = warp - 2;
     uint32_t c = 0;
     bool ok = true;
+#pragma unroll 1
     for (uint32_t index = 0; segment(index, ok); ++index) {
       const Segment &w = sm.seg[index & 7];
       const int t0 = w.t0, t1 = w.t1, cached = w.r.cached;
-      if (!(ok = wait(&sm.q_empty, (index & 1) ^ 1))) break;
-      stage_q(w, index, worker);
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.q_full);
+      // q of this segment, where it is not there yet; and ahead, once this one's
+      // first tile is on its way, of the next
+      bool staged = Cfg<RN>::kQ == 2 && index > 0;
+      uint32_t stage = index;
 #pragma unroll 1
-      for (int t = t0; ok && t < t1; ++t, ++c) {
+      for (int t = t0;; ++t, ++c) {
+        if (!staged) {
+          if (!(ok = wait(&sm.q_empty[stage % Cfg<RN>::kQ], ((stage / Cfg<RN>::kQ) & 1) ^ 1))) break;
+          stage_q(stage, worker);
+          staged = true;
+        }
+        if (t >= t1) break;
         const bool drafted = t >= cached;
         if (drafted) {
           if (!(ok = wait(&sm.k_empty[c % kK], empty_par(c, kK)))) break;
@@ -849,24 +972,40 @@ struct Tile {
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
-          if (!drafted) mbar_arrive(&sm.v_empty[c % kV]);
+          mbar_arrive(drafted ? &sm.box_full[c & 7] : &sm.v_empty[c % kV]);
           mbar_arrive(&sm.vh_full[c & 1]);
         }
         // as the copying warp: every phase of v_full is waited on
-        if (drafted) ok = wait(&sm.v_full[c % kV], full_par(c, kV));
+        if (drafted && !(ok = wait(&sm.v_full[c % kV], full_par(c, kV)))) break;
+        if (Cfg<RN>::kQ == 2 && t == t0) {
+          bool more;
+          more = segment(index + 1, ok);
+          if (!ok) break;
+          stage = index + 1;
+          staged = !more;
+        }
       }
       if (!ok) break;
     }
   }
 
   // ------------------------------------------------------------ warps 6-13: softmax
-  uint32_t group_phase;
-  // The four warps of one half of the rows.
-  __device__ __forceinline__ bool meet(int half) {
+  uint32_t group_phase, both_phase;
+  // The four warps of one group, and all eight.
+  __device__ __forceinline__ bool meet(int group) {
     __syncwarp();
-    if (lane == 0) mbar_arrive(&sm.group[half]);
-    const bool ok = wait(&sm.group[half], group_phase);
+    if (lane == 0) mbar_arrive(&sm.group[group]);
+    const bool ok = wait(&sm.group[group], group_phase);
     group_phase ^= 1;
+    return ok;
+  }
+  __device__ __forceinline__ bool meet_both() {
+    fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.both);
+    const bool ok = wait(&sm.both, both_phase);
+    both_phase ^= 1;
+    fence_after();
     return ok;
   }
 
@@ -882,19 +1021,28 @@ struct Tile {
   }
 
   // Scores of a tile that needs more than a factor, in place: bent, biased and
-  // masked, in base-2 units.  tok: the thread's token; drafted: a drafted tile.
+  // masked, in base-2 units.  tok: the thread's token; unit: its k's.
   __device__ __forceinline__ void bend(const Segment &w, int ring, int t, uint32_t c, bool drafted,
-                                       int tok, int c0, int mine, uint32_t s_at) {
-    const float2 unit = sm.unit[c & 1][tok];
+                                       float unit, int tok, int c0, int mine, uint32_t s_at) {
     const int at = w.r.from + t * kTok + tok, j = (t - w.r.cached) * kTok + tok;
-    const bool exists = drafted || at < w.r.len, special = drafted && unit.x < 0.0f;
-    const int position = !drafted ? at : p.slopes ? w.r.len + depth_of(w.b, min(j, p.N - 1)) : 0;
+    const bool exists = drafted ? j < w.r.nodes : at < w.r.len, special = drafted && unit < 0.0f;
+    const int quarter = tok >> 5, window = drafted ? 0 : p.window;
+    if (!__any_sync(kAll, exists)) {  // a warp past the last token
+      const float hidden[8] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY,
+                               -INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+      for (int ch = 0; ch * 8 < mine; ++ch) tmem_store8(s_at + ch * 8, hidden);
+      tmem_stored();
+      return;
+    }
+    const int position = !drafted ? at : (!kPlain && p.slopes && exists) ? w.r.len + depth_of(w.b, j) : 0;
+    __syncwarp();
     if (__any_sync(kAll, special))  // k is not finite: its products term by term
 #pragma unroll 1
       for (int i = 0; i < mine; ++i) {
         float s = tmem_load1(s_at + i);
         const float rf = sm.rf[ring][c0 + i];
-        if (special && rf != 0.0f && j < w.r.nodes)
+        if (special && rf != 0.0f && exists)
           s = -plain_dot(p, w.b, w.h, w.rt * RN + c0 + i, j) * (p.scale * kLog2e / rf);
         __syncwarp();
         tmem_store1(s_at + i, s);
@@ -907,13 +1055,13 @@ struct Tile {
       tmem_wait8(s);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const int col = c0 + ch * 8 + k, pos = sm.pos[ring][col];
-        bool seen = pos >= 0 && exists;
+        const int col = c0 + ch * 8 + k;
+        bool seen = exists;
         if (drafted)
-          seen = seen && ((sm.see[c & 1][sm.node[ring][col]][tok >> 5] >> (tok & 31)) & 1u);
-        else if (p.window > 0)
-          seen = seen && pos - at < p.window;
-        float y = s[k] * (unit.x * sm.rf[ring][col]);
+          seen = seen && (sm.see[c & 1][quarter][col] >> lane & 1u);
+        else if (window > 0)
+          seen = seen && sm.pos[ring][col] - at < window;
+        float y = s[k] * (unit * sm.rf[ring][col]);
         if (!kPlain) y = bent(y, ring, col, position);
         s[k] = seen ? y : -INFINITY;
       }
@@ -942,44 +1090,49 @@ struct Tile {
   }
 
   __device__ __forceinline__ void softmax() {
-    constexpr int kCh = RN / 16;         // most chunks of 8 columns of a half
-    constexpr bool kHold = RN == 64;     // a thread's scores fit its registers
-    const int half = warp >= 10, quarter = warp & 3, tok = quarter * 32 + lane;
-    const int mine = columns / 2, c0 = half * mine;  // columns of this half, a multiple of 8
+    constexpr bool kTurns = Cfg<RN>::kTurns, kHold = Cfg<RN>::kHold;
+    constexpr int kCols = Cfg<RN>::kCols, kCh = kCols / 8;
+    const int group = warp >= 10, quarter = warp & 3, tok = quarter * 32 + lane;
+    // the group's columns: all of every other tile, or half of every tile
+    const int mine = kTurns ? (min(RN, p.N * p.G) + 7) / 8 * 8 : columns / 2;
+    const int c0 = kTurns ? 0 : group * mine;
     const bool leader = lane == 0 && quarter == 0;
     const uint32_t lanes = sm.tmem + ((uint32_t)quarter << 21);  // TMEM lanes of this warp
-    const uint32_t o_at = lanes + 2 * RN + c0;
+    const uint32_t o_at = lanes + (kTurns ? 2 + group : 2) * RN + c0;
     const specdec_kv_cache &kv = p.cache;
-    uint32_t c = 0;
-    group_phase = 0;
-    f2 l[RN / 4];
+    uint32_t c = 0;  // the tile's number, of all
+    group_phase = both_phase = 0;
+    f2 l[kCols / 2];
+    float *const nms = sm.nm[group];
     bool ok = true;
     for (uint32_t index = 0; segment(index, ok); ++index) {
       const Segment &w = sm.seg[index & 7];
       const int ring = index & 3, t0 = w.t0, t1 = w.t1;
       float vref = 0.0f;
+      uint32_t last = ~0u;  // the group's last tile of the segment
 #pragma unroll
-      for (int i = 0; i < RN / 4; ++i) l[i] = 0ull;
+      for (int i = 0; i < kCols / 2; ++i) l[i] = 0ull;
       // the rows have seen nothing yet
-      if (tok < mine) sm.nm[c0 + tok] = kUnseen;
+      if (tok < mine) nms[tok] = kUnseen;
 #pragma unroll 1
       for (int t = t0; ok && t < t1; ++t, ++c) {
-        const bool drafted = t >= w.r.cached;
+        if (kTurns && (int)(c & 1) != group) continue;
+        const bool drafted = t >= w.r.cached, first = last == ~0u;
         const uint32_t s_at = lanes + (c & 1) * RN + c0;
-        if (!(ok = wait(&sm.vh_full[c & 1], (c >> 1) & 1))) break;
+        if (!(ok = wait(&sm.box_full[c & 7], (c >> 3) & 1))) break;
+        const float2 unit = drafted ? sm.unit[c & 1][tok] : sm.boxes[c & 7][tok >> box_shift];
         if (!(ok = wait(&sm.s_full[c & 1], (c >> 1) & 1))) break;
         fence_after();
-        const float2 unit = sm.unit[c & 1][tok];
         // a plain tile's scores are a factor away; the others are written back
         const int past = w.r.from + t * kTok + kTok - w.r.len;
         const bool kept = !kPlain || drafted || past > 0 || partly_hidden(p, w.r, t);
-        if (kept) bend(w, ring, t, c, drafted, tok, c0, mine, s_at);
-        const float v_unit = drafted || past + tok < kTok ? unit.y : 0.0f;
+        if (kept) bend(w, ring, t, c, drafted, unit.x, tok, c0, mine, s_at);
+        const bool exists = drafted ? (t - w.r.cached) * kTok + tok < w.r.nodes : past + tok < kTok;
+        const float v_unit = exists ? unit.y : 0.0f;
         const float k_unit = kept ? 1.0f : unit.x;
         const f2 ks = pair(k_unit, k_unit);
         const float *factor = kept ? sm.ones : sm.rf[ring] + c0;
-        const float *minus = sm.nm + c0;
-        float x[kHold ? RN / 2 : 8];
+        float x[kHold ? kCols : 8];
         bool moved = false;
         for (;;) {
           float top = -INFINITY;
@@ -990,26 +1143,25 @@ struct Tile {
           }
 #pragma unroll
           for (int ch = 0; ch < kCh; ++ch) {
-            if (ch * 8 >= mine) break;
+            if (ch * 8 >= mine) continue;
             float *s = x + (kHold ? ch * 8 : 0);
             if (!kHold) tmem_load8(s_at + ch * 8, s);
             tmem_wait8(s);
 #pragma unroll
             for (int k = 0; k < 8; k += 4) {
               const ulonglong2 r = *reinterpret_cast<const ulonglong2 *>(factor + ch * 8 + k);
-              const ulonglong2 n = *reinterpret_cast<const ulonglong2 *>(minus + ch * 8 + k);
+              const ulonglong2 n = *reinterpret_cast<const ulonglong2 *>(nms + ch * 8 + k);
               unpair(fma2(pair(s[k], s[k + 1]), mul2(r.x, ks), n.x), s[k], s[k + 1]);
               unpair(fma2(pair(s[k + 2], s[k + 3]), mul2(r.y, ks), n.y), s[k + 2], s[k + 3]);
               top = fmaxf(fmaxf(top, fmaxf(s[k], s[k + 1])), fmaxf(s[k + 2], s[k + 3]));
             }
           }
           if (moved) break;
-          // scores far above a maximum, or a larger unit of v: all four warps move
-          const bool first = t == t0;
+          // scores far above a maximum, or a larger unit of v: the group moves
           if (__any_sync(kAll, top > kRaise + kLift || v_unit > vref) && lane == 0)
-            sm.vote[half][c & 3] = 1;
-          if (!(ok = meet(half))) break;
-          if (!first && !*(volatile int *)&sm.vote[half][c & 3]) break;
+            sm.vote[group][(c >> kTurns) & 3] = 1;
+          if (!(ok = meet(group))) break;
+          if (!first && !*(volatile int *)&sm.vote[group][(c >> kTurns) & 3]) break;
           // maxima of the tile: a warp's by column, then the four warps'
 #pragma unroll 1
           for (int ch = 0; ch * 8 < mine; ++ch) {
@@ -1022,34 +1174,33 @@ struct Tile {
               float z = y[k] * (k_unit * factor[ch * 8 + k]);
               if (!(z == z)) z = INFINITY;  // its row becomes NaN
               const int best = __reduce_max_sync(kAll, ordered(z));
-              if (lane == 0) sm.red[quarter][c0 + ch * 8 + k] = unordered(best);
+              if (lane == 0) sm.red[group][quarter][ch * 8 + k] = unordered(best);
             }
           }
           const int vmax = __reduce_max_sync(kAll, __float_as_int(v_unit));  // units are >= 0
-          if (lane == 0) sm.vred[half][quarter] = __int_as_float(vmax);
-          if (!(ok = meet(half))) break;
-          const float unit_max = fmaxf(fmaxf(sm.vred[half][0], sm.vred[half][1]),
-                                       fmaxf(sm.vred[half][2], sm.vred[half][3]));
+          if (lane == 0) sm.vred[group][quarter] = __int_as_float(vmax);
+          if (!(ok = meet(group))) break;
+          const float unit_max = fmaxf(fmaxf(sm.vred[group][0], sm.vred[group][1]),
+                                       fmaxf(sm.vred[group][2], sm.vred[group][3]));
           // headroom of 4, so that units of one size move once
           const float to = unit_max > vref ? fminf(unit_max * 4.0f, 0x1p126f) : vref;
           const float v_fac = to > 0.0f ? __fdividef(vref, to) : 1.0f;
           vref = to;
           if (tok < mine) {
-            const int col = c0 + tok;
-            const float best = fmaxf(fmaxf(sm.red[0][col], sm.red[1][col]),
-                                     fmaxf(sm.red[2][col], sm.red[3][col]));
-            const float nm = sm.nm[col];
+            const float best = fmaxf(fmaxf(sm.red[group][0][tok], sm.red[group][1][tok]),
+                                     fmaxf(sm.red[group][2][tok], sm.red[group][3][tok]));
+            const float nm = nms[tok];
             float f = 1.0f;
             if (best > -INFINITY && (nm == kUnseen || kLift - best < nm)) {
               f = nm == kUnseen ? 0.0f : ex2_approx(kLift - best - nm);
-              sm.nm[col] = kLift - best;
+              nms[tok] = kLift - best;
             }
-            sm.fac[0][col] = f;
-            sm.fac[1][col] = f * v_fac;
+            sm.fac[group][0][tok] = f;
+            sm.fac[group][1][tok] = f * v_fac;
           }
-          if (!first && !(ok = wait(&sm.pv_done[(c - 1) & 1], ((c - 1) >> 1) & 1))) break;
+          if (!first && !(ok = wait(&sm.pv_done[last & 1], (last >> 1) & 1))) break;
           fence_after();
-          if (!(ok = meet(half))) break;
+          if (!(ok = meet(group))) break;
           if (!first) {
 #pragma unroll 1
             for (int ch = 0; ch * 8 < mine; ++ch) {
@@ -1057,20 +1208,26 @@ struct Tile {
               tmem_load8(o_at + ch * 8, o);
               tmem_wait8(o);
 #pragma unroll
-              for (int k = 0; k < 8; ++k) o[k] *= sm.fac[1][c0 + ch * 8 + k];
+              for (int k = 0; k < 8; ++k) o[k] *= sm.fac[group][1][ch * 8 + k];
               tmem_store8(o_at + ch * 8, o);
             }
             tmem_stored();
 #pragma unroll
-            for (int i = 0; i < RN / 4; ++i)
+            for (int i = 0; i < kCols / 2; ++i)
               if (2 * i < mine)
-                l[i] = mul2(l[i], *reinterpret_cast<const f2 *>(&sm.fac[0][c0 + 2 * i]));
+                l[i] = mul2(l[i], *reinterpret_cast<const f2 *>(&sm.fac[group][0][2 * i]));
           }
           if (!kHold) break;
           moved = true;  // once more, under the new maxima
         }
         if (!ok) break;
-        if (leader) sm.vote[half][(c + 2) & 3] = 0;
+        last = c;
+        if (kHold) {  // the scores are in registers: the next ones may come
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.s_empty[c & 1]);
+        }
+        if (leader) sm.vote[group][((c >> kTurns) + 2) & 3] = 0;
         // P^T of two tiles ago has been read
         if (!(ok = wait(&sm.pv_done[c & 1], ((c >> 1) & 1) ^ 1))) break;
         const float ratio = vref > 0.0f ? __fdividef(v_unit, vref) : 0.0f;
@@ -1078,7 +1235,7 @@ struct Tile {
         uint8_t *pt = sm.pt[c & 1][0] + tok * kRow;
 #pragma unroll
         for (int ch = 0; ch < kCh; ++ch) {
-          if (ch * 8 >= mine) break;
+          if (ch * 8 >= mine) continue;
           float *s = x + (kHold ? ch * 8 : 0);
           if (!kHold) {
             tmem_load8(s_at + ch * 8, s);
@@ -1086,7 +1243,7 @@ struct Tile {
 #pragma unroll
             for (int k = 0; k < 8; k += 4) {
               const ulonglong2 r = *reinterpret_cast<const ulonglong2 *>(factor + ch * 8 + k);
-              const ulonglong2 n = *reinterpret_cast<const ulonglong2 *>(minus + ch * 8 + k);
+              const ulonglong2 n = *reinterpret_cast<const ulonglong2 *>(nms + ch * 8 + k);
               unpair(fma2(pair(s[k], s[k + 1]), mul2(r.x, ks), n.x), s[k], s[k + 1]);
               unpair(fma2(pair(s[k + 2], s[k + 3]), mul2(r.y, ks), n.y), s[k + 2], s[k + 3]);
             }
@@ -1109,7 +1266,7 @@ struct Tile {
         fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&sm.s_empty[c & 1]);
+          if (!kHold) mbar_arrive(&sm.s_empty[c & 1]);
           mbar_arrive(&sm.p_full[c & 1]);
         }
       }
@@ -1118,30 +1275,61 @@ struct Tile {
       // the segment's sums, by column
 #pragma unroll
       for (int ch = 0; ch < kCh; ++ch) {
-        if (ch * 8 >= mine) break;
+        if (ch * 8 >= mine) continue;
         float v[8];
 #pragma unroll
         for (int k = 0; k < 4; ++k) unpair(l[ch * 4 + k], v[2 * k], v[2 * k + 1]);
         const float sum = sum8(v);
-        if ((lane & 3) == 0) sm.red[quarter][c0 + ch * 8 + (lane >> 2)] = sum;
+        if ((lane & 3) == 0) sm.red[group][quarter][ch * 8 + (lane >> 2)] = sum;
       }
-      if (!(ok = wait(&sm.pv_done[(c - 1) & 1], ((c - 1) >> 1) & 1))) break;
-      fence_after();
-      if (!(ok = meet(half))) break;
-      // both halves are past the segment before; nobody is seven ahead
-      if (leader && half == 0) sm.bad[(index + 7) & 7] = sm.dirty[(index + 7) & 7] = 0;
+      if (leader) sm.vlast[group] = vref;
+      if (last != ~0u && !(ok = wait(&sm.pv_done[last & 1], (last >> 1) & 1))) break;
+      if (!(ok = meet_both())) break;
+      // both groups are past the segment before; nobody is seven ahead
+      if (leader && group == 0) sm.bad[(index + 7) & 7] = sm.dirty[(index + 7) & 7] = 0;
       const int bad = w.r.bad | *(volatile int *)&sm.bad[index & 7];
       const bool dirty = *(volatile int *)&sm.dirty[index & 7] != 0, whole = w.whole;
       float *part = p.part + (size_t)(2 * blockIdx.x + (t0 == 0)) * partial_floats(RN, kv.D);
-      if (tok < mine) {  // a thread for each row: its factor and its statistics
-        const int col = c0 + tok, row = w.rt * RN + col, n = row / p.G;
-        const float sum = (sm.red[0][col] + sm.red[1][col]) + (sm.red[2][col] + sm.red[3][col]);
-        const float nm = sm.nm[col];
+      // results: each group writes half of the columns.  A thread for each row
+      // first: its statistics, and its factors of the accumulators
+      const int out_n = kTurns ? columns / 2 : mine, out_0 = group * out_n;
+      // a column's factors and place take the room of its sums, which only its own
+      // thread reads
+      float *const out_fac = kTurns ? &sm.red[0][0][out_0] : &sm.red[group][0][0];
+      if (tok < out_n) {
+        const int col = out_0 + tok, row = w.rt * RN + col, n = node_of(row);
+        float nm, sum, f[2];
+        if (kTurns) {
+          const float na = sm.nm[0][col], nb = sm.nm[1][col];
+          nm = fminf(na, nb);
+          // NaN sums stay, whatever the factors; an unseen side counts nothing
+          f[0] = na == kUnseen ? 0.0f : ex2_approx(nm - na);
+          f[1] = nb == kUnseen ? 0.0f : ex2_approx(nm - nb);
+          if (na == nm) f[0] = 1.0f;
+          if (nb == nm) f[1] = 1.0f;
+          float part_sum[2];
+#pragma unroll
+          for (int g = 0; g < 2; ++g)
+            part_sum[g] = (sm.red[g][0][col] + sm.red[g][1][col]) +
+                          (sm.red[g][2][col] + sm.red[g][3][col]);
+          sum = part_sum[0] * f[0] + part_sum[1] * f[1];
+          // an accumulator without a tile holds nothing
+          f[0] = part_sum[0] == 0.0f ? 0.0f : f[0] * sm.vlast[0];
+          f[1] = part_sum[1] == 0.0f ? 0.0f : f[1] * sm.vlast[1];
+        } else {
+          nm = nms[tok];
+          sum = (sm.red[group][0][tok] + sm.red[group][1][tok]) +
+                (sm.red[group][2][tok] + sm.red[group][3][tok]);
+          f[0] = vref;
+          f[1] = 0.0f;
+        }
+        const bool in = row < p.N * p.G && (!kTurns || col < mine);
         const bool empty = bad || n >= w.r.nodes || (nm == kUnseen && sum == 0.0f);
         const int at = (w.b * p.N + n) * p.Hq + w.h * p.G + row - n * p.G;
-        const bool in = row < p.N * p.G;
-        sm.red[0][col] = __int_as_float(in ? at : -1);  // nobody else reads this column
-        sm.fac[0][col] = empty ? 0.0f : whole ? __fdividef(vref, sum) : vref;
+        const float inv = empty ? 0.0f : whole ? __fdividef(1.0f, sum) : 1.0f;
+        out_fac[tok] = empty ? 0.0f : f[0] * inv;
+        out_fac[kCols + tok] = empty ? 0.0f : f[1] * inv;
+        out_fac[2 * kCols + tok] = __int_as_float(in ? at : -1);
         if (in && whole && p.lse)
           p.lse[at] = empty ? -INFINITY : (log2f(sum) - nm) * 0.6931471805599453f;
         if (in && !whole) {
@@ -1149,41 +1337,52 @@ struct Tile {
           part[(size_t)col * (kv.D + 2) + 1] = bad ? -(float)bad : empty ? 0.0f : sum;
         }
       }
-      if (!(ok = meet(half))) break;
+      if (!(ok = meet(group))) break;
+      const uint32_t y_at = lanes + 2 * RN + out_0;
       if (dirty)  // what the products left out because it is not finite
 #pragma unroll 1
-        for (int i = 0; i < mine; ++i) {
-          float o = tmem_load1(o_at + i);
-          if (sm.fac[0][c0 + i] != 0.0f && __float_as_int(sm.red[0][c0 + i]) >= 0 && tok < kv.D)
-            o += stray(p, box, w.b, w.h, t0, t1, sm.node[ring][c0 + i] + w.rt * RN / p.G,
-                       sm.pos[ring][c0 + i], tok);
+        for (int i = 0; i < out_n; ++i) {
+          const float f = out_fac[i], f2nd = kTurns ? out_fac[kCols + i] : 0.0f;
+          float extra = 0.0f;
+          if (__float_as_int(out_fac[2 * kCols + i]) >= 0 && tok < kv.D && (f != 0.0f || f2nd != 0.0f))
+            extra = stray(p, box, w.b, w.h, t0, t1, sm.node[ring][out_0 + i] + node_of(w.rt * RN),
+                          sm.pos[ring][out_0 + i], tok);
           __syncwarp();
-          tmem_store1(o_at + i, o);
+          // to an accumulator that counts
+          const uint32_t at = f != 0.0f ? y_at + i : y_at + RN + i;
+          if (f == 0.0f && f2nd == 0.0f) continue;
+          tmem_store1(at, tmem_load1(at) + extra);
           tmem_stored();
         }
 #pragma unroll 1
-      for (int ch = 0; ch * 8 < mine; ++ch) {
-        float o[8];
+      for (int i = 0; i < out_n; i += 4) {
+        float o[4], o2[4];
         __syncwarp();
-        tmem_load8(o_at + ch * 8, o);
-        tmem_wait8(o);
+        tmem_load4(y_at + i, o);
+        if (kTurns) tmem_load4(y_at + RN + i, o2);
+        tmem_wait4(o);
+        if (kTurns) tmem_wait4(o2);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int col = c0 + ch * 8 + k, at = __float_as_int(sm.red[0][col]);
-          const float f = sm.fac[0][col];
-          if (at < 0 || tok >= kv.D) continue;
-          const float y = f != 0.0f ? o[k] * f : 0.0f;
-          if (whole)
-            reinterpret_cast<unsigned short *>(p.out)[(long long)at * kv.D + tok] =
-                (unsigned short)pack_bf16x2(y, 0.0f);
-          else
-            part[(size_t)col * (kv.D + 2) + 2 + tok] = y;
+        for (int k = 0; k < 4; ++k) {
+          const int at = __float_as_int(out_fac[2 * kCols + i + k]);
+          const float f = out_fac[i + k];
+          float y = f != 0.0f ? o[k] * f : 0.0f;
+          if (kTurns) {
+            const float f2nd = out_fac[kCols + i + k];
+            y += f2nd != 0.0f ? o2[k] * f2nd : 0.0f;
+          }
+          if (at >= 0 && tok < kv.D) {
+            if (whole)
+              reinterpret_cast<unsigned short *>(p.out)[(long long)at * kv.D + tok] =
+                  (unsigned short)pack_bf16x2(y, 0.0f);
+            else
+              part[(size_t)(out_0 + i + k) * (kv.D + 2) + 2 + tok] = y;
+          }
         }
       }
-      if (whole && leader && half == 0 && w.h == 0 && w.rt == 0) p.row_status[w.b] = bad;
-      fence_before();
-      if (leader) sm.done[half] = index + 1;
-      if (!(ok = meet(half))) break;
+      if (whole && leader && group == 0 && w.h == 0 && w.rt == 0) p.row_status[w.b] = bad;
+      if (leader) sm.done[group] = index + 1;
+      if (!(ok = meet_both())) break;
     }
   }
 
@@ -1221,7 +1420,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                        const __grid_constant__ CUtensorMap v_map, int box) {
   extern __shared__ __align__(1024) uint8_t raw[];
   using S = Smem<RN>;
-  S &sm = *reinterpret_cast<S *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  // an offset, not a rounded pointer: the compiler has to know that it is shared memory
+  S &sm = *reinterpret_cast<S *>(raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u));
   const int tid = threadIdx.x, warp = tid >> 5;
   if (tid == 0) {
     for (int i = 0; i < Cfg<RN>::kK; ++i) {
@@ -1232,13 +1432,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.v_full[i], 1);
       mbar_init(&sm.v_empty[i], 4);
     }
-    mbar_init(&sm.q_full, 4);
-    mbar_init(&sm.q_empty, 1);
+    for (int i = 0; i < Cfg<RN>::kQ; ++i) {
+      mbar_init(&sm.q_full[i], 4);
+      mbar_init(&sm.q_empty[i], 1);
+    }
     mbar_init(&sm.fin, 1);
+    mbar_init(&sm.both, 8);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.s_empty[i], 8);
-      mbar_init(&sm.p_full[i], 8);
+      mbar_init(&sm.s_empty[i], Cfg<RN>::kTurns ? 4 : 8);
+      mbar_init(&sm.p_full[i], Cfg<RN>::kTurns ? 4 : 8);
       mbar_init(&sm.vh_full[i], 4);
       mbar_init(&sm.pv_done[i], 1);
       mbar_init(&sm.group[i], 4);
@@ -1248,16 +1451,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 8; ++i) {
       sm.bad[i] = sm.dirty[i] = 0;
       mbar_init(&sm.seg_full[i], 1);
+      mbar_init(&sm.box_full[i], 4);
     }
     sm.give_up = 0;
     fence_mbar_init();
     fence_async_smem();
   }
-  if (tid < RN / 2) sm.ones[tid] = 1.0f;
+  if (tid < Cfg<RN>::kCols) sm.ones[tid] = 1.0f;
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_addr(&sm.tmem)),
-                 "r"(Cfg<RN>::kCols)
+                 "r"(Cfg<RN>::kTmem)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -1286,7 +1490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(sm.tmem),
-                 "r"(Cfg<RN>::kCols));
+                 "r"(Cfg<RN>::kTmem));
 }
 
 // Joins the units that the cuts between CTAs divide.  Block (i, part): the unit
@@ -1400,7 +1604,7 @@ int box_rows(int block) {  // the largest power of two that divides the block an
   return box;
 }
 
-int rows_of(int N, int G) { return N * G <= 64 ? 64 : 128; }
+int rows_of(int N, int G) { return N * G <= 32 ? 32 : N * G <= 64 ? 64 : 128; }
 
 template <int RN, bool kPlain>
 cudaError_t launch_rn(AttendParams p, cudaStream_t stream) {
@@ -1440,7 +1644,10 @@ bool attend_tile_applies(const AttendParams &p) {
 
 cudaError_t launch_attend_tile(const AttendParams &p, cudaStream_t stream) {
   const bool plain = p.softcap == 0.0f && !p.slopes;
-  if (rows_of(p.N, p.G) == 64)
+  const int rows = rows_of(p.N, p.G);
+  if (rows == 32)
+    return plain ? launch_rn<32, true>(p, stream) : launch_rn<32, false>(p, stream);
+  if (rows == 64)
     return plain ? launch_rn<64, true>(p, stream) : launch_rn<64, false>(p, stream);
   return plain ? launch_rn<128, true>(p, stream) : launch_rn<128, false>(p, stream);
 }
