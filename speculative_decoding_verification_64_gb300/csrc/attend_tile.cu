@@ -25,13 +25,16 @@
 //     reduced once, at the end.
 //   * V's block scales ride on P, over a running unit (of the largest so far).
 //
-// A persistent grid, one CTA per SM.  All tiles of all requests, heads and row
-// tiles form one line that is cut into equal parts, one per CTA, from the
-// lengths on the device: any mix of lengths keeps all SMs busy to the end.
-// What a cut divides is joined by a second kernel, in order.
-// Roles: warp 0 copies (TMA), warp 1 issues products, warps 2-5 widen V, stage
-// q and build drafted tiles, warps 6-13 take the softmax and write results.
-// Every wait is bounded in time.
+// A persistent grid.  All tiles of all requests, heads and row tiles form one
+// line that is cut into equal parts, one per CTA, from the lengths on the device:
+// any mix of lengths keeps all SMs busy to the end.  What a cut divides is joined
+// by a second kernel, in order.  Up to 64 rows an SM holds two CTAs: one's
+// beginnings and ends of requests, which are chains of short steps, overlap the
+// other's tiles.  With 128 rows one CTA takes the whole SM.
+// Roles: warp 0 copies (TMA), warp 1 issues products, the next warps widen V,
+// stage q and build drafted tiles, the last four or eight take the softmax and
+// write results.  A request's drafted tiles come first: they are built while the
+// results of the request before are written.  Every wait is bounded in time.
 #include <cstddef>
 
 #include <cuda.h>
@@ -42,10 +45,9 @@ namespace specdec {
 namespace {
 
 constexpr int kTok = 128;
-constexpr int kThreads = 448;
 constexpr int kRow = 128;              // bytes of a shared-memory row: one swizzle span
 constexpr int kTileBytes = kTok * kRow;
-constexpr int kMaxCtas = 160;
+constexpr int kMaxSms = 160;
 constexpr int kWaitTries = 1000000;
 constexpr float kRaise = 8.0f;
 constexpr float kLift = 6.0f;
@@ -54,39 +56,32 @@ constexpr unsigned kAll = 0xffffffffu;
 
 template <int RN>
 struct Cfg {
-  // Up to 64 rows the two softmax groups take the tiles in turn, each with an
-  // output accumulator, maxima and sums of its own, joined at a segment's end; a
-  // tile's fixed costs (waits, votes, fences) then overlap.  With 128 rows a
-  // thread could not hold the sums: the groups take half of the rows each.
-  static constexpr bool kTurns = RN <= 64;
-  static constexpr int kCols = kTurns ? RN : RN / 2;  // most columns of a softmax thread
-  static constexpr bool kHold = RN == 32;             // its scores stay in registers
-  static constexpr int kK = RN <= 64 ? 3 : 2;         // stages of K codes
-  static constexpr int kV = RN == 32 ? 3 : RN == 64 ? 2 : 1;  // stages of V codes
-  static constexpr int kQ = kTurns ? 2 : 1;           // stages of q: the next segment's ahead
-  static constexpr int kLag = kTurns ? 2 : 1;         // tiles whose outputs follow their scores
+  static constexpr int kCtas = RN <= 64 ? 2 : 1;       // CTAs an SM
+  static constexpr int kGroups = RN <= 64 ? 1 : 2;     // softmax groups of four warps: a part of the rows each
+  static constexpr int kWorkers = RN <= 64 ? 2 : 4;    // warps that widen V
+  static constexpr int kFirst = 2 + kWorkers;          // first softmax warp
+  static constexpr int kThreads = 32 * (kFirst + 4 * kGroups);
+  static constexpr int kCols = RN / kGroups;           // most columns of a softmax thread
+  static constexpr bool kHold = RN == 32;              // its scores stay in registers
+  static constexpr int kK = RN == 64 ? 1 : 2;          // stages of K codes
+  static constexpr int kBuf = RN <= 64 ? 1 : 2;        // buffers of widened V, and of P^T
   static constexpr int kTmem = RN == 32 ? 128 : RN == 64 ? 256 : 512;
-  static constexpr int kSpans = RN <= 64 ? 1 : 2;     // 64-row groups of P^T
+  static constexpr int kSpans = RN <= 64 ? 1 : 2;      // 64-row groups of P^T
 };
 
 // one CTA's part of the line of tiles
 struct Plan {
-  long long total, first, count;  // tiles in all, the part's first, the part's
-  int b, off;                     // first request, first tile of it
+  int b, off;       // first request, first tile of it
+  long long count;  // the end's, b << 32 | off
 };
 
-// The part that tile x belongs to, of n that split `total` tiles (part i begins
-// at tile total * i / n).
 // (Out of line: one copy of a 64-bit division.  The kernels' code has to stay
-// small, as five roles' loops share an SM's instruction cache.)
+// small, as all roles' loops share an SM's instruction cache.)
 __device__ __noinline__ long long divide(long long a, long long b) { return a / b; }
-__device__ __forceinline__ int part_of(long long x, long long total, int n) {
-  return (int)divide((x + 1) * n - 1, total);
-}
 
 struct Request {
   int len, nodes, from;  // cached tokens, drafted ones, first token that the window leaves
-  int cached, tiles;     // tiles of cached tokens, and in all
+  int drafted, tiles;    // tiles of drafted tokens, and in all
   int bad;
 };
 
@@ -99,36 +94,37 @@ struct Segment {
 
 template <int RN>
 struct Smem {
-  uint8_t k[Cfg<RN>::kK][kTileBytes];   // K codes [token][128 B], 128-byte swizzle
-  uint8_t v[Cfg<RN>::kV][kTileBytes];   // V codes, the same (drafted tiles: the low terms of k)
-  uint8_t vh[2][2][kTileBytes];         // V in fp16, [64 elements][token][128 B]
-  uint8_t pt[2][Cfg<RN>::kSpans][kTileBytes];  // P^T in fp16, [64 rows][token][128 B]
-  uint8_t q[Cfg<RN>::kQ][2][RN * kRow];  // q: high and low terms [row][128 B]
-  float2 boxes[8][8];                   // k and v scales of a tile's pieces
-  float2 unit[2][kTok];                 // the same per token (k below 0: it is not finite)
-  alignas(16) uint32_t see[2][4][RN];   // drafted tiles: bits of the nodes that a row sees
-  alignas(16) float rf[4][RN];
+  using C = Cfg<RN>;
+  uint8_t k[C::kK][kTileBytes];           // K codes [token][128 B], 128-byte swizzle
+  uint8_t v[kTileBytes];                  // V codes, the same (drafted tiles: the low terms of k)
+  uint8_t vh[C::kBuf][2][kTileBytes];     // V in fp16, [64 elements][token][128 B]
+  uint8_t pt[C::kBuf][C::kSpans][kTileBytes];  // P^T in fp16, [64 rows][token][128 B]
+  uint8_t q[2][RN * kRow];                // q: high and low terms [row][128 B]
+  float2 boxes[8][8];                     // k and v scales of a tile's pieces
+  float2 unit[2][kTok];                   // drafted tiles: per token (k below 0: it is not finite)
+  alignas(16) uint32_t see[2][4][RN];     // drafted tiles: bits of the nodes that a row sees
+  // of the segment's rows
+  alignas(16) float rf[4][RN];            // what turns a score into base-2 units
   float slope[4][RN];
   int pos[4][RN];
+  uint8_t node[4][RN];
   // per softmax group, by column
-  alignas(16) float nm[2][Cfg<RN>::kCols];      // kLift - m
-  alignas(16) float fac[2][2][Cfg<RN>::kCols];  // factors of l and O when m or the unit moves
-  float red[2][4][Cfg<RN>::kCols];
-  float vlast[2];
-  float vred[2][4];
-  int vote[2][4];
-  alignas(16) float ones[Cfg<RN>::kCols];
-  uint8_t node[4][RN];                  // of the nodes that the rows have
+  alignas(16) float nm[C::kGroups][C::kCols];      // kLift - m
+  alignas(16) float fac[C::kGroups][2][C::kCols];  // factors of l and O when m or the unit moves
+  alignas(16) float red[C::kGroups][4][C::kCols];
+  alignas(16) float ones[C::kCols];
+  float vred[C::kGroups][4];
+  int vote[C::kGroups][4];
   Segment seg[8];
   int bad[8], dirty[8];
-  uint64_t k_full[Cfg<RN>::kK], k_empty[Cfg<RN>::kK], v_full[Cfg<RN>::kV], v_empty[Cfg<RN>::kV];
-  uint64_t seg_full[8], box_full[8], q_full[Cfg<RN>::kQ], q_empty[Cfg<RN>::kQ];
-  uint64_t s_full[2], s_empty[2], p_full[2], vh_full[2], pv_done[2];
-  uint64_t group[2], both, fin;
+  uint64_t seg_full[8], box_full[8];
+  uint64_t k_full[C::kK], k_empty[C::kK], v_full, v_empty, q_full, q_empty;
+  uint64_t s_full[2], s_empty[2], p_full[C::kBuf], vh_full[C::kBuf], pv_done[C::kBuf];
+  uint64_t group[C::kGroups], both, fin;
   uint32_t tmem;
   int give_up;
-  int done[2];                          // segments that a half of the softmax warps finished
-  long long scan[kThreads / 32 + 1];
+  int done[C::kGroups];                   // segments that a softmax group finished
+  long long scan[16];
   Plan plan;
 };
 
@@ -296,22 +292,26 @@ __device__ __noinline__ Request request_of(const AttendParams &p, int b, int box
   if (r.nodes < 0 || r.nodes > p.N) r.bad |= SPECDEC_ROW_BAD_TREE;
   if (r.bad) r.len = r.nodes = 0;
   r.from = p.window > 0 ? max(0, r.len - p.window + 1) / box * box : 0;
-  r.cached = r.nodes > 0 ? (r.len - r.from + kTok - 1) / kTok : 0;
   // a request without tokens still has its rows to write
-  r.tiles = max(1, r.cached + (r.nodes + kTok - 1) / kTok);
+  r.drafted = max(1, (r.nodes + kTok - 1) / kTok);
+  r.tiles = r.drafted + (r.nodes > 0 ? (r.len - r.from + kTok - 1) / kTok : 0);
   return r;
 }
 
-// The part of CTA `i` of `n`; all threads of the CTA, `scan` shared.
-__device__ Plan make_plan(const AttendParams &p, int box, int i, int n, long long *scan,
-                          Plan *shared) {
+// What a segment costs beside its tiles, in tiles: q, the first maxima, results.
+constexpr int kExtra = 4;
+
+// The part of CTA `i` of `n`; all threads of the CTA, `scan` shared.  The line is
+// measured in costs: each unit its tiles and kExtra, which stands before them.
+__device__ __forceinline__ Plan make_plan(const AttendParams &p, int box, int i, int n,
+                                          long long *scan, Plan *shared) {
   const int t = threadIdx.x, threads = blockDim.x;
   const int units = p.cache.Hkv * p.row_tiles;
   const int per = (p.B + threads - 1) / threads;
   long long mine = 0;
 #pragma unroll 1
   for (int b = t * per; b < min(p.B, (t + 1) * per); ++b)
-    mine += (long long)request_of(p, b, box).tiles * units;
+    mine += (long long)(request_of(p, b, box).tiles + kExtra) * units;
   long long upto = mine;  // inclusive scan
 #pragma unroll 1
   for (int d = 1; d < 32; d <<= 1) {
@@ -327,62 +327,78 @@ __device__ Plan make_plan(const AttendParams &p, int box, int i, int n, long lon
     total += scan[w];
   }
   upto += before;
-  const long long first = divide(total * i, n), last = divide(total * (i + 1), n);
-  if (t == 0) {
-    shared->total = total;
-    shared->first = first;
-    shared->count = last - first;
-  }
-  if (first >= upto - mine && first < upto) {
-    long long at = upto - mine;
-    for (int b = t * per;; ++b) {
-      const long long here = (long long)request_of(p, b, box).tiles * units;
-      if (first < at + here) {
-        shared->b = b;
-        shared->off = (int)(first - at);
-        break;
+  // the tiles from the first cut to the second; a cut is found by the thread
+  // whose requests it falls among
+#pragma unroll 1
+  for (int side = 0; side < 2; ++side) {
+    const long long cut = divide(total * (i + side), n);
+    if (cut >= upto - mine && (cut < upto || (cut == total && upto == total && mine > 0))) {
+      long long at = upto - mine, tiles = 0;
+      int b = t * per, off = 0;
+#pragma unroll 1
+      for (;; ++b) {
+        const int each = request_of(p, b, box).tiles + kExtra;
+        const long long here = (long long)each * units;
+        if (cut < at + here || b == min(p.B, (t + 1) * per) - 1) {
+          const int in = (int)min(cut - at, here), unit = in / each;
+          off = unit * (each - kExtra) + max(0, in - unit * each - kExtra);
+          break;
+        }
+        at += here;
       }
-      at += here;
+      (void)tiles;
+      if (side == 0) {
+        shared->b = b;
+        shared->off = off;
+      } else {
+        shared->count = ((long long)b << 32) | (uint32_t)off;  // the end's place, for now
+      }
     }
   }
   __syncthreads();
-  const Plan r = *shared;
-  __syncthreads();
-  return r;
+  return *shared;
 }
 
 // Segments of a CTA's part: runs of tiles of one unit (request, head, row tile).
 // Warp 0 walks them and publishes each in shared memory for the other roles.
 struct Walk {
-  long long left;
-  int b, off;
+  int b, off, end_b, end_off;
   Request r;
 
   __device__ Walk(const AttendParams &p, int box, const Plan &plan)
-      : left(plan.count), b(plan.b), off(plan.off) {
-    if (left > 0) r = request_of(p, b, box);
+      : b(plan.b), off(plan.off), end_b((int)(plan.count >> 32)), end_off((int)plan.count) {
+    r = request_of(p, b, box);
   }
   __device__ __forceinline__ bool next(const AttendParams &p, int box, Segment &s) {
     s.b = -1;
-    if (left <= 0) return false;
     const int units = p.cache.Hkv * p.row_tiles;
-    if (off >= r.tiles * units) {
+    if (off >= r.tiles * units && b < end_b) {
       ++b;
       off = 0;
       r = request_of(p, b, box);
     }
+    const int last = b < end_b ? r.tiles * units : end_off;
+    if (off >= last) return false;
     const int unit = off / r.tiles;
     s.b = b;
     s.t0 = off - unit * r.tiles;
     s.h = unit / p.row_tiles;
     s.rt = unit - s.h * p.row_tiles;
-    s.t1 = (int)min((long long)r.tiles, s.t0 + left);
+    s.t1 = min(r.tiles, s.t0 + last - off);
     s.r = r;
     s.whole = s.t0 == 0 && s.t1 == r.tiles;
-    left -= s.t1 - s.t0;
     off += s.t1 - s.t0;
     return true;
   }
+};
+
+// What the join has to know of a CTA's part.
+struct Note {
+  int tiles;        // of the part
+  int first, head;  // its first segment: where in its unit, and how many tiles
+  int unit;         // that unit's tiles, and which it is
+  int b, h, rt;
+  int open;         // tiles done of a unit that was begun but not ended here, or 0
 };
 
 // Waits until the phase of `parity` is complete.  Gives up after kWaitTries
@@ -450,7 +466,7 @@ __device__ __noinline__ uint4 load8_narrow(const unsigned short *s) {
 
 // Whether a window hides part of cached tile t from some row.
 __device__ __forceinline__ bool partly_hidden(const AttendParams &p, const Request &r, int t) {
-  return p.window > 0 && r.from + t * kTok <= r.len + p.N - 1 - p.window;
+  return p.window > 0 && r.from + (t - r.drafted) * kTok <= r.len + p.N - 1 - p.window;
 }
 
 // q . k of one row and one drafted token, from global memory, term by term.
@@ -471,7 +487,7 @@ __device__ __noinline__ float stray(const AttendParams &p, int box, int b, int h
   const specdec_kv_cache &kv = p.cache;
   const Request r = request_of(p, b, box);
   float sum = 0.0f;
-  const int j0 = max(0, t0 - r.cached) * kTok, j1 = (t1 - r.cached) * kTok;
+  const int j0 = t0 * kTok, j1 = min(t1, r.drafted) * kTok;
   int a = n;
   for (int step = 0; a >= 0 && (p.window == 0 || step < p.window); ++step) {
     if (a >= j0 && a < j1) {
@@ -486,9 +502,9 @@ __device__ __noinline__ float stray(const AttendParams &p, int box, int b, int h
     }
     a = up;
   }
-  for (int t = t0; t < min(t1, r.cached) && partly_hidden(p, r, t); ++t)
+  for (int t = max(t0, r.drafted); t < t1 && partly_hidden(p, r, t); ++t)
     for (int i = 0; i < kTok; ++i) {
-      const int at = r.from + t * kTok + i;
+      const int at = r.from + (t - r.drafted) * kTok + i;
       if (at >= r.len || pos - at >= p.window) continue;
       const int id = kv.block_table[(long long)b * kv.max_blocks + at / kv.block];
       if (id < 0 || id >= kv.n_blocks) continue;
@@ -501,6 +517,11 @@ __device__ __noinline__ float stray(const AttendParams &p, int box, int b, int h
 
 // A partial: for each row m, l, then its D elements; flags as l < 0.
 __host__ __device__ inline size_t partial_floats(int RN, int D) { return (size_t)RN * (D + 2); }
+// Two slots a CTA: what it did of a unit begun before, and of one that it began.
+// Behind them the notes.
+__device__ __forceinline__ Note *notes_of(float *part, int RN, int D) {
+  return reinterpret_cast<Note *>(part + 4 * kMaxSms * partial_floats(RN, D));
+}
 
 // ---------------------------------------------------------------------------
 // the kernel
@@ -508,13 +529,14 @@ __host__ __device__ inline size_t partial_floats(int RN, int D) { return (size_t
 template <int RN, bool kPlain>
 struct Tile {
   using S = Smem<RN>;
-  static constexpr int kK = Cfg<RN>::kK, kV = Cfg<RN>::kV;
+  using C = Cfg<RN>;
+  static constexpr int kK = C::kK, kBuf = C::kBuf;
   const AttendParams &p;
   S &sm;
   const CUtensorMap *k_map, *v_map;
   const int box, lane, warp;
   const int box_shift;
-  const uint32_t g_magic;  // ceil(2^32 / G): row / G for rows below 2^16 * G
+  const uint32_t g_magic;  // ceil(2^32 / G): row / G for rows below 2^32 / G
   int columns;  // rows of a tile, a multiple of 16
 
   __device__ Tile(const AttendParams &p_, S &s_, const CUtensorMap *k_, const CUtensorMap *v_,
@@ -550,13 +572,30 @@ struct Tile {
   __device__ __forceinline__ Piece piece_of(const Segment &w, int t) const {
     const specdec_kv_cache &kv = p.cache;
     Piece x;
-    x.tok = w.r.from + t * kTok + lane * box;
-    x.mine = lane * box < kTok && x.tok < w.r.len && t < w.r.cached;
+    x.tok = w.r.from + (t - w.r.drafted) * kTok + lane * box;
+    x.mine = t >= w.r.drafted && lane * box < kTok && x.tok < w.r.len;
     x.id = x.mine ? __ldg(kv.block_table + (long long)w.b * kv.max_blocks + x.tok / kv.block) : 0;
     return x;
   }
-  __device__ __forceinline__ bool publish(Walk &walk, uint32_t index, Segment &w) {
+  Note note;
+  __device__ __forceinline__ bool take(Walk &walk, Segment &w) {
     const bool more = walk.next(p, box, w);
+    if (more) {
+      if (note.tiles == 0) {
+        note.first = w.t0;
+        note.head = w.t1 - w.t0;
+        note.unit = w.r.tiles;
+        note.b = w.b;
+        note.h = w.h;
+        note.rt = w.rt;
+      }
+      note.tiles += w.t1 - w.t0;
+      note.open = w.t0 == 0 && !w.whole ? w.t1 : 0;
+    }
+    return more;
+  }
+  __device__ __forceinline__ bool publish(Walk &walk, uint32_t index, Segment &w) {
+    const bool more = take(walk, w);
     if (lane == 0) {
       sm.seg[index & 7] = w;
       mbar_arrive(&sm.seg_full[index & 7]);
@@ -567,6 +606,7 @@ struct Tile {
   __device__ __forceinline__ void copies(const Plan &plan) {
     const specdec_kv_cache &kv = p.cache;
     uint32_t c = 0, index = 0;
+    note.tiles = note.first = note.head = note.open = 0;
     Walk walk(p, box, plan);
     Segment w, ahead;
     bool ok = true, more = publish(walk, 0, ahead);
@@ -577,10 +617,10 @@ struct Tile {
       Piece next = piece_of(w, w.t0);
 #pragma unroll 1
       for (int t = w.t0; t < w.t1; ++t, ++c) {
-        const int ks = c % kK, vs = c % kV;
+        const int ks = c % kK;
         Piece x = next;
         if (t + 1 < w.t1) next = piece_of(w, t + 1);  // the next tile's ids load meanwhile
-        const bool cached = t < w.r.cached;
+        const bool cached = t >= w.r.drafted;
         if (x.id < 0 || x.id >= kv.n_blocks) {
           x.id = 0;
           sm.bad[index & 7] = SPECDEC_ROW_BAD_CACHE;
@@ -598,12 +638,12 @@ struct Tile {
           __syncwarp();
           if (x.mine) tma_rows(sm.k[ks] + lane * box * kRow, k_map, row, &sm.k_full[ks]);
         }
-        if (!(ok = wait(&sm.v_empty[vs], empty_par(c, kV)))) break;
+        if (!(ok = wait(&sm.v_empty, empty_par(c, 1)))) break;
         if (cached) {
-          if (lane == 0) mbar_arrive_expect_tx(&sm.v_full[vs], bytes);
+          if (lane == 0) mbar_arrive_expect_tx(&sm.v_full, bytes);
           __syncwarp();
           if (x.mine) {
-            tma_rows(sm.v[vs] + lane * box * kRow, v_map, row, &sm.v_full[vs]);
+            tma_rows(sm.v + lane * box * kRow, v_map, row, &sm.v_full);
             sm.boxes[c & 7][lane] = unit;
           }
           __syncwarp();
@@ -614,25 +654,28 @@ struct Tile {
     // Every copy has been waited on by its reader, unless somebody gave up: then
     // copies in flight get time to land before the CTA may leave.
     copied = c;
+#pragma unroll 1
+    while (take(walk, w)) {
+    }
+    if (lane == 0) notes_of(p.part, RN, kv.D)[blockIdx.x] = note;
   }
 
   uint32_t copied;
   __device__ void drain() {
     for (uint32_t i = copied > kK ? copied - kK : 0; i < copied; ++i)
       mbar_wait_bounded(&sm.k_full[i % kK], full_par(i, kK));
-    for (uint32_t i = copied > kV ? copied - kV : 0; i < copied; ++i)
-      mbar_wait_bounded(&sm.v_full[i % kV], full_par(i, kV));
+    if (copied > 0) mbar_wait_bounded(&sm.v_full, full_par(copied - 1, 1));
   }
 
   // ------------------------------------------------------------ warp 1: products
-  __device__ __forceinline__ void scores(uint32_t c, bool drafted, int q, bool ends) {
+  __device__ __forceinline__ void scores(uint32_t c, bool drafted, bool ends) {
     if (elected()) {
       const uint32_t d = sm_tmem + (c & 1) * RN, idesc = shape(columns, false);
       const int steps = (p.cache.D + 31) / 32;
       // 32 elements a step: 32 bytes, 2 units of the descriptor's address
       const uint64_t ka = operand(smem_addr(sm.k[c % kK]), 1024, 16);
-      const uint64_t qa = operand(smem_addr(sm.q[q][0]), 1024, 16);
-      const uint64_t qb = operand(smem_addr(sm.q[q][1]), 1024, 16);
+      const uint64_t qa = operand(smem_addr(sm.q[0]), 1024, 16);
+      const uint64_t qb = operand(smem_addr(sm.q[1]), 1024, 16);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (i >= steps) continue;
@@ -640,7 +683,7 @@ struct Tile {
         mma_issue<true>(d, ka + 2 * i, qb + 2 * i, idesc, true);
       }
       if (drafted) {
-        const uint64_t kl = operand(smem_addr(sm.v[c % kV]), 1024, 16);
+        const uint64_t kl = operand(smem_addr(sm.v), 1024, 16);
 #pragma unroll 1
         for (int i = 0; i < steps; ++i) {
           mma_issue<true>(d, kl + 2 * i, qa + 2 * i, idesc, true);
@@ -649,30 +692,30 @@ struct Tile {
       }
       mma_commit(&sm.s_full[c & 1]);
       mma_commit(&sm.k_empty[c % kK]);
-      if (drafted) {  // the low terms stood in a V slot, which four arrivals free
-        mbar_arrive(&sm.v_empty[c % kV]);
-        mbar_arrive(&sm.v_empty[c % kV]);
-        mbar_arrive(&sm.v_empty[c % kV]);
-        mma_commit(&sm.v_empty[c % kV]);
+      if (drafted) {  // the low terms stood in V's place, which an arrival of each worker frees
+#pragma unroll
+        for (int i = 1; i < C::kWorkers; ++i) mbar_arrive(&sm.v_empty);
+        mma_commit(&sm.v_empty);
       }
-      if (ends) mma_commit(&sm.q_empty[q]);
+      if (ends) mma_commit(&sm.q_empty);
     }
     __syncwarp();
   }
 
   __device__ __forceinline__ bool outputs(uint32_t c, bool first) {
-    if (!wait(&sm.vh_full[c & 1], (c >> 1) & 1) || !wait(&sm.p_full[c & 1], (c >> 1) & 1))
+    if (!wait(&sm.vh_full[c % kBuf], full_par(c, kBuf)) ||
+        !wait(&sm.p_full[c % kBuf], full_par(c, kBuf)))
       return false;
     fence_after();
     if (elected()) {
-      const uint32_t d = sm_tmem + (Cfg<RN>::kTurns ? 2 + (c & 1) : 2) * RN;
+      const uint32_t d = sm_tmem + 2 * RN;
       const uint32_t idesc = shape(columns, true);
-      const uint64_t va = operand(smem_addr(sm.vh[c & 1][0]), 1024, kTileBytes);
-      const uint64_t pb = operand(smem_addr(sm.pt[c & 1][0]), 1024, kTileBytes);
+      const uint64_t va = operand(smem_addr(sm.vh[c % kBuf][0]), 1024, kTileBytes);
+      const uint64_t pb = operand(smem_addr(sm.pt[c % kBuf][0]), 1024, kTileBytes);
 #pragma unroll
       for (int i = 0; i < kTok / 16; ++i)  // 16 tokens a step: 2048 bytes
         mma_issue<false>(d, va + 128 * i, pb + 128 * i, idesc, !first || i > 0);
-      mma_commit(&sm.pv_done[c & 1]);
+      mma_commit(&sm.pv_done[c % kBuf]);
     }
     __syncwarp();
     return true;
@@ -680,45 +723,43 @@ struct Tile {
 
   uint32_t sm_tmem;
   __device__ __forceinline__ void products() {
-    constexpr int kLag = Cfg<RN>::kLag, kQ = Cfg<RN>::kQ;
-    uint32_t c = 0, done = 0;  // tiles whose scores, and whose outputs were issued
-    uint32_t firsts = 0;       // bit k: tile c - 1 - k is its accumulator's first
-    bool ok = true;
+    uint32_t c = 0;
+    bool ok = true, pending = false, pending_first = false;  // outputs of tile c - 1
     sm_tmem = sm.tmem;
 #pragma unroll 1
     for (uint32_t index = 0; segment(index, ok); ++index) {
       const int t0 = sm.seg[index & 7].t0, t1 = sm.seg[index & 7].t1;
-      const int cached = sm.seg[index & 7].r.cached;
+      const int drafts = sm.seg[index & 7].r.drafted;
 #pragma unroll 1
       for (int t = t0; t < t1; ++t, ++c) {
-        const bool drafted = t >= cached;
-        // Outputs of the tiles before: up to kLag stay behind, so that scores run
-        // ahead of the softmax.  Before a drafted tile fewer: its operands wait for
-        // room that those outputs free.  And where q has one place only, none
-        // before a segment: the next q waits for the softmax of the last.
-        const uint32_t behind = kQ == 1 && t == t0 ? 0 : drafted ? 1 : kLag;
-#pragma unroll 1
-        for (; ok && c - done > behind; ++done) ok = outputs(done, (firsts >> (c - 1 - done)) & 1);
-        if (!ok) break;
-        if (t == t0 && !(ok = wait(&sm.q_full[index % kQ], (index / kQ) & 1))) break;
+        const bool drafted = t < drafts, first = t == t0;
+        // Scores run a tile ahead of outputs; but at a segment's start, and before
+        // a drafted tile that needs the room which they free, outputs come first.
+        const bool flush = first || (kBuf == 1 && drafted);
+        if (flush && pending) {
+          if (!(ok = outputs(c - 1, pending_first))) break;
+          pending = false;
+        }
+        if (first && !(ok = wait(&sm.q_full, index & 1))) break;
         if (!(ok = wait(&sm.box_full[c & 7], (c >> 3) & 1))) break;
         if (drafted) {
           if (lane == 0) {  // nobody copies into this tile's slots
             mbar_arrive(&sm.k_full[c % kK]);
-            mbar_arrive(&sm.v_full[c % kV]);
+            mbar_arrive(&sm.v_full);
           }
         } else if (!(ok = wait(&sm.k_full[c % kK], full_par(c, kK)))) {
           break;
         }
         if (!(ok = wait(&sm.s_empty[c & 1], ((c >> 1) & 1) ^ 1))) break;
         fence_after();
-        scores(c, drafted, index % kQ, t == t1 - 1);
-        firsts = firsts << 1 | (t - t0 < (Cfg<RN>::kTurns ? 2 : 1));
+        scores(c, drafted, t == t1 - 1);
+        if (pending && !(ok = outputs(c - 1, pending_first))) break;
+        pending = true;
+        pending_first = first;
       }
       if (!ok) break;
     }
-#pragma unroll 1
-    for (; ok && done < c; ++done) ok = outputs(done, (firsts >> (c - 1 - done)) & 1);
+    if (ok && pending) outputs(c - 1, pending_first);
     // products in flight end before the CTA may leave
     if (elected()) mma_commit(&sm.fin);
     __syncwarp();
@@ -783,7 +824,7 @@ struct Tile {
 
   __device__ __forceinline__ void stage_q(uint32_t index, int worker) {
     const Segment &w = sm.seg[index & 7];
-    const int D = p.cache.D, ring = index & 3, e = (lane & 15) * 8, q = index % Cfg<RN>::kQ;
+    const int D = p.cache.D, ring = index & 3, e = (lane & 15) * 8;
     const int nodes = w.r.nodes, row0 = w.rt * RN;
     const bool wide = ((reinterpret_cast<uintptr_t>(p.q) | (uintptr_t)(p.q_stride * 2)) & 15) == 0;
     const long long first = (long long)w.b * p.N;
@@ -795,12 +836,12 @@ struct Tile {
     };
     uint4 next = load(worker * 2 + (lane >> 4));
 #pragma unroll 1
-    for (int r = worker * 2 + (lane >> 4); r < columns; r += 8) {
+    for (int r = worker * 2 + (lane >> 4); r < columns; r += 2 * C::kWorkers) {
       const uint4 x = next;
-      next = load(r + 8);
+      next = load(r + 2 * C::kWorkers);
       bool all;
       const int ex = unit_exponent(row_top(x, all), 7);
-      split(sm.q[q][0], sm.q[q][1], r, e, x, ex);
+      split(sm.q[0], sm.q[1], r, e, x, ex);
       if ((lane & 15) == 0) {
         const int row = row0 + r, n = node_of(row);
         const bool in = row < p.N * p.G && n < nodes;
@@ -815,7 +856,7 @@ struct Tile {
     }
     fence_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&sm.q_full[q]);
+    if (lane == 0) mbar_arrive(&sm.q_full);
   }
 
   // NaN codes of a tile that a window hides in part: out of the products, as
@@ -823,10 +864,10 @@ struct Tile {
   __device__ __noinline__ static bool sift(uint8_t *codes, int tid) {
     bool odd = false;
 #pragma unroll 1
-    for (int i = 0; i < 32; ++i) {  // the thread's own pieces, as widen reads them
-      const int at = (i >> 2) * 128 + tid, tok = at >> 3;
+    for (int i = 0; i < 4 * (kTok / (4 * C::kWorkers)); ++i) {  // the thread's own pieces
+      const int tok = (tid >> 3) + (i >> 2) * 4 * C::kWorkers;
       uint32_t *w = reinterpret_cast<uint32_t *>(codes + tok * kRow +
-                                                 (((at & 7) ^ (tok & 7)) << 4)) + (i & 3);
+                                                 (((tid & 7) ^ (tok & 7)) << 4)) + (i & 3);
       uint32_t keep = 0;
       for (int s = 0; s < 32; s += 8)
         if (((*w >> s) & 0x7Fu) != 0x7Fu) keep |= 0xFFu << s;
@@ -839,33 +880,34 @@ struct Tile {
   // V codes of a cached tile to fp16; tokens past the length as zeros.
   __device__ __forceinline__ void widen(const Segment &w, uint32_t index, int t, uint32_t c,
                                         int worker) {
-    const int held = w.r.len - (w.r.from + t * kTok), tid = worker * 32 + lane;
-    uint8_t *src = sm.v[c % kV];
+    constexpr int kStep = 4 * C::kWorkers;  // tokens at once: 8 lanes each
+    const int held = w.r.len - (w.r.from + (t - w.r.drafted) * kTok), tid = worker * 32 + lane;
+    uint8_t *src = sm.v;
     if (partly_hidden(p, w.r, t) && sift(src, tid)) sm.dirty[index & 7] = 1;
-    // a thread's pieces are 16 tokens apart: the same place in the swizzle
-    const int tok0 = tid >> 3, j = tid & 7, x7 = tok0 & 7, side = j >> 2, piece = (j & 3) * 2;
-    src += tok0 * kRow + ((j ^ x7) << 4);
-    // lanes of the two 64-element groups write odd and even pieces in turn:
-    // eight lanes cover eight different 16-byte banks
-    uint8_t *dst = sm.vh[c & 1][side] + tok0 * kRow;
-    uint8_t *d0 = dst + (((piece + side) ^ x7) << 4), *d1 = dst + (((piece + 1 - side) ^ x7) << 4);
+    // a thread's pieces are whole groups of 8 tokens apart: the same place in the
+    // swizzle, or every second of two
+    const int tok0 = tid >> 3, j = tid & 7, side = j >> 2, piece = (j & 3) * 2;
 #pragma unroll 4
-    for (int i = 0; i < 8; ++i) {
-      uint4 x = *reinterpret_cast<const uint4 *>(src + i * 16 * kRow);
-      if (tok0 + 16 * i >= held) x = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = 0; i < kTok / kStep; ++i) {
+      const int tok = tok0 + i * kStep, x7 = tok & 7;
+      uint4 x = *reinterpret_cast<const uint4 *>(src + tok * kRow + ((j ^ x7) << 4));
+      if (tok >= held) x = make_uint4(0u, 0u, 0u, 0u);
       const uint4 lo = make_uint4(e4m3x2_to_half2(x.x & 0xFFFFu), e4m3x2_to_half2(x.x >> 16),
                                   e4m3x2_to_half2(x.y & 0xFFFFu), e4m3x2_to_half2(x.y >> 16));
       const uint4 hi = make_uint4(e4m3x2_to_half2(x.z & 0xFFFFu), e4m3x2_to_half2(x.z >> 16),
                                   e4m3x2_to_half2(x.w & 0xFFFFu), e4m3x2_to_half2(x.w >> 16));
-      *reinterpret_cast<uint4 *>(d0 + i * 16 * kRow) = side ? hi : lo;
-      *reinterpret_cast<uint4 *>(d1 + i * 16 * kRow) = side ? lo : hi;
+      // lanes of the two 64-element groups write odd and even pieces in turn:
+      // eight lanes cover eight different 16-byte banks
+      uint8_t *dst = sm.vh[c % kBuf][side] + tok * kRow;
+      *reinterpret_cast<uint4 *>(dst + (((piece + side) ^ x7) << 4)) = side ? hi : lo;
+      *reinterpret_cast<uint4 *>(dst + (((piece + 1 - side) ^ x7) << 4)) = side ? lo : hi;
     }
   }
 
   // A tile of drafted tokens: nodes [j0, j0 + 128).
   __device__ __forceinline__ void build(const Segment &w, uint32_t index, int t, uint32_t c,
                                         int worker) {
-    const int D = p.cache.D, j0 = (t - w.r.cached) * kTok, e = (lane & 15) * 8;
+    const int D = p.cache.D, j0 = t * kTok, e = (lane & 15) * 8;
     const int nodes = w.r.nodes, held = min(nodes - j0, kTok);
     const long long first = (long long)w.b * p.N;
     const bool k_wide =
@@ -873,7 +915,7 @@ struct Tile {
     const bool v_wide =
         ((reinterpret_cast<uintptr_t>(p.v_new) | (uintptr_t)(p.v_stride * 2)) & 15) == 0;
 #pragma unroll 1
-    for (int r = worker * 2 + (lane >> 4); r - (lane >> 4) < held; r += 8) {
+    for (int r = worker * 2 + (lane >> 4); r - (lane >> 4) < held; r += 2 * C::kWorkers) {
       const bool in = r < held && e < D;
       const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
       const uint4 x = in ? load8(p.k_new, (first + j0 + r) * p.k_stride + (long long)w.h * D + e, k_wide)
@@ -882,7 +924,7 @@ struct Tile {
                          : zero;
       bool all;
       const int ek = unit_exponent(row_top(x, all), 7);
-      split(sm.k[c % kK], sm.v[c % kV], r, e, x, ek);
+      split(sm.k[c % kK], sm.v, r, e, x, ek);
       const float k_unit = all ? pow2i(ek) : -1.0f;
       const int ev = unit_exponent(row_top(y, all), 10);
       const float inv = pow2i(-ev);
@@ -894,7 +936,7 @@ struct Tile {
         const float v0 = bf16_lo(b[i]), v1 = bf16_hi(b[i]);
         a[i] = pack_half2(finite(v0) ? v0 * inv : 0.0f, finite(v1) ? v1 * inv : 0.0f);
       }
-      *reinterpret_cast<uint4 *>(sm.vh[c & 1][e >> 6] + r * kRow +
+      *reinterpret_cast<uint4 *>(sm.vh[c % kBuf][e >> 6] + r * kRow +
                                  ((((e & 63) >> 3) ^ (r & 7)) << 4)) =
           make_uint4(a[0], a[1], a[2], a[3]);
       if ((lane & 15) == 0) sm.unit[c & 1][r] = make_float2(k_unit, pow2i(ev));
@@ -902,34 +944,36 @@ struct Tile {
     // past the last node: weights there are 0, but V must not be NaN
     const int tid = worker * 32 + lane;
 #pragma unroll 1
-    for (int i = max(held, 0) * 8 + tid; i < kTok * 8; i += 128) {
+    for (int i = max(held, 0) * 8 + tid; i < kTok * 8; i += 32 * C::kWorkers) {
       const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-      reinterpret_cast<uint4 *>(sm.vh[c & 1][0])[i] = zero;
-      reinterpret_cast<uint4 *>(sm.vh[c & 1][1])[i] = zero;
+      reinterpret_cast<uint4 *>(sm.vh[c % kBuf][0])[i] = zero;
+      reinterpret_cast<uint4 *>(sm.vh[c % kBuf][1])[i] = zero;
     }
     // what each row sees of this tile: its node's ancestors, as bits
-    const int n = node_of(w.rt * RN + tid);
-    uint32_t bits[4] = {0u, 0u, 0u, 0u};
-    if (tid < columns && n < nodes) {
-      int a = n;
 #pragma unroll 1
-      for (int step = 0; a >= j0; ++step) {
-        if (a < j0 + kTok && (p.window == 0 || step < p.window)) {
-          const uint32_t bit = 1u << ((a - j0) & 31);
+    for (int col = tid; col < columns; col += 32 * C::kWorkers) {
+      const int n = node_of(w.rt * RN + col);
+      uint32_t bits[4] = {0u, 0u, 0u, 0u};
+      if (n < nodes) {
+        int a = n;
+#pragma unroll 1
+        for (int step = 0; a >= j0; ++step) {
+          if (a < j0 + kTok && (p.window == 0 || step < p.window)) {
+            const uint32_t bit = 1u << ((a - j0) & 31);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if ((a - j0) >> 5 == i) bits[i] |= bit;
+            for (int i = 0; i < 4; ++i)
+              if ((a - j0) >> 5 == i) bits[i] |= bit;
+          }
+          a = above(first, a);
         }
-        a = above(first, a);
       }
-    }
-    if (tid < columns)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sm.see[c & 1][i][tid] = bits[i];
+      for (int i = 0; i < 4; ++i) sm.see[c & 1][i][col] = bits[i];
+    }
     if (p.parent) {
       bool wrong = false;
 #pragma unroll 1
-      for (int i = tid; i < nodes; i += 128) {
+      for (int i = tid; i < nodes; i += 32 * C::kWorkers) {
         const int up = __ldg(p.parent + first + i);
         wrong |= i == 0 ? up != -1 : (up < 0 || up >= i);
       }
@@ -944,27 +988,19 @@ struct Tile {
 #pragma unroll 1
     for (uint32_t index = 0; segment(index, ok); ++index) {
       const Segment &w = sm.seg[index & 7];
-      const int t0 = w.t0, t1 = w.t1, cached = w.r.cached;
-      // q of this segment, where it is not there yet; and ahead, once this one's
-      // first tile is on its way, of the next
-      bool staged = Cfg<RN>::kQ == 2 && index > 0;
-      uint32_t stage = index;
+      const int t0 = w.t0, t1 = w.t1, drafts = w.r.drafted;
+      if (!(ok = wait(&sm.q_empty, (index & 1) ^ 1))) break;
+      stage_q(index, worker);
 #pragma unroll 1
-      for (int t = t0;; ++t, ++c) {
-        if (!staged) {
-          if (!(ok = wait(&sm.q_empty[stage % Cfg<RN>::kQ], ((stage / Cfg<RN>::kQ) & 1) ^ 1))) break;
-          stage_q(stage, worker);
-          staged = true;
-        }
-        if (t >= t1) break;
-        const bool drafted = t >= cached;
+      for (int t = t0; t < t1; ++t, ++c) {
+        const bool drafted = t < drafts;
         if (drafted) {
           if (!(ok = wait(&sm.k_empty[c % kK], empty_par(c, kK)))) break;
-          if (!(ok = wait(&sm.v_empty[c % kV], empty_par(c, kV)))) break;
-        } else if (!(ok = wait(&sm.v_full[c % kV], full_par(c, kV)))) {
+          if (!(ok = wait(&sm.v_empty, empty_par(c, 1)))) break;
+        } else if (!(ok = wait(&sm.v_full, full_par(c, 1)))) {
           break;
         }
-        if (!(ok = wait(&sm.pv_done[c & 1], ((c >> 1) & 1) ^ 1))) break;
+        if (!(ok = wait(&sm.pv_done[c % kBuf], empty_par(c, kBuf)))) break;
         if (drafted)
           build(w, index, t, c, worker);
         else
@@ -972,26 +1008,21 @@ struct Tile {
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(drafted ? &sm.box_full[c & 7] : &sm.v_empty[c % kV]);
-          mbar_arrive(&sm.vh_full[c & 1]);
+          if (!drafted) mbar_arrive(&sm.v_empty);
+          mbar_arrive(&sm.vh_full[c % kBuf]);
         }
+        // four arrivals complete box_full
+        if (drafted && lane < 4 / C::kWorkers) mbar_arrive(&sm.box_full[c & 7]);
         // as the copying warp: every phase of v_full is waited on
-        if (drafted && !(ok = wait(&sm.v_full[c % kV], full_par(c, kV)))) break;
-        if (Cfg<RN>::kQ == 2 && t == t0) {
-          bool more;
-          more = segment(index + 1, ok);
-          if (!ok) break;
-          stage = index + 1;
-          staged = !more;
-        }
+        if (drafted && !(ok = wait(&sm.v_full, full_par(c, 1)))) break;
       }
       if (!ok) break;
     }
   }
 
-  // ------------------------------------------------------------ warps 6-13: softmax
+  // ------------------------------------------------------------ the last warps: softmax
   uint32_t group_phase, both_phase;
-  // The four warps of one group, and all eight.
+  // The four warps of one group, and all softmax warps.
   __device__ __forceinline__ bool meet(int group) {
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.group[group]);
@@ -999,12 +1030,17 @@ struct Tile {
     group_phase ^= 1;
     return ok;
   }
-  __device__ __forceinline__ bool meet_both() {
+  __device__ __forceinline__ bool meet_all() {
     fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sm.both);
-    const bool ok = wait(&sm.both, both_phase);
-    both_phase ^= 1;
+    bool ok;
+    if (C::kGroups == 1) {
+      ok = meet(0);
+    } else {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.both);
+      ok = wait(&sm.both, both_phase);
+      both_phase ^= 1;
+    }
     fence_after();
     return ok;
   }
@@ -1024,7 +1060,7 @@ struct Tile {
   // masked, in base-2 units.  tok: the thread's token; unit: its k's.
   __device__ __forceinline__ void bend(const Segment &w, int ring, int t, uint32_t c, bool drafted,
                                        float unit, int tok, int c0, int mine, uint32_t s_at) {
-    const int at = w.r.from + t * kTok + tok, j = (t - w.r.cached) * kTok + tok;
+    const int at = w.r.from + (t - w.r.drafted) * kTok + tok, j = t * kTok + tok;
     const bool exists = drafted ? j < w.r.nodes : at < w.r.len, special = drafted && unit < 0.0f;
     const int quarter = tok >> 5, window = drafted ? 0 : p.window;
     if (!__any_sync(kAll, exists)) {  // a warp past the last token
@@ -1070,72 +1106,90 @@ struct Tile {
     tmem_stored();
   }
 
-  // Sums of 8 values over a warp's lanes: lane 4 i holds that of value i.
-  __device__ __forceinline__ float sum8(const float *v) const {
+  // Sums, or maxima, of 8 values over a warp's lanes: lane 4 i holds that of value i.
+  template <bool kMax>
+  __device__ __forceinline__ float over_lanes(const float *v) const {
+    auto join = [](float a, float b) { return kMax ? fmaxf(a, b) : a + b; };
     float a[4], b[2];
+    bool up = lane & 16;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const bool up = lane & 16;
-      a[k] = (up ? v[k + 4] : v[k]) + __shfl_xor_sync(kAll, up ? v[k] : v[k + 4], 16);
-    }
+    for (int k = 0; k < 4; ++k)
+      a[k] = join(up ? v[k + 4] : v[k], __shfl_xor_sync(kAll, up ? v[k] : v[k + 4], 16));
+    up = lane & 8;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const bool up = lane & 8;
-      b[k] = (up ? a[k + 2] : a[k]) + __shfl_xor_sync(kAll, up ? a[k] : a[k + 2], 8);
-    }
-    const bool up = lane & 4;
-    float x = (up ? b[1] : b[0]) + __shfl_xor_sync(kAll, up ? b[0] : b[1], 4);
-    x += __shfl_xor_sync(kAll, x, 2);
-    return x + __shfl_xor_sync(kAll, x, 1);
+    for (int k = 0; k < 2; ++k)
+      b[k] = join(up ? a[k + 2] : a[k], __shfl_xor_sync(kAll, up ? a[k] : a[k + 2], 8));
+    up = lane & 4;
+    float x = join(up ? b[1] : b[0], __shfl_xor_sync(kAll, up ? b[0] : b[1], 4));
+    x = join(x, __shfl_xor_sync(kAll, x, 2));
+    return join(x, __shfl_xor_sync(kAll, x, 1));
   }
 
   __device__ __forceinline__ void softmax() {
-    constexpr bool kTurns = Cfg<RN>::kTurns, kHold = Cfg<RN>::kHold;
-    constexpr int kCols = Cfg<RN>::kCols, kCh = kCols / 8;
-    const int group = warp >= 10, quarter = warp & 3, tok = quarter * 32 + lane;
-    // the group's columns: all of every other tile, or half of every tile
-    const int mine = kTurns ? (min(RN, p.N * p.G) + 7) / 8 * 8 : columns / 2;
-    const int c0 = kTurns ? 0 : group * mine;
+    constexpr bool kHold = C::kHold;
+    constexpr int kCols = C::kCols, kCh = kCols / 8;
+    const int group = C::kGroups == 1 ? 0 : (warp - C::kFirst) >> 2;
+    const int quarter = warp & 3, tok = quarter * 32 + lane;
+    // the group's columns
+    const int mine = C::kGroups == 1 ? (min(RN, p.N * p.G) + 7) / 8 * 8 : columns / 2;
+    const int c0 = group * mine;
     const bool leader = lane == 0 && quarter == 0;
     const uint32_t lanes = sm.tmem + ((uint32_t)quarter << 21);  // TMEM lanes of this warp
-    const uint32_t o_at = lanes + (kTurns ? 2 + group : 2) * RN + c0;
+    const uint32_t o_at = lanes + 2 * RN + c0;
     const specdec_kv_cache &kv = p.cache;
     uint32_t c = 0;  // the tile's number, of all
     group_phase = both_phase = 0;
     f2 l[kCols / 2];
     float *const nms = sm.nm[group];
-    bool ok = true;
-    for (uint32_t index = 0; segment(index, ok); ++index) {
+    if (tok < mine) nms[tok] = 0.0f;
+    bool ok = meet(group);
+#pragma unroll 1
+    for (uint32_t index = 0; ok && segment(index, ok); ++index) {
       const Segment &w = sm.seg[index & 7];
       const int ring = index & 3, t0 = w.t0, t1 = w.t1;
       float vref = 0.0f;
-      uint32_t last = ~0u;  // the group's last tile of the segment
 #pragma unroll
       for (int i = 0; i < kCols / 2; ++i) l[i] = 0ull;
-      // the rows have seen nothing yet
-      if (tok < mine) nms[tok] = kUnseen;
+      bool unseen = true;  // the thread's column (tok) has seen no score yet
 #pragma unroll 1
-      for (int t = t0; ok && t < t1; ++t, ++c) {
-        if (kTurns && (int)(c & 1) != group) continue;
-        const bool drafted = t >= w.r.cached, first = last == ~0u;
+      for (int t = t0; t < t1; ++t, ++c) {
+        const bool drafted = t < w.r.drafted, first = t == t0;
         const uint32_t s_at = lanes + (c & 1) * RN + c0;
         if (!(ok = wait(&sm.box_full[c & 7], (c >> 3) & 1))) break;
         const float2 unit = drafted ? sm.unit[c & 1][tok] : sm.boxes[c & 7][tok >> box_shift];
         if (!(ok = wait(&sm.s_full[c & 1], (c >> 1) & 1))) break;
         fence_after();
         // a plain tile's scores are a factor away; the others are written back
-        const int past = w.r.from + t * kTok + kTok - w.r.len;
+        const int past = drafted ? (t + 1) * kTok - w.r.nodes
+                                 : w.r.from + (t - w.r.drafted + 1) * kTok - w.r.len;
         const bool kept = !kPlain || drafted || past > 0 || partly_hidden(p, w.r, t);
         if (kept) bend(w, ring, t, c, drafted, unit.x, tok, c0, mine, s_at);
-        const bool exists = drafted ? (t - w.r.cached) * kTok + tok < w.r.nodes : past + tok < kTok;
-        const float v_unit = exists ? unit.y : 0.0f;
+        const float v_unit = past + tok < kTok ? unit.y : 0.0f;
         const float k_unit = kept ? 1.0f : unit.x;
         const f2 ks = pair(k_unit, k_unit);
         const float *factor = kept ? sm.ones : sm.rf[ring] + c0;
         float x[kHold ? kCols : 8];
-        bool moved = false;
+        // Passes over the scores: 0 under the present maxima, with a vote; where
+        // they have to move, 1 for the tile's own (columns without any at 0), and
+        // 2 under the new ones.
+        int pass = first ? 1 : 0;
+#pragma unroll 1
         for (;;) {
           float top = -INFINITY;
+          if (!kHold && pass == 1) {  // the warp's maxima
+#pragma unroll 1
+            for (int ch = 0; ch * 8 < mine; ++ch) {
+              float y[8];
+              tmem_load8(s_at + ch * 8, y);
+              tmem_wait8(y);
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                y[k] = fmaf(y[k], k_unit * factor[ch * 8 + k], nms[ch * 8 + k]);
+              const float best = over_lanes<true>(y);
+              if ((lane & 3) == 0) sm.red[group][quarter][ch * 8 + (lane >> 2)] = best;
+              __syncwarp();
+            }
+          }
           if (kHold) {
 #pragma unroll
             for (int ch = 0; ch < kCh; ++ch)
@@ -1143,38 +1197,42 @@ struct Tile {
           }
 #pragma unroll
           for (int ch = 0; ch < kCh; ++ch) {
-            if (ch * 8 >= mine) continue;
+            if (ch * 8 >= mine || (!kHold && pass == 1)) continue;
             float *s = x + (kHold ? ch * 8 : 0);
             if (!kHold) tmem_load8(s_at + ch * 8, s);
+            ulonglong2 r[2], n[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              r[k] = *reinterpret_cast<const ulonglong2 *>(factor + ch * 8 + 4 * k);
+              n[k] = *reinterpret_cast<const ulonglong2 *>(nms + ch * 8 + 4 * k);
+            }
             tmem_wait8(s);
 #pragma unroll
-            for (int k = 0; k < 8; k += 4) {
-              const ulonglong2 r = *reinterpret_cast<const ulonglong2 *>(factor + ch * 8 + k);
-              const ulonglong2 n = *reinterpret_cast<const ulonglong2 *>(nms + ch * 8 + k);
-              unpair(fma2(pair(s[k], s[k + 1]), mul2(r.x, ks), n.x), s[k], s[k + 1]);
-              unpair(fma2(pair(s[k + 2], s[k + 3]), mul2(r.y, ks), n.y), s[k + 2], s[k + 3]);
-              top = fmaxf(fmaxf(top, fmaxf(s[k], s[k + 1])), fmaxf(s[k + 2], s[k + 3]));
+            for (int k = 0; k < 2; ++k) {
+              float *y = s + 4 * k;
+              unpair(fma2(pair(y[0], y[1]), mul2(r[k].x, ks), n[k].x), y[0], y[1]);
+              unpair(fma2(pair(y[2], y[3]), mul2(r[k].y, ks), n[k].y), y[2], y[3]);
+              top = fmaxf(fmaxf(top, fmaxf(y[0], y[1])), fmaxf(y[2], y[3]));
             }
           }
-          if (moved) break;
-          // scores far above a maximum, or a larger unit of v: the group moves
-          if (__any_sync(kAll, top > kRaise + kLift || v_unit > vref) && lane == 0)
-            sm.vote[group][(c >> kTurns) & 3] = 1;
-          if (!(ok = meet(group))) break;
-          if (!first && !*(volatile int *)&sm.vote[group][(c >> kTurns) & 3]) break;
-          // maxima of the tile: a warp's by column, then the four warps'
-#pragma unroll 1
-          for (int ch = 0; ch * 8 < mine; ++ch) {
-            float y[8];
-            __syncwarp();
-            tmem_load8(s_at + ch * 8, y);
-            tmem_wait8(y);
+          if (pass == 2) break;
+          if (pass == 0) {
+            // scores far above a maximum, or a larger unit of v: the group moves
+            if (__any_sync(kAll, top > kRaise + kLift || v_unit > vref) && lane == 0)
+              sm.vote[group][c & 3] = 1;
+            if (!(ok = meet(group))) break;
+            if (!*(volatile int *)&sm.vote[group][c & 3]) break;
+            if (tok < mine && unseen) nms[tok] = 0.0f;
+            if (!(ok = meet(group))) break;
+            pass = 1;
+            continue;
+          }
+          if (kHold) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              float z = y[k] * (k_unit * factor[ch * 8 + k]);
-              if (!(z == z)) z = INFINITY;  // its row becomes NaN
-              const int best = __reduce_max_sync(kAll, ordered(z));
-              if (lane == 0) sm.red[group][quarter][ch * 8 + k] = unordered(best);
+            for (int ch = 0; ch < kCh; ++ch) {
+              if (ch * 8 >= mine) continue;
+              const float best = over_lanes<true>(x + ch * 8);
+              if ((lane & 3) == 0) sm.red[group][quarter][ch * 8 + (lane >> 2)] = best;
             }
           }
           const int vmax = __reduce_max_sync(kAll, __float_as_int(v_unit));  // units are >= 0
@@ -1191,14 +1249,17 @@ struct Tile {
                                      fmaxf(sm.red[group][2][tok], sm.red[group][3][tok]));
             const float nm = nms[tok];
             float f = 1.0f;
-            if (best > -INFINITY && (nm == kUnseen || kLift - best < nm)) {
-              f = nm == kUnseen ? 0.0f : ex2_approx(kLift - best - nm);
-              nms[tok] = kLift - best;
+            if (best > -INFINITY && (unseen || best > kLift)) {
+              nms[tok] = kLift - (best - nm);
+              f = unseen ? 0.0f : ex2_approx(kLift - best);
+              unseen = false;
+            } else if (unseen) {
+              nms[tok] = kUnseen;
             }
             sm.fac[group][0][tok] = f;
             sm.fac[group][1][tok] = f * v_fac;
           }
-          if (!first && !(ok = wait(&sm.pv_done[last & 1], (last >> 1) & 1))) break;
+          if (!first && !(ok = wait(&sm.pv_done[(c - 1) % kBuf], full_par(c - 1, kBuf)))) break;
           fence_after();
           if (!(ok = meet(group))) break;
           if (!first) {
@@ -1218,34 +1279,38 @@ struct Tile {
                 l[i] = mul2(l[i], *reinterpret_cast<const f2 *>(&sm.fac[group][0][2 * i]));
           }
           if (!kHold) break;
-          moved = true;  // once more, under the new maxima
+          pass = 2;
         }
         if (!ok) break;
-        last = c;
         if (kHold) {  // the scores are in registers: the next ones may come
           fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.s_empty[c & 1]);
         }
-        if (leader) sm.vote[group][((c >> kTurns) + 2) & 3] = 0;
-        // P^T of two tiles ago has been read
-        if (!(ok = wait(&sm.pv_done[c & 1], ((c >> 1) & 1) ^ 1))) break;
+        if (leader) sm.vote[group][(c + 2) & 3] = 0;
+        // P^T of the tile before in this buffer has been read
+        if (!(ok = wait(&sm.pv_done[c % kBuf], empty_par(c, kBuf)))) break;
         const float ratio = vref > 0.0f ? __fdividef(v_unit, vref) : 0.0f;
         const f2 r2 = pair(ratio, ratio);
-        uint8_t *pt = sm.pt[c & 1][0] + tok * kRow;
+        uint8_t *pt = sm.pt[c % kBuf][0] + tok * kRow;
 #pragma unroll
         for (int ch = 0; ch < kCh; ++ch) {
           if (ch * 8 >= mine) continue;
           float *s = x + (kHold ? ch * 8 : 0);
           if (!kHold) {
             tmem_load8(s_at + ch * 8, s);
+            ulonglong2 r[2], n[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              r[k] = *reinterpret_cast<const ulonglong2 *>(factor + ch * 8 + 4 * k);
+              n[k] = *reinterpret_cast<const ulonglong2 *>(nms + ch * 8 + 4 * k);
+            }
             tmem_wait8(s);
 #pragma unroll
-            for (int k = 0; k < 8; k += 4) {
-              const ulonglong2 r = *reinterpret_cast<const ulonglong2 *>(factor + ch * 8 + k);
-              const ulonglong2 n = *reinterpret_cast<const ulonglong2 *>(nms + ch * 8 + k);
-              unpair(fma2(pair(s[k], s[k + 1]), mul2(r.x, ks), n.x), s[k], s[k + 1]);
-              unpair(fma2(pair(s[k + 2], s[k + 3]), mul2(r.y, ks), n.y), s[k + 2], s[k + 3]);
+            for (int k = 0; k < 2; ++k) {
+              float *y = s + 4 * k;
+              unpair(fma2(pair(y[0], y[1]), mul2(r[k].x, ks), n[k].x), y[0], y[1]);
+              unpair(fma2(pair(y[2], y[3]), mul2(r[k].y, ks), n[k].y), y[2], y[3]);
             }
           }
           uint32_t out[4];
@@ -1267,7 +1332,7 @@ struct Tile {
         __syncwarp();
         if (lane == 0) {
           if (!kHold) mbar_arrive(&sm.s_empty[c & 1]);
-          mbar_arrive(&sm.p_full[c & 1]);
+          mbar_arrive(&sm.p_full[c % kBuf]);
         }
       }
       if (!ok) break;
@@ -1279,110 +1344,73 @@ struct Tile {
         float v[8];
 #pragma unroll
         for (int k = 0; k < 4; ++k) unpair(l[ch * 4 + k], v[2 * k], v[2 * k + 1]);
-        const float sum = sum8(v);
+        const float sum = over_lanes<false>(v);
         if ((lane & 3) == 0) sm.red[group][quarter][ch * 8 + (lane >> 2)] = sum;
       }
-      if (leader) sm.vlast[group] = vref;
-      if (last != ~0u && !(ok = wait(&sm.pv_done[last & 1], (last >> 1) & 1))) break;
-      if (!(ok = meet_both())) break;
-      // both groups are past the segment before; nobody is seven ahead
+      if (!(ok = wait(&sm.pv_done[(c - 1) % kBuf], full_par(c - 1, kBuf)))) break;
+      if (!(ok = meet_all())) break;
+      // all are past the segment before; nobody is seven ahead
       if (leader && group == 0) sm.bad[(index + 7) & 7] = sm.dirty[(index + 7) & 7] = 0;
       const int bad = w.r.bad | *(volatile int *)&sm.bad[index & 7];
       const bool dirty = *(volatile int *)&sm.dirty[index & 7] != 0, whole = w.whole;
       float *part = p.part + (size_t)(2 * blockIdx.x + (t0 == 0)) * partial_floats(RN, kv.D);
-      // results: each group writes half of the columns.  A thread for each row
-      // first: its statistics, and its factors of the accumulators
-      const int out_n = kTurns ? columns / 2 : mine, out_0 = group * out_n;
-      // a column's factors and place take the room of its sums, which only its own
-      // thread reads
-      float *const out_fac = kTurns ? &sm.red[0][0][out_0] : &sm.red[group][0][0];
-      if (tok < out_n) {
-        const int col = out_0 + tok, row = w.rt * RN + col, n = node_of(row);
-        float nm, sum, f[2];
-        if (kTurns) {
-          const float na = sm.nm[0][col], nb = sm.nm[1][col];
-          nm = fminf(na, nb);
-          // NaN sums stay, whatever the factors; an unseen side counts nothing
-          f[0] = na == kUnseen ? 0.0f : ex2_approx(nm - na);
-          f[1] = nb == kUnseen ? 0.0f : ex2_approx(nm - nb);
-          if (na == nm) f[0] = 1.0f;
-          if (nb == nm) f[1] = 1.0f;
-          float part_sum[2];
-#pragma unroll
-          for (int g = 0; g < 2; ++g)
-            part_sum[g] = (sm.red[g][0][col] + sm.red[g][1][col]) +
-                          (sm.red[g][2][col] + sm.red[g][3][col]);
-          sum = part_sum[0] * f[0] + part_sum[1] * f[1];
-          // an accumulator without a tile holds nothing
-          f[0] = part_sum[0] == 0.0f ? 0.0f : f[0] * sm.vlast[0];
-          f[1] = part_sum[1] == 0.0f ? 0.0f : f[1] * sm.vlast[1];
-        } else {
-          nm = nms[tok];
-          sum = (sm.red[group][0][tok] + sm.red[group][1][tok]) +
-                (sm.red[group][2][tok] + sm.red[group][3][tok]);
-          f[0] = vref;
-          f[1] = 0.0f;
-        }
-        const bool in = row < p.N * p.G && (!kTurns || col < mine);
-        const bool empty = bad || n >= w.r.nodes || (nm == kUnseen && sum == 0.0f);
+      // results; a thread for each row first: its statistics, the factor of its
+      // outputs and their place (in the room of its sums, which only it reads)
+      float *const out_fac = sm.red[group][0];
+      if (tok < mine) {
+        const int col = c0 + tok, row = w.rt * RN + col, n = node_of(row);
+        const float nm = nms[tok];
+        const float sum = (sm.red[group][0][tok] + sm.red[group][1][tok]) +
+                          (sm.red[group][2][tok] + sm.red[group][3][tok]);
+        const bool in = row < p.N * p.G;
+        const bool empty = bad || n >= w.r.nodes || sum == 0.0f;
         const int at = (w.b * p.N + n) * p.Hq + w.h * p.G + row - n * p.G;
-        const float inv = empty ? 0.0f : whole ? __fdividef(1.0f, sum) : 1.0f;
-        out_fac[tok] = empty ? 0.0f : f[0] * inv;
-        out_fac[kCols + tok] = empty ? 0.0f : f[1] * inv;
-        out_fac[2 * kCols + tok] = __int_as_float(in ? at : -1);
+        out_fac[tok] = empty ? 0.0f : whole ? __fdividef(vref, sum) : vref;
+        out_fac[kCols + tok] = __int_as_float(in ? at : -1);
         if (in && whole && p.lse)
           p.lse[at] = empty ? -INFINITY : (log2f(sum) - nm) * 0.6931471805599453f;
         if (in && !whole) {
           part[(size_t)col * (kv.D + 2)] = empty ? -INFINITY : -nm;
           part[(size_t)col * (kv.D + 2) + 1] = bad ? -(float)bad : empty ? 0.0f : sum;
         }
+        nms[tok] = 0.0f;  // for the next segment
       }
       if (!(ok = meet(group))) break;
-      const uint32_t y_at = lanes + 2 * RN + out_0;
       if (dirty)  // what the products left out because it is not finite
 #pragma unroll 1
-        for (int i = 0; i < out_n; ++i) {
-          const float f = out_fac[i], f2nd = kTurns ? out_fac[kCols + i] : 0.0f;
+        for (int i = 0; i < mine; ++i) {
           float extra = 0.0f;
-          if (__float_as_int(out_fac[2 * kCols + i]) >= 0 && tok < kv.D && (f != 0.0f || f2nd != 0.0f))
-            extra = stray(p, box, w.b, w.h, t0, t1, sm.node[ring][out_0 + i] + node_of(w.rt * RN),
-                          sm.pos[ring][out_0 + i], tok);
+          if (__float_as_int(out_fac[kCols + i]) >= 0 && tok < kv.D && out_fac[i] != 0.0f)
+            extra = stray(p, box, w.b, w.h, t0, t1, sm.node[ring][c0 + i] + node_of(w.rt * RN),
+                          sm.pos[ring][c0 + i], tok);
           __syncwarp();
-          // to an accumulator that counts
-          const uint32_t at = f != 0.0f ? y_at + i : y_at + RN + i;
-          if (f == 0.0f && f2nd == 0.0f) continue;
-          tmem_store1(at, tmem_load1(at) + extra);
+          tmem_store1(o_at + i, tmem_load1(o_at + i) + extra);
           tmem_stored();
         }
 #pragma unroll 1
-      for (int i = 0; i < out_n; i += 4) {
-        float o[4], o2[4];
+      for (int i = 0; i < mine; i += 8) {
+        float o[8];
         __syncwarp();
-        tmem_load4(y_at + i, o);
-        if (kTurns) tmem_load4(y_at + RN + i, o2);
-        tmem_wait4(o);
-        if (kTurns) tmem_wait4(o2);
+        tmem_load8(o_at + i, o);
+        tmem_wait8(o);
+        if (tok < kv.D) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int at = __float_as_int(out_fac[2 * kCols + i + k]);
-          const float f = out_fac[i + k];
-          float y = f != 0.0f ? o[k] * f : 0.0f;
-          if (kTurns) {
-            const float f2nd = out_fac[kCols + i + k];
-            y += f2nd != 0.0f ? o2[k] * f2nd : 0.0f;
-          }
-          if (at >= 0 && tok < kv.D) {
-            if (whole)
-              reinterpret_cast<unsigned short *>(p.out)[(long long)at * kv.D + tok] =
-                  (unsigned short)pack_bf16x2(y, 0.0f);
-            else
-              part[(size_t)(out_0 + i + k) * (kv.D + 2) + 2 + tok] = y;
+          for (int k = 0; k < 8; ++k) {
+            const int at = __float_as_int(out_fac[kCols + i + k]);
+            const float f = out_fac[i + k], y = f != 0.0f ? o[k] * f : 0.0f;
+            if (at >= 0) {
+              if (whole)
+                reinterpret_cast<unsigned short *>(p.out)[(long long)at * kv.D + tok] =
+                    (unsigned short)pack_bf16x2(y, 0.0f);
+              else
+                part[(size_t)(c0 + i + k) * (kv.D + 2) + 2 + tok] = y;
+            }
           }
         }
       }
-      if (whole && leader && group == 0 && w.h == 0 && w.rt == 0) p.row_status[w.b] = bad;
+      if (leader && group == 0 && whole && w.h == 0 && w.rt == 0) p.row_status[w.b] = bad;
       if (leader) sm.done[group] = index + 1;
-      if (!(ok = meet_both())) break;
+      if (!(ok = meet_all())) break;
     }
   }
 
@@ -1392,10 +1420,12 @@ struct Tile {
     const specdec_kv_cache &kv = p.cache;
     Walk walk(p, box, plan);
     Segment w;
+#pragma unroll 1
     for (int index = 0; walk.next(p, box, w); ++index) {
       if (index < finished) continue;
       float *part = p.part + (size_t)(2 * blockIdx.x + (w.t0 == 0)) * partial_floats(RN, kv.D);
-      for (int col = threadIdx.x; col < columns; col += kThreads) {
+#pragma unroll 1
+      for (int col = threadIdx.x; col < columns; col += C::kThreads) {
         const int row = w.rt * RN + col, n = row / p.G;
         if (row >= p.N * p.G) continue;
         const long long at = ((long long)w.b * p.N + n) * p.Hq + w.h * p.G + row - n * p.G;
@@ -1414,54 +1444,55 @@ struct Tile {
 };
 
 template <int RN, bool kPlain>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<RN>::kThreads, Cfg<RN>::kCtas)
     attend_tile_kernel(const __grid_constant__ AttendParams p,
                        const __grid_constant__ CUtensorMap k_map,
                        const __grid_constant__ CUtensorMap v_map, int box) {
   extern __shared__ __align__(1024) uint8_t raw[];
   using S = Smem<RN>;
+  using C = Cfg<RN>;
   // an offset, not a rounded pointer: the compiler has to know that it is shared memory
   S &sm = *reinterpret_cast<S *>(raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u));
   const int tid = threadIdx.x, warp = tid >> 5;
-  if (tid == 0) {
-    for (int i = 0; i < Cfg<RN>::kK; ++i) {
-      mbar_init(&sm.k_full[i], 1);
-      mbar_init(&sm.k_empty[i], 1);
+  if (tid < 8) {
+    sm.bad[tid] = sm.dirty[tid] = 0;
+    mbar_init(&sm.seg_full[tid], 1);
+    mbar_init(&sm.box_full[tid], 4);
+    if (tid < C::kK) {
+      mbar_init(&sm.k_full[tid], 1);
+      mbar_init(&sm.k_empty[tid], 1);
     }
-    for (int i = 0; i < Cfg<RN>::kV; ++i) {
-      mbar_init(&sm.v_full[i], 1);
-      mbar_init(&sm.v_empty[i], 4);
+    if (tid < 2) {
+      mbar_init(&sm.s_full[tid], 1);
+      mbar_init(&sm.s_empty[tid], 4 * C::kGroups);
     }
-    for (int i = 0; i < Cfg<RN>::kQ; ++i) {
-      mbar_init(&sm.q_full[i], 4);
-      mbar_init(&sm.q_empty[i], 1);
+    if (tid < C::kBuf) {
+      mbar_init(&sm.p_full[tid], 4 * C::kGroups);
+      mbar_init(&sm.vh_full[tid], C::kWorkers);
+      mbar_init(&sm.pv_done[tid], 1);
     }
-    mbar_init(&sm.fin, 1);
-    mbar_init(&sm.both, 8);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.s_empty[i], Cfg<RN>::kTurns ? 4 : 8);
-      mbar_init(&sm.p_full[i], Cfg<RN>::kTurns ? 4 : 8);
-      mbar_init(&sm.vh_full[i], 4);
-      mbar_init(&sm.pv_done[i], 1);
-      mbar_init(&sm.group[i], 4);
-      sm.done[i] = 0;
-      for (int k = 0; k < 4; ++k) sm.vote[i][k] = 0;
+    if (tid < C::kGroups) {
+      mbar_init(&sm.group[tid], 4);
+      sm.done[tid] = 0;
     }
-    for (int i = 0; i < 8; ++i) {
-      sm.bad[i] = sm.dirty[i] = 0;
-      mbar_init(&sm.seg_full[i], 1);
-      mbar_init(&sm.box_full[i], 4);
+    if (tid < 4 * C::kGroups) sm.vote[tid >> 2][tid & 3] = 0;
+    if (tid == 0) {
+      mbar_init(&sm.v_full, 1);
+      mbar_init(&sm.v_empty, C::kWorkers);
+      mbar_init(&sm.q_full, C::kWorkers);
+      mbar_init(&sm.q_empty, 1);
+      mbar_init(&sm.both, 4 * C::kGroups);
+      mbar_init(&sm.fin, 1);
+      sm.give_up = 0;
     }
-    sm.give_up = 0;
     fence_mbar_init();
     fence_async_smem();
   }
-  if (tid < Cfg<RN>::kCols) sm.ones[tid] = 1.0f;
+  if (tid < C::kCols) sm.ones[tid] = 1.0f;
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_addr(&sm.tmem)),
-                 "r"(Cfg<RN>::kTmem)
+                 "r"(C::kTmem)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
@@ -1476,7 +1507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tile.copies(plan);
   else if (warp == 1)
     tile.products();
-  else if (warp < 6)
+  else if (warp < C::kFirst)
     tile.operands();
   else
     tile.softmax();
@@ -1485,83 +1516,94 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_after();
   if (sm.give_up) {
     if (warp == 0) tile.drain();
-    tile.give_up_results(p, box, plan, min(sm.done[0], sm.done[1]), tile.columns);
+    tile.give_up_results(p, box, plan, min(sm.done[0], sm.done[C::kGroups - 1]), tile.columns);
     __syncthreads();
   }
   if (warp == 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(sm.tmem),
-                 "r"(Cfg<RN>::kTmem));
+                 "r"(C::kTmem));
 }
 
-// Joins the units that the cuts between CTAs divide.  Block (i, part): the unit
-// that CTA i - 1 began and CTA i goes on with, an eighth of its rows.
-constexpr int kJoinParts = 8;
-__global__ void __launch_bounds__(256)
-    attend_tile_join_kernel(const AttendParams p, int box, int ctas, int RN) {
-  __shared__ long long scan[33];
-  __shared__ Plan shared;
+// Joins the units that the cuts between CTAs divide.  Block (i, y): the unit that
+// CTA i was in the middle of at its start, if it is the first that was; the y-th
+// part of its rows.
+constexpr int kJoinRows = 8;  // a warp each
+__global__ void __launch_bounds__(32 * kJoinRows)
+    attend_tile_join_kernel(const __grid_constant__ AttendParams p, int ctas, int RN) {
   pdl_wait();
   pdl_launch_dependents();
-  const int i = blockIdx.x + 1, D = p.cache.D;
-  const Plan plan = make_plan(p, box, i, ctas, scan, &shared);
-  if (plan.count == 0) return;
-  Walk walk(p, box, plan);
-  Segment w;
-  walk.next(p, box, w);
-  if (w.t0 == 0) return;  // a unit begins here
-  const long long u0 = plan.first - w.t0;
-  const int begun = part_of(u0, plan.total, ctas);
-  if (part_of(plan.first - 1, plan.total, ctas) != begun) return;  // another CTA was here before
-  // the beginning is in slot 1 of its CTA, what follows in slot 0 of theirs; with
-  // fewer tiles than CTAs some have none, and each other has one
-  const long long u1 = u0 + w.r.tiles;
-  const bool few = plan.total < ctas;
-  const int parts = few ? (int)(u1 - plan.first) : part_of(u1 - 1, plan.total, ctas) - i + 1;
+  const int i = blockIdx.x, D = p.cache.D, lane = threadIdx.x & 31;
   const size_t size = partial_floats(RN, D);
-  const float *head = p.part + (size_t)(2 * begun + 1) * size;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int any_bad = 0;
-  for (int col = blockIdx.y * 8 + warp; col < RN; col += 8 * kJoinParts) {
-    const int row = w.rt * RN + col, n = row / p.G;
-    if (row >= p.N * p.G) break;
-    auto record = [&](int s) {
-      const int at = few && s > 0 ? part_of(plan.first + s - 1, plan.total, ctas) : i + s - 1;
-      return (s == 0 ? head : p.part + (size_t)(2 * at) * size) + (size_t)col * (D + 2);
-    };
-    float all = -INFINITY, sum = 0.0f;
-    int bad = 0;
-    for (int s = lane; s <= parts; s += 32) {
-      const float *rec = record(s);
-      all = fmaxf(all, rec[0]);
-      if (rec[1] < 0.0f) bad |= (int)-rec[1];
-    }
-    bad = __reduce_or_sync(kAll, bad);
-    any_bad |= bad;
+  const Note *notes = notes_of(p.part, RN, D);
+  const Note me = notes[i];
+  if (me.first == 0) return;  // begins with a unit, or has no tile
+  // the CTAs before: the one that began the unit is the last that has tiles
+  int begun = -1;
+#pragma unroll 1
+  for (int at = i - 1; at >= 0 && begun < 0; at -= 32) {
+    const unsigned full = __ballot_sync(kAll, at - lane >= 0 && notes[at - lane].tiles > 0);
+    if (full) begun = at - (__ffs(full) - 1);
+  }
+  if (begun < 0 || notes[begun].open != me.first) return;  // it was in the middle, too
+  // parts: that one's second slot, then first slots until the unit's end
+  const int r = blockIdx.y * kJoinRows + (threadIdx.x >> 5), row = me.rt * RN + r, n = row / p.G;
+  int left = me.unit - me.first, last = -1;
+#pragma unroll 1
+  for (int at = i; at < ctas && last < 0; at += 32) {
+    int upto = 0;
+    if (at + lane < ctas && notes[at + lane].tiles > 0) upto = notes[at + lane].head;
 #pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) all = fmaxf(all, __shfl_xor_sync(kAll, all, d));
-    const bool empty = bad || all == -INFINITY;
-    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int s = 0; !empty && s <= parts; ++s) {
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(kAll, upto, d);
+      if (lane >= d) upto += o;
+    }
+    const unsigned ends = __ballot_sync(kAll, upto >= left);
+    if (ends) last = at + __ffs(ends) - 1;
+    left -= __shfl_sync(kAll, upto, 31);
+  }
+  const int parts = last - i + 2;
+  if (r >= RN || row >= p.N * p.G) return;
+  const float *head = p.part + (size_t)(2 * begun + 1) * size + (size_t)r * (D + 2);
+  auto record = [&](int s) {
+    return s == 0 ? head : p.part + (size_t)(2 * (i + s - 1)) * size + (size_t)r * (D + 2);
+  };
+  auto has = [&](int s) { return s == 0 || notes[i + s - 1].tiles > 0; };
+  float all = -INFINITY, sum = 0.0f;
+  int bad = 0;
+#pragma unroll 1
+  for (int s = lane; s < parts; s += 32) {
+    if (!has(s)) continue;
+    const float *rec = record(s);
+    all = fmaxf(all, rec[0]);
+    if (rec[1] < 0.0f) bad |= (int)-rec[1];
+  }
+  bad = __reduce_or_sync(kAll, bad);
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) all = fmaxf(all, __shfl_xor_sync(kAll, all, d));
+  const bool empty = bad || all == -INFINITY;
+  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (!empty) {
+#pragma unroll 4
+    for (int s = 0; s < parts; ++s) {
+      if (!has(s)) continue;
       const float *rec = record(s);
-      const float m = rec[0];
-      if (m == -INFINITY) continue;
-      const float f = ex2_approx(m - all);
+      const float m = rec[0], f = m == -INFINITY ? 0.0f : ex2_approx(m - all);
       sum += rec[1] * f;
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         if (lane + 32 * k < D) acc[k] += f * rec[2 + lane + 32 * k];
     }
-    const float inv = empty ? 0.0f : 1.0f / sum;
-    const long long at = ((long long)w.b * p.N + n) * p.Hq + w.h * p.G + row - n * p.G;
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (lane + 32 * k < D)
-        reinterpret_cast<unsigned short *>(p.out)[at * D + lane + 32 * k] =
-            (unsigned short)pack_bf16x2(empty ? 0.0f : acc[k] * inv, 0.0f);
-    if (p.lse && lane == 0)
-      p.lse[at] = empty ? -INFINITY : (all + log2f(sum)) * 0.6931471805599453f;
   }
-  if (w.h == 0 && w.rt == 0 && blockIdx.y == 0 && threadIdx.x == 0) p.row_status[w.b] = any_bad;
+  const float inv = empty ? 0.0f : 1.0f / sum;
+  const long long at = ((long long)me.b * p.N + n) * p.Hq + me.h * p.G + row - n * p.G;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (lane + 32 * k < D)
+      reinterpret_cast<unsigned short *>(p.out)[at * D + lane + 32 * k] =
+          (unsigned short)pack_bf16x2(empty ? 0.0f : acc[k] * inv, 0.0f);
+  if (p.lse && lane == 0)
+    p.lse[at] = empty ? -INFINITY : (all + log2f(sum)) * 0.6931471805599453f;
+  if (me.h == 0 && row == 0 && lane == 0) p.row_status[me.b] = bad;
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
@@ -1576,8 +1618,7 @@ EncodeFn encode_fn() {
   void *sym = nullptr;
   cudaDriverEntryPointQueryResult found;
   if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &sym, 12000, cudaEnableDefault,
-                                       &found) !=
-          cudaSuccess ||
+                                       &found) != cudaSuccess ||
       found != cudaDriverEntryPointSuccess)
     return nullptr;
   f = reinterpret_cast<EncodeFn>(sym);
@@ -1611,9 +1652,10 @@ cudaError_t launch_rn(AttendParams p, cudaStream_t stream) {
   static DeviceOnce once;
   const int smem = (int)sizeof(Smem<RN>) + 1024;
   static_assert(offsetof(Smem<RN>, rf) % 16 == 0 && offsetof(Smem<RN>, nm) % 16 == 0 &&
-                    offsetof(Smem<RN>, ones) % 16 == 0 && offsetof(Smem<RN>, fac) % 16 == 0,
-                "read in 16-byte vectors");
-  static_assert(sizeof(Smem<RN>) + 1024 <= 232448, "shared memory of a CTA");
+                    offsetof(Smem<RN>, ones) % 16 == 0 && offsetof(Smem<RN>, fac) % 16 == 0 &&
+                    offsetof(Smem<RN>, q) % 1024 == 0,
+                "read in 16-byte vectors, and by swizzled copies and products");
+  static_assert((sizeof(Smem<RN>) + 2048) * Cfg<RN>::kCtas <= 233472, "shared memory of an SM");
   cudaError_t err = smem_opt_in_once(once, attend_tile_kernel<RN, kPlain>, smem);
   if (err != cudaSuccess) return err;
   CUtensorMap k_map, v_map;
@@ -1622,24 +1664,29 @@ cudaError_t launch_rn(AttendParams p, cudaStream_t stream) {
     return cudaErrorInvalidValue;
   p.row_tiles = (p.N * p.G + RN - 1) / RN;
   const int sms = device_sm_count();
-  const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
-  err = launch_pdl(attend_tile_kernel<RN, kPlain>, dim3((unsigned)ctas), dim3(kThreads),
+  const int ctas = (sms < kMaxSms ? sms : kMaxSms) * Cfg<RN>::kCtas;
+  err = launch_pdl(attend_tile_kernel<RN, kPlain>, dim3((unsigned)ctas), dim3(Cfg<RN>::kThreads),
                    (size_t)smem, stream, p, k_map, v_map, box);
   if (err != cudaSuccess) return err;
-  return launch_pdl(attend_tile_join_kernel, dim3((unsigned)(ctas - 1), kJoinParts), dim3(256), 0,
-                    stream, p, box, ctas, RN);
+  const int rows = p.N * p.G < RN ? p.N * p.G : RN;
+  return launch_pdl(attend_tile_join_kernel,
+                    dim3((unsigned)ctas, (unsigned)((rows + kJoinRows - 1) / kJoinRows)),
+                    dim3(32 * kJoinRows), 0, stream, p, ctas, RN);
 }
 
 }  // namespace
 
 size_t attend_tile_workspace_bytes(int N, int G, int D) {
-  return (size_t)2 * kMaxCtas * partial_floats(rows_of(N, G), D) * sizeof(float);
+  const int RN = rows_of(N, G);
+  return 4 * kMaxSms * partial_floats(RN, D) * sizeof(float) + 2 * kMaxSms * sizeof(Note);
 }
 
 bool attend_tile_applies(const AttendParams &p) {
   const specdec_kv_cache &kv = p.cache;
+  const long long units = (long long)kv.Hkv * ((p.N * p.G + 127) / 128 + 1);
   return p.dtype == SPECDEC_BF16 && kv.D <= kRow &&
-         (long long)kv.n_blocks * kv.Hkv * kv.block < (1ll << 31) - kTok;
+         (long long)kv.n_blocks * kv.Hkv * kv.block < (1ll << 31) - kTok &&
+         ((long long)kv.max_blocks * kv.block / kTok + p.N + kExtra) * units < (1ll << 31);
 }
 
 cudaError_t launch_attend_tile(const AttendParams &p, cudaStream_t stream) {
