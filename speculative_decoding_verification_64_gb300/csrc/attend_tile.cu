@@ -63,7 +63,8 @@ struct Cfg {
   static constexpr int kThreads = 32 * (kFirst + 4 * kGroups);
   static constexpr int kCols = RN / kGroups;           // most columns of a softmax thread
   static constexpr bool kHold = RN == 32;              // its scores stay in registers
-  static constexpr int kK = RN == 64 ? 1 : 2;          // stages of K codes
+  static constexpr int kK = RN <= 64 ? 1 : 2;          // stages of K codes (free once scores are made)
+  static constexpr int kV = RN == 32 ? 2 : 1;          // stages of V codes (free once widened)
   static constexpr int kBuf = RN <= 64 ? 1 : 2;        // buffers of widened V, and of P^T
   static constexpr int kTmem = RN == 32 ? 128 : RN == 64 ? 256 : 512;
   static constexpr int kSpans = RN <= 64 ? 1 : 2;      // 64-row groups of P^T
@@ -96,7 +97,7 @@ template <int RN>
 struct Smem {
   using C = Cfg<RN>;
   uint8_t k[C::kK][kTileBytes];           // K codes [token][128 B], 128-byte swizzle
-  uint8_t v[kTileBytes];                  // V codes, the same (drafted tiles: the low terms of k)
+  uint8_t v[C::kV][kTileBytes];           // V codes, the same (drafted tiles: the low terms of k)
   uint8_t vh[C::kBuf][2][kTileBytes];     // V in fp16, [64 elements][token][128 B]
   uint8_t pt[C::kBuf][C::kSpans][kTileBytes];  // P^T in fp16, [64 rows][token][128 B]
   uint8_t q[2][RN * kRow];                // q: high and low terms [row][128 B]
@@ -118,7 +119,7 @@ struct Smem {
   Segment seg[8];
   int bad[8], dirty[8];
   uint64_t seg_full[8], box_full[8];
-  uint64_t k_full[C::kK], k_empty[C::kK], v_full, v_empty, q_full, q_empty;
+  uint64_t k_full[C::kK], k_empty[C::kK], v_full[C::kV], v_empty[C::kV], q_full, q_empty;
   uint64_t s_full[2], s_empty[2], p_full[C::kBuf], vh_full[C::kBuf], pv_done[C::kBuf];
   uint64_t group[C::kGroups], both, fin;
   uint32_t tmem;
@@ -210,19 +211,6 @@ __device__ __forceinline__ void tmem_store8(uint32_t at, const float *x) {
                "f"(x[7])
                : "memory");
 }
-__device__ __forceinline__ void tmem_load4(uint32_t at, float *x) {
-  uint32_t r[4];
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(at)
-               : "memory");
-#pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ void tmem_wait4(float *x) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+f"(x[0]), "+f"(x[1]), "+f"(x[2]), "+f"(x[3])::"memory");
-}
 __device__ __forceinline__ float tmem_load1(uint32_t at) {
   uint32_t r;
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;"
@@ -261,15 +249,6 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
   f2 r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
-}
-
-// float order as int order (NaN above everything or below)
-__device__ __forceinline__ int ordered(float x) {
-  const int i = __float_as_int(x);
-  return i >= 0 ? i : i ^ 0x7FFFFFFF;
-}
-__device__ __forceinline__ float unordered(int i) {
-  return __int_as_float(i >= 0 ? i : i ^ 0x7FFFFFFF);
 }
 
 // 2^k, k in [-126, 127].
@@ -333,7 +312,7 @@ __device__ __forceinline__ Plan make_plan(const AttendParams &p, int box, int i,
   for (int side = 0; side < 2; ++side) {
     const long long cut = divide(total * (i + side), n);
     if (cut >= upto - mine && (cut < upto || (cut == total && upto == total && mine > 0))) {
-      long long at = upto - mine, tiles = 0;
+      long long at = upto - mine;
       int b = t * per, off = 0;
 #pragma unroll 1
       for (;; ++b) {
@@ -346,7 +325,6 @@ __device__ __forceinline__ Plan make_plan(const AttendParams &p, int box, int i,
         }
         at += here;
       }
-      (void)tiles;
       if (side == 0) {
         shared->b = b;
         shared->off = off;
@@ -530,7 +508,7 @@ template <int RN, bool kPlain>
 struct Tile {
   using S = Smem<RN>;
   using C = Cfg<RN>;
-  static constexpr int kK = C::kK, kBuf = C::kBuf;
+  static constexpr int kK = C::kK, kV = C::kV, kBuf = C::kBuf;
   const AttendParams &p;
   S &sm;
   const CUtensorMap *k_map, *v_map;
@@ -617,7 +595,7 @@ struct Tile {
       Piece next = piece_of(w, w.t0);
 #pragma unroll 1
       for (int t = w.t0; t < w.t1; ++t, ++c) {
-        const int ks = c % kK;
+        const int ks = c % kK, vs = c % kV;
         Piece x = next;
         if (t + 1 < w.t1) next = piece_of(w, t + 1);  // the next tile's ids load meanwhile
         const bool cached = t >= w.r.drafted;
@@ -636,18 +614,18 @@ struct Tile {
         if (cached) {
           if (lane == 0) mbar_arrive_expect_tx(&sm.k_full[ks], bytes);
           __syncwarp();
-          if (x.mine) tma_rows(sm.k[ks] + lane * box * kRow, k_map, row, &sm.k_full[ks]);
-        }
-        if (!(ok = wait(&sm.v_empty, empty_par(c, 1)))) break;
-        if (cached) {
-          if (lane == 0) mbar_arrive_expect_tx(&sm.v_full, bytes);
-          __syncwarp();
           if (x.mine) {
-            tma_rows(sm.v + lane * box * kRow, v_map, row, &sm.v_full);
+            tma_rows(sm.k[ks] + lane * box * kRow, k_map, row, &sm.k_full[ks]);
             sm.boxes[c & 7][lane] = unit;
           }
           __syncwarp();
           if (lane < 4) mbar_arrive(&sm.box_full[c & 7]);
+        }
+        if (!(ok = wait(&sm.v_empty[vs], empty_par(c, kV)))) break;
+        if (cached) {
+          if (lane == 0) mbar_arrive_expect_tx(&sm.v_full[vs], bytes);
+          __syncwarp();
+          if (x.mine) tma_rows(sm.v[vs] + lane * box * kRow, v_map, row, &sm.v_full[vs]);
         }
       }
     }
@@ -664,7 +642,8 @@ struct Tile {
   __device__ void drain() {
     for (uint32_t i = copied > kK ? copied - kK : 0; i < copied; ++i)
       mbar_wait_bounded(&sm.k_full[i % kK], full_par(i, kK));
-    if (copied > 0) mbar_wait_bounded(&sm.v_full, full_par(copied - 1, 1));
+    for (uint32_t i = copied > kV ? copied - kV : 0; i < copied; ++i)
+      mbar_wait_bounded(&sm.v_full[i % kV], full_par(i, kV));
   }
 
   // ------------------------------------------------------------ warp 1: products
@@ -683,7 +662,7 @@ struct Tile {
         mma_issue<true>(d, ka + 2 * i, qb + 2 * i, idesc, true);
       }
       if (drafted) {
-        const uint64_t kl = operand(smem_addr(sm.v), 1024, 16);
+        const uint64_t kl = operand(smem_addr(sm.v[c % kV]), 1024, 16);
 #pragma unroll 1
         for (int i = 0; i < steps; ++i) {
           mma_issue<true>(d, kl + 2 * i, qa + 2 * i, idesc, true);
@@ -694,8 +673,8 @@ struct Tile {
       mma_commit(&sm.k_empty[c % kK]);
       if (drafted) {  // the low terms stood in V's place, which an arrival of each worker frees
 #pragma unroll
-        for (int i = 1; i < C::kWorkers; ++i) mbar_arrive(&sm.v_empty);
-        mma_commit(&sm.v_empty);
+        for (int i = 1; i < C::kWorkers; ++i) mbar_arrive(&sm.v_empty[c % kV]);
+        mma_commit(&sm.v_empty[c % kV]);
       }
       if (ends) mma_commit(&sm.q_empty);
     }
@@ -745,7 +724,7 @@ struct Tile {
         if (drafted) {
           if (lane == 0) {  // nobody copies into this tile's slots
             mbar_arrive(&sm.k_full[c % kK]);
-            mbar_arrive(&sm.v_full);
+            mbar_arrive(&sm.v_full[c % kV]);
           }
         } else if (!(ok = wait(&sm.k_full[c % kK], full_par(c, kK)))) {
           break;
@@ -864,43 +843,39 @@ struct Tile {
   __device__ __noinline__ static bool sift(uint8_t *codes, int tid) {
     bool odd = false;
 #pragma unroll 1
-    for (int i = 0; i < 4 * (kTok / (4 * C::kWorkers)); ++i) {  // the thread's own pieces
-      const int tok = (tid >> 3) + (i >> 2) * 4 * C::kWorkers;
-      uint32_t *w = reinterpret_cast<uint32_t *>(codes + tok * kRow +
-                                                 (((tid & 7) ^ (tok & 7)) << 4)) + (i & 3);
-      uint32_t keep = 0;
-      for (int s = 0; s < 32; s += 8)
-        if (((*w >> s) & 0x7Fu) != 0x7Fu) keep |= 0xFFu << s;
-      odd |= keep != kAll;
-      *w &= keep;
+    for (int i = tid >> 4; i < kTok; i += 2 * C::kWorkers) {  // the thread's own pieces
+      uint32_t *w = reinterpret_cast<uint32_t *>(codes + i * kRow +
+                                                 ((((tid & 15) >> 1) ^ (i & 7)) << 4) + (tid & 1) * 8);
+#pragma unroll 1
+      for (int k = 0; k < 2; ++k) {
+        uint32_t keep = 0;
+        for (int s = 0; s < 32; s += 8)
+          if (((w[k] >> s) & 0x7Fu) != 0x7Fu) keep |= 0xFFu << s;
+        odd |= keep != kAll;
+        w[k] &= keep;
+      }
     }
     return odd;
   }
 
-  // V codes of a cached tile to fp16; tokens past the length as zeros.
+  // V codes of a cached tile to fp16; tokens past the length as zeros.  A thread
+  // takes 8 codes at a time, 16 lanes a token: 8 bytes in, 16 out, each half-warp
+  // over all banks.
   __device__ __forceinline__ void widen(const Segment &w, uint32_t index, int t, uint32_t c,
                                         int worker) {
-    constexpr int kStep = 4 * C::kWorkers;  // tokens at once: 8 lanes each
     const int held = w.r.len - (w.r.from + (t - w.r.drafted) * kTok), tid = worker * 32 + lane;
-    uint8_t *src = sm.v;
-    if (partly_hidden(p, w.r, t) && sift(src, tid)) sm.dirty[index & 7] = 1;
-    // a thread's pieces are whole groups of 8 tokens apart: the same place in the
-    // swizzle, or every second of two
-    const int tok0 = tid >> 3, j = tid & 7, side = j >> 2, piece = (j & 3) * 2;
+    if (partly_hidden(p, w.r, t) && sift(sm.v[c % kV], tid)) sm.dirty[index & 7] = 1;
+    const int h = tid & 15;
+    const uint8_t *src = sm.v[c % kV] + (h & 1) * 8;
+    uint8_t *dst = sm.vh[c % kBuf][h >> 3];
 #pragma unroll 4
-    for (int i = 0; i < kTok / kStep; ++i) {
-      const int tok = tok0 + i * kStep, x7 = tok & 7;
-      uint4 x = *reinterpret_cast<const uint4 *>(src + tok * kRow + ((j ^ x7) << 4));
-      if (tok >= held) x = make_uint4(0u, 0u, 0u, 0u);
-      const uint4 lo = make_uint4(e4m3x2_to_half2(x.x & 0xFFFFu), e4m3x2_to_half2(x.x >> 16),
-                                  e4m3x2_to_half2(x.y & 0xFFFFu), e4m3x2_to_half2(x.y >> 16));
-      const uint4 hi = make_uint4(e4m3x2_to_half2(x.z & 0xFFFFu), e4m3x2_to_half2(x.z >> 16),
-                                  e4m3x2_to_half2(x.w & 0xFFFFu), e4m3x2_to_half2(x.w >> 16));
-      // lanes of the two 64-element groups write odd and even pieces in turn:
-      // eight lanes cover eight different 16-byte banks
-      uint8_t *dst = sm.vh[c % kBuf][side] + tok * kRow;
-      *reinterpret_cast<uint4 *>(dst + (((piece + side) ^ x7) << 4)) = side ? hi : lo;
-      *reinterpret_cast<uint4 *>(dst + (((piece + 1 - side) ^ x7) << 4)) = side ? lo : hi;
+    for (int tok = tid >> 4; tok < kTok; tok += 2 * C::kWorkers) {
+      const int x7 = tok & 7;
+      uint2 x = *reinterpret_cast<const uint2 *>(src + tok * kRow + (((h >> 1) ^ x7) << 4));
+      if (tok >= held) x = make_uint2(0u, 0u);
+      *reinterpret_cast<uint4 *>(dst + tok * kRow + (((h & 7) ^ x7) << 4)) =
+          make_uint4(e4m3x2_to_half2(x.x), e4m3x2_to_half2(x.x >> 16), e4m3x2_to_half2(x.y),
+                     e4m3x2_to_half2(x.y >> 16));
     }
   }
 
@@ -924,7 +899,7 @@ struct Tile {
                          : zero;
       bool all;
       const int ek = unit_exponent(row_top(x, all), 7);
-      split(sm.k[c % kK], sm.v, r, e, x, ek);
+      split(sm.k[c % kK], sm.v[c % kV], r, e, x, ek);
       const float k_unit = all ? pow2i(ek) : -1.0f;
       const int ev = unit_exponent(row_top(y, all), 10);
       const float inv = pow2i(-ev);
@@ -996,8 +971,8 @@ struct Tile {
         const bool drafted = t < drafts;
         if (drafted) {
           if (!(ok = wait(&sm.k_empty[c % kK], empty_par(c, kK)))) break;
-          if (!(ok = wait(&sm.v_empty, empty_par(c, 1)))) break;
-        } else if (!(ok = wait(&sm.v_full, full_par(c, 1)))) {
+          if (!(ok = wait(&sm.v_empty[c % kV], empty_par(c, kV)))) break;
+        } else if (!(ok = wait(&sm.v_full[c % kV], full_par(c, kV)))) {
           break;
         }
         if (!(ok = wait(&sm.pv_done[c % kBuf], empty_par(c, kBuf)))) break;
@@ -1008,13 +983,13 @@ struct Tile {
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
-          if (!drafted) mbar_arrive(&sm.v_empty);
+          if (!drafted) mbar_arrive(&sm.v_empty[c % kV]);
           mbar_arrive(&sm.vh_full[c % kBuf]);
         }
         // four arrivals complete box_full
         if (drafted && lane < 4 / C::kWorkers) mbar_arrive(&sm.box_full[c & 7]);
         // as the copying warp: every phase of v_full is waited on
-        if (drafted && !(ok = wait(&sm.v_full, full_par(c, 1)))) break;
+        if (drafted && !(ok = wait(&sm.v_full[c % kV], full_par(c, kV)))) break;
       }
       if (!ok) break;
     }
@@ -1175,6 +1150,8 @@ struct Tile {
         int pass = first ? 1 : 0;
 #pragma unroll 1
         for (;;) {
+          // one body for all passes, not a copy each
+          asm volatile("" : "+r"(pass));
           float top = -INFINITY;
           if (!kHold && pass == 1) {  // the warp's maxima
 #pragma unroll 1
@@ -1355,8 +1332,10 @@ struct Tile {
       const bool dirty = *(volatile int *)&sm.dirty[index & 7] != 0, whole = w.whole;
       float *part = p.part + (size_t)(2 * blockIdx.x + (t0 == 0)) * partial_floats(RN, kv.D);
       // results; a thread for each row first: its statistics, the factor of its
-      // outputs and their place (in the room of its sums, which only it reads)
+      // outputs (in the room of a sum that only it reads) and their address (in that
+      // of the factors)
       float *const out_fac = sm.red[group][0];
+      unsigned long long *const out_at = reinterpret_cast<unsigned long long *>(sm.fac[group]);
       if (tok < mine) {
         const int col = c0 + tok, row = w.rt * RN + col, n = node_of(row);
         const float nm = nms[tok];
@@ -1365,13 +1344,16 @@ struct Tile {
         const bool in = row < p.N * p.G;
         const bool empty = bad || n >= w.r.nodes || sum == 0.0f;
         const int at = (w.b * p.N + n) * p.Hq + w.h * p.G + row - n * p.G;
+        float *rec = part + (size_t)col * (kv.D + 2);
         out_fac[tok] = empty ? 0.0f : whole ? __fdividef(vref, sum) : vref;
-        out_fac[kCols + tok] = __int_as_float(in ? at : -1);
+        out_at[tok] = !in     ? 0ull
+                      : whole ? reinterpret_cast<unsigned long long>(p.out) + (size_t)at * kv.D * 2
+                              : reinterpret_cast<unsigned long long>(rec + 2);
         if (in && whole && p.lse)
           p.lse[at] = empty ? -INFINITY : (log2f(sum) - nm) * 0.6931471805599453f;
         if (in && !whole) {
-          part[(size_t)col * (kv.D + 2)] = empty ? -INFINITY : -nm;
-          part[(size_t)col * (kv.D + 2) + 1] = bad ? -(float)bad : empty ? 0.0f : sum;
+          rec[0] = empty ? -INFINITY : -nm;
+          rec[1] = bad ? -(float)bad : empty ? 0.0f : sum;
         }
         nms[tok] = 0.0f;  // for the next segment
       }
@@ -1380,7 +1362,7 @@ struct Tile {
 #pragma unroll 1
         for (int i = 0; i < mine; ++i) {
           float extra = 0.0f;
-          if (__float_as_int(out_fac[kCols + i]) >= 0 && tok < kv.D && out_fac[i] != 0.0f)
+          if (out_at[i] && tok < kv.D && out_fac[i] != 0.0f)
             extra = stray(p, box, w.b, w.h, t0, t1, sm.node[ring][c0 + i] + node_of(w.rt * RN),
                           sm.pos[ring][c0 + i], tok);
           __syncwarp();
@@ -1396,15 +1378,13 @@ struct Tile {
         if (tok < kv.D) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const int at = __float_as_int(out_fac[kCols + i + k]);
+            const unsigned long long at = out_at[i + k];
             const float f = out_fac[i + k], y = f != 0.0f ? o[k] * f : 0.0f;
-            if (at >= 0) {
-              if (whole)
-                reinterpret_cast<unsigned short *>(p.out)[(long long)at * kv.D + tok] =
-                    (unsigned short)pack_bf16x2(y, 0.0f);
-              else
-                part[(size_t)(c0 + i + k) * (kv.D + 2) + 2 + tok] = y;
-            }
+            if (at == 0) continue;
+            if (whole)
+              reinterpret_cast<unsigned short *>(at)[tok] = (unsigned short)pack_bf16x2(y, 0.0f);
+            else
+              reinterpret_cast<float *>(at)[tok] = y;
           }
         }
       }
@@ -1462,6 +1442,10 @@ __global__ void __launch_bounds__(Cfg<RN>::kThreads, Cfg<RN>::kCtas)
       mbar_init(&sm.k_full[tid], 1);
       mbar_init(&sm.k_empty[tid], 1);
     }
+    if (tid < C::kV) {
+      mbar_init(&sm.v_full[tid], 1);
+      mbar_init(&sm.v_empty[tid], C::kWorkers);
+    }
     if (tid < 2) {
       mbar_init(&sm.s_full[tid], 1);
       mbar_init(&sm.s_empty[tid], 4 * C::kGroups);
@@ -1477,8 +1461,6 @@ __global__ void __launch_bounds__(Cfg<RN>::kThreads, Cfg<RN>::kCtas)
     }
     if (tid < 4 * C::kGroups) sm.vote[tid >> 2][tid & 3] = 0;
     if (tid == 0) {
-      mbar_init(&sm.v_full, 1);
-      mbar_init(&sm.v_empty, C::kWorkers);
       mbar_init(&sm.q_full, C::kWorkers);
       mbar_init(&sm.q_empty, 1);
       mbar_init(&sm.both, 4 * C::kGroups);
