@@ -31,9 +31,9 @@
 // by a second kernel, in order.  Up to 64 rows an SM holds two CTAs: one's
 // beginnings and ends of requests, which are chains of short steps, overlap the
 // other's tiles.  With 128 rows one CTA takes the whole SM.
-// Roles: warp 0 copies (TMA), warp 1 issues products, the next warps widen V,
-// stage q and build drafted tiles, the last four or eight take the softmax and
-// write results.  A request's drafted tiles come first: they are built while the
+// Roles: warp 0 copies (TMA), warp 1 issues products, warps 4-7 widen V, stage q
+// and build drafted tiles, the last four or eight take the softmax and write
+// results.  A request's drafted tiles come first: they are built while the
 // results of the request before are written.  Every wait is bounded in time.
 #include <cstddef>
 
@@ -58,8 +58,15 @@ template <int RN>
 struct Cfg {
   static constexpr int kCtas = RN <= 64 ? 2 : 1;       // CTAs an SM
   static constexpr int kGroups = RN <= 64 ? 1 : 2;     // softmax groups of four warps: a part of the rows each
-  static constexpr int kWorkers = RN <= 64 ? 2 : 4;    // warps that widen V
-  static constexpr int kFirst = 2 + kWorkers;          // first softmax warp
+  static constexpr int kWorkers = 4;                   // warps that widen V: one on each quarter of the SM
+  static constexpr int kFirst = 8;                     // first softmax warp
+  // Registers a thread: of the launch (what two CTAs, or one, leave room for), and
+  // of the three kinds of warpgroup, which share out those of the launch:
+  // kIssue + kWiden + kGroups kSoft = (2 + kGroups) kRegs
+  static constexpr int kRegs = RN <= 64 ? 80 : 128;
+  static constexpr int kIssue = RN <= 64 ? 64 : 72, kWiden = RN <= 64 ? 48 : 88;
+  static constexpr int kSoft = RN <= 64 ? 128 : 176;
+  static_assert(kIssue + kWiden + kGroups * kSoft == (2 + kGroups) * kRegs, "");
   static constexpr int kThreads = 32 * (kFirst + 4 * kGroups);
   static constexpr int kCols = RN / kGroups;           // most columns of a softmax thread
   static constexpr bool kHold = RN == 32;              // its scores stay in registers
@@ -957,7 +964,7 @@ struct Tile {
   }
 
   __device__ __forceinline__ void operands() {
-    const int worker = warp - 2;
+    const int worker = warp - 4;
     uint32_t c = 0;
     bool ok = true;
 #pragma unroll 1
@@ -1405,7 +1412,7 @@ struct Tile {
       if (index < finished) continue;
       float *part = p.part + (size_t)(2 * blockIdx.x + (w.t0 == 0)) * partial_floats(RN, kv.D);
 #pragma unroll 1
-      for (int col = threadIdx.x; col < columns; col += C::kThreads) {
+      for (int col = threadIdx.x - 32 * C::kFirst; col < columns; col += C::kThreads - 32 * C::kFirst) {
         const int row = w.rt * RN + col, n = row / p.G;
         if (row >= p.N * p.G) continue;
         const long long at = ((long long)w.b * p.N + n) * p.Hq + w.h * p.G + row - n * p.G;
@@ -1418,7 +1425,7 @@ struct Tile {
           part[(size_t)col * (kv.D + 2) + 1] = -(float)SPECDEC_ROW_INTERNAL;
         }
       }
-      if (threadIdx.x == 0) p.row_status[w.b] = SPECDEC_ROW_INTERNAL;
+      if (threadIdx.x == 32 * C::kFirst) p.row_status[w.b] = SPECDEC_ROW_INTERNAL;
     }
   }
 };
@@ -1485,20 +1492,27 @@ __global__ void __launch_bounds__(Cfg<RN>::kThreads, Cfg<RN>::kCtas)
   fence_after();
   const Plan plan = make_plan(p, box, blockIdx.x, gridDim.x, sm.scan, &sm.plan);
   Tile<RN, kPlain> tile(p, sm, &k_map, &v_map, box);
-  if (warp == 0)
-    tile.copies(plan);
-  else if (warp == 1)
-    tile.products();
-  else if (warp < C::kFirst)
+  // warps 0-3: copies, products (two stay idle); 4-7: operands; the others: softmax
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kIssue));
+    if (warp == 0)
+      tile.copies(plan);
+    else if (warp == 1)
+      tile.products();
+  } else if (warp < C::kFirst) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kWiden));
     tile.operands();
-  else
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoft));
     tile.softmax();
+  }
   fence_before();
   __syncthreads();
   fence_after();
   if (sm.give_up) {
     if (warp == 0) tile.drain();
-    tile.give_up_results(p, box, plan, min(sm.done[0], sm.done[C::kGroups - 1]), tile.columns);
+    if (warp >= C::kFirst)
+      tile.give_up_results(p, box, plan, min(sm.done[0], sm.done[C::kGroups - 1]), tile.columns);
     __syncthreads();
   }
   if (warp == 1)
