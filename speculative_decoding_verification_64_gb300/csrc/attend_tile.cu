@@ -68,12 +68,13 @@ struct Cfg {
   static constexpr int kSoft = RN <= 64 ? 128 : 176;
   static_assert(kIssue + kWiden + kGroups * kSoft == (2 + kGroups) * kRegs, "");
   static constexpr int kThreads = 32 * (kFirst + 4 * kGroups);
-  static constexpr int kCols = RN / kGroups;           // most columns of a softmax thread
-  static constexpr bool kHold = RN == 32;              // its scores stay in registers
+  // most columns of a softmax thread (40 and their scores fit its registers, 48 do not)
+  static constexpr int kCols = RN == 48 ? 40 : RN / kGroups;
+  static constexpr bool kHold = RN <= 48;              // its scores stay in registers
   static constexpr int kK = RN <= 64 ? 1 : 2;          // stages of K codes (free once scores are made)
-  static constexpr int kV = RN == 32 ? 2 : 1;          // stages of V codes (free once widened)
+  static constexpr int kV = RN <= 48 ? 3 : 2;          // half tiles of V codes (free once widened)
   static constexpr int kBuf = RN <= 64 ? 1 : 2;        // buffers of widened V, and of P^T
-  static constexpr int kTmem = RN == 32 ? 128 : RN == 64 ? 256 : 512;
+  static constexpr int kTmem = RN == 32 ? 128 : RN <= 64 ? 256 : 512;
   static constexpr int kSpans = RN <= 64 ? 1 : 2;      // 64-row groups of P^T
 };
 
@@ -104,9 +105,10 @@ template <int RN>
 struct Smem {
   using C = Cfg<RN>;
   uint8_t k[C::kK][kTileBytes];           // K codes [token][128 B], 128-byte swizzle
-  uint8_t v[C::kV][kTileBytes];           // V codes, the same (drafted tiles: the low terms of k)
+  uint8_t v[C::kV][kTileBytes / 2];       // V codes, the same, 64 tokens each
   uint8_t vh[C::kBuf][2][kTileBytes];     // V in fp16, [64 elements][token][128 B]
-  uint8_t pt[C::kBuf][C::kSpans][kTileBytes];  // P^T in fp16, [64 rows][token][128 B]
+  // P^T in fp16, [64 rows][token][128 B]; before a drafted tile's, the low terms of its k
+  uint8_t pt[C::kBuf][C::kSpans][kTileBytes];
   uint8_t q[2][RN * kRow];                // q: high and low terms [row][128 B]
   float2 boxes[8][8];                     // k and v scales of a tile's pieces
   float2 unit[2][kTok];                   // drafted tiles: per token (k below 0: it is not finite)
@@ -201,8 +203,7 @@ __device__ __forceinline__ void tmem_load8(uint32_t at, float *x) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
                  "=r"(r[7])
-               : "r"(at)
-               : "memory");
+               : "r"(at));
 #pragma unroll
   for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(r[i]);
 }
@@ -210,7 +211,7 @@ __device__ __forceinline__ void tmem_load8(uint32_t at, float *x) {
 __device__ __forceinline__ void tmem_wait8(float *x) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+f"(x[0]), "+f"(x[1]), "+f"(x[2]), "+f"(x[3]), "+f"(x[4]), "+f"(x[5]),
-                 "+f"(x[6]), "+f"(x[7])::"memory");
+                 "+f"(x[6]), "+f"(x[7]));
 }
 __device__ __forceinline__ void tmem_store8(uint32_t at, const float *x) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at),
@@ -231,6 +232,20 @@ __device__ __forceinline__ void tmem_store1(uint32_t at, float x) {
 }
 __device__ __forceinline__ void tmem_stored() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void store_global16(bool here, unsigned long long at, uint32_t x) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b16 t;\n\tsetp.ne.u32 p, %0, 0;\n\tcvt.u16.u32 t, %2;\n\t"
+      "@p st.global.u16 [%1], t;\n\t}" ::"r"((uint32_t)here),
+      "l"(at), "r"(x)
+      : "memory");
+}
+__device__ __forceinline__ void store_global32(bool here, unsigned long long at, float x) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %0, 0;\n\t@p st.global.f32 [%1], %2;\n\t}" ::"r"(
+                   (uint32_t)here),
+               "l"(at), "f"(x)
+               : "memory");
 }
 
 using f2 = unsigned long long;  // two float32 values in one register pair
@@ -590,7 +605,7 @@ struct Tile {
 
   __device__ __forceinline__ void copies(const Plan &plan) {
     const specdec_kv_cache &kv = p.cache;
-    uint32_t c = 0, index = 0;
+    uint32_t c = 0, v = 0, index = 0;  // tiles; half tiles of V
     note.tiles = note.first = note.head = note.open = 0;
     Walk walk(p, box, plan);
     Segment w, ahead;
@@ -602,7 +617,7 @@ struct Tile {
       Piece next = piece_of(w, w.t0);
 #pragma unroll 1
       for (int t = w.t0; t < w.t1; ++t, ++c) {
-        const int ks = c % kK, vs = c % kV;
+        const int ks = c % kK;
         Piece x = next;
         if (t + 1 < w.t1) next = piece_of(w, t + 1);  // the next tile's ids load meanwhile
         const bool cached = t >= w.r.drafted;
@@ -618,38 +633,44 @@ struct Tile {
         // drafted tiles have nothing to copy, but a phase missed here would make
         // the slot's next wait take an old phase of the same parity for its own
         if (!(ok = wait(&sm.k_empty[ks], empty_par(c, kK)))) break;
-        if (cached) {
-          if (lane == 0) mbar_arrive_expect_tx(&sm.k_full[ks], bytes);
-          __syncwarp();
-          if (x.mine) {
-            tma_rows(sm.k[ks] + lane * box * kRow, k_map, row, &sm.k_full[ks]);
-            sm.boxes[c & 7][lane] = unit;
-          }
-          __syncwarp();
-          if (lane < 4) mbar_arrive(&sm.box_full[c & 7]);
+        if (!cached) continue;
+        if (lane == 0) mbar_arrive_expect_tx(&sm.k_full[ks], bytes);
+        __syncwarp();
+        if (x.mine) {
+          tma_rows(sm.k[ks] + lane * box * kRow, k_map, row, &sm.k_full[ks]);
+          sm.boxes[c & 7][lane] = unit;
         }
-        if (!(ok = wait(&sm.v_empty[vs], empty_par(c, kV)))) break;
-        if (cached) {
-          if (lane == 0) mbar_arrive_expect_tx(&sm.v_full[vs], bytes);
+        __syncwarp();
+        if (lane < 4) mbar_arrive(&sm.box_full[c & 7]);
+#pragma unroll
+        for (int half = 0; half < 2; ++half, ++v) {
+          if (!(ok = wait(&sm.v_empty[v % kV], empty_par(v, kV)))) break;
+          const bool here = x.mine && (lane * box >= kTok / 2) == (half == 1);
+          const uint32_t n = (uint32_t)__popc(__ballot_sync(kAll, here)) * box * kRow;
+          if (lane == 0) mbar_arrive_expect_tx(&sm.v_full[v % kV], n);
           __syncwarp();
-          if (x.mine) tma_rows(sm.v[vs] + lane * box * kRow, v_map, row, &sm.v_full[vs]);
+          if (here)
+            tma_rows(sm.v[v % kV] + (lane * box - half * (kTok / 2)) * kRow, v_map, row,
+                     &sm.v_full[v % kV]);
         }
+        if (!ok) break;
       }
     }
     // Every copy has been waited on by its reader, unless somebody gave up: then
     // copies in flight get time to land before the CTA may leave.
     copied = c;
+    copied_v = v;
 #pragma unroll 1
     while (take(walk, w)) {
     }
     if (lane == 0) notes_of(p.part, RN, kv.D)[blockIdx.x] = note;
   }
 
-  uint32_t copied;
+  uint32_t copied, copied_v;
   __device__ void drain() {
     for (uint32_t i = copied > kK ? copied - kK : 0; i < copied; ++i)
       mbar_wait_bounded(&sm.k_full[i % kK], full_par(i, kK));
-    for (uint32_t i = copied > kV ? copied - kV : 0; i < copied; ++i)
+    for (uint32_t i = copied_v > kV ? copied_v - kV : 0; i < copied_v; ++i)
       mbar_wait_bounded(&sm.v_full[i % kV], full_par(i, kV));
   }
 
@@ -669,7 +690,7 @@ struct Tile {
         mma_issue<true>(d, ka + 2 * i, qb + 2 * i, idesc, true);
       }
       if (drafted) {
-        const uint64_t kl = operand(smem_addr(sm.v[c % kV]), 1024, 16);
+        const uint64_t kl = operand(smem_addr(sm.pt[c % kBuf][0]), 1024, 16);
 #pragma unroll 1
         for (int i = 0; i < steps; ++i) {
           mma_issue<true>(d, kl + 2 * i, qa + 2 * i, idesc, true);
@@ -678,11 +699,6 @@ struct Tile {
       }
       mma_commit(&sm.s_full[c & 1]);
       mma_commit(&sm.k_empty[c % kK]);
-      if (drafted) {  // the low terms stood in V's place, which an arrival of each worker frees
-#pragma unroll
-        for (int i = 1; i < C::kWorkers; ++i) mbar_arrive(&sm.v_empty[c % kV]);
-        mma_commit(&sm.v_empty[c % kV]);
-      }
       if (ends) mma_commit(&sm.q_empty);
     }
     __syncwarp();
@@ -729,10 +745,7 @@ struct Tile {
         if (first && !(ok = wait(&sm.q_full, index & 1))) break;
         if (!(ok = wait(&sm.box_full[c & 7], (c >> 3) & 1))) break;
         if (drafted) {
-          if (lane == 0) {  // nobody copies into this tile's slots
-            mbar_arrive(&sm.k_full[c % kK]);
-            mbar_arrive(&sm.v_full[c % kV]);
-          }
+          if (lane == 0) mbar_arrive(&sm.k_full[c % kK]);  // nobody copies into its slot
         } else if (!(ok = wait(&sm.k_full[c % kK], full_par(c, kK)))) {
           break;
         }
@@ -820,24 +833,35 @@ struct Tile {
       return load8(p.q, (first + n) * p.q_stride + (long long)(w.h * p.G + row - n * p.G) * D + e,
                    wide);
     };
-    uint4 next = load(worker * 2 + (lane >> 4));
+    constexpr int kBatch = 4, kStep = 2 * C::kWorkers;  // loads in flight; rows at once
 #pragma unroll 1
-    for (int r = worker * 2 + (lane >> 4); r < columns; r += 2 * C::kWorkers) {
-      const uint4 x = next;
-      next = load(r + 2 * C::kWorkers);
-      bool all;
-      const int ex = unit_exponent(row_top(x, all), 7);
-      split(sm.q[0], sm.q[1], r, e, x, ex);
-      if ((lane & 15) == 0) {
-        const int row = row0 + r, n = node_of(row);
-        const bool in = row < p.N * p.G && n < nodes;
-        sm.node[ring][r] = (uint8_t)(n - node_of(row0));
+    for (int r0 = worker * 2 + (lane >> 4); r0 < columns; r0 += kBatch * kStep) {
+      uint4 x[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) x[i] = load(r0 + i * kStep);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int r = r0 + i * kStep;
+        if (r - (lane >> 4) >= columns) break;
+        bool all;
+        const int ex = unit_exponent(row_top(x[i], all), 7);
+        split(sm.q[0], sm.q[1], r, e, x[i], ex);
         // a q that is not finite makes its row NaN
-        sm.rf[ring][r] = in ? (all ? p.scale * kLog2e * pow2i(ex) : __int_as_float(0x7fc00000)) : 0.0f;
-        sm.pos[ring][r] = in ? w.r.len + ((p.window > 0 || p.slopes) ? depth_of(w.b, n) : 0) : -1;
+        if ((lane & 15) == 0) sm.rf[ring][r] = all ? pow2i(ex) : __int_as_float(0x7fc00000);
+      }
+    }
+    __syncwarp();
+    if (lane < 16) {  // the warp's own rows: worker * 2 + {0, 1} + 8 i
+      const int r = worker * 2 + (lane & 1) + (lane >> 1) * kStep;
+#pragma unroll 1
+      for (int col = r; col < columns; col += 8 * kStep) {
+        const int row = row0 + col, n = node_of(row);
+        const bool in = row < p.N * p.G && n < nodes;
+        sm.node[ring][col] = (uint8_t)(n - node_of(row0));
+        sm.rf[ring][col] = in ? p.scale * kLog2e * sm.rf[ring][col] : 0.0f;
+        sm.pos[ring][col] = in ? w.r.len + ((p.window > 0 || p.slopes) ? depth_of(w.b, n) : 0) : -1;
         if (!kPlain)
-          sm.slope[ring][r] =
-              (in && p.slopes) ? p.slopes[w.h * p.G + row - n * p.G] * kLog2e : 0.0f;
+          sm.slope[ring][col] = (in && p.slopes) ? p.slopes[w.h * p.G + row - n * p.G] * kLog2e : 0.0f;
       }
     }
     fence_async_smem();
@@ -850,7 +874,7 @@ struct Tile {
   __device__ __noinline__ static bool sift(uint8_t *codes, int tid) {
     bool odd = false;
 #pragma unroll 1
-    for (int i = tid >> 4; i < kTok; i += 2 * C::kWorkers) {  // the thread's own pieces
+    for (int i = tid >> 4; i < kTok / 2; i += 2 * C::kWorkers) {  // the thread's own pieces
       uint32_t *w = reinterpret_cast<uint32_t *>(codes + i * kRow +
                                                  ((((tid & 15) >> 1) ^ (i & 7)) << 4) + (tid & 1) * 8);
 #pragma unroll 1
@@ -865,24 +889,28 @@ struct Tile {
     return odd;
   }
 
-  // V codes of a cached tile to fp16; tokens past the length as zeros.  A thread
+  // Half a tile of V codes to fp16; tokens past the length as zeros.  A thread
   // takes 8 codes at a time, 16 lanes a token: 8 bytes in, 16 out, each half-warp
-  // over all banks.
-  __device__ __forceinline__ void widen(const Segment &w, uint32_t index, int t, uint32_t c,
-                                        int worker) {
-    const int held = w.r.len - (w.r.from + (t - w.r.drafted) * kTok), tid = worker * 32 + lane;
-    if (partly_hidden(p, w.r, t) && sift(sm.v[c % kV], tid)) sm.dirty[index & 7] = 1;
-    const int h = tid & 15;
-    const uint8_t *src = sm.v[c % kV] + (h & 1) * 8;
-    uint8_t *dst = sm.vh[c % kBuf][h >> 3];
-#pragma unroll 4
-    for (int tok = tid >> 4; tok < kTok; tok += 2 * C::kWorkers) {
-      const int x7 = tok & 7;
-      uint2 x = *reinterpret_cast<const uint2 *>(src + tok * kRow + (((h >> 1) ^ x7) << 4));
-      if (tok >= held) x = make_uint2(0u, 0u);
-      *reinterpret_cast<uint4 *>(dst + tok * kRow + (((h & 7) ^ x7) << 4)) =
-          make_uint4(e4m3x2_to_half2(x.x), e4m3x2_to_half2(x.x >> 16), e4m3x2_to_half2(x.y),
-                     e4m3x2_to_half2(x.y >> 16));
+  // over all banks; all loads before the first store, which the compiler cannot
+  // know to be elsewhere.
+  __device__ __forceinline__ void widen(uint8_t *codes, uint8_t *vh, int held, int worker) {
+    constexpr int kStep = 2 * C::kWorkers, kBatch = kTok / 2 / kStep;
+    const int tid = worker * 32 + lane, h = tid & 15, tok0 = tid >> 4;
+    const uint8_t *src = codes + (h & 1) * 8;
+    uint8_t *dst = vh + (h >> 3) * kTileBytes;
+    uint2 x[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int tok = tok0 + i * kStep;
+      x[i] = *reinterpret_cast<const uint2 *>(src + tok * kRow + (((h >> 1) ^ (tok & 7)) << 4));
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int tok = tok0 + i * kStep;
+      if (tok >= held) x[i] = make_uint2(0u, 0u);
+      *reinterpret_cast<uint4 *>(dst + tok * kRow + (((h & 7) ^ (tok & 7)) << 4)) =
+          make_uint4(e4m3x2_to_half2(x[i].x), e4m3x2_to_half2(x[i].x >> 16),
+                     e4m3x2_to_half2(x[i].y), e4m3x2_to_half2(x[i].y >> 16));
     }
   }
 
@@ -906,7 +934,7 @@ struct Tile {
                          : zero;
       bool all;
       const int ek = unit_exponent(row_top(x, all), 7);
-      split(sm.k[c % kK], sm.v[c % kV], r, e, x, ek);
+      split(sm.k[c % kK], sm.pt[c % kBuf][0], r, e, x, ek);
       const float k_unit = all ? pow2i(ek) : -1.0f;
       const int ev = unit_exponent(row_top(y, all), 10);
       const float inv = pow2i(-ev);
@@ -936,7 +964,14 @@ struct Tile {
     for (int col = tid; col < columns; col += 32 * C::kWorkers) {
       const int n = node_of(w.rt * RN + col);
       uint32_t bits[4] = {0u, 0u, 0u, 0u};
-      if (n < nodes) {
+      if (n < nodes && !p.parent) {  // a chain: nodes lo .. n
+        const int lo = max(p.window > 0 ? n - p.window + 1 : 0, j0) - j0, hi = min(n - j0, kTok - 1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int a = max(lo - 32 * i, 0), z = min(hi - 32 * i, 31);
+          bits[i] = z < a ? 0u : (kAll >> (31 - z)) & (kAll << a);
+        }
+      } else if (n < nodes) {
         int a = n;
 #pragma unroll 1
         for (int step = 0; a >= j0; ++step) {
@@ -965,7 +1000,7 @@ struct Tile {
 
   __device__ __forceinline__ void operands() {
     const int worker = warp - 4;
-    uint32_t c = 0;
+    uint32_t c = 0, v = 0;
     bool ok = true;
 #pragma unroll 1
     for (uint32_t index = 0; segment(index, ok); ++index) {
@@ -976,27 +1011,30 @@ struct Tile {
 #pragma unroll 1
       for (int t = t0; t < t1; ++t, ++c) {
         const bool drafted = t < drafts;
+        // room: outputs of the tile before in this buffer are done
+        if (!(ok = wait(&sm.pv_done[c % kBuf], empty_par(c, kBuf)))) break;
         if (drafted) {
           if (!(ok = wait(&sm.k_empty[c % kK], empty_par(c, kK)))) break;
-          if (!(ok = wait(&sm.v_empty[c % kV], empty_par(c, kV)))) break;
-        } else if (!(ok = wait(&sm.v_full[c % kV], full_par(c, kV)))) {
-          break;
-        }
-        if (!(ok = wait(&sm.pv_done[c % kBuf], empty_par(c, kBuf)))) break;
-        if (drafted)
           build(w, index, t, c, worker);
-        else
-          widen(w, index, t, c, worker);
+        } else {
+          const int held = w.r.len - (w.r.from + (t - drafts) * kTok);
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half, ++v) {
+            if (!(ok = wait(&sm.v_full[v % kV], full_par(v, kV)))) break;
+            uint8_t *codes = sm.v[v % kV];
+            if (partly_hidden(p, w.r, t) && sift(codes, worker * 32 + lane)) sm.dirty[index & 7] = 1;
+            widen(codes, sm.vh[c % kBuf][0] + half * (kTileBytes / 2), held - half * (kTok / 2), worker);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.v_empty[v % kV]);
+          }
+          if (!ok) break;
+        }
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
-          if (!drafted) mbar_arrive(&sm.v_empty[c % kV]);
           mbar_arrive(&sm.vh_full[c % kBuf]);
+          if (drafted) mbar_arrive(&sm.box_full[c & 7]);
         }
-        // four arrivals complete box_full
-        if (drafted && lane < 4 / C::kWorkers) mbar_arrive(&sm.box_full[c & 7]);
-        // as the copying warp: every phase of v_full is waited on
-        if (drafted && !(ok = wait(&sm.v_full[c % kV], full_par(c, kV)))) break;
       }
       if (!ok) break;
     }
@@ -1382,17 +1420,30 @@ struct Tile {
         __syncwarp();
         tmem_load8(o_at + i, o);
         tmem_wait8(o);
-        if (tok < kv.D) {
+        unsigned long long at[8];
+        float f[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const unsigned long long at = out_at[i + k];
-            const float f = out_fac[i + k], y = f != 0.0f ? o[k] * f : 0.0f;
-            if (at == 0) continue;
-            if (whole)
-              reinterpret_cast<unsigned short *>(at)[tok] = (unsigned short)pack_bf16x2(y, 0.0f);
-            else
-              reinterpret_cast<float *>(at)[tok] = y;
-          }
+        for (int k = 0; k < 8; k += 4) {
+          const float4 x = *reinterpret_cast<const float4 *>(out_fac + i + k);
+          f[k] = x.x;
+          f[k + 1] = x.y;
+          f[k + 2] = x.z;
+          f[k + 3] = x.w;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; k += 2) {
+          const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(out_at + i + k);
+          at[k] = x.x;
+          at[k + 1] = x.y;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float y = f[k] != 0.0f ? o[k] * f[k] : 0.0f;
+          const bool here = at[k] != 0 && tok < kv.D;
+          if (whole)
+            store_global16(here, at[k] + 2 * tok, pack_bf16x2(y, 0.0f));
+          else
+            store_global32(here, at[k] + 4 * tok, y);
         }
       }
       if (leader && group == 0 && whole && w.h == 0 && w.rt == 0) p.row_status[w.b] = bad;
@@ -1635,13 +1686,16 @@ bool encode(CUtensorMap *map, void *codes, const specdec_kv_cache &kv, int box) 
            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int box_rows(int block) {  // the largest power of two that divides the block and the tile
+int box_rows(int block) {  // the largest power of two that divides the block and half a tile
   int box = 16;
-  while (box < kTok && block % (2 * box) == 0) box *= 2;
+  while (box < kTok / 2 && block % (2 * box) == 0) box *= 2;
   return box;
 }
 
-int rows_of(int N, int G) { return N * G <= 32 ? 32 : N * G <= 64 ? 64 : 128; }
+int rows_of(int N, int G) {  // the classes of the kernel
+  const int rows = N * G;
+  return rows <= 32 ? 32 : rows <= 40 ? 48 : rows <= 64 ? 64 : 128;
+}
 
 template <int RN, bool kPlain>
 cudaError_t launch_rn(AttendParams p, cudaStream_t stream) {
@@ -1690,6 +1744,8 @@ cudaError_t launch_attend_tile(const AttendParams &p, cudaStream_t stream) {
   const int rows = rows_of(p.N, p.G);
   if (rows == 32)
     return plain ? launch_rn<32, true>(p, stream) : launch_rn<32, false>(p, stream);
+  if (rows == 48)
+    return plain ? launch_rn<48, true>(p, stream) : launch_rn<48, false>(p, stream);
   if (rows == 64)
     return plain ? launch_rn<64, true>(p, stream) : launch_rn<64, false>(p, stream);
   return plain ? launch_rn<128, true>(p, stream) : launch_rn<128, false>(p, stream);
