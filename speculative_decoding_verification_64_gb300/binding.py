@@ -678,20 +678,38 @@ def _raw_stream(stream) -> int:
     return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
 
 
-def _named(prefix: str, holder) -> dict:
-    """A holder's tensors under names of its own for ``_cuda`` (none for None)."""
-    return {} if holder is None else {f"{prefix}.{k}": t for k, t in vars(holder).items()}
+# torch's own lookup of the current stream without making a Stream object, where it has one
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _token_stride(t: torch.Tensor, name: str, dtype, B: int, N: int) -> int:
-    """Elements between consecutive tokens of a [B, N, H, D] tensor whose heads and
-    elements are contiguous (a whole tensor, or heads of a fused projection)."""
-    if t.dtype != dtype:
+def _here(stream, tensors, names):
+    """The raw stream of a call on these tensors (None skipped), which all have to live on the
+    current device.  These calls run once a layer and step, some on a single token, so their
+    checks are the plain attribute reads that cost least; ``_cuda`` words the error."""
+    dev = tensors[0].get_device()  # -1: host memory
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            dev = -1
+            break
+    if dev < 0 or dev != torch.cuda.current_device():
+        _cuda(**dict(zip(names, tensors)))
+    if stream is None and _current_raw_stream is not None:
+        return _current_raw_stream(dev)
+    return _raw_stream(stream)
+
+
+def _tokens4(t: torch.Tensor, name: str, dtype, B: int, N: int, H, D: int) -> int:
+    """Elements between consecutive tokens of a [B, N, H, D] tensor (H None: any) whose heads
+    and elements are contiguous (a whole tensor, or heads of a fused projection)."""
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 4 or t.shape[0] != B or t.shape[1] != N:
-        raise ValueError(f"{name} must have shape [{B}, {N}, heads, D], got {tuple(t.shape)}")
-    H, D = t.shape[2], t.shape[3]
+    shape = t.shape
+    if len(shape) != 4 or shape[0] != B or shape[1] != N or shape[3] != D or \
+            (H is not None and shape[2] != H):
+        raise ValueError(f"{name} must have shape [{B}, {N}, {'heads' if H is None else H}, {D}], "
+                         f"got {tuple(shape)}")
     s = t.stride()
+    H = shape[2]
     at = s[1] if N > 1 else s[0] if B > 1 else H * D
     if (s[3] != 1 and D > 1) or (s[2] != D and H > 1) or (B > 1 and N > 1 and s[0] != N * at):
         raise ValueError(f"{name}: heads and elements must be contiguous and tokens one stride "
@@ -699,22 +717,34 @@ def _token_stride(t: torch.Tensor, name: str, dtype, B: int, N: int) -> int:
     return at
 
 
+def _flat(t: torch.Tensor, name: str, dtype, shape):
+    """A contiguous tensor of this type and shape (a tuple)."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _req(t, name, dtype, shape, t.device)
+
+
+_CACHE_NAMES = ("cache.k", "cache.v", "cache.k_scale", "cache.v_scale", "cache.block_table",
+                "cache.length")
+
+
 def _cache_struct(c: KVCache, B: int) -> _CacheStruct:
-    dev = c.k.device
-    if c.k.dim() != 4:
-        raise ValueError(f"cache.k must be [n_blocks, Hkv, block, D], got {tuple(c.k.shape)}")
-    nb, Hkv, block, D = c.k.shape
-    for t, name, dtype, shape in ((c.k, "cache.k", torch.float8_e4m3fn, (nb, Hkv, block, D)),
-                                  (c.v, "cache.v", torch.float8_e4m3fn, (nb, Hkv, block, D)),
-                                  (c.k_scale, "cache.k_scale", torch.float32, (nb, Hkv)),
-                                  (c.v_scale, "cache.v_scale", torch.float32, (nb, Hkv)),
-                                  (c.block_table, "cache.block_table", torch.int32,
-                                   (B, c.block_table.shape[-1])),
-                                  (c.length, "cache.length", torch.int32, (B,))):
-        _req(t, name, dtype, shape, dev)
-    return _CacheStruct(c.k.data_ptr(), c.v.data_ptr(), c.k_scale.data_ptr(),
-                        c.v_scale.data_ptr(), c.block_table.data_ptr(), c.length.data_ptr(),
-                        nb, c.block_table.shape[1], block, Hkv, D)
+    k, v, ks, vs, table, length = c.k, c.v, c.k_scale, c.v_scale, c.block_table, c.length
+    shape = k.shape
+    if len(shape) != 4:
+        raise ValueError(f"cache.k must be [n_blocks, Hkv, block, D], got {tuple(shape)}")
+    nb, Hkv, block, D = shape
+    f8 = torch.float8_e4m3fn
+    _flat(k, "cache.k", f8, shape)
+    _flat(v, "cache.v", f8, shape)
+    _flat(ks, "cache.k_scale", torch.float32, (nb, Hkv))
+    _flat(vs, "cache.v_scale", torch.float32, (nb, Hkv))
+    if table.dim() != 2:
+        raise ValueError(f"cache.block_table must be [B, max_blocks], got {tuple(table.shape)}")
+    width = table.shape[1]
+    _flat(table, "cache.block_table", torch.int32, (B, width))
+    _flat(length, "cache.length", torch.int32, (B,))
+    return _CacheStruct(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(),
+                        table.data_ptr(), length.data_ptr(), nb, width, block, Hkv, D)
 
 
 def rope_frequencies(rot: int, theta: float = 10000.0, factor: float = 1.0,
@@ -758,38 +788,39 @@ def rope(q: torch.Tensor, k: Optional[torch.Tensor], freq: torch.Tensor,
     returns the turned (q, k).  Positions are ``positions`` [B, N], or ``base`` [B] plus the
     depth of each node of ``parent`` [B, N] (a chain without it).  ``backward``: the
     gradient, from dq and dk."""
-    _cuda(q=q, k=k, freq=freq, positions=positions, base=base, parent=parent, q_out=q_out,
-          k_out=k_out)
-    dt, dev = dtype_code(q), q.device
+    raw = _here(stream, (q, k, freq, positions, base, parent, q_out, k_out),
+                ("q", "k", "freq", "positions", "base", "parent", "q_out", "k_out"))
+    dt = dtype_code(q)
     if q.dim() != 4:
         raise ValueError(f"q must be [B, N, Hq, D], got {tuple(q.shape)}")
     B, N, Hq, D = q.shape
-    q_at = _token_stride(q, "q", q.dtype, B, N)
+    q_at = _tokens4(q, "q", q.dtype, B, N, Hq, D)
     Hk = k_at = 0
     if k is not None:
-        k_at, Hk = _token_stride(k, "k", q.dtype, B, N), k.shape[2]
-        if k.shape[3] != D:
-            raise ValueError(f"k must have heads of {D} elements, got {k.shape[3]}")
-    _req(freq, "freq", torch.int64, (freq.numel(),), dev)
-    for t, name, shape in ((positions, "positions", (B, N)), (base, "base", (B,)),
-                           (parent, "parent", (B, N))):
-        if t is not None:
-            _req(t, name, torch.int32, shape, dev)
+        k_at, Hk = _tokens4(k, "k", q.dtype, B, N, None, D), k.shape[2]
+    half = freq.numel()
+    _flat(freq, "freq", torch.int64, (half,))
+    if positions is not None:
+        _flat(positions, "positions", torch.int32, (B, N))
+    if base is not None:
+        _flat(base, "base", torch.int32, (B,))
+    if parent is not None:
+        _flat(parent, "parent", torch.int32, (B, N))
     if q_out is None:
-        q_out = torch.empty((B, N, Hq, D), dtype=q.dtype, device=dev)
+        q_out = torch.empty((B, N, Hq, D), dtype=q.dtype, device=q.device)
     else:
-        _req(q_out, "q_out", q.dtype, (B, N, Hq, D), dev)
+        _flat(q_out, "q_out", q.dtype, (B, N, Hq, D))
     if k is None:
         k_out = None
     elif k_out is None:
-        k_out = torch.empty((B, N, Hk, D), dtype=q.dtype, device=dev)
+        k_out = torch.empty((B, N, Hk, D), dtype=q.dtype, device=q.device)
     else:
-        _req(k_out, "k_out", q.dtype, (B, N, Hk, D), dev)
+        _flat(k_out, "k_out", q.dtype, (B, N, Hk, D))
     rc = load_library().specdec_rope(
         q.data_ptr(), _raw(k), dt, q_at, k_at, freq.data_ptr(), _raw(positions), _raw(base),
-        _raw(parent), B, N, Hq, Hk, D, 2 * freq.numel(),
+        _raw(parent), B, N, Hq, Hk, D, 2 * half,
         (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_BACKWARD if backward else 0), magnitude,
-        q_out.data_ptr(), _raw(k_out), _raw_stream(stream))
+        q_out.data_ptr(), _raw(k_out), raw)
     _check(rc, "specdec_rope")
     return q_out, k_out
 
@@ -803,32 +834,31 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache,
     or of 0 .. N-1.  After a verify step: ``count=r.n_accepted, extra=1`` and, for a tree,
     ``path=r.path_nodes``.  ``cache.length`` is left alone: set it to the result's
     ``length`` for the next step."""
-    _cuda(k=k, v=v, count=count, path=path,
-          **_named("cache", cache), **_named("out", out))
-    dt, dev = dtype_code(k), k.device
+    raw = _here(stream, (k, v, count, path, cache.k, cache.v, cache.k_scale, cache.v_scale,
+                         cache.block_table, cache.length) +
+                (() if out is None else (out.length, out.row_status)),
+                ("k", "v", "count", "path") + _CACHE_NAMES + ("out.length", "out.row_status"))
+    dt = dtype_code(k)
     if k.dim() != 4:
         raise ValueError(f"k must be [B, N, Hkv, D], got {tuple(k.shape)}")
     B, N = k.shape[:2]
-    k_at, v_at = _token_stride(k, "k", k.dtype, B, N), _token_stride(v, "v", k.dtype, B, N)
     c = _cache_struct(cache, B)
-    for t, name in ((k, "k"), (v, "v")):
-        if t.shape[2] != c.Hkv or t.shape[3] != c.D:
-            raise ValueError(f"{name} must have {c.Hkv} heads of {c.D} elements, as the cache, "
-                             f"got {tuple(t.shape)}")
+    k_at = _tokens4(k, "k", k.dtype, B, N, c.Hkv, c.D)
+    v_at = _tokens4(v, "v", k.dtype, B, N, c.Hkv, c.D)
     if count is not None:
-        _req(count, "count", torch.int32, (B,), dev)
+        _flat(count, "count", torch.int32, (B,))
     if path is not None:
-        _req(path, "path", torch.int32, (B, path.shape[-1]), dev)
+        _flat(path, "path", torch.int32, (B, path.shape[-1]))
     if out is None:
-        both = torch.empty((2, B), dtype=torch.int32, device=dev)
-        out = AppendOut(both[0], both[1])
+        out = AppendOut(torch.empty(B, dtype=torch.int32, device=k.device),
+                        torch.empty(B, dtype=torch.int32, device=k.device))
     else:
-        _req(out.length, "out.length", torch.int32, (B,), dev)
-        _req(out.row_status, "out.row_status", torch.int32, (B,), dev)
+        _flat(out.length, "out.length", torch.int32, (B,))
+        _flat(out.row_status, "out.row_status", torch.int32, (B,))
     rc = load_library().specdec_kv_append(
         k.data_ptr(), v.data_ptr(), dt, k_at, v_at, _raw(count), extra, _raw(path),
         path.shape[1] if path is not None else 0, ctypes.addressof(c), B, N,
-        out.length.data_ptr(), out.row_status.data_ptr(), _raw_stream(stream))
+        out.length.data_ptr(), out.row_status.data_ptr(), raw)
     _check(rc, "specdec_kv_append")
     return out
 
@@ -853,41 +883,44 @@ def attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: KVCache,
     """Attention of drafted tokens (``specdec_attend``): q [B, N, Hq, D] over the request's
     cached tokens and, by the chain or the tree ``parent`` [B, N], over the drafted tokens'
     own k, v [B, N, Hkv, D].  ``scale`` defaults to D ** -0.5."""
-    _cuda(q=q, k=k, v=v, parent=parent, n_nodes=n_nodes, slopes=slopes, workspace=workspace,
-          **_named("cache", cache), **_named("out", out))
-    dt, dev = dtype_code(q), q.device
+    raw = _here(stream, (q, k, v, parent, n_nodes, slopes, workspace, cache.k, cache.v,
+                         cache.k_scale, cache.v_scale, cache.block_table, cache.length) +
+                (() if out is None else (out.out, out.lse, out.row_status)),
+                ("q", "k", "v", "parent", "n_nodes", "slopes", "workspace") + _CACHE_NAMES +
+                ("out.out", "out.lse", "out.row_status"))
+    dtype = q.dtype
+    dt = dtype_code(q)
     if q.dim() != 4:
         raise ValueError(f"q must be [B, N, Hq, D], got {tuple(q.shape)}")
     B, N, Hq, D = q.shape
-    q_at = _token_stride(q, "q", q.dtype, B, N)
-    k_at, v_at = _token_stride(k, "k", q.dtype, B, N), _token_stride(v, "v", q.dtype, B, N)
     c = _cache_struct(cache, B)
-    for t, name in ((k, "k"), (v, "v")):
-        if t.shape[2] != c.Hkv or t.shape[3] != c.D:
-            raise ValueError(f"{name} must have {c.Hkv} heads of {c.D} elements, as the cache, "
-                             f"got {tuple(t.shape)}")
     if D != c.D:
         raise ValueError(f"q has heads of {D} elements, the cache of {c.D}")
-    for t, name, dtype, shape in ((parent, "parent", torch.int32, (B, N)),
-                                  (n_nodes, "n_nodes", torch.int32, (B,)),
-                                  (slopes, "slopes", torch.float32, (Hq,))):
-        if t is not None:
-            _req(t, name, dtype, shape, dev)
+    q_at = _tokens4(q, "q", dtype, B, N, Hq, D)
+    k_at = _tokens4(k, "k", dtype, B, N, c.Hkv, D)
+    v_at = _tokens4(v, "v", dtype, B, N, c.Hkv, D)
+    if parent is not None:
+        _flat(parent, "parent", torch.int32, (B, N))
+    if n_nodes is not None:
+        _flat(n_nodes, "n_nodes", torch.int32, (B,))
+    if slopes is not None:
+        _flat(slopes, "slopes", torch.float32, (Hq,))
     if out is None:
-        out = AttendOut(torch.empty((B, N, Hq, D), dtype=q.dtype, device=dev),
+        dev = q.device
+        out = AttendOut(torch.empty((B, N, Hq, D), dtype=dtype, device=dev),
                         torch.empty((B, N, Hq), dtype=torch.float32, device=dev),
                         torch.empty(B, dtype=torch.int32, device=dev))
     else:
-        _req(out.out, "out.out", q.dtype, (B, N, Hq, D), dev)
+        _flat(out.out, "out.out", dtype, (B, N, Hq, D))
         if out.lse is not None:
-            _req(out.lse, "out.lse", torch.float32, (B, N, Hq), dev)
-        _req(out.row_status, "out.row_status", torch.int32, (B,), dev)
+            _flat(out.lse, "out.lse", torch.float32, (B, N, Hq))
+        _flat(out.row_status, "out.row_status", torch.int32, (B,))
     if workspace is None:
         workspace = alloc_attend_workspace(q, cache)
     rc = load_library().specdec_attend(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), dt, q_at, k_at, v_at, _raw(parent),
         _raw(n_nodes), ctypes.addressof(c), B, N, Hq, D ** -0.5 if scale is None else scale,
         softcap, _raw(slopes), window, out.out.data_ptr(), _raw(out.lse),
-        out.row_status.data_ptr(), workspace.data_ptr(), workspace.numel(), _raw_stream(stream))
+        out.row_status.data_ptr(), workspace.data_ptr(), workspace.numel(), raw)
     _check(rc, "specdec_attend")
     return out

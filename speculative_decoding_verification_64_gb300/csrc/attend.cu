@@ -32,7 +32,10 @@
 // granule, non-finite v are taken out of the products (0 * NaN would reach rows
 // that do not see them) and added to the rows that do.
 //
-// With several splits a second kernel joins their partials in split order.
+// The tokens' granules, drafted ones last, are split over up to eight CTAs, a
+// cluster, that join their partials through each other's shared memory: one
+// launch.  More splits than that (few heads over a long cache) go through the
+// workspace and a second kernel.
 #include "attention_common.cuh"
 
 namespace specdec {
@@ -81,21 +84,22 @@ __device__ __forceinline__ uint2 ldg_stream8(const uint8_t *p) {
   return r;
 }
 
-template <int DP, bool kF32>
+template <int DP, bool kF32, bool kPlain>
 struct Kernel {
   static constexpr int KC = DP / 64;  // 16-byte pieces of a token that a lane takes for q k^T
   static constexpr int VB = DP / 8;   // consecutive elements that a lane takes for p v
   static constexpr int NT = DP / 8;   // 8-column tiles of the output
   static constexpr int KS = DP / 16;  // inner steps of q k^T
-  static constexpr int U = DP > 128 || kF32 ? 1 : 2;  // granules a warp has in flight
+  static constexpr int U = 1;  // granules a warp has in flight
 
   struct Smem {
     uint4 q[KS][32];                    // A operands, in register order
     uint4 q_lo[kF32 ? KS : 1][32];      // the low terms of float32 activations
     float q_exp[kRows];                 // 2^e taken out of each row
-    float o[2][kRows][DP + 4];          // joining of the warps
-    float m[kWarps][kRows], l[kWarps][kRows], vref[kWarps];
-    int bad[kWarps];
+    float o[2][kRows][DP + 4];          // joining of the warps; o[0]: the CTA's sums
+    float m[kWarps][kRows], l[kWarps][kRows];
+    float all_m[kRows], all_l[kRows];   // the CTA's
+    int bad[kWarps], all_bad;
   };
 
   const AttendParams &p;
@@ -113,12 +117,12 @@ struct Kernel {
   __device__ Kernel(const AttendParams &p_, Smem &s_)
       : p(p_), sm(s_), lane(threadIdx.x & 31), warp(threadIdx.x >> 5), g((threadIdx.x & 31) >> 2),
         c(threadIdx.x & 3) {
-    // row tiles of one split are neighbours: they read the same tokens
+    // splits are neighbours (a cluster's CTAs), then row tiles, which read the same tokens
     int i = blockIdx.x;
-    tile = i % p.row_tiles;
-    i /= p.row_tiles;
     split = i % p.splits;
     i /= p.splits;
+    tile = i % p.row_tiles;
+    i /= p.row_tiles;
     h = i % p.cache.Hkv;
     b = i / p.cache.Hkv;
   }
@@ -131,7 +135,9 @@ struct Kernel {
   // scores: products -> base-2 exponents, masked where hidden
   // -------------------------------------------------------------------------
   __device__ __forceinline__ float score(float dot, float k_unit, int i, int dist) const {
-    float s = dot * (k_unit * rf[i]);  // natural units
+    // kPlain: neither cap nor bias, and rf carries log2(e)
+    float s = dot * (k_unit * rf[i]);
+    if (kPlain) return s;
     if (p.softcap > 0.0f) {
       const float y = s / p.softcap;
       float t;
@@ -222,15 +228,17 @@ struct Kernel {
     float ks, vs;
   };
 
-  // The block of token t and its slot there; ok = a block id in range.
+  __device__ __forceinline__ int block_of(int t) const {
+    return p.block_shift >= 0 ? t >> p.block_shift : t / p.cache.block;
+  }
   __device__ __forceinline__ int block_id(int t) const {
-    return __ldg(p.cache.block_table + (long long)b * p.cache.max_blocks + t / p.cache.block);
+    return __ldg(p.cache.block_table + (long long)b * p.cache.max_blocks + block_of(t));
   }
 
   __device__ __forceinline__ void load(Codes &w, int t0, int id) const {
     const specdec_kv_cache &kv = p.cache;
     const long long cell = (long long)id * kv.Hkv + h;
-    const int slot = t0 % kv.block;
+    const int slot = t0 - block_of(t0) * kv.block;
     const uint8_t *k = reinterpret_cast<const uint8_t *>(kv.k) +
                        (cell * kv.block + slot) * kv.D;
     const uint8_t *v = reinterpret_cast<const uint8_t *>(kv.v) +
@@ -354,7 +362,8 @@ struct Kernel {
     hit = __reduce_or_sync(kAll, hit);
     const specdec_kv_cache &kv = p.cache;
     const uint8_t *v = reinterpret_cast<const uint8_t *>(kv.v) +
-                       (((long long)id * kv.Hkv + h) * kv.block + t0 % kv.block) * kv.D;
+                       (((long long)id * kv.Hkv + h) * kv.block + t0 - block_of(t0) * kv.block) *
+                           kv.D;
     while (hit) {
       const int t = __ffs(hit) - 1;
       hit &= hit - 1;
@@ -433,30 +442,54 @@ struct Kernel {
   // -------------------------------------------------------------------------
   // the drafted tokens themselves
   // -------------------------------------------------------------------------
+  // The node above a, -1 above a root.
+  __device__ __forceinline__ int up_from(int a) const {
+    if (!p.parent || a == 0) return a - 1;
+    const int up = __ldg(p.parent + (long long)b * p.N + a);
+    return up < a ? max(up, -1) : -1;
+  }
+
   // Nodes of [j0, j0 + 16) that node n sees, as bits.
-  __device__ __forceinline__ unsigned above(int n, int depth, int j0) const {
+  __device__ __forceinline__ unsigned above(int n, int j0) const {
     unsigned bits = 0;
-    int a = n, at = depth;
-    while (a >= j0) {
-      if (a < j0 + kGran && (p.window == 0 || depth - at < p.window)) bits |= 1u << (a - j0);
-      int up = a - 1;
-      if (p.parent && a > 0) {
-        up = p.parent[(long long)b * p.N + a];
-        if (up >= a) up = -1;
-      }
-      a = up;
-      --at;
+    int a = n;
+    for (int step = 0; a >= j0 && (p.window == 0 || step < p.window); ++step) {
+      if (a < j0 + kGran) bits |= 1u << (a - j0);
+      a = up_from(a);
     }
     return bits;
+  }
+
+  // 4 consecutive activations; `wide`: on a multiple of their 4 elements
+  __device__ __forceinline__ float4 act4(const void *base, long long at, bool wide) const {
+    if (!wide) return act4_narrow(base, at);
+    if (kF32) return __ldg(reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(base) + at));
+    const uint2 w = __ldg(reinterpret_cast<const uint2 *>(reinterpret_cast<const unsigned short *>(base) + at));
+    return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+  }
+  static __device__ __noinline__ float4 act4_narrow(const void *base, long long at) {
+    constexpr int dt = kF32 ? SPECDEC_F32 : SPECDEC_BF16;
+    return make_float4(load_elem(base, dt, at), load_elem(base, dt, at + 1), load_elem(base, dt, at + 2),
+                       load_elem(base, dt, at + 3));
+  }
+  __device__ __forceinline__ bool wide_rows(const void *base, long long stride) const {
+    constexpr int bytes = kF32 ? 16 : 8;
+    return ((reinterpret_cast<uintptr_t>(base) | (uintptr_t)(stride * (bytes / 4))) & (bytes - 1)) == 0;
+  }
+  static __device__ __forceinline__ float size_of(float x) {  // of what is finite
+    const float a = fabsf(x);
+    return a < INFINITY ? a : 0.0f;
+  }
+  static __device__ __forceinline__ float top4(const float4 &x) {
+    return fmaxf(fmaxf(size_of(x.x), size_of(x.y)), fmaxf(size_of(x.z), size_of(x.w)));
   }
 
   __device__ __forceinline__ void drafted(int j0) {
     const specdec_kv_cache &kv = p.cache;
     const long long first = (long long)b * p.N + j0;
     const int held = min(nodes - j0, kGran);
-    unsigned see[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) see[i] = live[i] ? above(node[i], pos[i] - len, j0) : 0u;
+    const bool k_wide = wide_rows(p.k_new, p.k_stride), v_wide = wide_rows(p.v_new, p.v_stride);
+    const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 
     // q k^T, the node's k in units of its size
     float s[1][2][4], unit_k[2];
@@ -464,13 +497,19 @@ struct Kernel {
     for (int nt = 0; nt < 2; ++nt) {
       const int t = nt * 8 + g;
       const long long at = (first + t) * p.k_stride + (long long)h * kv.D;
+      float4 x[KC][4];
       float top = 0.0f;
-      if (t < held)
-        for (int i = 0; i < KC; ++i)
-          for (int e = (c + 4 * i) * 16; e < (c + 4 * i) * 16 + 16 && e < kv.D; ++e) {
-            const float x = fabsf(act(p.k_new, at + e));
-            if (x < INFINITY) top = fmaxf(top, x);
-          }
+#pragma unroll
+      for (int i = 0; i < KC; ++i)
+#pragma unroll
+        for (int sub = 0; sub < 4; ++sub) {
+          const int e = (c + 4 * i) * 16 + sub * 4;
+          x[i][sub] = (t < held && e < kv.D) ? act4(p.k_new, at + e, k_wide) : zero;
+        }
+#pragma unroll
+      for (int i = 0; i < KC; ++i)
+#pragma unroll
+        for (int sub = 0; sub < 4; ++sub) top = fmaxf(top, top4(x[i][sub]));
       top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
       top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
       const int ex = unit_exponent(top);
@@ -478,19 +517,18 @@ struct Kernel {
       const float inv = pow2i(-ex);
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[0][nt][e] = 0.0f;
-      for (int i = 0; i < KC; ++i)
-        for (int sub = 0; sub < 4; ++sub) {
-          const int e = (c + 4 * i) * 16 + sub * 4;
-          float x[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            x[k] = (t < held && e < kv.D) ? act(p.k_new, at + e + k) * inv : 0.0f;
-          const uint32_t b0 = pack_half2(x[0], x[1]), b1 = pack_half2(x[2], x[3]);
+      for (int i = 0; i < KC; ++i)
+#pragma unroll
+        for (int sub = 0; sub < 4; ++sub) {
+          const float4 y = make_float4(x[i][sub].x * inv, x[i][sub].y * inv, x[i][sub].z * inv,
+                                       x[i][sub].w * inv);
+          const uint32_t b0 = pack_half2(y.x, y.y), b1 = pack_half2(y.z, y.w);
           const uint4 qa = sm.q[i * 4 + sub][lane];
           const uint32_t a[4] = {qa.x, qa.y, qa.z, qa.w};
           mma16816(s[0][nt], a, b0, b1);
           if (kF32) {
-            const uint32_t l0 = low_half2(x[0], x[1], b0), l1 = low_half2(x[2], x[3], b1);
+            const uint32_t l0 = low_half2(y.x, y.y, b0), l1 = low_half2(y.z, y.w, b1);
             const uint4 ql = sm.q_lo[i * 4 + sub][lane];
             const uint32_t al[4] = {ql.x, ql.y, ql.z, ql.w};
             mma16816(s[0][nt], al, b0, b1);
@@ -498,6 +536,9 @@ struct Kernel {
           }
         }
     }
+    unsigned see[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) see[i] = live[i] ? above(node[i], j0) : 0u;
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
@@ -511,7 +552,8 @@ struct Kernel {
       }
     raise<1>(s);
 
-    // p v, the node's v in units of its size
+    // p v, the node's v in units of its size; tokens 2c, 2c + 1, 2c + 8, 2c + 9
+    float4 x[4][VB / 4];
     float unit_v[4], inv_v[4];
     float top_unit = 0.0f;
     unsigned hit = 0;
@@ -519,15 +561,29 @@ struct Kernel {
     for (int j = 0; j < 4; ++j) {
       const int t = (j >> 1) * 8 + 2 * c + (j & 1);
       const long long at = (first + t) * p.v_stride + (long long)h * kv.D;
+#pragma unroll
+      for (int i = 0; i < VB / 4; ++i) {
+        const int e = g * VB + 4 * i;
+        x[j][i] = (t < held && e < kv.D) ? act4(p.v_new, at + e, v_wide) : zero;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int t = (j >> 1) * 8 + 2 * c + (j & 1);
       float top = 0.0f;
-      if (t < held)
-        for (int e = g * VB; e < (g + 1) * VB && e < kv.D; ++e) {
-          const float x = fabsf(act(p.v_new, at + e));
-          if (x < INFINITY)
-            top = fmaxf(top, x);
-          else
-            hit |= 1u << t;
+#pragma unroll
+      for (int i = 0; i < VB / 4; ++i) {
+        float4 &y = x[j][i];
+        top = fmaxf(top, top4(y));
+        const bool all = finite(y.x) && finite(y.y) && finite(y.z) && finite(y.w);
+        if (!all) {
+          hit |= 1u << t;
+          y.x = finite(y.x) ? y.x : 0.0f;
+          y.y = finite(y.y) ? y.y : 0.0f;
+          y.z = finite(y.z) ? y.z : 0.0f;
+          y.w = finite(y.w) ? y.w : 0.0f;
         }
+      }
 #pragma unroll
       for (int d = 4; d <= 16; d <<= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
       const int ex = unit_exponent(top);
@@ -544,35 +600,32 @@ struct Kernel {
     uint32_t a[4], a_lo[4];
     weights(s[0], unit_v, a, a_lo);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      float x[4];
+    for (int i = 0; i < VB / 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int t = (j >> 1) * 8 + 2 * c + (j & 1), e = g * VB + n;
-        x[j] = 0.0f;
-        if (t < held && e < kv.D) {
-          const float y = act(p.v_new, (first + t) * p.v_stride + (long long)h * kv.D + e);
-          if (finite(y)) x[j] = y * inv_v[j];
+      for (int k = 0; k < 4; ++k) {
+        const int n = 4 * i + k;
+        float y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          y[j] = (k == 0 ? x[j][i].x : k == 1 ? x[j][i].y : k == 2 ? x[j][i].z : x[j][i].w) * inv_v[j];
+        const uint32_t b0 = pack_half2(y[0], y[1]), b1 = pack_half2(y[2], y[3]);
+        mma16816(o[n], a, b0, b1);
+        if (kF32) {
+          mma16816(o[n], a_lo, b0, b1);
+          mma16816(o[n], a, low_half2(y[0], y[1], b0), low_half2(y[2], y[3], b1));
         }
       }
-      const uint32_t b0 = pack_half2(x[0], x[1]), b1 = pack_half2(x[2], x[3]);
-      mma16816(o[n], a, b0, b1);
-      if (kF32) {
-        mma16816(o[n], a_lo, b0, b1);
-        mma16816(o[n], a, low_half2(x[0], x[1], b0), low_half2(x[2], x[3], b1));
-      }
-    }
     while (hit) {  // infinities and NaN reach the rows that see their node, no others
       const int t = __ffs(hit) - 1;
       hit &= hit - 1;
-      for (int n = 0; n < NT; ++n)
-        for (int e = 0; e < 4; ++e) {
-          const int d = column(n, e);
-          if (d < kv.D && ((see[e >> 1] >> t) & 1u)) {
-            const float y = act(p.v_new, (first + t) * p.v_stride + (long long)h * kv.D + d);
-            if (!finite(y)) add_to(n, e, y);
-          }
+#pragma unroll 1
+      for (int n = 0; n < 4 * NT; ++n) {
+        const int d = column(n >> 2, n & 3);
+        if (d < kv.D && ((see[(n >> 1) & 1] >> t) & 1u)) {
+          const float y = act(p.v_new, (first + t) * p.v_stride + (long long)h * kv.D + d);
+          if (!finite(y)) add_to(n >> 2, n & 3, y);
         }
+      }
     }
   }
 
@@ -594,11 +647,7 @@ struct Kernel {
   __device__ __forceinline__ int depth_of(int n) const {
     if (!p.parent) return n;
     int depth = 0;
-    for (int a = n; a > 0; ++depth) {
-      const int up = p.parent[(long long)b * p.N + a];
-      if (up < 0 || up >= a) break;
-      a = up;
-    }
+    for (int a = up_from(n); a >= 0; a = up_from(a)) ++depth;
     return depth;
   }
 
@@ -629,39 +678,51 @@ struct Kernel {
       if (__syncthreads_or(wrong)) bad |= SPECDEC_ROW_BAD_TREE;
     }
 
-    // q: rows to fp16 by a power of two each, in operand order
-    for (int r = warp; r < kRows; r += kWarps) {
-      const int row = row0 + r, n = row / p.G;
+    // q: rows to fp16 by a power of two each, in operand order; a lane takes 4
+    // elements of a row (8 of 256), one lane's part of one step
+    constexpr int kPer = DP > 128 ? 2 : 1, kMine = kRows / kWarps;
+    const bool q_wide = wide_rows(p.q, p.q_stride);
+    float4 qx[kMine][kPer];
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int row = row0 + warp + kWarps * i, n = row / p.G;
       const bool in = row < R && n < nodes;
       const long long at = in ? ((long long)b * p.N + n) * p.q_stride +
                                     (long long)(h * p.G + row - n * p.G) * kv.D
                               : 0;
-      float top = 0.0f;
-      for (int e = lane; in && e < kv.D; e += 32) {
-        const float x = fabsf(act(p.q, at + e));
-        if (x < INFINITY) top = fmaxf(top, x);
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        const int e = 4 * (lane + 32 * k);
+        qx[i][k] = (in && e < kv.D) ? act4(p.q, at + e, q_wide) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       }
+    }
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int r = warp + kWarps * i;
+      float top = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) top = fmaxf(top, top4(qx[i][k]));
 #pragma unroll
       for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
       const int ex = unit_exponent(top);
       const float inv = pow2i(-ex);
       if (lane == 0) sm.q_exp[r] = pow2i(ex);
-      // elements 4 w .. 4 w + 3 are one lane's part of one step
-      for (int w = lane; w < DP / 4; w += 32) {
-        float x[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          x[k] = (in && 4 * w < kv.D) ? act(p.q, at + 4 * w + k) * inv : 0.0f;
+      for (int k = 0; k < kPer; ++k) {
+        const int w = lane + 32 * k;
+        if (w >= DP / 4) continue;
+        const float4 x = make_float4(qx[i][k].x * inv, qx[i][k].y * inv, qx[i][k].z * inv,
+                                     qx[i][k].w * inv);
         const int piece = w >> 2, sub = w & 3;           // 16-element piece, step in it
         const int cc = piece & 3, ks = (piece >> 2) * 4 + sub;
         uint32_t *dst = reinterpret_cast<uint32_t *>(&sm.q[ks][(r & 7) * 4 + cc]);
-        const uint32_t x01 = pack_half2(x[0], x[1]), x23 = pack_half2(x[2], x[3]);
+        const uint32_t x01 = pack_half2(x.x, x.y), x23 = pack_half2(x.z, x.w);
         dst[r >> 3] = x01;
         dst[2 + (r >> 3)] = x23;
         if (kF32) {
           dst = reinterpret_cast<uint32_t *>(&sm.q_lo[ks][(r & 7) * 4 + cc]);
-          dst[r >> 3] = low_half2(x[0], x[1], x01);
-          dst[2 + (r >> 3)] = low_half2(x[2], x[3], x23);
+          dst[r >> 3] = low_half2(x.x, x.y, x01);
+          dst[2 + (r >> 3)] = low_half2(x.z, x.w, x23);
         }
       }
     }
@@ -673,8 +734,8 @@ struct Kernel {
       const int r = g + 8 * i, row = row0 + r;
       node[i] = row / p.G;
       live[i] = row < R && node[i] < nodes;
-      pos[i] = len + (live[i] ? depth_of(node[i]) : 0);
-      rf[i] = p.scale * sm.q_exp[r];
+      pos[i] = len + (live[i] && (p.slopes || p.window > 0) ? depth_of(node[i]) : 0);
+      rf[i] = (kPlain ? p.scale * kLog2e : p.scale) * sm.q_exp[r];
       slope[i] = (p.slopes && live[i]) ? p.slopes[h * p.G + row - node[i] * p.G] : 0.0f;
       m[i] = -INFINITY;
       l[i] = 0.0f;
@@ -685,17 +746,19 @@ struct Kernel {
       for (int e = 0; e < 4; ++e) o[j][e] = 0.0f;
 
     if (nodes > 0) {
-      // the split's share of the tokens that the window leaves
+      // the split's share of the granules: those of the tokens that the window
+      // leaves, then the drafted ones
       int from = p.window > 0 ? max(0, len - p.window + 1) : 0;
       from = from / kGran * kGran;
-      const int unit = kGran * kWarps;
-      const int share = ((len - from + p.splits - 1) / p.splits + unit - 1) / unit * unit;
-      const int lo = (int)min((long long)len, from + (long long)split * share);
-      const int hi = (int)min((long long)len, lo + (long long)share);
-      if (lo < hi && !cached(lo, hi)) bad |= SPECDEC_ROW_BAD_CACHE;
-      // drafted tokens: the last split's, that has the fewest cached ones
-      if (split == p.splits - 1)
-        for (int j0 = kGran * warp; j0 < nodes; j0 += kGran * kWarps) drafted(j0);
+      const int cached_n = (len - from + kGran - 1) / kGran, all_n = cached_n + (nodes + kGran - 1) / kGran;
+      const int share = (all_n + p.splits - 1) / p.splits;
+      const int g0 = min(all_n, split * share), g1 = min(all_n, g0 + share);
+      const int c1 = min(g1, cached_n);
+      if (g0 < c1 && !cached(from + g0 * kGran, min(len, from + c1 * kGran)))
+        bad |= SPECDEC_ROW_BAD_CACHE;
+      // drafted ones go on where the cached ones leave the warps
+      for (int i = max(g0, cached_n); i < g1; ++i)
+        if ((i - g0) % kWarps == warp) drafted((i - cached_n) * kGran);
     }
 
     // quads hold parts of l; rows past the request's nodes took part unmasked
@@ -756,48 +819,87 @@ struct Kernel {
       }
       __syncthreads();
     }
-    if (warp != 0) return;
-
-    if (p.splits > 1) {
-      float *part = p.part + ((((long long)b * kv.Hkv + h) * p.row_tiles + tile) * p.splits +
-                              split) * partial_floats(kv.D);
-      if (c == 0) {
+    if (warp == 0) {  // the CTA's sums
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sm.o[0][g + 8 * (e >> 1)][column(j, e)] = o[j][e];
+      if (c == 0)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          part[g + 8 * i] = all[i];
-          part[kRows + g + 8 * i] = bad ? -(float)bad : sum[i];
+          sm.all_m[g + 8 * i] = all[i];
+          sm.all_l[g + 8 * i] = sum[i];
         }
+      if (lane == 0) sm.all_bad = bad;
+    }
+    __syncwarp();
+    const bool joined = p.splits > 1 && p.clustered;
+    if (joined) {
+      asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                       : "memory");
+    } else {
+      __syncthreads();
+    }
+    if (p.splits > 1 && !p.clustered) {
+      float *part = p.part + ((((long long)b * kv.Hkv + h) * p.row_tiles + tile) * p.splits + split) *
+                                 partial_floats(kv.D);
+      for (int i = threadIdx.x; i < kRows * kv.D; i += kThreads)
+        part[2 * kRows + i] = sm.o[0][i / kv.D][i % kv.D];
+      if (threadIdx.x < kRows) {
+        part[threadIdx.x] = sm.all_m[threadIdx.x];
+        part[kRows + threadIdx.x] = bad ? -(float)bad : sm.all_l[threadIdx.x];
       }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            const int d = column(j, k);
-            if (d < kv.D) part[2 * kRows + (g + 8 * i) * kv.D + d] = o[j][2 * i + k];
-          }
       return;
     }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int row = row0 + g + 8 * i;
-      if (row >= R) continue;
+    // rows of this CTA: all of them, or its share of the cluster's
+    const int parts = joined ? p.splits : 1, per = kRows / parts, r0 = joined ? split * per : 0;
+    if (joined) {
+      bad = 0;
+      for (int s = 0; s < parts; ++s) bad |= __float_as_int(remote(reinterpret_cast<float *>(&sm.all_bad), s));
+    }
+    for (int i = warp; i < per; i += kWarps) {
+      const int r = r0 + i, row = row0 + r;
+      if (row >= R) break;
       const int n = row / p.G;
       const long long at = ((long long)b * p.N + n) * p.Hq + h * p.G + row - n * p.G;
-      const bool empty = bad || !live[i] || all[i] == -INFINITY;
-      const float inv = empty ? 0.0f : 1.0f / sum[i];
+      float f[8], top = -INFINITY, total = 0.0f;
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
+      for (int s = 0; s < 8; ++s) {
+        f[s] = s < parts ? (joined ? remote(&sm.all_m[r], s) : sm.all_m[r]) : -INFINITY;
+        top = fmaxf(top, f[s]);
+      }
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const int d = column(j, k);
-          if (d < kv.D) store_out(at * kv.D + d, empty ? 0.0f : o[j][2 * i + k] * inv);
-        }
-      if (c == 0 && p.lse)
-        p.lse[at] = empty ? -INFINITY : (all[i] - kLift + log2f(sum[i])) * 0.6931471805599453f;
+      for (int s = 0; s < 8; ++s) {
+        f[s] = f[s] > -INFINITY ? ex2_approx(f[s] - top) : 0.0f;
+        if (s < parts && f[s] > 0.0f) total += f[s] * (joined ? remote(&sm.all_l[r], s) : sm.all_l[r]);
+      }
+      const bool empty = bad || n >= nodes || top == -INFINITY;
+      const float inv = empty ? 0.0f : 1.0f / total;
+      for (int d = lane; d < kv.D; d += 32) {
+        float x = 0.0f;
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+          if (s < parts && f[s] != 0.0f) x += f[s] * (joined ? remote(&sm.o[0][r][d], s) : sm.o[0][r][d]);
+        store_out(at * kv.D + d, empty ? 0.0f : x * inv);
+      }
+      if (lane == 0 && p.lse)
+        p.lse[at] = empty ? -INFINITY : (top - kLift + log2f(total)) * 0.6931471805599453f;
     }
-    if (tile == 0 && h == 0 && lane == 0) p.row_status[b] = bad;
+    if (tile == 0 && h == 0 && r0 == 0 && threadIdx.x == 0) p.row_status[b] = bad;
+    __syncwarp();
+    if (joined)  // no CTA leaves while another reads its shared memory
+      asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                       : "memory");
+  }
+
+  // A float of CTA `rank` of the cluster at this CTA's address `x`.
+  __device__ __forceinline__ float remote(const float *x, int rank) const {
+    float r;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                 : "=f"(r)
+                 : "r"(cluster_addr(smem_addr(x), (uint32_t)rank))
+                 : "memory");
+    return r;
   }
 
   __device__ __forceinline__ void store_out(long long i, float x) const {
@@ -808,12 +910,12 @@ struct Kernel {
   }
 };
 
-template <int DP, bool kF32>
+template <int DP, bool kF32, bool kPlain>
 __global__ void __launch_bounds__(kThreads) attend_stream_kernel(const AttendParams p) {
   extern __shared__ __align__(16) uint8_t raw[];
   pdl_wait();
   pdl_launch_dependents();
-  using K = Kernel<DP, kF32>;
+  using K = Kernel<DP, kF32, kPlain>;
   K k(p, *reinterpret_cast<typename K::Smem *>(raw));
   k.run();
 }
@@ -887,50 +989,85 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams p) 
 
 int row_tiles_of(int N, int G) { return (N * G + kRows - 1) / kRows; }
 
-// Splits of the tokens: as many as give the device's SMs a few CTAs each.  A
-// function of the sizes alone, so that the workspace is too.
-int splits_of(long long B, int N, int Hkv, int G) {
+// Splits of the tokens: as many as give the device's SMs a few CTAs each; the
+// most for any length, which sizes the workspace ...
+int most_splits(long long B, int N, int Hkv, int G) {
   const long long ctas = B * Hkv * row_tiles_of(N, G);
   const long long s = 608 / ctas;  // 4 for each of 152 SMs
   return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
 }
-
-template <int DP, bool kF32>
-cudaError_t launch_stream(const AttendParams &p, cudaStream_t stream) {
-  static DeviceOnce once;
-  const int smem = (int)sizeof(typename Kernel<DP, kF32>::Smem);
-  const cudaError_t err = smem_opt_in_once(once, attend_stream_kernel<DP, kF32>, smem);
-  if (err != cudaSuccess) return err;
-  return launch_pdl(attend_stream_kernel<DP, kF32>,
-                    dim3((unsigned)(p.splits * p.row_tiles * p.B * p.cache.Hkv)),
-                    dim3(kThreads), (size_t)smem, stream, p);
+// ... and no more than leave each warp a granule where the cache is full; up to
+// eight as a power of two, which a cluster joins.
+int splits_of(const AttendParams &p) {
+  const int most = most_splits(p.B, p.N, p.cache.Hkv, p.G);
+  long long tokens = (long long)p.cache.max_blocks * p.cache.block;
+  if (p.window > 0 && tokens > p.window + kGran) tokens = p.window + kGran;
+  const long long granules = (tokens + kGran - 1) / kGran + (p.N + kGran - 1) / kGran;
+  const long long useful = (granules + kWarps - 1) / kWarps;
+  const long long s = useful < most ? useful : most;
+  if (s >= 24) return (int)s;  // 8 would leave warps three times the work
+  return s >= 8 ? 8 : s >= 4 ? 4 : s >= 2 ? 2 : 1;
 }
 
-template <bool kF32>
+template <int DP, bool kF32, bool kPlain>
+cudaError_t launch_stream(const AttendParams &p, cudaStream_t stream) {
+  static DeviceOnce once;
+  const int smem = (int)sizeof(typename Kernel<DP, kF32, kPlain>::Smem);
+  const cudaError_t err = smem_opt_in_once(once, attend_stream_kernel<DP, kF32, kPlain>, smem);
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.splits * p.row_tiles * p.B * p.cache.Hkv));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)p.splits;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.clustered && p.splits > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, attend_stream_kernel<DP, kF32, kPlain>, p);
+}
+
+// bfloat16 calls that the streaming kernel takes: few rows over few tokens.
+bool stream_is_quicker(const AttendParams &p) {
+  return p.stream_mode == 1;
+}
+
+template <bool kF32, bool kPlain>
 cudaError_t launch_type(const AttendParams &p, cudaStream_t stream) {
-  if (p.cache.D <= 64) return launch_stream<64, kF32>(p, stream);
-  if (p.cache.D <= 128) return launch_stream<128, kF32>(p, stream);
-  return launch_stream<256, kF32>(p, stream);
+  if (p.cache.D <= 64) return launch_stream<64, kF32, kPlain>(p, stream);
+  if (p.cache.D <= 128) return launch_stream<128, kF32, kPlain>(p, stream);
+  return launch_stream<256, kF32, kPlain>(p, stream);
 }
 
 }  // namespace
 
 size_t attend_workspace_bytes(long long B, int N, int Hq, int Hkv, int D, int dtype) {
-  const int G = Hq / Hkv, s = splits_of(B, N, Hkv, G);
+  const int G = Hq / Hkv, s = most_splits(B, N, Hkv, G);
   const size_t stream =
-      s == 1 ? 0 : (size_t)B * Hkv * row_tiles_of(N, G) * s * partial_floats(D) * sizeof(float);
+      s <= 8 ? 0 : (size_t)B * Hkv * row_tiles_of(N, G) * s * partial_floats(D) * sizeof(float);
   // which kernel a call takes depends on the pool too, which the sizes here do not name
   const size_t tile = dtype == SPECDEC_BF16 && D <= 128 ? attend_tile_workspace_bytes(N, G, D) : 0;
   return stream > tile ? stream : tile;
 }
 
 cudaError_t launch_attend(AttendParams p, cudaStream_t stream) {
-  if (attend_tile_applies(p)) return launch_attend_tile(p, stream);
-  p.splits = splits_of(p.B, p.N, p.cache.Hkv, p.G);
   p.row_tiles = row_tiles_of(p.N, p.G);
-  cudaError_t err = p.dtype == SPECDEC_F32 ? launch_type<true>(p, stream)
-                                           : launch_type<false>(p, stream);
-  if (err != cudaSuccess || p.splits == 1) return err;
+  p.splits = splits_of(p);
+  p.clustered = p.splits <= 8;
+  p.block_shift = -1;
+  for (int i = 4; i < 12; ++i)
+    if (p.cache.block == 1 << i) p.block_shift = i;
+  if (attend_tile_applies(p) && !stream_is_quicker(p)) return launch_attend_tile(p, stream);
+  const bool plain = p.softcap == 0.0f && !p.slopes;
+  cudaError_t err =
+      p.dtype == SPECDEC_F32
+          ? (plain ? launch_type<true, true>(p, stream) : launch_type<true, false>(p, stream))
+          : (plain ? launch_type<false, true>(p, stream) : launch_type<false, false>(p, stream));
+  if (err != cudaSuccess || p.clustered) return err;
   const long long rows = (long long)p.B * p.N * p.Hq;
   return launch_pdl(attend_join_kernel, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, stream, p);
 }

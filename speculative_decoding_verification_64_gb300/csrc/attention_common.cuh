@@ -43,6 +43,9 @@ struct AttendParams {
   int32_t *row_status;
   float *part;  // split partials in the workspace
   int splits, row_tiles;
+  bool clustered;   // the splits are one cluster
+  int block_shift;  // log2(cache.block), or -1
+  int stream_mode;
 };
 
 cudaError_t launch_rope(const RopeParams &p, cudaStream_t stream);
