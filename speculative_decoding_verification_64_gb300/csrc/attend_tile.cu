@@ -70,7 +70,7 @@ struct Cfg {
   static constexpr int kThreads = 32 * (kFirst + 4 * kGroups);
   // most columns of a softmax thread (40 and their scores fit its registers, 48 do not)
   static constexpr int kCols = RN == 48 ? 40 : RN / kGroups;
-  static constexpr bool kHold = RN <= 48;              // its scores stay in registers
+  static constexpr bool kHold = RN != 64;              // its scores stay in registers
   static constexpr int kK = RN <= 64 ? 1 : 2;          // stages of K codes (free once scores are made)
   static constexpr int kV = RN <= 48 ? 3 : 2;          // half tiles of V codes (free once widened)
   static constexpr int kBuf = RN <= 64 ? 1 : 2;        // buffers of widened V, and of P^T
@@ -113,11 +113,12 @@ struct Smem {
   float2 boxes[8][8];                     // k and v scales of a tile's pieces
   float2 unit[2][kTok];                   // drafted tiles: per token (k below 0: it is not finite)
   alignas(16) uint32_t see[2][4][RN];     // drafted tiles: bits of the nodes that a row sees
-  // of the segment's rows
-  alignas(16) float rf[4][RN];            // what turns a score into base-2 units
-  float slope[4][RN];
-  int pos[4][RN];
-  uint8_t node[4][RN];
+  // of the rows of three segments (q is staged for the next while the results of
+  // the one before may still be written)
+  alignas(16) float rf[3][RN];            // what turns a product into base-2 units
+  alignas(16) float slope[3][RN], lag[3][RN];  // bias by distance: slope, slope * (pos - len)
+  int pos[3][RN];
+  uint8_t node[3][RN];
   // per softmax group, by column
   alignas(16) float nm[C::kGroups][C::kCols];      // kLift - m
   alignas(16) float fac[C::kGroups][2][C::kCols];  // factors of l and O when m or the unit moves
@@ -246,6 +247,12 @@ __device__ __forceinline__ void store_global32(bool here, unsigned long long at,
                    (uint32_t)here),
                "l"(at), "f"(x)
                : "memory");
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 using f2 = unsigned long long;  // two float32 values in one register pair
@@ -545,6 +552,11 @@ struct Tile {
         warp(threadIdx.x >> 5), box_shift(box_ == 128 ? 7 : box_ == 64 ? 6 : box_ == 32 ? 5 : 4),
         g_magic((uint32_t)(0xFFFFFFFFu / (uint32_t)p_.G) + 1u) {
     columns = (min(RN, p.N * p.G) + 15) / 16 * 16;
+    if (!kPlain) {
+      cap_in = p.softcap > 0.0f ? 2.0f / p.softcap : 0.0f;
+      cap_at = p.softcap * kLog2e;
+      cap_out = -2.0f * cap_at;
+    }
   }
 
   // Bounded wait of a whole warp; false when it, or another, gave up.
@@ -823,7 +835,7 @@ struct Tile {
 
   __device__ __forceinline__ void stage_q(uint32_t index, int worker) {
     const Segment &w = sm.seg[index & 7];
-    const int D = p.cache.D, ring = index & 3, e = (lane & 15) * 8;
+    const int D = p.cache.D, ring = index % 3, e = (lane & 15) * 8;
     const int nodes = w.r.nodes, row0 = w.rt * RN;
     const bool wide = ((reinterpret_cast<uintptr_t>(p.q) | (uintptr_t)(p.q_stride * 2)) & 15) == 0;
     const long long first = (long long)w.b * p.N;
@@ -860,8 +872,11 @@ struct Tile {
         sm.node[ring][col] = (uint8_t)(n - node_of(row0));
         sm.rf[ring][col] = in ? p.scale * kLog2e * sm.rf[ring][col] : 0.0f;
         sm.pos[ring][col] = in ? w.r.len + ((p.window > 0 || p.slopes) ? depth_of(w.b, n) : 0) : -1;
-        if (!kPlain)
-          sm.slope[ring][col] = (in && p.slopes) ? p.slopes[w.h * p.G + row - n * p.G] * kLog2e : 0.0f;
+        if (!kPlain) {
+          const float slope = (in && p.slopes) ? p.slopes[w.h * p.G + row - n * p.G] * kLog2e : 0.0f;
+          sm.slope[ring][col] = slope;
+          sm.lag[ring][col] = slope * (float)(sm.pos[ring][col] - w.r.len);
+        }
       }
     }
     fence_async_smem();
@@ -1065,16 +1080,13 @@ struct Tile {
     return ok;
   }
 
-  __device__ __forceinline__ float bent(float y, int ring, int col, int token_pos) const {
-    if (p.softcap > 0.0f) {
-      // 1 - 2 / (1 + e^2u): absolute error below 2^-22
-      const float cap = p.softcap * kLog2e;
-      const float u = __fdividef(y, p.softcap);  // = 2u log2(e) / 2 of the natural argument
-      y = cap * (1.0f - __fdividef(2.0f, 1.0f + ex2_approx(2.0f * u)));
-    }
-    if (p.slopes) y -= sm.slope[ring][col] * (float)(sm.pos[ring][col] - token_pos);
-    return y;
+  // The cap: y to cap tanh(y / cap), both in base-2 units; 1 - 2 / (1 + e^2u) for
+  // tanh(u), absolute error below 2^-22.
+  __device__ __forceinline__ float capped(float y) const {
+    const float e = ex2_approx(y * cap_in);
+    return fmaf(cap_out, rcp_approx(1.0f + e), cap_at);
   }
+  float cap_in, cap_out, cap_at;  // 2 / softcap, -2 and 1 times softcap log2(e)
 
   // Scores of a tile that needs more than a factor, in place: bent, biased and
   // masked, in base-2 units.  tok: the thread's token; unit: its k's.
@@ -1091,7 +1103,8 @@ struct Tile {
       tmem_stored();
       return;
     }
-    const int position = !drafted ? at : (!kPlain && p.slopes && exists) ? w.r.len + depth_of(w.b, j) : 0;
+    const float position =  // of the token, from the length
+        kPlain ? 0.0f : (float)(!drafted ? at - w.r.len : p.slopes && exists ? depth_of(w.b, j) : 0);
     __syncwarp();
     if (__any_sync(kAll, special))  // k is not finite: its products term by term
 #pragma unroll 1
@@ -1118,7 +1131,11 @@ struct Tile {
         else if (window > 0)
           seen = seen && sm.pos[ring][col] - at < window;
         float y = s[k] * (unit * sm.rf[ring][col]);
-        if (!kPlain) y = bent(y, ring, col, position);
+        if (!kPlain) {
+          if (cap_in > 0.0f) y = capped(y);
+          // (position - len) - (pos - len), each exact
+          y = fmaf(sm.slope[ring][col], position, y - sm.lag[ring][col]);
+        }
         s[k] = seen ? y : -INFINITY;
       }
       tmem_store8(s_at + ch * 8, s);
@@ -1166,7 +1183,7 @@ struct Tile {
 #pragma unroll 1
     for (uint32_t index = 0; ok && segment(index, ok); ++index) {
       const Segment &w = sm.seg[index & 7];
-      const int ring = index & 3, t0 = w.t0, t1 = w.t1;
+      const int ring = index % 3, t0 = w.t0, t1 = w.t1;
       float vref = 0.0f;
 #pragma unroll
       for (int i = 0; i < kCols / 2; ++i) l[i] = 0ull;
@@ -1182,12 +1199,16 @@ struct Tile {
         // a plain tile's scores are a factor away; the others are written back
         const int past = drafted ? (t + 1) * kTok - w.r.nodes
                                  : w.r.from + (t - w.r.drafted + 1) * kTok - w.r.len;
-        const bool kept = !kPlain || drafted || past > 0 || partly_hidden(p, w.r, t);
+        const bool kept =
+            drafted || past > 0 || partly_hidden(p, w.r, t) || (!kPlain && !kHold);
         if (kept) bend(w, ring, t, c, drafted, unit.x, tok, c0, mine, s_at);
         const float v_unit = past + tok < kTok ? unit.y : 0.0f;
         const float k_unit = kept ? 1.0f : unit.x;
         const f2 ks = pair(k_unit, k_unit);
         const float *factor = kept ? sm.ones : sm.rf[ring] + c0;
+        const bool cap = !kPlain && !kept && cap_in > 0.0f, bias = !kPlain && !kept && p.slopes;
+        const float away = (float)(tok - (kTok - past));  // the token's position, from the length
+        const f2 away2 = pair(away, away);
         float x[kHold ? kCols : 8];
         // Passes over the scores: 0 under the present maxima, with a vote; where
         // they have to move, 1 for the tile's own (columns without any at 0), and
@@ -1232,8 +1253,25 @@ struct Tile {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               float *y = s + 4 * k;
-              unpair(fma2(pair(y[0], y[1]), mul2(r[k].x, ks), n[k].x), y[0], y[1]);
-              unpair(fma2(pair(y[2], y[3]), mul2(r[k].y, ks), n[k].y), y[2], y[3]);
+              if (!kPlain && cap) {
+                unpair(mul2(pair(y[0], y[1]), mul2(r[k].x, ks)), y[0], y[1]);
+                unpair(mul2(pair(y[2], y[3]), mul2(r[k].y, ks)), y[2], y[3]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[i] = capped(y[i]);
+                unpair(add2(pair(y[0], y[1]), n[k].x), y[0], y[1]);
+                unpair(add2(pair(y[2], y[3]), n[k].y), y[2], y[3]);
+              } else {
+                unpair(fma2(pair(y[0], y[1]), mul2(r[k].x, ks), n[k].x), y[0], y[1]);
+                unpair(fma2(pair(y[2], y[3]), mul2(r[k].y, ks), n[k].y), y[2], y[3]);
+              }
+              if (!kPlain && bias) {
+                const int at = ch * 8 + 4 * k;
+                const ulonglong2 sl = *reinterpret_cast<const ulonglong2 *>(&sm.slope[ring][c0 + at]);
+                const ulonglong2 lg = *reinterpret_cast<const ulonglong2 *>(&sm.lag[ring][c0 + at]);
+                const f2 minus1 = pair(-1.0f, -1.0f);
+                unpair(add2(pair(y[0], y[1]), fma2(sl.x, away2, mul2(lg.x, minus1))), y[0], y[1]);
+                unpair(add2(pair(y[2], y[3]), fma2(sl.y, away2, mul2(lg.y, minus1))), y[2], y[3]);
+              }
               top = fmaxf(fmaxf(top, fmaxf(y[0], y[1])), fmaxf(y[2], y[3]));
             }
           }
