@@ -60,17 +60,8 @@ struct Cfg {
   static constexpr int kGroups = RN <= 64 ? 1 : 2;     // softmax groups of four warps: a part of the rows each
   static constexpr int kWorkers = 4;                   // warps that widen V: one on each quarter of the SM
   static constexpr int kFirst = 8;                     // first softmax warp
-  // Registers a thread: of the launch (what two CTAs, or one, leave room for), and
-  // of the three kinds of warpgroup, which share out those of the launch:
-  // kIssue + kWiden + kGroups kSoft = (2 + kGroups) kRegs
-  static constexpr int kRegs = RN <= 64 ? 80 : 128;
-  static constexpr int kIssue = RN <= 64 ? 64 : 72, kWiden = RN <= 64 ? 48 : 88;
-  static constexpr int kSoft = RN <= 64 ? 128 : 176;
-  static_assert(kIssue + kWiden + kGroups * kSoft == (2 + kGroups) * kRegs, "");
   static constexpr int kThreads = 32 * (kFirst + 4 * kGroups);
-  // most columns of a softmax thread (40 and their scores fit its registers, 48 do not)
-  static constexpr int kCols = RN == 48 ? 40 : RN / kGroups;
-  static constexpr bool kHold = RN != 64;              // its scores stay in registers
+  static constexpr int kCols = RN / kGroups;           // most columns of a softmax thread
   static constexpr int kK = RN <= 64 ? 1 : 2;          // stages of K codes (free once scores are made)
   static constexpr int kV = RN <= 48 ? 3 : 2;          // half tiles of V codes (free once widened)
   static constexpr int kBuf = RN <= 64 ? 1 : 2;        // buffers of widened V, and of P^T
@@ -621,11 +612,16 @@ struct Tile {
     note.tiles = note.first = note.head = note.open = 0;
     Walk walk(p, box, plan);
     Segment w, ahead;
-    bool ok = true, more = publish(walk, 0, ahead);
+    bool ok = true, more = true;
+    // each segment is published one ahead, so that the others prepare it
 #pragma unroll 1
-    for (; ok && more; ++index) {
+    for (;; ++index) {
       w = ahead;
-      more = publish(walk, index + 1, ahead);  // the others prepare the next one
+      const bool have = index > 0 && more;
+      if (more) more = publish(walk, index, ahead);
+      if (index == 0) continue;
+      if (!have) break;
+      if (!ok) continue;  // after giving up: only the notes go on
       Piece next = piece_of(w, w.t0);
 #pragma unroll 1
       for (int t = w.t0; t < w.t1; ++t, ++c) {
@@ -635,7 +631,7 @@ struct Tile {
         const bool cached = t >= w.r.drafted;
         if (x.id < 0 || x.id >= kv.n_blocks) {
           x.id = 0;
-          sm.bad[index & 7] = SPECDEC_ROW_BAD_CACHE;
+          sm.bad[(index - 1) & 7] = SPECDEC_ROW_BAD_CACHE;
         }
         const long long cell = (long long)x.id * kv.Hkv + w.h;
         const int row = (int)(cell * kv.block + x.tok % kv.block);
@@ -672,9 +668,6 @@ struct Tile {
     // copies in flight get time to land before the CTA may leave.
     copied = c;
     copied_v = v;
-#pragma unroll 1
-    while (take(walk, w)) {
-    }
     if (lane == 0) notes_of(p.part, RN, kv.D)[blockIdx.x] = note;
   }
 
@@ -716,13 +709,18 @@ struct Tile {
     __syncwarp();
   }
 
+  // O^T += V^T P^T of tile c, as soon as both are there.
   __device__ __forceinline__ bool outputs(uint32_t c, bool first) {
-    if (!wait(&sm.vh_full[c % kBuf], full_par(c, kBuf)) ||
-        !wait(&sm.p_full[c % kBuf], full_par(c, kBuf)))
+    return outputs_of(sm, sm_tmem + 2 * RN, columns, c, first);
+  }
+  static __device__ __noinline__ bool outputs_of(S &sm, uint32_t d, int columns, uint32_t c,
+                                                 bool first) {
+    const uint32_t give_up = smem_addr(&sm.give_up);
+    if (!__all_sync(kAll, wait_lane(smem_addr(&sm.vh_full[c % kBuf]), full_par(c, kBuf), give_up) &&
+                              wait_lane(smem_addr(&sm.p_full[c % kBuf]), full_par(c, kBuf), give_up)))
       return false;
     fence_after();
     if (elected()) {
-      const uint32_t d = sm_tmem + 2 * RN;
       const uint32_t idesc = shape(columns, true);
       const uint64_t va = operand(smem_addr(sm.vh[c % kBuf][0]), 1024, kTileBytes);
       const uint64_t pb = operand(smem_addr(sm.pt[c % kBuf][0]), 1024, kTileBytes);
@@ -1088,25 +1086,28 @@ struct Tile {
   }
   float cap_in, cap_out, cap_at;  // 2 / softcap, -2 and 1 times softcap log2(e)
 
-  // Scores of a tile that needs more than a factor, in place: bent, biased and
-  // masked, in base-2 units.  tok: the thread's token; unit: its k's.
-  __device__ __forceinline__ void bend(const Segment &w, int ring, int t, uint32_t c, bool drafted,
-                                       float unit, int tok, int c0, int mine, uint32_t s_at) {
+  // Scores of a tile that needs more than a factor, in place: capped, biased and
+  // masked, in base-2 units.  Returns the thread's largest under the present
+  // maxima.  tok: the thread's token; unit: its k's.
+  __device__ __forceinline__ float bend(const Segment &w, int ring, int t, uint32_t c, bool drafted,
+                                        bool hidden, float unit, int tok, int c0, int mine,
+                                        uint32_t s_at, const float *nms) {
     const int at = w.r.from + (t - w.r.drafted) * kTok + tok, j = t * kTok + tok;
     const bool exists = drafted ? j < w.r.nodes : at < w.r.len, special = drafted && unit < 0.0f;
-    const int quarter = tok >> 5, window = drafted ? 0 : p.window;
+    const int quarter = tok >> 5, window = hidden ? p.window : 0;
+    float top = -INFINITY;
     if (!__any_sync(kAll, exists)) {  // a warp past the last token
-      const float hidden[8] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY,
-                               -INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      const float none[8] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY,
+                             -INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-      for (int ch = 0; ch * 8 < mine; ++ch) tmem_store8(s_at + ch * 8, hidden);
+      for (int ch = 0; ch < mine; ch += 8) tmem_store8(s_at + ch, none);
       tmem_stored();
-      return;
+      return top;
     }
     const float position =  // of the token, from the length
         kPlain ? 0.0f : (float)(!drafted ? at - w.r.len : p.slopes && exists ? depth_of(w.b, j) : 0);
     __syncwarp();
-    if (__any_sync(kAll, special))  // k is not finite: its products term by term
+    if (__any_sync(kAll, special)) {  // k is not finite: its products term by term
 #pragma unroll 1
       for (int i = 0; i < mine; ++i) {
         float s = tmem_load1(s_at + i);
@@ -1117,30 +1118,52 @@ struct Tile {
         tmem_store1(s_at + i, s);
         tmem_stored();
       }
+    }
 #pragma unroll 1
-    for (int ch = 0; ch * 8 < mine; ++ch) {
+    for (int ch = 0; ch < mine; ch += 8) {
       float s[8];
-      tmem_load8(s_at + ch * 8, s);
+      tmem_load8(s_at + ch, s);
+      const float *rf = &sm.rf[ring][c0 + ch], *nm = nms + ch;
+      uint32_t seen = exists ? 0xFFu : 0u;
+      if (drafted) {
+        uint32_t bits = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          bits |= (sm.see[c & 1][quarter][c0 + ch + k] >> lane & 1u) << k;
+        seen &= bits;
+      } else if (window > 0) {
+        uint32_t bits = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) bits |= (uint32_t)(sm.pos[ring][c0 + ch + k] - at < window) << k;
+        seen &= bits;
+      }
       tmem_wait8(s);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const int col = c0 + ch * 8 + k;
-        bool seen = exists;
-        if (drafted)
-          seen = seen && (sm.see[c & 1][quarter][col] >> lane & 1u);
-        else if (window > 0)
-          seen = seen && sm.pos[ring][col] - at < window;
-        float y = s[k] * (unit * sm.rf[ring][col]);
+        float y = s[k] * (unit * rf[k]);
         if (!kPlain) {
           if (cap_in > 0.0f) y = capped(y);
           // (position - len) - (pos - len), each exact
-          y = fmaf(sm.slope[ring][col], position, y - sm.lag[ring][col]);
+          y = fmaf(sm.slope[ring][c0 + ch + k], position, y - sm.lag[ring][c0 + ch + k]);
         }
-        s[k] = seen ? y : -INFINITY;
+        s[k] = (seen >> k & 1u) ? y : -INFINITY;
+        top = fmaxf(top, s[k] + nm[k]);
       }
-      tmem_store8(s_at + ch * 8, s);
+      tmem_store8(s_at + ch, s);
     }
     tmem_stored();
+    return top;
+  }
+
+  // 8 scores under their columns' maxima: x = s * factor * unit + nm.
+  __device__ __forceinline__ void under(float *s, const float *factor, const float *nm, f2 unit) const {
+#pragma unroll
+    for (int k = 0; k < 8; k += 4) {
+      const ulonglong2 r = *reinterpret_cast<const ulonglong2 *>(factor + k);
+      const ulonglong2 n = *reinterpret_cast<const ulonglong2 *>(nm + k);
+      unpair(fma2(pair(s[k], s[k + 1]), mul2(r.x, unit), n.x), s[k], s[k + 1]);
+      unpair(fma2(pair(s[k + 2], s[k + 3]), mul2(r.y, unit), n.y), s[k + 2], s[k + 3]);
+    }
   }
 
   // Sums, or maxima, of 8 values over a warp's lanes: lane 4 i holds that of value i.
@@ -1162,9 +1185,11 @@ struct Tile {
     return join(x, __shfl_xor_sync(kAll, x, 1));
   }
 
+  // All loops over columns are rolled, 8 at a time, and what a thread keeps per
+  // column (scores, sums) stays in tensor memory: their code, times all roles', has
+  // to stay inside the instruction cache.  (Sums and scores in registers, loops
+  // unrolled: 371 us for the drafted trees of 64 nodes, and 500 with the cap there.)
   __device__ __forceinline__ void softmax() {
-    constexpr bool kHold = C::kHold;
-    constexpr int kCols = C::kCols, kCh = kCols / 8;
     const int group = C::kGroups == 1 ? 0 : (warp - C::kFirst) >> 2;
     const int quarter = warp & 3, tok = quarter * 32 + lane;
     // the group's columns
@@ -1172,11 +1197,10 @@ struct Tile {
     const int c0 = group * mine;
     const bool leader = lane == 0 && quarter == 0;
     const uint32_t lanes = sm.tmem + ((uint32_t)quarter << 21);  // TMEM lanes of this warp
-    const uint32_t o_at = lanes + 2 * RN + c0;
+    const uint32_t o_at = lanes + 2 * RN + c0, l_at = lanes + 3 * RN + c0;
     const specdec_kv_cache &kv = p.cache;
     uint32_t c = 0;  // the tile's number, of all
     group_phase = both_phase = 0;
-    f2 l[kCols / 2];
     float *const nms = sm.nm[group];
     if (tok < mine) nms[tok] = 0.0f;
     bool ok = meet(group);
@@ -1185,8 +1209,6 @@ struct Tile {
       const Segment &w = sm.seg[index & 7];
       const int ring = index % 3, t0 = w.t0, t1 = w.t1;
       float vref = 0.0f;
-#pragma unroll
-      for (int i = 0; i < kCols / 2; ++i) l[i] = 0ull;
       bool unseen = true;  // the thread's column (tok) has seen no score yet
 #pragma unroll 1
       for (int t = t0; t < t1; ++t, ++c) {
@@ -1199,101 +1221,49 @@ struct Tile {
         // a plain tile's scores are a factor away; the others are written back
         const int past = drafted ? (t + 1) * kTok - w.r.nodes
                                  : w.r.from + (t - w.r.drafted + 1) * kTok - w.r.len;
-        const bool kept =
-            drafted || past > 0 || partly_hidden(p, w.r, t) || (!kPlain && !kHold);
-        if (kept) bend(w, ring, t, c, drafted, unit.x, tok, c0, mine, s_at);
+        const bool hidden = !drafted && partly_hidden(p, w.r, t);
+        const bool bent = !kPlain || drafted || past > 0 || hidden;
         const float v_unit = past + tok < kTok ? unit.y : 0.0f;
-        const float k_unit = kept ? 1.0f : unit.x;
+        const float k_unit = bent ? 1.0f : unit.x;
         const f2 ks = pair(k_unit, k_unit);
-        const float *factor = kept ? sm.ones : sm.rf[ring] + c0;
-        const bool cap = !kPlain && !kept && cap_in > 0.0f, bias = !kPlain && !kept && p.slopes;
-        const float away = (float)(tok - (kTok - past));  // the token's position, from the length
-        const f2 away2 = pair(away, away);
-        float x[kHold ? kCols : 8];
-        // Passes over the scores: 0 under the present maxima, with a vote; where
-        // they have to move, 1 for the tile's own (columns without any at 0), and
-        // 2 under the new ones.
-        int pass = first ? 1 : 0;
+        const float *factor = bent ? sm.ones : sm.rf[ring] + c0;
+        float top = -INFINITY;
+        if (bent) {
+          top = bend(w, ring, t, c, drafted, hidden, unit.x, tok, c0, mine, s_at, nms);
+        } else if (!first) {
 #pragma unroll 1
-        for (;;) {
-          // one body for all passes, not a copy each
-          asm volatile("" : "+r"(pass));
-          float top = -INFINITY;
-          if (!kHold && pass == 1) {  // the warp's maxima
-#pragma unroll 1
-            for (int ch = 0; ch * 8 < mine; ++ch) {
-              float y[8];
-              tmem_load8(s_at + ch * 8, y);
-              tmem_wait8(y);
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                y[k] = fmaf(y[k], k_unit * factor[ch * 8 + k], nms[ch * 8 + k]);
-              const float best = over_lanes<true>(y);
-              if ((lane & 3) == 0) sm.red[group][quarter][ch * 8 + (lane >> 2)] = best;
-              __syncwarp();
-            }
-          }
-          if (kHold) {
-#pragma unroll
-            for (int ch = 0; ch < kCh; ++ch)
-              if (ch * 8 < mine) tmem_load8(s_at + ch * 8, x + ch * 8);
-          }
-#pragma unroll
-          for (int ch = 0; ch < kCh; ++ch) {
-            if (ch * 8 >= mine || (!kHold && pass == 1)) continue;
-            float *s = x + (kHold ? ch * 8 : 0);
-            if (!kHold) tmem_load8(s_at + ch * 8, s);
-            ulonglong2 r[2], n[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              r[k] = *reinterpret_cast<const ulonglong2 *>(factor + ch * 8 + 4 * k);
-              n[k] = *reinterpret_cast<const ulonglong2 *>(nms + ch * 8 + 4 * k);
-            }
+          for (int ch = 0; ch < mine; ch += 8) {
+            float s[8];
+            tmem_load8(s_at + ch, s);
             tmem_wait8(s);
+            under(s, factor + ch, nms + ch, ks);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              float *y = s + 4 * k;
-              if (!kPlain && cap) {
-                unpair(mul2(pair(y[0], y[1]), mul2(r[k].x, ks)), y[0], y[1]);
-                unpair(mul2(pair(y[2], y[3]), mul2(r[k].y, ks)), y[2], y[3]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) y[i] = capped(y[i]);
-                unpair(add2(pair(y[0], y[1]), n[k].x), y[0], y[1]);
-                unpair(add2(pair(y[2], y[3]), n[k].y), y[2], y[3]);
-              } else {
-                unpair(fma2(pair(y[0], y[1]), mul2(r[k].x, ks), n[k].x), y[0], y[1]);
-                unpair(fma2(pair(y[2], y[3]), mul2(r[k].y, ks), n[k].y), y[2], y[3]);
-              }
-              if (!kPlain && bias) {
-                const int at = ch * 8 + 4 * k;
-                const ulonglong2 sl = *reinterpret_cast<const ulonglong2 *>(&sm.slope[ring][c0 + at]);
-                const ulonglong2 lg = *reinterpret_cast<const ulonglong2 *>(&sm.lag[ring][c0 + at]);
-                const f2 minus1 = pair(-1.0f, -1.0f);
-                unpair(add2(pair(y[0], y[1]), fma2(sl.x, away2, mul2(lg.x, minus1))), y[0], y[1]);
-                unpair(add2(pair(y[2], y[3]), fma2(sl.y, away2, mul2(lg.y, minus1))), y[2], y[3]);
-              }
-              top = fmaxf(fmaxf(top, fmaxf(y[0], y[1])), fmaxf(y[2], y[3]));
-            }
+            for (int k = 0; k < 8; k += 2) top = fmaxf(top, fmaxf(s[k], s[k + 1]));
           }
-          if (pass == 2) break;
-          if (pass == 0) {
-            // scores far above a maximum, or a larger unit of v: the group moves
-            if (__any_sync(kAll, top > kRaise + kLift || v_unit > vref) && lane == 0)
-              sm.vote[group][c & 3] = 1;
-            if (!(ok = meet(group))) break;
-            if (!*(volatile int *)&sm.vote[group][c & 3]) break;
+        }
+        // Scores far above a maximum, or a larger unit of v, and the group's maxima
+        // move; at a segment's start they are all at 0 and move from there.
+        bool move = first;
+        if (!first) {
+          if (__any_sync(kAll, top > kRaise + kLift || v_unit > vref) && lane == 0)
+            sm.vote[group][c & 3] = 1;
+          if (!(ok = meet(group))) break;
+          move = *(volatile int *)&sm.vote[group][c & 3] != 0;
+          if (move) {
             if (tok < mine && unseen) nms[tok] = 0.0f;
             if (!(ok = meet(group))) break;
-            pass = 1;
-            continue;
           }
-          if (kHold) {
-#pragma unroll
-            for (int ch = 0; ch < kCh; ++ch) {
-              if (ch * 8 >= mine) continue;
-              const float best = over_lanes<true>(x + ch * 8);
-              if ((lane & 3) == 0) sm.red[group][quarter][ch * 8 + (lane >> 2)] = best;
-            }
+        }
+        if (move) {
+#pragma unroll 1
+          for (int ch = 0; ch < mine; ch += 8) {
+            float s[8];
+            tmem_load8(s_at + ch, s);
+            tmem_wait8(s);
+            under(s, factor + ch, nms + ch, ks);
+            const float best = over_lanes<true>(s);
+            if ((lane & 3) == 0) sm.red[group][quarter][ch + (lane >> 2)] = best;
+            __syncwarp();
           }
           const int vmax = __reduce_max_sync(kAll, __float_as_int(v_unit));  // units are >= 0
           if (lane == 0) sm.vred[group][quarter] = __int_as_float(vmax);
@@ -1322,30 +1292,21 @@ struct Tile {
           if (!first && !(ok = wait(&sm.pv_done[(c - 1) % kBuf], full_par(c - 1, kBuf)))) break;
           fence_after();
           if (!(ok = meet(group))) break;
-          if (!first) {
+          if (!first) {  // the sums, then the outputs
 #pragma unroll 1
-            for (int ch = 0; ch * 8 < mine; ++ch) {
+            for (int i = 0; i < 2 * mine; i += 8) {
+              const int ch = i < mine ? i : i - mine;
+              const uint32_t at = i < mine ? l_at + ch : o_at + ch;
+              const float *fac = sm.fac[group][i >= mine] + ch;
               float o[8];
-              tmem_load8(o_at + ch * 8, o);
+              tmem_load8(at, o);
               tmem_wait8(o);
 #pragma unroll
-              for (int k = 0; k < 8; ++k) o[k] *= sm.fac[group][1][ch * 8 + k];
-              tmem_store8(o_at + ch * 8, o);
+              for (int k = 0; k < 8; ++k) o[k] *= fac[k];
+              tmem_store8(at, o);
             }
             tmem_stored();
-#pragma unroll
-            for (int i = 0; i < kCols / 2; ++i)
-              if (2 * i < mine)
-                l[i] = mul2(l[i], *reinterpret_cast<const f2 *>(&sm.fac[group][0][2 * i]));
           }
-          if (!kHold) break;
-          pass = 2;
-        }
-        if (!ok) break;
-        if (kHold) {  // the scores are in registers: the next ones may come
-          fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.s_empty[c & 1]);
         }
         if (leader) sm.vote[group][(c + 2) & 3] = 0;
         // P^T of the tile before in this buffer has been read
@@ -1353,59 +1314,50 @@ struct Tile {
         const float ratio = vref > 0.0f ? __fdividef(v_unit, vref) : 0.0f;
         const f2 r2 = pair(ratio, ratio);
         uint8_t *pt = sm.pt[c % kBuf][0] + tok * kRow;
-#pragma unroll
-        for (int ch = 0; ch < kCh; ++ch) {
-          if (ch * 8 >= mine) continue;
-          float *s = x + (kHold ? ch * 8 : 0);
-          if (!kHold) {
-            tmem_load8(s_at + ch * 8, s);
-            ulonglong2 r[2], n[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              r[k] = *reinterpret_cast<const ulonglong2 *>(factor + ch * 8 + 4 * k);
-              n[k] = *reinterpret_cast<const ulonglong2 *>(nms + ch * 8 + 4 * k);
-            }
-            tmem_wait8(s);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              float *y = s + 4 * k;
-              unpair(fma2(pair(y[0], y[1]), mul2(r[k].x, ks), n[k].x), y[0], y[1]);
-              unpair(fma2(pair(y[2], y[3]), mul2(r[k].y, ks), n[k].y), y[2], y[3]);
-            }
-          }
+#pragma unroll 1
+        for (int ch = 0; ch < mine; ch += 8) {
+          float s[8], l[8];
+          tmem_load8(s_at + ch, s);
+          tmem_load8(l_at + ch, l);
+          tmem_wait8(s);
+          tmem_wait8(l);
+          under(s, factor + ch, nms + ch, ks);
           uint32_t out[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const f2 e = pair(ex2_approx(s[2 * k]), ex2_approx(s[2 * k + 1]));
-            l[ch * 4 + k] = add2(l[ch * 4 + k], e);
+            if (first) l[2 * k] = l[2 * k + 1] = 0.0f;
+            unpair(add2(pair(l[2 * k], l[2 * k + 1]), e), l[2 * k], l[2 * k + 1]);
             float a, b;
             unpair(mul2(e, r2), a, b);
             out[k] = pack_half2(a, b);
           }
-          const int col = c0 + ch * 8;
+          tmem_store8(l_at + ch, l);
+          const int col = c0 + ch;
           *reinterpret_cast<uint4 *>(pt + (col >> 6) * kTileBytes +
                                      ((((col & 63) >> 3) ^ (tok & 7)) << 4)) =
               make_uint4(out[0], out[1], out[2], out[3]);
         }
+        tmem_stored();
         fence_async_smem();
         fence_before();
         __syncwarp();
         if (lane == 0) {
-          if (!kHold) mbar_arrive(&sm.s_empty[c & 1]);
+          mbar_arrive(&sm.s_empty[c & 1]);
           mbar_arrive(&sm.p_full[c % kBuf]);
         }
       }
       if (!ok) break;
 
       // the segment's sums, by column
-#pragma unroll
-      for (int ch = 0; ch < kCh; ++ch) {
-        if (ch * 8 >= mine) continue;
-        float v[8];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) unpair(l[ch * 4 + k], v[2 * k], v[2 * k + 1]);
-        const float sum = over_lanes<false>(v);
-        if ((lane & 3) == 0) sm.red[group][quarter][ch * 8 + (lane >> 2)] = sum;
+#pragma unroll 1
+      for (int ch = 0; ch < mine; ch += 8) {
+        float l[8];
+        tmem_load8(l_at + ch, l);
+        tmem_wait8(l);
+        const float sum = over_lanes<false>(l);
+        if ((lane & 3) == 0) sm.red[group][quarter][ch + (lane >> 2)] = sum;
+        __syncwarp();
       }
       if (!(ok = wait(&sm.pv_done[(c - 1) % kBuf], full_par(c - 1, kBuf)))) break;
       if (!(ok = meet_all())) break;
@@ -1583,16 +1535,13 @@ __global__ void __launch_bounds__(Cfg<RN>::kThreads, Cfg<RN>::kCtas)
   Tile<RN, kPlain> tile(p, sm, &k_map, &v_map, box);
   // warps 0-3: copies, products (two stay idle); 4-7: operands; the others: softmax
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kIssue));
     if (warp == 0)
       tile.copies(plan);
     else if (warp == 1)
       tile.products();
   } else if (warp < C::kFirst) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kWiden));
     tile.operands();
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoft));
     tile.softmax();
   }
   fence_before();
@@ -1732,7 +1681,7 @@ int box_rows(int block) {  // the largest power of two that divides the block an
 
 int rows_of(int N, int G) {  // the classes of the kernel
   const int rows = N * G;
-  return rows <= 32 ? 32 : rows <= 40 ? 48 : rows <= 64 ? 64 : 128;
+  return rows <= 32 ? 32 : rows <= 48 ? 48 : rows <= 64 ? 64 : 128;
 }
 
 template <int RN, bool kPlain>
