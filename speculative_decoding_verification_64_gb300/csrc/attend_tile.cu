@@ -104,12 +104,11 @@ struct Smem {
   float2 boxes[8][8];                     // k and v scales of a tile's pieces
   float2 unit[2][kTok];                   // drafted tiles: per token (k below 0: it is not finite)
   alignas(16) uint32_t see[2][4][RN];     // drafted tiles: bits of the nodes that a row sees
-  // of the rows of three segments (q is staged for the next while the results of
-  // the one before may still be written)
-  alignas(16) float rf[3][RN];            // what turns a product into base-2 units
-  alignas(16) float slope[3][RN], lag[3][RN];  // bias by distance: slope, slope * (pos - len)
-  int pos[3][RN];
-  uint8_t node[3][RN];
+  // of the rows of four segments: the next one's are staged while the results of the
+  // one three before may still be written
+  alignas(16) float rf[4][RN];            // what turns a product into base-2 units
+  float slope[4][RN], depth[4][RN];       // of the bias by distance; position from the length
+  uint8_t node[4][RN];
   // per softmax group, by column
   alignas(16) float nm[C::kGroups][C::kCols];      // kLift - m
   alignas(16) float fac[C::kGroups][2][C::kCols];  // factors of l and O when m or the unit moves
@@ -126,7 +125,7 @@ struct Smem {
   uint32_t tmem;
   int give_up;
   int done[C::kGroups];                   // segments that a softmax group finished
-  long long scan[16];
+  long long scan[16];                     // of the plan: one a warp
   Plan plan;
 };
 
@@ -638,10 +637,15 @@ struct Tile {
         const uint32_t bytes = (uint32_t)__popc(__ballot_sync(kAll, x.mine)) * box * kRow;
         float2 unit = make_float2(0.0f, 0.0f);
         if (x.mine) unit = make_float2(__ldg(kv.k_scale + cell), __ldg(kv.v_scale + cell));
-        // drafted tiles have nothing to copy, but a phase missed here would make
-        // the slot's next wait take an old phase of the same parity for its own
         if (!(ok = wait(&sm.k_empty[ks], empty_par(c, kK)))) break;
-        if (!cached) continue;
+        // Drafted tiles have nothing to copy, but their products wait for this
+        // arrival: were they done before the wait above looks, it would miss their
+        // phase and take the next one of the same parity for it.
+        if (!cached) {
+          if (lane == 0) mbar_arrive(&sm.k_full[ks]);
+          __syncwarp();
+          continue;
+        }
         if (lane == 0) mbar_arrive_expect_tx(&sm.k_full[ks], bytes);
         __syncwarp();
         if (x.mine) {
@@ -754,11 +758,7 @@ struct Tile {
         }
         if (first && !(ok = wait(&sm.q_full, index & 1))) break;
         if (!(ok = wait(&sm.box_full[c & 7], (c >> 3) & 1))) break;
-        if (drafted) {
-          if (lane == 0) mbar_arrive(&sm.k_full[c % kK]);  // nobody copies into its slot
-        } else if (!(ok = wait(&sm.k_full[c % kK], full_par(c, kK)))) {
-          break;
-        }
+        if (!(ok = wait(&sm.k_full[c % kK], full_par(c, kK)))) break;
         if (!(ok = wait(&sm.s_empty[c & 1], ((c >> 1) & 1) ^ 1))) break;
         fence_after();
         scores(c, drafted, t == t1 - 1);
@@ -833,7 +833,7 @@ struct Tile {
 
   __device__ __forceinline__ void stage_q(uint32_t index, int worker) {
     const Segment &w = sm.seg[index & 7];
-    const int D = p.cache.D, ring = index % 3, e = (lane & 15) * 8;
+    const int D = p.cache.D, ring = index & 3, e = (lane & 15) * 8;
     const int nodes = w.r.nodes, row0 = w.rt * RN;
     const bool wide = ((reinterpret_cast<uintptr_t>(p.q) | (uintptr_t)(p.q_stride * 2)) & 15) == 0;
     const long long first = (long long)w.b * p.N;
@@ -869,12 +869,10 @@ struct Tile {
         const bool in = row < p.N * p.G && n < nodes;
         sm.node[ring][col] = (uint8_t)(n - node_of(row0));
         sm.rf[ring][col] = in ? p.scale * kLog2e * sm.rf[ring][col] : 0.0f;
-        sm.pos[ring][col] = in ? w.r.len + ((p.window > 0 || p.slopes) ? depth_of(w.b, n) : 0) : -1;
-        if (!kPlain) {
-          const float slope = (in && p.slopes) ? p.slopes[w.h * p.G + row - n * p.G] * kLog2e : 0.0f;
-          sm.slope[ring][col] = slope;
-          sm.lag[ring][col] = slope * (float)(sm.pos[ring][col] - w.r.len);
-        }
+        const int depth = in && (p.window > 0 || p.slopes) ? depth_of(w.b, n) : 0;
+        sm.depth[ring][col] = (float)depth;
+        if (!kPlain)
+          sm.slope[ring][col] = in && p.slopes ? p.slopes[w.h * p.G + row - n * p.G] * kLog2e : 0.0f;
       }
     }
     fence_async_smem();
@@ -1095,6 +1093,7 @@ struct Tile {
     const int at = w.r.from + (t - w.r.drafted) * kTok + tok, j = t * kTok + tok;
     const bool exists = drafted ? j < w.r.nodes : at < w.r.len, special = drafted && unit < 0.0f;
     const int quarter = tok >> 5, window = hidden ? p.window : 0;
+    const float reach = (float)(window + at - w.r.len);
     float top = -INFINITY;
     if (!__any_sync(kAll, exists)) {  // a warp past the last token
       const float none[8] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY,
@@ -1134,7 +1133,7 @@ struct Tile {
       } else if (window > 0) {
         uint32_t bits = 0;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) bits |= (uint32_t)(sm.pos[ring][c0 + ch + k] - at < window) << k;
+        for (int k = 0; k < 8; ++k) bits |= (uint32_t)(sm.depth[ring][c0 + ch + k] < reach) << k;
         seen &= bits;
       }
       tmem_wait8(s);
@@ -1143,8 +1142,7 @@ struct Tile {
         float y = s[k] * (unit * rf[k]);
         if (!kPlain) {
           if (cap_in > 0.0f) y = capped(y);
-          // (position - len) - (pos - len), each exact
-          y = fmaf(sm.slope[ring][c0 + ch + k], position, y - sm.lag[ring][c0 + ch + k]);
+          y = fmaf(sm.slope[ring][c0 + ch + k], position - sm.depth[ring][c0 + ch + k], y);  // (exact)
         }
         s[k] = (seen >> k & 1u) ? y : -INFINITY;
         top = fmaxf(top, s[k] + nm[k]);
@@ -1207,7 +1205,7 @@ struct Tile {
 #pragma unroll 1
     for (uint32_t index = 0; ok && segment(index, ok); ++index) {
       const Segment &w = sm.seg[index & 7];
-      const int ring = index % 3, t0 = w.t0, t1 = w.t1;
+      const int ring = index & 3, t0 = w.t0, t1 = w.t1;
       float vref = 0.0f;
       bool unseen = true;  // the thread's column (tok) has seen no score yet
 #pragma unroll 1
@@ -1399,7 +1397,7 @@ struct Tile {
           float extra = 0.0f;
           if (out_at[i] && tok < kv.D && out_fac[i] != 0.0f)
             extra = stray(p, box, w.b, w.h, t0, t1, sm.node[ring][c0 + i] + node_of(w.rt * RN),
-                          sm.pos[ring][c0 + i], tok);
+                          w.r.len + (int)sm.depth[ring][c0 + i], tok);
           __syncwarp();
           tmem_store1(o_at + i, tmem_load1(o_at + i) + extra);
           tmem_stored();
