@@ -51,6 +51,7 @@ constexpr int kMaxSms = 160;
 constexpr int kWaitTries = 1000000;
 constexpr float kRaise = 8.0f;
 constexpr float kLift = 6.0f;
+constexpr float kMost = 15.0f;  // a weight's exponent is cut off there, until the maxima move
 constexpr float kUnseen = 1e30f;       // minus the maximum of a row that has seen nothing
 constexpr unsigned kAll = 0xffffffffu;
 
@@ -60,6 +61,13 @@ struct Cfg {
   static constexpr int kGroups = RN <= 64 ? 1 : 2;     // softmax groups of four warps: a part of the rows each
   static constexpr int kWorkers = 4;                   // warps that widen V: one on each quarter of the SM
   static constexpr int kFirst = 8;                     // first softmax warp
+  // Registers a thread: of the launch (what two CTAs, or one, leave room for), and
+  // of the three kinds of warpgroup, which share out those of the launch:
+  // kIssue + kWiden + kGroups kSoft = (2 + kGroups) kRegs
+  static constexpr int kRegs = RN <= 64 ? 80 : 128;
+  static constexpr int kIssue = RN <= 64 ? 64 : 72, kWiden = RN <= 64 ? 64 : 88;
+  static constexpr int kSoft = RN <= 64 ? 112 : 176;
+  static_assert(kIssue + kWiden + kGroups * kSoft == (2 + kGroups) * kRegs, "");
   static constexpr int kThreads = 32 * (kFirst + 4 * kGroups);
   static constexpr int kCols = RN / kGroups;           // most columns of a softmax thread
   static constexpr int kK = RN <= 64 ? 1 : 2;          // stages of K codes (free once scores are made)
@@ -116,12 +124,13 @@ struct Smem {
   alignas(16) float ones[C::kCols];
   float vred[C::kGroups][4];
   int vote[C::kGroups][4];
+  uint32_t moves[C::kGroups];             // waits of the products on `again`
   Segment seg[8];
   int bad[8], dirty[8];
   uint64_t seg_full[8], box_full[8];
   uint64_t k_full[C::kK], k_empty[C::kK], v_full[C::kV], v_empty[C::kV], q_full, q_empty;
   uint64_t s_full[2], s_empty[2], p_full[C::kBuf], vh_full[C::kBuf], pv_done[C::kBuf];
-  uint64_t group[C::kGroups], both, fin;
+  uint64_t group[C::kGroups], again[C::kGroups], both, fin;
   uint32_t tmem;
   int give_up;
   int done[C::kGroups];                   // segments that a softmax group finished
@@ -239,6 +248,11 @@ __device__ __forceinline__ void store_global32(bool here, unsigned long long at,
                : "memory");
 }
 
+__device__ __forceinline__ float min_nan(float a, float b) {  // NaN if one is
+  float y;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -723,6 +737,15 @@ struct Tile {
     if (!__all_sync(kAll, wait_lane(smem_addr(&sm.vh_full[c % kBuf]), full_par(c, kBuf), give_up) &&
                               wait_lane(smem_addr(&sm.p_full[c % kBuf]), full_par(c, kBuf), give_up)))
       return false;
+    // a group whose maxima move writes its weights again
+#pragma unroll 1
+    for (int g = 0; g < C::kGroups; ++g)
+      if (*(volatile int *)&sm.vote[g][c & 3]) {
+        const uint32_t parity = *(volatile uint32_t *)&sm.moves[g] & 1;
+        if (!__all_sync(kAll, wait_lane(smem_addr(&sm.again[g]), parity, give_up))) return false;
+        if (elected()) sm.moves[g] += 1;
+        __syncwarp();
+      }
     fence_after();
     if (elected()) {
       const uint32_t idesc = shape(columns, true);
@@ -1053,13 +1076,20 @@ struct Tile {
 
   // ------------------------------------------------------------ the last warps: softmax
   uint32_t group_phase, both_phase;
-  // The four warps of one group, and all softmax warps.
-  __device__ __forceinline__ bool meet(int group) {
+  // The four warps of one group: a warp's arrival, and the wait for all; and all
+  // softmax warps.
+  __device__ __forceinline__ void arrive(int group) {
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.group[group]);
+  }
+  __device__ __forceinline__ bool join(int group) {
     const bool ok = wait(&sm.group[group], group_phase);
     group_phase ^= 1;
     return ok;
+  }
+  __device__ __forceinline__ bool meet(int group) {
+    arrive(group);
+    return join(group);
   }
   __device__ __forceinline__ bool meet_all() {
     fence_before();
@@ -1085,23 +1115,21 @@ struct Tile {
   float cap_in, cap_out, cap_at;  // 2 / softcap, -2 and 1 times softcap log2(e)
 
   // Scores of a tile that needs more than a factor, in place: capped, biased and
-  // masked, in base-2 units.  Returns the thread's largest under the present
-  // maxima.  tok: the thread's token; unit: its k's.
-  __device__ __forceinline__ float bend(const Segment &w, int ring, int t, uint32_t c, bool drafted,
-                                        bool hidden, float unit, int tok, int c0, int mine,
-                                        uint32_t s_at, const float *nms) {
+  // masked, in base-2 units.  tok: the thread's token; unit: its k's.
+  __device__ __forceinline__ void bend(const Segment &w, int ring, int t, uint32_t c, bool drafted,
+                                       bool hidden, float unit, int tok, int c0, int mine,
+                                       uint32_t s_at) {
     const int at = w.r.from + (t - w.r.drafted) * kTok + tok, j = t * kTok + tok;
     const bool exists = drafted ? j < w.r.nodes : at < w.r.len, special = drafted && unit < 0.0f;
     const int quarter = tok >> 5, window = hidden ? p.window : 0;
     const float reach = (float)(window + at - w.r.len);
-    float top = -INFINITY;
     if (!__any_sync(kAll, exists)) {  // a warp past the last token
       const float none[8] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY,
                              -INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
       for (int ch = 0; ch < mine; ch += 8) tmem_store8(s_at + ch, none);
       tmem_stored();
-      return top;
+      return;
     }
     const float position =  // of the token, from the length
         kPlain ? 0.0f : (float)(!drafted ? at - w.r.len : p.slopes && exists ? depth_of(w.b, j) : 0);
@@ -1122,7 +1150,7 @@ struct Tile {
     for (int ch = 0; ch < mine; ch += 8) {
       float s[8];
       tmem_load8(s_at + ch, s);
-      const float *rf = &sm.rf[ring][c0 + ch], *nm = nms + ch;
+      const float *rf = &sm.rf[ring][c0 + ch];
       uint32_t seen = exists ? 0xFFu : 0u;
       if (drafted) {
         uint32_t bits = 0;
@@ -1145,12 +1173,10 @@ struct Tile {
           y = fmaf(sm.slope[ring][c0 + ch + k], position - sm.depth[ring][c0 + ch + k], y);  // (exact)
         }
         s[k] = (seen >> k & 1u) ? y : -INFINITY;
-        top = fmaxf(top, s[k] + nm[k]);
       }
       tmem_store8(s_at + ch, s);
     }
     tmem_stored();
-    return top;
   }
 
   // 8 scores under their columns' maxima: x = s * factor * unit + nm.
@@ -1190,9 +1216,9 @@ struct Tile {
   __device__ __forceinline__ void softmax() {
     const int group = C::kGroups == 1 ? 0 : (warp - C::kFirst) >> 2;
     const int quarter = warp & 3, tok = quarter * 32 + lane;
-    // the group's columns
-    const int mine = C::kGroups == 1 ? (min(RN, p.N * p.G) + 7) / 8 * 8 : columns / 2;
-    const int c0 = group * mine;
+    // the group's columns, in eights
+    const int parts = (min(RN, p.N * p.G) + 7) / 8, each = (parts + C::kGroups - 1) / C::kGroups;
+    const int c0 = group * each * 8, mine = max(min(each, parts - group * each), 0) * 8;
     const bool leader = lane == 0 && quarter == 0;
     const uint32_t lanes = sm.tmem + ((uint32_t)quarter << 21);  // TMEM lanes of this warp
     const uint32_t o_at = lanes + 2 * RN + c0, l_at = lanes + 3 * RN + c0;
@@ -1212,9 +1238,9 @@ struct Tile {
       for (int t = t0; t < t1; ++t, ++c) {
         const bool drafted = t < w.r.drafted, first = t == t0;
         const uint32_t s_at = lanes + (c & 1) * RN + c0;
-        if (!(ok = wait(&sm.box_full[c & 7], (c >> 3) & 1))) break;
-        const float2 unit = drafted ? sm.unit[c & 1][tok] : sm.boxes[c & 7][tok >> box_shift];
+        // (the scores' products have waited for the units, too)
         if (!(ok = wait(&sm.s_full[c & 1], (c >> 1) & 1))) break;
+        const float2 unit = drafted ? sm.unit[c & 1][tok] : sm.boxes[c & 7][tok >> box_shift];
         fence_after();
         // a plain tile's scores are a factor away; the others are written back
         const int past = drafted ? (t + 1) * kTok - w.r.nodes
@@ -1225,125 +1251,123 @@ struct Tile {
         const float k_unit = bent ? 1.0f : unit.x;
         const f2 ks = pair(k_unit, k_unit);
         const float *factor = bent ? sm.ones : sm.rf[ring] + c0;
-        float top = -INFINITY;
-        if (bent) {
-          top = bend(w, ring, t, c, drafted, hidden, unit.x, tok, c0, mine, s_at, nms);
-        } else if (!first) {
-#pragma unroll 1
-          for (int ch = 0; ch < mine; ch += 8) {
-            float s[8];
-            tmem_load8(s_at + ch, s);
-            tmem_wait8(s);
-            under(s, factor + ch, nms + ch, ks);
-#pragma unroll
-            for (int k = 0; k < 8; k += 2) top = fmaxf(top, fmaxf(s[k], s[k + 1]));
-          }
-        }
-        // Scores far above a maximum, or a larger unit of v, and the group's maxima
-        // move; at a segment's start they are all at 0 and move from there.
-        bool move = first;
-        if (!first) {
-          if (__any_sync(kAll, top > kRaise + kLift || v_unit > vref) && lane == 0)
-            sm.vote[group][c & 3] = 1;
-          if (!(ok = meet(group))) break;
-          move = *(volatile int *)&sm.vote[group][c & 3] != 0;
-          if (move) {
-            if (tok < mine && unseen) nms[tok] = 0.0f;
-            if (!(ok = meet(group))) break;
-          }
-        }
-        if (move) {
-#pragma unroll 1
-          for (int ch = 0; ch < mine; ch += 8) {
-            float s[8];
-            tmem_load8(s_at + ch, s);
-            tmem_wait8(s);
-            under(s, factor + ch, nms + ch, ks);
-            const float best = over_lanes<true>(s);
-            if ((lane & 3) == 0) sm.red[group][quarter][ch + (lane >> 2)] = best;
-            __syncwarp();
-          }
-          const int vmax = __reduce_max_sync(kAll, __float_as_int(v_unit));  // units are >= 0
-          if (lane == 0) sm.vred[group][quarter] = __int_as_float(vmax);
-          if (!(ok = meet(group))) break;
-          const float unit_max = fmaxf(fmaxf(sm.vred[group][0], sm.vred[group][1]),
-                                       fmaxf(sm.vred[group][2], sm.vred[group][3]));
-          // headroom of 4, so that units of one size move once
-          const float to = unit_max > vref ? fminf(unit_max * 4.0f, 0x1p126f) : vref;
-          const float v_fac = to > 0.0f ? __fdividef(vref, to) : 1.0f;
-          vref = to;
-          if (tok < mine) {
-            const float best = fmaxf(fmaxf(sm.red[group][0][tok], sm.red[group][1][tok]),
-                                     fmaxf(sm.red[group][2][tok], sm.red[group][3][tok]));
-            const float nm = nms[tok];
-            float f = 1.0f;
-            if (best > -INFINITY && (unseen || best > kLift)) {
-              nms[tok] = kLift - (best - nm);
-              f = unseen ? 0.0f : ex2_approx(kLift - best);
-              unseen = false;
-            } else if (unseen) {
-              nms[tok] = kUnseen;
-            }
-            sm.fac[group][0][tok] = f;
-            sm.fac[group][1][tok] = f * v_fac;
-          }
-          if (!first && !(ok = wait(&sm.pv_done[(c - 1) % kBuf], full_par(c - 1, kBuf)))) break;
-          fence_after();
-          if (!(ok = meet(group))) break;
-          if (!first) {  // the sums, then the outputs
-#pragma unroll 1
-            for (int i = 0; i < 2 * mine; i += 8) {
-              const int ch = i < mine ? i : i - mine;
-              const uint32_t at = i < mine ? l_at + ch : o_at + ch;
-              const float *fac = sm.fac[group][i >= mine] + ch;
-              float o[8];
-              tmem_load8(at, o);
-              tmem_wait8(o);
-#pragma unroll
-              for (int k = 0; k < 8; ++k) o[k] *= fac[k];
-              tmem_store8(at, o);
-            }
-            tmem_stored();
-          }
-        }
-        if (leader) sm.vote[group][(c + 2) & 3] = 0;
+        if (bent) bend(w, ring, t, c, drafted, hidden, unit.x, tok, c0, mine, s_at);
         // P^T of the tile before in this buffer has been read
         if (!(ok = wait(&sm.pv_done[c % kBuf], empty_par(c, kBuf)))) break;
-        const float ratio = vref > 0.0f ? __fdividef(v_unit, vref) : 0.0f;
-        const f2 r2 = pair(ratio, ratio);
+        if (leader) sm.vote[group][(c - kBuf) & 3] = 0;
         uint8_t *pt = sm.pt[c % kBuf][0] + tok * kRow;
+        // The weights are made under the maxima as they are, which seldom move: if
+        // scores turn out far above a maximum, or a unit of v larger than the outputs',
+        // they are taken back, the maxima move, and they are made again.  At a
+        // segment's start the maxima are all at 0 and move from there.
+        int round = first ? 2 : 0;  // 0: make, 1: take back, 2: move and make
 #pragma unroll 1
-        for (int ch = 0; ch < mine; ch += 8) {
-          float s[8], l[8];
-          tmem_load8(s_at + ch, s);
-          tmem_load8(l_at + ch, l);
-          tmem_wait8(s);
-          tmem_wait8(l);
-          under(s, factor + ch, nms + ch, ks);
-          uint32_t out[4];
+        for (;; ++round) {
+          if (round == 2) {
+            if (!first) {
+              if (!(ok = meet(group))) break;  // all have read the maxima
+              if (tok < mine && unseen) nms[tok] = 0.0f;
+              if (!(ok = meet(group))) break;
+            }
+#pragma unroll 1
+            for (int ch = 0; ch < mine; ch += 8) {
+              float s[8];
+              tmem_load8(s_at + ch, s);
+              tmem_wait8(s);
+              under(s, factor + ch, nms + ch, ks);
+              const float best = over_lanes<true>(s);
+              if ((lane & 3) == 0) sm.red[group][quarter][ch + (lane >> 2)] = best;
+              __syncwarp();
+            }
+            const int vmax = __reduce_max_sync(kAll, __float_as_int(v_unit));  // units are >= 0
+            if (lane == 0) sm.vred[group][quarter] = __int_as_float(vmax);
+            if (!(ok = meet(group))) break;
+            const float unit_max = fmaxf(fmaxf(sm.vred[group][0], sm.vred[group][1]),
+                                         fmaxf(sm.vred[group][2], sm.vred[group][3]));
+            // headroom of 4, so that units of one size move once
+            const float to = unit_max > vref ? fminf(unit_max * 4.0f, 0x1p126f) : vref;
+            const float v_fac = to > 0.0f ? __fdividef(vref, to) : 1.0f;
+            vref = to;
+            if (tok < mine) {
+              const float best = fmaxf(fmaxf(sm.red[group][0][tok], sm.red[group][1][tok]),
+                                       fmaxf(sm.red[group][2][tok], sm.red[group][3][tok]));
+              const float nm = nms[tok];
+              float f = 1.0f;
+              if (best > -INFINITY && (unseen || best > kLift)) {
+                nms[tok] = kLift - (best - nm);
+                f = unseen ? 0.0f : ex2_approx(kLift - best);
+                unseen = false;
+              } else if (unseen) {
+                nms[tok] = kUnseen;
+              }
+              sm.fac[group][0][tok] = f;
+              sm.fac[group][1][tok] = f * v_fac;
+            }
+            if (!first && !(ok = wait(&sm.pv_done[(c - 1) % kBuf], full_par(c - 1, kBuf)))) break;
+            fence_after();
+            if (!(ok = meet(group))) break;
+            if (!first) {  // the sums, then the outputs
+#pragma unroll 1
+              for (int i = 0; i < 2 * mine; i += 8) {
+                const int ch = i < mine ? i : i - mine;
+                const uint32_t at = i < mine ? l_at + ch : o_at + ch;
+                const float *fac = sm.fac[group][i >= mine] + ch;
+                float o[8];
+                tmem_load8(at, o);
+                tmem_wait8(o);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const f2 e = pair(ex2_approx(s[2 * k]), ex2_approx(s[2 * k + 1]));
-            if (first) l[2 * k] = l[2 * k + 1] = 0.0f;
-            unpair(add2(pair(l[2 * k], l[2 * k + 1]), e), l[2 * k], l[2 * k + 1]);
-            float a, b;
-            unpair(mul2(e, r2), a, b);
-            out[k] = pack_half2(a, b);
+                for (int k = 0; k < 8; ++k) o[k] *= fac[k];
+                tmem_store8(at, o);
+              }
+              tmem_stored();
+            }
           }
-          tmem_store8(l_at + ch, l);
-          const int col = c0 + ch;
-          *reinterpret_cast<uint4 *>(pt + (col >> 6) * kTileBytes +
-                                     ((((col & 63) >> 3) ^ (tok & 7)) << 4)) =
-              make_uint4(out[0], out[1], out[2], out[3]);
+          const float ratio = vref > 0.0f ? __fdividef(v_unit, vref) : 0.0f;
+          const f2 r2 = pair(ratio, ratio), sign = round == 1 ? pair(-1.0f, -1.0f) : pair(1.0f, 1.0f);
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int ch = 0; ch < mine; ch += 8) {
+            float s[8], l[8];
+            tmem_load8(s_at + ch, s);
+            tmem_load8(l_at + ch, l);
+            tmem_wait8(s);
+            tmem_wait8(l);
+            under(s, factor + ch, nms + ch, ks);
+            uint32_t out[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              top = fmaxf(top, fmaxf(s[2 * k], s[2 * k + 1]));
+              const f2 e = pair(ex2_approx(min_nan(s[2 * k], kMost)), ex2_approx(min_nan(s[2 * k + 1], kMost)));
+              if (first) l[2 * k] = l[2 * k + 1] = 0.0f;
+              unpair(fma2(e, sign, pair(l[2 * k], l[2 * k + 1])), l[2 * k], l[2 * k + 1]);
+              float a, b;
+              unpair(mul2(e, r2), a, b);
+              out[k] = pack_half2(a, b);
+            }
+            tmem_store8(l_at + ch, l);
+            const int col = c0 + ch;
+            *reinterpret_cast<uint4 *>(pt + (col >> 6) * kTileBytes +
+                                       ((((col & 63) >> 3) ^ (tok & 7)) << 4)) =
+                make_uint4(out[0], out[1], out[2], out[3]);
+          }
+          tmem_stored();
+          if (round == 1) continue;
+          const bool vote = round == 0 && __any_sync(kAll, top > kRaise + kLift || v_unit > vref);
+          fence_async_smem();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (vote) sm.vote[group][c & 3] = 1;
+            mbar_arrive(round == 0 || first ? &sm.p_full[c % kBuf] : &sm.again[group]);
+          }
+          if (round == 2) break;
+          if (!(ok = wait(&sm.p_full[c % kBuf], full_par(c, kBuf)))) break;
+          if (*(volatile int *)&sm.vote[group][c & 3] == 0) break;
         }
-        tmem_stored();
-        fence_async_smem();
+        if (!ok) break;
         fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&sm.s_empty[c & 1]);
-          mbar_arrive(&sm.p_full[c % kBuf]);
-        }
+        if (lane == 0) mbar_arrive(&sm.s_empty[c & 1]);
       }
       if (!ok) break;
 
@@ -1503,6 +1527,8 @@ __global__ void __launch_bounds__(Cfg<RN>::kThreads, Cfg<RN>::kCtas)
     }
     if (tid < C::kGroups) {
       mbar_init(&sm.group[tid], 4);
+      mbar_init(&sm.again[tid], 4);
+      sm.moves[tid] = 0;
       sm.done[tid] = 0;
     }
     if (tid < 4 * C::kGroups) sm.vote[tid >> 2][tid & 3] = 0;
@@ -1533,13 +1559,16 @@ __global__ void __launch_bounds__(Cfg<RN>::kThreads, Cfg<RN>::kCtas)
   Tile<RN, kPlain> tile(p, sm, &k_map, &v_map, box);
   // warps 0-3: copies, products (two stay idle); 4-7: operands; the others: softmax
   if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kIssue));
     if (warp == 0)
       tile.copies(plan);
     else if (warp == 1)
       tile.products();
   } else if (warp < C::kFirst) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kWiden));
     tile.operands();
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoft));
     tile.softmax();
   }
   fence_before();
@@ -1613,18 +1642,37 @@ __global__ void __launch_bounds__(32 * kJoinRows)
 #pragma unroll
   for (int d = 16; d >= 1; d >>= 1) all = fmaxf(all, __shfl_xor_sync(kAll, all, d));
   const bool empty = bad || all == -INFINITY;
+  // a lane for each part's factor; then the parts' outputs, eight loads in flight
   float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   if (!empty) {
-#pragma unroll 4
-    for (int s = 0; s < parts; ++s) {
-      if (!has(s)) continue;
-      const float *rec = record(s);
-      const float m = rec[0], f = m == -INFINITY ? 0.0f : ex2_approx(m - all);
-      sum += rec[1] * f;
+#pragma unroll 1
+    for (int s0 = 0; s0 < parts; s0 += 32) {
+      const int s = s0 + lane;
+      float f = 0.0f;
+      if (s < parts && has(s)) {
+        const float *rec = record(s);
+        f = rec[0] == -INFINITY ? 0.0f : ex2_approx(rec[0] - all);
+        sum += rec[1] * f;
+      }
+#pragma unroll 1
+      for (int i0 = 0; i0 < min(32, parts - s0); i0 += 8) {
+        float x[8][4], g[8];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (lane + 32 * k < D) acc[k] += f * rec[2 + lane + 32 * k];
+        for (int j = 0; j < 8; ++j) {
+          g[j] = __shfl_sync(kAll, f, i0 + j);  // 0 past the last part
+          const float *rec = record(s0 + i0 + j) + 2;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            x[j][k] = g[j] != 0.0f && lane + 32 * k < D ? rec[lane + 32 * k] : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[k] += g[j] * x[j][k];
+      }
     }
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
   }
   const float inv = empty ? 0.0f : 1.0f / sum;
   const long long at = ((long long)me.b * p.N + n) * p.Hq + me.h * p.G + row - n * p.G;
