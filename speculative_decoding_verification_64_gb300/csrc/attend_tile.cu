@@ -273,11 +273,6 @@ __device__ __forceinline__ f2 mul2(f2 a, f2 b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-  f2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
   f2 r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
@@ -1594,10 +1589,10 @@ __global__ void __launch_bounds__(32 * kJoinRows)
   pdl_wait();
   pdl_launch_dependents();
   const int i = blockIdx.x, D = p.cache.D, lane = threadIdx.x & 31;
-  const size_t size = partial_floats(RN, D);
+  const int size = (int)partial_floats(RN, D);
   const Note *notes = notes_of(p.part, RN, D);
-  const Note me = notes[i];
-  if (me.first == 0) return;  // begins with a unit, or has no tile
+  const int mine = notes[i].first, unit = notes[i].unit;
+  if (mine == 0) return;  // begins with a unit, or has no tile
   // the CTAs before: the one that began the unit is the last that has tiles
   int begun = -1;
 #pragma unroll 1
@@ -1605,85 +1600,90 @@ __global__ void __launch_bounds__(32 * kJoinRows)
     const unsigned full = __ballot_sync(kAll, at - lane >= 0 && notes[at - lane].tiles > 0);
     if (full) begun = at - (__ffs(full) - 1);
   }
-  if (begun < 0 || notes[begun].open != me.first) return;  // it was in the middle, too
-  // parts: that one's second slot, then first slots until the unit's end
-  const int r = blockIdx.y * kJoinRows + (threadIdx.x >> 5), row = me.rt * RN + r, n = row / p.G;
-  int left = me.unit - me.first, last = -1;
+  if (begun < 0 || notes[begun].open != mine) return;  // it was in the middle, too
+  const int row = notes[i].rt * RN + blockIdx.y * kJoinRows + (threadIdx.x >> 5);
+  const int r = row - notes[i].rt * RN;
+  if (r >= RN || row >= p.N * p.G) return;
+  // Parts: that one's second slot, then first slots until the unit's end.  32 at a
+  // time, a lane each: its maximum, sum and flags; the factors that bring both and
+  // the outputs under the largest maximum; then the outputs, four elements a lane.
+  float all = -INFINITY, sum = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  int bad = 0, left = unit - mine;
+  const float *const part = p.part + r * (D + 2);
 #pragma unroll 1
-  for (int at = i; at < ctas && last < 0; at += 32) {
-    int upto = 0;
-    if (at + lane < ctas && notes[at + lane].tiles > 0) upto = notes[at + lane].head;
+  for (int at = i - 1; left > 0 && at < ctas; at += 32) {  // CTA at + lane; i - 1 stands for `begun`
+    const int cta = at + lane;
+    int head = 0, slot = 2 * cta;
+    if (cta < i) {
+      slot = 2 * begun + 1;
+    } else if (cta < ctas && notes[cta].tiles > 0) {
+      head = notes[cta].head;
+    }
+    int upto = head;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int o = __shfl_up_sync(kAll, upto, d);
       if (lane >= d) upto += o;
     }
-    const unsigned ends = __ballot_sync(kAll, upto >= left);
-    if (ends) last = at + __ffs(ends) - 1;
+    const bool in = cta < i || (head > 0 && upto - head < left);
+    float m = -INFINITY, l = 0.0f;
+    if (in) {
+      m = part[slot * size];
+      l = part[slot * size + 1];
+    }
+    if (l < 0.0f) bad |= (int)-l;
+    float most = m;
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) most = fmaxf(most, __shfl_xor_sync(kAll, most, d));
+    most = fmaxf(all, most);
+    const float before = all > -INFINITY ? ex2_approx(all - most) : 0.0f;
+    const float f = m > -INFINITY ? ex2_approx(m - most) : 0.0f;
+    all = most;
+    sum = sum * before + l * f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[k] *= before;
+    const unsigned full = __ballot_sync(kAll, f > 0.0f);
+#pragma unroll 1
+    for (int s = 0; full >> s; s += 4) {
+      float2 x[4][2];
+      float g[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int from = (s + u) & 31;
+        g[u] = (full >> s >> u & 1) ? __shfl_sync(kAll, f, from) : 0.0f;
+        const float *rec = part + __shfl_sync(kAll, slot, from) * size + 2 + 4 * lane;
+        x[u][0] = x[u][1] = make_float2(0.0f, 0.0f);
+        if ((full >> s >> u & 1) && 4 * lane < D) {
+          x[u][0] = *reinterpret_cast<const float2 *>(rec);
+          x[u][1] = *reinterpret_cast<const float2 *>(rec + 2);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        acc[0] += g[u] * x[u][0].x;
+        acc[1] += g[u] * x[u][0].y;
+        acc[2] += g[u] * x[u][1].x;
+        acc[3] += g[u] * x[u][1].y;
+      }
+      if (s == 28) break;
+    }
     left -= __shfl_sync(kAll, upto, 31);
   }
-  const int parts = last - i + 2;
-  if (r >= RN || row >= p.N * p.G) return;
-  const float *head = p.part + (size_t)(2 * begun + 1) * size + (size_t)r * (D + 2);
-  auto record = [&](int s) {
-    return s == 0 ? head : p.part + (size_t)(2 * (i + s - 1)) * size + (size_t)r * (D + 2);
-  };
-  auto has = [&](int s) { return s == 0 || notes[i + s - 1].tiles > 0; };
-  float all = -INFINITY, sum = 0.0f;
-  int bad = 0;
-#pragma unroll 1
-  for (int s = lane; s < parts; s += 32) {
-    if (!has(s)) continue;
-    const float *rec = record(s);
-    all = fmaxf(all, rec[0]);
-    if (rec[1] < 0.0f) bad |= (int)-rec[1];
-  }
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
   bad = __reduce_or_sync(kAll, bad);
-#pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) all = fmaxf(all, __shfl_xor_sync(kAll, all, d));
   const bool empty = bad || all == -INFINITY;
-  // a lane for each part's factor; then the parts' outputs, eight loads in flight
-  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (!empty) {
-#pragma unroll 1
-    for (int s0 = 0; s0 < parts; s0 += 32) {
-      const int s = s0 + lane;
-      float f = 0.0f;
-      if (s < parts && has(s)) {
-        const float *rec = record(s);
-        f = rec[0] == -INFINITY ? 0.0f : ex2_approx(rec[0] - all);
-        sum += rec[1] * f;
-      }
-#pragma unroll 1
-      for (int i0 = 0; i0 < min(32, parts - s0); i0 += 8) {
-        float x[8][4], g[8];
+  const float inv = empty ? 0.0f : __fdividef(1.0f, sum);
+  const int n = row / p.G, h = notes[i].h, b = notes[i].b;
+  const long long at = ((long long)b * p.N + n) * p.Hq + h * p.G + row - n * p.G;
+  if (4 * lane < D) {
+    unsigned short *out = reinterpret_cast<unsigned short *>(p.out) + at * D + 4 * lane;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          g[j] = __shfl_sync(kAll, f, i0 + j);  // 0 past the last part
-          const float *rec = record(s0 + i0 + j) + 2;
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            x[j][k] = g[j] != 0.0f && lane + 32 * k < D ? rec[lane + 32 * k] : 0.0f;
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) acc[k] += g[j] * x[j][k];
-      }
-    }
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
+    for (int k = 0; k < 4; ++k)
+      out[k] = (unsigned short)pack_bf16x2(empty ? 0.0f : acc[k] * inv, 0.0f);
   }
-  const float inv = empty ? 0.0f : 1.0f / sum;
-  const long long at = ((long long)me.b * p.N + n) * p.Hq + me.h * p.G + row - n * p.G;
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (lane + 32 * k < D)
-      reinterpret_cast<unsigned short *>(p.out)[at * D + lane + 32 * k] =
-          (unsigned short)pack_bf16x2(empty ? 0.0f : acc[k] * inv, 0.0f);
-  if (p.lse && lane == 0)
-    p.lse[at] = empty ? -INFINITY : (all + log2f(sum)) * 0.6931471805599453f;
-  if (me.h == 0 && row == 0 && lane == 0) p.row_status[me.b] = bad;
+  if (p.lse && lane == 0) p.lse[at] = empty ? -INFINITY : (all + log2f(sum)) * 0.6931471805599453f;
+  if (h == 0 && row == 0 && lane == 0) p.row_status[b] = bad;
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
