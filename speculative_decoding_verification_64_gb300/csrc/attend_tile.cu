@@ -1254,8 +1254,10 @@ struct Tile {
         // The weights are made under the maxima as they are, which seldom move: if
         // scores turn out far above a maximum, or a unit of v larger than the outputs',
         // they are taken back, the maxima move, and they are made again.  At a
-        // segment's start the maxima are all at 0 and move from there.
-        int round = first ? 2 : 0;  // 0: make, 1: take back, 2: move and make
+        // segment's start the maxima are all at 0 and move from there; after the drafted
+        // tokens, of which a row sees a few only, they move at once.
+        const bool sure = first || t == w.r.drafted;
+        int round = sure ? 2 : 0;  // 0: make, 1: take back, 2: move and make
 #pragma unroll 1
         for (;; ++round) {
           if (round == 2) {
@@ -1353,7 +1355,7 @@ struct Tile {
           __syncwarp();
           if (lane == 0) {
             if (vote) sm.vote[group][c & 3] = 1;
-            mbar_arrive(round == 0 || first ? &sm.p_full[c % kBuf] : &sm.again[group]);
+            mbar_arrive(round == 0 || sure ? &sm.p_full[c % kBuf] : &sm.again[group]);
           }
           if (round == 2) break;
           if (!(ok = wait(&sm.p_full[c % kBuf], full_par(c, kBuf)))) break;
