@@ -141,6 +141,9 @@ struct Smem {
 // ---------------------------------------------------------------------------
 // PTX
 // ---------------------------------------------------------------------------
+__device__ __forceinline__ void prefetch_l2(const void *at) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+}
 __device__ __forceinline__ void tma_rows(void *dst, const CUtensorMap *map, int row, uint64_t *bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
@@ -218,6 +221,16 @@ __device__ __forceinline__ void tmem_store8(uint32_t at, const float *x) {
                "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]),
                "f"(x[7])
                : "memory");
+}
+__device__ __forceinline__ void tmem_load4(uint32_t at, float *x) {
+  uint32_t r[4];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];\n\t"
+               "tcgen05.wait::ld.sync.aligned;"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(r[i]);
 }
 __device__ __forceinline__ float tmem_load1(uint32_t at) {
   uint32_t r;
@@ -605,8 +618,24 @@ struct Tile {
     }
     return more;
   }
+  // The rows that the others read next, towards the L2.
+  __device__ __forceinline__ void fetch(const Segment &w) const {
+    const long long first = (long long)w.b * p.N;
+    const int D = p.cache.D;
+#pragma unroll 1
+    for (int n = lane; n < w.r.nodes; n += 32) {
+      const char *q = reinterpret_cast<const char *>(p.q) + ((first + n) * p.q_stride + w.h * p.G * D) * 2;
+#pragma unroll 1
+      for (int i = 0; i < p.G * D * 2; i += 128) prefetch_l2(q + i);
+      if (w.t0 < w.r.drafted) {
+        prefetch_l2(reinterpret_cast<const char *>(p.k_new) + ((first + n) * p.k_stride + w.h * D) * 2);
+        prefetch_l2(reinterpret_cast<const char *>(p.v_new) + ((first + n) * p.v_stride + w.h * D) * 2);
+      }
+    }
+  }
   __device__ __forceinline__ bool publish(Walk &walk, uint32_t index, Segment &w) {
     const bool more = take(walk, w);
+    if (more) fetch(w);
     if (lane == 0) {
       sm.seg[index & 7] = w;
       mbar_arrive(&sm.seg_full[index & 7]);
@@ -855,43 +884,37 @@ struct Tile {
     const int nodes = w.r.nodes, row0 = w.rt * RN;
     const bool wide = ((reinterpret_cast<uintptr_t>(p.q) | (uintptr_t)(p.q_stride * 2)) & 15) == 0;
     const long long first = (long long)w.b * p.N;
-    auto load = [&](int r) {
-      const int row = row0 + r, n = node_of(row);
-      if (r >= columns || row >= p.N * p.G || n >= nodes || e >= D) return make_uint4(0u, 0u, 0u, 0u);
-      return load8(p.q, (first + n) * p.q_stride + (long long)(w.h * p.G + row - n * p.G) * D + e,
-                   wide);
-    };
-    constexpr int kBatch = 4, kStep = 2 * C::kWorkers;  // loads in flight; rows at once
+    constexpr int kStep = 2 * C::kWorkers;  // rows at once
+    const int r0 = worker * 2 + (lane >> 4);
+    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+    // a row is loaded while the one before is split
 #pragma unroll 1
-    for (int r0 = worker * 2 + (lane >> 4); r0 < columns; r0 += kBatch * kStep) {
-      uint4 x[kBatch];
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) x[i] = load(r0 + i * kStep);
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int r = r0 + i * kStep;
-        if (r - (lane >> 4) >= columns) break;
+    for (int r = r0; r - (lane >> 4) < columns + kStep; r += kStep) {
+      uint4 next = make_uint4(0u, 0u, 0u, 0u);
+      {
+        const int row = row0 + r, n = node_of(row);
+        if (r < columns && row < p.N * p.G && n < nodes && e < D)
+          next = load8(p.q, (first + n) * p.q_stride + (w.h * p.G + row - n * p.G) * D + e, wide);
+      }
+      if (r != r0) {
+        const int col = r - kStep, row = row0 + col, n = node_of(row);
         bool all;
-        const int ex = unit_exponent(row_top(x[i], all), 7);
-        split(sm.q[0], sm.q[1], r, e, x[i], ex);
-        // a q that is not finite makes its row NaN
-        if ((lane & 15) == 0) sm.rf[ring][r] = all ? pow2i(ex) : __int_as_float(0x7fc00000);
+        const int ex = unit_exponent(row_top(x, all), 7);
+        split(sm.q[0], sm.q[1], col, e, x, ex);
+        if ((lane & 15) == 0) {
+          const bool in = row < p.N * p.G && n < nodes;
+          // a q that is not finite makes its row NaN
+          const float unit = all ? pow2i(ex) : __int_as_float(0x7fc00000);
+          const int depth = in && (p.window > 0 || p.slopes) ? depth_of(w.b, n) : 0;
+          sm.node[ring][col] = (uint8_t)(n - node_of(row0));
+          sm.rf[ring][col] = in ? p.scale * kLog2e * unit : 0.0f;
+          sm.depth[ring][col] = (float)depth;
+          if (!kPlain)
+            sm.slope[ring][col] = in && p.slopes ? p.slopes[w.h * p.G + row - n * p.G] * kLog2e : 0.0f;
+        }
+        __syncwarp();
       }
-    }
-    __syncwarp();
-    if (lane < 16) {  // the warp's own rows: worker * 2 + {0, 1} + 8 i
-      const int r = worker * 2 + (lane & 1) + (lane >> 1) * kStep;
-#pragma unroll 1
-      for (int col = r; col < columns; col += 8 * kStep) {
-        const int row = row0 + col, n = node_of(row);
-        const bool in = row < p.N * p.G && n < nodes;
-        sm.node[ring][col] = (uint8_t)(n - node_of(row0));
-        sm.rf[ring][col] = in ? p.scale * kLog2e * sm.rf[ring][col] : 0.0f;
-        const int depth = in && (p.window > 0 || p.slopes) ? depth_of(w.b, n) : 0;
-        sm.depth[ring][col] = (float)depth;
-        if (!kPlain)
-          sm.slope[ring][col] = in && p.slopes ? p.slopes[w.h * p.G + row - n * p.G] * kLog2e : 0.0f;
-      }
+      x = next;
     }
     fence_async_smem();
     __syncwarp();
@@ -1424,35 +1447,23 @@ struct Tile {
           tmem_stored();
         }
 #pragma unroll 1
-      for (int i = 0; i < mine; i += 8) {
-        float o[8];
+      for (int i = 0; i < mine; i += 4) {
+        float o[4];
         __syncwarp();
-        tmem_load8(o_at + i, o);
-        tmem_wait8(o);
-        unsigned long long at[8];
-        float f[8];
+        tmem_load4(o_at + i, o);
+        const float4 f = *reinterpret_cast<const float4 *>(out_fac + i);
+        const ulonglong2 a = *reinterpret_cast<const ulonglong2 *>(out_at + i);
+        const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(out_at + i + 2);
+        const float y[4] = {f.x != 0.0f ? o[0] * f.x : 0.0f, f.y != 0.0f ? o[1] * f.y : 0.0f,
+                            f.z != 0.0f ? o[2] * f.z : 0.0f, f.w != 0.0f ? o[3] * f.w : 0.0f};
+        const unsigned long long at[4] = {a.x, a.y, b.x, b.y};
 #pragma unroll
-        for (int k = 0; k < 8; k += 4) {
-          const float4 x = *reinterpret_cast<const float4 *>(out_fac + i + k);
-          f[k] = x.x;
-          f[k + 1] = x.y;
-          f[k + 2] = x.z;
-          f[k + 3] = x.w;
-        }
-#pragma unroll
-        for (int k = 0; k < 8; k += 2) {
-          const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(out_at + i + k);
-          at[k] = x.x;
-          at[k + 1] = x.y;
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float y = f[k] != 0.0f ? o[k] * f[k] : 0.0f;
+        for (int k = 0; k < 4; ++k) {
           const bool here = at[k] != 0 && tok < kv.D;
           if (whole)
-            store_global16(here, at[k] + 2 * tok, pack_bf16x2(y, 0.0f));
+            store_global16(here, at[k] + 2 * tok, pack_bf16x2(y[k], 0.0f));
           else
-            store_global32(here, at[k] + 4 * tok, y);
+            store_global32(here, at[k] + 4 * tok, y[k]);
         }
       }
       if (leader && group == 0 && whole && w.h == 0 && w.rt == 0) p.row_status[w.b] = bad;
