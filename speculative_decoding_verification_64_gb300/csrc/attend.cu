@@ -957,29 +957,37 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams p) 
 #pragma unroll
   for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
   const bool empty = bad != 0 || all == -INFINITY;
-  float acc[SPECDEC_MAX_HEAD_DIM / 32];
+  const float inv = empty ? 0.0f : __fdividef(1.0f, sum);
+  // four splits at a time, 128 elements of each, all loads before the sums
+#pragma unroll 1
+  for (int d0 = lane; d0 < D; d0 += 128) {
+    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+    for (int s = 0; s < p.splits; s += 4) {
+      float x[4][4], w[4];
 #pragma unroll
-  for (int i = 0; i < SPECDEC_MAX_HEAD_DIM / 32; ++i) acc[i] = 0.0f;
-  for (int s = 0; s < p.splits; ++s) {
-    const float w = __shfl_sync(kAll, s < 32 ? f[0] : f[1], s & 31);
-    const float ms = __shfl_sync(kAll, s < 32 ? m[0] : m[1], s & 31);
-    if (ms == -INFINITY) continue;
+      for (int u = 0; u < 4; ++u) {
+        // (0 past the last split, and for one without tokens, whose sums are not there)
+        w[u] = __shfl_sync(kAll, s < 32 ? f[0] : f[1], (s + u) & 31);
+        const float *rec = part + (s + u) * stride + 2 * kRows + r * D + d0;
 #pragma unroll
-    for (int i = 0; i < SPECDEC_MAX_HEAD_DIM / 32; ++i) {
-      const int d = lane + 32 * i;
-      if (d < D) acc[i] += w * part[s * stride + 2 * kRows + r * D + d];
+        for (int k = 0; k < 4; ++k) x[u][k] = w[u] != 0.0f && d0 + 32 * k < D ? rec[32 * k] : 0.0f;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[k] += w[u] * x[u][k];
     }
-  }
-  const float inv = empty ? 0.0f : 1.0f / sum;
 #pragma unroll
-  for (int i = 0; i < SPECDEC_MAX_HEAD_DIM / 32; ++i) {
-    const int d = lane + 32 * i;
-    if (d >= D) continue;
-    const float x = empty ? 0.0f : acc[i] * inv;
-    if (p.dtype == SPECDEC_F32)
-      reinterpret_cast<float *>(p.out)[at * D + d] = x;
-    else
-      reinterpret_cast<unsigned short *>(p.out)[at * D + d] = (unsigned short)pack_bf16x2(x, 0.0f);
+    for (int k = 0; k < 4; ++k) {
+      const int d = d0 + 32 * k;
+      if (d >= D) continue;
+      const float y = empty ? 0.0f : acc[k] * inv;
+      if (p.dtype == SPECDEC_F32)
+        reinterpret_cast<float *>(p.out)[at * D + d] = y;
+      else
+        reinterpret_cast<unsigned short *>(p.out)[at * D + d] = (unsigned short)pack_bf16x2(y, 0.0f);
+    }
   }
   if (lane == 0) {
     if (p.lse) p.lse[at] = empty ? -INFINITY : (all - kLift + log2f(sum)) * 0.6931471805599453f;
@@ -996,16 +1004,22 @@ int most_splits(long long B, int N, int Hkv, int G) {
   const long long s = 608 / ctas;  // 4 for each of 152 SMs
   return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
 }
-// ... and no more than leave each warp a granule where the cache is full; up to
-// eight as a power of two, which a cluster joins.
-int splits_of(const AttendParams &p) {
-  const int most = most_splits(p.B, p.N, p.cache.Hkv, p.G);
+// Granules that a request can hold: of what its blocks hold, or the window leaves.
+long long granules_of(const AttendParams &p) {
   long long tokens = (long long)p.cache.max_blocks * p.cache.block;
   if (p.window > 0 && tokens > p.window + kGran) tokens = p.window + kGran;
-  const long long granules = (tokens + kGran - 1) / kGran + (p.N + kGran - 1) / kGran;
-  const long long useful = (granules + kWarps - 1) / kWarps;
+  return (tokens + kGran - 1) / kGran + (p.N + kGran - 1) / kGran;
+}
+// ... and no more than leave each warp a granule where the cache is full; up to
+// eight as a power of two, which a cluster joins.  More than eight go through the
+// workspace, which pays once eight leave a warp more than 32 granules: one request
+// of 5 (8 heads of 128, float32) takes 24.8 us with eight and 42.4 us with 33 over
+// 2048 tokens, 63.6 and 69.1 over 16384, 219 and 135 over 65536.
+int splits_of(const AttendParams &p) {
+  const int most = most_splits(p.B, p.N, p.cache.Hkv, p.G);
+  const long long granules = granules_of(p), useful = (granules + kWarps - 1) / kWarps;
   const long long s = useful < most ? useful : most;
-  if (s >= 24) return (int)s;  // 8 would leave warps three times the work
+  if (s >= 24 && granules > 8 * kWarps * 32) return (int)s;
   return s >= 8 ? 8 : s >= 4 ? 4 : s >= 2 ? 2 : 1;
 }
 
@@ -1031,9 +1045,15 @@ cudaError_t launch_stream(const AttendParams &p, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, attend_stream_kernel<DP, kF32, kPlain>, p);
 }
 
-// bfloat16 calls that the streaming kernel takes: few rows over few tokens.
+// bfloat16 calls that the streaming kernel takes before the tiles' kernel: as many
+// CTAs as run at once, two an SM, with up to 4 granules a warp, or 16 of narrow
+// heads.  (us here and there: one request of 5 over 128 tokens 18.5 and 22.3, over
+// 4096 28.7 and 28.7; 4 of 1 over 777 20.6 and 20.6, over 4096 28.9 and 25.3; 16 of
+// 1 over 16 18.5 and 22.0, over 128, with 384 CTAs, 32.9 and 21.9; heads of 64, 16
+// requests of 5 over 2048 24.8 and 31.7, over 4096 37.1 and 36.7.)
 bool stream_is_quicker(const AttendParams &p) {
-  return p.stream_mode == 1;
+  const long long ctas = (long long)p.B * p.cache.Hkv * p.row_tiles * p.splits;
+  return ctas <= 304 && granules_of(p) <= (long long)p.splits * kWarps * (p.cache.D <= 64 ? 16 : 4);
 }
 
 template <bool kF32, bool kPlain>

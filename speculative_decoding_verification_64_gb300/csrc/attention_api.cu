@@ -4,7 +4,6 @@
 // their arguments before any device work.
 #include <climits>
 #include <cmath>
-#include <cstdlib>
 
 #include "attention_common.cuh"
 
@@ -219,7 +218,6 @@ int specdec_attend(const void *q, const void *k_new, const void *v_new, int dtyp
   p.lse = lse;
   p.row_status = row_status;
   p.part = reinterpret_cast<float *>(workspace);
-  { const char *e = getenv("SD_STREAM"); p.stream_mode = e ? atoi(e) : 0; }
   return cuda_status(launch_attend(p, static_cast<cudaStream_t>(stream)));
 }
 

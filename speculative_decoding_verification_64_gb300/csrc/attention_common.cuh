@@ -45,7 +45,6 @@ struct AttendParams {
   int splits, row_tiles;
   bool clustered;   // the splits are one cluster
   int block_shift;  // log2(cache.block), or -1
-  int stream_mode;
 };
 
 cudaError_t launch_rope(const RopeParams &p, cudaStream_t stream);
