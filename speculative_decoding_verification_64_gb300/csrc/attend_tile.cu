@@ -58,15 +58,15 @@ constexpr unsigned kAll = 0xffffffffu;
 template <int RN>
 struct Cfg {
   static constexpr int kCtas = RN <= 64 ? 2 : 1;       // CTAs an SM
-  static constexpr int kGroups = RN <= 64 ? 1 : 2;     // softmax groups of four warps: a part of the rows each
+  static constexpr int kGroups = RN <= 64 ? 1 : 4;     // softmax groups of four warps: a part of the rows each
   static constexpr int kWorkers = 4;                   // warps that widen V: one on each quarter of the SM
   static constexpr int kFirst = 8;                     // first softmax warp
   // Registers a thread: of the launch (what two CTAs, or one, leave room for), and
   // of the three kinds of warpgroup, which share out those of the launch:
   // kIssue + kWiden + kGroups kSoft = (2 + kGroups) kRegs
-  static constexpr int kRegs = RN <= 64 ? 80 : 128;
-  static constexpr int kIssue = RN <= 64 ? 64 : 72, kWiden = RN <= 64 ? 64 : 88;
-  static constexpr int kSoft = RN <= 64 ? 112 : 176;
+  static constexpr int kRegs = 80;
+  static constexpr int kIssue = 64, kWiden = 64;
+  static constexpr int kSoft = RN <= 64 ? 112 : 88;
   static_assert(kIssue + kWiden + kGroups * kSoft == (2 + kGroups) * kRegs, "");
   static constexpr int kThreads = 32 * (kFirst + 4 * kGroups);
   static constexpr int kCols = RN / kGroups;           // most columns of a softmax thread
@@ -134,7 +134,7 @@ struct Smem {
   uint32_t tmem;
   int give_up;
   int done[C::kGroups];                   // segments that a softmax group finished
-  long long scan[16];                     // of the plan: one a warp
+  long long scan[32];                     // of the plan: one a warp
   Plan plan;
 };
 
@@ -1126,10 +1126,6 @@ struct Tile {
 
   // The cap: y to cap tanh(y / cap), both in base-2 units; 1 - 2 / (1 + e^2u) for
   // tanh(u), absolute error below 2^-22.
-  __device__ __forceinline__ float capped(float y) const {
-    const float e = ex2_approx(y * cap_in);
-    return fmaf(cap_out, rcp_approx(1.0f + e), cap_at);
-  }
   float cap_in, cap_out, cap_at;  // 2 / softcap, -2 and 1 times softcap log2(e)
 
   // Scores of a tile that needs more than a factor, in place: capped, biased and
@@ -1183,14 +1179,37 @@ struct Tile {
         seen &= bits;
       }
       tmem_wait8(s);
+      const f2 u2 = pair(unit, unit);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        float y = s[k] * (unit * rf[k]);
-        if (!kPlain) {
-          if (cap_in > 0.0f) y = capped(y);
-          y = fmaf(sm.slope[ring][c0 + ch + k], position - sm.depth[ring][c0 + ch + k], y);  // (exact)
+      for (int k = 0; k < 8; k += 4) {
+        const ulonglong2 r = *reinterpret_cast<const ulonglong2 *>(rf + k);
+        unpair(mul2(pair(s[k], s[k + 1]), mul2(r.x, u2)), s[k], s[k + 1]);
+        unpair(mul2(pair(s[k + 2], s[k + 3]), mul2(r.y, u2)), s[k + 2], s[k + 3]);
+      }
+      if (!kPlain && cap_in > 0.0f) {
+#pragma unroll
+        for (int k = 0; k < 8; k += 2) {
+          float e, f;
+          unpair(mul2(pair(s[k], s[k + 1]), pair(cap_in, cap_in)), e, f);
+          e = rcp_approx(1.0f + ex2_approx(e));
+          f = rcp_approx(1.0f + ex2_approx(f));
+          unpair(fma2(pair(e, f), pair(cap_out, cap_out), pair(cap_at, cap_at)), s[k], s[k + 1]);
         }
-        s[k] = (seen >> k & 1u) ? y : -INFINITY;
+      }
+      if (!kPlain && p.slopes) {
+#pragma unroll
+        for (int k = 0; k < 8; k += 4) {
+          const float4 g = *reinterpret_cast<const float4 *>(&sm.slope[ring][c0 + ch + k]);
+          const float4 d = *reinterpret_cast<const float4 *>(&sm.depth[ring][c0 + ch + k]);
+          s[k] = fmaf(g.x, position - d.x, s[k]);  // (differences are exact)
+          s[k + 1] = fmaf(g.y, position - d.y, s[k + 1]);
+          s[k + 2] = fmaf(g.z, position - d.z, s[k + 2]);
+          s[k + 3] = fmaf(g.w, position - d.w, s[k + 3]);
+        }
+      }
+      if (__any_sync(kAll, seen != 0xFFu)) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s[k] = (seen >> k & 1u) ? s[k] : -INFINITY;
       }
       tmem_store8(s_at + ch, s);
     }
@@ -1539,7 +1558,6 @@ __global__ void __launch_bounds__(Cfg<RN>::kThreads, Cfg<RN>::kCtas)
       sm.moves[tid] = 0;
       sm.done[tid] = 0;
     }
-    if (tid < 4 * C::kGroups) sm.vote[tid >> 2][tid & 3] = 0;
     if (tid == 0) {
       mbar_init(&sm.q_full, C::kWorkers);
       mbar_init(&sm.q_empty, 1);
@@ -1551,6 +1569,7 @@ __global__ void __launch_bounds__(Cfg<RN>::kThreads, Cfg<RN>::kCtas)
     fence_async_smem();
   }
   if (tid < C::kCols) sm.ones[tid] = 1.0f;
+  if (tid < 4 * C::kGroups) sm.vote[tid >> 2][tid & 3] = 0;
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_addr(&sm.tmem)),
@@ -1584,8 +1603,11 @@ __global__ void __launch_bounds__(Cfg<RN>::kThreads, Cfg<RN>::kCtas)
   fence_after();
   if (sm.give_up) {
     if (warp == 0) tile.drain();
-    if (warp >= C::kFirst)
-      tile.give_up_results(p, box, plan, min(sm.done[0], sm.done[C::kGroups - 1]), tile.columns);
+    if (warp >= C::kFirst) {
+      int finished = sm.done[0];
+      for (int i = 1; i < C::kGroups; ++i) finished = min(finished, sm.done[i]);
+      tile.give_up_results(p, box, plan, finished, tile.columns);
+    }
     __syncthreads();
   }
   if (warp == 1)
