@@ -26,33 +26,65 @@ __device__ __forceinline__ float scale_for(float a) {
   return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-// 16 consecutive elements as float32 values.
+// 16 consecutive elements, as they stand in memory and as float32 values.
+template <int DT>
+struct Raw {
+  uint4 w[DT == SPECDEC_F32 ? 4 : 2];
+};
+
 template <int DT, bool kVec>
-__device__ __forceinline__ void load16(const char *in, float *x) {
-  if (!kVec) {
+__device__ __forceinline__ Raw<DT> load16(const char *in) {
+  constexpr int kWords = sizeof(Raw<DT>) / 16;
+  Raw<DT> r;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = load_elem(in, DT, i);
-  } else if (DT == SPECDEC_F32) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 w = __ldg(reinterpret_cast<const float4 *>(in) + i);
-      x[4 * i] = w.x;
-      x[4 * i + 1] = w.y;
-      x[4 * i + 2] = w.z;
-      x[4 * i + 3] = w.w;
+  for (int i = 0; i < kWords; ++i) {
+    if constexpr (kVec) {
+      r.w[i] = __ldg(reinterpret_cast<const uint4 *>(in) + i);
+      continue;
     }
-  } else {
+    uint32_t a[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint4 w = __ldg(reinterpret_cast<const uint4 *>(in) + i);
-      const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+    for (int k = 0; k < 4; ++k) {
+      if (DT == SPECDEC_F32) {
+        a[k] = __ldg(reinterpret_cast<const uint32_t *>(in) + 4 * i + k);
+      } else {
+        const unsigned short *h = reinterpret_cast<const unsigned short *>(in) + 8 * i + 2 * k;
+        a[k] = __ldg(h) | (uint32_t)__ldg(h + 1) << 16;
+      }
+    }
+    r.w[i] = make_uint4(a[0], a[1], a[2], a[3]);
+  }
+  return r;
+}
+
+template <int DT>
+__device__ __forceinline__ void values16(const Raw<DT> &r, float *x) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+  for (int i = 0; i < (int)sizeof(r) / 16; ++i) {
+    const uint32_t a[4] = {r.w[i].x, r.w[i].y, r.w[i].z, r.w[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (DT == SPECDEC_F32) {
+        x[4 * i + k] = __uint_as_float(a[k]);
+      } else {
         x[8 * i + 2 * k] = bf16_lo(a[k]);
         x[8 * i + 2 * k + 1] = bf16_hi(a[k]);
       }
     }
   }
+}
+
+// The largest finite size of 16 elements and `top`.
+template <int DT>
+__device__ __forceinline__ float top16(const Raw<DT> &r, float top) {
+  float x[16];
+  values16<DT>(r, x);
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const float a = fabsf(x[k]);
+    if (a < INFINITY) top = fmaxf(top, a);
+  }
+  return top;
 }
 
 // kT threads work on one task: 32 (a warp) or the whole CTA.
@@ -76,20 +108,21 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendParams p) {
   pdl_wait();
   pdl_launch_dependents();
   constexpr int es = DT == SPECDEC_F32 ? 4 : 2;
+  constexpr int kHeld = DT == SPECDEC_F32 ? 2 : kT == 32 ? 4 : 2;  // a thread's first values
   const specdec_kv_cache &c = p.cache;
   const int t = kT == 32 ? threadIdx.x & 31 : threadIdx.x;
   // task = ((b * blocks + m) * 2 + side) * Hkv + h
-  long long task = blockIdx.x;
+  uint32_t task = blockIdx.x;
   if (kT == 32) {
     task = task * 8 + (threadIdx.x >> 5);
-    if (task >= (long long)p.B * p.blocks * 2 * c.Hkv) return;
+    if (task >= (uint32_t)p.B * p.blocks * 2 * c.Hkv) return;
   }
-  const int h = (int)(task % c.Hkv);
-  task /= c.Hkv;
+  const int h = (int)(task % (uint32_t)c.Hkv);
+  task /= (uint32_t)c.Hkv;
   const int side = (int)(task & 1);
   task >>= 1;
-  const int m = (int)(task % p.blocks);
-  const long long b = task / p.blocks;
+  const int m = (int)(task % (uint32_t)p.blocks);
+  const long long b = task / (uint32_t)p.blocks;
 
   const int len = c.length[b];
   const long long count = (long long)(p.count ? p.count[b] : p.N) + p.extra;
@@ -99,6 +132,27 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendParams p) {
       len + count > most)
     status = SPECDEC_ROW_BAD_CACHE;
   const int first = status ? 0 : len / c.block;
+
+  // this task's tokens: slots [off, off + take) of the block, tokens j0 ...
+  const long long start = (long long)(first + m) * c.block;
+  const int off = m == 0 ? len - first * c.block : 0;
+  const long long j0 = start + off - len;
+  const int take = status ? 0 : (int)max(min((long long)(c.block - off), count - j0), 0ll);
+  const char *src = reinterpret_cast<const char *>(side ? p.v : p.k) + (long long)h * c.D * es;
+  const long long stride = (side ? p.v_stride : p.k_stride) * es;
+  const uint32_t per = c.D / 16, vecs = take * per;
+  auto load = [&](uint32_t i) {
+    const uint32_t j = i / per, e = (i - j * per) * 16;
+    int n = (int)j0 + (int)j;
+    if (p.path) n = min(max(p.path[b * p.path_len + n], 0), p.N - 1);  // (checked below)
+    return load16<DT, kVec>(src + (b * p.N + n) * stride + (int)e * es);
+  };
+  // the first values are under way while the blocks and the path are checked
+  Raw<DT> held[kHeld];
+#pragma unroll
+  for (int q = 0; q < kHeld; ++q)
+    if (t + q * kT < vecs) held[q] = load(t + q * kT);
+
   if (!status && count > 0) {
     // every task of a request checks all that the request touches, so that a
     // request is appended whole or not at all
@@ -122,32 +176,18 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendParams p) {
   }
   if (status || count == 0) return;
 
-  // this task's tokens: slots [off, off + take) of the block, tokens j0 ...
-  const long long start = (long long)(first + m) * c.block;
-  const int off = m == 0 ? len - first * c.block : 0;
-  const long long j0 = start + off - len;
-  if (j0 >= count) return;
-  const int take = (int)min((long long)(c.block - off), count - j0);
+  if (take <= 0) return;
   const int id = c.block_table[b * c.max_blocks + first + m];
   const long long cell = (long long)id * c.Hkv + h;
   uint8_t *codes = reinterpret_cast<uint8_t *>(side ? c.v : c.k) + cell * c.block * c.D;
   float *scale = (side ? c.v_scale : c.k_scale) + cell;
-  const char *src = reinterpret_cast<const char *>(side ? p.v : p.k) + (long long)h * c.D * es;
-  const long long stride = (side ? p.v_stride : p.k_stride) * es;
-  const int per = c.D / 16, vecs = take * per;
 
   float top = 0.0f;
-  for (int i = t; i < vecs; i += kT) {
-    const int j = i / per, e = (i - j * per) * 16;
-    const long long n = p.path ? p.path[b * p.path_len + j0 + j] : j0 + j;
-    float x[16];
-    load16<DT, kVec>(src + (b * p.N + n) * stride + e * es, x);
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const float a = fabsf(x[k]);
-      if (a < INFINITY) top = fmaxf(top, a);
-    }
-  }
+  for (int q = 0; q < kHeld; ++q)
+    if (t + q * kT < vecs) top = top16<DT>(held[q], top);
+#pragma unroll 1
+  for (uint32_t i = t + kHeld * kT; i < vecs; i += kT) top = top16<DT>(load(i), top);
 #pragma unroll
   for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
   if (kT > 32) {
@@ -165,7 +205,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendParams p) {
     } else {
       // the tokens that stand before: 16 codes a thread, each thread its own
       const float ratio = __fdiv_rn(was, s);
-      for (int i = t; i < off * per; i += kT) {
+      for (uint32_t i = t; i < off * per; i += kT) {
         uint4 w = reinterpret_cast<uint4 *>(codes)[i];
         uint32_t a[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -185,23 +225,25 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendParams p) {
   // x / s is exact for a power of two; an old scale of another kind needs the division
   const bool pow2 = (__float_as_uint(s) & 0x7FFFFFu) == 0;
   const float inv = pow2 ? __fdiv_rn(1.0f, s) : 0.0f;
-  for (int i = t; i < vecs; i += kT) {
-    const int j = i / per, e = (i - j * per) * 16;
-    const long long n = p.path ? p.path[b * p.path_len + j0 + j] : j0 + j;
+  auto put = [&](uint32_t i, const Raw<DT> &r) {  // (token, element) of the block: slot off + i / per
     float x[16];
-    load16<DT, kVec>(src + (b * p.N + n) * stride + e * es, x);
-    uint32_t a[4];
+    values16<DT>(r, x);
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
       const float y = pow2 ? x[k] * inv : __fdiv_rn(x[k], s);
       x[k] = finite(x[k]) ? y : __int_as_float(0x7fc00000);
     }
+    uint32_t a[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       a[k] = pack_e4m3x2(x[4 * k], x[4 * k + 1]) | pack_e4m3x2(x[4 * k + 2], x[4 * k + 3]) << 16;
-    *reinterpret_cast<uint4 *>(codes + (long long)(off + j) * c.D + e) =
-        make_uint4(a[0], a[1], a[2], a[3]);
-  }
+    reinterpret_cast<uint4 *>(codes)[off * per + i] = make_uint4(a[0], a[1], a[2], a[3]);
+  };
+#pragma unroll
+  for (int q = 0; q < kHeld; ++q)
+    if (t + q * kT < vecs) put(t + q * kT, held[q]);
+#pragma unroll 1
+  for (uint32_t i = t + kHeld * kT; i < vecs; i += kT) put(i, load(i));
 }
 
 template <int DT, bool kVec>
