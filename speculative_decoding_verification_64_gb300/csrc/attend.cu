@@ -36,6 +36,12 @@
 // cluster, that join their partials through each other's shared memory: one
 // launch.  More splits than that (few heads over a long cache) go through the
 // workspace and a second kernel.
+//
+// Takes float32 calls, heads wider than 128 elements and small bfloat16 calls.
+// Measured (8 heads of 128, G = 4): one request of 1 node over 777 tokens 20.5 us,
+// of 5 over 2048 in float32 26.6 us.  Such calls are bound by latency: about 16 us
+// pass before the first granule's products, in dependent loads and in code that
+// is not in the instruction caches yet.
 #include "attention_common.cuh"
 
 namespace specdec {

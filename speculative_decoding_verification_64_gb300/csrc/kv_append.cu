@@ -8,10 +8,15 @@
 // step; e4m3's own exponent covers the factor of two that a finer scale would
 // give.
 //
-// One task is one block of tokens, of one head, of k or of v: its values are
-// read for their maximum and again (from L1 or L2) for their codes, 16 elements
-// a thread.  Bound by HBM for prompts; a verify step's few tokens are bound by
-// latency: there a task is one warp, for many tokens it is a CTA.
+// One task is one block of tokens, of one head, of k or of v; a thread takes 16
+// elements at a time and holds its first ones in registers between the maximum
+// and the codes (only what is beyond them is read again, from L1 or L2).  A verify
+// step's few tokens are a warp's work, a prompt's blocks a CTA's.
+//
+// Measured: 8 prompts of 8191 tokens, 8 heads of 128, 123 us, 3.3 TB/s, against
+// 139 us with every value read twice; what is left is each CTA's chain of length,
+// table and values, eight or so CTAs deep on an SM.  256 requests of up to 9
+// tokens 12.3 us, the same chain once, in cold caches.
 #include "attention_common.cuh"
 
 namespace specdec {
@@ -40,19 +45,19 @@ __device__ __forceinline__ Raw<DT> load16(const char *in) {
   for (int i = 0; i < kWords; ++i) {
     if constexpr (kVec) {
       r.w[i] = __ldg(reinterpret_cast<const uint4 *>(in) + i);
-      continue;
-    }
-    uint32_t a[4];
+    } else {
+      uint32_t a[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (DT == SPECDEC_F32) {
-        a[k] = __ldg(reinterpret_cast<const uint32_t *>(in) + 4 * i + k);
-      } else {
-        const unsigned short *h = reinterpret_cast<const unsigned short *>(in) + 8 * i + 2 * k;
-        a[k] = __ldg(h) | (uint32_t)__ldg(h + 1) << 16;
+      for (int k = 0; k < 4; ++k) {
+        if (DT == SPECDEC_F32) {
+          a[k] = __ldg(reinterpret_cast<const uint32_t *>(in) + 4 * i + k);
+        } else {
+          const unsigned short *h = reinterpret_cast<const unsigned short *>(in) + 8 * i + 2 * k;
+          a[k] = __ldg(h) | (uint32_t)__ldg(h + 1) << 16;
+        }
       }
+      r.w[i] = make_uint4(a[0], a[1], a[2], a[3]);
     }
-    r.w[i] = make_uint4(a[0], a[1], a[2], a[3]);
   }
   return r;
 }
