@@ -13,9 +13,9 @@
 // and the codes (only what is beyond them is read again, from L1 or L2).  A verify
 // step's few tokens are a warp's work, a prompt's blocks a CTA's.
 //
-// Measured: 8 prompts of 8191 tokens, 8 heads of 128, 123 us, 3.3 TB/s, against
+// Measured: 8 prompts of 8191 tokens, 8 heads of 128, 111 us, 3.6 TB/s, against
 // 139 us with every value read twice; what is left is each CTA's chain of length,
-// table and values, eight or so CTAs deep on an SM.  256 requests of up to 9
+// table and values, eighteen rounds of CTAs.  256 requests of up to 9
 // tokens 12.3 us, the same chain once, in cold caches.
 #include "attention_common.cuh"
 
@@ -107,8 +107,10 @@ __device__ __forceinline__ bool task_any(bool x) {
   return __syncthreads_or(x) != 0;
 }
 
+// Six CTAs an SM for bfloat16 prompts: 111 us for the prompts above, with the 62
+// registers that the compiler would take 123, with eight CTAs 119.
 template <int DT, bool kVec, int kT>
-__global__ void __launch_bounds__(256) kv_append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(256, kT == 256 && DT != SPECDEC_F32 ? 6 : 3) kv_append_kernel(const AppendParams p) {
   __shared__ float red[8];
   pdl_wait();
   pdl_launch_dependents();
