@@ -776,6 +776,9 @@ struct Kernel {
       }
       l[i] += __shfl_xor_sync(kAll, l[i], 1);
       l[i] += __shfl_xor_sync(kAll, l[i], 2);
+      // maxima pass over NaN scores, sums do not: where all were NaN the row has a
+      // maximum of 0 from here on, as one without would count as having seen nothing
+      if (l[i] != l[i] && m[i] == -INFINITY) m[i] = 0.0f;
     }
     bad = __reduce_or_sync(kAll, bad);
     if (c == 0) {
@@ -868,24 +871,28 @@ struct Kernel {
       if (row >= R) break;
       const int n = row / p.G;
       const long long at = ((long long)b * p.N + n) * p.Hq + h * p.G + row - n * p.G;
+      // (a part under a factor of 0 takes part all the same: its sums may be NaN)
       float f[8], top = -INFINITY, total = 0.0f;
+      unsigned seen = 0;
 #pragma unroll
       for (int s = 0; s < 8; ++s) {
         f[s] = s < parts ? (joined ? remote(&sm.all_m[r], s) : sm.all_m[r]) : -INFINITY;
+        seen |= (unsigned)(f[s] > -INFINITY) << s;
         top = fmaxf(top, f[s]);
       }
 #pragma unroll
-      for (int s = 0; s < 8; ++s) {
-        f[s] = f[s] > -INFINITY ? ex2_approx(f[s] - top) : 0.0f;
-        if (s < parts && f[s] > 0.0f) total += f[s] * (joined ? remote(&sm.all_l[r], s) : sm.all_l[r]);
-      }
+      for (int s = 0; s < 8; ++s)
+        if (seen >> s & 1u) {
+          f[s] = ex2_approx(f[s] - top);
+          total += f[s] * (joined ? remote(&sm.all_l[r], s) : sm.all_l[r]);
+        }
       const bool empty = bad || n >= nodes || top == -INFINITY;
       const float inv = empty ? 0.0f : 1.0f / total;
       for (int d = lane; d < kv.D; d += 32) {
         float x = 0.0f;
 #pragma unroll
         for (int s = 0; s < 8; ++s)
-          if (s < parts && f[s] != 0.0f) x += f[s] * (joined ? remote(&sm.o[0][r][d], s) : sm.o[0][r][d]);
+          if (seen >> s & 1u) x += f[s] * (joined ? remote(&sm.o[0][r][d], s) : sm.o[0][r][d]);
         store_out(at * kv.D + d, empty ? 0.0f : x * inv);
       }
       if (lane == 0 && p.lse)
@@ -954,9 +961,12 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams p) 
   bad = __reduce_or_sync(kAll, bad);
 #pragma unroll
   for (int d = 16; d >= 1; d >>= 1) all = fmaxf(all, __shfl_xor_sync(kAll, all, d));
+  // (a part under a factor of 0 takes part all the same: its sums may be NaN)
   float f[2], sum = 0.0f;
+  unsigned seen[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
+    seen[i] = __ballot_sync(kAll, m[i] > -INFINITY);
     f[i] = m[i] > -INFINITY ? ex2_approx(m[i] - all) : 0.0f;
     sum += l[i] * f[i];
   }
@@ -973,11 +983,12 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams p) 
       float x[4][4], w[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        // (0 past the last split, and for one without tokens, whose sums are not there)
+        // (not past the last split, nor of one without tokens)
+        const bool in = (s < 32 ? seen[0] : seen[1]) >> ((s + u) & 31) & 1u;
         w[u] = __shfl_sync(kAll, s < 32 ? f[0] : f[1], (s + u) & 31);
         const float *rec = part + (s + u) * stride + 2 * kRows + r * D + d0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) x[u][k] = w[u] != 0.0f && d0 + 32 * k < D ? rec[32 * k] : 0.0f;
+        for (int k = 0; k < 4; ++k) x[u][k] = in && d0 + 32 * k < D ? rec[32 * k] : 0.0f;
       }
 #pragma unroll
       for (int u = 0; u < 4; ++u)

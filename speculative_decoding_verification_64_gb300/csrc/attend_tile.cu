@@ -1690,7 +1690,8 @@ __global__ void __launch_bounds__(32 * kJoinRows)
     sum = sum * before + l * f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) acc[k] *= before;
-    const unsigned full = __ballot_sync(kAll, f > 0.0f);
+    // (a part under a factor of 0 takes part all the same: its outputs may be NaN)
+    const unsigned full = __ballot_sync(kAll, m > -INFINITY);
 #pragma unroll 1
     for (int s = 0; full >> s; s += 4) {
       float2 x[4][2];

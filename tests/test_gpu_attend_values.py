@@ -1,0 +1,154 @@
+"""Attention of drafted tokens where its inputs are unusual: against the formula in 64 bits, on each
+way that a call can take (the streaming kernel with its splits joined in a cluster and through the
+workspace, and the tensor-core kernel).
+
+Tolerance, with p the weights of a row, S the largest scale * sum |q| |k| of it and Q the largest
+scale * (max |q| sum |k| + max |k| sum |q|):
+  * a score is off by at most 2^-19 (1 + S) for float32 activations (two fp16 terms an operand);
+    for bfloat16 ones by 2^-16 (1 + S) + 2^-17 Q: q and the drafted k are two e4m3 terms in units of
+    their largest element, in [2^7, 2^8), so what they leave is at most half of e4m3's smallest
+    step, 2^-10, which is 2^-17 of that element;
+  * a cap adds no more than 2^-20 of the score itself;
+  * weights carry 2^-11 of themselves (2^-21 in two terms), and as fp16 numbers at least 2^-25 where
+    the row's largest contribution stands at 2^5 or above: with U the largest size that a token's
+    unit can carry (448 scales, twice a drafted token's largest element), n 2^-30 max(p U) in all.
+    |out error| <= (sum p |v| (2 ds + 2 dw) + n 2^-30 max(p U)) / sum p  (+ 2^-8 |out| in bfloat16)
+    |lse error| <= ds + 2^-20 (1 + |lse|)
+"""
+import math
+
+import numpy as np
+import pytest
+
+import attention_oracle as ref
+from test_gpu_attend import tokens
+from test_gpu_attend_tiles import Large
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+F32, BF16 = torch.float32, torch.bfloat16
+WAYS = [pytest.param(d, w, id=f"{n}-{i}") for d, n in ((F32, "f32"), (BF16, "bf16"))
+        for w, i in ((False, "small"), (True, "large"))]
+ways = pytest.mark.parametrize("dtype,large", WAYS)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from speculative_decoding_verification_64_gb300 import binding, build
+    build.build()
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    return binding
+
+
+def on(lib, large):
+    """The binding, or the binding with the call made large (see test_gpu_attend_tiles.py)."""
+    return Large(lib) if large else lib
+
+
+def expected(q, k_new, v_new, parent, k, v, v_unit, length, scale, softcap=0.0, window=0):
+    """One request in float64; v_unit [length, Hkv]: 448 times the scale of each cached token.
+    Returns out, lse, sum p |v| / sum p, S, Q and n max(p U) / sum p."""
+    N, Hq, D = q.shape
+    G = Hq // k_new.shape[1]
+    out, mag, floor = (torch.zeros(N, Hq, D, dtype=torch.float64) for _ in range(3))
+    lse = torch.full((N, Hq), -math.inf, dtype=torch.float64)
+    S, Q = torch.zeros(N, Hq, dtype=torch.float64), torch.zeros(N, Hq, dtype=torch.float64)
+    for n in range(N):
+        up = ref.ancestors(parent, n)
+        where = length + len(up) - 1
+        dist = [where - j for j in range(length)] + list(range(len(up)))
+        keep = [i for i, d in enumerate(dist) if window == 0 or d < window]
+        keys = torch.cat((k, k_new[up]))[keep]
+        vals = torch.cat((v, v_new[up]))[keep]
+        units = torch.cat((v_unit, 2 * v_new[up].abs().amax(-1)))[keep]
+        for h in range(Hq):
+            kk, vv, uu = keys[:, h // G], vals[:, h // G], units[:, h // G]
+            a, b = kk.abs().nan_to_num(0, 0, 0), q[n, h].abs().nan_to_num(0, 0, 0)
+            S[n, h] = (a @ b).max() * abs(scale)
+            Q[n, h] = (a.sum(-1) * b.max() + a.amax(-1) * b.sum()).max() * abs(scale)
+            s = kk @ q[n, h] * scale
+            if softcap:
+                s = softcap * torch.tanh(s / softcap)
+            if float(s.max()) == -math.inf:
+                continue
+            p = torch.exp(s - s.max())
+            lse[n, h] = torch.log(p.sum()) + s.max()
+            out[n, h] = (p / p.sum()) @ vv
+            mag[n, h] = (p / p.sum()) @ vv.abs()
+            floor[n, h] = len(keep) * float((p / p.sum() * uu).max())
+    return out, lse, mag, S, Q, floor
+
+
+def check(r, q, k, v, cache, block, parents, scale, **how):
+    f32 = q.dtype == F32
+    got, lse = r.out.double().cpu(), r.lse.double().cpu()
+    for b in range(q.shape[0]):
+        kc, vc = (ref.cached_values(cache, n, b, block) for n in ("k", "v"))
+        n = int(cache["length"][b])
+        ids = cache["block_table"][b, :-(-n // block)].long()
+        unit = 448 * cache["v_scale"][ids].double().repeat_interleave(block, 0)[:n]
+        want, wl, A, S, Q, floor = expected(
+            q[b].double().cpu(), k[b].double().cpu(), v[b].double().cpu(),
+            None if parents is None else parents[b], kc, vc, unit, n, scale, **how)
+        ds = 2.0 ** (-19 if f32 else -16) * (1 + S) + (0 if f32 else 2.0 ** -17) * Q + \
+            (2.0 ** -20 * S if how.get("softcap") else 0)
+        dw = 2.0 ** (-21 if f32 else -11)
+        tol = A * (2 * ds + 2 * dw)[..., None] + 2.0 ** -30 * floor
+        if not f32:
+            tol = tol + want.abs() * 2.0 ** -8
+        assert torch.equal(torch.isnan(lse[b]), torch.isnan(wl)), b
+        empty = wl == -math.inf
+        assert (got[b][empty] == 0).all() and (lse[b][empty] == -math.inf).all(), b
+        bad = ~torch.isfinite(want)
+        assert torch.equal(torch.isfinite(got[b]), ~bad), b
+        err = torch.where(bad, 0.0, (got[b] - want).abs())
+        assert (err <= torch.where(bad, 1.0, tol)).all(), \
+            (b, float((err - tol).nan_to_num(-1).max()), float(err.max()))
+        ok = torch.isfinite(wl)
+        assert ((lse[b] - wl).abs()[ok] <= (ds + 2.0 ** -20 * (1 + wl.abs()))[ok]).all(), b
+    assert (r.row_status.cpu() == 0).all()
+
+
+# ---- scores that are not a number ----
+
+@ways
+@pytest.mark.parametrize("Hkv,D", [(2, 128), (1, 64)])
+def test_a_query_that_is_not_a_number(lib, dtype, large, Hkv, D):
+    """Its row is NaN, in out and in lse, and no other row."""
+    rng = np.random.default_rng(1)
+    lens, N, Hq, block = [40, 0, 17], 3, 4 * Hkv, 16
+    q, k, v = tokens(rng, 3, N, Hq, Hkv, D, dtype)
+    q[0, 1, 2, 5] = q[1, 0, 0, 0] = q[2, 2, 3, D - 1] = float("nan")
+    cache = ref.make_cache(rng, lens, [0] * 3, block, Hkv, D)
+    r = on(lib, large).attend(q, k, v, ref.on_gpu(cache))
+    check(r, q, k, v, cache, block, None, D ** -0.5)
+    assert torch.isnan(r.out[0, 1, 2]).all() and torch.isnan(r.lse[1, 0, 0])
+
+
+@ways
+@pytest.mark.parametrize("lens", [[64, 0, 33], [1, 16, 500]])
+def test_a_lone_drafted_key_that_is_not_a_number(lib, dtype, large, lens):
+    rng = np.random.default_rng(2)
+    q, k, v = tokens(rng, 3, 1, 4, 2, 128, dtype)
+    k[:, 0, 1, 7] = float("nan")
+    cache = ref.make_cache(rng, lens, [0] * 3, 16, 2, 128)
+    check(on(lib, large).attend(q, k, v, ref.on_gpu(cache)), q, k, v, cache, 16, None, 128 ** -0.5)
+
+
+@ways
+@pytest.mark.parametrize("scale", [0.0884, 4.0])
+@pytest.mark.parametrize("at", ["last", "first"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_cached_key_that_is_not_a_number(lib, dtype, large, scale, at, D):
+    """Alone in its granule of 16 tokens, also where all other scores are far above or below 0, so
+    that its part of the sums comes under a factor of 0."""
+    rng = np.random.default_rng(3)
+    lens, N, block = [33, 17, 1, 65, 529], 2, 16
+    q, k, v = tokens(rng, len(lens), N, 2, 1, D, dtype)
+    cache = ref.make_cache(rng, lens, [0] * len(lens), block, 1, D)
+    for b, n in enumerate(lens):
+        j = n - 1 if at == "last" else 0
+        cache["k"][cache["block_table"][b, j // block], 0, j % block, 11] = 0x7F
+    check(on(lib, large).attend(q, k, v, ref.on_gpu(cache), scale=scale), q, k, v, cache, block,
+          None, scale)
