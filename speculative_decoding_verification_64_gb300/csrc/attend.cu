@@ -1024,7 +1024,8 @@ int most_splits(long long B, int N, int Hkv, int G) {
 // Granules that a request can hold: of what its blocks hold, or the window leaves.
 long long granules_of(const AttendParams &p) {
   long long tokens = (long long)p.cache.max_blocks * p.cache.block;
-  if (p.window > 0 && tokens > p.window + kGran) tokens = p.window + kGran;
+  const long long reach = (long long)p.window + kGran;
+  if (p.window > 0 && tokens > reach) tokens = reach;
   return (tokens + kGran - 1) / kGran + (p.N + kGran - 1) / kGran;
 }
 // ... and no more than leave each warp a granule where the cache is full; up to

@@ -152,3 +152,20 @@ def test_a_cached_key_that_is_not_a_number(lib, dtype, large, scale, at, D):
         cache["k"][cache["block_table"][b, j // block], 0, j % block, 11] = 0x7F
     check(on(lib, large).attend(q, k, v, ref.on_gpu(cache), scale=scale), q, k, v, cache, block,
           None, scale)
+
+
+# ---- windows of any size ----
+
+@ways
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 17, 2 ** 30])
+def test_a_window_past_every_length_changes_nothing(lib, dtype, large, window):
+    rng = np.random.default_rng(9)
+    lens, N, Hq, Hkv, D, block = [3000, 700], 5, 8, 2, 128, 16
+    q, k, v = tokens(rng, 2, N, Hq, Hkv, D, dtype)
+    cache = ref.make_cache(rng, lens, [0] * 2, block, Hkv, D)
+    if large:   # room for many more tokens
+        cache["block_table"] = torch.cat([cache["block_table"],
+                                          torch.full((2, 2500), -1, dtype=torch.int32)], 1)
+    a, b = (lib.attend(q, k, v, ref.on_gpu(cache), window=w) for w in (0, window))
+    assert torch.equal(a.out, b.out) and torch.equal(a.lse, b.lse)
+    check(b, q, k, v, cache, block, None, D ** -0.5)
