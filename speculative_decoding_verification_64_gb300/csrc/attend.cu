@@ -146,13 +146,15 @@ struct Kernel {
     if (kPlain) return s;
     if (p.softcap > 0.0f) {
       const float y = s / p.softcap;
-      float t;
       if (kF32) {
-        t = tanhf(y);
+        s = tanhf(y) * p.softcap;
+      } else if (fabsf(y) < kTanhNear) {
+        const float y2 = y * y;
+        s *= fmaf(fmaf(fmaf(fmaf((float)kTanh4, y2, (float)kTanh3), y2, (float)kTanh2), y2,
+                       (float)kTanh1), y2, 1.0f);
       } else {  // 1 - 2 / (1 + e^2y): absolute error below 2^-22
-        t = 1.0f - __fdividef(2.0f, 1.0f + ex2_approx(y * (2.0f * kLog2e)));
+        s = (1.0f - __fdividef(2.0f, 1.0f + ex2_approx(y * (2.0f * kLog2e)))) * p.softcap;
       }
-      s = t * p.softcap;
     }
     if (p.slopes) s -= slope[i] * (float)dist;
     return s * kLog2e;

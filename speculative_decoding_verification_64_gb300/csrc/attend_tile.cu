@@ -279,6 +279,11 @@ __device__ __forceinline__ float min_nan(float a, float b) {  // NaN if one is
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
   return y;
 }
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -578,7 +583,8 @@ struct Tile {
         g_magic((uint32_t)(0xFFFFFFFFu / (uint32_t)p_.G) + 1u) {
     columns = (min(RN, p.N * p.G) + 15) / 16 * 16;
     if (!kPlain) {
-      cap_in = p.softcap > 0.0f ? 2.0f / p.softcap : 0.0f;
+      // (finite, so that a score of 0 stays 0 under the smallest caps)
+      cap_in = p.softcap > 0.0f ? fminf(2.0f / p.softcap, 3.4e38f) : 0.0f;
       cap_at = p.softcap * kLog2e;
       cap_out = -2.0f * cap_at;
     }
@@ -1137,9 +1143,38 @@ struct Tile {
     return ok;
   }
 
-  // The cap: y to cap tanh(y / cap), both in base-2 units; 1 - 2 / (1 + e^2u) for
-  // tanh(u), absolute error below 2^-22.
+  // The cap: y to cap tanh(y / cap), both in base-2 units.  With u = y / cap and z =
+  // 2 u log2(e): where all of a warp's scores are near 0, as most are under the caps that
+  // models have, y times the series of tanh(u) / u; else 1 - 2 / (1 + 2^z) for tanh(u),
+  // absolute error below 2^-22, in place of the series for those that are not near.
   float cap_in, cap_out, cap_at;  // 2 / softcap, -2 and 1 times softcap log2(e)
+  __device__ __forceinline__ void cap8(float *s) const {
+    constexpr double kU = 0.34657359027997264, kU2 = kU * kU;  // u = z ln(2) / 2
+    constexpr float kNear = (float)(kTanhNear / kU);
+    float z[8], far = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) {
+      const f2 y = pair(s[k], s[k + 1]), zz = mul2(y, pair(cap_in, cap_in)), x = mul2(zz, zz);
+      constexpr float c1 = (float)(kTanh1 * kU2), c2 = (float)(kTanh2 * kU2 * kU2),
+                      c3 = (float)(kTanh3 * kU2 * kU2 * kU2),
+                      c4 = (float)(kTanh4 * kU2 * kU2 * kU2 * kU2);
+      f2 t = fma2(pair(c4, c4), x, pair(c3, c3));
+      t = fma2(t, x, pair(c2, c2));
+      t = fma2(t, x, pair(c1, c1));
+      t = fma2(t, x, pair(1.0f, 1.0f));
+      unpair(zz, z[k], z[k + 1]);
+      unpair(mul2(y, t), s[k], s[k + 1]);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) far = max_nan(far, fabsf(z[k]));
+    if (__any_sync(kAll, !(far < kNear))) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float t = fmaf(rcp_approx(1.0f + ex2_approx(z[k])), cap_out, cap_at);
+        s[k] = fabsf(z[k]) < kNear ? s[k] : t;
+      }
+    }
+  }
 
   // Scores of a tile that needs more than a factor, in place: capped, biased and
   // masked, in base-2 units.  tok: the thread's token; unit: its k's.
@@ -1199,16 +1234,7 @@ struct Tile {
         unpair(mul2(pair(s[k], s[k + 1]), mul2(r.x, u2)), s[k], s[k + 1]);
         unpair(mul2(pair(s[k + 2], s[k + 3]), mul2(r.y, u2)), s[k + 2], s[k + 3]);
       }
-      if (!kPlain && cap_in > 0.0f) {
-#pragma unroll
-        for (int k = 0; k < 8; k += 2) {
-          float e, f;
-          unpair(mul2(pair(s[k], s[k + 1]), pair(cap_in, cap_in)), e, f);
-          e = rcp_approx(1.0f + ex2_approx(e));
-          f = rcp_approx(1.0f + ex2_approx(f));
-          unpair(fma2(pair(e, f), pair(cap_out, cap_out), pair(cap_at, cap_at)), s[k], s[k + 1]);
-        }
-      }
+      if (!kPlain && cap_in > 0.0f) cap8(s);
       if (!kPlain && p.slopes) {
 #pragma unroll
         for (int k = 0; k < 8; k += 4) {

@@ -96,6 +96,13 @@ __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
   return r;
 }
 
+// tanh(u) / u by its Taylor series, 1 + kTanh1 u^2 + ... + kTanh4 u^8, for sizes of u
+// below kTanhNear: the terms alternate and fall, so the error is below the next one,
+// 1382 / 155925 u^10 < 2^-26.  As a factor of the score it keeps the score's own bits
+// under a cap of any size, where cap (1 - 2 / (1 + e^2u)) is off by 2^-22 of the cap.
+constexpr float kTanhNear = 0.25f;
+constexpr double kTanh1 = -1.0 / 3, kTanh2 = 2.0 / 15, kTanh3 = -17.0 / 315, kTanh4 = 62.0 / 2835;
+
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
 
 #endif

@@ -169,3 +169,18 @@ def test_a_window_past_every_length_changes_nothing(lib, dtype, large, window):
     a, b = (lib.attend(q, k, v, ref.on_gpu(cache), window=w) for w in (0, window))
     assert torch.equal(a.out, b.out) and torch.equal(a.lse, b.lse)
     check(b, q, k, v, cache, block, None, D ** -0.5)
+
+
+# ---- caps of any size ----
+
+@ways
+@pytest.mark.parametrize("softcap", [1e-40, 1e-3, 0.5, 12.0, 30.0, 50.0, 1e4, 1e6, 1e7, 1e8, 1e20,
+                                     3e38])
+def test_caps_of_any_size(lib, dtype, large, softcap):
+    rng = np.random.default_rng(4)
+    lens, N, Hq, Hkv, D, block = [50, 0, 131], 5, 4, 2, 128, 16
+    q, k, v = tokens(rng, 3, N, Hq, Hkv, D, dtype)
+    q[0, 0] = 0
+    cache = ref.make_cache(rng, lens, [0] * 3, block, Hkv, D)
+    r = on(lib, large).attend(q, k, v, ref.on_gpu(cache), softcap=softcap)
+    check(r, q, k, v, cache, block, None, D ** -0.5, softcap=softcap)
