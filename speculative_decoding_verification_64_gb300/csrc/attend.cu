@@ -24,11 +24,17 @@
 // rounding of a bfloat16 result) around 2^6, so that weights down to 2^-20 of
 // the largest keep all of them.  Float32 activations are split into two fp16
 // terms each (22 bits) and the products repeated.  Maximum, sum and the
-// accumulators are float32.  The accumulators are in units of the largest
-// v scale so far; p carries the ratio of a block's scale to it.
+// accumulators are float32.
+//
+// A block's v scale, u = 2^k f with f in [1, 2), rides on the weights, whose fp16
+// range has to fit what a row sees and nothing else: each row has a maximum m of its
+// scores, for the sum, and one of s' - m + k, ko, for the outputs.  The products'
+// weights are 2^(s' - m + k - ko) f: a token that the row does not see, or sees with
+// next to no weight, leaves them alone whatever its size.  Both maxima are rounded up
+// to integers, so that factors between them are exact.
 //
 // The drafted tokens' own k and v take the same path as granules of 16 nodes,
-// scaled to fp16 by a power of two per node.  Where a mask hides part of a
+// scaled to fp16 by a power of two per node (f = 1).  Where a mask hides part of a
 // granule, non-finite v are taken out of the products (0 * NaN would reach rows
 // that do not see them) and added to the rows that do.
 //
@@ -55,8 +61,8 @@ constexpr float kRaise = 8.0f;  // the maximum moves when a score passes it by t
 constexpr float kLift = 6.0f;   // p = 2^(s' - m + kLift) <= 2^14: inside fp16
 constexpr unsigned kAll = 0xffffffffu;
 
-// A partial: m[16], l[16], then O[16][D]; a row's flags ride in l (< 0).
-__host__ __device__ inline size_t partial_floats(int D) { return (size_t)kRows * (D + 2); }
+// A partial: m[16], l[16], ko[16], then O[16][D]; a row's flags ride in l (< 0).
+__host__ __device__ inline size_t partial_floats(int D) { return (size_t)kRows * (D + 3); }
 
 __device__ __forceinline__ void mma16816(float *c, const uint32_t *a, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -73,6 +79,20 @@ __device__ __forceinline__ float pow2i(int k) { return __uint_as_float((uint32_t
 // top / 2^k is in [2^10, 2^11), clear of fp16's subnormals at both terms.
 __device__ __forceinline__ int unit_exponent(float top) {
   return min(max((int)(__float_as_uint(top) >> 23) - 127 - 10, -126), 126);
+}
+
+// x = 2^k f: k, and f in [1, 2), for x >= 0 (f below 1 where x is below 2^-126).
+__device__ __forceinline__ void split_unit(float x, float &k, float &f) {
+  const uint32_t u = __float_as_uint(x);
+  const bool normal = u >= 0x800000u;
+  k = normal ? (float)((int)(u >> 23) - 127) : -126.0f;
+  f = normal ? __uint_as_float((u & 0x7FFFFFu) | 0x3F800000u) : x * 0x1p126f;
+}
+
+// x 2^e for an integer e of any size (both factors are normal numbers).
+__device__ __forceinline__ float times_pow2(float x, float e) {
+  const int n = (int)fminf(fmaxf(e, -252.0f), 252.0f), half = n / 2;
+  return x * pow2i(half) * pow2i(n - half);
 }
 
 __device__ __forceinline__ uint4 ldg_stream(const uint8_t *p) {
@@ -103,8 +123,8 @@ struct Kernel {
     uint4 q_lo[kF32 ? KS : 1][32];      // the low terms of float32 activations
     float q_exp[kRows];                 // 2^e taken out of each row
     float o[2][kRows][DP + 4];          // joining of the warps; o[0]: the CTA's sums
-    float m[kWarps][kRows], l[kWarps][kRows];
-    float all_m[kRows], all_l[kRows];   // the CTA's
+    float m[kWarps][kRows], l[kWarps][kRows], ko[kWarps][kRows];
+    float all_m[kRows], all_l[kRows], all_ko[kRows];   // the CTA's
     int bad[kWarps], all_bad;
   };
 
@@ -117,7 +137,7 @@ struct Kernel {
   int node[2], pos[2];
   bool live[2];
   float rf[2], slope[2];
-  float m[2], l[2], vref;
+  float m[2], l[2], ko[2];  // maximum and sum of the scores; maximum with the units, from m
   float o[NT][4];
 
   __device__ Kernel(const AttendParams &p_, Smem &s_)
@@ -160,64 +180,62 @@ struct Kernel {
     return s * kLog2e;
   }
 
-  // One granule's softmax: x[nt][0..3] are base-2 scores (hidden ones -inf);
-  // returns p as A operands, scaled by v_unit (per own token, over vref), and
-  // adds to l.  Lanes of a quad share rows.
-  template <int kU>
-  __device__ __forceinline__ void raise(const float (*x)[2][4]) {
-    float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-    for (int u = 0; u < kU; ++u)
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          top[i] = fmaxf(top[i], fmaxf(x[u][nt][2 * i], x[u][nt][2 * i + 1]));
+  // One granule's softmax: x[nt][0..3] are base-2 scores (hidden ones -inf), k[0..3]
+  // the exponents of the v units of tokens 2c, 2c+1, 2c+8, 2c+9 (kSame: all alike).
+  // The maxima move where a score passes them.  Lanes of a quad share rows.
+  template <bool kSame>
+  __device__ __forceinline__ void raise(const float (*x)[4], const float *k) {
+    float to[2], at[2], best[2];  // m as it would be, where ko would stand from there, and the largest
     bool need = false;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      top[i] = fmaxf(top[i], __shfl_xor_sync(kAll, top[i], 1));
-      top[i] = fmaxf(top[i], __shfl_xor_sync(kAll, top[i], 2));
-      need |= top[i] > m[i] + kRaise;  // also the first time: m = -inf
+      float top = fmaxf(fmaxf(x[0][2 * i], x[0][2 * i + 1]), fmaxf(x[1][2 * i], x[1][2 * i + 1]));
+      top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
+      to[i] = fmaxf(m[i], ceilf(top));
+      at[i] = m[i] == -INFINITY ? -INFINITY : ko[i] + (m[i] - to[i]);
+      const float from = to[i] == -INFINITY ? 0.0f : to[i];
+      if (kSame) {
+        best[i] = top - from + k[0];
+      } else {
+        best[i] = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) best[i] = fmaxf(best[i], x[j >> 1][2 * i + (j & 1)] - from + k[j]);
+        best[i] = fmaxf(best[i], __shfl_xor_sync(kAll, best[i], 1));
+        best[i] = fmaxf(best[i], __shfl_xor_sync(kAll, best[i], 2));
+      }
+      need |= top > m[i] + kRaise || best[i] > at[i] + kRaise;  // also the first time: -inf
     }
     if (__any_sync(kAll, need)) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float to = fmaxf(m[i], top[i]);
-        const float f = m[i] == -INFINITY ? 0.0f : ex2_approx(m[i] - to);
-        l[i] *= f;
+        l[i] *= m[i] == -INFINITY ? 0.0f : ex2_approx(m[i] - to[i]);
+        ko[i] = fmaxf(at[i], ceilf(best[i]));
+        const float f = at[i] == -INFINITY ? 0.0f : ex2_approx(at[i] - ko[i]);
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           o[j][2 * i] *= f;
           o[j][2 * i + 1] *= f;
         }
-        m[i] = to;
+        m[i] = to[i];
       }
     }
   }
 
-  __device__ __forceinline__ void raise_unit(float unit) {
-    if (unit > vref) {  // the same in all lanes
-      const float f = __fdividef(vref, unit);
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[j][e] *= f;
-      vref = unit;
-    }
-  }
-
-  // p of one granule; unit[0..3]: v units over vref of tokens 2c, 2c+1, 2c+8, 2c+9.
-  __device__ __forceinline__ void weights(const float (*x)[4], const float *unit, uint32_t *a,
-                                          uint32_t *a_lo) {
+  // Adds p to l, and returns the products' weights as A operands; k and f: the v units
+  // 2^k f of tokens 2c, 2c+1, 2c+8, 2c+9.
+  __device__ __forceinline__ void weights(const float (*x)[4], const float *k, const float *f,
+                                          uint32_t *a, uint32_t *a_lo) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float at = m[i] == -INFINITY ? 0.0f : m[i] - kLift;
+      const float ato = ko[i] == -INFINITY ? 0.0f : ko[i];
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt) {
-        const float p0 = ex2_approx(x[nt][2 * i] - at), p1 = ex2_approx(x[nt][2 * i + 1] - at);
-        l[i] += p0 + p1;
-        const float w0 = p0 * unit[2 * nt], w1 = p1 * unit[2 * nt + 1];
+        const float x0 = x[nt][2 * i] - at, x1 = x[nt][2 * i + 1] - at;
+        l[i] += ex2_approx(x0) + ex2_approx(x1);
+        const float w0 = ex2_approx(x0 + (k[2 * nt] - ato)) * f[2 * nt];
+        const float w1 = ex2_approx(x1 + (k[2 * nt + 1] - ato)) * f[2 * nt + 1];
         const uint32_t w = pack_half2(w0, w1);
         a[2 * nt + i] = w;
         if (kF32)
@@ -429,15 +447,15 @@ struct Kernel {
             for (int e = 0; e < 4; ++e) s[u][nt][e] = -INFINITY;
         }
       }
-      raise<U>(s);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (t0 + u * kStep < to) {
-          raise_unit(w[u].vs);
-          const float r = __fdividef(w[u].vs, vref);
-          const float unit[4] = {r, r, r, r};
+          float uk, uf;
+          split_unit(w[u].vs, uk, uf);
+          const float k[4] = {uk, uk, uk, uk}, f[4] = {uf, uf, uf, uf};
+          raise<true>(s[u], k);
           uint32_t a[4], a_lo[4];
-          weights(s[u], unit, a, a_lo);
+          weights(s[u], k, f, a, a_lo);
           values(w[u], a, a_lo);
         }
         if (t0 + (U + u) * kStep < to) load(w[u], t0 + (U + u) * kStep, next[u]);
@@ -558,12 +576,9 @@ struct Kernel {
         const int dist = p.slopes && seen ? pos[i] - len - depth_of(j0 + t) : 0;
         s[0][nt][e] = seen ? score(s[0][nt][e], unit, i, dist) : -INFINITY;
       }
-    raise<1>(s);
-
     // p v, the node's v in units of its size; tokens 2c, 2c + 1, 2c + 8, 2c + 9
     float4 x[4][VB / 4];
-    float unit_v[4], inv_v[4];
-    float top_unit = 0.0f;
+    float unit_v[4], inv_v[4];  // the unit's exponent, and 1 / unit
     unsigned hit = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -595,18 +610,14 @@ struct Kernel {
 #pragma unroll
       for (int d = 4; d <= 16; d <<= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
       const int ex = unit_exponent(top);
-      unit_v[j] = pow2i(ex);
+      unit_v[j] = (float)ex;
       inv_v[j] = pow2i(-ex);
-      top_unit = fmaxf(top_unit, unit_v[j]);
     }
     hit = __reduce_or_sync(kAll, hit);
-    top_unit = fmaxf(top_unit, __shfl_xor_sync(kAll, top_unit, 1));
-    top_unit = fmaxf(top_unit, __shfl_xor_sync(kAll, top_unit, 2));
-    raise_unit(top_unit);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) unit_v[j] = __fdividef(unit_v[j], vref);
+    raise<false>(s[0], unit_v);
+    const float one[4] = {1.0f, 1.0f, 1.0f, 1.0f};
     uint32_t a[4], a_lo[4];
-    weights(s[0], unit_v, a, a_lo);
+    weights(s[0], unit_v, one, a, a_lo);
 #pragma unroll
     for (int i = 0; i < VB / 4; ++i)
 #pragma unroll
@@ -736,7 +747,6 @@ struct Kernel {
     }
     __syncthreads();
 
-    vref = 0x1p-126f;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = g + 8 * i, row = row0 + r;
@@ -745,7 +755,7 @@ struct Kernel {
       pos[i] = len + (live[i] && (p.slopes || p.window > 0) ? depth_of(node[i]) : 0);
       rf[i] = (kPlain ? p.scale * kLog2e : p.scale) * sm.q_exp[r];
       slope[i] = (p.slopes && live[i]) ? p.slopes[h * p.G + row - node[i] * p.G] : 0.0f;
-      m[i] = -INFINITY;
+      m[i] = ko[i] = -INFINITY;
       l[i] = 0.0f;
     }
 #pragma unroll
@@ -773,14 +783,14 @@ struct Kernel {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       if (!live[i]) {
-        m[i] = -INFINITY;
+        m[i] = ko[i] = -INFINITY;
         l[i] = 0.0f;
       }
       l[i] += __shfl_xor_sync(kAll, l[i], 1);
       l[i] += __shfl_xor_sync(kAll, l[i], 2);
       // maxima pass over NaN scores, sums do not: where all were NaN the row has a
       // maximum of 0 from here on, as one without would count as having seen nothing
-      if (l[i] != l[i] && m[i] == -INFINITY) m[i] = 0.0f;
+      if (l[i] != l[i] && m[i] == -INFINITY) m[i] = ko[i] = 0.0f;
     }
     bad = __reduce_or_sync(kAll, bad);
     if (c == 0) {
@@ -788,21 +798,24 @@ struct Kernel {
       for (int i = 0; i < 2; ++i) {
         sm.m[warp][g + 8 * i] = m[i];
         sm.l[warp][g + 8 * i] = l[i];
+        sm.ko[warp][g + 8 * i] = ko[i];
       }
     }
     if (lane == 0) sm.bad[warp] = bad;
     __syncthreads();
-    // every warp moves to the common maximum and to true units
-    float all[2], sum[2];
+    // every warp moves to the common maxima
+    float all[2], all_o[2], sum[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = g + 8 * i;
-      all[i] = -INFINITY;
+      all[i] = all_o[i] = -INFINITY;
       for (int w = 0; w < kWarps; ++w) all[i] = fmaxf(all[i], sm.m[w][r]);
+      for (int w = 0; w < kWarps; ++w)
+        if (sm.m[w][r] > -INFINITY) all_o[i] = fmaxf(all_o[i], sm.m[w][r] - all[i] + sm.ko[w][r]);
       sum[i] = 0.0f;
       for (int w = 0; w < kWarps; ++w)
         if (sm.m[w][r] > -INFINITY) sum[i] += sm.l[w][r] * ex2_approx(sm.m[w][r] - all[i]);
-      const float f = m[i] > -INFINITY ? ex2_approx(m[i] - all[i]) * vref : 0.0f;
+      const float f = m[i] > -INFINITY ? ex2_approx(m[i] - all[i] + ko[i] - all_o[i]) : 0.0f;
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         o[j][2 * i] = m[i] > -INFINITY ? o[j][2 * i] * f : 0.0f;
@@ -840,6 +853,7 @@ struct Kernel {
         for (int i = 0; i < 2; ++i) {
           sm.all_m[g + 8 * i] = all[i];
           sm.all_l[g + 8 * i] = sum[i];
+          sm.all_ko[g + 8 * i] = all_o[i];
         }
       if (lane == 0) sm.all_bad = bad;
     }
@@ -855,10 +869,11 @@ struct Kernel {
       float *part = p.part + ((((long long)b * kv.Hkv + h) * p.row_tiles + tile) * p.splits + split) *
                                  partial_floats(kv.D);
       for (int i = threadIdx.x; i < kRows * kv.D; i += kThreads)
-        part[2 * kRows + i] = sm.o[0][i / kv.D][i % kv.D];
+        part[3 * kRows + i] = sm.o[0][i / kv.D][i % kv.D];
       if (threadIdx.x < kRows) {
         part[threadIdx.x] = sm.all_m[threadIdx.x];
         part[kRows + threadIdx.x] = bad ? -(float)bad : sm.all_l[threadIdx.x];
+        part[2 * kRows + threadIdx.x] = sm.all_ko[threadIdx.x];
       }
       return;
     }
@@ -874,7 +889,7 @@ struct Kernel {
       const int n = row / p.G;
       const long long at = ((long long)b * p.N + n) * p.Hq + h * p.G + row - n * p.G;
       // (a part under a factor of 0 takes part all the same: its sums may be NaN)
-      float f[8], top = -INFINITY, total = 0.0f;
+      float f[8], fo[8], top = -INFINITY, top_o = -INFINITY, total = 0.0f;
       unsigned seen = 0;
 #pragma unroll
       for (int s = 0; s < 8; ++s) {
@@ -885,17 +900,21 @@ struct Kernel {
 #pragma unroll
       for (int s = 0; s < 8; ++s)
         if (seen >> s & 1u) {
-          f[s] = ex2_approx(f[s] - top);
-          total += f[s] * (joined ? remote(&sm.all_l[r], s) : sm.all_l[r]);
+          total += ex2_approx(f[s] - top) * (joined ? remote(&sm.all_l[r], s) : sm.all_l[r]);
+          fo[s] = f[s] - top + (joined ? remote(&sm.all_ko[r], s) : sm.all_ko[r]);
+          top_o = fmaxf(top_o, fo[s]);
         }
+#pragma unroll
+      for (int s = 0; s < 8; ++s)
+        if (seen >> s & 1u) fo[s] = ex2_approx(fo[s] - top_o);
       const bool empty = bad || n >= nodes || top == -INFINITY;
       const float inv = empty ? 0.0f : 1.0f / total;
       for (int d = lane; d < kv.D; d += 32) {
         float x = 0.0f;
 #pragma unroll
         for (int s = 0; s < 8; ++s)
-          if (seen >> s & 1u) x += f[s] * (joined ? remote(&sm.o[0][r][d], s) : sm.o[0][r][d]);
-        store_out(at * kv.D + d, empty ? 0.0f : x * inv);
+          if (seen >> s & 1u) x += fo[s] * (joined ? remote(&sm.o[0][r][d], s) : sm.o[0][r][d]);
+        store_out(at * kv.D + d, empty ? 0.0f : times_pow2(x * inv, top_o));
       }
       if (lane == 0 && p.lse)
         p.lse[at] = empty ? -INFINITY : (top - kLift + log2f(total)) * 0.6931471805599453f;
@@ -949,14 +968,15 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams p) 
   const float *part = p.part + (((b * Hkv + h) * p.row_tiles + row / kRows) * p.splits) * stride;
   const int r = row % kRows;
   // lane s holds split s and s + 32
-  float m[2], l[2];
+  float m[2], l[2], ko[2];
   int bad = 0;
-  float all = -INFINITY;
+  float all = -INFINITY, all_o = -INFINITY;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int s = lane + 32 * i;
     m[i] = s < p.splits ? part[s * stride + r] : -INFINITY;
     l[i] = s < p.splits ? part[s * stride + kRows + r] : 0.0f;
+    ko[i] = s < p.splits ? part[s * stride + 2 * kRows + r] : 0.0f;
     if (l[i] < 0.0f) bad |= (int)-l[i];
     all = fmaxf(all, m[i]);
   }
@@ -969,9 +989,17 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams p) 
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     seen[i] = __ballot_sync(kAll, m[i] > -INFINITY);
-    f[i] = m[i] > -INFINITY ? ex2_approx(m[i] - all) : 0.0f;
-    sum += l[i] * f[i];
+    f[i] = m[i] - all;
+    if (m[i] > -INFINITY) {
+      sum += l[i] * ex2_approx(f[i]);
+      f[i] += ko[i];
+      all_o = fmaxf(all_o, f[i]);
+    }
   }
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) all_o = fmaxf(all_o, __shfl_xor_sync(kAll, all_o, d));
+#pragma unroll
+  for (int i = 0; i < 2; ++i) f[i] = m[i] > -INFINITY ? ex2_approx(f[i] - all_o) : 0.0f;
 #pragma unroll
   for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
   const bool empty = bad != 0 || all == -INFINITY;
@@ -988,7 +1016,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams p) 
         // (not past the last split, nor of one without tokens)
         const bool in = (s < 32 ? seen[0] : seen[1]) >> ((s + u) & 31) & 1u;
         w[u] = __shfl_sync(kAll, s < 32 ? f[0] : f[1], (s + u) & 31);
-        const float *rec = part + (s + u) * stride + 2 * kRows + r * D + d0;
+        const float *rec = part + (s + u) * stride + 3 * kRows + r * D + d0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) x[u][k] = in && d0 + 32 * k < D ? rec[32 * k] : 0.0f;
       }
@@ -1001,7 +1029,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams p) 
     for (int k = 0; k < 4; ++k) {
       const int d = d0 + 32 * k;
       if (d >= D) continue;
-      const float y = empty ? 0.0f : acc[k] * inv;
+      const float y = empty ? 0.0f : times_pow2(acc[k] * inv, all_o);
       if (p.dtype == SPECDEC_F32)
         reinterpret_cast<float *>(p.out)[at * D + d] = y;
       else

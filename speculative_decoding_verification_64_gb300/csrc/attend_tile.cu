@@ -28,7 +28,13 @@
 //     does not fit it costs most.  Unrolled, with both in registers, 256 requests
 //     of 9 nodes over 4096 tokens took 583 us, rolled 473; loops over 16 rows in
 //     place of 8 cost 11 % more.
-//   * V's block scales ride on P, over a running unit (of the largest so far).
+//   * V's units (block scales, or a drafted token's power of two), u = 2^k f with f in
+//     [1, 2), ride on P.  P's fp16 range has to fit what a row sees and nothing else, so
+//     the running maximum m of a row is that of s' + k, of what its tokens put into the
+//     outputs: a token that a row does not see, or sees with next to no weight, leaves
+//     the row alone whatever its size.  The sum of the weights under such an m is far
+//     from 1, which float32 has room for: units from 2^-66 up (v from about 2^-56) keep
+//     all bits, smaller ones fewer in a row that sees nothing larger.
 //
 // A persistent grid.  All tiles of all requests, heads and row tiles form one
 // line that is cut into equal parts, one per CTA, from the lengths on the device:
@@ -64,7 +70,9 @@ constexpr int kMaxSms = 160;
 constexpr int kWaitTries = 1000000;
 constexpr float kRaise = 8.0f;
 constexpr float kLift = 6.0f;
-constexpr float kMost = 15.0f;  // a weight's exponent is cut off there, until the maxima move
+constexpr float kMost = 15.0f;  // P's exponent is cut off there, until the maxima move
+constexpr float kUnit = 0x1p30f;       // of the outputs
+constexpr float kLeast = -96.0f;       // least exponent of a token's unit in those, for the maxima
 constexpr float kUnseen = 1e30f;       // minus the maximum of a row that has seen nothing
 constexpr unsigned kAll = 0xffffffffu;
 
@@ -131,11 +139,11 @@ struct Smem {
   float slope[4][RN], depth[4][RN];       // of the bias by distance; position from the length
   uint8_t node[4][RN];
   // per softmax group, by column
-  alignas(16) float nm[C::kGroups][C::kCols];      // kLift - m
-  alignas(16) float fac[C::kGroups][2][C::kCols];  // factors of l and O when m or the unit moves
+  alignas(16) float nm[C::kGroups][C::kCols];      // kLift - m, m of scores and units
+  // the square root of l's and O's factor when m moves (at the end: addresses, 8 bytes each)
+  alignas(16) float fac[C::kGroups][2][C::kCols];
   alignas(16) float red[C::kGroups][4][C::kCols];
   alignas(16) float ones[C::kCols];
-  float vred[C::kGroups][4];
   int vote[C::kGroups][4];
   uint32_t moves[C::kGroups];             // waits of the products on `again`
   Segment seg[8];
@@ -312,6 +320,10 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
 
 // 2^k, k in [-126, 127].
 __device__ __forceinline__ float pow2i(int k) { return __uint_as_float((uint32_t)(k + 127) << 23); }
+// floor(log2(u)), at least kLeast, for u >= 0.
+__device__ __forceinline__ float exponent_of(float u) {
+  return fmaxf((float)((int)(__float_as_uint(u) >> 23) - 127), kLeast);
+}
 // k with top / 2^k in [2^at, 2^(at + 1)), inside the range of pow2i(+-k)
 __device__ __forceinline__ int unit_exponent(float top, int at) {
   return min(max((int)(__float_as_uint(top) >> 23) - 127 - at, -126), 126);
@@ -1308,7 +1320,6 @@ struct Tile {
     for (uint32_t index = 0; ok && segment(index, ok); ++index) {
       const Segment &w = sm.seg[index & 7];
       const int ring = index & 3, t0 = w.t0, t1 = w.t1;
-      float vref = 0.0f;
       bool unseen = true;  // the thread's column (tok) has seen no score yet
 #pragma unroll 1
       for (int t = t0; t < t1; ++t, ++c) {
@@ -1324,6 +1335,7 @@ struct Tile {
         const bool hidden = !drafted && partly_hidden(p, w.r, t);
         const bool bent = !kPlain || drafted || past > 0 || hidden;
         const float v_unit = past + tok < kTok ? unit.y : 0.0f;
+        const float ratio = v_unit * (1.0f / kUnit), v_k = exponent_of(ratio);
         const float k_unit = bent ? 1.0f : unit.x;
         const f2 ks = pair(k_unit, k_unit);
         const float *factor = bent ? sm.ones : sm.rf[ring] + c0;
@@ -1333,8 +1345,8 @@ struct Tile {
         if (leader) sm.vote[group][(c - kBuf) & 3] = 0;
         uint8_t *pt = sm.pt[c % kBuf][0] + tok * kRow;
         // The weights are made under the maxima as they are, which seldom move: if
-        // scores turn out far above a maximum, or a unit of v larger than the outputs',
-        // they are taken back, the maxima move, and they are made again.  At a
+        // some turn out far above a maximum, they are taken back, the maxima move, and
+        // they are made again.  At a
         // segment's start the maxima are all at 0 and move from there; after the drafted
         // tokens, of which a row sees a few only, they move at once.
         const bool sure = first || t == w.r.drafted;
@@ -1353,19 +1365,13 @@ struct Tile {
               tmem_load8(s_at + ch, s);
               tmem_wait8(s);
               under(s, factor + ch, nms + ch, ks);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) s[k] += v_k;
               const float best = over_lanes<true>(s);
               if ((lane & 3) == 0) sm.red[group][quarter][ch + (lane >> 2)] = best;
               __syncwarp();
             }
-            const int vmax = __reduce_max_sync(kAll, __float_as_int(v_unit));  // units are >= 0
-            if (lane == 0) sm.vred[group][quarter] = __int_as_float(vmax);
             if (!(ok = meet(group))) break;
-            const float unit_max = fmaxf(fmaxf(sm.vred[group][0], sm.vred[group][1]),
-                                         fmaxf(sm.vred[group][2], sm.vred[group][3]));
-            // headroom of 4, so that units of one size move once
-            const float to = unit_max > vref ? fminf(unit_max * 4.0f, 0x1p126f) : vref;
-            const float v_fac = to > 0.0f ? __fdividef(vref, to) : 1.0f;
-            vref = to;
             if (tok < mine) {
               const float best = fmaxf(fmaxf(sm.red[group][0][tok], sm.red[group][1][tok]),
                                        fmaxf(sm.red[group][2][tok], sm.red[group][3][tok]));
@@ -1373,13 +1379,12 @@ struct Tile {
               float f = 1.0f;
               if (best > -INFINITY && (unseen || best > kLift)) {
                 nms[tok] = kLift - (best - nm);
-                f = unseen ? 0.0f : ex2_approx(kLift - best);
+                f = unseen ? 0.0f : ex2_approx(0.5f * (kLift - best));
                 unseen = false;
               } else if (unseen) {
                 nms[tok] = kUnseen;
               }
               sm.fac[group][0][tok] = f;
-              sm.fac[group][1][tok] = f * v_fac;
             }
             if (!first && !(ok = wait(&sm.pv_done[(c - 1) % kBuf], full_par(c - 1, kBuf)))) break;
             fence_after();
@@ -1389,18 +1394,18 @@ struct Tile {
               for (int i = 0; i < 2 * mine; i += 8) {
                 const int ch = i < mine ? i : i - mine;
                 const uint32_t at = i < mine ? l_at + ch : o_at + ch;
-                const float *fac = sm.fac[group][i >= mine] + ch;
+                const float *fac = sm.fac[group][0] + ch;
                 float o[8];
                 tmem_load8(at, o);
                 tmem_wait8(o);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) o[k] *= fac[k];
+                for (int k = 0; k < 8; ++k) o[k] = o[k] * fac[k] * fac[k];
                 tmem_store8(at, o);
               }
               tmem_stored();
             }
           }
-          const float ratio = vref > 0.0f ? __fdividef(v_unit, vref) : 0.0f;
+          const float cut = kMost - v_k;
           const f2 r2 = pair(ratio, ratio), sign = round == 1 ? pair(-1.0f, -1.0f) : pair(1.0f, 1.0f);
           float top = -INFINITY;
 #pragma unroll 1
@@ -1415,7 +1420,7 @@ struct Tile {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               top = fmaxf(top, fmaxf(s[2 * k], s[2 * k + 1]));
-              const f2 e = pair(ex2_approx(min_nan(s[2 * k], kMost)), ex2_approx(min_nan(s[2 * k + 1], kMost)));
+              const f2 e = pair(ex2_approx(min_nan(s[2 * k], cut)), ex2_approx(min_nan(s[2 * k + 1], cut)));
               if (first) l[2 * k] = l[2 * k + 1] = 0.0f;
               unpair(fma2(e, sign, pair(l[2 * k], l[2 * k + 1])), l[2 * k], l[2 * k + 1]);
               float a, b;
@@ -1430,7 +1435,7 @@ struct Tile {
           }
           tmem_stored();
           if (round == 1) continue;
-          const bool vote = round == 0 && __any_sync(kAll, top > kRaise + kLift || v_unit > vref);
+          const bool vote = round == 0 && __any_sync(kAll, top + v_k > kRaise + kLift);
           fence_async_smem();
           fence_before();
           __syncwarp();
@@ -1480,7 +1485,7 @@ struct Tile {
         const bool empty = bad || n >= w.r.nodes || sum == 0.0f;
         const int at = (w.b * p.N + n) * p.Hq + w.h * p.G + row - n * p.G;
         float *rec = part + (size_t)col * (kv.D + 2);
-        out_fac[tok] = empty ? 0.0f : whole ? __fdividef(vref, sum) : vref;
+        out_fac[tok] = empty ? 0.0f : whole ? __fdividef(kUnit, sum) : 1.0f;
         out_at[tok] = !in     ? 0ull
                       : whole ? reinterpret_cast<unsigned long long>(p.out) + (size_t)at * kv.D * 2
                               : reinterpret_cast<unsigned long long>(rec + 2);
@@ -1710,12 +1715,13 @@ __global__ void __launch_bounds__(32 * kJoinRows)
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) most = fmaxf(most, __shfl_xor_sync(kAll, most, d));
     most = fmaxf(all, most);
-    const float before = all > -INFINITY ? ex2_approx(all - most) : 0.0f;
-    const float f = m > -INFINITY ? ex2_approx(m - most) : 0.0f;
+    // (square roots, as a factor may be out of range where what it scales is not)
+    const float before = all > -INFINITY ? ex2_approx(0.5f * (all - most)) : 0.0f;
+    const float f = m > -INFINITY ? ex2_approx(0.5f * (m - most)) : 0.0f;
     all = most;
-    sum = sum * before + l * f;
+    sum = sum * before * before + l * f * f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) acc[k] *= before;
+    for (int k = 0; k < 4; ++k) acc[k] = acc[k] * before * before;
     // (a part under a factor of 0 takes part all the same: its outputs may be NaN)
     const unsigned full = __ballot_sync(kAll, m > -INFINITY);
 #pragma unroll 1
@@ -1725,7 +1731,7 @@ __global__ void __launch_bounds__(32 * kJoinRows)
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int from = (s + u) & 31;
-        g[u] = (full >> s >> u & 1) ? __shfl_sync(kAll, f, from) : 0.0f;
+        g[u] = (full >> s >> u & 1) ? __shfl_sync(kAll, f * f, from) : 0.0f;
         const float *rec = part + __shfl_sync(kAll, slot, from) * size + 2 + 4 * lane;
         x[u][0] = x[u][1] = make_float2(0.0f, 0.0f);
         if ((full >> s >> u & 1) && 4 * lane < D) {
@@ -1748,7 +1754,7 @@ __global__ void __launch_bounds__(32 * kJoinRows)
   for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
   bad = __reduce_or_sync(kAll, bad);
   const bool empty = bad || all == -INFINITY;
-  const float inv = empty ? 0.0f : __fdividef(1.0f, sum);
+  const float inv = empty ? 0.0f : __fdividef(kUnit, sum);
   const int n = row / p.G, h = notes[i].h, b = notes[i].b;
   const long long at = ((long long)b * p.N + n) * p.Hq + h * p.G + row - n * p.G;
   if (4 * lane < D) {

@@ -184,3 +184,77 @@ def test_caps_of_any_size(lib, dtype, large, softcap):
     cache = ref.make_cache(rng, lens, [0] * 3, block, Hkv, D)
     r = on(lib, large).attend(q, k, v, ref.on_gpu(cache), softcap=softcap)
     check(r, q, k, v, cache, block, None, D ** -0.5, softcap=softcap)
+
+
+# ---- values of any size, seen or not ----
+
+@ways
+@pytest.mark.parametrize("size", [1e6, 1e9, 1e12, 1e30, 1e38, 1e-30])
+@pytest.mark.parametrize("N,Hkv,D", [(24, 2, 128), (9, 1, 64)])
+def test_a_drafted_value_of_any_size(lib, dtype, large, size, N, Hkv, D):
+    """Leaves of a tree whose v is huge, or tiny, do nothing to the rows that do not see them."""
+    rng = np.random.default_rng(5)
+    lens, block = [0, 47, 300], 16
+    parents = [ref.random_tree(rng, N) for _ in lens]
+    q, k, v = tokens(rng, 3, N, 4 * Hkv, Hkv, D, dtype)
+    for b in range(3):
+        leaves = [n for n in range(N) if n not in parents[b]]
+        v[b, leaves[0]] *= size
+        v[b, leaves[-1]] *= size / 1e3
+        v[b, parents[b][leaves[1]]] *= size ** 0.25
+    cache = ref.make_cache(rng, lens, [0] * 3, block, Hkv, D)
+    r = on(lib, large).attend(q, k, v, ref.on_gpu(cache), parent=torch.tensor(parents).int().cuda())
+    check(r, q, k, v, cache, block, parents, D ** -0.5)
+
+
+@ways
+@pytest.mark.parametrize("fall", [0.0, 20.0, 60.0, 80.0])
+@pytest.mark.parametrize("size", [1e30, 1e-30])
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_visible_block_of_any_size(lib, dtype, large, fall, size, D):
+    """A cached block whose v are 1e30 times the others', under scores `fall` below theirs: it takes
+    part by its weight times its size, be that nothing or all."""
+    rng = np.random.default_rng(6)
+    lens, N, block = [160, 700], 3, 32
+    q, k, v = tokens(rng, 2, N, 2, 1, D, dtype)
+    q[:] = 1.0
+    k *= 0.125
+    cache = ref.make_cache(rng, lens, [0] * 2, block, 1, D)
+    cache["k_scale"][:] = 2.0 ** -9
+    for b, n in enumerate(lens):
+        for i in (1, n // block - 1):
+            at = cache["block_table"][b, i]
+            cache["v_scale"][at] *= size
+            code = torch.tensor([-fall / D / 0.125 * 2.0 ** 4]).to(ref.E4M3).view(torch.uint8)
+            cache["k"][at] = code
+            cache["k_scale"][at] = 2.0 ** -4
+    r = on(lib, large).attend(q, k, v, ref.on_gpu(cache), scale=0.125)
+    check(r, q, k, v, cache, block, None, 0.125)
+
+
+@ways
+@pytest.mark.parametrize("window", [20, 60])
+def test_a_block_of_any_size_outside_of_windows(lib, dtype, large, window):
+    """Huge blocks that a window hides from some nodes of a long chain, or from all."""
+    rng = np.random.default_rng(7)
+    lens, N, D, block = [100, 131], 40, 64, 16
+    q, k, v = tokens(rng, 2, N, 2, 1, D, dtype)
+    cache = ref.make_cache(rng, lens, [0] * 2, block, 1, D)
+    for b, n in enumerate(lens):
+        cache["v_scale"][cache["block_table"][b, (n - window + 20) // block]] *= 1e25
+        cache["v_scale"][cache["block_table"][b, (n - window) // block]] *= 1e12
+    r = on(lib, large).attend(q, k, v, ref.on_gpu(cache), window=window)
+    check(r, q, k, v, cache, block, None, D ** -0.5, window=window)
+
+
+@ways
+def test_block_scales_of_every_size(lib, dtype, large):
+    rng = np.random.default_rng(8)
+    lens, N, Hq, Hkv, D, block = [333, 1000], 4, 4, 2, 128, 16
+    q, k, v = tokens(rng, 2, N, Hq, Hkv, D, dtype)
+    cache = ref.make_cache(rng, lens, [0] * 2, block, Hkv, D)
+    nb = cache["k"].shape[0]
+    cache["v_scale"] = torch.from_numpy(10.0 ** rng.uniform(-36, 35, (nb, Hkv))).float()
+    cache["v_scale"][::9] = 0.0
+    r = on(lib, large).attend(q, k, v, ref.on_gpu(cache))
+    check(r, q, k, v, cache, block, None, D ** -0.5)
