@@ -8,6 +8,7 @@ CPU fallback: if the library is missing or a call fails, an exception says so.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 import os
@@ -169,6 +170,13 @@ def _stream_ptr(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _on(stream):
+    """Where a call on ``stream`` makes its outputs and workspaces: with that stream current,
+    so that torch's allocator hands their memory out again in its order, and not to other
+    streams while the call's kernels still use it."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def _cuda(**tensors):
     """Every given tensor (None skipped) must live on one CUDA device, the
     current one: the library reads and writes device memory only (it has no
@@ -240,7 +248,7 @@ class TreeOut:
                        torch.empty(B, N, dtype=torch.float32, device=device) if with_p else None)
 
 
-def _linear_args(logits, q, draft_tokens, temperature, uniforms, out, workspace):
+def _linear_args(logits, q, draft_tokens, temperature, uniforms, out, workspace, stream):
     _cuda(logits=logits, q=q, draft_tokens=draft_tokens, temperature=temperature,
           uniforms=uniforms, workspace=workspace,
           **({} if out is None else {k: v for k, v in vars(out).items()}))
@@ -253,10 +261,10 @@ def _linear_args(logits, q, draft_tokens, temperature, uniforms, out, workspace)
     _req(draft_tokens, "draft_tokens", torch.int32, (B, gamma), dev)
     _req(temperature, "temperature", torch.float32, (B,), dev)
     _req(uniforms, "uniforms", torch.float32, (B, R), dev)
-    if out is None:
-        out = LinearOut.empty(B, gamma, dev)
-    if workspace is None:
-        workspace = alloc_workspace(B, R, V, dt, dev)
+    if out is None or workspace is None:
+        with _on(stream):
+            out = out if out is not None else LinearOut.empty(B, gamma, dev)
+            workspace = workspace if workspace is not None else alloc_workspace(B, R, V, dt, dev)
     return B, gamma, V, dt, out, workspace
 
 
@@ -266,7 +274,7 @@ def verify_linear(logits: torch.Tensor, q: torch.Tensor, draft_tokens: torch.Ten
                   stream=None) -> LinearOut:
     """Linear verify step (``specdec_verify_linear``) on CUDA tensors."""
     B, gamma, V, dt, out, ws = _linear_args(logits, q, draft_tokens, temperature, uniforms,
-                                            out, workspace)
+                                            out, workspace, stream)
     lib = load_library()
     rc = lib.specdec_verify_linear(
         _ptr(logits), _ptr(q), dt, _ptr(draft_tokens), _ptr(temperature), _ptr(uniforms),
@@ -286,7 +294,7 @@ def verify_linear_topk(logits: torch.Tensor, q: torch.Tensor, draft_tokens: torc
                        stream=None) -> LinearOut:
     """Linear verify with the top-k residual approximation (``specdec_verify_linear_topk``)."""
     B, gamma, V, dt, out, ws = _linear_args(logits, q, draft_tokens, temperature, uniforms,
-                                            out, workspace)
+                                            out, workspace, stream)
     rc = load_library().specdec_verify_linear_topk(
         _ptr(logits), _ptr(q), dt, _ptr(draft_tokens), _ptr(temperature), _ptr(uniforms),
         B, gamma, V, int(topk), _ptr(out.n_accepted), _ptr(out.out_tokens),
@@ -316,7 +324,7 @@ def linear_finalize(logits, q, draft_tokens, temperature, uniforms, out: LinearO
                     workspace: torch.Tensor, stream=None) -> LinearOut:
     """Phase 2 of the linear form (``specdec_linear_finalize``)."""
     B, gamma, V, dt, out, ws = _linear_args(logits, q, draft_tokens, temperature, uniforms,
-                                            out, workspace)
+                                            out, workspace, stream)
     rc = load_library().specdec_linear_finalize(
         _ptr(logits), _ptr(q), dt, _ptr(draft_tokens), _ptr(temperature), _ptr(uniforms),
         B, gamma, V, _ptr(out.n_accepted), _ptr(out.out_tokens), _ptr(out.final_token),
@@ -327,7 +335,7 @@ def linear_finalize(logits, q, draft_tokens, temperature, uniforms, out: LinearO
 
 
 def _tree_args(logits, q, node_tokens, parent, temperature, uniforms, max_depth, out,
-               workspace):
+               workspace, stream):
     _cuda(logits=logits, q=q, node_tokens=node_tokens, parent=parent, temperature=temperature,
           uniforms=uniforms, workspace=workspace,
           **({} if out is None else {k: v for k, v in vars(out).items()}))
@@ -340,10 +348,10 @@ def _tree_args(logits, q, node_tokens, parent, temperature, uniforms, max_depth,
     _req(parent, "parent", torch.int32, (B, N), dev)
     _req(temperature, "temperature", torch.float32, (B,), dev)
     _req(uniforms, "uniforms", torch.float32, (B, N), dev)
-    if out is None:
-        out = TreeOut.empty(B, N, max_depth, dev)
-    if workspace is None:
-        workspace = alloc_workspace(B, N, V, dt, dev)
+    if out is None or workspace is None:
+        with _on(stream):
+            out = out if out is not None else TreeOut.empty(B, N, max_depth, dev)
+            workspace = workspace if workspace is not None else alloc_workspace(B, N, V, dt, dev)
     return B, N, V, dt, out, workspace
 
 
@@ -352,7 +360,7 @@ def verify_tree(logits, q, node_tokens, parent, temperature, uniforms, max_depth
                 stream=None) -> TreeOut:
     """Token-tree verify step (``specdec_verify_tree``) on CUDA tensors."""
     B, N, V, dt, out, ws = _tree_args(logits, q, node_tokens, parent, temperature, uniforms,
-                                      max_depth, out, workspace)
+                                      max_depth, out, workspace, stream)
     rc = load_library().specdec_verify_tree(
         _ptr(logits), _ptr(q), dt, _ptr(node_tokens), _ptr(parent), _ptr(temperature),
         _ptr(uniforms), B, N, V, max_depth, _ptr(out.n_accepted), _ptr(out.path_nodes),
@@ -366,7 +374,7 @@ def tree_finalize(logits, q, node_tokens, parent, temperature, uniforms, max_dep
                   out: TreeOut, workspace: torch.Tensor, stream=None) -> TreeOut:
     """Phase 2 of the tree form (``specdec_tree_finalize``)."""
     B, N, V, dt, out, ws = _tree_args(logits, q, node_tokens, parent, temperature, uniforms,
-                                      max_depth, out, workspace)
+                                      max_depth, out, workspace, stream)
     rc = load_library().specdec_tree_finalize(
         _ptr(logits), _ptr(q), dt, _ptr(node_tokens), _ptr(parent), _ptr(temperature),
         _ptr(uniforms), B, N, V, max_depth, _ptr(out.n_accepted), _ptr(out.path_nodes),
@@ -388,9 +396,10 @@ def tree_staging_size(B: int, N: int, V: int, max_depth: int, dtype: int) -> int
     return int(load_library().specdec_tree_staging_size(B, N, V, max_depth, dtype))
 
 
-def _staging(nbytes: int, staging, device) -> torch.Tensor:
+def _staging(nbytes: int, staging, device, stream) -> torch.Tensor:
     if staging is None:
-        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+        with _on(stream):
+            return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
     if staging.device.type != "cuda" or staging.dtype != torch.uint8:
         raise ValueError("staging must be a uint8 CUDA tensor")
     _cuda(staging=staging)
@@ -426,7 +435,7 @@ def verify_linear_host(logits: torch.Tensor, q: torch.Tensor, draft_tokens: torc
     _req(temperature, "temperature", torch.float32, (B,), cpu)
     _req(uniforms, "uniforms", torch.float32, (B, R), cpu)
     out = _host_out(out, lambda: LinearOut.empty(B, gamma, cpu))
-    st = _staging(linear_staging_size(B, gamma, V, dt), staging, device)
+    st = _staging(linear_staging_size(B, gamma, V, dt), staging, device, stream)
     s = stream if stream is not None else torch.cuda.current_stream(st.device)
     rc = load_library().specdec_verify_linear_host(
         _ptr(logits), _ptr(q), dt, _ptr(draft_tokens), _ptr(temperature), _ptr(uniforms),
@@ -454,7 +463,7 @@ def verify_tree_host(logits, q, node_tokens, parent, temperature, uniforms, max_
     _req(temperature, "temperature", torch.float32, (B,), cpu)
     _req(uniforms, "uniforms", torch.float32, (B, N), cpu)
     out = _host_out(out, lambda: TreeOut.empty(B, N, max_depth, cpu))
-    st = _staging(tree_staging_size(B, N, V, max_depth, dt), staging, device)
+    st = _staging(tree_staging_size(B, N, V, max_depth, dt), staging, device, stream)
     s = stream if stream is not None else torch.cuda.current_stream(st.device)
     rc = load_library().specdec_verify_tree_host(
         _ptr(logits), _ptr(q), dt, _ptr(node_tokens), _ptr(parent), _ptr(temperature),
@@ -530,7 +539,8 @@ def philox_uniforms(key, counter, first_word: int, n: int, device="cuda", stream
     c = np.ascontiguousarray(np.asarray(counter, dtype=np.uint64).reshape(-1))
     if k.size != 2 or c.size != 4:
         raise ValueError("key must hold 2 and counter 4 64-bit words")
-    out = torch.empty(int(n), dtype=torch.float32, device=device)
+    with _on(stream):
+        out = torch.empty(int(n), dtype=torch.float32, device=device)
     rc = load_library().specdec_philox_uniforms(k.ctypes.data, c.ctypes.data, int(first_word),
                                                 int(n), _ptr(out) if n > 0 else None,
                                                 _stream_ptr(stream))
@@ -545,7 +555,8 @@ def row_entropy(logits: torch.Tensor, temperature: torch.Tensor, workspace: torc
     ``row_stats(..., entropy=True)`` call on those logits (``specdec_row_entropy``)."""
     _cuda(logits=logits, temperature=temperature, workspace=workspace)
     B, R, V = logits.shape
-    out = torch.empty((B, R), dtype=torch.float32, device=logits.device)
+    with _on(stream):
+        out = torch.empty((B, R), dtype=torch.float32, device=logits.device)
     rc = load_library().specdec_row_entropy(_ptr(workspace), workspace.numel(), dtype_code(logits),
                                             _ptr(temperature), B, R, V, _ptr(out),
                                             _stream_ptr(stream))
@@ -566,7 +577,8 @@ def final_mass(workspace: torch.Tensor, B: int, rows_per_request: int, V: int, d
     """Normaliser [B] of each request's final draw in the last verify call on
     ``workspace`` (``specdec_final_mass``; NaN where nothing was drawn)."""
     _cuda(workspace=workspace)
-    out = torch.empty(B, dtype=torch.float32, device=workspace.device)
+    with _on(stream):
+        out = torch.empty(B, dtype=torch.float32, device=workspace.device)
     rc = load_library().specdec_final_mass(_ptr(workspace), workspace.numel(), B,
                                            rows_per_request, V, dtype,
                                            _ptr(out) if B > 0 else None, _stream_ptr(stream))
@@ -594,7 +606,8 @@ def row_alpha(logits: torch.Tensor, q: torch.Tensor, temperature: torch.Tensor,
     _cuda(logits=logits, q=q, temperature=temperature, workspace=workspace)
     B, R, V = logits.shape
     gamma = R - 1
-    out = torch.empty((B, gamma), dtype=torch.float32, device=logits.device)
+    with _on(stream):
+        out = torch.empty((B, gamma), dtype=torch.float32, device=logits.device)
     rc = load_library().specdec_row_alpha(_ptr(logits), _ptr(q), dtype_code(logits),
                                           _ptr(temperature), B, gamma, V, _ptr(workspace),
                                           workspace.numel(), _ptr(out), _stream_ptr(stream))
@@ -610,7 +623,8 @@ def path_logprob(logits: torch.Tensor, temperature: torch.Tensor, out_tokens: to
     _cuda(logits=logits, temperature=temperature, out_tokens=out_tokens, n_accepted=n_accepted,
           workspace=workspace, path_nodes=path_nodes, row_status=row_status)
     B, R, V = logits.shape
-    out = torch.empty(B, dtype=torch.float32, device=logits.device)
+    with _on(stream):
+        out = torch.empty(B, dtype=torch.float32, device=logits.device)
     rc = load_library().specdec_path_logprob(
         _ptr(logits), dtype_code(logits), _ptr(temperature), _ptr(out_tokens), _ptr(n_accepted),
         _ptr(path_nodes), _ptr(row_status), B, R, V, out_tokens.shape[1], _ptr(workspace),
@@ -807,13 +821,15 @@ def rope(q: torch.Tensor, k: Optional[torch.Tensor], freq: torch.Tensor,
     if parent is not None:
         _flat(parent, "parent", torch.int32, (B, N))
     if q_out is None:
-        q_out = torch.empty((B, N, Hq, D), dtype=q.dtype, device=q.device)
+        with _on(stream):
+            q_out = torch.empty((B, N, Hq, D), dtype=q.dtype, device=q.device)
     else:
         _flat(q_out, "q_out", q.dtype, (B, N, Hq, D))
     if k is None:
         k_out = None
     elif k_out is None:
-        k_out = torch.empty((B, N, Hk, D), dtype=q.dtype, device=q.device)
+        with _on(stream):
+            k_out = torch.empty((B, N, Hk, D), dtype=q.dtype, device=q.device)
     else:
         _flat(k_out, "k_out", q.dtype, (B, N, Hk, D))
     rc = load_library().specdec_rope(
@@ -850,8 +866,9 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache,
     if path is not None:
         _flat(path, "path", torch.int32, (B, path.shape[-1]))
     if out is None:
-        out = AppendOut(torch.empty(B, dtype=torch.int32, device=k.device),
-                        torch.empty(B, dtype=torch.int32, device=k.device))
+        with _on(stream):
+            out = AppendOut(torch.empty(B, dtype=torch.int32, device=k.device),
+                            torch.empty(B, dtype=torch.int32, device=k.device))
     else:
         _flat(out.length, "out.length", torch.int32, (B,))
         _flat(out.row_status, "out.row_status", torch.int32, (B,))
@@ -907,16 +924,18 @@ def attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: KVCache,
         _flat(slopes, "slopes", torch.float32, (Hq,))
     if out is None:
         dev = q.device
-        out = AttendOut(torch.empty((B, N, Hq, D), dtype=dtype, device=dev),
-                        torch.empty((B, N, Hq), dtype=torch.float32, device=dev),
-                        torch.empty(B, dtype=torch.int32, device=dev))
+        with _on(stream):
+            out = AttendOut(torch.empty((B, N, Hq, D), dtype=dtype, device=dev),
+                            torch.empty((B, N, Hq), dtype=torch.float32, device=dev),
+                            torch.empty(B, dtype=torch.int32, device=dev))
     else:
         _flat(out.out, "out.out", dtype, (B, N, Hq, D))
         if out.lse is not None:
             _flat(out.lse, "out.lse", torch.float32, (B, N, Hq))
         _flat(out.row_status, "out.row_status", torch.int32, (B,))
     if workspace is None:
-        workspace = alloc_attend_workspace(q, cache)
+        with _on(stream):
+            workspace = alloc_attend_workspace(q, cache)
     rc = load_library().specdec_attend(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), dt, q_at, k_at, v_at, _raw(parent),
         _raw(n_nodes), ctypes.addressof(c), B, N, Hq, D ** -0.5 if scale is None else scale,
