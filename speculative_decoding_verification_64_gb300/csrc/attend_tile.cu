@@ -699,7 +699,7 @@ struct Tile {
         const bool cached = t >= w.r.drafted;
         if (x.id < 0 || x.id >= kv.n_blocks) {
           x.id = 0;
-          sm.bad[(index - 1) & 7] = SPECDEC_ROW_BAD_CACHE;
+          atomicOr(&sm.bad[(index - 1) & 7], SPECDEC_ROW_BAD_CACHE);  // (or BAD_TREE stands there)
         }
         const long long cell = (long long)x.id * kv.Hkv + w.h;
         const int row = (int)(cell * kv.block + x.tok % kv.block);
