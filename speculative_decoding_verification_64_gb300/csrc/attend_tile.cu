@@ -678,6 +678,7 @@ struct Tile {
     const specdec_kv_cache &kv = p.cache;
     uint32_t c = 0, v = 0, index = 0;  // tiles; half tiles of V
     note.tiles = note.first = note.head = note.open = 0;
+    copied = copied_v = 0;
     Walk walk(p, box, plan);
     Segment w, ahead;
     bool ok = true, more = true;
@@ -689,7 +690,6 @@ struct Tile {
       if (more) more = publish(walk, index, ahead);
       if (index == 0) continue;
       if (!have) break;
-      if (!ok) continue;  // after giving up: only the notes go on
       Piece next = piece_of(w, w.t0);
 #pragma unroll 1
       for (int t = w.t0; t < w.t1; ++t, ++c) {
@@ -710,6 +710,7 @@ struct Tile {
         // Drafted tiles have nothing to copy, but their products wait for this
         // arrival: were they done before the wait above looks, it would miss their
         // phase and take the next one of the same parity for it.
+        copied = c + 1;
         if (!cached) {
           if (lane == 0) mbar_arrive(&sm.k_full[ks]);
           __syncwarp();
@@ -733,18 +734,21 @@ struct Tile {
           if (here)
             tma_rows(sm.v[v % kV] + (lane * box - half * (kTok / 2)) * kRow, v_map, row,
                      &sm.v_full[v % kV]);
+          copied_v = v + 1;
         }
         if (!ok) break;
       }
+      if (!ok) break;
     }
-    // Every copy has been waited on by its reader, unless somebody gave up: then
-    // copies in flight get time to land before the CTA may leave.
-    copied = c;
-    copied_v = v;
+    // After giving up only the notes go on: no further segment is published, as its
+    // place in the ring may still be read.
+    while (more) more = take(walk, ahead);
     if (lane == 0) notes_of(p.part, RN, kv.D)[blockIdx.x] = note;
   }
 
-  uint32_t copied, copied_v;
+  // Every copy has been waited on by its reader, unless somebody gave up: then copies in
+  // flight get time to land before the CTA may leave.
+  uint32_t copied, copied_v;  // of K and of V: issued, on barriers of their own order
   __device__ void drain() {
     for (uint32_t i = copied > kK ? copied - kK : 0; i < copied; ++i)
       mbar_wait_bounded(&sm.k_full[i % kK], full_par(i, kK));
