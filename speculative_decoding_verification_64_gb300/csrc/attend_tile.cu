@@ -67,7 +67,7 @@ constexpr int kTok = 128;
 constexpr int kRow = 128;              // bytes of a shared-memory row: one swizzle span
 constexpr int kTileBytes = kTok * kRow;
 constexpr int kMaxSms = 160;
-constexpr int kWaitTries = 1000000;
+constexpr uint32_t kWaitClocks = 2000000000u;
 constexpr float kRaise = 8.0f;
 constexpr float kLift = 6.0f;
 constexpr float kMost = 15.0f;  // P's exponent is cut off there, until the maxima move
@@ -450,25 +450,28 @@ struct Note {
   int open;         // tiles done of a unit that was begun but not ended here, or 0
 };
 
-// Waits until the phase of `parity` is complete.  Gives up after kWaitTries
-// tries of up to about 2 us each (at least a few 10 ms in all, where no wait of
-// a working kernel takes 1 ms), and says so in shared memory at `give_up`.
+// Waits until the phase of `parity` is complete.  Gives up after kWaitClocks, about a
+// second, where no wait of a working kernel takes a tenth of that (the longest are for
+// rows that see values that are not finite, `stray` below: tens of ms at 1024 nodes), and
+// says so in shared memory at `give_up`.  (A 64-bit timer, or a look at `give_up` on the
+// way, are more code at each wait: 403 to 412 us for the 256 requests above, 375 so.)
 __device__ __forceinline__ bool wait_lane(uint32_t bar, uint32_t parity, uint32_t give_up) {
   uint32_t ok;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
-      "mov.u32 n, %4;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 t0, t;\n\t"
+      "mov.u32 t0, %%clock;\n\t"
       "AGAIN:\n\t"
       "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 2000;\n\t"
       "@p bra DONE;\n\t"
-      "sub.u32 n, n, 1;\n\t"
-      "setp.ne.u32 q, n, 0;\n\t"
+      "mov.u32 t, %%clock;\n\t"
+      "sub.u32 t, t, t0;\n\t"
+      "setp.lt.u32 q, t, %4;\n\t"
       "@q bra AGAIN;\n\t"
       "st.volatile.shared.u32 [%3], 1;\n\t"
       "DONE:\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(give_up), "n"(kWaitTries)
+      : "r"(bar), "r"(parity), "r"(give_up), "n"(kWaitClocks)
       : "memory");
   return ok != 0;
 }
