@@ -448,6 +448,7 @@ struct Note {
   int unit;         // that unit's tiles, and which it is
   int b, h, rt;
   int open;         // tiles done of a unit that was begun but not ended here, or 0
+  int lost, lost_to;  // requests of the segments that were given up, or -1
 };
 
 // Waits until the phase of `parity` is complete.  Gives up after kWaitClocks, about a
@@ -681,6 +682,7 @@ struct Tile {
     const specdec_kv_cache &kv = p.cache;
     uint32_t c = 0, v = 0, index = 0;  // tiles; half tiles of V
     note.tiles = note.first = note.head = note.open = 0;
+    note.lost = note.lost_to = -1;
     copied = copied_v = 0;
     Walk walk(p, box, plan);
     Segment w, ahead;
@@ -789,6 +791,15 @@ struct Tile {
     __syncwarp();
   }
 
+  // The test build in which waits give up without looking (see common.cuh): here for the
+  // copies of every second CTA, of all its segments or from the second one on.
+  __device__ __forceinline__ bool gives_up(uint32_t index) const {
+    if (kConsumerWaitNs != 0 || blockIdx.x % 2 == 0) return false;
+    if (blockIdx.x % 4 == 1 && index == 0) return false;
+    *(volatile int *)&sm.give_up = 1;
+    return true;
+  }
+
   // O^T += V^T P^T of tile c, as soon as both are there.
   __device__ __forceinline__ bool outputs(uint32_t c, bool first) {
     return outputs_of(sm, sm_tmem + 2 * RN, columns, c, first);
@@ -843,6 +854,10 @@ struct Tile {
         }
         if (first && !(ok = wait(&sm.q_full, index & 1))) break;
         if (!(ok = wait(&sm.box_full[c & 7], (c >> 3) & 1))) break;
+        if (gives_up(index)) {
+          ok = false;
+          break;
+        }
         if (!(ok = wait(&sm.k_full[c % kK], full_par(c, kK)))) break;
         if (!(ok = wait(&sm.s_empty[c & 1], ((c >> 1) & 1) ^ 1))) break;
         fence_after();
@@ -1536,21 +1551,30 @@ struct Tile {
             store_global32(here, at[k] + 4 * tok, y[k]);
         }
       }
-      if (leader && group == 0 && whole && w.h == 0 && w.rt == 0) p.row_status[w.b] = bad;
+      // the request's first segment sets the status, the join adds what others find
+      if (leader && group == 0 && w.h == 0 && w.rt == 0 && t0 == 0) p.row_status[w.b] = bad;
       if (leader) sm.done[group] = index + 1;
       if (!(ok = meet_all())) break;
     }
   }
 
-  // After a wait ran out: the segments that were not finished get no result.
+  // After a wait ran out: the segments that were not finished get no result, and the
+  // note says which requests that leaves without one.
   __device__ __noinline__ static void give_up_results(const AttendParams &p, int box,
                                                       const Plan &plan, int finished, int columns) {
     const specdec_kv_cache &kv = p.cache;
+    const bool first = threadIdx.x == 32 * C::kFirst;
+    Note *note = notes_of(p.part, RN, kv.D) + blockIdx.x;
     Walk walk(p, box, plan);
     Segment w;
 #pragma unroll 1
     for (int index = 0; walk.next(p, box, w); ++index) {
       if (index < finished) continue;
+      if (first) {
+        if (note->lost < 0) note->lost = w.b;
+        note->lost_to = w.b;
+        if (w.h == 0 && w.rt == 0 && w.t0 == 0) p.row_status[w.b] = SPECDEC_ROW_INTERNAL;
+      }
       float *part = p.part + (size_t)(2 * blockIdx.x + (w.t0 == 0)) * partial_floats(RN, kv.D);
 #pragma unroll 1
       for (int col = threadIdx.x - 32 * C::kFirst; col < columns; col += C::kThreads - 32 * C::kFirst) {
@@ -1566,7 +1590,6 @@ struct Tile {
           part[(size_t)col * (kv.D + 2) + 1] = -(float)SPECDEC_ROW_INTERNAL;
         }
       }
-      if (threadIdx.x == 32 * C::kFirst) p.row_status[w.b] = SPECDEC_ROW_INTERNAL;
     }
   }
 };
@@ -1668,7 +1691,8 @@ __global__ void __launch_bounds__(Cfg<RN>::kThreads, Cfg<RN>::kCtas)
 
 // Joins the units that the cuts between CTAs divide.  Block (i, y): the unit that
 // CTA i was in the middle of at its start, if it is the first that was; the y-th
-// part of its rows.
+// part of its rows.  Flags are added to the status that each request's first segment
+// has set: those of the parts, and of what CTA i gave up, whatever head that was of.
 constexpr int kJoinRows = 8;  // a warp each
 __global__ void __launch_bounds__(32 * kJoinRows)
     attend_tile_join_kernel(const __grid_constant__ AttendParams p, int ctas, int RN) {
@@ -1677,7 +1701,10 @@ __global__ void __launch_bounds__(32 * kJoinRows)
   const int i = blockIdx.x, D = p.cache.D, lane = threadIdx.x & 31;
   const int size = (int)partial_floats(RN, D);
   const Note *notes = notes_of(p.part, RN, D);
-  const int mine = notes[i].first, unit = notes[i].unit;
+  const int mine = notes[i].first, unit = notes[i].unit, lost = notes[i].lost;
+  if (lost >= 0 && blockIdx.y == 0)
+    for (int b = lost + threadIdx.x; b <= notes[i].lost_to; b += blockDim.x)
+      atomicOr(p.row_status + b, SPECDEC_ROW_INTERNAL);
   if (mine == 0) return;  // begins with a unit, or has no tile
   // the CTAs before: the one that began the unit is the last that has tiles
   int begun = -1;
@@ -1771,7 +1798,7 @@ __global__ void __launch_bounds__(32 * kJoinRows)
       out[k] = (unsigned short)pack_bf16x2(empty ? 0.0f : acc[k] * inv, 0.0f);
   }
   if (p.lse && lane == 0) p.lse[at] = empty ? -INFINITY : (all + log2f(sum)) * 0.6931471805599453f;
-  if (h == 0 && row == 0 && lane == 0) p.row_status[b] = bad;
+  if (bad && lane == 0) atomicOr(p.row_status + b, bad);
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
