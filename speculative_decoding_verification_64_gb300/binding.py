@@ -780,12 +780,12 @@ def rope_frequencies(rot: int, theta: float = 10000.0, factor: float = 1.0,
             keep = 0.0
             if original_length > 0:
                 # the ramp is linear in the pair's index, from where a pair turns
-                # beta_fast times over the original length to where it turns beta_slow times
+                # beta_fast times over the original length to where it turns beta_slow times,
+                # be that among the pairs or before the first or past the last
                 def at(n):
                     return rot * math.log(original_length / (n * 2.0 * math.pi)) / \
                         (2.0 * math.log(theta))
-                low = max(math.floor(at(beta_fast)), 0)
-                high = min(math.ceil(at(beta_slow)), rot // 2 - 1)
+                low, high = math.floor(at(beta_fast)), math.ceil(at(beta_slow))
                 keep = 1.0 - min(1.0, max(0.0, (i - low) / max(high - low, 1e-3)))
             turns = turns * keep + turns / factor * (1.0 - keep)
         word = int(math.ldexp(turns, 64)) % 2 ** 64
