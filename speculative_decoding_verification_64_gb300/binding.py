@@ -801,7 +801,13 @@ def rope(q: torch.Tensor, k: Optional[torch.Tensor], freq: torch.Tensor,
     """Rotary positions (``specdec_rope``) of q [B, N, Hq, D] and k [B, N, Hk, D] (or None):
     returns the turned (q, k).  Positions are ``positions`` [B, N], or ``base`` [B] plus the
     depth of each node of ``parent`` [B, N] (a chain without it).  ``backward``: the
-    gradient, from dq and dk."""
+    gradient, from dq and dk; it is also what autograd takes for q and k that need one
+    (no q_out or k_out then)."""
+    if torch.is_grad_enabled() and (q.requires_grad or (k is not None and k.requires_grad)):
+        if q_out is not None or k_out is not None:
+            raise ValueError("q_out and k_out cannot be given where q or k requires a gradient")
+        with _on(stream):
+            return _Rope.apply(q, k, freq, positions, base, parent, interleaved, backward, magnitude)
     raw = _here(stream, (q, k, freq, positions, base, parent, q_out, k_out),
                 ("q", "k", "freq", "positions", "base", "parent", "q_out", "k_out"))
     dt = dtype_code(q)
@@ -841,6 +847,23 @@ def rope(q: torch.Tensor, k: Optional[torch.Tensor], freq: torch.Tensor,
     return q_out, k_out
 
 
+class _Rope(torch.autograd.Function):
+    """``rope`` under autograd: the map is linear, its transpose the same call."""
+
+    @staticmethod
+    def forward(ctx, q, k, freq, positions, base, parent, interleaved, backward, magnitude):
+        ctx.save_for_backward(freq, positions, base, parent)
+        ctx.how = interleaved, not backward, magnitude
+        return rope(q, k, freq, positions, base, parent, interleaved, backward, magnitude)
+
+    @staticmethod
+    def backward(ctx, dq, dk):
+        if dk is not None and not ctx.needs_input_grad[1]:
+            dk = None
+        q, k = rope(dq.contiguous(), None if dk is None else dk.contiguous(), *ctx.saved_tensors, *ctx.how)
+        return (q, k) + (None,) * 7
+
+
 def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache,
               count: Optional[torch.Tensor] = None, extra: int = 0,
               path: Optional[torch.Tensor] = None, out: Optional[AppendOut] = None,
@@ -849,7 +872,7 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache,
     the first ``count[b] + extra`` nodes (N + extra without count) of ``path`` [B, path_len]
     or of 0 .. N-1.  After a verify step: ``count=r.n_accepted, extra=1`` and, for a tree,
     ``path=r.path_nodes``.  ``cache.length`` is left alone: set it to the result's
-    ``length`` for the next step."""
+    ``length`` for the next step.  (No gradient passes through the cache.)"""
     raw = _here(stream, (k, v, count, path, cache.k, cache.v, cache.k_scale, cache.v_scale,
                          cache.block_table, cache.length) +
                 (() if out is None else (out.length, out.row_status)),
@@ -899,7 +922,8 @@ def attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: KVCache,
            stream=None) -> AttendOut:
     """Attention of drafted tokens (``specdec_attend``): q [B, N, Hq, D] over the request's
     cached tokens and, by the chain or the tree ``parent`` [B, N], over the drafted tokens'
-    own k, v [B, N, Hkv, D].  ``scale`` defaults to D ** -0.5."""
+    own k, v [B, N, Hkv, D].  ``scale`` defaults to D ** -0.5.  (Inference only: the result
+    carries no gradient.)"""
     raw = _here(stream, (q, k, v, parent, n_nodes, slopes, workspace, cache.k, cache.v,
                          cache.k_scale, cache.v_scale, cache.block_table, cache.length) +
                 (() if out is None else (out.out, out.lse, out.row_status)),
