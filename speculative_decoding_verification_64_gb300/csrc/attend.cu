@@ -153,6 +153,8 @@ struct Kernel {
     b = i / p.cache.Hkv;
   }
 
+  __device__ __forceinline__ int row0() const { return tile * kRows; }
+
   __device__ __forceinline__ float act(const void *base, long long i) const {
     return load_elem(base, kF32 ? SPECDEC_F32 : SPECDEC_BF16, i);
   }
@@ -510,6 +512,20 @@ struct Kernel {
     return fmaxf(fmaxf(size_of(x.x), size_of(x.y)), fmaxf(size_of(x.z), size_of(x.w)));
   }
 
+  static __device__ __forceinline__ bool finite4(const float4 &x) {
+    return finite(x.x) && finite(x.y) && finite(x.z) && finite(x.w);
+  }
+
+  // q . k of one row and one drafted token, from global memory, term by term.
+  static __device__ __noinline__ float plain_dot(const void *q, long long q_at, const void *k,
+                                                 long long k_at, int D) {
+    constexpr int dt = kF32 ? SPECDEC_F32 : SPECDEC_BF16;
+    float s = 0.0f;
+#pragma unroll 1
+    for (int e = 0; e < D; ++e) s = fmaf(load_elem(q, dt, q_at + e), load_elem(k, dt, k_at + e), s);
+    return s;
+  }
+
   __device__ __forceinline__ void drafted(int j0) {
     const specdec_kv_cache &kv = p.cache;
     const long long first = (long long)b * p.N + j0;
@@ -519,6 +535,7 @@ struct Kernel {
 
     // q k^T, the node's k in units of its size
     float s[1][2][4], unit_k[2];
+    unsigned odd = 0;  // tokens whose k is not finite
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt) {
       const int t = nt * 8 + g;
@@ -535,7 +552,10 @@ struct Kernel {
 #pragma unroll
       for (int i = 0; i < KC; ++i)
 #pragma unroll
-        for (int sub = 0; sub < 4; ++sub) top = fmaxf(top, top4(x[i][sub]));
+        for (int sub = 0; sub < 4; ++sub) {
+          top = fmaxf(top, top4(x[i][sub]));
+          if (!finite4(x[i][sub])) odd |= 1u << t;
+        }
       top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
       top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
       const int ex = unit_exponent(top);
@@ -576,6 +596,27 @@ struct Kernel {
         const int dist = p.slopes && seen ? pos[i] - len - depth_of(j0 + t) : 0;
         s[0][nt][e] = seen ? score(s[0][nt][e], unit, i, dist) : -INFINITY;
       }
+    odd = __reduce_or_sync(kAll, odd);
+    if (odd) {  // infinities times the zeros of the other terms are not what q . k is
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll 1
+        for (int n = 0; n < 4; ++n) {
+          const int t = (n >> 1) * 8 + 2 * c + (n & 1);
+          if (!(odd >> t & see[i] >> t & 1u)) continue;
+          const int row = row0() + g + 8 * i;
+          const float dot = plain_dot(p.q,
+                                      ((long long)b * p.N + node[i]) * p.q_stride +
+                                          (long long)(h * p.G + row - node[i] * p.G) * kv.D,
+                                      p.k_new, (first + t) * p.k_stride + (long long)h * kv.D, kv.D);
+          const float y = score(dot, __fdiv_rn(1.0f, sm.q_exp[g + 8 * i]), i,
+                                p.slopes ? pos[i] - len - depth_of(j0 + t) : 0);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k == n) s[0][k >> 1][2 * i + (k & 1)] = y;
+        }
+      __syncwarp();
+    }
     // p v, the node's v in units of its size; tokens 2c, 2c + 1, 2c + 8, 2c + 9
     float4 x[4][VB / 4];
     float unit_v[4], inv_v[4];  // the unit's exponent, and 1 / unit
@@ -598,8 +639,7 @@ struct Kernel {
       for (int i = 0; i < VB / 4; ++i) {
         float4 &y = x[j][i];
         top = fmaxf(top, top4(y));
-        const bool all = finite(y.x) && finite(y.y) && finite(y.z) && finite(y.w);
-        if (!all) {
+        if (!finite4(y)) {
           hit |= 1u << t;
           y.x = finite(y.x) ? y.x : 0.0f;
           y.y = finite(y.y) ? y.y : 0.0f;
@@ -672,7 +712,7 @@ struct Kernel {
 
   // -------------------------------------------------------------------------
   __device__ __forceinline__ void run() {
-    const int row0 = tile * kRows, R = p.N * p.G;
+    const int row0 = this->row0(), R = p.N * p.G;
     const specdec_kv_cache &kv = p.cache;
     int bad = 0;
     len = kv.length[b];
@@ -719,13 +759,19 @@ struct Kernel {
     for (int i = 0; i < kMine; ++i) {
       const int r = warp + kWarps * i;
       float top = 0.0f;
+      bool all = true;
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) top = fmaxf(top, top4(qx[i][k]));
+      for (int k = 0; k < kPer; ++k) {
+        top = fmaxf(top, top4(qx[i][k]));
+        all &= finite4(qx[i][k]);
+      }
+      all = __all_sync(kAll, all);
 #pragma unroll
       for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
       const int ex = unit_exponent(top);
       const float inv = pow2i(-ex);
-      if (lane == 0) sm.q_exp[r] = pow2i(ex);
+      // a q that is not finite makes its row NaN
+      if (lane == 0) sm.q_exp[r] = all ? pow2i(ex) : __int_as_float(0x7fc00000);
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
         const int w = lane + 32 * k;

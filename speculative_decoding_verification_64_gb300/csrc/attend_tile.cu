@@ -1235,8 +1235,10 @@ struct Tile {
       for (int i = 0; i < mine; ++i) {
         float s = tmem_load1(s_at + i);
         const float rf = sm.rf[ring][c0 + i];
-        if (special && rf != 0.0f && exists)
-          s = -plain_dot(p, w.b, w.h, w.rt * RN + c0 + i, j) * (p.scale * kLog2e / rf);
+        // (rf is 0 under a scale of 0, and of rows that do not exist, which see nothing)
+        if (special && exists)
+          s = rf != 0.0f ? -plain_dot(p, w.b, w.h, w.rt * RN + c0 + i, j) * (p.scale * kLog2e / rf)
+                         : __int_as_float(0x7fc00000);
         __syncwarp();
         tmem_store1(s_at + i, s);
         tmem_stored();

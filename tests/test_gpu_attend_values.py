@@ -154,6 +154,44 @@ def test_a_cached_key_that_is_not_a_number(lib, dtype, large, scale, at, D):
           None, scale)
 
 
+@ways
+@pytest.mark.parametrize("scale", [0.0884, -0.0884, 0.0])
+@pytest.mark.parametrize("N,D", [(1, 128), (7, 64), (7, 128), (40, 128)])
+def test_infinite_drafted_keys(lib, dtype, large, scale, N, D):
+    """By the formula: scores of infinity, which make NaN, or of -infinity, which leave their token
+    out, or NaN where the query's element is 0."""
+    rng = np.random.default_rng(10)
+    lens, Hq, Hkv, block = [0, 17, 33], 4, 2, 16
+    parents = [ref.random_tree(rng, N) for _ in lens]
+    q, k, v = tokens(rng, 3, N, Hq, Hkv, D, dtype)
+    k[0, 0, 0, 3], k[1, N - 1, 1, 5], k[2, N // 2, 0, D - 1] = math.inf, -math.inf, math.inf
+    k[2, 0, 1, 0], k[2, 0, 1, 1], q[2, 0, 3, 0] = math.inf, -math.inf, 0
+    q[0, :, :2, 3] = -q[0, :, :2, 3].abs()     # all see node 0: -infinity there, or infinity
+    cache = ref.make_cache(rng, lens, [0] * 3, block, Hkv, D)
+    r = on(lib, large).attend(q, k, v, ref.on_gpu(cache), parent=torch.tensor(parents).int().cuda(),
+                              scale=scale)
+    check(r, q, k, v, cache, block, parents, scale)
+
+
+@ways
+@pytest.mark.parametrize("size", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+def test_a_query_that_is_not_finite_makes_its_row_nan(lib, dtype, large, size, softcap):
+    """Whatever its scores would be; a row that sees nothing stays empty."""
+    rng = np.random.default_rng(11)
+    B, N, Hq, Hkv, D, block = 3, 6, 4, 2, 128, 16
+    q, k, v = tokens(rng, B, N, Hq, Hkv, D, dtype)
+    q[0, 0, 1, 7] = q[1, 5, 3, 0] = q[2, 4, 2, 100] = size
+    cache = ref.make_cache(rng, [0, 40, 0], [0] * B, block, Hkv, D)
+    nodes = torch.tensor([6, 6, 4], dtype=torch.int32).cuda()
+    r = on(lib, large).attend(q, k, v, ref.on_gpu(cache), n_nodes=nodes, softcap=softcap)
+    for bad in ((0, 0, 1), (1, 5, 3)):
+        assert torch.isnan(r.out[bad]).all() and torch.isnan(r.lse[bad])
+    assert (r.out[2, 4:] == 0).all() and (r.lse[2, 4:] == -math.inf).all()
+    nan = torch.isnan(r.lse).cpu()
+    assert int(nan.sum()) == 2 and torch.isfinite(r.out[~nan]).all()
+
+
 # ---- windows of any size ----
 
 @ways
