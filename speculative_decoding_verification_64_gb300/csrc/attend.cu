@@ -1051,8 +1051,9 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams p) 
   const bool empty = bad != 0 || all == -INFINITY;
   const float inv = empty ? 0.0f : __fdividef(1.0f, sum);
   // four splits at a time, 128 elements of each, all loads before the sums
+  // (all lanes take every round, as each holds splits' factors)
 #pragma unroll 1
-  for (int d0 = lane; d0 < D; d0 += 128) {
+  for (int d0 = lane; d0 - lane < D; d0 += 128) {
     float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 1
     for (int s = 0; s < p.splits; s += 4) {

@@ -192,6 +192,21 @@ def test_a_query_that_is_not_finite_makes_its_row_nan(lib, dtype, large, size, s
     assert int(nan.sum()) == 2 and torch.isfinite(r.out[~nan]).all()
 
 
+# ---- heads of any size ----
+
+@ways
+@pytest.mark.parametrize("D", [16, 32, 48, 112, 128, 144, 160, 240, 256])
+@pytest.mark.parametrize("N", [1, 9])
+def test_heads_of_every_width_over_many_splits(lib, dtype, large, D, N):
+    """The join of splits takes 128 elements at a time, of which the last may be 16 only."""
+    rng = np.random.default_rng(12)
+    lens, Hq, Hkv, block = [897, 17, 400], 2, 1, 48
+    q, k, v = tokens(rng, 3, N, Hq, Hkv, D, dtype)
+    cache = ref.make_cache(rng, lens, [0] * 3, block, Hkv, D)
+    r = on(lib, large).attend(q, k, v, ref.on_gpu(cache))
+    check(r, q, k, v, cache, block, None, D ** -0.5)
+
+
 # ---- windows of any size ----
 
 @ways
