@@ -99,3 +99,49 @@ def test_streams_and_graphs(sd):
         assert (out.row_status == 0).all()
         cache["length"] = torch.tensor(lens, dtype=torch.int32)
         check(fresh, q, k, v, cache, block, None, [N] * B, D ** -0.5)
+
+
+def chain(q, k_new, v_new, k, v, scale, window):
+    """One request's chain in float64, all rows at once: out and the largest scale * sum |q| |k|."""
+    (N, Hq, D), G = q.shape, q.shape[1] // k_new.shape[1]
+    keys, vals = (torch.cat(x).double().repeat_interleave(G, 1) for x in ((k, k_new), (v, v_new)))
+    n = k.shape[0]
+    dist = n + torch.arange(N, device=q.device)[:, None] - torch.arange(n + N, device=q.device)
+    seen = (dist >= 0) & ((dist < window) if window else True)
+    s = torch.einsum("nhd,jhd->hnj", q.double(), keys) * scale
+    S = (torch.einsum("nhd,jhd->hnj", q.double().abs(), keys.abs()) * scale).amax()
+    p = torch.softmax(s.masked_fill(~seen, -math.inf), -1)
+    # (a hidden value has no part, finite or not)
+    out = torch.einsum("hnj,jhd->nhd", p, vals.nan_to_num(0.0))
+    bad = torch.einsum("nj,jhd->nhd", seen.double(), (~torch.isfinite(vals)).double()) > 0
+    return torch.where(bad, math.nan, out), torch.einsum("hnj,jhd->nhd", p, vals.abs().nan_to_num(0.0)), S
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("window,nan", [(0, False), (700, False), (700, True)])
+def test_the_longest_chunk_of_a_prompt(sd, dtype, window, nan):
+    """1024 nodes.  With v that is not finite in a drafted node and in tokens that the window hides
+    from some: each result looks for them one by one, which takes its time but is no error."""
+    rng = np.random.default_rng(3)
+    N, Hq, Hkv, D, block, n = 1024, 4, 2, 64, 16, 1500
+    q, k, v = tokens(rng, 1, N, Hq, Hkv, D, dtype)
+    cache = ref.make_cache(rng, [n], [0], block, Hkv, D)
+    if nan:
+        v[0, 300, 1, 7] = math.inf
+        for j in (n - 650, n - 100):
+            cache["v"][cache["block_table"][0, j // block], 0, j % block, 3] = 0x7F
+    kc, vc = (ref.cached_values(cache, x, 0, block).cuda() for x in ("k", "v"))
+    gpu = ref.on_gpu(cache)
+    more = torch.full((1, 2500), -1, dtype=torch.int32, device="cuda")
+    gpu.block_table = torch.cat([gpu.block_table, more], 1)   # room for a large call
+    r = sd.attend(q, k, v, gpu, window=window)
+    assert r.row_status.tolist() == [0]
+    want, A, S = chain(q[0], k[0], v[0], kc, vc, D ** -0.5, window)
+    # (the tolerance of test_gpu_attend.py with the largest S for all rows)
+    tol = A * (2 * 2.0 ** (-19 if dtype == torch.float32 else -16) * (1 + S) +
+               2 * 2.0 ** (-21 if dtype == torch.float32 else -11))
+    if dtype == torch.bfloat16:
+        tol = tol + want.abs().nan_to_num(0.0) * 2.0 ** -8
+    got, fine = r.out[0].double(), torch.isfinite(want)
+    assert torch.equal(torch.isfinite(got), fine)
+    assert ((got - want).abs()[fine] <= tol[fine]).all()
