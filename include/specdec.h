@@ -545,7 +545,14 @@ int specdec_kv_append(const void *k, const void *v, int dtype, long long k_strid
  *     s -= slopes[h] * (position of n - position of the token)      (slopes given)
  *     out = sum softmax(s) v,   lse = ln sum exp(s)
  * Masked tokens have no influence whatever they hold.  A node that sees
- * nothing, or only scores of -infinity, gets out = 0 and lse = -infinity.
+ * nothing, or only scores of -infinity, gets out = 0 and lse = -infinity; one
+ * that sees something gets NaN where its q is not finite, a score is NaN or
+ * +infinity.
+ * Scores, sums and outputs are held in float32.  The products carry float32 q,
+ * k, v and weights to 2^-21 of themselves.  In bfloat16 calls weights carry
+ * 2^-11, and an element of q, or of a drafted token's k, is exact or within
+ * 2^-17 of the largest element of its head.  v below 2^-56 may keep fewer bits
+ * in a row that sees nothing larger.
  *
  *   q             [B, N, Hq, D]; k_new, v_new [B, N, Hkv, D], float32 or bfloat16
  *                 (dtype), consecutive tokens *_stride elements apart
@@ -556,12 +563,14 @@ int specdec_kv_append(const void *k, const void *v, int dtype, long long k_strid
  *   out           [B, N, Hq, D] in dtype, contiguous
  *   lse           float32 [B, N, Hq] or NULL
  *   row_status    int32 [B]: SPECDEC_ROW_BAD_TREE, SPECDEC_ROW_BAD_CACHE (length
- *                 or a block id that is read), SPECDEC_ROW_INTERNAL; such a request
- *                 gets out = 0, lse = -infinity
+ *                 or a block id that is read); such a request gets out = 0, lse =
+ *                 -infinity.  SPECDEC_ROW_INTERNAL: some of its rows did, others may
+ *                 hold their results
  *   workspace     >= specdec_attend_workspace_size(...) bytes, 16-byte aligned;
  *                 0 bytes (NULL) where that is 0
  * Limits: N <= SPECDEC_MAX_TREE_NODES, Hq a multiple of Hkv, Hq <=
- * SPECDEC_MAX_HEADS, scale finite, softcap >= 0, window >= 0.
+ * SPECDEC_MAX_HEADS, scale finite, softcap >= 0, window >= 0.  A longer prompt
+ * goes in chunks, each appended to the cache before the next.
  * B = 0 and N = 0 are no-ops.
  */
 size_t specdec_attend_workspace_size(int B, int N, int Hq, int Hkv, int D, int dtype);

@@ -1108,8 +1108,8 @@ long long granules_of(const AttendParams &p) {
 // ... and no more than leave each warp a granule where the cache is full; up to
 // eight as a power of two, which a cluster joins.  More than eight go through the
 // workspace, which pays once eight leave a warp more than 32 granules: one request
-// of 5 (8 heads of 128, float32) takes 24.8 us with eight and 42.4 us with 33 over
-// 2048 tokens, 63.6 and 69.1 over 16384, 219 and 135 over 65536.
+// of 5 (8 heads of 128, float32) takes 26.5 us with eight and 36.4 us with 33 over
+// 2048 tokens, 66.8 and 62.4 over 16384, 230 and 133 over 65536.
 int splits_of(const AttendParams &p) {
   const int most = most_splits(p.B, p.N, p.cache.Hkv, p.G);
   const long long granules = granules_of(p), useful = (granules + kWarps - 1) / kWarps;
@@ -1142,10 +1142,10 @@ cudaError_t launch_stream(const AttendParams &p, cudaStream_t stream) {
 
 // bfloat16 calls that the streaming kernel takes before the tiles' kernel: as many
 // CTAs as run at once, two an SM, with up to 4 granules a warp, or 16 of narrow
-// heads.  (us here and there: one request of 5 over 128 tokens 18.5 and 22.3, over
-// 4096 28.7 and 28.7; 4 of 1 over 777 20.6 and 20.6, over 4096 28.9 and 25.3; 16 of
-// 1 over 16 18.5 and 22.0, over 128, with 384 CTAs, 32.9 and 21.9; heads of 64, 16
-// requests of 5 over 2048 24.8 and 31.7, over 4096 37.1 and 36.7.)
+// heads.  (us here and there: one request of 5 over 128 tokens 18.6 and 20.5, over
+// 4096 28.8 and 28.7; 4 of 1 over 777 20.7 and 20.5, over 4096 30.2 and 24.7; 16 of
+// 1 over 16 18.5 and 21.5, over 128, with 384 CTAs, 32.9 and 21.7; heads of 64, 16
+// requests of 5 over 2048 26.6 and 30.5, over 4096 37.2 and 35.4.)
 bool stream_is_quicker(const AttendParams &p) {
   const long long ctas = (long long)p.B * p.cache.Hkv * p.row_tiles * p.splits;
   return ctas <= 304 && granules_of(p) <= (long long)p.splits * kWarps * (p.cache.D <= 64 ? 16 : 4);

@@ -13,8 +13,9 @@
 //
 //   * K goes from the cache into the products as it is, e4m3.  A bfloat16 q has
 //     8 significant bits: scaled by a power of two per row it is the sum of two
-//     e4m3 values of 4 bits each, exactly for elements above 2^-10 of the row's
-//     largest (below, to 2^-19 of that).  Two products with K give q k^T.
+//     e4m3 values of 4 bits each, exactly for elements above 2^-9 of the row's largest;
+//     below, to 2^-17 of that, half of e4m3's smallest step: less than what a bfloat16 q
+//     has lost at its larger elements already.  Two products with K give q k^T.
 //   * V widens to fp16 exactly, in shared memory, four warps' work; P is fp16
 //     around 2^6 (11 bits, down to 2^-20 of the largest).  P in e4m3 would lose
 //     the many small weights under one large one.
@@ -42,17 +43,17 @@
 // by a second kernel, in order.  Up to 64 rows an SM holds two CTAs: one's
 // beginnings and ends of requests, which are chains of short steps, overlap the
 // other's tiles.  With 128 rows one CTA takes the whole SM, and four groups of
-// warps a quarter of the rows each (314 us for 32 trees of 64 nodes over 4096
-// tokens with a cap; two groups 343).
+// warps a quarter of the rows each (two groups took 9 % more for 32 trees of 64
+// nodes over 4096 tokens with a cap).
 // Roles: warp 0 copies (TMA), warp 1 issues products, warps 4-7 widen V, stage q
 // and build drafted tiles, the others take the softmax and write results.  A
 // request's drafted tiles come first: they are built while the results of the
 // request before are written.  Every wait is bounded in time.
 //
 // Measured (128 elements a head, 8 heads of k and v, G = 4): 256 requests of 9
-// nodes over 4096 tokens 402 us, 2.8 TB/s; 64 of 6 100 us, 2.8 TB/s; one of 5 over
-// 131071 80 us, 3.4 TB/s.  Neither HBM (42 %) nor the tensor cores (21 %) bound it
-// but the steps between: a tile's scores, softmax and products are a chain of
+// nodes over 4096 tokens 381 us, 2.9 TB/s; 64 of 6 97 us, 2.9 TB/s; one of 5 over
+// 131071 81 us, 3.3 TB/s; 32 trees of 64 over 4096 with a cap 306 us.  Neither HBM
+// (44 %) nor the tensor cores (busy 26 % of the time) bound it but the steps between: a tile's scores, softmax and products are a chain of
 // about 3300 clocks, of which an SM holds two.
 #include <cstddef>
 
@@ -455,7 +456,7 @@ struct Note {
 // second, where no wait of a working kernel takes a tenth of that (the longest are for
 // rows that see values that are not finite, `stray` below: tens of ms at 1024 nodes), and
 // says so in shared memory at `give_up`.  (A 64-bit timer, or a look at `give_up` on the
-// way, are more code at each wait: 403 to 412 us for the 256 requests above, 375 so.)
+// way, are more code at each wait: 7 to 10 % more time for the 256 requests above.)
 __device__ __forceinline__ bool wait_lane(uint32_t bar, uint32_t parity, uint32_t give_up) {
   uint32_t ok;
   asm volatile(
