@@ -89,8 +89,9 @@ extern "C" {
 #define SPECDEC_ROW_NONFINITE 4  /* a target row holds NaN or +inf, no finite value, or a max > 2^100 */
 #define SPECDEC_ROW_BAD_TEMP 8   /* temperature not 0 and not in [2^-20, 2^20] */
 #define SPECDEC_ROW_BAD_TREE 16  /* parent[0] != -1, parent[n] not in [0, n), or depth > max_depth */
-#define SPECDEC_ROW_INTERNAL 32  /* a kernel's bounded wait ran out: for a copy of its own, or (tree walk)
-                                    for another CTA of the request's cluster */
+#define SPECDEC_ROW_INTERNAL 32  /* a kernel's bounded wait ran out: for a copy of its own, (tree walk)
+                                    for another CTA of the request's cluster, or (attention) for
+                                    another warp */
 #define SPECDEC_ROW_BAD_CACHE 64 /* a cache length, token count or block id out of range */
 
 /* Limits. */
@@ -551,7 +552,7 @@ int specdec_kv_append(const void *k, const void *v, int dtype, long long k_strid
  * Scores, sums and outputs are held in float32.  The products carry float32 q,
  * k, v and weights to 2^-21 of themselves.  In bfloat16 calls weights carry
  * 2^-11, and an element of q, or of a drafted token's k, is exact or within
- * 2^-17 of the largest element of its head.  v below 2^-56 may keep fewer bits
+ * 2^-17 of the largest element of its head.  v below 2^-48 may keep fewer bits
  * in a row that sees nothing larger.
  *
  *   q             [B, N, Hq, D]; k_new, v_new [B, N, Hkv, D], float32 or bfloat16

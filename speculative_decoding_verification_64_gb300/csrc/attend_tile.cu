@@ -34,7 +34,7 @@
 //     the running maximum m of a row is that of s' + k, of what its tokens put into the
 //     outputs: a token that a row does not see, or sees with next to no weight, leaves
 //     the row alone whatever its size.  The sum of the weights under such an m is far
-//     from 1, which float32 has room for: units from 2^-66 up (v from about 2^-56) keep
+//     from 1, which float32 has room for: units from 2^-58 up (v from about 2^-48) keep
 //     all bits, smaller ones fewer in a row that sees nothing larger.
 //
 // A persistent grid.  All tiles of all requests, heads and row tiles form one
@@ -73,7 +73,9 @@ constexpr float kRaise = 8.0f;
 constexpr float kLift = 6.0f;
 constexpr float kMost = 15.0f;  // P's exponent is cut off there, until the maxima move
 constexpr float kUnit = 0x1p30f;       // of the outputs
-constexpr float kLeast = -96.0f;       // least exponent of a token's unit in those, for the maxima
+// Least exponent of a token's unit in those, for the maxima: weights of up to 2^(15 + 88),
+// and the sum of 2^24 of them inside float32.
+constexpr float kLeast = -88.0f;
 constexpr float kUnseen = 1e30f;       // minus the maximum of a row that has seen nothing
 constexpr unsigned kAll = 0xffffffffu;
 
