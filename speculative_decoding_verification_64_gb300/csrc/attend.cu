@@ -30,8 +30,8 @@
 // range has to fit what a row sees and nothing else: each row has a maximum m of its
 // scores, for the sum, and one of s' - m + k, ko, for the outputs.  The products'
 // weights are 2^(s' - m + k - ko) f: a token that the row does not see, or sees with
-// next to no weight, leaves them alone whatever its size.  Both maxima are rounded up
-// to integers, so that factors between them are exact.
+// next to no weight, leaves them alone whatever its size.  ko is an integer, so that the
+// token of the largest score, which may hold most of the weight, has a power of two.
 //
 // The drafted tokens' own k and v take the same path as granules of 16 nodes,
 // scaled to fp16 by a power of two per node (f = 1).  Where a mask hides part of a
@@ -89,10 +89,11 @@ __device__ __forceinline__ void split_unit(float x, float &k, float &f) {
   f = normal ? __uint_as_float((u & 0x7FFFFFu) | 0x3F800000u) : x * 0x1p126f;
 }
 
-// x 2^e for an integer e of any size (both factors are normal numbers).
+// x 2^e for an e of any size (all factors are normal numbers; exact for an integer).
 __device__ __forceinline__ float times_pow2(float x, float e) {
-  const int n = (int)fminf(fmaxf(e, -252.0f), 252.0f), half = n / 2;
-  return x * pow2i(half) * pow2i(n - half);
+  const float whole = rintf(fminf(fmaxf(e, -252.0f), 252.0f));
+  const int n = (int)whole, half = n / 2;
+  return x * ex2_approx(e - whole) * pow2i(half) * pow2i(n - half);
 }
 
 __device__ __forceinline__ uint4 ldg_stream(const uint8_t *p) {
@@ -194,7 +195,7 @@ struct Kernel {
       float top = fmaxf(fmaxf(x[0][2 * i], x[0][2 * i + 1]), fmaxf(x[1][2 * i], x[1][2 * i + 1]));
       top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
       top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
-      to[i] = fmaxf(m[i], ceilf(top));
+      to[i] = fmaxf(m[i], top);
       at[i] = m[i] == -INFINITY ? -INFINITY : ko[i] + (m[i] - to[i]);
       const float from = to[i] == -INFINITY ? 0.0f : to[i];
       if (kSame) {
@@ -212,7 +213,7 @@ struct Kernel {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         l[i] *= m[i] == -INFINITY ? 0.0f : ex2_approx(m[i] - to[i]);
-        ko[i] = fmaxf(at[i], ceilf(best[i]));
+        ko[i] = fmaxf(floorf(at[i]), ceilf(best[i]));  // (nothing is lost by a smaller unit)
         const float f = at[i] == -INFINITY ? 0.0f : ex2_approx(at[i] - ko[i]);
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
