@@ -548,7 +548,7 @@ int specdec_kv_append(const void *k, const void *v, int dtype, long long k_strid
  * Masked tokens have no influence whatever they hold.  A node that sees
  * nothing, or only scores of -infinity, gets out = 0 and lse = -infinity; one
  * that sees something gets NaN where its q is not finite, a score is NaN or
- * +infinity.
+ * +infinity.  A token whose score is -infinity takes no part.
  * Scores, sums and outputs are held in float32.  The products carry float32 q,
  * k, v and weights to 2^-21 of themselves.  In bfloat16 calls weights carry
  * 2^-11, and an element of q, or of a drafted token's k, is exact or within

@@ -675,7 +675,18 @@ struct Kernel {
           mma16816(o[n], a, low_half2(y[0], y[1], b0), low_half2(y[2], y[3], b1));
         }
       }
-    while (hit) {  // infinities and NaN reach the rows that see their node, no others
+    if (hit) {  // infinities and NaN reach the rows that see their node, no others ...
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {  // ... and not under a score of -infinity
+        unsigned none = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (s[0][k >> 1][2 * i + (k & 1)] == -INFINITY) none |= 1u << ((k >> 1) * 8 + 2 * c + (k & 1));
+        none |= __shfl_xor_sync(kAll, none, 1);
+        see[i] &= ~(none | __shfl_xor_sync(kAll, none, 2));
+      }
+    }
+    while (hit) {
       const int t = __ffs(hit) - 1;
       hit &= hit - 1;
 #pragma unroll 1

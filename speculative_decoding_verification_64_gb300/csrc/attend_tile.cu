@@ -140,7 +140,6 @@ struct Smem {
   // one three before may still be written
   alignas(16) float rf[4][RN];            // what turns a product into base-2 units
   float slope[4][RN], depth[4][RN];       // of the bias by distance; position from the length
-  uint8_t node[4][RN];
   // per softmax group, by column
   alignas(16) float nm[C::kGroups][C::kCols];      // kLift - m, m of scores and units
   // the square root of l's and O's factor when m moves (at the end: addresses, 8 bytes each)
@@ -529,6 +528,7 @@ __device__ __forceinline__ bool partly_hidden(const AttendParams &p, const Reque
 __device__ __noinline__ float plain_dot(const AttendParams &p, int b, int h, int row, int node) {
   const int D = p.cache.D, n = row / p.G, hq = h * p.G + row - n * p.G;
   float s = 0.0f;
+#pragma unroll 1
   for (int e = 0; e < D; ++e)
     s += load_elem(p.q, SPECDEC_BF16, ((long long)b * p.N + n) * p.q_stride + (long long)hq * D + e) *
          load_elem(p.k_new, SPECDEC_BF16,
@@ -536,20 +536,22 @@ __device__ __noinline__ float plain_dot(const AttendParams &p, int b, int h, int
   return s;
 }
 
-// The sum of what is not finite among the v that a node sees in tiles [t0, t1),
-// at element d: drafted tokens', and cached ones' at the window's edge.
+// The sum of what is not finite among the v that a row sees in tiles [t0, t1), at
+// element d: drafted tokens', and cached ones' at the window's edge.  A score of
+// -infinity, which takes a k that is not finite, leaves its token out.
 __device__ __noinline__ float stray(const AttendParams &p, int box, int b, int h, int t0, int t1,
-                                    int n, int pos, int d) {
+                                    int row, int pos, int d) {
   const specdec_kv_cache &kv = p.cache;
   const Request r = request_of(p, b, box);
   float sum = 0.0f;
   const int j0 = t0 * kTok, j1 = min(t1, r.drafted) * kTok;
-  int a = n;
+  int a = row / p.G;
+#pragma unroll 1
   for (int step = 0; a >= 0 && (p.window == 0 || step < p.window); ++step) {
     if (a >= j0 && a < j1) {
       const float y = load_elem(p.v_new, SPECDEC_BF16,
                                 ((long long)b * p.N + a) * p.v_stride + (long long)h * kv.D + d);
-      if (!finite(y)) sum += y;
+      if (!finite(y) && !(p.softcap == 0.0f && plain_dot(p, b, h, row, a) * p.scale == -INFINITY)) sum += y;
     }
     int up = a - 1;
     if (p.parent && a > 0) {
@@ -558,7 +560,9 @@ __device__ __noinline__ float stray(const AttendParams &p, int box, int b, int h
     }
     a = up;
   }
+#pragma unroll 1
   for (int t = max(t0, r.drafted); t < t1 && partly_hidden(p, r, t); ++t)
+#pragma unroll 1
     for (int i = 0; i < kTok; ++i) {
       const int at = r.from + (t - r.drafted) * kTok + i;
       if (at >= r.len || pos - at >= p.window) continue;
@@ -962,7 +966,6 @@ struct Tile {
           // a q that is not finite makes its row NaN
           const float unit = all ? pow2i(ex) : __int_as_float(0x7fc00000);
           const int depth = in && (p.window > 0 || p.slopes) ? depth_of(w.b, n) : 0;
-          sm.node[ring][col] = (uint8_t)(n - node_of(row0));
           sm.rf[ring][col] = in ? p.scale * kLog2e * unit : 0.0f;
           sm.depth[ring][col] = (float)depth;
           if (!kPlain)
@@ -1530,7 +1533,7 @@ struct Tile {
         for (int i = 0; i < mine; ++i) {
           float extra = 0.0f;
           if (out_at[i] && tok < kv.D && out_fac[i] != 0.0f)
-            extra = stray(p, box, w.b, w.h, t0, t1, sm.node[ring][c0 + i] + node_of(w.rt * RN),
+            extra = stray(p, box, w.b, w.h, t0, t1, w.rt * RN + c0 + i,
                           w.r.len + (int)sm.depth[ring][c0 + i], tok);
           __syncwarp();
           tmem_store1(o_at + i, tmem_load1(o_at + i) + extra);

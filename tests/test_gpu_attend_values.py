@@ -192,6 +192,25 @@ def test_a_query_that_is_not_finite_makes_its_row_nan(lib, dtype, large, size, s
     assert int(nan.sum()) == 2 and torch.isfinite(r.out[~nan]).all()
 
 
+@ways
+@pytest.mark.parametrize("N,D", [(1, 128), (6, 64), (40, 128)])
+def test_a_score_of_minus_infinity_leaves_its_token_out(lib, dtype, large, N, D):
+    """Also where its v is not finite: the result is that of a token with any other v."""
+    rng = np.random.default_rng(13)
+    lens, Hq, Hkv, block = [17, 40], 4, 2, 16
+    q, k, v = tokens(rng, 2, N, Hq, Hkv, D, dtype)
+    parents = [ref.random_tree(rng, N) for _ in lens]
+    cache = ref.make_cache(rng, lens, [0] * 2, block, Hkv, D)
+    q[:, :, :, 1] = q[:, :, :, 1].abs() + 0.5
+    k[0, 0, 0, 1] = k[1, N - 1, 1, 1] = -math.inf
+    how = dict(parent=torch.tensor(parents).int().cuda())
+    want = on(lib, large).attend(q, k, v, ref.on_gpu(cache), **how)
+    check(want, q, k, v, cache, block, parents, D ** -0.5)
+    v[0, 0, 0, 3], v[0, 0, 0, 4], v[1, N - 1, 1, D - 1] = math.inf, math.nan, -math.inf
+    got = on(lib, large).attend(q, k, v, ref.on_gpu(cache), **how)
+    assert torch.equal(got.out, want.out) and torch.equal(got.lse, want.lse)
+
+
 # ---- heads of any size ----
 
 @ways
