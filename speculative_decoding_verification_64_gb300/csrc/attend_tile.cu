@@ -524,57 +524,6 @@ __device__ __forceinline__ bool partly_hidden(const AttendParams &p, const Reque
   return p.window > 0 && r.from + (t - r.drafted) * kTok <= r.len + p.N - 1 - p.window;
 }
 
-// q . k of one row and one drafted token, from global memory, term by term.
-__device__ __noinline__ float plain_dot(const AttendParams &p, int b, int h, int row, int node) {
-  const int D = p.cache.D, n = row / p.G, hq = h * p.G + row - n * p.G;
-  float s = 0.0f;
-#pragma unroll 1
-  for (int e = 0; e < D; ++e)
-    s += load_elem(p.q, SPECDEC_BF16, ((long long)b * p.N + n) * p.q_stride + (long long)hq * D + e) *
-         load_elem(p.k_new, SPECDEC_BF16,
-                   ((long long)b * p.N + node) * p.k_stride + (long long)h * D + e);
-  return s;
-}
-
-// The sum of what is not finite among the v that a row sees in tiles [t0, t1), at
-// element d: drafted tokens', and cached ones' at the window's edge.  A score of
-// -infinity, which takes a k that is not finite, leaves its token out.
-__device__ __noinline__ float stray(const AttendParams &p, int box, int b, int h, int t0, int t1,
-                                    int row, int pos, int d) {
-  const specdec_kv_cache &kv = p.cache;
-  const Request r = request_of(p, b, box);
-  float sum = 0.0f;
-  const int j0 = t0 * kTok, j1 = min(t1, r.drafted) * kTok;
-  int a = row / p.G;
-#pragma unroll 1
-  for (int step = 0; a >= 0 && (p.window == 0 || step < p.window); ++step) {
-    if (a >= j0 && a < j1) {
-      const float y = load_elem(p.v_new, SPECDEC_BF16,
-                                ((long long)b * p.N + a) * p.v_stride + (long long)h * kv.D + d);
-      if (!finite(y) && !(p.softcap == 0.0f && plain_dot(p, b, h, row, a) * p.scale == -INFINITY)) sum += y;
-    }
-    int up = a - 1;
-    if (p.parent && a > 0) {
-      up = p.parent[(long long)b * p.N + a];
-      if (up >= a) up = -1;
-    }
-    a = up;
-  }
-#pragma unroll 1
-  for (int t = max(t0, r.drafted); t < t1 && partly_hidden(p, r, t); ++t)
-#pragma unroll 1
-    for (int i = 0; i < kTok; ++i) {
-      const int at = r.from + (t - r.drafted) * kTok + i;
-      if (at >= r.len || pos - at >= p.window) continue;
-      const int id = kv.block_table[(long long)b * kv.max_blocks + at / kv.block];
-      if (id < 0 || id >= kv.n_blocks) continue;
-      const uint8_t code = reinterpret_cast<const uint8_t *>(
-          kv.v)[(((long long)id * kv.Hkv + h) * kv.block + at % kv.block) * kv.D + d];
-      if ((code & 0x7Fu) == 0x7Fu) sum = __int_as_float(0x7fc00000);
-    }
-  return sum;
-}
-
 // A partial: for each row m, l, then its D elements; flags as l < 0.
 __host__ __device__ inline size_t partial_floats(int RN, int D) { return (size_t)RN * (D + 2); }
 // Two slots a CTA: what it did of a unit begun before, and of one that it began.
@@ -807,12 +756,12 @@ struct Tile {
     return true;
   }
 
-  // O^T += V^T P^T of tile c, as soon as both are there.
+  // O^T += V^T P^T of tile c, as soon as both are there.  (Inline, and what runs in rare
+  // cases last in this class: functions stand behind the kernel's body in this order, so
+  // that the size of the rare ones does not shift what runs at every tile within the
+  // instruction cache, which is worth up to 10 % either way.)
   __device__ __forceinline__ bool outputs(uint32_t c, bool first) {
-    return outputs_of(sm, sm_tmem + 2 * RN, columns, c, first);
-  }
-  static __device__ __noinline__ bool outputs_of(S &sm, uint32_t d, int columns, uint32_t c,
-                                                 bool first) {
+    const uint32_t d = sm_tmem + 2 * RN;
     const uint32_t give_up = smem_addr(&sm.give_up);
     if (!__all_sync(kAll, wait_lane(smem_addr(&sm.vh_full[c % kBuf]), full_par(c, kBuf), give_up) &&
                               wait_lane(smem_addr(&sm.p_full[c % kBuf]), full_par(c, kBuf), give_up)))
@@ -1564,6 +1513,57 @@ struct Tile {
       if (leader) sm.done[group] = index + 1;
       if (!(ok = meet_all())) break;
     }
+  }
+
+  // q . k of one row and one drafted token, from global memory, term by term.
+  static __device__ __noinline__ float plain_dot(const AttendParams &p, int b, int h, int row, int node) {
+    const int D = p.cache.D, n = row / p.G, hq = h * p.G + row - n * p.G;
+    float s = 0.0f;
+#pragma unroll 1
+    for (int e = 0; e < D; ++e)
+      s += load_elem(p.q, SPECDEC_BF16, ((long long)b * p.N + n) * p.q_stride + (long long)hq * D + e) *
+           load_elem(p.k_new, SPECDEC_BF16,
+                     ((long long)b * p.N + node) * p.k_stride + (long long)h * D + e);
+    return s;
+  }
+
+  // The sum of what is not finite among the v that a row sees in tiles [t0, t1), at
+  // element d: drafted tokens', and cached ones' at the window's edge.  A score of
+  // -infinity, which takes a k that is not finite, leaves its token out.
+  static __device__ __noinline__ float stray(const AttendParams &p, int box, int b, int h, int t0, int t1,
+                                      int row, int pos, int d) {
+    const specdec_kv_cache &kv = p.cache;
+    const Request r = request_of(p, b, box);
+    float sum = 0.0f;
+    const int j0 = t0 * kTok, j1 = min(t1, r.drafted) * kTok;
+    int a = row / p.G;
+#pragma unroll 1
+    for (int step = 0; a >= 0 && (p.window == 0 || step < p.window); ++step) {
+      if (a >= j0 && a < j1) {
+        const float y = load_elem(p.v_new, SPECDEC_BF16,
+                                  ((long long)b * p.N + a) * p.v_stride + (long long)h * kv.D + d);
+        if (!finite(y) && !(p.softcap == 0.0f && plain_dot(p, b, h, row, a) * p.scale == -INFINITY)) sum += y;
+      }
+      int up = a - 1;
+      if (p.parent && a > 0) {
+        up = p.parent[(long long)b * p.N + a];
+        if (up >= a) up = -1;
+      }
+      a = up;
+    }
+#pragma unroll 1
+    for (int t = max(t0, r.drafted); t < t1 && partly_hidden(p, r, t); ++t)
+#pragma unroll 1
+      for (int i = 0; i < kTok; ++i) {
+        const int at = r.from + (t - r.drafted) * kTok + i;
+        if (at >= r.len || pos - at >= p.window) continue;
+        const int id = kv.block_table[(long long)b * kv.max_blocks + at / kv.block];
+        if (id < 0 || id >= kv.n_blocks) continue;
+        const uint8_t code = reinterpret_cast<const uint8_t *>(
+            kv.v)[(((long long)id * kv.Hkv + h) * kv.block + at % kv.block) * kv.D + d];
+        if ((code & 0x7Fu) == 0x7Fu) sum = __int_as_float(0x7fc00000);
+      }
+    return sum;
   }
 
   // After a wait ran out: the segments that were not finished get no result, and the
