@@ -552,8 +552,9 @@ int specdec_kv_append(const void *k, const void *v, int dtype, long long k_strid
  * Scores, sums and outputs are held in float32.  The products carry float32 q,
  * k, v and weights to 2^-21 of themselves.  In bfloat16 calls weights carry
  * 2^-11, and an element of q, or of a drafted token's k, is exact or within
- * 2^-17 of the largest element of its head.  v below 2^-48 may keep fewer bits
- * in a row that sees nothing larger.
+ * 2^-17 of the largest element of its head; v below 2^-48, and weights below
+ * 2^-80 of a row's largest, may keep fewer bits in a row of which nothing else
+ * is left.
  *
  *   q             [B, N, Hq, D]; k_new, v_new [B, N, Hkv, D], float32 or bfloat16
  *                 (dtype), consecutive tokens *_stride elements apart

@@ -35,7 +35,8 @@
 //     outputs: a token that a row does not see, or sees with next to no weight, leaves
 //     the row alone whatever its size.  The sum of the weights under such an m is far
 //     from 1, which float32 has room for: units from 2^-58 up (v from about 2^-48) keep
-//     all bits, smaller ones fewer in a row that sees nothing larger.
+//     all bits, smaller ones (as after scores whose v is 0, weights below 2^-80 of
+//     theirs) fewer in a row that sees nothing larger.
 //
 // A persistent grid.  All tiles of all requests, heads and row tiles form one
 // line that is cut into equal parts, one per CTA, from the lengths on the device:
@@ -51,8 +52,8 @@
 // request before are written.  Every wait is bounded in time.
 //
 // Measured (128 elements a head, 8 heads of k and v, G = 4): 256 requests of 9
-// nodes over 4096 tokens 381 us, 2.9 TB/s; 64 of 6 97 us, 2.9 TB/s; one of 5 over
-// 131071 81 us, 3.3 TB/s; 32 trees of 64 over 4096 with a cap 306 us.  Neither HBM
+// nodes over 4096 tokens 379 us, 3.0 TB/s; 64 of 6 95 us, 2.9 TB/s; one of 5 over
+// 131071 81 us, 3.3 TB/s; 32 trees of 64 over 4096 with a cap 297 us.  Neither HBM
 // (44 %) nor the tensor cores (busy 26 % of the time) bound it but the steps between: a tile's scores, softmax and products are a chain of
 // about 3300 clocks, of which an SM holds two.
 #include <cstddef>
