@@ -54,8 +54,9 @@
 // Measured (128 elements a head, 8 heads of k and v, G = 4): 256 requests of 9
 // nodes over 4096 tokens 379 us, 3.0 TB/s; 64 of 6 95 us, 2.9 TB/s; one of 5 over
 // 131071 81 us, 3.3 TB/s; 32 trees of 64 over 4096 with a cap 297 us.  Neither HBM
-// (44 %) nor the tensor cores (busy 26 % of the time) bound it but the steps between: a tile's scores, softmax and products are a chain of
-// about 3300 clocks, of which an SM holds two.
+// (44 %) nor the tensor cores (busy 26 % of the time) bound it but the steps
+// between: a tile's scores, softmax and products are a chain of about 3300 clocks, of
+// which an SM holds two.
 #include <cstddef>
 
 #include <cuda.h>
