@@ -170,11 +170,14 @@ def _stream_ptr(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(s.cuda_stream)
 
 
+_HERE_AND_NOW = contextlib.nullcontext()
+
+
 def _on(stream):
     """Where a call on ``stream`` makes its outputs and workspaces: with that stream current,
     so that torch's allocator hands their memory out again in its order, and not to other
     streams while the call's kernels still use it."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return _HERE_AND_NOW if stream is None else torch.cuda.stream(stream)
 
 
 def _cuda(**tensors):
