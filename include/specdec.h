@@ -93,6 +93,7 @@ extern "C" {
                                     for another CTA of the request's cluster, or (attention) for
                                     another warp */
 #define SPECDEC_ROW_BAD_CACHE 64 /* a cache length, token count or block id out of range */
+#define SPECDEC_ROW_BAD_FILTER 128 /* top_k < 0 or > SPECDEC_MAX_TOPK, top_p or min_p not in [0, 1] */
 
 /* Limits. */
 #define SPECDEC_MAX_GAMMA 32       /* linear: drafted positions per request */
@@ -100,7 +101,10 @@ extern "C" {
 #define SPECDEC_MAX_TREE_DEPTH 64
 #define SPECDEC_MAX_V (1 << 21)
 #define SPECDEC_MAX_UNIFORMS (1ll << 40) /* words per specdec_philox_uniforms call */
-#define SPECDEC_MAX_TOPK 1024            /* candidates of specdec_verify_linear_topk */
+#define SPECDEC_MAX_TOPK 1024            /* candidates of specdec_verify_linear_topk; top_k of
+                                            specdec_sample, entries of a row's record */
+#define SPECDEC_MAX_DRAFT_V (1 << 19)    /* vocabulary of specdec_sample and specdec_distill */
+#define SPECDEC_MAX_DRAWS 64             /* draws a row of specdec_sample */
 
 /* ABI version of the loaded library (SPECDEC_ABI_VERSION at build time). */
 int specdec_abi_version(void);
@@ -582,6 +586,126 @@ int specdec_attend(const void *q, const void *k_new, const void *v_new, int dtyp
                    int B, int N, int Hq, float scale, float softcap, const float *slopes,
                    int window, void *out, float *lse, int32_t *row_status, void *workspace,
                    size_t workspace_bytes, void *stream);
+
+/*
+ * The draft side of the step: what specdec_verify_linear / specdec_verify_tree take as
+ * given (drafted tokens and q), and what a verify step leaves to train the draft with.
+ *
+ * Rows of logits stand in requests of R rows: row (b, r) at request_stride * b +
+ * row_stride * r elements, its V elements one after another.  Rows may be slices (of a
+ * padded vocabulary, of one position of a [B, gamma, V] array) and start anywhere an
+ * element may.  Rows that a call writes follow the same rule with strides of their own,
+ * may be the rows that it reads (same pointer and strides) and must not overlap them
+ * otherwise.  A row is usable as in specdec_row_stats: no NaN or +infinity, one finite
+ * value, none above 2^100; -infinity takes a token out.  row_status is per row here.
+ */
+
+/*
+ * Tokens drawn from rows of logits, and the distributions that they were drawn from.
+ *
+ * With w_v = exp((l_v - max l) / T) and tokens in the order of their place (the larger
+ * logit first, equal ones by index), these filters keep, one after another:
+ *   top_k  the first top_k places (0: all);
+ *   top_p  of those the fewest first places whose mass is at least top_p of theirs, one at
+ *          least (1: all);
+ *   min_p  of those the tokens with w_v >= min_p (0: all).
+ * Tokens at -infinity are never kept.  T = 0 is greedy: the first place alone.  Draw d
+ * takes the first kept token, by index, with
+ *     sum of w over the kept tokens up to it  >  uniforms[b, r, d] * sum over all kept,
+ * the convention of the verify calls' final draw.  Several draws of a row are the i.i.d.
+ * children of a tree node.  Weights carry about 2^-35 of themselves, to 2^-42 of the
+ * largest, and their sums are exact: cuts and draws are those of 64-bit floating point but
+ * for borders nearer than about 1e-10 of the mass, and no order of the work shows in them.
+ *
+ *   logits      [B, R, V], float32 or bfloat16 (dtype)
+ *   temperature float32 [B]: 0 or in [2^-20, 2^20]
+ *   top_k       int32 [B], in [0, SPECDEC_MAX_TOPK], or NULL (0)
+ *   top_p       float32 [B], in [0, 1], or NULL (1)
+ *   min_p       float32 [B], in [0, 1], or NULL (0)
+ *   uniforms    float32 [B, R, S], in (0, 1); NULL with S = 0
+ *   tokens      int32 [B, R, S]; NULL with S = 0
+ *   rows        [B, R, V] in dtype, or NULL: the distribution w / sum over the kept, 0 for
+ *               the others (the q of the verify calls); with SPECDEC_SAMPLE_LOGITS the
+ *               logits of the kept, -infinity for the others (a target's rows under a
+ *               filter, for the verify calls at the same temperature)
+ *   kept        int32 [B, R]: how many tokens the filters kept
+ *   row_status  int32 [B, R]: SPECDEC_ROW_BAD_TEMP, SPECDEC_ROW_BAD_FILTER,
+ *               SPECDEC_ROW_NONFINITE, SPECDEC_ROW_INTERNAL; such a row gets tokens of -1,
+ *               NaN in rows, kept 0
+ * Limits: 0 <= S <= SPECDEC_MAX_DRAWS, V <= SPECDEC_MAX_DRAFT_V.  B = 0 is a no-op.
+ */
+#define SPECDEC_SAMPLE_LOGITS 1u
+int specdec_sample(const void *logits, int dtype, long long request_stride, long long row_stride,
+                   const float *temperature, const int32_t *top_k, const float *top_p,
+                   const float *min_p, const float *uniforms, int B, int R, int V, int S,
+                   unsigned flags, int32_t *tokens, void *rows, long long rows_request_stride,
+                   long long rows_row_stride, int32_t *kept, int32_t *row_status, void *stream);
+
+/*
+ * The K largest logits of every row, largest first, equal ones by index, and the row's
+ * log-sum-exp: a record of the target's row to train a draft with (specdec_distill).
+ *   logits      [B, R, V]
+ *   temperature of the log-sum-exp, in [2^-20, 2^20]; values are not divided by it
+ *   values      float32 [B, R, K]
+ *   ids         int32 [B, R, K]
+ *   lse         float32 [B, R]: ln sum_v exp(l_v / temperature)
+ *   row_status  int32 [B, R]: SPECDEC_ROW_NONFINITE, SPECDEC_ROW_INTERNAL; such a row gets
+ *               NaN values and lse, and ids of -1
+ *   workspace   >= specdec_top_logits_workspace_size(...) bytes, 16-byte aligned
+ * Limits: 1 <= K <= min(V, SPECDEC_MAX_TOPK), V <= SPECDEC_MAX_V.  B = 0 is a no-op.
+ */
+size_t specdec_top_logits_workspace_size(int B, int R, int V, int dtype);
+int specdec_top_logits(const void *logits, int dtype, long long request_stride,
+                       long long row_stride, float temperature, int B, int R, int V, int K,
+                       float *values, int32_t *ids, float *lse, int32_t *row_status,
+                       void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Divergence of a draft's rows from a teacher's records, and its gradient.
+ *
+ * With s = softmax(x / T) of the draft's logits x and a record of K entries (id, z):
+ *   with teacher_lse   p_j = exp(z_j / T - lse), r = max(0, 1 - sum_j p_j);
+ *   without            p = softmax of z / T over the entries, r = 0;
+ *   loss = sum_j p_j (ln p_j - ln s_id_j) + r (ln r - ln s_rest),
+ * s_rest the mass of s outside the entries: the divergence KL(p || s), what the record
+ * does not name taken as one token.  The gradient written is weight * d loss / d x.
+ * r below 2^-20 (what a float32 lse leaves unsure) counts as 0 where s_rest is 0.
+ *
+ *   logits       [B, R, V], float32 or bfloat16 (dtype)
+ *   ids          int32 [B, R, K]; -1: no entry there.  No token twice
+ *   teacher      float32 [B, R, K]: the teacher's logits z (not read at ids of -1);
+ *                -infinity: p = 0
+ *   teacher_lse  float32 [B, R] (for the same temperature) or NULL
+ *   weight       float32 [B, R] or NULL (1)
+ *   temperature  T, in [2^-20, 2^20]
+ *   loss         float32 [B, R], without the weight
+ *   grad         [B, R, V] in dtype, or NULL: the loss alone
+ *   row_status   int32 [B, R]: SPECDEC_ROW_BAD_TOKEN (an id outside [-1, V), a token
+ *                twice), SPECDEC_ROW_NONFINITE (an unusable row, teacher or weight),
+ *                SPECDEC_ROW_INTERNAL; such a row gets NaN in its loss and its gradient
+ * A row of weight 0, or without an entry, gets loss 0, gradient 0 and status 0 whatever
+ * it holds.  Limits: 1 <= K <= SPECDEC_MAX_TOPK, V <= SPECDEC_MAX_DRAFT_V.  B = 0 is a
+ * no-op.
+ */
+int specdec_distill(const void *logits, int dtype, long long request_stride, long long row_stride,
+                    const int32_t *ids, const float *teacher, const float *teacher_lse,
+                    const float *weight, float temperature, int B, int R, int V, int K,
+                    float *loss, void *grad, long long grad_request_stride,
+                    long long grad_row_stride, int32_t *row_status, void *stream);
+
+/*
+ * The gradient of specdec_distill's rows under an incoming gradient dloss float32 [B, R] of
+ * each row's weighted loss: grad, which holds weight * d loss / d x from specdec_distill
+ * with the same arguments, becomes dloss * weight * d loss / d x.  Rows of dloss 1 are left
+ * as they are (nothing is read or written there), the others are computed anew, so that a
+ * value is rounded once.  grad must not overlap the logits.
+ */
+int specdec_distill_backward(const void *logits, int dtype, long long request_stride,
+                             long long row_stride, const int32_t *ids, const float *teacher,
+                             const float *teacher_lse, const float *weight, const float *dloss,
+                             float temperature, int B, int R, int V, int K, void *grad,
+                             long long grad_request_stride, long long grad_row_stride,
+                             void *stream);
 
 #ifdef __cplusplus
 }

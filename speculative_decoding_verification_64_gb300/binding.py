@@ -29,6 +29,7 @@ ROW_BAD_TEMP = 8
 ROW_BAD_TREE = 16
 ROW_INTERNAL = 32
 ROW_BAD_CACHE = 64
+ROW_BAD_FILTER = 128
 
 _lib = None
 
@@ -107,6 +108,22 @@ _EXPORTS = {
                        [ctypes.c_void_p] * 3 + [ctypes.c_int] * 3 + [ctypes.c_float] * 2 +
                        [ctypes.c_void_p, ctypes.c_int] + [ctypes.c_void_p] * 4 +
                        [ctypes.c_size_t, ctypes.c_void_p], ctypes.c_int),
+    "specdec_sample": ([ctypes.c_void_p, ctypes.c_int] + [ctypes.c_longlong] * 2 +
+                       [ctypes.c_void_p] * 5 + [ctypes.c_int] * 4 + [ctypes.c_uint] +
+                       [ctypes.c_void_p] * 2 + [ctypes.c_longlong] * 2 + [ctypes.c_void_p] * 3,
+                       ctypes.c_int),
+    "specdec_top_logits_workspace_size": ([ctypes.c_int] * 4, ctypes.c_size_t),
+    "specdec_top_logits": ([ctypes.c_void_p, ctypes.c_int] + [ctypes.c_longlong] * 2 +
+                           [ctypes.c_float] + [ctypes.c_int] * 4 + [ctypes.c_void_p] * 5 +
+                           [ctypes.c_size_t, ctypes.c_void_p], ctypes.c_int),
+    "specdec_distill": ([ctypes.c_void_p, ctypes.c_int] + [ctypes.c_longlong] * 2 +
+                        [ctypes.c_void_p] * 4 + [ctypes.c_float] + [ctypes.c_int] * 4 +
+                        [ctypes.c_void_p] * 2 + [ctypes.c_longlong] * 2 + [ctypes.c_void_p] * 2,
+                        ctypes.c_int),
+    "specdec_distill_backward": ([ctypes.c_void_p, ctypes.c_int] + [ctypes.c_longlong] * 2 +
+                                 [ctypes.c_void_p] * 5 + [ctypes.c_float] + [ctypes.c_int] * 4 +
+                                 [ctypes.c_void_p] + [ctypes.c_longlong] * 2 + [ctypes.c_void_p],
+                                 ctypes.c_int),
 }
 
 
@@ -970,3 +987,263 @@ def attend(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: KVCache,
         out.row_status.data_ptr(), workspace.data_ptr(), workspace.numel(), raw)
     _check(rc, "specdec_attend")
     return out
+
+
+# ---------------------------------------------------------------------------
+# the draft side of the step: sampling, records of the target's rows, distillation
+# ---------------------------------------------------------------------------
+
+SAMPLE_LOGITS = 1
+
+
+@dataclasses.dataclass
+class SampleOut:
+    tokens: Optional[torch.Tensor]  # int32 [B, R, S]
+    rows: Optional[torch.Tensor]    # [B, R, V] in the logits' dtype
+    kept: torch.Tensor              # int32 [B, R]
+    row_status: torch.Tensor        # int32 [B, R]
+
+
+@dataclasses.dataclass
+class TopOut:
+    values: torch.Tensor      # float32 [B, R, K], largest first
+    ids: torch.Tensor         # int32 [B, R, K]
+    lse: torch.Tensor         # float32 [B, R]
+    row_status: torch.Tensor  # int32 [B, R]
+
+
+@dataclasses.dataclass
+class DistillOut:
+    loss: torch.Tensor            # float32 [B, R]
+    grad: Optional[torch.Tensor]  # [B, R, V] in the logits' dtype
+    row_status: torch.Tensor      # int32 [B, R]
+
+
+def _rows3(t: torch.Tensor, name: str, dtype, shape):
+    """The strides, in elements, of requests and of rows of a [B, R, V] tensor whose rows are
+    contiguous (``shape`` None: any)."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [B, R, V], got {tuple(t.shape)}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    s = t.stride()
+    if s[2] != 1 and t.shape[2] > 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous, got strides {s}")
+    return s[0], s[1]
+
+
+def _sample(logits, temperature, uniforms, top_k, top_p, min_p, rows, flags, out, stream):
+    raw = _here(stream, (logits, temperature, uniforms, top_k, top_p, min_p) +
+                (() if out is None else (out.tokens, out.rows, out.kept, out.row_status)),
+                ("logits", "temperature", "uniforms", "top_k", "top_p", "min_p", "out.tokens",
+                 "out.rows", "out.kept", "out.row_status"))
+    dtype = logits.dtype
+    dt = dtype_code(logits)
+    request, row = _rows3(logits, "logits", dtype, None)
+    B, R, V = logits.shape
+    _flat(temperature, "temperature", torch.float32, (B,))
+    if top_k is not None:
+        _flat(top_k, "top_k", torch.int32, (B,))
+    if top_p is not None:
+        _flat(top_p, "top_p", torch.float32, (B,))
+    if min_p is not None:
+        _flat(min_p, "min_p", torch.float32, (B,))
+    S = 0
+    if uniforms is not None:
+        if uniforms.dim() != 3:
+            raise ValueError(f"uniforms must be [B, R, S], got {tuple(uniforms.shape)}")
+        S = uniforms.shape[2]
+        _flat(uniforms, "uniforms", torch.float32, (B, R, S))
+    if out is None:
+        dev = logits.device
+        with _on(stream):
+            out = SampleOut(
+                None if uniforms is None else torch.empty((B, R, S), dtype=torch.int32, device=dev),
+                torch.empty((B, R, V), dtype=dtype, device=dev) if rows else None,
+                torch.empty((B, R), dtype=torch.int32, device=dev),
+                torch.empty((B, R), dtype=torch.int32, device=dev))
+    else:
+        if uniforms is not None:
+            if out.tokens is None:
+                raise ValueError("out.tokens is missing")
+            _flat(out.tokens, "out.tokens", torch.int32, (B, R, S))
+        _flat(out.kept, "out.kept", torch.int32, (B, R))
+        _flat(out.row_status, "out.row_status", torch.int32, (B, R))
+    to_request = to_row = 0
+    if out.rows is not None:
+        to_request, to_row = _rows3(out.rows, "out.rows", dtype, logits.shape)
+    rc = load_library().specdec_sample(
+        logits.data_ptr(), dt, request, row, temperature.data_ptr(), _raw(top_k), _raw(top_p),
+        _raw(min_p), uniforms.data_ptr() if S else None, B, R, V, S, flags,
+        out.tokens.data_ptr() if S else None, _raw(out.rows), to_request, to_row,
+        out.kept.data_ptr(), out.row_status.data_ptr(), raw)
+    _check(rc, "specdec_sample")
+    return out
+
+
+def sample(logits: torch.Tensor, temperature: torch.Tensor, uniforms: torch.Tensor,
+           top_k: Optional[torch.Tensor] = None, top_p: Optional[torch.Tensor] = None,
+           min_p: Optional[torch.Tensor] = None, probs: bool = True,
+           out: Optional[SampleOut] = None, stream=None) -> SampleOut:
+    """S tokens of every row of logits [B, R, V] from uniforms [B, R, S], under every request's
+    temperature and filters [B] (``specdec_sample``): ``out.tokens`` [B, R, S] and, with
+    ``probs``, ``out.rows`` [B, R, V], the distributions that they were drawn from: drafted
+    tokens and q of the verify calls.  An ``out`` of the caller's decides by its ``rows``,
+    which may be a slice such as ``q[:, i:i + 1]``, or None."""
+    return _sample(logits, temperature, uniforms, top_k, top_p, min_p, probs, 0, out, stream)
+
+
+def filter_logits(logits: torch.Tensor, temperature: torch.Tensor,
+                  top_k: Optional[torch.Tensor] = None, top_p: Optional[torch.Tensor] = None,
+                  min_p: Optional[torch.Tensor] = None, out: Optional[SampleOut] = None,
+                  stream=None) -> SampleOut:
+    """``out.rows`` [B, R, V]: the logits of what the filters of ``sample`` keep, -infinity for
+    the rest (``specdec_sample`` with SPECDEC_SAMPLE_LOGITS).  A verify call on the target's
+    rows so filtered, at the same temperature, emits tokens of the filtered distribution.
+    ``out.rows`` may be the logits themselves."""
+    return _sample(logits, temperature, None, top_k, top_p, min_p, True, SAMPLE_LOGITS, out, stream)
+
+
+def top_logits_workspace_size(B: int, R: int, V: int, dtype: int) -> int:
+    return int(load_library().specdec_top_logits_workspace_size(B, R, V, dtype))
+
+
+def top_logits(logits: torch.Tensor, k: int, temperature: float = 1.0,
+               out: Optional[TopOut] = None, workspace: Optional[torch.Tensor] = None,
+               stream=None) -> TopOut:
+    """The k largest of every row of logits [B, R, V] (largest first, equal ones by index)
+    and its log-sum-exp at ``temperature`` (``specdec_top_logits``): the record of a target's
+    row that ``distill`` learns from."""
+    raw = _here(stream, (logits, workspace) +
+                (() if out is None else (out.values, out.ids, out.lse, out.row_status)),
+                ("logits", "workspace", "out.values", "out.ids", "out.lse", "out.row_status"))
+    dt = dtype_code(logits)
+    request, row = _rows3(logits, "logits", logits.dtype, None)
+    B, R, V = logits.shape
+    dev = logits.device
+    if out is None:
+        with _on(stream):
+            out = TopOut(torch.empty((B, R, k), dtype=torch.float32, device=dev),
+                         torch.empty((B, R, k), dtype=torch.int32, device=dev),
+                         torch.empty((B, R), dtype=torch.float32, device=dev),
+                         torch.empty((B, R), dtype=torch.int32, device=dev))
+    else:
+        _flat(out.values, "out.values", torch.float32, (B, R, k))
+        _flat(out.ids, "out.ids", torch.int32, (B, R, k))
+        _flat(out.lse, "out.lse", torch.float32, (B, R))
+        _flat(out.row_status, "out.row_status", torch.int32, (B, R))
+    if workspace is None:
+        with _on(stream):
+            workspace = torch.empty(max(top_logits_workspace_size(B, R, V, dt), 256),
+                                    dtype=torch.uint8, device=dev)
+    rc = load_library().specdec_top_logits(
+        logits.data_ptr(), dt, request, row, temperature, B, R, V, k, out.values.data_ptr(),
+        out.ids.data_ptr(), out.lse.data_ptr(), out.row_status.data_ptr(), workspace.data_ptr(),
+        workspace.numel(), raw)
+    _check(rc, "specdec_top_logits")
+    return out
+
+
+def _distill_rows(logits, ids, teacher, lse, weight):
+    """The checked sizes and strides of a distillation's inputs."""
+    dt = dtype_code(logits)
+    request, row = _rows3(logits, "logits", logits.dtype, None)
+    B, R, V = logits.shape
+    if ids.dim() != 3:
+        raise ValueError(f"ids must be [B, R, K], got {tuple(ids.shape)}")
+    K = ids.shape[2]
+    _flat(ids, "ids", torch.int32, (B, R, K))
+    _flat(teacher, "teacher", torch.float32, (B, R, K))
+    if lse is not None:
+        _flat(lse, "lse", torch.float32, (B, R))
+    if weight is not None:
+        _flat(weight, "weight", torch.float32, (B, R))
+    return dt, request, row, B, R, V, K
+
+
+def distill(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor,
+            lse: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None,
+            temperature: float = 1.0, grad: bool = True, out: Optional[DistillOut] = None,
+            stream=None) -> DistillOut:
+    """Divergence of the draft's rows of logits [B, R, V] from a teacher's records (ids int32
+    and logits float32 [B, R, K], with the rows' ``lse`` [B, R] or renormalised over their
+    entries), and ``weight`` times its gradient (``specdec_distill``).  An ``out`` of the
+    caller's decides by its ``grad``, which may be the logits themselves, or None.
+    ``distill_loss`` is the same under autograd."""
+    raw = _here(stream, (logits, ids, teacher, lse, weight) +
+                (() if out is None else (out.loss, out.grad, out.row_status)),
+                ("logits", "ids", "teacher", "lse", "weight", "out.loss", "out.grad", "out.row_status"))
+    dt, request, row, B, R, V, K = _distill_rows(logits, ids, teacher, lse, weight)
+    dev = logits.device
+    if out is None:
+        with _on(stream):
+            out = DistillOut(torch.empty((B, R), dtype=torch.float32, device=dev),
+                             torch.empty((B, R, V), dtype=logits.dtype, device=dev) if grad else None,
+                             torch.empty((B, R), dtype=torch.int32, device=dev))
+    else:
+        _flat(out.loss, "out.loss", torch.float32, (B, R))
+        _flat(out.row_status, "out.row_status", torch.int32, (B, R))
+    g_request = g_row = 0
+    if out.grad is not None:
+        g_request, g_row = _rows3(out.grad, "out.grad", logits.dtype, logits.shape)
+    rc = load_library().specdec_distill(
+        logits.data_ptr(), dt, request, row, ids.data_ptr(), teacher.data_ptr(), _raw(lse),
+        _raw(weight), temperature, B, R, V, K, out.loss.data_ptr(), _raw(out.grad), g_request,
+        g_row, out.row_status.data_ptr(), raw)
+    _check(rc, "specdec_distill")
+    return out
+
+
+def distill_loss(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor,
+                 lse: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None,
+                 temperature: float = 1.0, stream=None) -> torch.Tensor:
+    """``weight`` times the divergences of ``distill``, float32 [B, R], under autograd (for the
+    logits).  The gradient is made with the loss, from one look at the logits, and holds for
+    rows whose incoming gradient is 1, as under ``.sum()``: a mean is cheaper as weights of
+    1 / n than as a division afterwards.  A malformed row's loss and gradient are NaN."""
+    with _on(stream):
+        if torch.is_grad_enabled() and logits.requires_grad:
+            return _Distill.apply(logits, ids, teacher, lse, weight, temperature)
+        loss = distill(logits, ids, teacher, lse, weight, temperature, grad=False).loss
+        return loss if weight is None else loss * weight
+
+
+class _Distill(torch.autograd.Function):
+    """``distill`` under autograd.  The first backward turns the forward's gradient into its
+    own, in place; a second one (over a retained graph) makes it anew."""
+
+    @staticmethod
+    def forward(ctx, logits, ids, teacher, lse, weight, temperature):
+        r = distill(logits, ids, teacher, lse, weight, temperature)
+        ctx.save_for_backward(logits, ids, teacher, lse, weight)
+        ctx.temperature, ctx.grad = temperature, r.grad
+        return r.loss if weight is None else r.loss * weight
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dloss):
+        logits, ids, teacher, lse, weight = ctx.saved_tensors
+        dloss = dloss.contiguous()
+        grad, ctx.grad = ctx.grad, None
+        if grad is None:
+            w = dloss if weight is None else dloss * weight
+            grad = distill(logits, ids, teacher, lse, w, ctx.temperature).grad
+        else:
+            _distill_backward(logits, ids, teacher, lse, weight, ctx.temperature, dloss, grad)
+        return (grad,) + (None,) * 5
+
+
+def _distill_backward(logits, ids, teacher, lse, weight, temperature, dloss, grad):
+    """A forward's gradient becomes ``dloss`` times itself (``specdec_distill_backward``)."""
+    raw = _here(None, (logits, ids, teacher, lse, weight, dloss, grad),
+                ("logits", "ids", "teacher", "lse", "weight", "dloss", "grad"))
+    dt, request, row, B, R, V, K = _distill_rows(logits, ids, teacher, lse, weight)
+    g_request, g_row = _rows3(grad, "grad", logits.dtype, logits.shape)
+    _flat(dloss, "dloss", torch.float32, (B, R))
+    rc = load_library().specdec_distill_backward(
+        logits.data_ptr(), dt, request, row, ids.data_ptr(), teacher.data_ptr(), _raw(lse),
+        _raw(weight), dloss.data_ptr(), temperature, B, R, V, K, grad.data_ptr(), g_request, g_row,
+        raw)
+    _check(rc, "specdec_distill_backward")

@@ -1,0 +1,328 @@
+// Divergence of a draft's row from the K entries of a teacher's record, and its gradient
+// (specdec_distill).  With s = softmax(x / T) over the row and p_j the teacher's share of
+// entry j (token id_j):
+//     L = sum_j p_j (ln p_j - ln s_id_j) + r (ln r - ln s_rest)
+//     dL/dx_v = (s_v - p_v) / T at an entry's token, (s_v - r s_v / s_rest) / T elsewhere,
+// r = 1 - sum p_j and s_rest = the mass of s outside the entries when the teacher's
+// log-sum-exp is given; without it p = softmax over the entries and r = 0.
+//
+// A row is held in shared memory by a cluster of CTAs: it is read from HBM once, whatever
+// is computed from it, and the gradient is written once.  While the copies land, the
+// teacher's shares are made; then each CTA's maximum, and its sum of exponentials with the
+// entries taken out (their logits put to -infinity in shared memory, so that s_rest is a sum
+// and no difference of two near equal ones); one exchange of five words between the CTAs;
+// the gradient, straight from registers to global memory, then the entries' own values.  The
+// few terms of the loss are added in 64 bits, the rest is float32.
+#include "draft_common.cuh"
+
+namespace specdec {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kPerThread = SPECDEC_MAX_TOPK / kThreads;
+
+struct DistillSmem {
+  Exchange ex;
+  Arrival in;
+  double red[4][kWarps];
+  float redf[2][kWarps];
+  int status;
+  int entries;
+};
+
+// Dynamic shared memory: DistillSmem, the share, one bit for each of its elements, and a
+// position, logit and teacher's share for each entry.
+struct Layout {
+  int share, bits, pos, total;
+};
+
+__host__ __device__ inline Layout layout_of(int vectors, int elem_bytes, int K) {
+  Layout l;
+  l.share = ((int)sizeof(DistillSmem) + 127) / 128 * 128;
+  l.bits = l.share + vectors * 16;
+  l.pos = l.bits + (vectors * (16 / elem_bytes) + 31) / 32 * 4;
+  l.total = l.pos + K * 12;
+  return l;
+}
+
+template <int DT, bool kGrad>
+__global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParams p, int vectors) {
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  constexpr int es = Elem<DT>::kBytes, kN = Elem<DT>::kN;
+  DistillSmem &sm = *reinterpret_cast<DistillSmem *>(smem_raw);
+  const Layout l = layout_of(vectors, es, p.K);
+  uint8_t *buf = smem_raw + l.share;
+  uint32_t *bits = reinterpret_cast<uint32_t *>(smem_raw + l.bits);
+  int *pos = reinterpret_cast<int *>(smem_raw + l.pos);
+  float *at_x = reinterpret_cast<float *>(pos + p.K);
+  float *at_p = at_x + p.K;
+  const int tid = threadIdx.x;
+  const int rank = cluster_rank(), size = cluster_size();
+  const long long n = blockIdx.x / size;  // the row
+  const long long b = n / p.R;
+  const int r = (int)(n - b * p.R);
+  int turn = 0;
+
+  if (tid == 0) {
+    for (int i = 0; i < kChunks; ++i) mbar_init(&sm.in.full[i], 1);
+    sm.in.gave_up = 0;
+    sm.status = 0;
+    sm.entries = 0;
+    fence_mbar_init();
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  cluster_arrive();  // all CTAs run before one writes to another (waited for below)
+  __syncthreads();
+
+  const uint8_t *row = reinterpret_cast<const uint8_t *>(p.x) +
+                       (b * p.x_at.request + r * p.x_at.row) * es;
+  uint8_t *out = kGrad ? reinterpret_cast<uint8_t *>(p.grad) +
+                             (b * p.grad_at.request + r * p.grad_at.row) * es
+                       : nullptr;
+  const Share s = share_of<DT>(row, p.V, rank, size);
+  float w = p.weight ? p.weight[n] : 1.0f;
+  if (p.dloss) {
+    const float d = p.dloss[n];
+    if (d == 1.0f) {  // the gradient that stands there is the one
+      cluster_wait();
+      return;
+    }
+    if (w != 0.0f) w *= d;
+  }
+
+  // the entries: K <= 4 a thread, their ids and logits in registers
+  int id[kPerThread];
+  float z[kPerThread];
+  float zmax = -INFINITY;
+  int status = 0, some = 0;
+  if (w != 0.0f) {
+    if (tid == 0) share_copy(s, buf, sm.in);
+    share_edges<DT>(s, row, buf);
+    for (int i = tid; i < (l.pos - l.bits) / 4; i += kThreads) bits[i] = 0;
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+      const int j = tid + i * kThreads;
+      id[i] = -1;
+      z[i] = -INFINITY;
+      if (j >= p.K) continue;
+      id[i] = p.ids[n * p.K + j];
+      if (id[i] < -1 || id[i] >= p.V) {
+        status |= SPECDEC_ROW_BAD_TOKEN;
+        id[i] = -1;
+      }
+      if (id[i] < 0) continue;
+      some = 1;
+      z[i] = p.teacher[n * p.K + j];
+      if (!(z[i] < INFINITY)) status |= SPECDEC_ROW_NONFINITE;
+      zmax = fmaxf(zmax, z[i]);
+    }
+    if (!(fabsf(w) < INFINITY)) status |= SPECDEC_ROW_NONFINITE;
+  }
+  some = __syncthreads_or(some);
+  const bool wrong = __syncthreads_or(status) != 0;
+  cluster_wait();
+  // a row without weight or entries: nothing to learn, whatever its logits hold
+  const bool none = w == 0.0f || (!some && !wrong);
+
+  const double inv_t = 1.0 / (double)p.temperature;
+  const float c = temperature_scale(p.temperature);
+  float m = -INFINITY;
+  double sums[4] = {0.0, 0.0, 0.0, 0.0};  // s outside the entries, s at them, loss terms, p
+  double L = 0.0;
+  float coef = 0.0f, M = 0.0f, inv_s = 0.0f;
+  int st = 0;
+  if (w != 0.0f) {
+    // ln p_j = z_j / T - shift
+    double shift;
+    if (p.lse) {
+      const float given = p.lse[n];
+      if (!(fabsf(given) < INFINITY)) status |= SPECDEC_ROW_NONFINITE;
+      shift = given;
+    } else {
+      zmax = cta_max_nan<kWarps>(zmax, sm.redf[0]);
+      double zs = 0.0;
+#pragma unroll
+      for (int i = 0; i < kPerThread; ++i)
+        if (id[i] >= 0 && z[i] > -INFINITY) zs += expf((float)(((double)z[i] - zmax) * inv_t));
+      zs = cta_sum<kWarps>(zs, sm.red[0]);
+      if (some && !(zmax > -INFINITY)) status |= SPECDEC_ROW_NONFINITE;
+      shift = zmax * inv_t + log(zs);
+    }
+
+    // the largest logit, as the copies land
+    for (int i = 0; i < kChunks; ++i) {
+      share_wait(sm.in, i);
+      const int v1 = 1 + chunk_begin(s, i + 1);
+      for (int v = 1 + chunk_begin(s, i) + tid; v < v1; v += kThreads) {
+        float x[kN];
+        widen<DT>(*reinterpret_cast<const uint4 *>(buf + (size_t)v * 16), x);
+#pragma unroll
+        for (int e = 0; e < kN; ++e) m = fmax_nan(m, x[e]);
+      }
+    }
+    if (tid < 2) {
+      float x[kN];
+      widen<DT>(*reinterpret_cast<const uint4 *>(buf + (size_t)(tid ? s.nvec - 1 : 0) * 16), x);
+#pragma unroll
+      for (int e = 0; e < kN; ++e) m = fmax_nan(m, x[e]);
+    }
+    m = cta_max_nan<kWarps>(m, sm.redf[1]);
+    const float ref = m > -INFINITY ? m : 0.0f;
+
+    // this CTA's entries: noted, and taken out of the row
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+      if (id[i] < s.begin || id[i] >= s.end) continue;
+      const int at = id[i] - s.first;
+      if (atomicOr(&bits[at >> 5], 1u << (at & 31)) >> (at & 31) & 1u) {
+        status |= SPECDEC_ROW_BAD_TOKEN;  // the same token twice
+        continue;
+      }
+      const double lp = z[i] > -INFINITY ? z[i] * inv_t - shift : -INFINITY;
+      const float pj = expf((float)lp);
+      const float x = get_elem<DT>(buf + (size_t)at * es);
+      put_elem<DT>(buf + (size_t)at * es, -INFINITY);
+      sums[1] += ex2_approx((x - ref) * c);
+      if (pj > 0.0f) sums[2] += pj * (lp - ((double)x - ref) * inv_t);
+      sums[3] += pj;
+      const int k = atomicAdd(&sm.entries, 1);  // (their order decides nothing)
+      pos[k] = at;
+      at_x[k] = x;
+      at_p[k] = pj;
+    }
+    __syncthreads();
+    float rest = 0.0f;
+    for (int v = tid; v < s.nvec; v += kThreads) {
+      float x[kN], q = 0.0f;
+      widen<DT>(*reinterpret_cast<const uint4 *>(buf + (size_t)v * 16), x);
+#pragma unroll
+      for (int e = 0; e < kN; ++e) q += ex2_approx((x[e] - ref) * c);
+      rest += q;
+    }
+    sums[0] = rest;
+
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int d = 16; d >= 1; d >>= 1) sums[i] += shfl_xor_d(sums[i], d);
+    }
+    if ((tid & 31) == 0)
+      for (int i = 0; i < 4; ++i) sm.red[i][tid >> 5] = sums[i];
+    if (status) atomicOr(&sm.status, status);
+    __syncthreads();
+    unsigned long long rec[kWords];
+    if (tid < 32) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        double t = 0.0;
+        for (int k = 0; k < kWarps; ++k) t += sm.red[i][k];
+        rec[i] = (unsigned long long)__double_as_longlong(t);
+      }
+      const int mine = sm.status | (sm.in.gave_up ? SPECDEC_ROW_INTERNAL : 0);
+      rec[4] = (unsigned long long)(uint32_t)mine << 32 | __float_as_uint(m);
+    }
+    const unsigned long long(*got)[kWords] = exchange(sm.ex, turn, rec, 5, rank, size);
+
+    M = -INFINITY;
+    for (int k = 0; k < size; ++k) {
+      M = fmax_nan(M, __uint_as_float((uint32_t)got[k][4]));
+      st |= (int)(got[k][4] >> 32);
+    }
+    if (!(M > -INFINITY && M <= kMaxLogit)) st |= SPECDEC_ROW_NONFINITE;
+    if (none) st = 0;
+    double S = 0.0, others = 0.0, mass = 0.0;
+    for (int k = 0; k < size; ++k) {
+      const float mk = __uint_as_float((uint32_t)got[k][4]);
+      const float rk = mk > -INFINITY ? mk : 0.0f;
+      const double f = mk > -INFINITY ? (double)ex2_approx((mk - M) * c) : 0.0;
+      const double q = __longlong_as_double((long long)got[k][0]) * f;
+      const double pk = __longlong_as_double((long long)got[k][3]);
+      others += q;
+      S += q + __longlong_as_double((long long)got[k][1]) * f;
+      mass += pk;
+      // that CTA's loss terms stand against its own maximum
+      L += __longlong_as_double((long long)got[k][2]);
+      if (pk > 0.0) L += pk * ((double)M - rk) * inv_t;
+    }
+    L += mass * log(S);
+    inv_s = (float)(1.0 / S);
+    double share = 1.0;  // what is left of s outside the entries
+    if (p.lse) {
+      double left = fmax(1.0 - mass, 0.0);
+      const double of = others / S;
+      // a log-sum-exp in float32 leaves about 2^-21 of the mass unsure: nothing is asked
+      // of a row that has nothing to give
+      if (!(of > 0.0) && left < 0x1p-20) left = 0.0;
+      if (left > 0.0) {
+        L += left * (log(left) - log(of));
+        share = of > 0.0 ? 1.0 - left / of : 0.0;
+      }
+    }
+    coef = (float)fmin(fmax((double)w * inv_t * share / S, -3.0e38), 3.0e38);
+  }
+
+  if (rank == 0 && tid == 0 && p.loss) {
+    p.loss[n] = st ? __int_as_float(0x7fc00000) : none ? 0.0f : (float)L;
+    p.row_status[n] = st;
+  }
+  if (kGrad) {
+    const float fill = st ? __int_as_float(0x7fc00000) : 0.0f;
+    const bool plain = st != 0 || none;
+    const bool like =
+        ((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0;
+    for (int v = tid; v < s.nvec; v += kThreads) {
+      float x[kN];
+      if (plain) {
+#pragma unroll
+        for (int e = 0; e < kN; ++e) x[e] = fill;
+      } else {
+        widen<DT>(*reinterpret_cast<const uint4 *>(buf + (size_t)v * 16), x);
+#pragma unroll
+        for (int e = 0; e < kN; ++e) x[e] = coef * ex2_approx((x[e] - M) * c);
+      }
+      const uint4 y = narrow<DT>(x);
+      if (like)
+        store_like<DT>(s, out, v, y);
+      else
+        *reinterpret_cast<uint4 *>(buf + (size_t)v * 16) = y;
+    }
+    __syncthreads();
+    if (!plain) {
+      const float k = (float)((double)w * inv_t);
+      for (int j = tid; j < sm.entries; j += kThreads) {
+        const float y = k * (ex2_approx((at_x[j] - M) * c) * inv_s - at_p[j]);
+        put_elem<DT>(like ? out + (ptrdiff_t)(s.first + pos[j]) * es : buf + (size_t)pos[j] * es, y);
+      }
+    }
+    if (!like) {
+      __syncthreads();
+      store_unlike<DT, kThreads>(s, buf, out);
+    }
+  }
+  if (w != 0.0f && sm.in.gave_up && tid == 0) share_drain(sm.in);
+}
+
+template <int DT, bool kGrad>
+cudaError_t launch_dt(const DistillParams &p, cudaStream_t stream) {
+  static DeviceOnce once;
+  const cudaError_t err = cluster_opt_in_once(once, distill_kernel<DT, kGrad>, 227 * 1024);
+  if (err != cudaSuccess) return err;
+  constexpr int es = Elem<DT>::kBytes;
+  const long long rows = (long long)p.B * p.R;
+  const int size = cluster_for(rows, p.V, es, 66 * 1024, 3);
+  const int vectors = share_vectors(p.V, es, size);
+  return launch_clusters(distill_kernel<DT, kGrad>, rows, size, kThreads,
+                         layout_of(vectors, es, p.K).total, stream, p, vectors);
+}
+
+}  // namespace
+
+cudaError_t launch_distill(const DistillParams &p, cudaStream_t stream) {
+  if (p.dtype == SPECDEC_F32)
+    return p.grad ? launch_dt<SPECDEC_F32, true>(p, stream) : launch_dt<SPECDEC_F32, false>(p, stream);
+  return p.grad ? launch_dt<SPECDEC_BF16, true>(p, stream) : launch_dt<SPECDEC_BF16, false>(p, stream);
+}
+
+}  // namespace specdec

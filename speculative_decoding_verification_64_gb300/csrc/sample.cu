@@ -1,0 +1,676 @@
+// Tokens drawn from rows of logits under temperature, top-k, top-p and min-p, and the
+// rows' distributions or what the filters leave of their logits (specdec_sample).
+//
+// With w_v = exp((l_v - max) / T), tokens in the order of their place (larger first, equal
+// ones by index): top-k keeps the first k, top-p the shortest run of those whose mass is
+// at least p of theirs, min-p those with w >= min_p.  What is kept is a run of places again,
+// so that one cut (value, index) says it all.  A draw is the first kept token, by index,
+// whose cumulative mass exceeds u times the kept mass.
+//
+// A row is held in shared memory by a cluster of CTAs and read from HBM once.
+//   * With top-k: each thread's maximum is one group's; the k-th largest of those (its top 16
+//     bits) bounds the k-th logit from below, the few tokens that reach it are gathered by
+//     rank 0, sorted, weighed, cut and drawn from.
+//   * With top-p alone: a search over places.  A pass adds the weights of all places above a
+//     bracket, and in it; when the cut is inside and the bracket's tokens fit a list, they
+//     are sorted and the cut is found among them.
+//   * The draws of such rows: the passes leave the kept mass of every run of 32 vectors; a
+//     draw looks its run up, and a warp weighs that run once more.
+// Which token is cut last, or drawn, turns on sums over the vocabulary: weights and sums are
+// those of draft_weight.cuh, as good as 64-bit floating point for this.  The cluster's
+// CTAs exchange a record of a few words at each step.
+#include "draft_weight.cuh"
+
+namespace specdec {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kList = 2048;   // tokens that rank 0 can sort
+constexpr int kMine = 1024;   // tokens that a CTA can bring
+constexpr int kKeys = 4096;   // groups' maxima (256 of each of 16 CTAs)
+constexpr int kAll = 0x7FFFFFFF;
+constexpr float kLeast = -3.402823466e38f;
+
+using u64 = unsigned long long;
+
+__device__ const WeightTable g_table = make_table();
+
+struct SampleSmem {
+  Exchange ex;
+  Arrival in;
+  float2 table[kTable];
+  union {
+    u64 list[kList];
+    uint32_t key[kKeys];
+  };
+  u64 mine[kMine];
+  u64 red[2][kWarps];
+  float redf[kWarps];
+  unsigned total[16];
+  int n_mine, n_kept;
+  u64 cut[2];
+};
+
+struct Layout {
+  int share, steps, total;
+};
+
+__host__ __device__ inline Layout layout_of(int vectors) {
+  Layout l;
+  l.share = ((int)sizeof(SampleSmem) + 127) / 128 * 128;
+  l.steps = l.share + vectors * 16;
+  l.total = l.steps + (vectors + 31) / 32 * 8;
+  return l;
+}
+
+// A run of places down to one: x above the value, or equal to it with an index up to the
+// bound.
+struct Cut {
+  float value;
+  int index;
+  __device__ __forceinline__ bool holds(float x, int at) const {
+    return x > value || (x == value && at <= index);
+  }
+};
+
+// Places >= q; q's lower half is 2^32 - 1 - index.
+__device__ __forceinline__ Cut cut_at(u64 q) {
+  const uint32_t low = (uint32_t)q;
+  Cut c;
+  c.value = place_value(q);
+  c.index = (int)min(0xFFFFFFFFu - low, (uint32_t)kAll);
+  if (q >> 32 == 0x7FFFFFFFu) {  // the key that -0 would have: no token's, but equal to 0
+    c.value = 0.0f;
+    c.index = kAll;
+  }
+  return c;
+}
+
+__device__ __forceinline__ u64 warp_sum_u64(u64 v) {
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) v += shfl_xor_u64(v, d);
+  return v;
+}
+
+// Inclusive sums over the lanes of a warp.
+__device__ __forceinline__ u64 warp_incscan(u64 v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const u64 y = shfl_up_u64(v, d);
+    if (lane >= d) v += y;
+  }
+  return v;
+}
+
+__device__ __forceinline__ u64 shfl_u64(u64 v, int from) {
+  return (u64)__shfl_sync(kFull, (uint32_t)v, from) |
+         (u64)__shfl_sync(kFull, (uint32_t)(v >> 32), from) << 32;
+}
+
+// Exclusive sums over the CTA's threads in thread order, and the total.
+__device__ __forceinline__ u64 cta_exscan(u64 v, u64 *red, u64 &total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const u64 inc = warp_incscan(v);
+  __syncthreads();
+  if (lane == 31) red[warp] = inc;
+  __syncthreads();
+  u64 pre = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) pre += red[w];
+    total += red[w];
+  }
+  return pre + inc - v;
+}
+
+template <int DT>
+__device__ __forceinline__ void load_share(const Share &s, const uint8_t *buf, int v, float *x) {
+  if (v < s.nvec) {
+    widen<DT>(*reinterpret_cast<const uint4 *>(buf + (size_t)v * 16), x);
+  } else {
+#pragma unroll
+    for (int e = 0; e < Elem<DT>::kN; ++e) x[e] = -INFINITY;
+  }
+}
+
+// What a pass over the CTA's share found: mass above the cut, in the bracket below it, of
+// everything; tokens above.  (Those in the bracket are counted by sm.n_mine.)
+struct Found {
+  u64 above, in, all;
+  int n_above;
+};
+
+// One pass: steps[i] gets the mass above `hi` of the share's vectors 32 i .. 32 i + 31; with
+// kBracket also tokens from `lo` up to `hi`, which go on the list.  Sums of each warp.
+template <int DT, bool kBracket>
+__device__ __forceinline__ Found weigh(const Share &s, const uint8_t *buf, const WeightOf &w,
+                                       const Cut &hi, const Cut &lo, u64 *steps, SampleSmem &sm) {
+  constexpr int kN = Elem<DT>::kN;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Found f = {0, 0, 0, 0};
+  u64 in = 0, all = 0;
+  int n_above = 0;
+  for (int i = warp; 32 * i < s.nvec; i += kWarps) {
+    const int v = 32 * i + lane;
+    float x[kN];
+    load_share<DT>(s, buf, v, x);
+    const int at = s.first + v * kN;
+    float2 sum_a = both(0.0f), sum_i = both(0.0f), sum_z = both(0.0f);  // (a, b) each
+#pragma unroll
+    for (int e = 0; e < kN; e += 2) {
+      float2 a, b;
+      weight2(make_float2(x[e], x[e + 1]), w, sm.table, a, b);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float y = x[e + h];
+        const bool some = y >= w.least;
+        const float2 ab =
+            make_float2(some ? (h ? a.y : a.x) : 0.0f, some ? (h ? b.y : b.x) : 0.0f);
+        const bool above = hi.holds(y, at + e + h);
+        if (above) {
+          sum_a = __fadd2_rn(sum_a, ab);
+          ++n_above;
+        }
+        if (kBracket) {
+          sum_z = __fadd2_rn(sum_z, ab);
+          if (!above && lo.holds(y, at + e + h)) {
+            sum_i = __fadd2_rn(sum_i, ab);
+            const int k = atomicAdd(&sm.n_mine, 1);  // (sorted later)
+            if (k < kMine) sm.mine[k] = place_of(y, at + e + h);
+          }
+        }
+      }
+    }
+    const u64 t = warp_sum_u64(fixed_of(sum_a.x, sum_a.y));
+    if (lane == 0) steps[i] = t;
+    f.above += t;
+    if (kBracket) {
+      in += fixed_of(sum_i.x, sum_i.y);
+      all += fixed_of(sum_z.x, sum_z.y);
+    }
+  }
+  f.n_above = __reduce_add_sync(kFull, n_above);
+  if (kBracket) {
+    f.in = warp_sum_u64(in);
+    f.all = warp_sum_u64(all);
+  }
+  return f;
+}
+
+// The tokens from `lo` up, on the list.
+template <int DT>
+__device__ __forceinline__ void gather(const Share &s, const uint8_t *buf, const Cut &lo,
+                                       SampleSmem &sm) {
+  constexpr int kN = Elem<DT>::kN;
+  for (int v = threadIdx.x; v < s.nvec; v += kThreads) {
+    float x[kN];
+    load_share<DT>(s, buf, v, x);
+    const int at = s.first + v * kN;
+#pragma unroll
+    for (int e = 0; e < kN; ++e) {
+      if (!lo.holds(x[e], at + e)) continue;
+      const int k = atomicAdd(&sm.n_mine, 1);
+      if (k < kMine) sm.mine[k] = place_of(x[e], at + e);
+    }
+  }
+}
+
+// All CTAs' lists, by rank 0; the CTAs' numbers are the lower halves of record word `at`.
+__device__ __forceinline__ int collect(const u64 (*got)[kWords], int word, int size, SampleSmem &sm) {
+  int all = 0;
+  for (int q = 0; q < size; ++q) {
+    const int m = (int)(uint32_t)got[q][word];
+    const uint32_t at = cluster_addr(smem_addr(sm.mine), q);
+    for (int i = threadIdx.x; i < m; i += kThreads) sm.list[all + i] = remote_get(at + 8u * i);
+    all += m;
+  }
+  __syncthreads();
+  sort_down<kThreads>(sm.list, all);
+  return all;
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleParams p, int vectors) {
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  constexpr int es = Elem<DT>::kBytes, kN = Elem<DT>::kN;
+  SampleSmem &sm = *reinterpret_cast<SampleSmem *>(smem_raw);
+  const Layout l = layout_of(vectors);
+  uint8_t *buf = smem_raw + l.share;
+  u64 *steps = reinterpret_cast<u64 *>(smem_raw + l.steps);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = cluster_rank(), size = cluster_size();
+  const long long n = blockIdx.x / size;  // the row
+  const long long b = n / p.R;
+  const int r = (int)(n - b * p.R);
+  int turn = 0;
+
+  if (tid == 0) {
+    for (int i = 0; i < kChunks; ++i) mbar_init(&sm.in.full[i], 1);
+    sm.in.gave_up = 0;
+    sm.n_mine = 0;
+    fence_mbar_init();
+  }
+  if (tid < 16) sm.total[tid] = 0;
+  pdl_wait();
+  pdl_launch_dependents();
+  cluster_arrive();
+  __syncthreads();
+
+  const uint8_t *row = reinterpret_cast<const uint8_t *>(p.x) +
+                       (b * p.x_at.request + r * p.x_at.row) * es;
+  const Share s = share_of<DT>(row, p.V, rank, size);
+  if (tid == 0) share_copy(s, buf, sm.in);
+  share_edges<DT>(s, row, buf);
+  for (int i = tid; i < kTable; i += kThreads)
+    sm.table[i] = make_float2(g_table.at[i].hi, g_table.at[i].lo);
+
+  // the request's filters
+  float T = p.temperature[b];
+  int k = p.top_k ? p.top_k[b] : 0;
+  float top_p = p.top_p ? p.top_p[b] : 1.0f;
+  float min_p = p.min_p ? p.min_p[b] : 0.0f;
+  int st = 0;
+  if (!temperature_valid(T)) st |= SPECDEC_ROW_BAD_TEMP;
+  if (k < 0 || k > SPECDEC_MAX_TOPK || !(top_p >= 0.0f && top_p <= 1.0f) ||
+      !(min_p >= 0.0f && min_p <= 1.0f))
+    st |= SPECDEC_ROW_BAD_FILTER;
+  if (T == 0.0f || st) {  // greedy: the first of the largest
+    T = 1.0f;
+    k = 1;
+    top_p = 1.0f;
+    min_p = 0.0f;
+  }
+
+  // the largest logit, and the largest of each thread's part of every copy
+  float gm[kChunks];
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i) {
+    gm[i] = -INFINITY;
+    share_wait(sm.in, i);
+    const int v1 = 1 + chunk_begin(s, i + 1);
+    for (int v = 1 + chunk_begin(s, i) + tid; v < v1; v += kThreads) {
+      float x[kN];
+      widen<DT>(*reinterpret_cast<const uint4 *>(buf + (size_t)v * 16), x);
+#pragma unroll
+      for (int e = 0; e < kN; ++e) gm[i] = fmax_nan(gm[i], x[e]);
+    }
+  }
+  __syncthreads();
+  if (tid < 2) {
+    float x[kN];
+    widen<DT>(*reinterpret_cast<const uint4 *>(buf + (size_t)(tid ? s.nvec - 1 : 0) * 16), x);
+#pragma unroll
+    for (int e = 0; e < kN; ++e) gm[0] = fmax_nan(gm[0], x[e]);
+  }
+  float M = fmax_nan(fmax_nan(gm[0], gm[1]), fmax_nan(gm[2], gm[3]));
+  const int sub = size <= 2 ? 4 : size == 4 ? 2 : 1;  // groups a thread
+  const int groups = kThreads * sub * size;
+  cluster_wait();
+  if (k > 0) {
+    if (sub == 2) {
+      gm[0] = fmax_nan(gm[0], gm[2]);
+      gm[1] = fmax_nan(gm[1], gm[3]);
+    } else if (sub == 1) {
+      gm[0] = M;
+    }
+    for (int q = 0; q < size; ++q) {
+      const uint32_t to = cluster_addr(smem_addr(&sm.key[(rank * kThreads + tid) * sub]), q);
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i)
+        if (i < sub) remote_put(to + 4u * i, order_key(gm[i]) >> 16);
+    }
+  }
+  M = cta_max_nan<kWarps>(M, sm.redf);
+  u64 rec[kWords];
+  rec[0] = (u64)(sm.in.gave_up ? SPECDEC_ROW_INTERNAL : 0) << 32 | __float_as_uint(M);
+  const u64(*got)[kWords] = exchange(sm.ex, turn, rec, 1, rank, size);
+  M = -INFINITY;
+  for (int q = 0; q < size; ++q) {
+    M = fmax_nan(M, __uint_as_float((uint32_t)got[q][0]));
+    st |= (int)(got[q][0] >> 32);
+  }
+  if (!(st & SPECDEC_ROW_INTERNAL) && !(M > -INFINITY && M <= kMaxLogit)) st |= SPECDEC_ROW_NONFINITE;
+
+  // (from here every CTA of the cluster takes the same branches: they turn on the
+  // request's filters and on exchanged records)
+  const WeightOf w = weight_of(M, T);
+  Cut cut = {kLeast, kAll};  // everything but -infinity
+  u64 Z = 0;                 // the kept mass
+  int kept = 0;
+  const float floor_value =
+      min_p > 0.0f ? __double2float_ru((double)M + (double)T * log((double)min_p)) : kLeast;
+  const u64 over = ((u64)order_key(M) + 1) << 32;  // above every place
+  const float *u = p.uniforms + n * p.S;
+  int32_t *tokens = p.tokens + n * p.S;
+
+  if (!st && k > 0) {
+    // ---- top-k: the few largest, by rank 0 --------------------------------------------
+    uint32_t bound = 0;
+    for (int bit = 15; bit >= 0; --bit) {
+      const uint32_t t = bound | 1u << bit;
+      unsigned m = 0;
+      for (int i = tid; i < groups; i += kThreads) m += sm.key[i] >= t;
+      m = __reduce_add_sync(kFull, m);
+      if (lane == 0 && m) atomicAdd(&sm.total[bit], m);
+      __syncthreads();
+      if (sm.total[bit] >= (unsigned)k) bound = t;
+    }
+    // At least k tokens (or all that are finite) stand at places >= from, fewer than k at
+    // places >= H.  Where those at `from` are too many to list, halves of what is between:
+    // at the end exactly k.
+    u64 from = (u64)max(bound << 16, kLeastKey) << 32, H = over, probe = from;
+    for (;;) {
+      gather<DT>(s, buf, cut_at(probe), sm);
+      __syncthreads();
+      rec[0] = (u64)(uint32_t)sm.n_mine;
+      got = exchange(sm.ex, turn, rec, 1, rank, size);
+      int all = 0;
+      bool fits = true;
+      for (int q = 0; q < size; ++q) {
+        all += (int)got[q][0];
+        fits = fits && got[q][0] <= kMine;
+      }
+      const bool enough = probe == from || all >= k;
+      if (enough && fits && all <= kList) break;
+      if (enough) from = probe;
+      else H = probe;
+      probe = from + (H - from) / 2;
+      __syncthreads();
+      if (tid == 0) sm.n_mine = 0;
+      __syncthreads();
+    }
+    if (rank == 0) {
+      const int m = min(k, collect(got, 0, size, sm));
+      // weights of the first k, four a thread, and their sums
+      constexpr int kEach = SPECDEC_MAX_TOPK / kThreads;
+      u64 wt[kEach], mine = 0, whole;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int j = tid * kEach + i;
+        wt[i] = j < m ? weight_fixed(place_value(sm.list[j]), w, sm.table) : 0;
+        mine += wt[i];
+      }
+      u64 before = cta_exscan(mine, sm.red[0], whole);
+      const u64 want = top_p < 1.0f ? share_at_least(top_p, whole) : ~0ull;
+      // kept: places before which less than the wanted mass stands
+      int c = 0;
+      u64 sum = before;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int j = tid * kEach + i;
+        c += j < m && (sum < want || j == 0) && place_value(sm.list[j]) >= floor_value;
+        sum += wt[i];
+      }
+      if (tid == 0) sm.n_kept = 0;
+      __syncthreads();
+      c = __reduce_add_sync(kFull, c);
+      if (lane == 0) atomicAdd(&sm.n_kept, c);
+      __syncthreads();
+      const int nk = sm.n_kept;
+      // (sm.mine's own tokens are on the list by now: it holds weights)
+      sum = before;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int j = tid * kEach + i;
+        sum += wt[i];
+        if (j == nk - 1) {
+          sm.cut[0] = sm.list[j];
+          sm.cut[1] = sum;
+        }
+        if (j < nk) sm.mine[j] = wt[i];
+      }
+      __syncthreads();
+      Z = sm.cut[1];
+      rec[0] = sm.cut[0];
+      rec[1] = Z;
+      rec[2] = (u64)nk;
+      if (p.S > 0) {
+        // the kept by index, and the draws
+        for (int i = tid; i < nk; i += kThreads)
+          sm.list[i] = (u64)(uint32_t)sm.list[i] << 32 | (uint32_t)i;
+        __syncthreads();
+        sort_down<kThreads>(sm.list, nk);
+        int token[kEach];
+        mine = 0;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+          const int j = tid * kEach + i;
+          const u64 q = j < nk ? sm.list[j] : 0;
+          token[i] = (int)(0xFFFFFFFFu - (uint32_t)(q >> 32));
+          wt[i] = j < nk ? sm.mine[(uint32_t)q] : 0;
+          mine += wt[i];
+        }
+        before = cta_exscan(mine, sm.red[1], whole);
+        for (int d = 0; d < p.S; ++d) {
+          const u64 target = uniform_target(u[d], Z);
+          sum = before;
+#pragma unroll
+          for (int i = 0; i < kEach; ++i) {
+            if (sum <= target && target < sum + wt[i]) tokens[d] = token[i];
+            sum += wt[i];
+          }
+        }
+      }
+    }
+    got = exchange(sm.ex, turn, rec, 3, rank, size);
+    cut = cut_at(got[0][0]);
+    Z = got[0][1];
+    kept = (int)got[0][2];
+  } else if (!st) {
+    // ---- the whole vocabulary ----------------------------------------------------------
+    bool weighed = false;  // steps[] holds the kept mass
+    u64 mass = 0;          // of this CTA
+    int count = 0;
+    if (top_p < 1.0f) {
+      // less than the wanted mass stands above H, all of it above L: sums are exact, so that
+      // this holds throughout, and halves end
+      u64 L = (u64)max(order_key(w.least), kLeastKey) << 32, H = over, lo = L;
+      Found f;  // of the whole row
+      u64 want;
+      for (;;) {
+        const Found m = weigh<DT, true>(s, buf, w, cut_at(H), cut_at(lo), steps, sm);
+        __syncthreads();
+        if (tid < 3) sm.red[0][tid] = 0;
+        if (tid == 3) sm.total[0] = 0;
+        __syncthreads();
+        if (lane == 0) {
+          atomicAdd(&sm.red[0][0], m.above);
+          atomicAdd(&sm.red[0][1], m.in);
+          atomicAdd(&sm.red[0][2], m.all);
+          atomicAdd(&sm.total[0], (unsigned)m.n_above);
+        }
+        __syncthreads();
+        rec[0] = mass = sm.red[0][0];
+        rec[1] = sm.red[0][1];
+        rec[2] = sm.red[0][2];
+        rec[3] = (u64)sm.total[0] << 32 | (uint32_t)sm.n_mine;
+        got = exchange(sm.ex, turn, rec, 4, rank, size);
+        f = {0, 0, 0, 0};
+        int n_in = 0;
+        bool fits = true;
+        for (int q = 0; q < size; ++q) {
+          f.above += got[q][0];
+          f.in += got[q][1];
+          f.all += got[q][2];
+          f.n_above += (int)(got[q][3] >> 32);
+          const int here = (int)(uint32_t)got[q][3];
+          n_in += here;
+          fits = fits && here <= kMine;
+        }
+        want = max(share_at_least(top_p, f.all), 1ull);
+        const bool inside = want <= f.above + f.in;
+        if (inside && fits && n_in <= kList) break;
+        if (inside)
+          L = lo;
+        else
+          H = lo;
+        lo = L + (H - L) / 2;  // (L itself where one place is left)
+        __syncthreads();
+        if (tid == 0) sm.n_mine = 0;
+        __syncthreads();
+      }
+      if (rank == 0) {
+        const int all = collect(got, 3, size, sm);
+        constexpr int kEach = kList / kThreads;
+        u64 wt[kEach], mine = 0, whole;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+          const int j = tid * kEach + i;
+          wt[i] = j < all ? weight_fixed(place_value(sm.list[j]), w, sm.table) : 0;
+          mine += wt[i];
+        }
+        u64 sum = f.above + cta_exscan(mine, sm.red[1], whole);
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+          const int j = tid * kEach + i;
+          if (sum < want && sum + wt[i] >= want) {
+            sm.cut[0] = sm.list[j];
+            sm.cut[1] = (u64)(f.n_above + j + 1);
+          }
+          sum += wt[i];
+        }
+        __syncthreads();
+        rec[0] = sm.cut[0];
+        rec[1] = sm.cut[1];
+      }
+      got = exchange(sm.ex, turn, rec, 2, rank, size);
+      cut = cut_at(got[0][0]);
+      kept = (int)got[0][1];
+      weighed = !(floor_value > cut.value);
+      if (weighed) {
+        // the list's kept tokens join their runs
+        u64 add = 0, more;
+        for (int i = tid; i < sm.n_mine; i += kThreads) {
+          const u64 q = sm.mine[i];
+          if (!cut.holds(place_value(q), place_index(q))) continue;
+          const u64 t = weight_fixed(place_value(q), w, sm.table);
+          atomicAdd(&steps[((place_index(q) - s.first) / kN) >> 5], t);
+          add += t;
+        }
+        (void)cta_exscan(add, sm.red[0], more);
+        mass += more;
+      }
+    }
+    if (!weighed) {
+      if (floor_value > cut.value) cut = {floor_value, kAll};
+      const Found m = weigh<DT, false>(s, buf, w, cut, cut, steps, sm);
+      u64 total;
+      (void)cta_exscan(lane == 0 ? m.above : 0, sm.red[0], total);
+      mass = total;
+      (void)cta_exscan(lane == 0 ? (u64)m.n_above : 0, sm.red[1], total);
+      count = (int)total;
+    }
+    rec[0] = mass;
+    rec[1] = (u64)(uint32_t)count;
+    got = exchange(sm.ex, turn, rec, 2, rank, size);
+    u64 before = 0;
+    int c = 0;
+    for (int q = 0; q < size; ++q) {
+      if (q < rank) before += got[q][0];
+      Z += got[q][0];
+      c += (int)got[q][1];
+    }
+    if (!weighed) kept = c;
+
+    // the draws that fall into this CTA's mass
+    for (int d = warp; d < p.S; d += kWarps) {
+      const u64 target = uniform_target(u[d], Z);
+      if (target < before || target - before >= mass) continue;
+      u64 left = target - before;
+      // the run of 32 vectors: 32 runs at a time
+      int at = -1;
+      const int n_steps = (s.nvec + 31) / 32;
+      for (int i0 = 0; i0 < n_steps && at < 0; i0 += 32) {
+        const u64 t = i0 + lane < n_steps ? steps[i0 + lane] : 0;
+        const u64 inc = warp_incscan(t);
+        const unsigned hit = __ballot_sync(kFull, inc > left);
+        if (hit) at = i0 + __ffs(hit) - 1;
+        left -= hit ? shfl_u64(inc - t, __ffs(hit) - 1) : shfl_u64(inc, 31);
+      }
+      // the token: the run's weights once more
+      const int v = 32 * at + lane;
+      float x[kN];
+      load_share<DT>(s, buf, v, x);
+      const int first = s.first + v * kN;
+      u64 t = 0;
+#pragma unroll
+      for (int e = 0; e < kN; ++e)
+        if (cut.holds(x[e], first + e)) t += weight_fixed(x[e], w, sm.table);
+      u64 sum = warp_incscan(t) - t;
+      if (sum <= left && left < sum + t) {
+        int e = 0;
+        for (; e < kN - 1; ++e) {
+          if (cut.holds(x[e], first + e)) sum += weight_fixed(x[e], w, sm.table);
+          if (left < sum) break;
+        }
+        tokens[d] = first + e;
+      }
+    }
+  }
+
+  if (st) {
+    if (rank == 0)
+      for (int d = tid; d < p.S; d += kThreads) tokens[d] = -1;
+    kept = 0;
+  }
+  if (rank == 0 && tid == 0) {
+    p.kept[n] = kept;
+    p.row_status[n] = st;
+  }
+  if (p.rows) {
+    uint8_t *out = reinterpret_cast<uint8_t *>(p.rows) +
+                   (b * p.rows_at.request + r * p.rows_at.row) * es;
+    const bool like =
+        ((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0;
+    const float c = temperature_scale(T);
+    const float g = (float)(w.ref * (double)kFixed / (double)Z);
+    __syncthreads();  // (draws read the share)
+    for (int v = tid; v < s.nvec; v += kThreads) {
+      float x[kN];
+      load_share<DT>(s, buf, v, x);
+      const int at = s.first + v * kN;
+#pragma unroll
+      for (int e = 0; e < kN; ++e) {
+        const bool in = cut.holds(x[e], at + e);
+        if (p.logits)
+          x[e] = st ? __int_as_float(0x7fc00000) : in ? x[e] : -INFINITY;
+        else
+          x[e] = st ? __int_as_float(0x7fc00000) : in ? g * ex2_approx((x[e] - M) * c) : 0.0f;
+      }
+      const uint4 y = narrow<DT>(x);
+      if (like)
+        store_like<DT>(s, out, v, y);
+      else
+        *reinterpret_cast<uint4 *>(buf + (size_t)v * 16) = y;
+    }
+    if (!like) {
+      __syncthreads();
+      store_unlike<DT, kThreads>(s, buf, out);
+    }
+  }
+  if (sm.in.gave_up && tid == 0) share_drain(sm.in);
+}
+
+template <int DT>
+cudaError_t launch_dt(const SampleParams &p, cudaStream_t stream) {
+  static DeviceOnce once;
+  const cudaError_t err = cluster_opt_in_once(once, sample_kernel<DT>, 227 * 1024);
+  if (err != cudaSuccess) return err;
+  constexpr int es = Elem<DT>::kBytes;
+  const long long rows = (long long)p.B * p.R;
+  const int size = cluster_for(rows, p.V, es, 36 * 1024, 3);
+  const int vectors = share_vectors(p.V, es, size);
+  return launch_clusters(sample_kernel<DT>, rows, size, kThreads, layout_of(vectors).total, stream, p,
+                         vectors);
+}
+
+}  // namespace
+
+cudaError_t launch_sample(const SampleParams &p, cudaStream_t stream) {
+  return p.dtype == SPECDEC_F32 ? launch_dt<SPECDEC_F32>(p, stream) : launch_dt<SPECDEC_BF16>(p, stream);
+}
+
+}  // namespace specdec
