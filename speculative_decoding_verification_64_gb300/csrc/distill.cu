@@ -25,8 +25,9 @@ constexpr int kPerThread = SPECDEC_MAX_TOPK / kThreads;
 struct DistillSmem {
   Exchange ex;
   Arrival in;
-  double red[4][kWarps];
-  float redf[2][kWarps];
+  double terms[2][kWarps];
+  float red[4][kWarps];
+  double shift;
   int status;
   int entries;
 };
@@ -126,29 +127,34 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
   // a row without weight or entries: nothing to learn, whatever its logits hold
   const bool none = w == 0.0f || (!some && !wrong);
 
-  const double inv_t = 1.0 / (double)p.temperature;
+  // (64-bit operations are few and of single warps: this GPU has two of their lanes an SM)
+  const double inv_t = p.inv_t;
   const float c = temperature_scale(p.temperature);
   float m = -INFINITY;
-  double sums[4] = {0.0, 0.0, 0.0, 0.0};  // s outside the entries, s at them, loss terms, p
-  double L = 0.0;
-  float coef = 0.0f, M = 0.0f, inv_s = 0.0f;
+  const unsigned long long(*got)[kWords] = nullptr;
+  float coef = 0.0f, M = 0.0f, inv_s = 0.0f, S = 0.0f, left = 0.0f, of = 0.0f;
   int st = 0;
   if (w != 0.0f) {
     // ln p_j = z_j / T - shift
-    double shift;
+    double shift = 0.0;
     if (p.lse) {
       const float given = p.lse[n];
       if (!(fabsf(given) < INFINITY)) status |= SPECDEC_ROW_NONFINITE;
       shift = given;
     } else {
-      zmax = cta_max_nan<kWarps>(zmax, sm.redf[0]);
-      double zs = 0.0;
+      zmax = cta_max_nan<kWarps>(zmax, sm.red[0]);
+      float zs = 0.0f;
 #pragma unroll
       for (int i = 0; i < kPerThread; ++i)
-        if (id[i] >= 0 && z[i] > -INFINITY) zs += expf((float)(((double)z[i] - zmax) * inv_t));
-      zs = cta_sum<kWarps>(zs, sm.red[0]);
+        if (z[i] > -INFINITY) zs += expf((float)(((double)z[i] - zmax) * inv_t));
+      zs = cta_sum<kWarps>(zs, sm.red[1]);
       if (some && !(zmax > -INFINITY)) status |= SPECDEC_ROW_NONFINITE;
-      shift = zmax * inv_t + log(zs);
+      if (tid < 32) {
+        shift = zmax * inv_t + log((double)zs);
+        if (tid == 0) sm.shift = shift;
+      }
+      __syncthreads();
+      shift = sm.shift;
     }
 
     // the largest logit, as the copies land
@@ -168,13 +174,17 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
 #pragma unroll
       for (int e = 0; e < kN; ++e) m = fmax_nan(m, x[e]);
     }
-    m = cta_max_nan<kWarps>(m, sm.redf[1]);
+    m = cta_max_nan<kWarps>(m, sm.red[2]);
     const float ref = m > -INFINITY ? m : 0.0f;
 
     // this CTA's entries: noted, and taken out of the row
+    float at_s = 0.0f;
+    double terms = 0.0, at_mass = 0.0;  // loss terms, and p
+    int mine = 0;
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
       if (id[i] < s.begin || id[i] >= s.end) continue;
+      mine = 1;
       const int at = id[i] - s.first;
       if (atomicOr(&bits[at >> 5], 1u << (at & 31)) >> (at & 31) & 1u) {
         status |= SPECDEC_ROW_BAD_TOKEN;  // the same token twice
@@ -184,14 +194,26 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
       const float pj = expf((float)lp);
       const float x = get_elem<DT>(buf + (size_t)at * es);
       put_elem<DT>(buf + (size_t)at * es, -INFINITY);
-      sums[1] += ex2_approx((x - ref) * c);
-      if (pj > 0.0f) sums[2] += pj * (lp - ((double)x - ref) * inv_t);
-      sums[3] += pj;
+      at_s += ex2_approx((x - ref) * c);
+      if (pj > 0.0f) terms += pj * (lp - ((double)x - ref) * inv_t);
+      at_mass += pj;
       const int k = atomicAdd(&sm.entries, 1);  // (their order decides nothing)
       pos[k] = at;
       at_x[k] = x;
       at_p[k] = pj;
     }
+    if (__any_sync(kFull, mine)) {
+#pragma unroll
+      for (int d = 16; d >= 1; d >>= 1) {
+        terms += __shfl_xor_sync(kFull, terms, d);
+        at_mass += __shfl_xor_sync(kFull, at_mass, d);
+      }
+    }
+    if ((tid & 31) == 0) {
+      sm.terms[0][tid >> 5] = terms;
+      sm.terms[1][tid >> 5] = at_mass;
+    }
+    if (status) atomicOr(&sm.status, status);
     __syncthreads();
     float rest = 0.0f;
     for (int v = tid; v < s.nvec; v += kThreads) {
@@ -201,71 +223,81 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
       for (int e = 0; e < kN; ++e) q += ex2_approx((x[e] - ref) * c);
       rest += q;
     }
-    sums[0] = rest;
-
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-#pragma unroll
-      for (int d = 16; d >= 1; d >>= 1) sums[i] += shfl_xor_d(sums[i], d);
+    for (int d = 16; d >= 1; d >>= 1) {
+      rest += __shfl_xor_sync(kFull, rest, d);
+      at_s += __shfl_xor_sync(kFull, at_s, d);
     }
-    if ((tid & 31) == 0)
-      for (int i = 0; i < 4; ++i) sm.red[i][tid >> 5] = sums[i];
-    if (status) atomicOr(&sm.status, status);
+    if ((tid & 31) == 0) {
+      sm.red[0][tid >> 5] = rest;
+      sm.red[3][tid >> 5] = at_s;
+    }
     __syncthreads();
     unsigned long long rec[kWords];
     if (tid < 32) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        double t = 0.0;
-        for (int k = 0; k < kWarps; ++k) t += sm.red[i][k];
-        rec[i] = (unsigned long long)__double_as_longlong(t);
+      rest = at_s = 0.0f;
+      terms = at_mass = 0.0;
+      for (int k = 0; k < kWarps; ++k) {
+        rest += sm.red[0][k];
+        at_s += sm.red[3][k];
+        terms += sm.terms[0][k];
+        at_mass += sm.terms[1][k];
       }
-      const int mine = sm.status | (sm.in.gave_up ? SPECDEC_ROW_INTERNAL : 0);
-      rec[4] = (unsigned long long)(uint32_t)mine << 32 | __float_as_uint(m);
+      const int wrong_here = sm.status | (sm.in.gave_up ? SPECDEC_ROW_INTERNAL : 0);
+      rec[0] = (unsigned long long)__float_as_uint(at_s) << 32 | __float_as_uint(rest);
+      rec[1] = (unsigned long long)(uint32_t)wrong_here << 32 | __float_as_uint(m);
+      rec[2] = (unsigned long long)__double_as_longlong(terms);
+      rec[3] = (unsigned long long)__double_as_longlong(at_mass);
     }
-    const unsigned long long(*got)[kWords] = exchange(sm.ex, turn, rec, 5, rank, size);
+    got = exchange(sm.ex, turn, rec, 4, rank, size);
 
     M = -INFINITY;
     for (int k = 0; k < size; ++k) {
-      M = fmax_nan(M, __uint_as_float((uint32_t)got[k][4]));
-      st |= (int)(got[k][4] >> 32);
+      M = fmax_nan(M, __uint_as_float((uint32_t)got[k][1]));
+      st |= (int)(got[k][1] >> 32);
     }
     if (!(M > -INFINITY && M <= kMaxLogit)) st |= SPECDEC_ROW_NONFINITE;
     if (none) st = 0;
-    double S = 0.0, others = 0.0, mass = 0.0;
+    float others = 0.0f;
+    double mass = 0.0;
     for (int k = 0; k < size; ++k) {
-      const float mk = __uint_as_float((uint32_t)got[k][4]);
-      const float rk = mk > -INFINITY ? mk : 0.0f;
-      const double f = mk > -INFINITY ? (double)ex2_approx((mk - M) * c) : 0.0;
-      const double q = __longlong_as_double((long long)got[k][0]) * f;
-      const double pk = __longlong_as_double((long long)got[k][3]);
+      const float mk = __uint_as_float((uint32_t)got[k][1]);
+      const float f = mk > -INFINITY ? ex2_approx((mk - M) * c) : 0.0f;
+      const float q = __uint_as_float((uint32_t)got[k][0]) * f;
       others += q;
-      S += q + __longlong_as_double((long long)got[k][1]) * f;
-      mass += pk;
-      // that CTA's loss terms stand against its own maximum
-      L += __longlong_as_double((long long)got[k][2]);
-      if (pk > 0.0) L += pk * ((double)M - rk) * inv_t;
+      S += q + __uint_as_float((uint32_t)(got[k][0] >> 32)) * f;
+      mass += __longlong_as_double((long long)got[k][3]);
     }
-    L += mass * log(S);
-    inv_s = (float)(1.0 / S);
-    double share = 1.0;  // what is left of s outside the entries
+    inv_s = 1.0f / S;
+    of = others * inv_s;
+    float share = 1.0f;  // what is left of s outside the entries
     if (p.lse) {
-      double left = fmax(1.0 - mass, 0.0);
-      const double of = others / S;
       // a log-sum-exp in float32 leaves about 2^-21 of the mass unsure: nothing is asked
       // of a row that has nothing to give
-      if (!(of > 0.0) && left < 0x1p-20) left = 0.0;
-      if (left > 0.0) {
-        L += left * (log(left) - log(of));
-        share = of > 0.0 ? 1.0 - left / of : 0.0;
-      }
+      left = fmaxf((float)(1.0 - mass), 0.0f);
+      if (!(of > 0.0f) && left < 0x1p-20f) left = 0.0f;
+      share = of > 0.0f ? 1.0f - left / of : 0.0f;
     }
-    coef = (float)fmin(fmax((double)w * inv_t * share / S, -3.0e38), 3.0e38);
+    coef = fminf(fmaxf(w * (float)inv_t * share * inv_s, -3.0e38f), 3.0e38f);
   }
 
-  if (rank == 0 && tid == 0 && p.loss) {
-    p.loss[n] = st ? __int_as_float(0x7fc00000) : none ? 0.0f : (float)L;
-    p.row_status[n] = st;
+  if (rank == 0 && tid < 32 && p.loss) {
+    double L = 0.0;
+    if (w != 0.0f) {
+      for (int k = 0; k < size; ++k) {
+        // that CTA's terms stand against its own maximum
+        const float mk = __uint_as_float((uint32_t)got[k][1]);
+        const double pk = __longlong_as_double((long long)got[k][3]);
+        L += __longlong_as_double((long long)got[k][2]);
+        if (pk > 0.0 && mk > -INFINITY) L += pk * ((double)M - mk) * inv_t;
+        L += pk * log((double)S);
+      }
+      if (left > 0.0f) L += left * (log((double)left) - log((double)of));
+    }
+    if (tid == 0) {
+      p.loss[n] = st ? __int_as_float(0x7fc00000) : none ? 0.0f : (float)L;
+      p.row_status[n] = st;
+    }
   }
   if (kGrad) {
     const float fill = st ? __int_as_float(0x7fc00000) : 0.0f;
@@ -290,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
     }
     __syncthreads();
     if (!plain) {
-      const float k = (float)((double)w * inv_t);
+      const float k = w * (float)inv_t;
       for (int j = tid; j < sm.entries; j += kThreads) {
         const float y = k * (ex2_approx((at_x[j] - M) * c) * inv_s - at_p[j]);
         put_elem<DT>(like ? out + (ptrdiff_t)(s.first + pos[j]) * es : buf + (size_t)pos[j] * es, y);

@@ -85,6 +85,7 @@ int distill_params(DistillParams &p, const void *logits, int dtype, RowsAt at, c
   p.lse = lse;
   p.weight = weight;
   p.temperature = temperature;
+  p.inv_t = 1.0 / (double)temperature;
   p.dtype = dtype;
   p.B = B;
   p.R = R;

@@ -52,6 +52,7 @@ struct DistillParams {
   const float *weight;   // [B, R] or NULL
   const float *dloss;    // [B, R]: the backward call; NULL otherwise
   float temperature;
+  double inv_t;          // 1 / temperature
   int dtype, B, R, V, K;
   float *loss;           // [B, R]; NULL in the backward call, as row_status
   void *grad;            // or NULL
@@ -208,6 +209,12 @@ __device__ __forceinline__ unsigned long long remote_get(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ uint32_t remote_get32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
 constexpr int kWords = 8;  // of one CTA's record in an exchange
 
 // What the CTAs of a cluster tell one another: two buffers used in turn, so that a CTA
@@ -236,19 +243,15 @@ __device__ __forceinline__ const unsigned long long (*exchange(Exchange &ex, int
 
 // ---- sums over a CTA ------------------------------------------------------------------
 
-__device__ __forceinline__ double shfl_xor_d(double v, int m) {
-  return __shfl_xor_sync(kFull, v, m);
-}
-
 // Sum of v over the CTA in a fixed order; `red` holds one value a warp.  Every thread
 // gets it.  A barrier before `red` is used again.
 template <int kWarps>
-__device__ __forceinline__ double cta_sum(double v, double *red) {
+__device__ __forceinline__ float cta_sum(float v, float *red) {
 #pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) v += shfl_xor_d(v, d);
+  for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  double s = 0.0;
+  float s = 0.0f;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) s += red[w];
   return s;

@@ -45,38 +45,43 @@ constexpr WeightTable make_table() {
 
 constexpr float kFixed = 0x1p42f;  // units of a weight of 1
 
-// What a row's weights need.
+// What a row's weights need.  (No 64-bit arithmetic: this GPU has little of it.)
 struct WeightOf {
   float ch, cl;     // c = log2(e) / T
   float off;        // taken from the logits first: 0, or M where M c is large (the
                     // difference is exact then for every logit that weighs anything)
   float magic;      // 12288 - M c, a multiple of 2^-10
-  float least;      // logits below weigh nothing (less than 2^-60)
-  double ref;       // the weight of M (about 1)
+  float least;      // logits (less off) below count as this one, whose weight of 2^-60 is 0
+                    // in fixed point
+  float rest;       // M c less its rounding: the weight of M is 2^rest
 };
 
-__device__ __forceinline__ WeightOf weight_of(float M, float T) {
+__device__ __forceinline__ WeightOf weight_of(float M, float ch, float cl) {
   WeightOf w;
-  const double c = 1.4426950408889634 / (double)T;
-  w.ch = (float)c;
-  w.cl = (float)(c - (double)w.ch);
-  w.off = fabs((double)M * c) >= 2047.0 ? M : 0.0f;
-  const double mc = ((double)M - w.off) * c;
-  const double mr = rint(mc * 1024.0) * 0x1p-10;
-  w.magic = (float)(12288.0 - mr);
-  w.least = (float)((double)M - 60.0 / c);
-  w.ref = exp2(mc - mr);
+  w.ch = ch;
+  w.cl = cl;
+  float mc = M * ch, low = fmaf(M, cl, fmaf(M, ch, -mc));
+  w.off = 0.0f;
+  if (fabsf(mc) >= 2047.0f) {
+    w.off = M;
+    mc = low = 0.0f;
+  }
+  const float mr = rintf(mc * 1024.0f) * 0x1p-10f;
+  w.magic = 12288.0f - mr;
+  w.least = (M - w.off) - 60.0f / ch;
+  w.rest = (mc - mr) + low;
   return w;
 }
 
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // Two weights as a + b: a a multiple of 2^-20, b one of 2^-42 and not above 2^-20, so that
-// float32 sums of eight are exact.  What comes out for logits below w.least means nothing.
+// float32 sums of eight are exact.
 __device__ __forceinline__ void weight2(float2 l, const WeightOf &w, const float2 *table, float2 &a,
                                         float2 &b) {
   const float2 ch = both(w.ch), magic = both(w.magic);
   l = __fadd2_rn(l, both(-w.off));
+  l = make_float2(fmaxf(l.x, w.least), fmaxf(l.y, w.least));
   const float2 t = __ffma2_rn(l, ch, magic);  // 12288 + x, rounded to a multiple of 2^-10
   const float2 at = __fadd2_rn(t, both(-w.magic));
   float2 f = __ffma2_rn(l, ch, make_float2(-at.x, -at.y));
@@ -107,7 +112,6 @@ __device__ __forceinline__ unsigned long long fixed_of(float a, float b) {
 
 __device__ __forceinline__ unsigned long long weight_fixed(float l, const WeightOf &w,
                                                            const float2 *table) {
-  if (!(l >= w.least)) return 0ull;
   float2 a, b;
   weight2(both(l), w, table, a, b);
   return fixed_of(a.x, b.x);

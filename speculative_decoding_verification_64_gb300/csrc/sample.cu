@@ -11,9 +11,11 @@
 //   * With top-k: each thread's maximum is one group's; the k-th largest of those (its top 16
 //     bits) bounds the k-th logit from below, the few tokens that reach it are gathered by
 //     rank 0, sorted, weighed, cut and drawn from.
-//   * With top-p alone: a search over places.  A pass adds the weights of all places above a
-//     bracket, and in it; when the cut is inside and the bracket's tokens fit a list, they
-//     are sorted and the cut is found among them.
+//   * With top-p alone: a histogram of the logits, 1/128 octave of weight a bin, says about
+//     where the cut is.  A pass adds the weights of all places above a bracket around it, and
+//     in it; when the cut is inside and the bracket's tokens fit a list, they are sorted and
+//     the cut is found among them.  A bracket that missed is placed anew by what the pass
+//     found, and where that fails, between the places known to hold the cut, halves of them.
 //   * The draws of such rows: the passes leave the kept mass of every run of 32 vectors; a
 //     draw looks its run up, and a warp weighs that run once more.
 // Which token is cut last, or drawn, turns on sums over the vocabulary: weights and sums are
@@ -29,6 +31,10 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kList = 2048;   // tokens that rank 0 can sort
 constexpr int kMine = 1024;   // tokens that a CTA can bring
 constexpr int kKeys = 4096;   // groups' maxima (256 of each of 16 CTAs)
+constexpr int kBins = 4096;   // of the histogram
+constexpr float kOctave = 128.0f;  // bins of a factor of two in weight
+constexpr int kBudget = 600;  // tokens of a first bracket on either side
+constexpr int kTries = 3;     // brackets placed by the histogram
 constexpr int kAll = 0x7FFFFFFF;
 constexpr float kLeast = -3.402823466e38f;
 
@@ -43,10 +49,15 @@ struct SampleSmem {
   union {
     u64 list[kList];
     uint32_t key[kKeys];
+    uint32_t bin[kBins];
   };
   u64 mine[kMine];
   u64 red[2][kWarps];
-  float redf[kWarps];
+  float redf[2][kWarps];
+  float ch, cl;        // log2(e) / T
+  double drop;         // T ln(min_p)
+  int bracket_bin, bracket_first, bracket_last;
+  float bracket_before;
   unsigned total[16];
   int n_mine, n_kept;
   u64 cut[2];
@@ -145,6 +156,7 @@ struct Found {
 
 // One pass: steps[i] gets the mass above `hi` of the share's vectors 32 i .. 32 i + 31; with
 // kBracket also tokens from `lo` up to `hi`, which go on the list.  Sums of each warp.
+// Tokens between the two values are few where it counts, and looked at one by one.
 template <int DT, bool kBracket>
 __device__ __forceinline__ Found weigh(const Share &s, const uint8_t *buf, const WeightOf &w,
                                        const Cut &hi, const Cut &lo, u64 *steps, SampleSmem &sm) {
@@ -153,44 +165,57 @@ __device__ __forceinline__ Found weigh(const Share &s, const uint8_t *buf, const
   Found f = {0, 0, 0, 0};
   u64 in = 0, all = 0;
   int n_above = 0;
+  const float low = kBracket ? lo.value : hi.value;
   for (int i = warp; 32 * i < s.nvec; i += kWarps) {
     const int v = 32 * i + lane;
     float x[kN];
     load_share<DT>(s, buf, v, x);
-    const int at = s.first + v * kN;
-    float2 sum_a = both(0.0f), sum_i = both(0.0f), sum_z = both(0.0f);  // (a, b) each
+    float2 sum_a = both(0.0f), sum_z = both(0.0f);  // (a, b) each
+    int n1 = 0, n2 = 0;
 #pragma unroll
     for (int e = 0; e < kN; e += 2) {
       float2 a, b;
       weight2(make_float2(x[e], x[e + 1]), w, sm.table, a, b);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float y = x[e + h];
-        const bool some = y >= w.least;
-        const float2 ab =
-            make_float2(some ? (h ? a.y : a.x) : 0.0f, some ? (h ? b.y : b.x) : 0.0f);
-        const bool above = hi.holds(y, at + e + h);
-        if (above) {
-          sum_a = __fadd2_rn(sum_a, ab);
-          ++n_above;
-        }
-        if (kBracket) {
-          sum_z = __fadd2_rn(sum_z, ab);
-          if (!above && lo.holds(y, at + e + h)) {
-            sum_i = __fadd2_rn(sum_i, ab);
-            const int k = atomicAdd(&sm.n_mine, 1);  // (sorted later)
-            if (k < kMine) sm.mine[k] = place_of(y, at + e + h);
-          }
+      if (kBracket) {
+        sum_z = __fadd2_rn(sum_z, make_float2(a.x, b.x));
+        sum_z = __fadd2_rn(sum_z, make_float2(a.y, b.y));
+      }
+      if (x[e] > hi.value) {
+        sum_a = __fadd2_rn(sum_a, make_float2(a.x, b.x));
+        ++n1;
+      }
+      if (x[e + 1] > hi.value) {
+        sum_a = __fadd2_rn(sum_a, make_float2(a.y, b.y));
+        ++n1;
+      }
+      n2 += x[e] >= low;
+      n2 += x[e + 1] >= low;
+    }
+    u64 above = fixed_of(sum_a.x, sum_a.y);
+    if (n2 != n1) {
+      const int at = s.first + v * kN;
+#pragma unroll 1
+      for (int e = 0; e < kN; ++e) {
+        const float y = get_elem<DT>(buf + (size_t)v * 16 + e * Elem<DT>::kBytes);
+        if (y > hi.value || y < low) continue;
+        const bool kept = hi.holds(y, at + e);
+        if (!kept && (!kBracket || !lo.holds(y, at + e))) continue;
+        const u64 t = weight_fixed(y, w, sm.table);
+        if (kept) {
+          above += t;
+          ++n1;
+        } else {
+          in += t;
+          const int k = atomicAdd(&sm.n_mine, 1);  // (sorted later)
+          if (k < kMine) sm.mine[k] = place_of(y, at + e);
         }
       }
     }
-    const u64 t = warp_sum_u64(fixed_of(sum_a.x, sum_a.y));
+    n_above += n1;
+    const u64 t = warp_sum_u64(above);
     if (lane == 0) steps[i] = t;
     f.above += t;
-    if (kBracket) {
-      in += fixed_of(sum_i.x, sum_i.y);
-      all += fixed_of(sum_z.x, sum_z.y);
-    }
+    if (kBracket) all += fixed_of(sum_z.x, sum_z.y);
   }
   f.n_above = __reduce_add_sync(kFull, n_above);
   if (kBracket) {
@@ -198,6 +223,130 @@ __device__ __forceinline__ Found weigh(const Share &s, const uint8_t *buf, const
     f.all = warp_sum_u64(all);
   }
   return f;
+}
+
+// The row's histogram, in every CTA: bin j counts the tokens whose weight is 2^(-j / 128) to
+// 2^(-(j + 1) / 128), the last one those below too.
+template <int DT>
+__device__ __forceinline__ void histogram(const Share &s, const uint8_t *buf, float M, float ch,
+                                          int rank, int size, SampleSmem &sm) {
+  constexpr int kN = Elem<DT>::kN;
+  for (int i = threadIdx.x; i < kBins; i += kThreads) sm.bin[i] = 0;
+  __syncthreads();
+  const float c = ch * kOctave;
+  for (int v = threadIdx.x; v < s.nvec; v += kThreads) {
+    float x[kN];
+    load_share<DT>(s, buf, v, x);
+#pragma unroll
+    for (int e = 0; e < kN; ++e) {
+      const float y = fminf((M - x[e]) * c, (float)(kBins - 1));
+      if (x[e] >= kLeast) atomicAdd(&sm.bin[(int)y], 1u);
+    }
+  }
+  cluster_sync();
+  // each CTA adds up its part of the bins and, once nobody reads the parts any more, gives
+  // the sums to all
+  const int per = kBins / size;
+  uint32_t sum[kBins / kThreads];
+#pragma unroll
+  for (int i = 0; i < kBins / kThreads; ++i) {
+    const int j = threadIdx.x + i * kThreads;
+    sum[i] = 0;
+    if (j >= per) continue;
+    for (int q = 0; q < size; ++q)
+      sum[i] += remote_get32(cluster_addr(smem_addr(&sm.bin[rank * per + j]), q));
+  }
+  cluster_sync();
+#pragma unroll
+  for (int i = 0; i < kBins / kThreads; ++i) {
+    const int j = threadIdx.x + i * kThreads;
+    if (j >= per) continue;
+    for (int q = 0; q < size; ++q)
+      remote_put(cluster_addr(smem_addr(&sm.bin[rank * per + j]), q), sum[i]);
+  }
+  cluster_sync();
+}
+
+// Where the mass of the histogram's first bins reaches `want` (of weights as they stand
+// there; a share of all of it where `share` is set): the bins of a bracket around that
+// place, no more than kBudget tokens and 32 bins to either side, and the mass before them.
+__device__ __forceinline__ void place_bracket(float want, bool share, SampleSmem &sm, int &first,
+                                              int &last, float &before) {
+  constexpr int kEach = kBins / kThreads;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  float mass[kEach], mine = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int j = tid * kEach + i;
+    mass[i] = (float)sm.bin[j] * ex2_approx(-((float)j + 0.5f) / kOctave);
+    mine += mass[i];
+  }
+  float inc = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const float y = __shfl_up_sync(kFull, inc, d);
+    if (lane >= d) inc += y;
+  }
+  __syncthreads();
+  if (lane == 31) sm.redf[1][warp] = inc;
+  if (tid == 0) sm.bracket_bin = kBins;
+  __syncthreads();
+  float run = inc - mine, whole = 0.0f;
+#pragma unroll
+  for (int q = 0; q < kWarps; ++q) {
+    if (q < warp) run += sm.redf[1][q];
+    whole += sm.redf[1][q];
+  }
+  if (share) want *= whole;
+  // the first bin whose mass reaches it (rounded sums of neighbours may both, or overlap:
+  // the first one, the same in every CTA)
+  int at = kBins;
+  float b = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    if (at == kBins && mass[i] > 0.0f && run + mass[i] >= want) {
+      at = tid * kEach + i;
+      b = run;
+    }
+    run += mass[i];
+  }
+  if (at < kBins) atomicMin(&sm.bracket_bin, at);
+  __syncthreads();
+  if (at == sm.bracket_bin && at < kBins) sm.bracket_before = b;
+  __syncthreads();
+  if (warp == 0) {
+    at = sm.bracket_bin;
+    b = sm.bracket_before;
+    if (at == kBins) {  // (beyond what rounded sums reach)
+      at = kBins - 1;
+      b = whole;
+    }
+    unsigned up = at - 1 - lane >= 0 ? sm.bin[at - 1 - lane] : 0;
+    unsigned down = at + 1 + lane < kBins ? sm.bin[at + 1 + lane] : 0;
+    float m = (float)up * ex2_approx(-((float)(at - 1 - lane) + 0.5f) / kOctave);
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const unsigned y = __shfl_up_sync(kFull, up, d), z = __shfl_up_sync(kFull, down, d);
+      if (lane >= d) {
+        up += y;
+        down += z;
+      }
+    }
+    const int n_up = __popc(__ballot_sync(kFull, up <= kBudget && at - 1 - lane >= 0));
+    const int n_down = __popc(__ballot_sync(kFull, down <= kBudget && at + 1 + lane < kBins));
+    if (lane >= n_up) m = 0.0f;
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) m += __shfl_xor_sync(kFull, m, d);
+    if (lane == 0) {
+      sm.bracket_before = b - m;
+      sm.bracket_first = at - n_up;
+      sm.bracket_last = at + n_down;
+    }
+  }
+  __syncthreads();
+  before = sm.bracket_before;
+  first = sm.bracket_first;
+  last = sm.bracket_last;
 }
 
 // The tokens from `lo` up, on the list.
@@ -283,6 +432,15 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleParams 
     top_p = 1.0f;
     min_p = 0.0f;
   }
+  if (warp == 1) {
+    const double c = 1.4426950408889634 / (double)T;
+    const double drop = min_p > 0.0f ? (double)T * log((double)min_p) : 0.0;
+    if (lane == 0) {
+      sm.ch = (float)c;
+      sm.cl = (float)(c - (double)(float)c);
+      sm.drop = drop;
+    }
+  }
 
   // the largest logit, and the largest of each thread's part of every copy
   float gm[kChunks];
@@ -323,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleParams 
         if (i < sub) remote_put(to + 4u * i, order_key(gm[i]) >> 16);
     }
   }
-  M = cta_max_nan<kWarps>(M, sm.redf);
+  M = cta_max_nan<kWarps>(M, sm.redf[0]);
   u64 rec[kWords];
   rec[0] = (u64)(sm.in.gave_up ? SPECDEC_ROW_INTERNAL : 0) << 32 | __float_as_uint(M);
   const u64(*got)[kWords] = exchange(sm.ex, turn, rec, 1, rank, size);
@@ -336,12 +494,12 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleParams 
 
   // (from here every CTA of the cluster takes the same branches: they turn on the
   // request's filters and on exchanged records)
-  const WeightOf w = weight_of(M, T);
+  const WeightOf w = weight_of(M, sm.ch, sm.cl);
   Cut cut = {kLeast, kAll};  // everything but -infinity
   u64 Z = 0;                 // the kept mass
   int kept = 0;
   const float floor_value =
-      min_p > 0.0f ? __double2float_ru((double)M + (double)T * log((double)min_p)) : kLeast;
+      min_p > 0.0f ? __double2float_ru((double)M + sm.drop) : kLeast;
   const u64 over = ((u64)order_key(M) + 1) << 32;  // above every place
   const float *u = p.uniforms + n * p.S;
   int32_t *tokens = p.tokens + n * p.S;
@@ -467,11 +625,29 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleParams 
     if (top_p < 1.0f) {
       // less than the wanted mass stands above H, all of it above L: sums are exact, so that
       // this holds throughout, and halves end
-      u64 L = (u64)max(order_key(w.least), kLeastKey) << 32, H = over, lo = L;
+      u64 L = (u64)max(order_key(M - 45.0f / w.ch), kLeastKey) << 32, H = over, lo, hi;
       Found f;  // of the whole row
-      u64 want;
-      for (;;) {
-        const Found m = weigh<DT, true>(s, buf, w, cut_at(H), cut_at(lo), steps, sm);
+      u64 want = 0;
+      float guess = top_p, before = 0.0f;
+      histogram<DT>(s, buf, M, w.ch, rank, size, sm);
+      for (int tries = 0;; ++tries) {
+        lo = L + (H - L) / 2;  // (L itself where one place is left)
+        hi = H;
+        if (tries < kTries) {
+          int first, last;
+          place_bracket(guess, tries == 0, sm, first, last, before);
+          const float bin = 1.0f / (w.ch * kOctave);
+          const u64 from = (u64)max(order_key(M - (float)(last + 1) * bin), kLeastKey) << 32;
+          const u64 to = first > 0 ? (u64)order_key(M - (float)first * bin) << 32 : over;
+          // (what the bins say may lie beyond what is known: then halves)
+          if (max(from, L) < min(to, H)) {
+            lo = max(from, L);
+            hi = min(to, H);
+          } else {
+            tries = kTries;
+          }
+        }
+        const Found m = weigh<DT, true>(s, buf, w, cut_at(hi), cut_at(lo), steps, sm);
         __syncthreads();
         if (tid < 3) sm.red[0][tid] = 0;
         if (tid == 3) sm.total[0] = 0;
@@ -500,14 +676,22 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleParams 
           n_in += here;
           fits = fits && here <= kMine;
         }
+        fits = fits && n_in <= kList;
         want = max(share_at_least(top_p, f.all), 1ull);
-        const bool inside = want <= f.above + f.in;
-        if (inside && fits && n_in <= kList) break;
-        if (inside)
-          L = lo;
-        else
+        if (want <= f.above) {
+          L = hi;
+        } else if (want > f.above + f.in) {
           H = lo;
-        lo = L + (H - L) / 2;  // (L itself where one place is left)
+        } else if (fits) {
+          break;
+        } else {
+          L = lo;
+          H = hi;
+          tries = kTries;
+        }
+        // the histogram's mass is off by what the pass shows at the bracket's upper end
+        const float unit = ex2_approx(-w.rest) / kFixed;
+        guess = before + ((float)want - (float)f.above) * unit;
         __syncthreads();
         if (tid == 0) sm.n_mine = 0;
         __syncthreads();
@@ -603,7 +787,8 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleParams 
       if (sum <= left && left < sum + t) {
         int e = 0;
         for (; e < kN - 1; ++e) {
-          if (cut.holds(x[e], first + e)) sum += weight_fixed(x[e], w, sm.table);
+          const float y = get_elem<DT>(buf + (size_t)v * 16 + e * es);
+          if (cut.holds(y, first + e)) sum += weight_fixed(y, w, sm.table);
           if (left < sum) break;
         }
         tokens[d] = first + e;
@@ -626,7 +811,11 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleParams 
     const bool like =
         ((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0;
     const float c = temperature_scale(T);
-    const float g = (float)(w.ref * (double)kFixed / (double)Z);
+    // 2^rest 2^42 / Z, rounded about once: 1 / Z's error and 2^rest - 1 are small terms
+    const float zf = __ull2float_rn(Z), q0 = __fdiv_rn(kFixed, zf);
+    const float off = fmaf(-q0, zf, kFixed) / zf - (float)(long long)(Z - __float2ull_rn(zf)) * (q0 / zf);
+    const float up = w.rest * fmaf(w.rest, fmaf(w.rest, 0.0555041087f, 0.240226507f), 0.693147181f);
+    const float g = q0 + fmaf(q0, up, off);
     __syncthreads();  // (draws read the share)
     for (int v = tid; v < s.nvec; v += kThreads) {
       float x[kN];

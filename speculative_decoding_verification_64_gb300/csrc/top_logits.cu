@@ -159,7 +159,7 @@ struct PickSmem {
     uint32_t count[1 << kDigit];
   } u;
   unsigned long long list[kList];
-  double red[kPickWarps];
+  float red[kPickWarps];
   float redf[kPickWarps];
   unsigned int total[16];
   int n, digit, need;
@@ -241,10 +241,10 @@ __global__ void __launch_bounds__(kPickThreads) top_pick_kernel(const TopParams 
     }
     return;
   }
-  double S = 0.0;
+  float S = 0.0f;
   for (int i = tid; i < p.spr; i += kPickThreads) {
     const float2 q = __ldg(part + i);
-    if (q.x > -INFINITY) S += (double)(q.y * ex2_approx((q.x - M) * c));
+    if (q.x > -INFINITY) S += q.y * ex2_approx((q.x - M) * c);
   }
   S = cta_sum<kPickWarps>(S, sm.red);
 
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kPickThreads) top_pick_kernel(const TopParams 
     p.ids[n * p.K + i] = place_index(q);
   }
   if (tid == 0) {
-    p.lse[n] = (float)((double)M / (double)p.temperature + log(S));
+    p.lse[n] = (float)((double)M / (double)p.temperature + log((double)S));
     p.row_status[n] = 0;
   }
 }
