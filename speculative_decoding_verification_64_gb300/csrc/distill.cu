@@ -12,7 +12,8 @@
 // entries taken out (their logits put to -infinity in shared memory, so that s_rest is a sum
 // and no difference of two near equal ones); one exchange of five words between the CTAs;
 // the gradient, straight from registers to global memory, then the entries' own values.  The
-// few terms of the loss are added in 64 bits, the rest is float32.
+// terms of the loss are float32, added in 64-bit fixed point (an SM has two lanes for 64-bit
+// floating point: one logarithm a row is all that is left to them).
 #include "draft_common.cuh"
 
 namespace specdec {
@@ -25,12 +26,15 @@ constexpr int kPerThread = SPECDEC_MAX_TOPK / kThreads;
 struct DistillSmem {
   Exchange ex;
   Arrival in;
-  double terms[2][kWarps];
-  float red[4][kWarps];
-  double shift;
+  long long terms[2][kWarps];
+  float red[5][kWarps];
   int status;
   int entries;
 };
+
+constexpr float kTerm = 0x1p40f;  // units of the fixed-point sums
+constexpr float kMost = 0x1p12f;  // terms that they take (1024 of them); the larger are added
+                                  // in float32, where a loss with such a term ends anyway
 
 // Dynamic shared memory: DistillSmem, the share, one bit for each of its elements, and a
 // position, logit and teacher's share for each entry.
@@ -127,59 +131,54 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
   // a row without weight or entries: nothing to learn, whatever its logits hold
   const bool none = w == 0.0f || (!some && !wrong);
 
-  // (64-bit operations are few and of single warps: this GPU has two of their lanes an SM)
-  const double inv_t = p.inv_t;
   const float c = temperature_scale(p.temperature);
   float m = -INFINITY;
   const unsigned long long(*got)[kWords] = nullptr;
-  float coef = 0.0f, M = 0.0f, inv_s = 0.0f, S = 0.0f, left = 0.0f, of = 0.0f;
+  float coef = 0.0f, M = 0.0f, inv_s = 0.0f, S = 0.0f, left = 0.0f, of = 0.0f, zs = 1.0f;
+  long long mass = 0;
   int st = 0;
   if (w != 0.0f) {
-    // ln p_j = z_j / T - shift
-    double shift = 0.0;
+    // p_j = e^y_j / zs: y_j = z_j / T - lse and zs = 1, or y_j = (z_j - zmax) / T
+    float lse = 0.0f;
     if (p.lse) {
-      const float given = p.lse[n];
-      if (!(fabsf(given) < INFINITY)) status |= SPECDEC_ROW_NONFINITE;
-      shift = given;
+      lse = p.lse[n];
+      if (!(fabsf(lse) < INFINITY)) status |= SPECDEC_ROW_NONFINITE;
+      zmax = 0.0f;
     } else {
       zmax = cta_max_nan<kWarps>(zmax, sm.red[0]);
-      float zs = 0.0f;
+      if (some && !(zmax > -INFINITY)) status |= SPECDEC_ROW_NONFINITE;
+    }
+    // (1 / T in two parts, so that z / T is rounded once)
+    auto y_of = [&](float zj) {
+      const float dz = zj - zmax;
+      return fmaf(dz, p.inv_t, -lse) + dz * p.inv_t_low;
+    };
+    if (!p.lse) {
+      zs = 0.0f;
 #pragma unroll
       for (int i = 0; i < kPerThread; ++i)
-        if (z[i] > -INFINITY) zs += expf((float)(((double)z[i] - zmax) * inv_t));
+        if (z[i] > -INFINITY) zs += expf(y_of(z[i]));
       zs = cta_sum<kWarps>(zs, sm.red[1]);
-      if (some && !(zmax > -INFINITY)) status |= SPECDEC_ROW_NONFINITE;
-      if (tid < 32) {
-        shift = zmax * inv_t + log((double)zs);
-        if (tid == 0) sm.shift = shift;
-      }
-      __syncthreads();
-      shift = sm.shift;
     }
+    const float inv_zs = 1.0f / zs;
 
     // the largest logit, as the copies land
+    uint32_t top = no_max<DT>();
     for (int i = 0; i < kChunks; ++i) {
       share_wait(sm.in, i);
       const int v1 = 1 + chunk_begin(s, i + 1);
-      for (int v = 1 + chunk_begin(s, i) + tid; v < v1; v += kThreads) {
-        float x[kN];
-        widen<DT>(*reinterpret_cast<const uint4 *>(buf + (size_t)v * 16), x);
-#pragma unroll
-        for (int e = 0; e < kN; ++e) m = fmax_nan(m, x[e]);
-      }
+      for (int v = 1 + chunk_begin(s, i) + tid; v < v1; v += kThreads)
+        top = vector_max<DT>(*reinterpret_cast<const uint4 *>(buf + (size_t)v * 16), top);
     }
-    if (tid < 2) {
-      float x[kN];
-      widen<DT>(*reinterpret_cast<const uint4 *>(buf + (size_t)(tid ? s.nvec - 1 : 0) * 16), x);
-#pragma unroll
-      for (int e = 0; e < kN; ++e) m = fmax_nan(m, x[e]);
-    }
-    m = cta_max_nan<kWarps>(m, sm.red[2]);
+    if (tid < 2)
+      top = vector_max<DT>(
+          *reinterpret_cast<const uint4 *>(buf + (size_t)(tid ? s.nvec - 1 : 0) * 16), top);
+    m = cta_max_nan<kWarps>(max_of<DT>(top), sm.red[2]);
     const float ref = m > -INFINITY ? m : 0.0f;
 
     // this CTA's entries: noted, and taken out of the row
-    float at_s = 0.0f;
-    double terms = 0.0, at_mass = 0.0;  // loss terms, and p
+    float at_s = 0.0f, large = 0.0f;
+    long long terms = 0, at_mass = 0;  // sum p_j (y_j - (x_j - ref) / T), and of p_j
     int mine = 0;
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
@@ -190,13 +189,20 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
         status |= SPECDEC_ROW_BAD_TOKEN;  // the same token twice
         continue;
       }
-      const double lp = z[i] > -INFINITY ? z[i] * inv_t - shift : -INFINITY;
-      const float pj = expf((float)lp);
+      const float y = z[i] > -INFINITY ? y_of(z[i]) : -INFINITY;
+      const float pj = expf(y) * inv_zs;
       const float x = get_elem<DT>(buf + (size_t)at * es);
       put_elem<DT>(buf + (size_t)at * es, -INFINITY);
       at_s += ex2_approx((x - ref) * c);
-      if (pj > 0.0f) terms += pj * (lp - ((double)x - ref) * inv_t);
-      at_mass += pj;
+      if (pj > 0.0f) {
+        const float dx = x - ref;
+        const float t = x > -INFINITY ? pj * (y - fmaf(dx, p.inv_t, dx * p.inv_t_low)) : INFINITY;
+        if (fabsf(t) < kMost)
+          terms += __float2ll_rn(t * kTerm);
+        else
+          large += t;
+        at_mass += __float2ll_rn(fminf(pj, kMost) * kTerm);
+      }
       const int k = atomicAdd(&sm.entries, 1);  // (their order decides nothing)
       pos[k] = at;
       at_x[k] = x;
@@ -207,66 +213,69 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
       for (int d = 16; d >= 1; d >>= 1) {
         terms += __shfl_xor_sync(kFull, terms, d);
         at_mass += __shfl_xor_sync(kFull, at_mass, d);
+        at_s += __shfl_xor_sync(kFull, at_s, d);
+        large += __shfl_xor_sync(kFull, large, d);
       }
     }
     if ((tid & 31) == 0) {
       sm.terms[0][tid >> 5] = terms;
       sm.terms[1][tid >> 5] = at_mass;
+      sm.red[3][tid >> 5] = at_s;
+      sm.red[4][tid >> 5] = large;
     }
     if (status) atomicOr(&sm.status, status);
     __syncthreads();
-    float rest = 0.0f;
+    float2 sum0 = both(0.0f), sum1 = both(0.0f);
     for (int v = tid; v < s.nvec; v += kThreads) {
-      float x[kN], q = 0.0f;
-      widen<DT>(*reinterpret_cast<const uint4 *>(buf + (size_t)v * 16), x);
+      float2 x[kN / 2];
+      widen2<DT>(*reinterpret_cast<const uint4 *>(buf + (size_t)v * 16), x);
 #pragma unroll
-      for (int e = 0; e < kN; ++e) q += ex2_approx((x[e] - ref) * c);
-      rest += q;
+      for (int e = 0; e < kN / 2; e += 2) {
+        sum0 = __fadd2_rn(sum0, exp2_pair(x[e], ref, c));
+        sum1 = __fadd2_rn(sum1, exp2_pair(x[e + 1], ref, c));
+      }
     }
+    sum0 = __fadd2_rn(sum0, sum1);
+    float rest = sum0.x + sum0.y;
 #pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) {
-      rest += __shfl_xor_sync(kFull, rest, d);
-      at_s += __shfl_xor_sync(kFull, at_s, d);
-    }
-    if ((tid & 31) == 0) {
-      sm.red[0][tid >> 5] = rest;
-      sm.red[3][tid >> 5] = at_s;
-    }
+    for (int d = 16; d >= 1; d >>= 1) rest += __shfl_xor_sync(kFull, rest, d);
+    if ((tid & 31) == 0) sm.red[0][tid >> 5] = rest;
     __syncthreads();
     unsigned long long rec[kWords];
     if (tid < 32) {
-      rest = at_s = 0.0f;
-      terms = at_mass = 0.0;
+      rest = at_s = large = 0.0f;
+      terms = at_mass = 0;
       for (int k = 0; k < kWarps; ++k) {
         rest += sm.red[0][k];
         at_s += sm.red[3][k];
+        large += sm.red[4][k];
         terms += sm.terms[0][k];
         at_mass += sm.terms[1][k];
       }
       const int wrong_here = sm.status | (sm.in.gave_up ? SPECDEC_ROW_INTERNAL : 0);
       rec[0] = (unsigned long long)__float_as_uint(at_s) << 32 | __float_as_uint(rest);
       rec[1] = (unsigned long long)(uint32_t)wrong_here << 32 | __float_as_uint(m);
-      rec[2] = (unsigned long long)__double_as_longlong(terms);
-      rec[3] = (unsigned long long)__double_as_longlong(at_mass);
+      rec[2] = (unsigned long long)terms;
+      rec[3] = (unsigned long long)at_mass;
+      rec[4] = __float_as_uint(large);
     }
-    got = exchange(sm.ex, turn, rec, 4, rank, size);
+    got = exchange(sm.ex, turn, rec, 5, rank, size);
 
     M = -INFINITY;
     for (int k = 0; k < size; ++k) {
       M = fmax_nan(M, __uint_as_float((uint32_t)got[k][1]));
       st |= (int)(got[k][1] >> 32);
+      mass += (long long)got[k][3];
     }
     if (!(M > -INFINITY && M <= kMaxLogit)) st |= SPECDEC_ROW_NONFINITE;
     if (none) st = 0;
     float others = 0.0f;
-    double mass = 0.0;
     for (int k = 0; k < size; ++k) {
       const float mk = __uint_as_float((uint32_t)got[k][1]);
       const float f = mk > -INFINITY ? ex2_approx((mk - M) * c) : 0.0f;
       const float q = __uint_as_float((uint32_t)got[k][0]) * f;
       others += q;
       S += q + __uint_as_float((uint32_t)(got[k][0] >> 32)) * f;
-      mass += __longlong_as_double((long long)got[k][3]);
     }
     inv_s = 1.0f / S;
     of = others * inv_s;
@@ -274,28 +283,31 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
     if (p.lse) {
       // a log-sum-exp in float32 leaves about 2^-21 of the mass unsure: nothing is asked
       // of a row that has nothing to give
-      left = fmaxf((float)(1.0 - mass), 0.0f);
+      left = fmaxf((float)((1ll << 40) - mass) * 0x1p-40f, 0.0f);
       if (!(of > 0.0f) && left < 0x1p-20f) left = 0.0f;
       share = of > 0.0f ? 1.0f - left / of : 0.0f;
     }
-    coef = fminf(fmaxf(w * (float)inv_t * share * inv_s, -3.0e38f), 3.0e38f);
+    coef = fminf(fmaxf(w * p.inv_t * share * inv_s, -3.0e38f), 3.0e38f);
   }
 
   if (rank == 0 && tid < 32 && p.loss) {
-    double L = 0.0;
+    float L = 0.0f;
     if (w != 0.0f) {
+      // sum p_j (y_j - ln zs - (x_j - M) / T + ln S): that CTA's terms stand against its own
+      // maximum; without a log-sum-exp the p_j are 1 in all by definition
+      double t = p.lse ? (double)mass * log((double)S) : 0x1p40 * log((double)(S * (1.0f / zs)));
       for (int k = 0; k < size; ++k) {
-        // that CTA's terms stand against its own maximum
         const float mk = __uint_as_float((uint32_t)got[k][1]);
-        const double pk = __longlong_as_double((long long)got[k][3]);
-        L += __longlong_as_double((long long)got[k][2]);
-        if (pk > 0.0 && mk > -INFINITY) L += pk * ((double)M - mk) * inv_t;
-        L += pk * log((double)S);
+        const long long pk = (long long)got[k][3];
+        t += (double)(long long)got[k][2];
+        if (pk && mk > -INFINITY) t += (double)pk * (((double)M - mk) * ((double)p.inv_t + p.inv_t_low));
       }
-      if (left > 0.0f) L += left * (log((double)left) - log((double)of));
+      L = (float)(t * 0x1p-40);
+      for (int k = 0; k < size; ++k) L += __uint_as_float((uint32_t)got[k][4]);
+      if (left > 0.0f) L += left * logf(left / of);
     }
     if (tid == 0) {
-      p.loss[n] = st ? __int_as_float(0x7fc00000) : none ? 0.0f : (float)L;
+      p.loss[n] = st ? __int_as_float(0x7fc00000) : none ? 0.0f : L;
       p.row_status[n] = st;
     }
   }
@@ -305,16 +317,16 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
     const bool like =
         ((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0;
     for (int v = tid; v < s.nvec; v += kThreads) {
-      float x[kN];
+      float2 x[kN / 2];
       if (plain) {
 #pragma unroll
-        for (int e = 0; e < kN; ++e) x[e] = fill;
+        for (int e = 0; e < kN / 2; ++e) x[e] = both(fill);
       } else {
-        widen<DT>(*reinterpret_cast<const uint4 *>(buf + (size_t)v * 16), x);
+        widen2<DT>(*reinterpret_cast<const uint4 *>(buf + (size_t)v * 16), x);
 #pragma unroll
-        for (int e = 0; e < kN; ++e) x[e] = coef * ex2_approx((x[e] - M) * c);
+        for (int e = 0; e < kN / 2; ++e) x[e] = __fmul2_rn(both(coef), exp2_pair(x[e], M, c));
       }
-      const uint4 y = narrow<DT>(x);
+      const uint4 y = narrow2<DT>(x);
       if (like)
         store_like<DT>(s, out, v, y);
       else
@@ -322,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
     }
     __syncthreads();
     if (!plain) {
-      const float k = w * (float)inv_t;
+      const float k = w * p.inv_t;
       for (int j = tid; j < sm.entries; j += kThreads) {
         const float y = k * (ex2_approx((at_x[j] - M) * c) * inv_s - at_p[j]);
         put_elem<DT>(like ? out + (ptrdiff_t)(s.first + pos[j]) * es : buf + (size_t)pos[j] * es, y);

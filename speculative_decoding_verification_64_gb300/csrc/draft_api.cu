@@ -85,7 +85,8 @@ int distill_params(DistillParams &p, const void *logits, int dtype, RowsAt at, c
   p.lse = lse;
   p.weight = weight;
   p.temperature = temperature;
-  p.inv_t = 1.0 / (double)temperature;
+  p.inv_t = (float)(1.0 / (double)temperature);
+  p.inv_t_low = (float)(1.0 / (double)temperature - (double)p.inv_t);
   p.dtype = dtype;
   p.B = B;
   p.R = R;

@@ -52,7 +52,7 @@ struct DistillParams {
   const float *weight;   // [B, R] or NULL
   const float *dloss;    // [B, R]: the backward call; NULL otherwise
   float temperature;
-  double inv_t;          // 1 / temperature
+  float inv_t, inv_t_low;  // 1 / temperature, in two parts
   int dtype, B, R, V, K;
   float *loss;           // [B, R]; NULL in the backward call, as row_status
   void *grad;            // or NULL
@@ -105,6 +105,60 @@ __device__ __forceinline__ uint4 narrow(const float *x) {
                       __float_as_uint(x[3]));
   return make_uint4(two_bf16(x[0], x[1]), two_bf16(x[2], x[3]), two_bf16(x[4], x[5]),
                     two_bf16(x[6], x[7]));
+}
+
+// The same as pairs of neighbours, for packed arithmetic.
+template <int DT>
+__device__ __forceinline__ void widen2(const uint4 &w, float2 *x) {
+  const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+  if (DT == SPECDEC_F32) {
+    x[0] = make_float2(__uint_as_float(a[0]), __uint_as_float(a[1]));
+    x[1] = make_float2(__uint_as_float(a[2]), __uint_as_float(a[3]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = make_float2(bf16_lo(a[i]), bf16_hi(a[i]));
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ uint4 narrow2(const float2 *x) {
+  if (DT == SPECDEC_F32)
+    return make_uint4(__float_as_uint(x[0].x), __float_as_uint(x[0].y), __float_as_uint(x[1].x),
+                      __float_as_uint(x[1].y));
+  return make_uint4(two_bf16(x[0].x, x[0].y), two_bf16(x[1].x, x[1].y), two_bf16(x[2].x, x[2].y),
+                    two_bf16(x[3].x, x[3].y));
+}
+
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// 2^((x - m) c) of a pair
+__device__ __forceinline__ float2 exp2_pair(float2 x, float m, float c) {
+  x = __fmul2_rn(__fadd2_rn(x, both(-m)), both(c));
+  return make_float2(ex2_approx(x.x), ex2_approx(x.y));
+}
+
+// The larger of a vector's elements and `m` (NaN where one is), held as 16 bytes' own types:
+// two bfloat16 or one float32 in a word.
+template <int DT>
+__device__ __forceinline__ uint32_t vector_max(const uint4 &w, uint32_t m) {
+  uint32_t r = m;
+  const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (DT == SPECDEC_F32)
+      r = __float_as_uint(fmax_nan(__uint_as_float(r), __uint_as_float(a[i])));
+    else
+      asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(r) : "r"(a[i]));
+  }
+  return r;
+}
+template <int DT>
+__device__ __forceinline__ uint32_t no_max() {
+  return DT == SPECDEC_F32 ? 0xFF800000u : 0xFF80FF80u;
+}
+template <int DT>
+__device__ __forceinline__ float max_of(uint32_t m) {
+  return DT == SPECDEC_F32 ? __uint_as_float(m) : fmax_nan(bf16_lo(m), bf16_hi(m));
 }
 
 template <int DT>

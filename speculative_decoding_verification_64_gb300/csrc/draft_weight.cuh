@@ -4,8 +4,7 @@
 //
 // With c = log2(e) / T as a pair of floats, x = (l - M) c is cut at the nearest multiple of
 // 2^-10: 2^x = 2^n 2^(j/1024) 2^f with |f| <= 2^-11.  2^(j/1024) comes from a table of
-// pairs, 2^f - 1 = f (ln 2 + f (ln^2 2 / 2 + f ln^3 2 / 6)) with an error of 2^-49.  The
-// difference l c - (M c + n + j / 1024) is one fused multiply-add, so that neither product
+// pairs, 2^f - 1 = f (ln 2 + f ln^2 2 / 2) with an error of 2^-37.  The difference l c - (M c + n + j / 1024) is one fused multiply-add, so that neither product
 // is rounded on its own; M c itself is first rounded to a multiple of 2^-10, which scales
 // all weights of a row alike.
 #pragma once
@@ -35,15 +34,19 @@ constexpr WeightTable make_table() {
   WeightTable t{};
   for (int j = 0; j < kTable; ++j) {
     const double y = exp_series(j * (0.693147180559945309417232121458 / kTable));
-    t.at[j].hi = (float)y;
-    t.at[j].lo = (float)(y - (double)t.at[j].hi);
+    // (the upper part below the value, so that the lower one is positive and both can be
+    // scaled by adding to their exponents)
+    float hi = (float)(y - 0x1p-25);
+    if ((double)hi >= y) hi = (float)(y - 0x1p-23);
+    t.at[j].hi = hi;
+    t.at[j].lo = (float)(y - (double)hi);
   }
   return t;
 }
 
 #ifdef __CUDACC__
 
-constexpr float kFixed = 0x1p42f;  // units of a weight of 1
+constexpr float kFixed = 0x1p42f;  // fixed-point units of a weight of 1
 
 // What a row's weights need.  (No 64-bit arithmetic: this GPU has little of it.)
 struct WeightOf {
@@ -73,48 +76,52 @@ __device__ __forceinline__ WeightOf weight_of(float M, float ch, float cl) {
   return w;
 }
 
-__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+// Two weights, each a + b with a a multiple of 2^-21 and b one of 2^-42 not above 2^-20: as
+// the bits of 6 + a and of 3 * 2^-20 + b, which count those units from kBits6 and kBitsB.
+// (Integer sums of them are exact, and cost less than float32 ones.)
+constexpr uint32_t kBits6 = 0x40C00000u, kBitsB = 0x36400000u;
 
-// Two weights as a + b: a a multiple of 2^-20, b one of 2^-42 and not above 2^-20, so that
-// float32 sums of eight are exact.
-__device__ __forceinline__ void weight2(float2 l, const WeightOf &w, const float2 *table, float2 &a,
-                                        float2 &b) {
-  const float2 ch = both(w.ch), magic = both(w.magic);
+__device__ __forceinline__ void weight2(float2 l, const WeightOf &w, const float2 *table, uint32_t *a,
+                                        uint32_t *b) {
+  const float2 ch = both(w.ch);
   l = __fadd2_rn(l, both(-w.off));
   l = make_float2(fmaxf(l.x, w.least), fmaxf(l.y, w.least));
-  const float2 t = __ffma2_rn(l, ch, magic);  // 12288 + x, rounded to a multiple of 2^-10
-  const float2 at = __fadd2_rn(t, both(-w.magic));
-  float2 f = __ffma2_rn(l, ch, make_float2(-at.x, -at.y));
+  const float2 t = __ffma2_rn(l, ch, both(w.magic));  // 12288 + x, rounded to a multiple of 2^-10
+  const float2 at = __fadd2_rn(both(w.magic), make_float2(-t.x, -t.y));
+  float2 f = __ffma2_rn(l, ch, at);
   f = __ffma2_rn(l, both(w.cl), f);
-  float2 m = __ffma2_rn(f, both(0.0555041087f), both(0.240226507f));
-  m = __ffma2_rn(f, m, both(0.693147181f));
-  m = __fmul2_rn(f, m);
+  // 2^f - 1 to 2^-37
+  const float2 m = __fmul2_rn(f, __ffma2_rn(f, both(0.240226507f), both(0.693147181f)));
   const uint32_t i0 = __float_as_uint(t.x), i1 = __float_as_uint(t.y);
   const float2 t0 = table[i0 & (kTable - 1)], t1 = table[i1 & (kTable - 1)];
   // (the bits of 12288.0 above the index leave nothing in the exponent's place)
   const uint32_t e0 = (i0 << 13) & 0xFF800000u, e1 = (i1 << 13) & 0xFF800000u;
   const float2 hi = make_float2(__uint_as_float(__float_as_uint(t0.x) + e0),
                                 __uint_as_float(__float_as_uint(t1.x) + e1));
-  const float2 s = make_float2(__uint_as_float(0x3F800000u + e0), __uint_as_float(0x3F800000u + e1));
-  const float2 lo = __fmul2_rn(make_float2(t0.y, t1.y), s);
+  const float2 lo = make_float2(__uint_as_float(__float_as_uint(t0.y) + e0),
+                                __uint_as_float(__float_as_uint(t1.y) + e1));
   const float2 v = __ffma2_rn(hi, m, lo);
-  const float2 y = __fadd2_rn(hi, v);
-  const float2 rest = __fadd2_rn(__fadd2_rn(hi, make_float2(-y.x, -y.y)), v);
-  a = __fadd2_rn(__fadd2_rn(y, both(12.0f)), both(-12.0f));
-  b = __fadd2_rn(__fadd2_rn(y, make_float2(-a.x, -a.y)), rest);
-  b = __fadd2_rn(__fadd2_rn(b, both(0x1.8p-19f)), both(-0x1.8p-19f));
+  const float2 y = __fadd2_rn(__fadd2_rn(hi, both(6.0f)), v);
+  // hi - a, with a within 2^-21 of hi + v: exact
+  const float2 d = __fadd2_rn(hi, __fadd2_rn(both(6.0f), make_float2(-y.x, -y.y)));
+  const float2 z = __fadd2_rn(__fadd2_rn(d, v), both(0x1.8p-19f));
+  a[0] = __float_as_uint(y.x);
+  a[1] = __float_as_uint(y.y);
+  b[0] = __float_as_uint(z.x);
+  b[1] = __float_as_uint(z.y);
 }
 
-// a + b in fixed point (whole numbers).
-__device__ __forceinline__ unsigned long long fixed_of(float a, float b) {
-  return (unsigned long long)(__float2ll_rz(a * kFixed) + __float2ll_rz(b * kFixed));
+// The fixed-point sum of n weights from the sums of their bits.
+__device__ __forceinline__ unsigned long long fixed_sum(uint32_t a, uint32_t b, int n) {
+  return ((unsigned long long)(a - (uint32_t)n * kBits6) << 21) +
+         (unsigned long long)(long long)(int32_t)(b - (uint32_t)n * kBitsB);
 }
 
 __device__ __forceinline__ unsigned long long weight_fixed(float l, const WeightOf &w,
                                                            const float2 *table) {
-  float2 a, b;
+  uint32_t a[2], b[2];
   weight2(both(l), w, table, a, b);
-  return fixed_of(a.x, b.x);
+  return fixed_sum(a[0], b[0], 1);
 }
 
 // The least integer that is at least p Z, for p in [0, 1) and Z < 2^63.

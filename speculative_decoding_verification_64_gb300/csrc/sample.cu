@@ -16,8 +16,8 @@
 //     in it; when the cut is inside and the bracket's tokens fit a list, they are sorted and
 //     the cut is found among them.  A bracket that missed is placed anew by what the pass
 //     found, and where that fails, between the places known to hold the cut, halves of them.
-//   * The draws of such rows: the passes leave the kept mass of every run of 32 vectors; a
-//     draw looks its run up, and a warp weighs that run once more.
+//   * The draws of such rows: the passes leave the kept mass of every run of 32 to 128 vectors;
+//     a draw looks its run up, and a warp weighs that run once more.
 // Which token is cut last, or drawn, turns on sums over the vocabulary: weights and sums are
 // those of draft_weight.cuh, as good as 64-bit floating point for this.  The cluster's
 // CTAs exchange a record of a few words at each step.
@@ -54,7 +54,6 @@ struct SampleSmem {
   u64 mine[kMine];
   u64 red[2][kWarps];
   float redf[2][kWarps];
-  float ch, cl;        // log2(e) / T
   double drop;         // T ln(min_p)
   int bracket_bin, bracket_first, bracket_last;
   float bracket_before;
@@ -147,81 +146,106 @@ __device__ __forceinline__ void load_share(const Share &s, const uint8_t *buf, i
   }
 }
 
-// What a pass over the CTA's share found: mass above the cut, in the bracket below it, of
-// everything; tokens above.  (Those in the bracket are counted by sm.n_mine.)
+// What a pass over the CTA's share found: mass down to the bracket, in it, of everything;
+// tokens down to it.  (Those in it are counted by sm.n_mine.)
 struct Found {
   u64 above, in, all;
   int n_above;
 };
 
-// One pass: steps[i] gets the mass above `hi` of the share's vectors 32 i .. 32 i + 31; with
-// kBracket also tokens from `lo` up to `hi`, which go on the list.  Sums of each warp.
-// Tokens between the two values are few where it counts, and looked at one by one.
+// The vectors of a run: 32 steps of a warp at most, so that a lane's sums fit 32 bits.
+__device__ __forceinline__ int run_steps(const Share &s) {
+  return s.nvec > 1024 ? 4 : s.nvec > 512 ? 2 : 1;
+}
+
+// Sums over a warp of lanes' sums of bits (at most 32 weights each).
+__device__ __forceinline__ u64 warp_fixed(uint32_t a, uint32_t b, int n) {
+  a -= (uint32_t)n * kBits6;
+  const int32_t d = (int32_t)(b - (uint32_t)n * kBitsB);
+  const u64 low = __reduce_add_sync(kFull, (uint32_t)d & 0xFFFFu);
+  const int high = __reduce_add_sync(kFull, d >> 16);
+  return ((u64)__reduce_add_sync(kFull, a) << 21) + low + (u64)((long long)high << 16);
+}
+
+// One pass over the share's runs: steps[i] gets run i's mass of the places down to `hi`;
+// with kBracket also the tokens from there down to `lo`, which go on the list, and the mass
+// of everything.  Sums of each warp.  Tokens that equal a bound or lie between are few where
+// it counts, and looked at one by one.
 template <int DT, bool kBracket>
 __device__ __forceinline__ Found weigh(const Share &s, const uint8_t *buf, const WeightOf &w,
                                        const Cut &hi, const Cut &lo, u64 *steps, SampleSmem &sm) {
   constexpr int kN = Elem<DT>::kN;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per = run_steps(s);
   Found f = {0, 0, 0, 0};
-  u64 in = 0, all = 0;
+  u64 in = 0;
   int n_above = 0;
-  const float low = kBracket ? lo.value : hi.value;
-  for (int i = warp; 32 * i < s.nvec; i += kWarps) {
-    const int v = 32 * i + lane;
-    float x[kN];
-    load_share<DT>(s, buf, v, x);
-    float2 sum_a = both(0.0f), sum_z = both(0.0f);  // (a, b) each
-    int n1 = 0, n2 = 0;
-#pragma unroll
-    for (int e = 0; e < kN; e += 2) {
-      float2 a, b;
-      weight2(make_float2(x[e], x[e + 1]), w, sm.table, a, b);
-      if (kBracket) {
-        sum_z = __fadd2_rn(sum_z, make_float2(a.x, b.x));
-        sum_z = __fadd2_rn(sum_z, make_float2(a.y, b.y));
-      }
-      if (x[e] > hi.value) {
-        sum_a = __fadd2_rn(sum_a, make_float2(a.x, b.x));
-        ++n1;
-      }
-      if (x[e + 1] > hi.value) {
-        sum_a = __fadd2_rn(sum_a, make_float2(a.y, b.y));
-        ++n1;
-      }
-      n2 += x[e] >= low;
-      n2 += x[e + 1] >= low;
-    }
-    u64 above = fixed_of(sum_a.x, sum_a.y);
-    if (n2 != n1) {
-      const int at = s.first + v * kN;
+  const float top = hi.value, low = kBracket ? lo.value : hi.value;
+  for (int i = warp; 32 * per * i < s.nvec; i += kWarps) {
+    uint32_t a_sum = 0, b_sum = 0, az_sum = 0, bz_sum = 0;
+    u64 one_by_one = 0;
+    int n = 0, more = 0;
 #pragma unroll 1
-      for (int e = 0; e < kN; ++e) {
-        const float y = get_elem<DT>(buf + (size_t)v * 16 + e * Elem<DT>::kBytes);
-        if (y > hi.value || y < low) continue;
-        const bool kept = hi.holds(y, at + e);
-        if (!kept && (!kBracket || !lo.holds(y, at + e))) continue;
-        const u64 t = weight_fixed(y, w, sm.table);
-        if (kept) {
-          above += t;
-          ++n1;
-        } else {
-          in += t;
-          const int k = atomicAdd(&sm.n_mine, 1);  // (sorted later)
-          if (k < kMine) sm.mine[k] = place_of(y, at + e);
+    for (int q = 0; q < per; ++q) {
+      const int v = 32 * (per * i + q) + lane;
+      float2 x[kN / 2];
+      if (v < s.nvec) {
+        widen2<DT>(*reinterpret_cast<const uint4 *>(buf + (size_t)v * 16), x);
+      } else {
+#pragma unroll
+        for (int e = 0; e < kN / 2; ++e) x[e] = both(-INFINITY);
+      }
+      bool near = false;
+#pragma unroll
+      for (int e = 0; e < kN / 2; ++e) {
+        uint32_t a[2], b[2];
+        weight2(x[e], w, sm.table, a, b);
+        if (kBracket) {
+          az_sum += a[0] + a[1];
+          bz_sum += b[0] + b[1];
+        }
+        const bool k0 = x[e].x > top, k1 = x[e].y > top;
+        if (k0) {
+          a_sum += a[0];
+          b_sum += b[0];
+          ++n;
+        }
+        if (k1) {
+          a_sum += a[1];
+          b_sum += b[1];
+          ++n;
+        }
+        near |= (x[e].x >= low && !k0) || (x[e].y >= low && !k1);
+      }
+      if (near) {
+        const int at = s.first + v * kN;
+#pragma unroll 1
+        for (int e = 0; e < kN; ++e) {
+          const float y = get_elem<DT>(buf + (size_t)v * 16 + e * Elem<DT>::kBytes);
+          if (y > top || y < low) continue;
+          const bool kept = hi.holds(y, at + e);
+          if (!kept && (!kBracket || !lo.holds(y, at + e))) continue;
+          const u64 t = weight_fixed(y, w, sm.table);
+          if (kept) {
+            one_by_one += t;
+            ++more;
+          } else {
+            in += t;
+            const int k = atomicAdd(&sm.n_mine, 1);  // (sorted later)
+            if (k < kMine) sm.mine[k] = place_of(y, at + e);
+          }
         }
       }
     }
-    n_above += n1;
-    const u64 t = warp_sum_u64(above);
+    n_above += n + more;
+    u64 t = warp_fixed(a_sum, b_sum, n);
+    if (__any_sync(kFull, more)) t += warp_sum_u64(one_by_one);
     if (lane == 0) steps[i] = t;
     f.above += t;
-    if (kBracket) all += fixed_of(sum_z.x, sum_z.y);
+    if (kBracket) f.all += warp_fixed(az_sum, bz_sum, per * kN);
   }
   f.n_above = __reduce_add_sync(kFull, n_above);
-  if (kBracket) {
-    f.in = warp_sum_u64(in);
-    f.all = warp_sum_u64(all);
-  }
+  if (kBracket) f.in = warp_sum_u64(in);
   return f;
 }
 
@@ -432,37 +456,31 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleParams 
     top_p = 1.0f;
     min_p = 0.0f;
   }
-  if (warp == 1) {
-    const double c = 1.4426950408889634 / (double)T;
-    const double drop = min_p > 0.0f ? (double)T * log((double)min_p) : 0.0;
-    if (lane == 0) {
-      sm.ch = (float)c;
-      sm.cl = (float)(c - (double)(float)c);
-      sm.drop = drop;
-    }
+  if (warp == 1 && min_p > 0.0f) {
+    const double drop = (double)T * log((double)min_p);
+    if (lane == 0) sm.drop = drop;
   }
+  // log2(e) / T in two parts: the quotient, and what is left of it
+  const float ch = __fdiv_rn(kLog2e, T);
+  const float cl = __fdiv_rn(fmaf(-ch, T, kLog2e) + 1.9259629e-8f, T);
 
   // the largest logit, and the largest of each thread's part of every copy
-  float gm[kChunks];
+  uint32_t top[kChunks];
 #pragma unroll
   for (int i = 0; i < kChunks; ++i) {
-    gm[i] = -INFINITY;
+    top[i] = no_max<DT>();
     share_wait(sm.in, i);
     const int v1 = 1 + chunk_begin(s, i + 1);
-    for (int v = 1 + chunk_begin(s, i) + tid; v < v1; v += kThreads) {
-      float x[kN];
-      widen<DT>(*reinterpret_cast<const uint4 *>(buf + (size_t)v * 16), x);
-#pragma unroll
-      for (int e = 0; e < kN; ++e) gm[i] = fmax_nan(gm[i], x[e]);
-    }
+    for (int v = 1 + chunk_begin(s, i) + tid; v < v1; v += kThreads)
+      top[i] = vector_max<DT>(*reinterpret_cast<const uint4 *>(buf + (size_t)v * 16), top[i]);
   }
   __syncthreads();
-  if (tid < 2) {
-    float x[kN];
-    widen<DT>(*reinterpret_cast<const uint4 *>(buf + (size_t)(tid ? s.nvec - 1 : 0) * 16), x);
+  if (tid < 2)
+    top[0] = vector_max<DT>(
+        *reinterpret_cast<const uint4 *>(buf + (size_t)(tid ? s.nvec - 1 : 0) * 16), top[0]);
+  float gm[kChunks];
 #pragma unroll
-    for (int e = 0; e < kN; ++e) gm[0] = fmax_nan(gm[0], x[e]);
-  }
+  for (int i = 0; i < kChunks; ++i) gm[i] = max_of<DT>(top[i]);
   float M = fmax_nan(fmax_nan(gm[0], gm[1]), fmax_nan(gm[2], gm[3]));
   const int sub = size <= 2 ? 4 : size == 4 ? 2 : 1;  // groups a thread
   const int groups = kThreads * sub * size;
@@ -494,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleParams 
 
   // (from here every CTA of the cluster takes the same branches: they turn on the
   // request's filters and on exchanged records)
-  const WeightOf w = weight_of(M, sm.ch, sm.cl);
+  const WeightOf w = weight_of(M, ch, cl);
   Cut cut = {kLeast, kAll};  // everything but -infinity
   u64 Z = 0;                 // the kept mass
   int kept = 0;
@@ -731,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleParams 
           const u64 q = sm.mine[i];
           if (!cut.holds(place_value(q), place_index(q))) continue;
           const u64 t = weight_fixed(place_value(q), w, sm.table);
-          atomicAdd(&steps[((place_index(q) - s.first) / kN) >> 5], t);
+          atomicAdd(&steps[(place_index(q) - s.first) / kN / (32 * run_steps(s))], t);
           add += t;
         }
         (void)cta_exscan(add, sm.red[0], more);
@@ -764,34 +782,44 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleParams 
       const u64 target = uniform_target(u[d], Z);
       if (target < before || target - before >= mass) continue;
       u64 left = target - before;
-      // the run of 32 vectors: 32 runs at a time
+      // the run: 32 at a time
       int at = -1;
-      const int n_steps = (s.nvec + 31) / 32;
-      for (int i0 = 0; i0 < n_steps && at < 0; i0 += 32) {
-        const u64 t = i0 + lane < n_steps ? steps[i0 + lane] : 0;
+      const int per = run_steps(s), runs = (s.nvec + 32 * per - 1) / (32 * per);
+      for (int i0 = 0; i0 < runs && at < 0; i0 += 32) {
+        const u64 t = i0 + lane < runs ? steps[i0 + lane] : 0;
         const u64 inc = warp_incscan(t);
         const unsigned hit = __ballot_sync(kFull, inc > left);
         if (hit) at = i0 + __ffs(hit) - 1;
         left -= hit ? shfl_u64(inc - t, __ffs(hit) - 1) : shfl_u64(inc, 31);
       }
       // the token: the run's weights once more
-      const int v = 32 * at + lane;
-      float x[kN];
-      load_share<DT>(s, buf, v, x);
-      const int first = s.first + v * kN;
-      u64 t = 0;
-#pragma unroll
-      for (int e = 0; e < kN; ++e)
-        if (cut.holds(x[e], first + e)) t += weight_fixed(x[e], w, sm.table);
-      u64 sum = warp_incscan(t) - t;
-      if (sum <= left && left < sum + t) {
-        int e = 0;
-        for (; e < kN - 1; ++e) {
-          const float y = get_elem<DT>(buf + (size_t)v * 16 + e * es);
-          if (cut.holds(y, first + e)) sum += weight_fixed(y, w, sm.table);
-          if (left < sum) break;
+      for (int q = 0; q < per; ++q) {
+        const int v = 32 * (per * at + q) + lane;
+        const int first = s.first + v * kN;
+        u64 t = 0;
+        if (v < s.nvec) {
+#pragma unroll 1
+          for (int e = 0; e < kN; ++e) {
+            const float y = get_elem<DT>(buf + (size_t)v * 16 + e * es);
+            if (cut.holds(y, first + e)) t += weight_fixed(y, w, sm.table);
+          }
         }
-        tokens[d] = first + e;
+        const u64 inc = warp_incscan(t), whole = shfl_u64(inc, 31);
+        if (left >= whole) {
+          left -= whole;
+          continue;
+        }
+        u64 sum = inc - t;
+        if (sum <= left && left < inc) {
+          int e = 0;
+          for (; e < kN - 1; ++e) {
+            const float y = get_elem<DT>(buf + (size_t)v * 16 + e * es);
+            if (cut.holds(y, first + e)) sum += weight_fixed(y, w, sm.table);
+            if (left < sum) break;
+          }
+          tokens[d] = first + e;
+        }
+        break;
       }
     }
   }
@@ -810,26 +838,58 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleParams 
                    (b * p.rows_at.request + r * p.rows_at.row) * es;
     const bool like =
         ((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0;
-    const float c = temperature_scale(T);
     // 2^rest 2^42 / Z, rounded about once: 1 / Z's error and 2^rest - 1 are small terms
     const float zf = __ull2float_rn(Z), q0 = __fdiv_rn(kFixed, zf);
     const float off = fmaf(-q0, zf, kFixed) / zf - (float)(long long)(Z - __float2ull_rn(zf)) * (q0 / zf);
     const float up = w.rest * fmaf(w.rest, fmaf(w.rest, 0.0555041087f, 0.240226507f), 0.693147181f);
     const float g = q0 + fmaf(q0, up, off);
+    const bool ties = cut.index != kAll;
     __syncthreads();  // (draws read the share)
     for (int v = tid; v < s.nvec; v += kThreads) {
-      float x[kN];
-      load_share<DT>(s, buf, v, x);
-      const int at = s.first + v * kN;
+      const uint4 in = *reinterpret_cast<const uint4 *>(buf + (size_t)v * 16);
+      float2 x[kN / 2];
+      widen2<DT>(in, x);
+      // which elements are kept: a bit each
+      unsigned kept_bits = 0;
 #pragma unroll
-      for (int e = 0; e < kN; ++e) {
-        const bool in = cut.holds(x[e], at + e);
-        if (p.logits)
-          x[e] = st ? __int_as_float(0x7fc00000) : in ? x[e] : -INFINITY;
-        else
-          x[e] = st ? __int_as_float(0x7fc00000) : in ? g * ex2_approx((x[e] - M) * c) : 0.0f;
+      for (int e = 0; e < kN / 2; ++e) {
+        kept_bits |= (x[e].x >= cut.value ? 1u : 0u) << (2 * e);
+        kept_bits |= (x[e].y >= cut.value ? 2u : 0u) << (2 * e);
       }
-      const uint4 y = narrow<DT>(x);
+      if (ties && kept_bits) {
+        const int at = s.first + v * kN;
+#pragma unroll
+        for (int e = 0; e < kN; ++e) {
+          const float y = e & 1 ? x[e / 2].y : x[e / 2].x;
+          if (y == cut.value && at + e > cut.index) kept_bits &= ~(1u << e);
+        }
+      }
+      uint4 y = make_uint4(0u, 0u, 0u, 0u);
+      if (st) {
+#pragma unroll
+        for (int e = 0; e < kN / 2; ++e) x[e] = both(__int_as_float(0x7fc00000));
+        y = narrow2<DT>(x);
+      } else if (p.logits) {
+        uint32_t a[4] = {in.x, in.y, in.z, in.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (DT == SPECDEC_F32) {
+            if (!(kept_bits >> e & 1u)) a[e] = 0xFF800000u;
+          } else {
+            if (!(kept_bits >> (2 * e) & 1u)) a[e] = (a[e] & 0xFFFF0000u) | 0xFF80u;
+            if (!(kept_bits >> (2 * e) & 2u)) a[e] = (a[e] & 0xFFFFu) | 0xFF800000u;
+          }
+        }
+        y = make_uint4(a[0], a[1], a[2], a[3]);
+      } else if (kept_bits) {
+#pragma unroll
+        for (int e = 0; e < kN / 2; ++e) {
+          x[e] = __fmul2_rn(both(g), exp2_pair(x[e], M, ch));
+          if (!(kept_bits >> (2 * e) & 1u)) x[e].x = 0.0f;
+          if (!(kept_bits >> (2 * e) & 2u)) x[e].y = 0.0f;
+        }
+        y = narrow2<DT>(x);
+      }
       if (like)
         store_like<DT>(s, out, v, y);
       else
