@@ -33,8 +33,12 @@ constexpr int kMine = 1024;   // tokens that a CTA can bring
 constexpr int kKeys = 4096;   // groups' maxima (256 of each of 16 CTAs)
 constexpr int kBins = 4096;   // of the histogram
 constexpr float kOctave = 128.0f;  // bins of a factor of two in weight
-constexpr int kBudget = 600;  // tokens of a first bracket on either side
-constexpr int kTries = 3;     // brackets placed by the histogram
+// A bracket reaches to either side of the place that the histogram names by this share of
+// the mass (bins hold their mass to 0.27 %, the sum of many to 0.02 %), or this many tokens
+// where that is less (a value of bfloat16 rows holds some 200 of a flat row), or 32 bins.
+constexpr float kMargin = 0.0025f;
+constexpr int kBudget = 256;
+constexpr int kTries = 2;     // brackets placed by the histogram
 constexpr int kAll = 0x7FFFFFFF;
 constexpr float kLeast = -3.402823466e38f;
 
@@ -58,6 +62,8 @@ struct SampleSmem {
   int bracket_bin, bracket_first, bracket_last;
   float bracket_before;
   unsigned total[16];
+  int count[kWarps];
+  int listed[kMaxCluster];  // tokens on each CTA's list
   int n_mine, n_kept;
   u64 cut[2];
 };
@@ -146,10 +152,10 @@ __device__ __forceinline__ void load_share(const Share &s, const uint8_t *buf, i
   }
 }
 
-// What a pass over the CTA's share found: mass down to the bracket, in it, of everything;
-// tokens down to it.  (Those in it are counted by sm.n_mine.)
+// What a pass over the CTA's share found: mass down to the cut, and of everything; tokens
+// down to the cut.
 struct Found {
-  u64 above, in, all;
+  u64 above, all;
   int n_above;
 };
 
@@ -167,20 +173,31 @@ __device__ __forceinline__ u64 warp_fixed(uint32_t a, uint32_t b, int n) {
   return ((u64)__reduce_add_sync(kFull, a) << 21) + low + (u64)((long long)high << 16);
 }
 
-// One pass over the share's runs: steps[i] gets run i's mass of the places down to `hi`;
-// with kBracket also the tokens from there down to `lo`, which go on the list, and the mass
-// of everything.  Sums of each warp.  Tokens that equal a bound or lie between are few where
-// it counts, and looked at one by one.
-template <int DT, bool kBracket>
+// The next float that orders below x (-infinity below the least finite one).
+__device__ __forceinline__ float just_below(float x) {
+  const uint32_t k = order_key(x) - 1;
+  return key_float(k == 0x7FFFFFFFu ? k - 1 : k);  // (past -0, which orders with 0)
+}
+
+enum Pass {
+  kWhole,   // a cut that takes all tokens of its value
+  kTies,    // one that takes those up to an index
+  kBracket  // also a second cut below the first: the tokens between them go on the list
+};
+
+// One pass over the share's runs: steps[i] gets run i's mass of the places down to `hi`.
+// Sums of each warp.  Tokens of the bounds' values and those between are few where it
+// counts, and looked at one by one.
+template <int DT, Pass kPass>
 __device__ __forceinline__ Found weigh(const Share &s, const uint8_t *buf, const WeightOf &w,
                                        const Cut &hi, const Cut &lo, u64 *steps, SampleSmem &sm) {
   constexpr int kN = Elem<DT>::kN;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per = run_steps(s);
-  Found f = {0, 0, 0, 0};
-  u64 in = 0;
+  Found f = {0, 0, 0};
   int n_above = 0;
-  const float top = hi.value, low = kBracket ? lo.value : hi.value;
+  const float top = hi.index == kAll ? just_below(hi.value) : hi.value;
+  const float low = kPass == kBracket ? lo.value : hi.value;
   for (int i = warp; 32 * per * i < s.nvec; i += kWarps) {
     uint32_t a_sum = 0, b_sum = 0, az_sum = 0, bz_sum = 0;
     u64 one_by_one = 0;
@@ -195,12 +212,12 @@ __device__ __forceinline__ Found weigh(const Share &s, const uint8_t *buf, const
 #pragma unroll
         for (int e = 0; e < kN / 2; ++e) x[e] = both(-INFINITY);
       }
-      bool near = false;
+      unsigned near = 0;
 #pragma unroll
       for (int e = 0; e < kN / 2; ++e) {
         uint32_t a[2], b[2];
         weight2(x[e], w, sm.table, a, b);
-        if (kBracket) {
+        if (kPass == kBracket) {
           az_sum += a[0] + a[1];
           bz_sum += b[0] + b[1];
         }
@@ -215,37 +232,79 @@ __device__ __forceinline__ Found weigh(const Share &s, const uint8_t *buf, const
           b_sum += b[1];
           ++n;
         }
-        near |= (x[e].x >= low && !k0) || (x[e].y >= low && !k1);
+        if (kPass != kWhole) {
+          if (x[e].x >= low && !k0) near |= 1u << (2 * e);
+          if (x[e].y >= low && !k1) near |= 2u << (2 * e);
+        }
       }
-      if (near) {
-        const int at = s.first + v * kN;
-#pragma unroll 1
-        for (int e = 0; e < kN; ++e) {
+      if (kPass != kWhole) {
+        while (near) {
+          const int e = __ffs(near) - 1;
+          near &= near - 1;
           const float y = get_elem<DT>(buf + (size_t)v * 16 + e * Elem<DT>::kBytes);
-          if (y > top || y < low) continue;
-          const bool kept = hi.holds(y, at + e);
-          if (!kept && (!kBracket || !lo.holds(y, at + e))) continue;
-          const u64 t = weight_fixed(y, w, sm.table);
-          if (kept) {
-            one_by_one += t;
+          const int at = s.first + v * kN + e;
+          if (hi.holds(y, at)) {
+            one_by_one += weight_fixed(y, w, sm.table);
             ++more;
-          } else {
-            in += t;
+          } else if (kPass == kBracket && lo.holds(y, at)) {
             const int k = atomicAdd(&sm.n_mine, 1);  // (sorted later)
-            if (k < kMine) sm.mine[k] = place_of(y, at + e);
+            if (k < kMine) sm.mine[k] = place_of(y, at);
           }
         }
       }
     }
     n_above += n + more;
     u64 t = warp_fixed(a_sum, b_sum, n);
-    if (__any_sync(kFull, more)) t += warp_sum_u64(one_by_one);
+    if (kPass != kWhole && __any_sync(kFull, more)) t += warp_sum_u64(one_by_one);
     if (lane == 0) steps[i] = t;
     f.above += t;
-    if (kBracket) f.all += warp_fixed(az_sum, bz_sum, per * kN);
+    if (kPass == kBracket) f.all += warp_fixed(az_sum, bz_sum, per * kN);
   }
   f.n_above = __reduce_add_sync(kFull, n_above);
-  if (kBracket) f.in = warp_sum_u64(in);
+  return f;
+}
+
+// The same, and the sums of the cluster: `mine` gets this CTA's mass, sm.n_mine of `n_in`
+// tokens between the cuts are on its list, and `fits` says that all CTAs' are on theirs.
+template <int DT, Pass kPass>
+__device__ __forceinline__ Found weigh_row(const Share &s, const uint8_t *buf, const WeightOf &w,
+                                           const Cut &hi, const Cut &lo, u64 *steps, int rank,
+                                           int size, int &turn, u64 &mine, u64 &before, int &n_in,
+                                           bool &fits, SampleSmem &sm) {
+  const Found m = weigh<DT, kPass>(s, buf, w, hi, lo, steps, sm);
+  const int warp = threadIdx.x >> 5;
+  __syncthreads();  // (the sums' last readers)
+  if ((threadIdx.x & 31) == 0) {
+    sm.red[0][warp] = m.above;
+    sm.red[1][warp] = m.all;
+    sm.count[warp] = m.n_above;
+  }
+  __syncthreads();
+  u64 rec[kWords] = {0, 0, 0};
+#pragma unroll
+  for (int q = 0; q < kWarps; ++q) {
+    rec[0] += sm.red[0][q];
+    rec[1] += sm.red[1][q];
+    rec[2] += (u64)sm.count[q] << 32;
+  }
+  rec[2] |= (uint32_t)sm.n_mine;
+  mine = rec[0];
+  const u64(*got)[kWords] = exchange(sm.ex, turn, rec, 3, rank, size);
+  Found f = {0, 0, 0};
+  before = 0;
+  n_in = 0;
+  fits = true;
+  for (int q = 0; q < size; ++q) {
+    if (q < rank) before += got[q][0];
+    f.above += got[q][0];
+    f.all += got[q][1];
+    f.n_above += (int)(got[q][2] >> 32);
+    const int here = (int)(uint32_t)got[q][2];
+    if (threadIdx.x == 0) sm.listed[q] = here;
+    n_in += here;
+    fits = fits && here <= kMine;
+  }
+  fits = fits && n_in <= kList;
   return f;
 }
 
@@ -293,7 +352,7 @@ __device__ __forceinline__ void histogram(const Share &s, const uint8_t *buf, fl
 
 // Where the mass of the histogram's first bins reaches `want` (of weights as they stand
 // there; a share of all of it where `share` is set): the bins of a bracket around that
-// place, no more than kBudget tokens and 32 bins to either side, and the mass before them.
+// place, and the mass before them.
 __device__ __forceinline__ void place_bracket(float want, bool share, SampleSmem &sm, int &first,
                                               int &last, float &before) {
   constexpr int kEach = kBins / kThreads;
@@ -347,18 +406,26 @@ __device__ __forceinline__ void place_bracket(float want, bool share, SampleSmem
     }
     unsigned up = at - 1 - lane >= 0 ? sm.bin[at - 1 - lane] : 0;
     unsigned down = at + 1 + lane < kBins ? sm.bin[at + 1 + lane] : 0;
-    float m = (float)up * ex2_approx(-((float)(at - 1 - lane) + 0.5f) / kOctave);
+    const float m_up = (float)up * ex2_approx(-((float)(at - 1 - lane) + 0.5f) / kOctave);
+    float to_up = m_up;
+    float to_down = (float)down * ex2_approx(-((float)(at + 1 + lane) + 0.5f) / kOctave);
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const unsigned y = __shfl_up_sync(kFull, up, d), z = __shfl_up_sync(kFull, down, d);
+      const float f = __shfl_up_sync(kFull, to_up, d), g = __shfl_up_sync(kFull, to_down, d);
       if (lane >= d) {
         up += y;
         down += z;
+        to_up += f;
+        to_down += g;
       }
     }
-    const int n_up = __popc(__ballot_sync(kFull, up <= kBudget && at - 1 - lane >= 0));
-    const int n_down = __popc(__ballot_sync(kFull, down <= kBudget && at + 1 + lane < kBins));
-    if (lane >= n_up) m = 0.0f;
+    // as many bins as stay below both, and the one that passes the margin
+    const float margin = kMargin * whole;
+    const int n_up = min(min(at, 32), 1 + __popc(__ballot_sync(kFull, up <= kBudget && to_up < margin)));
+    const int n_down = min(min(kBins - 1 - at, 32),
+                           1 + __popc(__ballot_sync(kFull, down <= kBudget && to_down < margin)));
+    float m = lane < n_up ? m_up : 0.0f;
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) m += __shfl_xor_sync(kFull, m, d);
     if (lane == 0) {
@@ -391,11 +458,12 @@ __device__ __forceinline__ void gather(const Share &s, const uint8_t *buf, const
   }
 }
 
-// All CTAs' lists, by rank 0; the CTAs' numbers are the lower halves of record word `at`.
-__device__ __forceinline__ int collect(const u64 (*got)[kWords], int word, int size, SampleSmem &sm) {
+// All CTAs' lists, by rank 0, sorted.
+__device__ __forceinline__ int collect(int size, SampleSmem &sm) {
   int all = 0;
+  __syncthreads();  // (their numbers)
   for (int q = 0; q < size; ++q) {
-    const int m = (int)(uint32_t)got[q][word];
+    const int m = sm.listed[q];
     const uint32_t at = cluster_addr(smem_addr(sm.mine), q);
     for (int i = threadIdx.x; i < m; i += kThreads) sm.list[all + i] = remote_get(at + 8u * i);
     all += m;
@@ -546,6 +614,7 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleParams 
       int all = 0;
       bool fits = true;
       for (int q = 0; q < size; ++q) {
+        if (tid == 0) sm.listed[q] = (int)got[q][0];
         all += (int)got[q][0];
         fits = fits && got[q][0] <= kMine;
       }
@@ -559,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleParams 
       __syncthreads();
     }
     if (rank == 0) {
-      const int m = min(k, collect(got, 0, size, sm));
+      const int m = min(k, collect(size, sm));
       // weights of the first k, four a thread, and their sums
       constexpr int kEach = SPECDEC_MAX_TOPK / kThreads;
       u64 wt[kEach], mine = 0, whole;
@@ -637,112 +706,124 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleParams 
     kept = (int)got[0][2];
   } else if (!st) {
     // ---- the whole vocabulary ----------------------------------------------------------
-    bool weighed = false;  // steps[] holds the kept mass
-    u64 mass = 0;          // of this CTA
-    int count = 0;
+    bool weighed = false;    // steps[] holds the kept mass
+    u64 mass = 0, before = 0;  // kept in this CTA, and in those before it
+    int n_in;
+    bool fits;
+    if (floor_value > kLeast) cut = {floor_value, kAll};
     if (top_p < 1.0f) {
-      // less than the wanted mass stands above H, all of it above L: sums are exact, so that
+      // less than the wanted mass stands above H, all of it down to L: sums are exact, so that
       // this holds throughout, and halves end
-      u64 L = (u64)max(order_key(M - 45.0f / w.ch), kLeastKey) << 32, H = over, lo, hi;
+      u64 L = (u64)max(order_key(M - 45.0f / ch), kLeastKey) << 32, H = over, lo, hi;
+      const u64 least = (u64)order_key(cut.value) << 32;  // min_p's cut
+      int n_low = kAll, n_high = 0;                       // tokens down to L and to H
+      float guess = top_p, hist_before;
       Found f;  // of the whole row
-      u64 want = 0;
-      float guess = top_p, before = 0.0f;
-      histogram<DT>(s, buf, M, w.ch, rank, size, sm);
+      u64 want;
+      histogram<DT>(s, buf, M, ch, rank, size, sm);
       for (int tries = 0;; ++tries) {
-        lo = L + (H - L) / 2;  // (L itself where one place is left)
-        hi = H;
         if (tries < kTries) {
           int first, last;
-          place_bracket(guess, tries == 0, sm, first, last, before);
-          const float bin = 1.0f / (w.ch * kOctave);
+          place_bracket(guess, tries == 0, sm, first, last, hist_before);
+          const float bin = 1.0f / (ch * kOctave);
           const u64 from = (u64)max(order_key(M - (float)(last + 1) * bin), kLeastKey) << 32;
           const u64 to = first > 0 ? (u64)order_key(M - (float)first * bin) << 32 : over;
-          // (what the bins say may lie beyond what is known: then halves)
-          if (max(from, L) < min(to, H)) {
-            lo = max(from, L);
-            hi = min(to, H);
-          } else {
-            tries = kTries;
+          lo = max(from, L);
+          hi = min(to, H);
+          if (lo >= hi && tries == 0) {  // (bins finer than the logits: what they weigh, first)
+            lo = L;
+            hi = H;
+          } else if (lo >= hi) {  // (the bins point beyond what is known)
+            tries = kTries - 1;
+            continue;
           }
-        }
-        const Found m = weigh<DT, true>(s, buf, w, cut_at(hi), cut_at(lo), steps, sm);
-        __syncthreads();
-        if (tid < 3) sm.red[0][tid] = 0;
-        if (tid == 3) sm.total[0] = 0;
-        __syncthreads();
-        if (lane == 0) {
-          atomicAdd(&sm.red[0][0], m.above);
-          atomicAdd(&sm.red[0][1], m.in);
-          atomicAdd(&sm.red[0][2], m.all);
-          atomicAdd(&sm.total[0], (unsigned)m.n_above);
-        }
-        __syncthreads();
-        rec[0] = mass = sm.red[0][0];
-        rec[1] = sm.red[0][1];
-        rec[2] = sm.red[0][2];
-        rec[3] = (u64)sm.total[0] << 32 | (uint32_t)sm.n_mine;
-        got = exchange(sm.ex, turn, rec, 4, rank, size);
-        f = {0, 0, 0, 0};
-        int n_in = 0;
-        bool fits = true;
-        for (int q = 0; q < size; ++q) {
-          f.above += got[q][0];
-          f.in += got[q][1];
-          f.all += got[q][2];
-          f.n_above += (int)(got[q][3] >> 32);
-          const int here = (int)(uint32_t)got[q][3];
-          n_in += here;
-          fits = fits && here <= kMine;
-        }
-        fits = fits && n_in <= kList;
-        want = max(share_at_least(top_p, f.all), 1ull);
-        if (want <= f.above) {
-          L = hi;
-        } else if (want > f.above + f.in) {
-          H = lo;
-        } else if (fits) {
-          break;
+        } else if (n_low - n_high <= kMine || H - L <= 1) {
+          lo = L;
+          hi = H;
         } else {
-          L = lo;
+          hi = L + (H - L) / 2;
+          f = weigh_row<DT, kTies>(s, buf, w, cut_at(hi), cut_at(hi), steps, rank, size, turn, mass,
+                                   before, n_in, fits, sm);
+          if (want <= f.above) {
+            L = hi;
+            n_low = f.n_above;
+          } else {
+            H = hi;
+            n_high = f.n_above;
+          }
+          continue;
+        }
+        // a bracket below min_p's cut: all that can be asked is what stands down to that
+        const bool floored = hi <= least;
+        if (floored) lo = hi = min(least, over);
+        f = weigh_row<DT, kBracket>(s, buf, w, cut_at(hi), cut_at(lo), steps, rank, size, turn, mass,
+                                    before, n_in, fits, sm);
+        want = max(share_at_least(top_p, f.all), 1ull);
+        if (want > f.above && floored) {
+          weighed = true;
+          break;
+        }
+        u64 in = 0;
+        if (want > f.above && fits && !floored) {
+          // the list: in place order, up to the one that reaches the mass
+          u64 rec2[kWords];
+          if (rank == 0) {
+            const int all = collect(size, sm);
+            constexpr int kEach = kList / kThreads;
+            u64 wt[kEach], mine = 0;
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+              const int j = tid * kEach + i;
+              wt[i] = j < all ? weight_fixed(place_value(sm.list[j]), w, sm.table) : 0;
+              mine += wt[i];
+            }
+            u64 sum = f.above + cta_exscan(mine, sm.red[1], in);
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+              const int j = tid * kEach + i;
+              if (sum < want && sum + wt[i] >= want) {
+                sm.cut[0] = sm.list[j];
+                sm.cut[1] = (u64)(f.n_above + j + 1);
+              }
+              sum += wt[i];
+            }
+            __syncthreads();
+            rec2[0] = sm.cut[0];
+            rec2[1] = sm.cut[1];
+            rec2[2] = in;
+          }
+          got = exchange(sm.ex, turn, rec2, 3, rank, size);
+          in = got[0][2];
+          if (want <= f.above + in) {
+            cut = cut_at(got[0][0]);
+            kept = (int)got[0][1];
+            break;
+          }
+          H = lo;
+          n_high = f.n_above + n_in;
+        } else if (want > f.above) {
           H = hi;
-          tries = kTries;
+          n_high = f.n_above;
+          tries = kTries;  // (too many for the list)
+        } else {
+          L = hi;
+          n_low = f.n_above;
         }
         // the histogram's mass is off by what the pass shows at the bracket's upper end
         const float unit = ex2_approx(-w.rest) / kFixed;
-        guess = before + ((float)want - (float)f.above) * unit;
+        guess = hist_before + ((float)want - (float)f.above) * unit;
+        // (rank 0's list stands where its histogram was: it is made again)
+        if (tries < kTries - 1) histogram<DT>(s, buf, M, ch, rank, size, sm);
         __syncthreads();
         if (tid == 0) sm.n_mine = 0;
         __syncthreads();
       }
-      if (rank == 0) {
-        const int all = collect(got, 3, size, sm);
-        constexpr int kEach = kList / kThreads;
-        u64 wt[kEach], mine = 0, whole;
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-          const int j = tid * kEach + i;
-          wt[i] = j < all ? weight_fixed(place_value(sm.list[j]), w, sm.table) : 0;
-          mine += wt[i];
-        }
-        u64 sum = f.above + cta_exscan(mine, sm.red[1], whole);
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-          const int j = tid * kEach + i;
-          if (sum < want && sum + wt[i] >= want) {
-            sm.cut[0] = sm.list[j];
-            sm.cut[1] = (u64)(f.n_above + j + 1);
-          }
-          sum += wt[i];
-        }
-        __syncthreads();
-        rec[0] = sm.cut[0];
-        rec[1] = sm.cut[1];
-      }
-      got = exchange(sm.ex, turn, rec, 2, rank, size);
-      cut = cut_at(got[0][0]);
-      kept = (int)got[0][1];
-      weighed = !(floor_value > cut.value);
       if (weighed) {
+        kept = f.n_above;
+        Z = f.above;
+      } else if (floor_value > cut.value) {
+        cut = {floor_value, kAll};
+      } else {
         // the list's kept tokens join their runs
         u64 add = 0, more;
         for (int i = tid; i < sm.n_mine; i += kThreads) {
@@ -754,28 +835,22 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleParams 
         }
         (void)cta_exscan(add, sm.red[0], more);
         mass += more;
+        rec[0] = mass;
+        got = exchange(sm.ex, turn, rec, 1, rank, size);
+        before = 0;
+        for (int q = 0; q < size; ++q) {
+          if (q < rank) before += got[q][0];
+          Z += got[q][0];
+        }
+        weighed = true;
       }
     }
     if (!weighed) {
-      if (floor_value > cut.value) cut = {floor_value, kAll};
-      const Found m = weigh<DT, false>(s, buf, w, cut, cut, steps, sm);
-      u64 total;
-      (void)cta_exscan(lane == 0 ? m.above : 0, sm.red[0], total);
-      mass = total;
-      (void)cta_exscan(lane == 0 ? (u64)m.n_above : 0, sm.red[1], total);
-      count = (int)total;
+      const Found f = weigh_row<DT, kWhole>(s, buf, w, cut, cut, steps, rank, size, turn, mass, before,
+                                            n_in, fits, sm);
+      Z = f.above;
+      kept = f.n_above;
     }
-    rec[0] = mass;
-    rec[1] = (u64)(uint32_t)count;
-    got = exchange(sm.ex, turn, rec, 2, rank, size);
-    u64 before = 0;
-    int c = 0;
-    for (int q = 0; q < size; ++q) {
-      if (q < rank) before += got[q][0];
-      Z += got[q][0];
-      c += (int)got[q][1];
-    }
-    if (!weighed) kept = c;
 
     // the draws that fall into this CTA's mass
     for (int d = warp; d < p.S; d += kWarps) {
@@ -844,51 +919,54 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleParams 
     const float up = w.rest * fmaf(w.rest, fmaf(w.rest, 0.0555041087f, 0.240226507f), 0.693147181f);
     const float g = q0 + fmaf(q0, up, off);
     const bool ties = cut.index != kAll;
+    // kept: above this, and what of the cut's own value the index lets through
+    const float under = ties ? cut.value : just_below(cut.value);
     __syncthreads();  // (draws read the share)
     for (int v = tid; v < s.nvec; v += kThreads) {
       const uint4 in = *reinterpret_cast<const uint4 *>(buf + (size_t)v * 16);
       float2 x[kN / 2];
       widen2<DT>(in, x);
-      // which elements are kept: a bit each
-      unsigned kept_bits = 0;
-#pragma unroll
-      for (int e = 0; e < kN / 2; ++e) {
-        kept_bits |= (x[e].x >= cut.value ? 1u : 0u) << (2 * e);
-        kept_bits |= (x[e].y >= cut.value ? 2u : 0u) << (2 * e);
-      }
-      if (ties && kept_bits) {
-        const int at = s.first + v * kN;
-#pragma unroll
-        for (int e = 0; e < kN; ++e) {
-          const float y = e & 1 ? x[e / 2].y : x[e / 2].x;
-          if (y == cut.value && at + e > cut.index) kept_bits &= ~(1u << e);
-        }
-      }
-      uint4 y = make_uint4(0u, 0u, 0u, 0u);
+      uint4 y;
       if (st) {
 #pragma unroll
         for (int e = 0; e < kN / 2; ++e) x[e] = both(__int_as_float(0x7fc00000));
-        y = narrow2<DT>(x);
       } else if (p.logits) {
-        uint32_t a[4] = {in.x, in.y, in.z, in.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (DT == SPECDEC_F32) {
-            if (!(kept_bits >> e & 1u)) a[e] = 0xFF800000u;
-          } else {
-            if (!(kept_bits >> (2 * e) & 1u)) a[e] = (a[e] & 0xFFFF0000u) | 0xFF80u;
-            if (!(kept_bits >> (2 * e) & 2u)) a[e] = (a[e] & 0xFFFFu) | 0xFF800000u;
+        for (int e = 0; e < kN / 2; ++e)
+          x[e] = make_float2(x[e].x > under ? x[e].x : -INFINITY, x[e].y > under ? x[e].y : -INFINITY);
+      } else {
+        // (most vectors of a row under a filter keep nothing)
+        if (max_of<DT>(vector_max<DT>(in, no_max<DT>())) > under) {
+#pragma unroll
+          for (int e = 0; e < kN / 2; ++e) {
+            const float2 q = __fmul2_rn(both(g), exp2_pair(x[e], M, ch));
+            x[e] = make_float2(x[e].x > under ? q.x : 0.0f, x[e].y > under ? q.y : 0.0f);
           }
-        }
-        y = make_uint4(a[0], a[1], a[2], a[3]);
-      } else if (kept_bits) {
+        } else {
 #pragma unroll
-        for (int e = 0; e < kN / 2; ++e) {
-          x[e] = __fmul2_rn(both(g), exp2_pair(x[e], M, ch));
-          if (!(kept_bits >> (2 * e) & 1u)) x[e].x = 0.0f;
-          if (!(kept_bits >> (2 * e) & 2u)) x[e].y = 0.0f;
+          for (int e = 0; e < kN / 2; ++e) x[e] = both(0.0f);
         }
-        y = narrow2<DT>(x);
+      }
+      y = narrow2<DT>(x);
+      if (ties && !st) {
+        // tokens of the cut's value
+        const int at = s.first + v * kN;
+        const float same = p.logits ? cut.value : g * exp2_pair(both(cut.value), M, ch).x;
+        const uint32_t a[4] = {in.x, in.y, in.z, in.w};
+        uint32_t o[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int e = 0; e < kN; ++e) {
+          const float z = DT == SPECDEC_F32 ? __uint_as_float(a[e & 3])
+                                            : e & 1 ? bf16_hi(a[e >> 1]) : bf16_lo(a[e >> 1]);
+          if (z != cut.value || at + e > cut.index) continue;
+          if (DT == SPECDEC_F32)
+            o[e & 3] = p.logits ? a[e & 3] : __float_as_uint(same);
+          else if (e & 1)
+            o[e >> 1] = (o[e >> 1] & 0xFFFFu) | two_bf16(0.0f, same);
+          else
+            o[e >> 1] = (o[e >> 1] & 0xFFFF0000u) | two_bf16(same, 0.0f);
+        }
+        y = make_uint4(o[0], o[1], o[2], o[3]);
       }
       if (like)
         store_like<DT>(s, out, v, y);

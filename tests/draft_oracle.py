@@ -33,7 +33,8 @@ def keep(x, T, k=0, p=1.0, m=0.0):
                 if run * den >= want:
                     n = i + 1
                     break
-        while n > 1 and m > 0 and w[n - 1] < m:
+        # exp(z) >= m as z >= ln m: a z of -1e-40 is below ln 1, where its exp rounds to 1
+        while n > 1 and m > 0 and (x[order[n - 1]] - x[order[0]]) / T < np.log(m):
             n -= 1
         order, w = order[:n], w[:n]
     kept = np.zeros(len(x))

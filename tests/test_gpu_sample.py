@@ -155,13 +155,31 @@ def test_temperatures_and_offsets(sd, T, offset):
         check(sd, x, [T] * 3, dtype=dtype, k=[0, 50, 0], p=[1.0, 0.9, 0.9])
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_flat_rows_and_rows_of_few_values(sd, dtype):
+    """Borders among thousands of near equal tokens, heavy heads, logits coarser than any bin."""
+    rng = np.random.default_rng(21)
+    V = 40000
+    x = np.stack([rng.standard_normal(V) * 0.01, rng.standard_normal(V) * 3, rng.integers(-3, 4, V) * 1.0,
+                  np.where(np.arange(V) < 3, 12.0, rng.standard_normal(V)), np.linspace(-1, 1, V),
+                  1000 + rng.integers(0, 3, V) * 8.0])[:, None]
+    T = [1.0, 0.7, 0.5, 1.0, 2.0, 2.0 ** -20]
+    for p, m in ((0.9, 0.0), (0.5, 0.0), (0.999, 0.0), (0.95, 0.001), (0.3, 0.9), (0.9, 0.5), (1e-6, 0.0)):
+        check(sd, x, T, dtype=dtype, p=[p] * 6, m=[m] * 6)
+
+
 def test_zeros_of_both_signs_and_denormals(sd):
     x = np.zeros((1, 1, 6000))
     x[0, 0, ::2] = -0.0
     x[0, 0, 1::3] = -1e-40
     x[0, 0, 2::5] = 1e-40
-    for f in (dict(k=[700]), dict(p=[0.4]), dict(p=[0.7]), dict()):
+    for f in (dict(k=[700]), dict(p=[0.4]), dict(p=[0.7]), dict(), dict(m=[1.0])):
         check(sd, x, [1.0], S=4, **f)
+    x[0, 0, 1::2] = -1.0     # the largest is a zero
+    for f in (dict(k=[2000]), dict(p=[0.4]), dict(m=[1.0]), dict(m=[0.9], p=[0.5])):
+        f = {n: [min(v[0], 1000)] for n, v in f.items()}
+        for dtype in ("f32", "bf16"):
+            check(sd, x, [1.0], S=4, dtype=dtype, **f)
 
 
 @pytest.mark.parametrize("S", [0, 1, 63, 64])
