@@ -201,7 +201,8 @@ __device__ __forceinline__ int place_index(unsigned long long p) {
 }
 
 // Sorts list[0, n) downwards: a bitonic network over the next power of two, whose rest is
-// filled with 0 (below every token).
+// filled with 0 (below every token).  Exchanges over up to 32 places stay within a warp's
+// own 64, so that only the wider ones need the CTA's barrier.
 template <int kThreads>
 __device__ __forceinline__ void sort_down(unsigned long long *list, int n) {
   int len = 2;
@@ -218,7 +219,10 @@ __device__ __forceinline__ void sort_down(unsigned long long *list, int n) {
           list[o] = a;
         }
       }
-      __syncthreads();
+      if (j > 32 || (j == 1 && (k > 32 || k == len)))
+        __syncthreads();
+      else
+        __syncwarp();
     }
   }
 }

@@ -31,7 +31,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kList = 2048;   // tokens that rank 0 can sort
 constexpr int kMine = 1024;   // tokens that a CTA can bring
 constexpr int kKeys = 4096;   // groups' maxima (256 of each of 16 CTAs)
-constexpr int kBins = 4096;   // of the histogram
+constexpr int kBins = 2560;   // of the histogram: 20 octaves
 constexpr float kOctave = 128.0f;  // bins of a factor of two in weight
 // A bracket reaches to either side of the place that the histogram names by this share of
 // the mass (bins hold their mass to 0.27 %, the sum of many to 0.02 %), or this many tokens
@@ -39,6 +39,9 @@ constexpr float kOctave = 128.0f;  // bins of a factor of two in weight
 constexpr float kMargin = 0.0025f;
 constexpr int kBudget = 256;
 constexpr int kTries = 2;     // brackets placed by the histogram
+// Halves of 2^64 places, and the brackets before them: no search is longer, and what would
+// be (sums that changed between two passes) ends as SPECDEC_ROW_INTERNAL.
+constexpr int kLimit = 80;
 constexpr int kAll = 0x7FFFFFFF;
 constexpr float kLeast = -3.402823466e38f;
 
@@ -49,7 +52,8 @@ __device__ const WeightTable g_table = make_table();
 struct SampleSmem {
   Exchange ex;
   Arrival in;
-  float2 table[kTable];
+  alignas(8) uint64_t tabled;
+  alignas(16) float2 table[kTable];
   union {
     u64 list[kList];
     uint32_t key[kKeys];
@@ -64,8 +68,9 @@ struct SampleSmem {
   unsigned total[16];
   int count[kWarps];
   int listed[kMaxCluster];  // tokens on each CTA's list
+  float tail[kMaxCluster];  // each CTA's mass below the histogram's bins
   int n_mine, n_kept;
-  u64 cut[2];
+  u64 cut[3];
 };
 
 struct Layout {
@@ -309,7 +314,8 @@ __device__ __forceinline__ Found weigh_row(const Share &s, const uint8_t *buf, c
 }
 
 // The row's histogram, in every CTA: bin j counts the tokens whose weight is 2^(-j / 128) to
-// 2^(-(j + 1) / 128), the last one those below too.
+// 2^(-(j + 1) / 128).  What weighs less than the last bin's is added up instead (there most
+// tokens of a row of text stand, many of one value, and a cut hardly ever).
 template <int DT>
 __device__ __forceinline__ void histogram(const Share &s, const uint8_t *buf, float M, float ch,
                                           int rank, int size, SampleSmem &sm) {
@@ -317,15 +323,33 @@ __device__ __forceinline__ void histogram(const Share &s, const uint8_t *buf, fl
   for (int i = threadIdx.x; i < kBins; i += kThreads) sm.bin[i] = 0;
   __syncthreads();
   const float c = ch * kOctave;
+  float tail = 0.0f;
   for (int v = threadIdx.x; v < s.nvec; v += kThreads) {
-    float x[kN];
-    load_share<DT>(s, buf, v, x);
+    float2 x[kN / 2];
+    widen2<DT>(*reinterpret_cast<const uint4 *>(buf + (size_t)v * 16), x);
 #pragma unroll
-    for (int e = 0; e < kN; ++e) {
-      const float y = fminf((M - x[e]) * c, (float)(kBins - 1));
-      if (x[e] >= kLeast) atomicAdd(&sm.bin[(int)y], 1u);
+    for (int e = 0; e < kN / 2; ++e) {
+      const float2 y = __fmul2_rn(__fadd2_rn(x[e], both(-M)), both(-c));
+      if (y.x < (float)kBins)
+        atomicAdd(&sm.bin[(int)y.x], 1u);
+      else
+        tail += ex2_approx(y.x * (-1.0f / kOctave));
+      if (y.y < (float)kBins)
+        atomicAdd(&sm.bin[(int)y.y], 1u);
+      else
+        tail += ex2_approx(y.y * (-1.0f / kOctave));
     }
   }
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) tail += __shfl_xor_sync(kFull, tail, d);
+  if ((threadIdx.x & 31) == 0) sm.redf[0][threadIdx.x >> 5] = tail;
+  __syncthreads();
+  if ((int)threadIdx.x < size) {
+    tail = 0.0f;
+    for (int q = 0; q < kWarps; ++q) tail += sm.redf[0][q];
+    remote_put(cluster_addr(smem_addr(&sm.tail[rank]), threadIdx.x), __float_as_uint(tail));
+  }
+  __syncwarp();
   cluster_sync();
   // each CTA adds up its part of the bins and, once nobody reads the parts any more, gives
   // the sums to all
@@ -353,7 +377,7 @@ __device__ __forceinline__ void histogram(const Share &s, const uint8_t *buf, fl
 // Where the mass of the histogram's first bins reaches `want` (of weights as they stand
 // there; a share of all of it where `share` is set): the bins of a bracket around that
 // place, and the mass before them.
-__device__ __forceinline__ void place_bracket(float want, bool share, SampleSmem &sm, int &first,
+__device__ __forceinline__ void place_bracket(float want, bool share, int size, SampleSmem &sm, int &first,
                                               int &last, float &before) {
   constexpr int kEach = kBins / kThreads;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -380,7 +404,9 @@ __device__ __forceinline__ void place_bracket(float want, bool share, SampleSmem
     if (q < warp) run += sm.redf[1][q];
     whole += sm.redf[1][q];
   }
-  if (share) want *= whole;
+  float tail = 0.0f;
+  for (int q = 0; q < size; ++q) tail += sm.tail[q];
+  if (share) want *= whole + tail;
   // the first bin whose mass reaches it (rounded sums of neighbours may both, or overlap:
   // the first one, the same in every CTA)
   int at = kBins;
@@ -474,7 +500,7 @@ __device__ __forceinline__ int collect(int size, SampleSmem &sm) {
 }
 
 template <int DT>
-__global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleParams p, int vectors) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams p, int vectors) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
   constexpr int es = Elem<DT>::kBytes, kN = Elem<DT>::kN;
   SampleSmem &sm = *reinterpret_cast<SampleSmem *>(smem_raw);
@@ -488,25 +514,26 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleParams 
   const int r = (int)(n - b * p.R);
   int turn = 0;
 
+  const uint8_t *row = reinterpret_cast<const uint8_t *>(p.x) +
+                       (b * p.x_at.request + r * p.x_at.row) * es;
+  const Share s = share_of<DT>(row, p.V, rank, size);
   if (tid == 0) {
     for (int i = 0; i < kChunks; ++i) mbar_init(&sm.in.full[i], 1);
+    mbar_init(&sm.tabled, 1);
     sm.in.gave_up = 0;
     sm.n_mine = 0;
     fence_mbar_init();
+    // (the table is no kernel's output)
+    mbar_arrive_expect_tx(&sm.tabled, (uint32_t)sizeof(sm.table));
+    bulk_copy_g2s(sm.table, &g_table, (uint32_t)sizeof(sm.table), &sm.tabled);
   }
   if (tid < 16) sm.total[tid] = 0;
   pdl_wait();
   pdl_launch_dependents();
+  if (tid == 0) share_copy(s, buf, sm.in);
   cluster_arrive();
   __syncthreads();
-
-  const uint8_t *row = reinterpret_cast<const uint8_t *>(p.x) +
-                       (b * p.x_at.request + r * p.x_at.row) * es;
-  const Share s = share_of<DT>(row, p.V, rank, size);
-  if (tid == 0) share_copy(s, buf, sm.in);
   share_edges<DT>(s, row, buf);
-  for (int i = tid; i < kTable; i += kThreads)
-    sm.table[i] = make_float2(g_table.at[i].hi, g_table.at[i].lo);
 
   // the request's filters
   float T = p.temperature[b];
@@ -542,6 +569,7 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleParams 
     for (int v = 1 + chunk_begin(s, i) + tid; v < v1; v += kThreads)
       top[i] = vector_max<DT>(*reinterpret_cast<const uint4 *>(buf + (size_t)v * 16), top[i]);
   }
+  if (!mbar_wait_bounded(&sm.tabled, 0, kConsumerWaitNs)) sm.in.gave_up = 1;
   __syncthreads();
   if (tid < 2)
     top[0] = vector_max<DT>(
@@ -606,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleParams 
     // places >= H.  Where those at `from` are too many to list, halves of what is between:
     // at the end exactly k.
     u64 from = (u64)max(bound << 16, kLeastKey) << 32, H = over, probe = from;
-    for (;;) {
+    for (int i = 0;; ++i) {
       gather<DT>(s, buf, cut_at(probe), sm);
       __syncthreads();
       rec[0] = (u64)(uint32_t)sm.n_mine;
@@ -620,6 +648,10 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleParams 
       }
       const bool enough = probe == from || all >= k;
       if (enough && fits && all <= kList) break;
+      if (i == kLimit) {
+        st = SPECDEC_ROW_INTERNAL;
+        break;
+      }
       if (enough) from = probe;
       else H = probe;
       probe = from + (H - from) / 2;
@@ -627,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleParams 
       if (tid == 0) sm.n_mine = 0;
       __syncthreads();
     }
-    if (rank == 0) {
+    if (rank == 0 && !st) {
       const int m = min(k, collect(size, sm));
       // weights of the first k, four a thread, and their sums
       constexpr int kEach = SPECDEC_MAX_TOPK / kThreads;
@@ -722,9 +754,13 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleParams 
       u64 want;
       histogram<DT>(s, buf, M, ch, rank, size, sm);
       for (int tries = 0;; ++tries) {
+        if (tries == kLimit) {
+          st = SPECDEC_ROW_INTERNAL;
+          break;
+        }
         if (tries < kTries) {
           int first, last;
-          place_bracket(guess, tries == 0, sm, first, last, hist_before);
+          place_bracket(guess, tries == 0, size, sm, first, last, hist_before);
           const float bin = 1.0f / (ch * kOctave);
           const u64 from = (u64)max(order_key(M - (float)(last + 1) * bin), kLeastKey) << 32;
           const u64 to = first > 0 ? (u64)order_key(M - (float)first * bin) << 32 : over;
@@ -784,19 +820,22 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleParams 
               if (sum < want && sum + wt[i] >= want) {
                 sm.cut[0] = sm.list[j];
                 sm.cut[1] = (u64)(f.n_above + j + 1);
+                sm.cut[2] = sum + wt[i];
               }
               sum += wt[i];
             }
             __syncthreads();
             rec2[0] = sm.cut[0];
             rec2[1] = sm.cut[1];
-            rec2[2] = in;
+            rec2[2] = sm.cut[2];
+            rec2[3] = in;
           }
-          got = exchange(sm.ex, turn, rec2, 3, rank, size);
-          in = got[0][2];
+          got = exchange(sm.ex, turn, rec2, 4, rank, size);
+          in = got[0][3];
           if (want <= f.above + in) {
             cut = cut_at(got[0][0]);
             kept = (int)got[0][1];
+            Z = got[0][2];
             break;
           }
           H = lo;
@@ -818,11 +857,15 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleParams 
         if (tid == 0) sm.n_mine = 0;
         __syncthreads();
       }
-      if (weighed) {
+      if (st) {
+        weighed = true;
+      } else if (weighed) {
         kept = f.n_above;
         Z = f.above;
       } else if (floor_value > cut.value) {
         cut = {floor_value, kAll};
+      } else if (p.S == 0) {
+        weighed = true;
       } else {
         // the list's kept tokens join their runs
         u64 add = 0, more;
@@ -838,10 +881,7 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleParams 
         rec[0] = mass;
         got = exchange(sm.ex, turn, rec, 1, rank, size);
         before = 0;
-        for (int q = 0; q < size; ++q) {
-          if (q < rank) before += got[q][0];
-          Z += got[q][0];
-        }
+        for (int q = 0; q < rank; ++q) before += got[q][0];
         weighed = true;
       }
     }
@@ -853,7 +893,7 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleParams 
     }
 
     // the draws that fall into this CTA's mass
-    for (int d = warp; d < p.S; d += kWarps) {
+    for (int d = warp; d < p.S && !st; d += kWarps) {
       const u64 target = uniform_target(u[d], Z);
       if (target < before || target - before >= mass) continue;
       u64 left = target - before;
@@ -871,14 +911,28 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleParams 
       for (int q = 0; q < per; ++q) {
         const int v = 32 * (per * at + q) + lane;
         const int first = s.first + v * kN;
-        u64 t = 0;
+        uint32_t a_sum = 0, b_sum = 0;
+        int n = 0;
         if (v < s.nvec) {
-#pragma unroll 1
-          for (int e = 0; e < kN; ++e) {
-            const float y = get_elem<DT>(buf + (size_t)v * 16 + e * es);
-            if (cut.holds(y, first + e)) t += weight_fixed(y, w, sm.table);
+          float2 x[kN / 2];
+          widen2<DT>(*reinterpret_cast<const uint4 *>(buf + (size_t)v * 16), x);
+#pragma unroll
+          for (int e = 0; e < kN / 2; ++e) {
+            uint32_t a[2], c[2];
+            weight2(x[e], w, sm.table, a, c);
+            if (cut.holds(x[e].x, first + 2 * e)) {
+              a_sum += a[0];
+              b_sum += c[0];
+              ++n;
+            }
+            if (cut.holds(x[e].y, first + 2 * e + 1)) {
+              a_sum += a[1];
+              b_sum += c[1];
+              ++n;
+            }
           }
         }
+        const u64 t = fixed_sum(a_sum, b_sum, n);
         const u64 inc = warp_incscan(t), whole = shfl_u64(inc, 31);
         if (left >= whole) {
           left -= whole;
@@ -978,7 +1032,10 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleParams 
       store_unlike<DT, kThreads>(s, buf, out);
     }
   }
-  if (sm.in.gave_up && tid == 0) share_drain(sm.in);
+  if (sm.in.gave_up && tid == 0) {
+    share_drain(sm.in);
+    mbar_wait_bounded(&sm.tabled, 0);
+  }
 }
 
 template <int DT>
@@ -988,7 +1045,7 @@ cudaError_t launch_dt(const SampleParams &p, cudaStream_t stream) {
   if (err != cudaSuccess) return err;
   constexpr int es = Elem<DT>::kBytes;
   const long long rows = (long long)p.B * p.R;
-  const int size = cluster_for(rows, p.V, es, 36 * 1024, 3);
+  const int size = cluster_for(rows, p.V, es, 68 * 1024, 2);
   const int vectors = share_vectors(p.V, es, size);
   return launch_clusters(sample_kernel<DT>, rows, size, kThreads, layout_of(vectors).total, stream, p,
                          vectors);
