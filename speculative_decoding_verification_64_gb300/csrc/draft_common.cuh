@@ -267,9 +267,15 @@ __device__ __forceinline__ unsigned long long remote_get(uint32_t addr) {
   return v;
 }
 
+// (one of many that may be under way together, between two barriers of the cluster)
+__device__ __forceinline__ unsigned long long remote_get_weak(uint32_t addr) {
+  unsigned long long v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr));
+  return v;
+}
 __device__ __forceinline__ uint32_t remote_get32(uint32_t addr) {
   uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr));
   return v;
 }
 

@@ -31,7 +31,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kList = 2048;   // tokens that rank 0 can sort
 constexpr int kMine = 1024;   // tokens that a CTA can bring
 constexpr int kKeys = 4096;   // groups' maxima (256 of each of 16 CTAs)
-constexpr int kBins = 2560;   // of the histogram: 20 octaves
+constexpr int kBins = 23 * 128;  // of the histogram: 23 octaves
 constexpr float kOctave = 128.0f;  // bins of a factor of two in weight
 // A bracket reaches to either side of the place that the histogram names by this share of
 // the mass (bins hold their mass to 0.27 %, the sum of many to 0.02 %), or this many tokens
@@ -57,18 +57,18 @@ struct SampleSmem {
   union {
     u64 list[kList];
     uint32_t key[kKeys];
-    uint32_t bin[kBins];
+    uint32_t bin[kBins + 32];
   };
   u64 mine[kMine];
   u64 red[2][kWarps];
   float redf[2][kWarps];
   double drop;         // T ln(min_p)
+  float piece[64], whole;   // of the histogram's mass
   int bracket_bin, bracket_first, bracket_last;
   float bracket_before;
   unsigned total[16];
   int count[kWarps];
   int listed[kMaxCluster];  // tokens on each CTA's list
-  float tail[kMaxCluster];  // each CTA's mass below the histogram's bins
   int n_mine, n_kept;
   u64 cut[3];
 };
@@ -313,111 +313,107 @@ __device__ __forceinline__ Found weigh_row(const Share &s, const uint8_t *buf, c
   return f;
 }
 
-// The row's histogram, in every CTA: bin j counts the tokens whose weight is 2^(-j / 128) to
-// 2^(-(j + 1) / 128).  What weighs less than the last bin's is added up instead (there most
-// tokens of a row of text stand, many of one value, and a cut hardly ever).
+__device__ __forceinline__ void count_bin(uint32_t at) {
+  asm volatile("red.shared::cta.add.u32 [%0], 1;" ::"r"(at) : "memory");
+}
+
+// A histogram of the CTA's tokens: bin j counts those whose weight is within half a bin of
+// 2^(-j / 128).  The lighter ones go to places of their own, one a lane (there most tokens
+// of a row of text stand, many of one value).  The bin's number is read off the bits of
+// 2^23 + j.  Ends with the cluster's barrier.
 template <int DT>
 __device__ __forceinline__ void histogram(const Share &s, const uint8_t *buf, float M, float ch,
-                                          int rank, int size, SampleSmem &sm) {
+                                          SampleSmem &sm) {
   constexpr int kN = Elem<DT>::kN;
   for (int i = threadIdx.x; i < kBins; i += kThreads) sm.bin[i] = 0;
   __syncthreads();
-  const float c = ch * kOctave;
-  float tail = 0.0f;
+  const float2 c = both(-ch * kOctave), one = both(8388608.0f);
+  const uint32_t base = smem_addr(sm.bin);
+  const uint32_t rest = kBins + (threadIdx.x & 31);
   for (int v = threadIdx.x; v < s.nvec; v += kThreads) {
     float2 x[kN / 2];
     widen2<DT>(*reinterpret_cast<const uint4 *>(buf + (size_t)v * 16), x);
 #pragma unroll
     for (int e = 0; e < kN / 2; ++e) {
-      const float2 y = __fmul2_rn(__fadd2_rn(x[e], both(-M)), both(-c));
-      if (y.x < (float)kBins)
-        atomicAdd(&sm.bin[(int)y.x], 1u);
-      else
-        tail += ex2_approx(y.x * (-1.0f / kOctave));
-      if (y.y < (float)kBins)
-        atomicAdd(&sm.bin[(int)y.y], 1u);
-      else
-        tail += ex2_approx(y.y * (-1.0f / kOctave));
+      const float2 y = __ffma2_rn(__fadd2_rn(x[e], both(-M)), c, one);
+      count_bin(base + 4 * min(__float_as_uint(y.x) - 0x4B000000u, rest));
+      count_bin(base + 4 * min(__float_as_uint(y.y) - 0x4B000000u, rest));
     }
-  }
-#pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) tail += __shfl_xor_sync(kFull, tail, d);
-  if ((threadIdx.x & 31) == 0) sm.redf[0][threadIdx.x >> 5] = tail;
-  __syncthreads();
-  if ((int)threadIdx.x < size) {
-    tail = 0.0f;
-    for (int q = 0; q < kWarps; ++q) tail += sm.redf[0][q];
-    remote_put(cluster_addr(smem_addr(&sm.tail[rank]), threadIdx.x), __float_as_uint(tail));
-  }
-  __syncwarp();
-  cluster_sync();
-  // each CTA adds up its part of the bins and, once nobody reads the parts any more, gives
-  // the sums to all
-  const int per = kBins / size;
-  uint32_t sum[kBins / kThreads];
-#pragma unroll
-  for (int i = 0; i < kBins / kThreads; ++i) {
-    const int j = threadIdx.x + i * kThreads;
-    sum[i] = 0;
-    if (j >= per) continue;
-    for (int q = 0; q < size; ++q)
-      sum[i] += remote_get32(cluster_addr(smem_addr(&sm.bin[rank * per + j]), q));
-  }
-  cluster_sync();
-#pragma unroll
-  for (int i = 0; i < kBins / kThreads; ++i) {
-    const int j = threadIdx.x + i * kThreads;
-    if (j >= per) continue;
-    for (int q = 0; q < size; ++q)
-      remote_put(cluster_addr(smem_addr(&sm.bin[rank * per + j]), q), sum[i]);
   }
   cluster_sync();
 }
 
-// Where the mass of the histogram's first bins reaches `want` (of weights as they stand
-// there; a share of all of it where `share` is set): the bins of a bracket around that
-// place, and the mass before them.
-__device__ __forceinline__ void place_bracket(float want, bool share, int size, SampleSmem &sm, int &first,
-                                              int &last, float &before) {
-  constexpr int kEach = kBins / kThreads;
+// Where the mass of the cluster's histograms reaches `want` in their first bins (of weights
+// as they stand there; a share of all of it where `share` is set): the bins of a bracket
+// around that place, and the mass before them.  The same in every CTA.
+__device__ __forceinline__ void place_bracket(float want, bool share, int size, SampleSmem &sm,
+                                              int &first, int &last, float &before) {
+  // pairs of bins a thread, those of a warp's threads next to one another
+  constexpr int kEach = (kBins / 2 + kThreads - 1) / kThreads;
+  static_assert(kBins % 64 == 0, "whole warps of pairs");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  float mass[kEach], mine = 0.0f;
+  const uint32_t bins = smem_addr(sm.bin);
+  // weight of bin j
+  auto weight = [](int j) { return ex2_approx((float)j * (-1.0f / kOctave)); };
+  u64 n[kEach];  // (counts of a row fit half of a word)
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) n[i] = 0;
+#pragma unroll 4
+  for (int q = 0; q < size; ++q) {
+    const uint32_t at = cluster_addr(bins, q);
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int j = i * kThreads + tid;
+      if (j < kBins / 2) n[i] += remote_get_weak(at + 8u * j);
+    }
+  }
+  __syncthreads();  // (the last readers of what follows)
+  float inc[kEach];  // mass of the warp's bins up to this thread's
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
-    const int j = tid * kEach + i;
-    mass[i] = (float)sm.bin[j] * ex2_approx(-((float)j + 0.5f) / kOctave);
-    mine += mass[i];
-  }
-  float inc = mine;
+    const int j = 2 * (i * kThreads + tid);
+    inc[i] = (float)(uint32_t)n[i] * weight(j) + (float)(uint32_t)(n[i] >> 32) * weight(j + 1);
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const float y = __shfl_up_sync(kFull, inc, d);
-    if (lane >= d) inc += y;
+    for (int d = 1; d < 32; d <<= 1) {
+      const float y = __shfl_up_sync(kFull, inc[i], d);
+      if (lane >= d) inc[i] += y;
+    }
+    if (lane == 31) sm.piece[i * kWarps + warp] = inc[i];
   }
-  __syncthreads();
-  if (lane == 31) sm.redf[1][warp] = inc;
   if (tid == 0) sm.bracket_bin = kBins;
   __syncthreads();
-  float run = inc - mine, whole = 0.0f;
+  if (warp == 0) {
+    // the pieces' sums, two a lane
+    static_assert(kEach * kWarps <= 64, "two pieces a lane");
+    const float p0 = 2 * lane < kEach * kWarps ? sm.piece[2 * lane] : 0.0f;
+    const float p1 = 2 * lane + 1 < kEach * kWarps ? sm.piece[2 * lane + 1] : 0.0f;
+    float sum = p0 + p1;
 #pragma unroll
-  for (int q = 0; q < kWarps; ++q) {
-    if (q < warp) run += sm.redf[1][q];
-    whole += sm.redf[1][q];
+    for (int d = 1; d < 32; d <<= 1) {
+      const float y = __shfl_up_sync(kFull, sum, d);
+      if (lane >= d) sum += y;
+    }
+    sm.piece[2 * lane] = sum - p1 - p0;
+    sm.piece[2 * lane + 1] = sum - p1;
+    if (lane == 31) sm.whole = sum;
   }
-  float tail = 0.0f;
-  for (int q = 0; q < size; ++q) tail += sm.tail[q];
-  if (share) want *= whole + tail;
+  __syncthreads();
+  const float whole = sm.whole;
+  if (share) want *= whole;
   // the first bin whose mass reaches it (rounded sums of neighbours may both, or overlap:
   // the first one, the same in every CTA)
   int at = kBins;
   float b = 0.0f;
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
-    if (at == kBins && mass[i] > 0.0f && run + mass[i] >= want) {
-      at = tid * kEach + i;
-      b = run;
+    const int j = 2 * (i * kThreads + tid);
+    const float m0 = (float)(uint32_t)n[i] * weight(j), m1 = (float)(uint32_t)(n[i] >> 32) * weight(j + 1);
+    const float to = sm.piece[i * kWarps + warp] + inc[i];
+    if (at == kBins && m0 + m1 > 0.0f && to >= want) {
+      const bool second = m0 == 0.0f || (m1 > 0.0f && to - m1 < want);
+      at = second ? j + 1 : j;
+      b = second ? to - m1 : to - m1 - m0;
     }
-    run += mass[i];
   }
   if (at < kBins) atomicMin(&sm.bracket_bin, at);
   __syncthreads();
@@ -430,14 +426,18 @@ __device__ __forceinline__ void place_bracket(float want, bool share, int size, 
       at = kBins - 1;
       b = whole;
     }
-    unsigned up = at - 1 - lane >= 0 ? sm.bin[at - 1 - lane] : 0;
-    unsigned down = at + 1 + lane < kBins ? sm.bin[at + 1 + lane] : 0;
-    const float m_up = (float)up * ex2_approx(-((float)(at - 1 - lane) + 0.5f) / kOctave);
-    float to_up = m_up;
-    float to_down = (float)down * ex2_approx(-((float)(at + 1 + lane) + 0.5f) / kOctave);
+    const int j_up = at - 1 - lane, j_down = at + 1 + lane;
+    uint32_t up = 0, down = 0;
+    for (int q = 0; q < size; ++q) {
+      const uint32_t from = cluster_addr(bins, q);
+      if (j_up >= 0) up += remote_get32(from + 4u * j_up);
+      if (j_down < kBins) down += remote_get32(from + 4u * j_down);
+    }
+    const float m_up = (float)up * weight(j_up);
+    float to_up = m_up, to_down = (float)down * weight(j_down);
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const unsigned y = __shfl_up_sync(kFull, up, d), z = __shfl_up_sync(kFull, down, d);
+      const uint32_t y = __shfl_up_sync(kFull, up, d), z = __shfl_up_sync(kFull, down, d);
       const float f = __shfl_up_sync(kFull, to_up, d), g = __shfl_up_sync(kFull, to_down, d);
       if (lane >= d) {
         up += y;
@@ -486,13 +486,13 @@ __device__ __forceinline__ void gather(const Share &s, const uint8_t *buf, const
 
 // All CTAs' lists, by rank 0, sorted.
 __device__ __forceinline__ int collect(int size, SampleSmem &sm) {
-  int all = 0;
   __syncthreads();  // (their numbers)
-  for (int q = 0; q < size; ++q) {
-    const int m = sm.listed[q];
-    const uint32_t at = cluster_addr(smem_addr(sm.mine), q);
-    for (int i = threadIdx.x; i < m; i += kThreads) sm.list[all + i] = remote_get(at + 8u * i);
-    all += m;
+  int all = 0;
+  for (int q = 0; q < size; ++q) all += sm.listed[q];
+  for (int i = threadIdx.x; i < all; i += kThreads) {
+    int q = 0, at = i;
+    while (at >= sm.listed[q]) at -= sm.listed[q++];
+    sm.list[i] = remote_get(cluster_addr(smem_addr(&sm.mine[at]), q));
   }
   __syncthreads();
   sort_down<kThreads>(sm.list, all);
@@ -531,15 +531,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   pdl_wait();
   pdl_launch_dependents();
   if (tid == 0) share_copy(s, buf, sm.in);
-  cluster_arrive();
-  __syncthreads();
-  share_edges<DT>(s, row, buf);
-
   // the request's filters
   float T = p.temperature[b];
   int k = p.top_k ? p.top_k[b] : 0;
   float top_p = p.top_p ? p.top_p[b] : 1.0f;
   float min_p = p.min_p ? p.min_p[b] : 0.0f;
+  cluster_arrive();
+  __syncthreads();
+  share_edges<DT>(s, row, buf);
+
   int st = 0;
   if (!temperature_valid(T)) st |= SPECDEC_ROW_BAD_TEMP;
   if (k < 0 || k > SPECDEC_MAX_TOPK || !(top_p >= 0.0f && top_p <= 1.0f) ||
@@ -663,11 +663,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       const int m = min(k, collect(size, sm));
       // weights of the first k, four a thread, and their sums
       constexpr int kEach = SPECDEC_MAX_TOPK / kThreads;
+      const int each = (m + kThreads - 1) / kThreads;  // of neighbours, a thread
       u64 wt[kEach], mine = 0, whole;
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
-        const int j = tid * kEach + i;
-        wt[i] = j < m ? weight_fixed(place_value(sm.list[j]), w, sm.table) : 0;
+        const int j = tid * each + i;
+        wt[i] = i < each && j < m ? weight_fixed(place_value(sm.list[j]), w, sm.table) : 0;
         mine += wt[i];
       }
       u64 before = cta_exscan(mine, sm.red[0], whole);
@@ -677,8 +678,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       u64 sum = before;
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
-        const int j = tid * kEach + i;
-        c += j < m && (sum < want || j == 0) && place_value(sm.list[j]) >= floor_value;
+        const int j = tid * each + i;
+        c += i < each && j < m && (sum < want || j == 0) && place_value(sm.list[j]) >= floor_value;
         sum += wt[i];
       }
       if (tid == 0) sm.n_kept = 0;
@@ -691,13 +692,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       sum = before;
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
-        const int j = tid * kEach + i;
+        const int j = tid * each + i;
         sum += wt[i];
-        if (j == nk - 1) {
+        if (i < each && j == nk - 1) {
           sm.cut[0] = sm.list[j];
           sm.cut[1] = sum;
         }
-        if (j < nk) sm.mine[j] = wt[i];
+        if (i < each && j < nk) sm.mine[j] = wt[i];
       }
       __syncthreads();
       Z = sm.cut[1];
@@ -714,10 +715,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         mine = 0;
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
-          const int j = tid * kEach + i;
-          const u64 q = j < nk ? sm.list[j] : 0;
+          const int j = tid * each + i;
+          const u64 q = i < each && j < nk ? sm.list[j] : 0;
           token[i] = (int)(0xFFFFFFFFu - (uint32_t)(q >> 32));
-          wt[i] = j < nk ? sm.mine[(uint32_t)q] : 0;
+          wt[i] = i < each && j < nk ? sm.mine[(uint32_t)q] : 0;
           mine += wt[i];
         }
         before = cta_exscan(mine, sm.red[1], whole);
@@ -752,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       float guess = top_p, hist_before;
       Found f;  // of the whole row
       u64 want;
-      histogram<DT>(s, buf, M, ch, rank, size, sm);
+      histogram<DT>(s, buf, M, ch, sm);
       for (int tries = 0;; ++tries) {
         if (tries == kLimit) {
           st = SPECDEC_ROW_INTERNAL;
@@ -762,8 +763,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
           int first, last;
           place_bracket(guess, tries == 0, size, sm, first, last, hist_before);
           const float bin = 1.0f / (ch * kOctave);
-          const u64 from = (u64)max(order_key(M - (float)(last + 1) * bin), kLeastKey) << 32;
-          const u64 to = first > 0 ? (u64)order_key(M - (float)first * bin) << 32 : over;
+          const u64 from = (u64)max(order_key(M - ((float)last + 0.5f) * bin), kLeastKey) << 32;
+          const u64 to = first > 0 ? (u64)order_key(M - ((float)first - 0.5f) * bin) << 32 : over;
           lo = max(from, L);
           hi = min(to, H);
           if (lo >= hi && tries == 0) {  // (bins finer than the logits: what they weigh, first)
@@ -806,17 +807,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
           if (rank == 0) {
             const int all = collect(size, sm);
             constexpr int kEach = kList / kThreads;
+            const int each = (all + kThreads - 1) / kThreads;  // of neighbours, a thread
             u64 wt[kEach], mine = 0;
 #pragma unroll
             for (int i = 0; i < kEach; ++i) {
-              const int j = tid * kEach + i;
-              wt[i] = j < all ? weight_fixed(place_value(sm.list[j]), w, sm.table) : 0;
+              const int j = tid * each + i;
+              wt[i] = i < each && j < all ? weight_fixed(place_value(sm.list[j]), w, sm.table) : 0;
               mine += wt[i];
             }
             u64 sum = f.above + cta_exscan(mine, sm.red[1], in);
 #pragma unroll
             for (int i = 0; i < kEach; ++i) {
-              const int j = tid * kEach + i;
+              const int j = tid * each + i;
               if (sum < want && sum + wt[i] >= want) {
                 sm.cut[0] = sm.list[j];
                 sm.cut[1] = (u64)(f.n_above + j + 1);
@@ -852,7 +854,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         const float unit = ex2_approx(-w.rest) / kFixed;
         guess = hist_before + ((float)want - (float)f.above) * unit;
         // (rank 0's list stands where its histogram was: it is made again)
-        if (tries < kTries - 1) histogram<DT>(s, buf, M, ch, rank, size, sm);
+        if (tries < kTries - 1) histogram<DT>(s, buf, M, ch, sm);
         __syncthreads();
         if (tid == 0) sm.n_mine = 0;
         __syncthreads();
