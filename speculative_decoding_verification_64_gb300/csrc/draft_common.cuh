@@ -261,6 +261,11 @@ __device__ __forceinline__ void remote_put(uint32_t addr, unsigned long long v) 
 __device__ __forceinline__ void remote_put(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
+__device__ __forceinline__ void remote_put16(uint32_t addr, uint32_t v) {
+  asm volatile("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tst.shared::cluster.u16 [%0], h;\n\t}" ::"r"(addr),
+               "r"(v)
+               : "memory");
+}
 __device__ __forceinline__ unsigned long long remote_get(uint32_t addr) {
   unsigned long long v;
   asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
@@ -492,9 +497,11 @@ __device__ __forceinline__ void store_like(const Share &s, uint8_t *row, int v, 
 // an SM, more where the rows leave SMs idle, none with less than 4 KB to do.
 inline int cluster_for(long long rows, int V, int elem_bytes, int share_bytes, int per_sm) {
   int c = 1;
-  while (c < kMaxCluster && (long long)V * elem_bytes > (long long)c * share_bytes) c *= 2;
+  while (c < kMaxCluster && (long long)V * elem_bytes > (long long)c * share_bytes)
+    c = c < 8 ? c + 1 : kMaxCluster;
   const long long slots = (long long)device_sm_count() * per_sm;
-  while (c < kMaxCluster && rows * c * 2 <= slots && (long long)V * elem_bytes > c * 8192ll) c *= 2;
+  while (c * 2 <= kMaxCluster && rows * c * 2 <= slots && (long long)V * elem_bytes > c * 8192ll) c *= 2;
+  if (c > 8) c = kMaxCluster;  // (of the sizes above 8, only this one)
   return c;
 }
 

@@ -28,7 +28,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kList = 2048;   // tokens that rank 0 can sort
+constexpr int kList = 1024;   // tokens that rank 0 can sort
 constexpr int kMine = 1024;   // tokens that a CTA can bring
 constexpr int kKeys = 4096;   // groups' maxima (256 of each of 16 CTAs)
 constexpr int kBins = 23 * 128;  // of the histogram: 23 octaves
@@ -56,7 +56,7 @@ struct SampleSmem {
   alignas(16) float2 table[kTable];
   union {
     u64 list[kList];
-    uint32_t key[kKeys];
+    uint16_t key[kKeys];
     uint32_t bin[kBins + 32];
   };
   u64 mine[kMine];
@@ -186,8 +186,7 @@ __device__ __forceinline__ float just_below(float x) {
 
 enum Pass {
   kWhole,   // a cut that takes all tokens of its value
-  kTies,    // one that takes those up to an index
-  kBracket  // also a second cut below the first: the tokens between them go on the list
+  kBracket  // two cuts of any kind: the tokens between them go on the list
 };
 
 // One pass over the share's runs: steps[i] gets run i's mass of the places down to `hi`.
@@ -299,6 +298,7 @@ __device__ __forceinline__ Found weigh_row(const Share &s, const uint8_t *buf, c
   before = 0;
   n_in = 0;
   fits = true;
+#pragma unroll 1
   for (int q = 0; q < size; ++q) {
     if (q < rank) before += got[q][0];
     f.above += got[q][0];
@@ -358,7 +358,7 @@ __device__ __forceinline__ void place_bracket(float want, bool share, int size, 
   u64 n[kEach];  // (counts of a row fit half of a word)
 #pragma unroll
   for (int i = 0; i < kEach; ++i) n[i] = 0;
-#pragma unroll 4
+#pragma unroll 2
   for (int q = 0; q < size; ++q) {
     const uint32_t at = cluster_addr(bins, q);
 #pragma unroll
@@ -428,6 +428,7 @@ __device__ __forceinline__ void place_bracket(float want, bool share, int size, 
     }
     const int j_up = at - 1 - lane, j_down = at + 1 + lane;
     uint32_t up = 0, down = 0;
+#pragma unroll 1
     for (int q = 0; q < size; ++q) {
       const uint32_t from = cluster_addr(bins, q);
       if (j_up >= 0) up += remote_get32(from + 4u * j_up);
@@ -488,6 +489,7 @@ __device__ __forceinline__ void gather(const Share &s, const uint8_t *buf, const
 __device__ __forceinline__ int collect(int size, SampleSmem &sm) {
   __syncthreads();  // (their numbers)
   int all = 0;
+#pragma unroll 1
   for (int q = 0; q < size; ++q) all += sm.listed[q];
   for (int i = threadIdx.x; i < all; i += kThreads) {
     int q = 0, at = i;
@@ -588,11 +590,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     } else if (sub == 1) {
       gm[0] = M;
     }
+#pragma unroll 1
     for (int q = 0; q < size; ++q) {
       const uint32_t to = cluster_addr(smem_addr(&sm.key[(rank * kThreads + tid) * sub]), q);
 #pragma unroll
       for (int i = 0; i < kChunks; ++i)
-        if (i < sub) remote_put(to + 4u * i, order_key(gm[i]) >> 16);
+        if (i < sub) remote_put16(to + 2u * i, order_key(gm[i]) >> 16);
     }
   }
   M = cta_max_nan<kWarps>(M, sm.redf[0]);
@@ -600,6 +603,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   rec[0] = (u64)(sm.in.gave_up ? SPECDEC_ROW_INTERNAL : 0) << 32 | __float_as_uint(M);
   const u64(*got)[kWords] = exchange(sm.ex, turn, rec, 1, rank, size);
   M = -INFINITY;
+#pragma unroll 1
   for (int q = 0; q < size; ++q) {
     M = fmax_nan(M, __uint_as_float((uint32_t)got[q][0]));
     st |= (int)(got[q][0] >> 32);
@@ -641,6 +645,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       got = exchange(sm.ex, turn, rec, 1, rank, size);
       int all = 0;
       bool fits = true;
+#pragma unroll 1
       for (int q = 0; q < size; ++q) {
         if (tid == 0) sm.listed[q] = (int)got[q][0];
         all += (int)got[q][0];
@@ -779,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
           hi = H;
         } else {
           hi = L + (H - L) / 2;
-          f = weigh_row<DT, kTies>(s, buf, w, cut_at(hi), cut_at(hi), steps, rank, size, turn, mass,
+          f = weigh_row<DT, kBracket>(s, buf, w, cut_at(hi), cut_at(hi), steps, rank, size, turn, mass,
                                    before, n_in, fits, sm);
           if (want <= f.above) {
             L = hi;
@@ -883,6 +888,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         rec[0] = mass;
         got = exchange(sm.ex, turn, rec, 1, rank, size);
         before = 0;
+#pragma unroll 1
         for (int q = 0; q < rank; ++q) before += got[q][0];
         weighed = true;
       }
