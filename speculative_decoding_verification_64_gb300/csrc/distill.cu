@@ -12,8 +12,9 @@
 // entries taken out (their logits put to -infinity in shared memory, so that s_rest is a sum
 // and no difference of two near equal ones); one exchange of five words between the CTAs;
 // the gradient, straight from registers to global memory, then the entries' own values.  The
-// terms of the loss are float32, added in 64-bit fixed point (an SM has two lanes for 64-bit
-// floating point: one logarithm a row is all that is left to them).
+// loss is sum p_j (z_j - x_j) / T + sum p_j (max / T + ln S - lse), S the row's sum against
+// its maximum: its terms are float32, added in 64-bit fixed point (an SM has two lanes for
+// 64-bit floating point).
 #include "draft_common.cuh"
 
 namespace specdec {
@@ -100,26 +101,34 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
   // the entries: K <= 4 a thread, their ids and logits in registers
   int id[kPerThread];
   float z[kPerThread];
-  float zmax = -INFINITY;
+  float zmax = -INFINITY, lse = 0.0f;
   int status = 0, some = 0;
   if (w != 0.0f) {
     if (tid == 0) share_copy(s, buf, sm.in);
-    share_edges<DT>(s, row, buf);
-    for (int i = tid; i < (l.pos - l.bits) / 4; i += kThreads) bits[i] = 0;
+    if (p.lse) lse = p.lse[n];
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
       const int j = tid + i * kThreads;
       id[i] = -1;
       z[i] = -INFINITY;
-      if (j >= p.K) continue;
-      id[i] = p.ids[n * p.K + j];
+      if (j < p.K) {
+        id[i] = p.ids[n * p.K + j];
+        z[i] = p.teacher[n * p.K + j];
+      }
+    }
+    share_edges<DT>(s, row, buf);
+    for (int i = tid; i < (l.pos - l.bits) / 4; i += kThreads) bits[i] = 0;
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
       if (id[i] < -1 || id[i] >= p.V) {
         status |= SPECDEC_ROW_BAD_TOKEN;
         id[i] = -1;
       }
-      if (id[i] < 0) continue;
+      if (id[i] < 0) {
+        z[i] = -INFINITY;
+        continue;
+      }
       some = 1;
-      z[i] = p.teacher[n * p.K + j];
       if (!(z[i] < INFINITY)) status |= SPECDEC_ROW_NONFINITE;
       zmax = fmaxf(zmax, z[i]);
     }
@@ -139,9 +148,7 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
   int st = 0;
   if (w != 0.0f) {
     // p_j = e^y_j / zs: y_j = z_j / T - lse and zs = 1, or y_j = (z_j - zmax) / T
-    float lse = 0.0f;
     if (p.lse) {
-      lse = p.lse[n];
       if (!(fabsf(lse) < INFINITY)) status |= SPECDEC_ROW_NONFINITE;
       zmax = 0.0f;
     } else {
@@ -178,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
 
     // this CTA's entries: noted, and taken out of the row
     float at_s = 0.0f, large = 0.0f;
-    long long terms = 0, at_mass = 0;  // sum p_j (y_j - (x_j - ref) / T), and of p_j
+    long long terms = 0, at_mass = 0;  // sum p_j (z_j - x_j) / T, and of p_j
     int mine = 0;
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
@@ -195,12 +202,12 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
       put_elem<DT>(buf + (size_t)at * es, -INFINITY);
       at_s += ex2_approx((x - ref) * c);
       if (pj > 0.0f) {
-        const float dx = x - ref;
-        const float t = x > -INFINITY ? pj * (y - fmaf(dx, p.inv_t, dx * p.inv_t_low)) : INFINITY;
+        const float dx = z[i] - x;
+        const float t = pj * fmaf(dx, p.inv_t, dx * p.inv_t_low);
         if (fabsf(t) < kMost)
           terms += __float2ll_rn(t * kTerm);
         else
-          large += t;
+          large += x > -INFINITY ? t : INFINITY;
         at_mass += __float2ll_rn(fminf(pj, kMost) * kTerm);
       }
       const int k = atomicAdd(&sm.entries, 1);  // (their order decides nothing)
@@ -290,26 +297,42 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
     coef = fminf(fmaxf(w * p.inv_t * share * inv_s, -3.0e38f), 3.0e38f);
   }
 
-  if (rank == 0 && tid < 32 && p.loss) {
+  if (rank == 0 && tid == 0 && p.loss) {
     float L = 0.0f;
     if (w != 0.0f) {
-      // sum p_j (y_j - ln zs - (x_j - M) / T + ln S): that CTA's terms stand against its own
-      // maximum; without a log-sum-exp the p_j are 1 in all by definition
-      double t = p.lse ? (double)mass * log((double)S) : 0x1p40 * log((double)(S * (1.0f / zs)));
+      // q = max / T + ln S - lse in units of 2^-40, 2^40 / T and ln S in parts that are rounded
+      // far below float32's half step of the whole
+      int e;
+      const float f = frexpf(S, &e);
+      float zt = 0.0f;  // without a log-sum-exp: zmax / T + ln zs is the entries' own
+      int ez = 0;
+      const float fz = frexpf(zs, &ez);
+      if (!p.lse) zt = zmax;
+      const float dm = M - zt, a = dm * p.inv_t;
+      const float low = fmaf(dm, p.inv_t, -a) + dm * p.inv_t_low;
+      long long t = 0;
       for (int k = 0; k < size; ++k) {
-        const float mk = __uint_as_float((uint32_t)got[k][1]);
-        const long long pk = (long long)got[k][3];
-        t += (double)(long long)got[k][2];
-        if (pk && mk > -INFINITY) t += (double)pk * (((double)M - mk) * ((double)p.inv_t + p.inv_t_low));
+        t += (long long)got[k][2];
+        L += __uint_as_float((uint32_t)got[k][4]);
       }
-      L = (float)(t * 0x1p-40);
-      for (int k = 0; k < size; ++k) L += __uint_as_float((uint32_t)got[k][4]);
+      float q;
+      if (fabsf(a) < 0x1p21f && fabsf(lse) < 0x1p21f) {
+        const long long kLn2 = 762123384786ll;  // ln 2 in units of 2^-40
+        const long long qf = __float2ll_rn(a * kTerm) + __float2ll_rn((low + logf(f) - logf(fz)) * kTerm) -
+                             __float2ll_rn(lse * kTerm) + (long long)(e - ez) * kLn2;
+        q = (float)qf * 0x1p-40f;
+        t += qf;
+      } else {
+        q = (a - lse) + (low + logf(S) - logf(zs));
+        L += q;
+      }
+      // sum p_j is 1 without a log-sum-exp (by definition) and 1 - r with one
+      if (p.lse) L -= q * ((float)((1ll << 40) - mass) * 0x1p-40f);
       if (left > 0.0f) L += left * logf(left / of);
+      L += (float)t * 0x1p-40f;
     }
-    if (tid == 0) {
-      p.loss[n] = st ? __int_as_float(0x7fc00000) : none ? 0.0f : L;
-      p.row_status[n] = st;
-    }
+    p.loss[n] = st ? __int_as_float(0x7fc00000) : none ? 0.0f : L;
+    p.row_status[n] = st;
   }
   if (kGrad) {
     const float fill = st ? __int_as_float(0x7fc00000) : 0.0f;
