@@ -378,7 +378,7 @@ cudaError_t launch_dt(const DistillParams &p, cudaStream_t stream) {
   if (err != cudaSuccess) return err;
   constexpr int es = Elem<DT>::kBytes;
   const long long rows = (long long)p.B * p.R;
-  const int size = cluster_for(rows, p.V, es, 66 * 1024, 3);
+  const int size = cluster_for(rows, p.V, es, 80 * 1024, 3);
   const int vectors = share_vectors(p.V, es, size);
   return launch_clusters(distill_kernel<DT, kGrad>, rows, size, kThreads,
                          layout_of(vectors, es, p.K).total, stream, p, vectors);

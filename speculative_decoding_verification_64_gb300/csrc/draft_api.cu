@@ -146,7 +146,8 @@ size_t specdec_top_logits_workspace_size(int B, int R, int V, int dtype) {
   if (rows_status(dtype, B, R, V, SPECDEC_MAX_V) != SPECDEC_OK || B == 0) return 0;
   const long long rows = (long long)B * R;
   return top_part_bytes(rows, V, dtype) +
-         align256((size_t)rows * stages_per_row(V, elem_bytes(dtype)) * 32 * sizeof(float));
+         align256((size_t)rows * stages_per_row(V, elem_bytes(dtype)) * kTopGroups *
+                    sizeof(float));
 }
 
 int specdec_top_logits(const void *logits, int dtype, long long request_stride,
@@ -169,6 +170,8 @@ int specdec_top_logits(const void *logits, int dtype, long long request_stride,
     return SPECDEC_ERR_WORKSPACE;
   p.x = logits;
   p.temperature = temperature;
+  p.inv_t = (float)(1.0 / (double)temperature);
+  p.inv_t_low = (float)(1.0 / (double)temperature - (double)p.inv_t);
   p.dtype = dtype;
   p.B = B;
   p.R = R;

@@ -29,14 +29,17 @@ struct SampleParams {
   int32_t *row_status;       // [B, R]
 };
 
+constexpr int kTopGroups = 16;  // of a stage's 8 KB
+
 struct TopParams {
   const void *x;
   RowsAt x_at;
   float temperature;
+  float inv_t, inv_t_low;  // 1 / temperature, in two parts
   int dtype, B, R, V, K;
   int spr;               // stages a row (as in the row statistics)
   float2 *part;          // [rows, spr]: each stage's maximum and sum, in the workspace
-  float *group;          // [rows, spr, 32]: its lanes' maxima
+  float *group;          // [rows, spr, kTopGroups]: the maximum of each 512 bytes
   float *values;         // [B, R, K]
   int32_t *ids;          // [B, R, K]
   float *lse;            // [B, R]
@@ -200,11 +203,44 @@ __device__ __forceinline__ int place_index(unsigned long long p) {
   return (int)(0xFFFFFFFFu - (uint32_t)p);
 }
 
-// Sorts list[0, n) downwards: a bitonic network over the next power of two, whose rest is
-// filled with 0 (below every token).  Exchanges over up to 32 places stay within a warp's
-// own 64, so that only the wider ones need the CTA's barrier.
+// Ranks kE tokens a thread among list[0, n) and puts them there.
+template <int kThreads, int kE>
+__device__ __forceinline__ void sort_by_rank(unsigned long long *list, int n) {
+  unsigned long long v[kE];
+  int rank[kE];
+#pragma unroll
+  for (int i = 0; i < kE; ++i) {
+    const int at = threadIdx.x + i * kThreads;
+    v[i] = at < n ? list[at] : 0ull;
+    rank[i] = 0;
+  }
+#pragma unroll 4
+  for (int j = 0; j < n; ++j) {
+    const unsigned long long q = list[j];
+#pragma unroll
+    for (int i = 0; i < kE; ++i) rank[i] += q > v[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kE; ++i)
+    if ((int)threadIdx.x + i * kThreads < n) list[rank[i]] = v[i];
+  __syncthreads();
+}
+
+// Sorts the CTA's list[0, n) downwards, all tokens of it different.  Up to 1024 each token
+// is compared with all others, which needs two barriers (96 tokens: about 500 clocks, where
+// a bitonic network of 28 steps took 6700); beyond that the network over the next power of
+// two, its rest filled with 0 (below every token).
 template <int kThreads>
-__device__ __forceinline__ void sort_down(unsigned long long *list, int n) {
+__device__ __noinline__ void sort_down(unsigned long long *list, int n) {
+  if (n <= kThreads) {
+    sort_by_rank<kThreads, 1>(list, n);
+    return;
+  }
+  if (n <= 4 * kThreads) {
+    sort_by_rank<kThreads, 4>(list, n);
+    return;
+  }
   int len = 2;
   while (len < n) len *= 2;
   for (int i = n + threadIdx.x; i < len; i += kThreads) list[i] = 0ull;
@@ -219,12 +255,21 @@ __device__ __forceinline__ void sort_down(unsigned long long *list, int n) {
           list[o] = a;
         }
       }
-      if (j > 32 || (j == 1 && (k > 32 || k == len)))
-        __syncthreads();
-      else
-        __syncwarp();
+      __syncthreads();
     }
   }
+}
+
+// m / T + ln s for s > 0, rounded about once: in units of 2^-40, where its parts are not
+// beyond them.  inv_t + inv_t_low is 1 / T.
+__device__ __forceinline__ float log_sum(float m, float inv_t, float inv_t_low, float s) {
+  int e;
+  const float f = frexpf(s, &e);
+  const float a = m * inv_t, low = fmaf(m, inv_t, -a) + m * inv_t_low;
+  if (!(fabsf(a) < 0x1p21f)) return a + (low + logf(s));
+  const long long t = __float2ll_rn(a * 0x1p40f) + __float2ll_rn((low + logf(f)) * 0x1p40f) +
+                      (long long)e * 762123384786ll;  // ln 2
+  return (float)t * 0x1p-40f;
 }
 
 // ---- clusters -------------------------------------------------------------------------

@@ -4,12 +4,12 @@
 //
 // First kernel, one pass over HBM, structured like the row statistics: a CTA an SM, 16 KB
 // bulk copies into a ring, a warp reduces an 8 KB stage held in registers.  Beside the
-// stage's maximum and sum it leaves the maximum of each lane's elements (16 vectors, 512
-// bytes apart): groups of 64 or 128 tokens.
+// stage's maximum and sum it leaves the maximum of every 512 bytes (one vector of each lane):
+// groups of 128 or 256 tokens.
 //
 // Second kernel, a CTA a row: the K-th largest of the groups' maxima (its top 16 bits) bounds
 // the K-th largest logit from below, since K groups hold one at least that large; only
-// groups whose maximum reaches the bound are read again (K of some thousand), and their
+// groups whose maximum reaches the bound are read again (K of some hundred), and their
 // few elements that reach it, K and some, are sorted in shared memory.  Where they are too
 // many for the list (long runs of equal logits), a radix selection over (value, index)
 // finds the K-th place first.
@@ -32,6 +32,18 @@ struct ScanSmem {
 // unit_geometry of a row that stands anywhere
 __device__ __forceinline__ UnitGeom geometry(const uint8_t *row, int V, int spr, int ju, int es) {
   return unit_geometry(row, V, spr, 0, ju, es);
+}
+
+constexpr int kGroups = kTopGroups;
+static_assert(kGroups == kVecPerLane, "a group is one vector of each lane");
+
+// Integers that order like the values (their own inverse), -0 just below +0.
+__device__ __forceinline__ int signed_key(float x) {
+  const int b = __float_as_int(x);
+  return b ^ (b >> 31 & 0x7FFFFFFF);
+}
+__device__ __forceinline__ float signed_float(int k) {
+  return __int_as_float(k ^ (k >> 31 & 0x7FFFFFFF));
 }
 
 constexpr float kGaveUp = -2.0f;  // a stage's sum, where its copy was not waited for
@@ -127,15 +139,22 @@ __global__ void __launch_bounds__(kThreads, 1) top_scan_kernel(const TopParams p
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.empty[slot]);
     if (!real) continue;
-    float lm = -INFINITY, wm = -INFINITY, sum = kGaveUp;
+    float wm = -INFINITY, sum = kGaveUp;
+    int group = signed_key(-INFINITY);
     if (ok) {
-      lm = lane_max<DT>(d);  // (with the row's edge elements, in stage 0)
-      wm = warp_max_nan(lm);
+      wm = warp_max_nan(lane_max<DT>(d));  // (with the row's edge elements, in stage 0)
       sum = wm > -INFINITY ? warp_sum(lane_sum<DT>(d, c, wm)) : 0.0f;
+#pragma unroll
+      for (int k = 0; k < kVecPerLane; ++k) {
+        int m = signed_key(max_of<DT>(vector_max<DT>(d.v[k], no_max<DT>())));
+        if (k == 0) m = max(m, signed_key(d.edge));
+        m = __reduce_max_sync(kFull, m);
+        if (lane == k) group = m;
+      }
     }
     const long long at_part = (long long)row * p.spr + u.j0 + t;
     if (lane == 0) p.part[at_part] = make_float2(wm, sum);
-    p.group[at_part * 32 + lane] = lm;
+    if (lane < kGroups) p.group[at_part * kGroups + lane] = signed_float(group);
   }
   if (sm.abort_flag && lane == 0) {
     const unsigned long long t0 = global_timer_ns();
@@ -149,58 +168,103 @@ __global__ void __launch_bounds__(kThreads, 1) top_scan_kernel(const TopParams p
 
 constexpr int kPickThreads = 256;
 constexpr int kPickWarps = kPickThreads / 32;
-constexpr int kKeys = 4096;  // maxima that the bound is found among
-constexpr int kList = 2048;  // tokens that reach it and can be sorted
-constexpr int kDigit = 11;   // bits of a digit of the radix selection
+constexpr int kKeys = 4096;   // maxima that the bound is found among
+constexpr int kList = 2048;   // tokens that reach it and can be sorted
+constexpr int kBatch = 1024;  // groups looked at together
+constexpr int kDigit = 11;    // bits of a digit of the radix selection
 
 struct PickSmem {
   union {
-    uint32_t key[kKeys];
+    uint16_t key[kKeys];
     uint32_t count[1 << kDigit];
   } u;
   unsigned long long list[kList];
-  float red[kPickWarps];
-  float redf[kPickWarps];
-  unsigned int total[16];
-  int n, digit, need;
+  uint16_t hit[kBatch];
+  float red[2][kPickWarps];
+  int n, hits, digit, need;
 };
 
-// Every element of the groups whose maximum reaches `from`, and the row's edges, that
-// reaches it too: f(x, index).  Two groups a warp at a time, a lane a vector of each.
-template <int DT, typename F>
-__device__ __forceinline__ void candidates(const TopParams &p, const uint8_t *row,
-                                           const float *group, float from, F &&f) {
-  constexpr int es = Elem<DT>::kBytes, kN = Elem<DT>::kN;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const UnitGeom g0 = geometry(row, p.V, p.spr, 0, es);
-  const int tail_begin = min(g0.tail_begin, p.V);   // (past it for rows that end before a boundary)
+// What is done with the elements that reach the bound: they go on the list (those whose
+// place is at or above `prefix`), or one digit of the places that share the prefix's bits
+// from `above` up is counted.
+struct Take {
+  float from;
+  unsigned long long prefix;
+  int above, lo;  // above = 0: the list
+};
+
+// Every element of the groups whose maximum reaches take.from, and the row's edges, that
+// reaches it too.  The groups of a batch are named first, then all of their vectors are
+// loaded, several a thread on their way together.
+template <int DT>
+__device__ __noinline__ void candidates(const uint8_t *row, int V, int spr, const float *group,
+                                        Take take, PickSmem &sm) {
+  constexpr int es = Elem<DT>::kBytes, kN = Elem<DT>::kN, kAhead = 4;
+  const int t = threadIdx.x;
+  const UnitGeom g0 = geometry(row, V, spr, 0, es);
+  const int tail_begin = min(g0.tail_begin, V);        // (past it for rows that end before a boundary)
   const int inside = (tail_begin - g0.head_end) / kN;  // vectors of the row's inside
   const uint4 *base = reinterpret_cast<const uint4 *>(row + (size_t)g0.head_end * es);
-  for (int st = warp; st < p.spr; st += kPickWarps) {
-    unsigned hit = __ballot_sync(kFull, __ldg(group + st * 32 + lane) >= from);
-    while (hit) {
-      const int a = __ffs(hit) - 1;
-      hit &= hit - 1;
-      const int b = hit ? __ffs(hit) - 1 : -1;
-      hit = hit ? hit & (hit - 1) : 0;
-      const int mine = lane < 16 ? a : b;
-      const int v = st * (kStageBytes / 16) + mine + 32 * (lane & 15);
-      if (mine >= 0 && v < inside) {
-        float x[kN];
-        widen<DT>(__ldg(base + v), x);
+  const int groups = spr * kGroups;
+  auto found = [&](float x, int at) {
+    const unsigned long long q = place_of(x, at);
+    if (take.above == 0) {
+      if (q < take.prefix) return;
+      const int i = atomicAdd(&sm.n, 1);  // (sorted later: their order decides nothing)
+      if (i < kList) sm.list[i] = q;
+    } else if (take.above == 64 || q >> take.above == take.prefix >> take.above) {
+      atomicAdd(&sm.u.count[(q >> take.lo) & ((1u << (take.above - take.lo)) - 1)], 1u);
+    }
+  };
+#pragma unroll 1
+  for (int g = 0; g < groups; g += kBatch) {
+    __syncthreads();  // (the last batch's readers)
+    if (t == 0) sm.hits = 0;
+    __syncthreads();
 #pragma unroll
-        for (int e = 0; e < kN; ++e)
-          if (x[e] >= from) f(x[e], g0.head_end + v * kN + e);
+    for (int i = 0; i < kBatch / kPickThreads; ++i) {
+      const int at = g + i * kPickThreads + t;
+      if (at < groups && __ldg(group + at) >= take.from)
+        sm.hit[atomicAdd(&sm.hits, 1)] = (uint16_t)(i * kPickThreads + t);
+    }
+    __syncthreads();
+    const int n = sm.hits * 32;  // vectors: 32 a group
+#pragma unroll 1
+    for (int i0 = t; i0 < n; i0 += kAhead * kPickThreads) {
+      uint4 w[kAhead];
+      int v[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int q = i0 + i * kPickThreads;
+        v[i] = q < n ? (g + sm.hit[q >> 5]) * 32 + (q & 31) : inside;
+        if (v[i] < inside) w[i] = __ldg(base + v[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (v[i] >= inside || !(max_of<DT>(vector_max<DT>(w[i], no_max<DT>())) >= take.from)) continue;
+        float x[kN];
+        widen<DT>(w[i], x);
+        unsigned reach = 0;
+#pragma unroll
+        for (int e = 0; e < kN; ++e) reach |= x[e] >= take.from ? 1u << e : 0u;
+        while (reach) {
+          const int e = __ffs(reach) - 1;
+          reach &= reach - 1;
+          float y = x[0];
+#pragma unroll
+          for (int q = 1; q < kN; ++q) y = e == q ? x[q] : y;
+          found(y, g0.head_end + v[i] * kN + e);
+        }
       }
     }
   }
-  const int n_head = g0.head_end, n_edge = n_head + p.V - tail_begin;
-  if ((int)threadIdx.x < n_edge) {
-    const int e = (int)threadIdx.x < n_head ? (int)threadIdx.x
-                                            : tail_begin + ((int)threadIdx.x - n_head);
+  const int n_head = g0.head_end, n_edge = n_head + V - tail_begin;
+  if (t < n_edge) {
+    const int e = t < n_head ? t : tail_begin + (t - n_head);
     const float x = load_elem(row, DT, e);
-    if (x >= from) f(x, e);
+    if (x >= take.from) found(x, e);
   }
+  __syncthreads();
 }
 
 template <int DT>
@@ -210,16 +274,18 @@ __global__ void __launch_bounds__(kPickThreads) top_pick_kernel(const TopParams 
   constexpr int es = Elem<DT>::kBytes;
   pdl_wait();
   pdl_launch_dependents();
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long long n = blockIdx.x;
   const long long b = n / p.R;
   const uint8_t *row = reinterpret_cast<const uint8_t *>(p.x) +
                        (b * p.x_at.request + (n - b * p.R) * p.x_at.row) * es;
-  const float *group = p.group + n * p.spr * 32;
+  const float *group = p.group + n * p.spr * kGroups;
   const float2 *part = p.part + n * p.spr;
   const float c = temperature_scale(p.temperature);
 
-  // maximum, sum, and whether the row can be used
+  // the groups' maxima, and the row's
+  const int groups = p.spr * kGroups, per = (groups + kKeys - 1) / kKeys;
+  const int keys = (groups + per - 1) / per;
   float M = -INFINITY;
   int lost = 0;
   for (int i = tid; i < p.spr; i += kPickThreads) {
@@ -227,7 +293,17 @@ __global__ void __launch_bounds__(kPickThreads) top_pick_kernel(const TopParams 
     M = fmax_nan(M, q.x);
     lost |= q.y == kGaveUp;
   }
-  M = cta_max_nan<kPickWarps>(M, sm.redf);
+#pragma unroll 4
+  for (int i = tid; i < keys; i += kPickThreads) {
+    float m = __ldg(group + i * per);
+    for (int j = i * per + 1; j < min(groups, (i + 1) * per); ++j) m = fmaxf(m, __ldg(group + j));
+    sm.u.key[i] = (uint16_t)(order_key(m) >> 16);
+  }
+  if (tid == 0) {
+    sm.n = 0;
+    if (keys & 1) sm.u.key[keys < kKeys ? keys : 0] = 0;  // (keys are read in pairs; 0 is no key)
+  }
+  M = cta_max_nan<kPickWarps>(M, sm.red[0]);
   int st = __syncthreads_or(lost) ? SPECDEC_ROW_INTERNAL : 0;
   if (!st && !(M > -INFINITY && M <= kMaxLogit)) st = SPECDEC_ROW_NONFINITE;
   if (st) {
@@ -241,74 +317,80 @@ __global__ void __launch_bounds__(kPickThreads) top_pick_kernel(const TopParams 
     }
     return;
   }
+
+  // a bound that K groups reach: the top 16 bits of the K-th largest maximum, bit by bit, by
+  // one warp (a barrier of the CTA for every bit takes eight times as long)
+  if (warp == 0) {
+    constexpr int kHeld = 8;  // pairs of keys that a lane holds
+    const uint32_t *pairs = reinterpret_cast<const uint32_t *>(sm.u.key);
+    const int n_pairs = (keys + 1) / 2;
+    uint32_t held[kHeld];
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) held[i] = lane + 32 * i < n_pairs ? pairs[lane + 32 * i] : 0;
+    const uint32_t most = order_key(M) >> 16;
+    uint32_t bound = 0;
+#pragma unroll 1
+    for (int bit = 15; bit >= 0; --bit) {
+      const uint32_t t = bound | 1u << bit;
+      if (t > most) continue;
+      unsigned m = 0;
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) m += ((held[i] & 0xFFFFu) >= t) + ((held[i] >> 16) >= t);
+      for (int i = lane + 32 * kHeld; i < n_pairs; i += 32)
+        m += ((pairs[i] & 0xFFFFu) >= t) + ((pairs[i] >> 16) >= t);
+      if (__reduce_add_sync(kFull, m) >= (unsigned)p.K) bound = t;
+    }
+    if (lane == 0) sm.digit = (int)bound;
+  }
+  __syncthreads();
+  const uint32_t bound = (uint32_t)sm.digit;
+  // (no bound above -infinity's key: fewer than K groups hold more, and every element counts)
+  const float from = bound << 16 >= kLeastKey ? key_float(bound << 16) : -INFINITY;
+
+  candidates<DT>(row, p.V, p.spr, group, {from, 0ull, 0, 0}, sm);
+  // the sum, while the list is completed
   float S = 0.0f;
   for (int i = tid; i < p.spr; i += kPickThreads) {
     const float2 q = __ldg(part + i);
     if (q.x > -INFINITY) S += q.y * ex2_approx((q.x - M) * c);
   }
-  S = cta_sum<kPickWarps>(S, sm.red);
-
-  // a bound that K groups reach: bit by bit, the top 16 bits of the K-th largest maximum
-  const int groups = p.spr * 32, per = (groups + kKeys - 1) / kKeys;
-  const int keys = (groups + per - 1) / per;
-  for (int i = tid; i < keys; i += kPickThreads) {
-    float m = -INFINITY;
-    for (int j = i * per; j < min(groups, (i + 1) * per); ++j) m = fmaxf(m, __ldg(group + j));
-    sm.u.key[i] = order_key(m) >> 16;
-  }
-  if (tid < 16) sm.total[tid] = 0;
-  if (tid == 0) sm.n = 0;
-  __syncthreads();
-  uint32_t bound = 0;
-  for (int bit = 15; bit >= 0; --bit) {
-    const uint32_t t = bound | 1u << bit;
-    unsigned m = 0;
-    for (int i = tid; i < keys; i += kPickThreads) m += sm.u.key[i] >= t;
-    m = __reduce_add_sync(kFull, m);
-    if ((tid & 31) == 0 && m) atomicAdd(&sm.total[bit], m);
-    __syncthreads();
-    if (sm.total[bit] >= (unsigned)p.K) bound = t;
-  }
-  // (no bound above -infinity's key: fewer than K groups hold more, and every element counts)
-  const float from = bound << 16 >= kLeastKey ? key_float(bound << 16) : -INFINITY;
-
-  candidates<DT>(p, row, group, from, [&](float x, int at) {
-    const int i = atomicAdd(&sm.n, 1);  // (sorted below: their order decides nothing)
-    if (i < kList) sm.list[i] = place_of(x, at);
-  });
-  __syncthreads();
+  S = cta_sum<kPickWarps>(S, sm.red[1]);
   if (sm.n > kList) {
-    // radix selection of the K-th place, 11 bits at a time
+    // radix selection of the K-th place, a digit at a time
     unsigned long long prefix = 0;
     int need = p.K;
+#pragma unroll 1
     for (int above = 64; above > 0;) {
-      const int lo = max(above - kDigit, 0), width = above - lo;
+      const int lo = max(above - kDigit, 0);
       __syncthreads();
       for (int i = tid; i < 1 << kDigit; i += kPickThreads) sm.u.count[i] = 0;
-      __syncthreads();
-      candidates<DT>(p, row, group, from, [&](float x, int at) {
-        const unsigned long long q = place_of(x, at);
-        if (above == 64 || q >> above == prefix >> above)
-          atomicAdd(&sm.u.count[(q >> lo) & ((1u << width) - 1)], 1u);
-      });
-      __syncthreads();
-      if (tid == 0) {
-        int d = (1 << width) - 1, left = need;
-        while (d > 0 && (unsigned)left > sm.u.count[d]) left -= (int)sm.u.count[d--];
-        sm.digit = d;
-        sm.need = left;
-        sm.n = 0;
+      candidates<DT>(row, p.V, p.spr, group, {from, prefix, above, lo}, sm);
+      if (warp == 0) {
+        // 64 digits a lane, from the largest down, then the one's own
+        constexpr int kLane = (1 << kDigit) / 32;
+        const int top = (1 << kDigit) - 1 - lane * kLane;
+        int mine = 0;
+        for (int i = 0; i < kLane; ++i) mine += (int)sm.u.count[top - i];
+        int inc = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int y = __shfl_up_sync(kFull, inc, d);
+          if (lane >= d) inc += y;
+        }
+        if (inc - mine < need && need <= inc) {
+          int left = need - (inc - mine), d = top;
+          while (left > (int)sm.u.count[d]) left -= (int)sm.u.count[d--];
+          sm.digit = d;
+          sm.need = left;
+        }
+        if (lane == 0) sm.n = 0;
       }
       __syncthreads();
       prefix |= (unsigned long long)sm.digit << lo;
       need = sm.need;
       above = lo;
     }
-    candidates<DT>(p, row, group, from, [&](float x, int at) {
-      const unsigned long long q = place_of(x, at);
-      if (q >= prefix) sm.list[atomicAdd(&sm.n, 1)] = q;  // (K of them)
-    });
-    __syncthreads();
+    candidates<DT>(row, p.V, p.spr, group, {from, prefix, 0, 0}, sm);  // (K of them)
   }
   sort_down<kPickThreads>(sm.list, sm.n);
   for (int i = tid; i < p.K; i += kPickThreads) {
@@ -317,7 +399,7 @@ __global__ void __launch_bounds__(kPickThreads) top_pick_kernel(const TopParams 
     p.ids[n * p.K + i] = place_index(q);
   }
   if (tid == 0) {
-    p.lse[n] = (float)((double)M / (double)p.temperature + log((double)S));
+    p.lse[n] = log_sum(M, p.inv_t, p.inv_t_low, S);
     p.row_status[n] = 0;
   }
 }

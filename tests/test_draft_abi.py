@@ -73,8 +73,8 @@ def test_top_logits_checks(sd):
     size = sd.top_logits_workspace_size
     assert size(0, 3, 1000, sd.BF16) == 0 and size(2, 0, 1000, sd.BF16) == 0
     assert size(2, 3, (1 << 21) + 1, sd.BF16) == 0 and size(2, 3, 1000, 5) == 0
-    assert size(2, 3, 1000, sd.BF16) >= 6 * (8 + 128)
-    assert size(2, 3, 128256, sd.BF16) >= 6 * 32 * (8 + 128)
+    assert size(2, 3, 1000, sd.BF16) >= 6 * (8 + 64)
+    assert size(2, 3, 128256, sd.BF16) >= 6 * 32 * (8 + 64)
     assert top(sd, B=0, logits=None) == 0
     for bad in ROWS + [dict(K=0), dict(K=1001), dict(temperature=0.0), dict(temperature=-1.0),
                        dict(temperature=float("nan")), dict(temperature=2.0 ** 21), dict(values=None),
