@@ -142,15 +142,18 @@ __global__ void __launch_bounds__(kThreads, 1) top_scan_kernel(const TopParams p
     float wm = -INFINITY, sum = kGaveUp;
     int group = signed_key(-INFINITY);
     if (ok) {
-      wm = warp_max_nan(lane_max<DT>(d));  // (with the row's edge elements, in stage 0)
-      sum = wm > -INFINITY ? warp_sum(lane_sum<DT>(d, c, wm)) : 0.0f;
+      // (a NaN comes out of these maxima as the positive one, whose key is the largest)
+      int all = signed_key(-INFINITY);
 #pragma unroll
       for (int k = 0; k < kVecPerLane; ++k) {
-        int m = signed_key(max_of<DT>(vector_max<DT>(d.v[k], no_max<DT>())));
-        if (k == 0) m = max(m, signed_key(d.edge));
-        m = __reduce_max_sync(kFull, m);
+        float f = max_of<DT>(vector_max<DT>(d.v[k], no_max<DT>()));
+        if (k == 0) f = fmax_nan(f, d.edge);  // the row's edge elements, in stage 0
+        const int m = __reduce_max_sync(kFull, signed_key(f));
         if (lane == k) group = m;
+        all = max(all, m);
       }
+      wm = signed_float(all);
+      sum = wm > -INFINITY ? warp_sum(lane_sum<DT>(d, c, wm)) : 0.0f;
     }
     const long long at_part = (long long)row * p.spr + u.j0 + t;
     if (lane == 0) p.part[at_part] = make_float2(wm, sum);
@@ -166,12 +169,15 @@ __global__ void __launch_bounds__(kThreads, 1) top_scan_kernel(const TopParams p
 
 // ---------------------------------------------------------------------------------------
 
-constexpr int kPickThreads = 256;
-constexpr int kPickWarps = kPickThreads / 32;
-constexpr int kKeys = 4096;   // maxima that the bound is found among
-constexpr int kList = 2048;   // tokens that reach it and can be sorted
+// Threads of a row's CTA: 256, or 128 for more rows than the SMs hold CTAs of 256 of
+// (2304 rows of 128256 tokens, 64 entries: 146 us in both kernels against 159 with 256;
+// 384 rows of 32003: 30.7 us against 24.6).
+constexpr int kFewThreads = 128, kManyThreads = 256;
+constexpr int kFewFrom = 8;   // CTAs an SM from which a row gets the fewer
+constexpr int kKeys = 2048;   // maxima that the bound is found among
+constexpr int kList = 1024;   // tokens that reach it and can be sorted
 constexpr int kBatch = 1024;  // groups looked at together
-constexpr int kDigit = 11;    // bits of a digit of the radix selection
+constexpr int kDigit = 10;    // bits of a digit of the radix selection
 
 struct PickSmem {
   union {
@@ -180,7 +186,7 @@ struct PickSmem {
   } u;
   unsigned long long list[kList];
   uint16_t hit[kBatch];
-  float red[2][kPickWarps];
+  float red[2][kManyThreads / 32];
   int n, hits, digit, need;
 };
 
@@ -196,7 +202,7 @@ struct Take {
 // Every element of the groups whose maximum reaches take.from, and the row's edges, that
 // reaches it too.  The groups of a batch are named first, then all of their vectors are
 // loaded, several a thread on their way together.
-template <int DT>
+template <int DT, int kPickThreads>
 __device__ __noinline__ void candidates(const uint8_t *row, int V, int spr, const float *group,
                                         Take take, PickSmem &sm) {
   constexpr int es = Elem<DT>::kBytes, kN = Elem<DT>::kN, kAhead = 4;
@@ -224,8 +230,13 @@ __device__ __noinline__ void candidates(const uint8_t *row, int V, int spr, cons
 #pragma unroll
     for (int i = 0; i < kBatch / kPickThreads; ++i) {
       const int at = g + i * kPickThreads + t;
-      if (at < groups && __ldg(group + at) >= take.from)
-        sm.hit[atomicAdd(&sm.hits, 1)] = (uint16_t)(i * kPickThreads + t);
+      const bool hit = at < groups && __ldg(group + at) >= take.from;
+      const unsigned all = __ballot_sync(kFull, hit);
+      int base_hit = 0;
+      if (all && (t & 31) == 0) base_hit = atomicAdd(&sm.hits, __popc(all));
+      base_hit = __shfl_sync(kFull, base_hit, 0);
+      if (hit)
+        sm.hit[base_hit + __popc(all & ((1u << (t & 31)) - 1))] = (uint16_t)(i * kPickThreads + t);
     }
     __syncthreads();
     const int n = sm.hits * 32;  // vectors: 32 a group
@@ -267,10 +278,11 @@ __device__ __noinline__ void candidates(const uint8_t *row, int V, int spr, cons
   __syncthreads();
 }
 
-template <int DT>
+template <int DT, int kPickThreads>
 __global__ void __launch_bounds__(kPickThreads) top_pick_kernel(const TopParams p) {
   __shared__ PickSmem sm;
   static_assert(kStageBytes == 16 * 32 * 16, "16 vectors a lane");
+  constexpr int kPickWarps = kPickThreads / 32;
   constexpr int es = Elem<DT>::kBytes;
   pdl_wait();
   pdl_launch_dependents();
@@ -333,9 +345,10 @@ __global__ void __launch_bounds__(kPickThreads) top_pick_kernel(const TopParams 
     for (int bit = 15; bit >= 0; --bit) {
       const uint32_t t = bound | 1u << bit;
       if (t > most) continue;
-      unsigned m = 0;
+      unsigned part[4] = {0, 0, 0, 0};
 #pragma unroll
-      for (int i = 0; i < kHeld; ++i) m += ((held[i] & 0xFFFFu) >= t) + ((held[i] >> 16) >= t);
+      for (int i = 0; i < kHeld; ++i) part[i & 3] += ((held[i] & 0xFFFFu) >= t) + ((held[i] >> 16) >= t);
+      unsigned m = (part[0] + part[1]) + (part[2] + part[3]);
       for (int i = lane + 32 * kHeld; i < n_pairs; i += 32)
         m += ((pairs[i] & 0xFFFFu) >= t) + ((pairs[i] >> 16) >= t);
       if (__reduce_add_sync(kFull, m) >= (unsigned)p.K) bound = t;
@@ -347,7 +360,7 @@ __global__ void __launch_bounds__(kPickThreads) top_pick_kernel(const TopParams 
   // (no bound above -infinity's key: fewer than K groups hold more, and every element counts)
   const float from = bound << 16 >= kLeastKey ? key_float(bound << 16) : -INFINITY;
 
-  candidates<DT>(row, p.V, p.spr, group, {from, 0ull, 0, 0}, sm);
+  candidates<DT, kPickThreads>(row, p.V, p.spr, group, {from, 0ull, 0, 0}, sm);
   // the sum, while the list is completed
   float S = 0.0f;
   for (int i = tid; i < p.spr; i += kPickThreads) {
@@ -364,9 +377,9 @@ __global__ void __launch_bounds__(kPickThreads) top_pick_kernel(const TopParams 
       const int lo = max(above - kDigit, 0);
       __syncthreads();
       for (int i = tid; i < 1 << kDigit; i += kPickThreads) sm.u.count[i] = 0;
-      candidates<DT>(row, p.V, p.spr, group, {from, prefix, above, lo}, sm);
+      candidates<DT, kPickThreads>(row, p.V, p.spr, group, {from, prefix, above, lo}, sm);
       if (warp == 0) {
-        // 64 digits a lane, from the largest down, then the one's own
+        // 32 digits a lane, from the largest down, then the one's own
         constexpr int kLane = (1 << kDigit) / 32;
         const int top = (1 << kDigit) - 1 - lane * kLane;
         int mine = 0;
@@ -390,7 +403,7 @@ __global__ void __launch_bounds__(kPickThreads) top_pick_kernel(const TopParams 
       need = sm.need;
       above = lo;
     }
-    candidates<DT>(row, p.V, p.spr, group, {from, prefix, 0, 0}, sm);  // (K of them)
+    candidates<DT, kPickThreads>(row, p.V, p.spr, group, {from, prefix, 0, 0}, sm);  // (K of them)
   }
   sort_down<kPickThreads>(sm.list, sm.n);
   for (int i = tid; i < p.K; i += kPickThreads) {
@@ -416,7 +429,11 @@ cudaError_t launch_dt(const TopParams &p, cudaStream_t stream) {
   if (grid > units) grid = units;
   err = launch_pdl(top_scan_kernel<DT>, dim3((unsigned)grid), dim3(kThreads), (size_t)smem, stream, p);
   if (err != cudaSuccess) return err;
-  return launch_pdl(top_pick_kernel<DT>, dim3((unsigned)rows), dim3(kPickThreads), 0, stream, p);
+  if (rows > (long long)kFewFrom * device_sm_count())
+    return launch_pdl(top_pick_kernel<DT, kFewThreads>, dim3((unsigned)rows), dim3(kFewThreads), 0,
+                      stream, p);
+  return launch_pdl(top_pick_kernel<DT, kManyThreads>, dim3((unsigned)rows), dim3(kManyThreads), 0,
+                    stream, p);
 }
 
 }  // namespace

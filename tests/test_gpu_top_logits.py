@@ -110,3 +110,16 @@ def test_workspace_and_outputs_of_the_caller(sd):
     with pytest.raises(sd.SpecdecError):
         sd.top_logits(x, 10, workspace=ws[:n - 16].clone())
     assert sd.top_logits(torch.zeros(0, 2, 5).cuda(), 2).ids.shape == (0, 2, 2)
+
+
+@pytest.mark.parametrize("K", [5, 64, 300])
+def test_many_rows(sd, K):
+    """More rows than the GPU holds at once, some with runs of equal logits."""
+    x = np.random.default_rng(K).standard_normal((700, 3, 600)).astype(np.float32)
+    x[5], x[699, :, ::2] = 0.5, 3.0
+    check(sd, x, K, rows={(0, 0), (5, 1), (300, 2), (699, 0), (699, 2)})
+    t = on_gpu(x, "bf16")
+    got = sd.top_logits(t, K)
+    want = torch.sort(t.float(), dim=-1, descending=True, stable=True)
+    assert torch.equal(got.ids, want.indices[..., :K].int())
+    assert torch.equal(got.values, want.values[..., :K])
