@@ -46,7 +46,7 @@ def test_rounds(example):
         of = (torch.exp(s) * rest).sum(-1)
         loss = (p * (z - lse[..., None] - s.gather(-1, ids))).sum(-1) + left * (torch.log(left) - torch.log(of))
         loss = (loss * t["weight"].double()).sum()
-        assert abs(float(loss) - float(t["loss"])) <= 1e-4 * abs(float(loss))
+        assert abs(loss.item() - t["loss"].item()) <= 1e-4 * abs(loss.item())
         loss.backward()
         # float32 products of 64 terms before and of up to 80 rows behind the kernel: 2^-24 * (64 + 80)
         # of sizes up to a few times the result's largest, and the kernel's own 2^-16 of it
