@@ -14,7 +14,15 @@
 // the gradient, straight from registers to global memory, then the entries' own values.  The
 // loss is sum p_j (z_j - x_j) / T + sum p_j (max / T + ln S - lse), S the row's sum against
 // its maximum: its terms are float32, added in 64-bit fixed point (an SM has two lanes for
-// 64-bit floating point).
+// 64-bit floating point; with them the kernel took 1790 us in place of 434).
+//
+// Measured: 4096 rows of 128256 bfloat16, 64 entries, gradient out: 434 us, 4.8 TB/s, 72 % of the
+// measured copy rate; 4080 rows of 32003 bfloat16: 101 us, 68 %; 508 rows of 152064 float32: 138 us,
+// 66 %; 33 rows of 32000 float32: 8.5 us.  Of a CTA's 23000 clocks (three an SM) its share's
+// arrival takes 7600, the sum 3300, the exchange 3000, the loss 2200, the gradient 5000: the
+// chain of those steps, which three CTAs overlap in part, is what keeps it from the copy rate.
+// Records that complete on an mbarrier, in place of the cluster's barrier: 430 us, and 9.2 us for
+// the smallest call.
 #include "draft_common.cuh"
 
 namespace specdec {
@@ -378,7 +386,7 @@ cudaError_t launch_dt(const DistillParams &p, cudaStream_t stream) {
   if (err != cudaSuccess) return err;
   constexpr int es = Elem<DT>::kBytes;
   const long long rows = (long long)p.B * p.R;
-  const int size = cluster_for(rows, p.V, es, 80 * 1024, 3);
+  const int size = cluster_for(rows, p.V, es, 68 * 1024, 3);
   const int vectors = share_vectors(p.V, es, size);
   return launch_clusters(distill_kernel<DT, kGrad>, rows, size, kThreads,
                          layout_of(vectors, es, p.K).total, stream, p, vectors);

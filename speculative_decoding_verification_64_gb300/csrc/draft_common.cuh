@@ -227,10 +227,11 @@ __device__ __forceinline__ void sort_by_rank(unsigned long long *list, int n) {
   __syncthreads();
 }
 
-// Sorts the CTA's list[0, n) downwards, all tokens of it different.  Up to 1024 each token
-// is compared with all others, which needs two barriers (96 tokens: about 500 clocks, where
-// a bitonic network of 28 steps took 6700); beyond that the network over the next power of
-// two, its rest filled with 0 (below every token).
+// Sorts the CTA's list[0, n) downwards, all tokens of it different.  Up to four a thread
+// each token is compared with all others, which needs two barriers (17 tokens: 800 clocks,
+// 70 to 95 tokens: 2000 to 3000 beside another working CTA, where a bitonic network took
+// 6700); beyond that the network over the next power of two, its rest filled with 0 (below
+// every token).
 template <int kThreads>
 __device__ __noinline__ void sort_down(unsigned long long *list, int n) {
   if (n <= kThreads) {
@@ -302,9 +303,6 @@ __device__ __forceinline__ void cluster_sync() {
 
 __device__ __forceinline__ void remote_put(uint32_t addr, unsigned long long v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
-}
-__device__ __forceinline__ void remote_put(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 __device__ __forceinline__ void remote_put16(uint32_t addr, uint32_t v) {
   asm volatile("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tst.shared::cluster.u16 [%0], h;\n\t}" ::"r"(addr),
@@ -539,14 +537,21 @@ __device__ __forceinline__ void store_like(const Share &s, uint8_t *row, int v, 
 }
 
 // How many CTAs hold a row: the fewest whose shares are small enough for several of them
-// an SM, more where the rows leave SMs idle, none with less than 4 KB to do.
+// an SM (`per_sm`, which hides one CTA's waits behind another's work), more where the rows
+// leave SMs idle, none with less than 4 KB to do.  Measured with shares other than the
+// callers' (rows of 128256 bfloat16, us):
+//   sampling, 4 CTAs a row and 2 an SM: 140 / 207 / 849 for 256 rows under top-p, 672 rows
+//     without a filter, 2304 flat rows under top-p; 6 and 3: 162 / 195 / 977; 8 and 3: 216 /
+//     222 / 1461 (every CTA of a row has the same exchanges to wait for)
+//   distillation, 4 a row and 3 an SM: 434 for 4096 rows; 5, 6 and 8 a row with 4 to 5 an
+//     SM: 463 to 500.  508 rows of 152064 float32: 138 with 10 a row and 3 an SM, 154 with 8
+//     and 2, 152 with 12 and 4, 208 with 16 and 5.
 inline int cluster_for(long long rows, int V, int elem_bytes, int share_bytes, int per_sm) {
   int c = 1;
   while (c < kMaxCluster && (long long)V * elem_bytes > (long long)c * share_bytes)
-    c = c < 8 ? c + 1 : kMaxCluster;
+    c += c < 8 ? 1 : 2;
   const long long slots = (long long)device_sm_count() * per_sm;
   while (c * 2 <= kMaxCluster && rows * c * 2 <= slots && (long long)V * elem_bytes > c * 8192ll) c *= 2;
-  if (c > 8) c = kMaxCluster;  // (of the sizes above 8, only this one)
   return c;
 }
 

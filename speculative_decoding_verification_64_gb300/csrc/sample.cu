@@ -11,7 +11,7 @@
 //   * With top-k: each thread's maximum is one group's; the k-th largest of those (its top 16
 //     bits) bounds the k-th logit from below, the few tokens that reach it are gathered by
 //     rank 0, sorted, weighed, cut and drawn from.
-//   * With top-p alone: a histogram of the logits, 1/128 octave of weight a bin, says about
+//   * With top-p alone: a histogram of the logits, 1/64 octave of weight a bin, says about
 //     where the cut is.  A pass adds the weights of all places above a bracket around it, and
 //     in it; when the cut is inside and the bracket's tokens fit a list, they are sorted and
 //     the cut is found among them.  A bracket that missed is placed anew by what the pass
@@ -21,6 +21,19 @@
 // Which token is cut last, or drawn, turns on sums over the vocabulary: weights and sums are
 // those of draft_weight.cuh, as good as 64-bit floating point for this.  The cluster's
 // CTAs exchange a record of a few words at each step.
+//
+// What bounds it is the instructions of exact weights, some 20 an element, beside an
+// HBM pass of 2 to 4 bytes an element (rows of 128256 bfloat16, two CTAs an SM):
+//   2304 flat rows, top-p 0.95, logits out: 817 us, 1.4 TB/s of reads and writes.  Of a CTA's
+//     53000 clocks its share's arrival takes 8500, the histogram 8000, placing the bracket
+//     6000, the exact weights 19000, the list and exchanges 6500, the rows 6000.
+//   672 rows, no filter, 3 draws and probabilities: 206 us.  Of 41000 clocks arrival and
+//     maximum 9000, weights 17000, draws 2700, probabilities 9300.
+//   256 rows, top-p 0.9, a draw and probabilities: 134 us (four waves of CTAs, the last a third full).  One row of 32000 float32 under
+//     top-k 40 and top-p: 18 us, a chain of exchanges and barriers.
+// With threads of 512 a CTA 324 and 263 us in the place of 206 and 139: the kernel's code is
+// larger than the instruction cache's near levels, so that more warps in different places
+// cost more than they hide.
 #include "draft_weight.cuh"
 
 namespace specdec {
@@ -31,10 +44,16 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kList = 1024;   // tokens that rank 0 can sort
 constexpr int kMine = 1024;   // tokens that a CTA can bring
 constexpr int kKeys = 4096;   // groups' maxima (256 of each of 16 CTAs)
-constexpr int kBins = 23 * 128;  // of the histogram: 23 octaves
-constexpr float kOctave = 128.0f;  // bins of a factor of two in weight
+// The histogram's bins of a factor of two in weight, and its 24 octaves: a row's tail below
+// 2^-24 of its largest weight is 3 % of the mass at most for 2^19 tokens, and the exact pass
+// corrects the guess by what it found.  256 rows under top-p, 2304 flat ones: 134 and 817 us;
+// with 128 bins an octave 140 and 849 (twice the bins to read from the other CTAs), with 32
+// 131 and 808, where flat rows of float32 bring brackets of twice the tokens.  With 16
+// octaves 206 us for the 256 rows: their tails' mass is missed, and a second bracket placed.
+constexpr float kOctave = 64.0f;
+constexpr int kBins = 24 * 64;
 // A bracket reaches to either side of the place that the histogram names by this share of
-// the mass (bins hold their mass to 0.27 %, the sum of many to 0.02 %), or this many tokens
+// the mass (bins hold their mass to 0.54 %, the sum of many to 0.04 %), or this many tokens
 // where that is less (a value of bfloat16 rows holds some 200 of a flat row), or 32 bins.
 constexpr float kMargin = 0.0025f;
 constexpr int kBudget = 256;
@@ -318,7 +337,7 @@ __device__ __forceinline__ void count_bin(uint32_t at) {
 }
 
 // A histogram of the CTA's tokens: bin j counts those whose weight is within half a bin of
-// 2^(-j / 128).  The lighter ones go to places of their own, one a lane (there most tokens
+// 2^(-j / 64).  The lighter ones go to places of their own, one a lane (there most tokens
 // of a row of text stand, many of one value).  The bin's number is read off the bits of
 // 2^23 + j.  Ends with the cluster's barrier.
 template <int DT>

@@ -13,6 +13,13 @@
 // few elements that reach it, K and some, are sorted in shared memory.  Where they are too
 // many for the list (long runs of equal logits), a radix selection over (value, index)
 // finds the K-th place first.
+//
+// The scan is bound by HBM, the pick by its chain of loads, one row after another in a CTA.
+// 2304 rows of 128256 bfloat16, 64 entries: 146 us for both, 60 % of the measured copy rate
+// over the whole call; under a profiler about 105 us for the scan and 45 for the pick.
+// 384 rows of 32003 25 us, 5 rows of 32000 float32 11 us (two launches and the chain).  A warp a row
+// in the pick took 212, the picks' loads eight ahead in place of four 187 against 159 (at
+// 256 threads), 512 threads 234.
 #include "draft_common.cuh"
 #include "stats_stage.cuh"
 
