@@ -8,7 +8,7 @@
 // whose cumulative mass exceeds u times the kept mass.
 //
 // A row is held in shared memory by a cluster of CTAs and read from HBM once.
-//   * With top-k: each thread's maximum is one group's; the k-th largest of those (its top 16
+//   * With top-k: the k-th largest of the maxima of some hundred groups of tokens (its top 16
 //     bits) bounds the k-th logit from below, the few tokens that reach it are gathered by
 //     rank 0, sorted, weighed, cut and drawn from.
 //   * With top-p alone: a histogram of the logits, 1/64 octave of weight a bin, says about
@@ -30,7 +30,8 @@
 //   672 rows, no filter, 3 draws and probabilities: 206 us.  Of 41000 clocks arrival and
 //     maximum 9000, weights 17000, draws 2700, probabilities 9300.
 //   256 rows, top-p 0.9, a draw and probabilities: 134 us (four waves of CTAs, the last a third full).  One row of 32000 float32 under
-//     top-k 40 and top-p: 18 us, a chain of exchanges and barriers.
+//     top-k 40 and top-p: 15 us, a chain of exchanges and barriers (and of instructions that
+//     are not cached yet).
 // With threads of 512 a CTA 324 and 263 us in the place of 206 and 139: the kernel's code is
 // larger than the instruction cache's near levels, so that more warps in different places
 // cost more than they hide.
@@ -43,6 +44,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kList = 1024;   // tokens that rank 0 can sort
 constexpr int kMine = 1024;   // tokens that a CTA can bring
+constexpr int kFewK = 128;    // top-k up to which some 500 groups name the bound
 constexpr int kKeys = 4096;   // groups' maxima (256 of each of 16 CTAs)
 // The histogram's bins of a factor of two in weight, and its 24 octaves: a row's tail below
 // 2^-24 of its largest weight is 3 % of the mass at most for 2^19 tokens, and the exact pass
@@ -85,7 +87,7 @@ struct SampleSmem {
   float piece[64], whole;   // of the histogram's mass
   int bracket_bin, bracket_first, bracket_last;
   float bracket_before;
-  unsigned total[16];
+  unsigned bound;      // of the k-th largest key
   int count[kWarps];
   int listed[kMaxCluster];  // tokens on each CTA's list
   int n_mine, n_kept;
@@ -164,16 +166,6 @@ __device__ __forceinline__ u64 cta_exscan(u64 v, u64 *red, u64 &total) {
     total += red[w];
   }
   return pre + inc - v;
-}
-
-template <int DT>
-__device__ __forceinline__ void load_share(const Share &s, const uint8_t *buf, int v, float *x) {
-  if (v < s.nvec) {
-    widen<DT>(*reinterpret_cast<const uint4 *>(buf + (size_t)v * 16), x);
-  } else {
-#pragma unroll
-    for (int e = 0; e < Elem<DT>::kN; ++e) x[e] = -INFINITY;
-  }
 }
 
 // What a pass over the CTA's share found: mass down to the cut, and of everything; tokens
@@ -492,14 +484,22 @@ __device__ __forceinline__ void gather(const Share &s, const uint8_t *buf, const
                                        SampleSmem &sm) {
   constexpr int kN = Elem<DT>::kN;
   for (int v = threadIdx.x; v < s.nvec; v += kThreads) {
+    const uint8_t *from = buf + (size_t)v * 16;
+    if (!(max_of<DT>(vector_max<DT>(*reinterpret_cast<const uint4 *>(from), no_max<DT>())) >= lo.value))
+      continue;
+    unsigned reach = 0;
     float x[kN];
-    load_share<DT>(s, buf, v, x);
-    const int at = s.first + v * kN;
+    widen<DT>(*reinterpret_cast<const uint4 *>(from), x);
 #pragma unroll
-    for (int e = 0; e < kN; ++e) {
-      if (!lo.holds(x[e], at + e)) continue;
+    for (int e = 0; e < kN; ++e) reach |= x[e] >= lo.value ? 1u << e : 0u;
+    while (reach) {
+      const int e = __ffs(reach) - 1;
+      reach &= reach - 1;
+      const float y = get_elem<DT>(from + e * Elem<DT>::kBytes);
+      const int at = s.first + v * kN + e;
+      if (!lo.holds(y, at)) continue;
       const int k = atomicAdd(&sm.n_mine, 1);
-      if (k < kMine) sm.mine[k] = place_of(x[e], at + e);
+      if (k < kMine) sm.mine[k] = place_of(y, at);
     }
   }
 }
@@ -548,7 +548,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     mbar_arrive_expect_tx(&sm.tabled, (uint32_t)sizeof(sm.table));
     bulk_copy_g2s(sm.table, &g_table, (uint32_t)sizeof(sm.table), &sm.tabled);
   }
-  if (tid < 16) sm.total[tid] = 0;
   pdl_wait();
   pdl_launch_dependents();
   if (tid == 0) share_copy(s, buf, sm.in);
@@ -599,8 +598,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
 #pragma unroll
   for (int i = 0; i < kChunks; ++i) gm[i] = max_of<DT>(top[i]);
   float M = fmax_nan(fmax_nan(gm[0], gm[1]), fmax_nan(gm[2], gm[3]));
-  const int sub = size <= 2 ? 4 : size == 4 ? 2 : 1;  // groups a thread
-  const int groups = kThreads * sub * size;
+  // top-k's groups: for small k a warp's lanes share some, 256 to 896 in all; else each thread
+  // has one to four
+  const bool few = k <= kFewK;
+  const int sub = few || size > 4 || size == 3 ? 1 : size == 4 ? 2 : 4;
+  const int fold = !few || size < 4 ? 1 : size < 8 ? 2 : size < 16 ? 4 : 8;
+  const int own = kThreads * sub / fold, groups = own * size;
   cluster_wait();
   if (k > 0) {
     if (sub == 2) {
@@ -610,11 +613,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       gm[0] = M;
     }
 #pragma unroll 1
-    for (int q = 0; q < size; ++q) {
-      const uint32_t to = cluster_addr(smem_addr(&sm.key[(rank * kThreads + tid) * sub]), q);
+    for (int d = 1; d < fold; d *= 2) gm[0] = fmax_nan(gm[0], __shfl_xor_sync(kFull, gm[0], d));
+    if (tid % fold == 0) {
+#pragma unroll 1
+      for (int q = 0; q < size; ++q) {
+        const uint32_t to = cluster_addr(smem_addr(&sm.key[rank * own + tid / fold * sub]), q);
 #pragma unroll
-      for (int i = 0; i < kChunks; ++i)
-        if (i < sub) remote_put16(to + 2u * i, order_key(gm[i]) >> 16);
+        for (int i = 0; i < kChunks; ++i)
+          if (i < sub) remote_put16(to + 2u * i, order_key(gm[i]) >> 16);
+      }
     }
   }
   M = cta_max_nan<kWarps>(M, sm.redf[0]);
@@ -643,16 +650,36 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
 
   if (!st && k > 0) {
     // ---- top-k: the few largest, by rank 0 --------------------------------------------
-    uint32_t bound = 0;
-    for (int bit = 15; bit >= 0; --bit) {
-      const uint32_t t = bound | 1u << bit;
-      unsigned m = 0;
-      for (int i = tid; i < groups; i += kThreads) m += sm.key[i] >= t;
-      m = __reduce_add_sync(kFull, m);
-      if (lane == 0 && m) atomicAdd(&sm.total[bit], m);
-      __syncthreads();
-      if (sm.total[bit] >= (unsigned)k) bound = t;
+    // (bit by bit, by one warp: with a barrier of the CTA for every bit this took 8000 to 9500
+    // of a small row's 30000 clocks)
+    if (warp == 0) {
+      constexpr int kHeld = 8;  // pairs of keys that a lane holds
+      const uint32_t *pairs = reinterpret_cast<const uint32_t *>(sm.key);
+      uint32_t held[kHeld], found = 0;
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) held[i] = lane + 32 * i < groups / 2 ? pairs[lane + 32 * i] : 0;
+      const uint32_t most = order_key(M) >> 16;
+#pragma unroll 1
+      for (int bit = 15; bit >= 0; --bit) {
+        const uint32_t t = found | 1u << bit;
+        if (t > most) continue;
+        unsigned m0 = 0, m1 = 0;
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+          m0 += (held[i] & 0xFFFFu) >= t;
+          m1 += (held[i] >> 16) >= t;
+        }
+#pragma unroll 4
+        for (int i = lane + 32 * kHeld; i < groups / 2; i += 32) {
+          m0 += (pairs[i] & 0xFFFFu) >= t;
+          m1 += (pairs[i] >> 16) >= t;
+        }
+        if (__reduce_add_sync(kFull, m0 + m1) >= (unsigned)k) found = t;
+      }
+      if (lane == 0) sm.bound = found;
     }
+    __syncthreads();
+    const uint32_t bound = sm.bound;
     // At least k tokens (or all that are finite) stand at places >= from, fewer than k at
     // places >= H.  Where those at `from` are too many to list, halves of what is between:
     // at the end exactly k.
