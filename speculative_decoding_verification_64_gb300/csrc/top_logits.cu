@@ -15,11 +15,11 @@
 // finds the K-th place first.
 //
 // The scan is bound by HBM, the pick by its chain of loads, one row after another in a CTA.
-// 2304 rows of 128256 bfloat16, 64 entries: 146 us for both, 60 % of the measured copy rate
-// over the whole call; under a profiler about 105 us for the scan and 45 for the pick.
-// 384 rows of 32003 25 us, 5 rows of 32000 float32 11 us (two launches and the chain).  A warp a row
-// in the pick took 212, the picks' loads eight ahead in place of four 187 against 159 (at
-// 256 threads), 512 threads 234.
+// 2304 rows of 128256 bfloat16, 64 entries: 135 us for both, 65 % of the measured copy rate
+// over the whole call; under a profiler the scan takes 105 us.
+// 384 rows of 32003 20 us, 5 rows of 32000 float32 11 us (two launches and the chain).  For
+// the 2304 rows, in the place of 159 at that time: a warp a row in the pick 212, its loads
+// eight ahead in place of four 187, 512 threads 234.
 #include "draft_common.cuh"
 #include "stats_stage.cuh"
 
@@ -178,14 +178,19 @@ __global__ void __launch_bounds__(kThreads, 1) top_scan_kernel(const TopParams p
 
 // Threads of a row's CTA: 256, or 128 for more rows than the SMs hold CTAs of 256 of
 // (2304 rows of 128256 tokens, 64 entries: 146 us in both kernels against 159 with 256;
-// 384 rows of 32003: 30.7 us against 24.6).
+// 384 rows of 32003: 30.7 us against 24.6; both before the vectors were noted, which gave 135
+// and 20).  The smaller ones get 64 registers, eight to an SM: 135 us, with 72 registers and
+// seven 141, with 48 and ten 141, with 40 and twelve 154.
 constexpr int kFewThreads = 128, kManyThreads = 256;
 constexpr int kFewFrom = 8;   // CTAs an SM from which a row gets the fewer
 constexpr int kKeys = 2048;   // maxima that the bound is found among
 constexpr int kList = 1024;   // tokens that reach it and can be sorted
 constexpr int kBatch = 1024;  // groups looked at together
+constexpr int kAhead = 4;     // loads of a thread under way together
+constexpr int kVecs = 256;    // vectors with such tokens that a warp notes
 constexpr int kDigit = 10;    // bits of a digit of the radix selection
 
+template <int kPickThreads>
 struct PickSmem {
   union {
     uint16_t key[kKeys];
@@ -193,7 +198,8 @@ struct PickSmem {
   } u;
   unsigned long long list[kList];
   uint16_t hit[kBatch];
-  float red[2][kManyThreads / 32];
+  uint16_t vec[kPickThreads / 32][kVecs];
+  float red[2][kPickThreads / 32];
   int n, hits, digit, need;
 };
 
@@ -207,13 +213,17 @@ struct Take {
 };
 
 // Every element of the groups whose maximum reaches take.from, and the row's edges, that
-// reaches it too.  The groups of a batch are named first, then all of their vectors are
-// loaded, several a thread on their way together.
+// reaches it too.  The groups of a batch are named first, then their vectors are loaded,
+// several a thread on their way together, and those with such an element noted; a warp
+// looks at the noted ones' elements together (one vector of 25 holds one: looked at as they came,
+// nearly every step of a warp went through that).
 template <int DT, int kPickThreads>
 __device__ __noinline__ void candidates(const uint8_t *row, int V, int spr, const float *group,
-                                        Take take, PickSmem &sm) {
-  constexpr int es = Elem<DT>::kBytes, kN = Elem<DT>::kN, kAhead = 4;
-  const int t = threadIdx.x;
+                                        Take take, PickSmem<kPickThreads> &sm) {
+  constexpr int es = Elem<DT>::kBytes, kN = Elem<DT>::kN;
+  const int t = threadIdx.x, lane = t & 31;
+  const unsigned below = (1u << lane) - 1;
+  uint16_t *vec = sm.vec[t >> 5];
   const UnitGeom g0 = geometry(row, V, spr, 0, es);
   const int tail_begin = min(g0.tail_begin, V);        // (past it for rows that end before a boundary)
   const int inside = (tail_begin - g0.head_end) / kN;  // vectors of the row's inside
@@ -240,28 +250,39 @@ __device__ __noinline__ void candidates(const uint8_t *row, int V, int spr, cons
       const bool hit = at < groups && __ldg(group + at) >= take.from;
       const unsigned all = __ballot_sync(kFull, hit);
       int base_hit = 0;
-      if (all && (t & 31) == 0) base_hit = atomicAdd(&sm.hits, __popc(all));
+      if (all && lane == 0) base_hit = atomicAdd(&sm.hits, __popc(all));
       base_hit = __shfl_sync(kFull, base_hit, 0);
-      if (hit)
-        sm.hit[base_hit + __popc(all & ((1u << (t & 31)) - 1))] = (uint16_t)(i * kPickThreads + t);
+      if (hit) sm.hit[base_hit + __popc(all & below)] = (uint16_t)(i * kPickThreads + t);
     }
     __syncthreads();
     const int n = sm.hits * 32;  // vectors: 32 a group
+    int noted = 0;
 #pragma unroll 1
-    for (int i0 = t; i0 < n; i0 += kAhead * kPickThreads) {
+    for (int i0 = t; i0 - lane < n; i0 += kAhead * kPickThreads) {
       uint4 w[kAhead];
-      int v[kAhead];
+      int v[kAhead];  // of the batch
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         const int q = i0 + i * kPickThreads;
-        v[i] = q < n ? (g + sm.hit[q >> 5]) * 32 + (q & 31) : inside;
-        if (v[i] < inside) w[i] = __ldg(base + v[i]);
+        v[i] = q < n ? sm.hit[q >> 5] * 32 + (q & 31) : inside;
+        if (v[i] < inside - 32 * g) w[i] = __ldg(base + 32 * g + v[i]);
       }
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        if (v[i] >= inside || !(max_of<DT>(vector_max<DT>(w[i], no_max<DT>())) >= take.from)) continue;
+        const bool some = v[i] < inside - 32 * g &&
+                          max_of<DT>(vector_max<DT>(w[i], no_max<DT>())) >= take.from;
+        const unsigned all = __ballot_sync(kFull, some);
+        if (some) vec[noted + __popc(all & below)] = (uint16_t)v[i];
+        noted += __popc(all);
+      }
+      // the noted ones, before there are too many or no more come
+      if (noted <= kVecs - 32 * kAhead && i0 - lane + kAhead * kPickThreads < n) continue;
+      __syncwarp();
+#pragma unroll 1
+      for (int k = lane; k < noted; k += 32) {
+        const int at = 32 * g + vec[k];
         float x[kN];
-        widen<DT>(w[i], x);
+        widen<DT>(__ldg(base + at), x);
         unsigned reach = 0;
 #pragma unroll
         for (int e = 0; e < kN; ++e) reach |= x[e] >= take.from ? 1u << e : 0u;
@@ -271,9 +292,11 @@ __device__ __noinline__ void candidates(const uint8_t *row, int V, int spr, cons
           float y = x[0];
 #pragma unroll
           for (int q = 1; q < kN; ++q) y = e == q ? x[q] : y;
-          found(y, g0.head_end + v[i] * kN + e);
+          found(y, g0.head_end + at * kN + e);
         }
       }
+      noted = 0;
+      __syncwarp();
     }
   }
   const int n_head = g0.head_end, n_edge = n_head + V - tail_begin;
@@ -286,8 +309,9 @@ __device__ __noinline__ void candidates(const uint8_t *row, int V, int spr, cons
 }
 
 template <int DT, int kPickThreads>
-__global__ void __launch_bounds__(kPickThreads) top_pick_kernel(const TopParams p) {
-  __shared__ PickSmem sm;
+__global__ void __launch_bounds__(kPickThreads, kPickThreads == kFewThreads ? 8 : 1)
+    top_pick_kernel(const TopParams p) {
+  __shared__ PickSmem<kPickThreads> sm;
   static_assert(kStageBytes == 16 * 32 * 16, "16 vectors a lane");
   constexpr int kPickWarps = kPickThreads / 32;
   constexpr int es = Elem<DT>::kBytes;
