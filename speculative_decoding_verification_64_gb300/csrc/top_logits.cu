@@ -180,7 +180,8 @@ __global__ void __launch_bounds__(kThreads, 1) top_scan_kernel(const TopParams p
 // (2304 rows of 128256 tokens, 64 entries: 146 us in both kernels against 159 with 256;
 // 384 rows of 32003: 30.7 us against 24.6; both before the vectors were noted, which gave 135
 // and 20).  The smaller ones get 64 registers, eight to an SM: 135 us, with 72 registers and
-// seven 141, with 48 and ten 141, with 40 and twelve 154.
+// seven 141, with 48 and ten 141, with 40 and twelve 154; the larger ones 80 registers and
+// three to an SM: 20 us for the 384 rows, with 94 and two 25, with 64 and four 21.
 constexpr int kFewThreads = 128, kManyThreads = 256;
 constexpr int kFewFrom = 8;   // CTAs an SM from which a row gets the fewer
 constexpr int kKeys = 2048;   // maxima that the bound is found among
@@ -309,7 +310,7 @@ __device__ __noinline__ void candidates(const uint8_t *row, int V, int spr, cons
 }
 
 template <int DT, int kPickThreads>
-__global__ void __launch_bounds__(kPickThreads, kPickThreads == kFewThreads ? 8 : 1)
+__global__ void __launch_bounds__(kPickThreads, kPickThreads == kFewThreads ? 8 : 3)
     top_pick_kernel(const TopParams p) {
   __shared__ PickSmem<kPickThreads> sm;
   static_assert(kStageBytes == 16 * 32 * 16, "16 vectors a lane");
