@@ -15,9 +15,9 @@
 // finds the K-th place first.
 //
 // The scan is bound by HBM, the pick by its chain of loads, one row after another in a CTA.
-// 2304 rows of 128256 bfloat16, 64 entries: 135 us for both, 65 % of the measured copy rate
-// over the whole call; under a profiler the scan takes 105 us.
-// 384 rows of 32003 20 us, 5 rows of 32000 float32 11 us (two launches and the chain).  For
+// 2304 rows of 128256 bfloat16, 64 entries: 132 us for both, 66 % of the measured copy rate
+// over the whole call.
+// 384 rows of 32003 19 us, 5 rows of 32000 float32 11 us (two launches and the chain).  For
 // the 2304 rows, in the place of 159 at that time: a warp a row in the pick 212, its loads
 // eight ahead in place of four 187, 512 threads 234.
 #include "draft_common.cuh"
@@ -51,6 +51,55 @@ __device__ __forceinline__ int signed_key(float x) {
 }
 __device__ __forceinline__ float signed_float(int k) {
   return __int_as_float(k ^ (k >> 31 & 0x7FFFFFFF));
+}
+
+// The maxima over a warp of each of a stage's groups (the row's edge elements are in the first
+// group of stage 0): the lane's `group` is that of group `of`, where that is one.  Returns the
+// maximum of all.  A NaN comes out as the positive one, whose key is the largest.
+template <int DT>
+__device__ __forceinline__ float group_maxima(const LaneData<DT> &d, int lane, float &group, int &of) {
+  if (DT == SPECDEC_F32) {
+    int mine = signed_key(-INFINITY), all = mine;
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) {
+      float f = max_of<DT>(vector_max<DT>(d.v[k], no_max<DT>()));
+      if (k == 0) f = fmax_nan(f, d.edge);
+      const int m = __reduce_max_sync(kFull, signed_key(f));
+      if (lane == k) mine = m;
+      all = max(all, m);
+    }
+    group = signed_float(mine);
+    of = lane;
+    return signed_float(all);
+  }
+  // bfloat16: groups k and k + 8 in one word; each step halves a lane's words and joins two
+  // lanes' (16 integer maxima over the warp in their place: 20 us for
+  // 384 rows of 32003, 19 with this)
+  auto max2 = [](uint32_t a, uint32_t b) {
+    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+    return a;
+  };
+  uint32_t w[kGroups / 2];
+#pragma unroll
+  for (int k = 0; k < kGroups / 2; ++k) {
+    const uint32_t a = vector_max<DT>(d.v[k], k == 0 ? 0xFF800000u | __float_as_uint(d.edge) >> 16 : no_max<DT>());
+    const uint32_t b = vector_max<DT>(d.v[k + kGroups / 2], no_max<DT>());
+    w[k] = max2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+  }
+#pragma unroll
+  for (int half = kGroups / 4; half >= 1; half /= 2) {
+    const bool upper = lane & (4 * half);
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      const uint32_t keep = upper ? w[i + half] : w[i], send = upper ? w[i] : w[i + half];
+      w[i] = max2(keep, __shfl_xor_sync(kFull, send, 4 * half));
+    }
+  }
+  uint32_t m = max2(w[0], __shfl_xor_sync(kFull, w[0], 2));
+  m = max2(m, __shfl_xor_sync(kFull, m, 1));
+  group = lane & 1 ? bf16_hi(m) : bf16_lo(m);
+  of = lane & 2 ? kGroups : (lane >> 2) + (lane & 1) * (kGroups / 2);
+  return signed_float(__reduce_max_sync(kFull, signed_key(max_of<DT>(m))));
 }
 
 constexpr float kGaveUp = -2.0f;  // a stage's sum, where its copy was not waited for
@@ -115,14 +164,40 @@ __global__ void __launch_bounds__(kThreads, 1) top_scan_kernel(const TopParams p
   }
 
   const float c = temperature_scale(p.temperature);
-  for (long long q = warp; q < n_local * kUnit; q += kConsumerWarps) {
-    const long long i = q / kUnit;
-    const int t = (int)(q - i * kUnit);
-    const long long g = first + i * stride;
-    const int row = (int)(g / upr);
+  // The CTA's stages in turn among its warps: stage t of unit i, kConsumerWarps further each
+  // time.  (Quotients by additions: four divisions of 64 bits were 300 of a stage's 1000
+  // instructions.)
+  constexpr int kWhole = kConsumerWarps / kUnit, kPart = kConsumerWarps % kUnit;
+  static_assert(kWhole < kSlots, "a warp's next stage is in the ring's next round at most");
+  UnitCursor cur, unit;
+  cur.init(first + warp / kUnit * stride, kWhole * stride, upr);
+  unit.init(0, stride, upr);
+  int next = warp % kUnit;
+  uint32_t slot_next = warp / kUnit, use_next = 0;
+  for (long long i = warp / kUnit; i < n_local;) {
+    const int t = next, row = cur.row;
     const uint8_t *at = row_at(row);
-    const UnitGeom u = geometry(at, p.V, p.spr, (int)(g - (long long)row * upr), es);
-    const uint32_t slot = (uint32_t)(i % kSlots), use = (uint32_t)(i / kSlots);
+    const UnitGeom u = geometry(at, p.V, p.spr, cur.ju, es);
+    const uint32_t slot = slot_next, use = use_next;
+    i += kWhole;
+    slot_next += kWhole;
+    next += kPart;
+    cur.advance(upr);
+    if (next >= kUnit) {
+      next -= kUnit;
+      ++i;
+      ++slot_next;
+      cur.row += unit.drow;
+      cur.ju += unit.dj;
+      if (cur.ju >= upr) {
+        cur.ju -= upr;
+        ++cur.row;
+      }
+    }
+    if (slot_next >= kSlots) {
+      slot_next -= kSlots;
+      ++use_next;
+    }
     const bool real = t < u.nst;
     LaneData<DT> d;
     d.edge = -INFINITY;
@@ -146,25 +221,15 @@ __global__ void __launch_bounds__(kThreads, 1) top_scan_kernel(const TopParams p
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.empty[slot]);
     if (!real) continue;
-    float wm = -INFINITY, sum = kGaveUp;
-    int group = signed_key(-INFINITY);
+    float wm = -INFINITY, sum = kGaveUp, group = -INFINITY;
+    int of = lane;  // the group whose maximum this lane has
     if (ok) {
-      // (a NaN comes out of these maxima as the positive one, whose key is the largest)
-      int all = signed_key(-INFINITY);
-#pragma unroll
-      for (int k = 0; k < kVecPerLane; ++k) {
-        float f = max_of<DT>(vector_max<DT>(d.v[k], no_max<DT>()));
-        if (k == 0) f = fmax_nan(f, d.edge);  // the row's edge elements, in stage 0
-        const int m = __reduce_max_sync(kFull, signed_key(f));
-        if (lane == k) group = m;
-        all = max(all, m);
-      }
-      wm = signed_float(all);
+      wm = group_maxima<DT>(d, lane, group, of);
       sum = wm > -INFINITY ? warp_sum(lane_sum<DT>(d, c, wm)) : 0.0f;
     }
     const long long at_part = (long long)row * p.spr + u.j0 + t;
     if (lane == 0) p.part[at_part] = make_float2(wm, sum);
-    if (lane < kGroups) p.group[at_part * kGroups + lane] = signed_float(group);
+    if (of < kGroups) p.group[at_part * kGroups + of] = group;
   }
   if (sm.abort_flag && lane == 0) {
     const unsigned long long t0 = global_timer_ns();
