@@ -13,16 +13,19 @@
 // and no difference of two near equal ones); one exchange of five words between the CTAs;
 // the gradient, straight from registers to global memory, then the entries' own values.  The
 // loss is sum p_j (z_j - x_j) / T + sum p_j (max / T + ln S - lse), S the row's sum against
-// its maximum: its terms are float32, added in 64-bit fixed point (an SM has two lanes for
-// 64-bit floating point; with them the kernel took 1790 us in place of 434).
+// its maximum: parts of some units each, whose sum may be a thousandth.  The entries' terms and
+// weights are pairs of float32 added in 64-bit fixed point (an SM has two lanes for 64-bit
+// floating point; with them the kernel took 1790 us in place of 434), and the last few steps of
+// a row are 64-bit.
 //
-// Measured: 4096 rows of 128256 bfloat16, 64 entries, gradient out: 434 us, 4.8 TB/s, 72 % of the
-// measured copy rate; 4080 rows of 32003 bfloat16: 101 us, 68 %; 508 rows of 152064 float32: 138 us,
-// 66 %; 33 rows of 32000 float32: 8.5 us.  Of a CTA's 23000 clocks (three an SM) its share's
+// Measured: 4096 rows of 128256 bfloat16, 64 entries, gradient out: 450 us, 4.7 TB/s, 69 % of the
+// measured copy rate; 4080 rows of 32003 bfloat16: 107 us, 64 %; 508 rows of 152064 float32: 146 us,
+// 62 %; 33 rows of 32000 float32: 10.3 us.  Of a CTA's 23000 clocks (three an SM) its share's
 // arrival takes 7600, the sum 3300, the exchange 3000, the loss 2200, the gradient 5000: the
 // chain of those steps, which three CTAs overlap in part, is what keeps it from the copy rate.
-// Records that complete on an mbarrier, in place of the cluster's barrier: 430 us, and 9.2 us for
-// the smallest call.
+// Records that complete on an mbarrier, in place of the cluster's barrier: 1 % less, and 1 us more for
+// the smallest call.  The pairs of the loss cost 4 % (434 us with float32 terms, whose loss was off
+// by 2e-7; with the last steps in 64-bit floating point 485).
 #include "draft_common.cuh"
 
 namespace specdec {
@@ -35,8 +38,8 @@ constexpr int kPerThread = SPECDEC_MAX_TOPK / kThreads;
 struct DistillSmem {
   Exchange ex;
   Arrival in;
-  long long terms[2][kWarps];
-  float red[5][kWarps];
+  long long terms[3][kWarps];
+  float red[4][kWarps];
   int status;
   int entries;
 };
@@ -58,6 +61,70 @@ __host__ __device__ inline Layout layout_of(int vectors, int elem_bytes, int K) 
   l.pos = l.bits + (vectors * (16 / elem_bytes) + 31) / 32 * 4;
   l.total = l.pos + K * 12;
   return l;
+}
+
+// ---- what the loss is made of, to about 1e-9 ------------------------------------------
+
+// A value as the sum of two.
+struct Two {
+  float hi, lo;
+};
+
+// (a - b) / T
+__device__ __forceinline__ Two over_t(float a, float b, float inv_t, float inv_t_low) {
+  const float d = a - b, z = d - a;
+  const float d_low = (a - (d - z)) - (b + z);
+  const float y = d * inv_t;
+  return {y, fmaf(d, inv_t, -y) + fmaf(d, inv_t_low, d_low * inv_t)};
+}
+
+// e^y for |y| < 87 (and no more than float32's beyond): y log2(e) = n + g, |g| <= 1/2, and
+// 2^g = 1 + g ln 2 + r by the series, the first two terms exact.
+__device__ __forceinline__ Two exp_two(Two y) {
+  if (!(fabsf(y.hi) < 87.0f)) return {expf(y.hi), 0.0f};
+  constexpr float kHi = kLog2e, kLo = 1.9259629e-8f, kMagic = 12582912.0f;  // 1.5 * 2^23
+  constexpr float kLn2 = 0.693147181f, kLn2Low = -1.90465422e-9f;
+  const float t = fmaf(y.hi, kHi, kMagic);
+  const float g = fmaf(y.hi, kHi, kMagic - t) + fmaf(y.hi, kLo, y.lo * kHi);
+  float r = 1.32154867e-6f;  // ln^i 2 / i!, i = 8 .. 2
+  r = fmaf(g, r, 1.52527338e-5f);
+  r = fmaf(g, r, 1.54035304e-4f);
+  r = fmaf(g, r, 1.33335581e-3f);
+  r = fmaf(g, r, 9.61812911e-3f);
+  r = fmaf(g, r, 5.55041087e-2f);
+  r = fmaf(g, r, 2.40226507e-1f);
+  const float h = g * kLn2, one = 1.0f + h;
+  const float low = (h - (one - 1.0f)) + fmaf(g, kLn2Low, fmaf(g, kLn2, -h));
+  const float scale = __int_as_float((__float_as_int(t) - __float_as_int(kMagic) + 127) << 23);
+  return {one * scale, fmaf(g * g, r, low) * scale};
+}
+
+__device__ __forceinline__ long long fixed_two(Two x) {
+  return __float2ll_rn(x.hi * kTerm) + __float2ll_rn(x.lo * kTerm);
+}
+
+// ln(v + low) in units of 2^-40, v > 0 a normal number: v = 2^e f with f in [3/4, 3/2), ln f =
+// 2 atanh u by its series, u = (f - 1) / (f + 1) as a pair, |u| <= 1/5.
+__device__ __forceinline__ long long ln_fixed(float v, float low) {
+  const int e = (__float_as_int(v) - 0x3F400000) >> 23;
+  const float f = __int_as_float(__float_as_int(v) - (e << 23));
+  const float num = f - 1.0f, den = f + 1.0f, den_low = f - (den - 1.0f);
+  const float by = __fdividef(1.0f, den), u = num * by, u2 = u * u;
+  const float u_low = by * (fmaf(-u, den, num) - u * den_low);
+  float r = 1.0f / 15.0f;
+  r = fmaf(u2, r, 1.0f / 13.0f);
+  r = fmaf(u2, r, 1.0f / 11.0f);
+  r = fmaf(u2, r, 1.0f / 9.0f);
+  r = fmaf(u2, r, 1.0f / 7.0f);
+  r = fmaf(u2, r, 1.0f / 5.0f);
+  r = fmaf(u2, r, 1.0f / 3.0f);
+  const float rest = 2.0f * fmaf(u * u2, r, u_low) + __fdividef(low, v);
+  return (long long)e * 762123384786ll + fixed_two({2.0f * u, rest});
+}
+
+// a b of numbers in units of 2^-40
+__device__ __forceinline__ long long mul_fixed(long long a, long long b) {
+  return (long long)((unsigned long long)__mul64hi(a, b) << 24 | (unsigned long long)(a * b) >> 40);
 }
 
 template <int DT, bool kGrad>
@@ -151,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
   const float c = temperature_scale(p.temperature);
   float m = -INFINITY;
   const unsigned long long(*got)[kWords] = nullptr;
-  float coef = 0.0f, M = 0.0f, inv_s = 0.0f, S = 0.0f, left = 0.0f, of = 0.0f, zs = 1.0f;
+  float coef = 0.0f, M = 0.0f, inv_s = 0.0f, left = 0.0f, inv_zs = 1.0f;
   long long mass = 0;
   int st = 0;
   if (w != 0.0f) {
@@ -163,19 +230,31 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
       zmax = cta_max_nan<kWarps>(zmax, sm.red[0]);
       if (some && !(zmax > -INFINITY)) status |= SPECDEC_ROW_NONFINITE;
     }
-    // (1 / T in two parts, so that z / T is rounded once)
-    auto y_of = [&](float zj) {
-      const float dz = zj - zmax;
-      return fmaf(dz, p.inv_t, -lse) + dz * p.inv_t_low;
-    };
     if (!p.lse) {
-      zs = 0.0f;
+      // (the loss goes by the sum of the shares that this leads to: it need not be exact)
+      float zs = 0.0f;
 #pragma unroll
       for (int i = 0; i < kPerThread; ++i)
-        if (z[i] > -INFINITY) zs += expf(y_of(z[i]));
-      zs = cta_sum<kWarps>(zs, sm.red[1]);
+        if (z[i] > -INFINITY) zs += ex2_approx((z[i] - zmax) * c);
+      inv_zs = 1.0f / cta_sum<kWarps>(zs, sm.red[1]);
     }
-    const float inv_zs = 1.0f / zs;
+
+    // the shares of this CTA's entries
+    float pj[kPerThread];
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+      pj[i] = 0.0f;
+      if (id[i] < s.begin || id[i] >= s.end) continue;
+      mine = 1;
+      if (!(z[i] > -INFINITY)) continue;
+      Two y = over_t(z[i], zmax, p.inv_t, p.inv_t_low);
+      const float l = y.hi - lse, q = l - y.hi;
+      y.lo += (y.hi - (l - q)) - (lse + q);
+      y.hi = l;
+      const Two e = exp_two(y);
+      pj[i] = (e.hi + e.lo) * inv_zs;
+    }
 
     // the largest logit, as the copies land
     uint32_t top = no_max<DT>();
@@ -192,36 +271,32 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
     const float ref = m > -INFINITY ? m : 0.0f;
 
     // this CTA's entries: noted, and taken out of the row
-    float at_s = 0.0f, large = 0.0f;
-    long long terms = 0, at_mass = 0;  // sum p_j (z_j - x_j) / T, and of p_j
-    int mine = 0;
+    float large = 0.0f;
+    long long terms = 0, at_mass = 0, at_s = 0;  // sums of p_j (z_j - x_j) / T, p_j, e^((x_j - ref) / T)
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
       if (id[i] < s.begin || id[i] >= s.end) continue;
-      mine = 1;
       const int at = id[i] - s.first;
       if (atomicOr(&bits[at >> 5], 1u << (at & 31)) >> (at & 31) & 1u) {
         status |= SPECDEC_ROW_BAD_TOKEN;  // the same token twice
         continue;
       }
-      const float y = z[i] > -INFINITY ? y_of(z[i]) : -INFINITY;
-      const float pj = expf(y) * inv_zs;
       const float x = get_elem<DT>(buf + (size_t)at * es);
       put_elem<DT>(buf + (size_t)at * es, -INFINITY);
-      at_s += ex2_approx((x - ref) * c);
-      if (pj > 0.0f) {
-        const float dx = z[i] - x;
-        const float t = pj * fmaf(dx, p.inv_t, dx * p.inv_t_low);
+      at_s += fixed_two(exp_two(over_t(x, ref, p.inv_t, p.inv_t_low)));
+      if (pj[i] > 0.0f) {
+        const Two d = over_t(z[i], x, p.inv_t, p.inv_t_low);
+        const float t = pj[i] * d.hi;
         if (fabsf(t) < kMost)
-          terms += __float2ll_rn(t * kTerm);
+          terms += fixed_two({t, fmaf(pj[i], d.hi, -t) + pj[i] * d.lo});
         else
           large += x > -INFINITY ? t : INFINITY;
-        at_mass += __float2ll_rn(fminf(pj, kMost) * kTerm);
+        at_mass += __float2ll_rn(fminf(pj[i], kMost) * kTerm);
       }
       const int k = atomicAdd(&sm.entries, 1);  // (their order decides nothing)
       pos[k] = at;
       at_x[k] = x;
-      at_p[k] = pj;
+      at_p[k] = pj[i];
     }
     if (__any_sync(kFull, mine)) {
 #pragma unroll
@@ -235,8 +310,8 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
     if ((tid & 31) == 0) {
       sm.terms[0][tid >> 5] = terms;
       sm.terms[1][tid >> 5] = at_mass;
-      sm.red[3][tid >> 5] = at_s;
-      sm.red[4][tid >> 5] = large;
+      sm.terms[2][tid >> 5] = at_s;
+      sm.red[3][tid >> 5] = large;
     }
     if (status) atomicOr(&sm.status, status);
     __syncthreads();
@@ -258,21 +333,21 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
     __syncthreads();
     unsigned long long rec[kWords];
     if (tid < 32) {
-      rest = at_s = large = 0.0f;
-      terms = at_mass = 0;
+      rest = large = 0.0f;
+      terms = at_mass = at_s = 0;
       for (int k = 0; k < kWarps; ++k) {
         rest += sm.red[0][k];
-        at_s += sm.red[3][k];
-        large += sm.red[4][k];
+        large += sm.red[3][k];
         terms += sm.terms[0][k];
         at_mass += sm.terms[1][k];
+        at_s += sm.terms[2][k];
       }
       const int wrong_here = sm.status | (sm.in.gave_up ? SPECDEC_ROW_INTERNAL : 0);
-      rec[0] = (unsigned long long)__float_as_uint(at_s) << 32 | __float_as_uint(rest);
+      rec[0] = (unsigned long long)at_s;
       rec[1] = (unsigned long long)(uint32_t)wrong_here << 32 | __float_as_uint(m);
       rec[2] = (unsigned long long)terms;
       rec[3] = (unsigned long long)at_mass;
-      rec[4] = __float_as_uint(large);
+      rec[4] = (unsigned long long)__float_as_uint(large) << 32 | __float_as_uint(rest);
     }
     got = exchange(sm.ex, turn, rec, 5, rank, size);
 
@@ -284,16 +359,16 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
     }
     if (!(M > -INFINITY && M <= kMaxLogit)) st |= SPECDEC_ROW_NONFINITE;
     if (none) st = 0;
-    float others = 0.0f;
+    float others = 0.0f, S = 0.0f;
     for (int k = 0; k < size; ++k) {
       const float mk = __uint_as_float((uint32_t)got[k][1]);
       const float f = mk > -INFINITY ? ex2_approx((mk - M) * c) : 0.0f;
-      const float q = __uint_as_float((uint32_t)got[k][0]) * f;
+      const float q = __uint_as_float((uint32_t)got[k][4]) * f;
       others += q;
-      S += q + __uint_as_float((uint32_t)(got[k][0] >> 32)) * f;
+      S += q + (float)(long long)got[k][0] * 0x1p-40f * f;
     }
     inv_s = 1.0f / S;
-    of = others * inv_s;
+    const float of = others * inv_s;
     float share = 1.0f;  // what is left of s outside the entries
     if (p.lse) {
       // a log-sum-exp in float32 leaves about 2^-21 of the mass unsure: nothing is asked
@@ -305,42 +380,76 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
     coef = fminf(fmaxf(w * p.inv_t * share * inv_s, -3.0e38f), 3.0e38f);
   }
 
-  if (rank == 0 && tid == 0 && p.loss) {
+  if (rank == 0 && tid < 32 && p.loss) {
     float L = 0.0f;
     if (w != 0.0f) {
-      // q = max / T + ln S - lse in units of 2^-40, 2^40 / T and ln S in parts that are rounded
-      // far below float32's half step of the whole
-      int e;
-      const float f = frexpf(S, &e);
-      float zt = 0.0f;  // without a log-sum-exp: zmax / T + ln zs is the entries' own
-      int ez = 0;
-      const float fz = frexpf(zs, &ez);
-      if (!p.lse) zt = zmax;
-      const float dm = M - zt, a = dm * p.inv_t;
-      const float low = fmaf(dm, p.inv_t, -a) + dm * p.inv_t_low;
-      long long t = 0;
-      for (int k = 0; k < size; ++k) {
-        t += (long long)got[k][2];
-        L += __uint_as_float((uint32_t)got[k][4]);
+      // The CTAs' sums against the row's maximum, one a lane; then ln S, and ln of s outside
+      // the entries and of r, or of what brings the shares' sum to 1.  (Sums of float32 leave
+      // 2e-7 of a loss that may be 1e-3.)
+      long long S = 0, O = 0, t = 0;
+      float large = 0.0f, others = 0.0f;
+      if (tid < size) {
+        const float mk = __uint_as_float((uint32_t)got[tid][1]);
+        const float rest = __uint_as_float((uint32_t)got[tid][4]);
+        const float at = (float)(long long)got[tid][0];
+        const float at_low = (float)((long long)got[tid][0] - (long long)at);
+        const Two f = mk > -INFINITY ? exp_two(over_t(mk, M, p.inv_t, p.inv_t_low)) : Two{0.0f, 0.0f};
+        others = f.hi * rest;
+        O = fixed_two({others, fmaf(f.hi, rest, -others) + f.lo * rest});
+        const float q = f.hi * at;
+        S = O + __float2ll_rn(q) + __float2ll_rn(fmaf(f.hi, at, -q) + f.lo * at + f.hi * at_low);
+        t = (long long)got[tid][2];
+        large = __uint_as_float((uint32_t)(got[tid][4] >> 32));
       }
-      float q;
-      if (fabsf(a) < 0x1p21f && fabsf(lse) < 0x1p21f) {
-        const long long kLn2 = 762123384786ll;  // ln 2 in units of 2^-40
-        const long long qf = __float2ll_rn(a * kTerm) + __float2ll_rn((low + logf(f) - logf(fz)) * kTerm) -
-                             __float2ll_rn(lse * kTerm) + (long long)(e - ez) * kLn2;
-        q = (float)qf * 0x1p-40f;
-        t += qf;
-      } else {
-        q = (a - lse) + (low + logf(S) - logf(zs));
-        L += q;
+#pragma unroll
+      for (int d = 1; d < kMaxCluster; d <<= 1) {
+        S += __shfl_xor_sync(kFull, S, d);
+        O += __shfl_xor_sync(kFull, O, d);
+        others += __shfl_xor_sync(kFull, others, d);
+        t += __shfl_xor_sync(kFull, t, d);
+        large += __shfl_xor_sync(kFull, large, d);
       }
-      // sum p_j is 1 without a log-sum-exp (by definition) and 1 - r with one
-      if (p.lse) L -= q * ((float)((1ll << 40) - mass) * 0x1p-40f);
-      if (left > 0.0f) L += left * logf(left / of);
-      L += (float)t * 0x1p-40f;
+      constexpr long long kOne = 1ll << 40;
+      const long long r = kOne - mass;
+      const long long arg = tid == 0 ? S : tid == 1 ? O : r;
+      float v = (float)arg * 0x1p-40f, low = (float)(arg - (long long)(float)arg) * 0x1p-40f;
+      if (tid == 1 && O < kOne >> 10) {  // (few units: as float32 has it)
+        v = others;
+        low = 0.0f;
+      } else if (tid == 2 && !p.lse) {
+        v = inv_zs;
+        low = 0.0f;
+      }
+      const long long ln = v >= 0x1p-126f ? ln_fixed(v, low) : 0;
+      const long long ln1 = __shfl_sync(kFull, ln, 1), ln2 = __shfl_sync(kFull, ln, 2);
+      if (tid == 0) {
+        const Two a = over_t(M, zmax, p.inv_t, p.inv_t_low);
+        long long q = ln;  // M / T + ln S less the teacher's normaliser
+        if (p.lse) {
+          if (fabsf(a.hi) < 0x1p20f && fabsf(lse) < 0x1p20f && mass < 2 * kOne) {
+            q += fixed_two(a) - __float2ll_rn(lse * kTerm);
+            t += mul_fixed(mass, q);
+          } else {
+            large += (float)mass * 0x1p-40f * ((a.hi - lse) + (a.lo + (float)ln * 0x1p-40f));
+          }
+          if (left > 0.0f) {
+            if (others > 0.0f) t += mul_fixed(r, ln2 - ln1 + ln);
+            else large = INFINITY;
+          }
+        } else {
+          // (the shares add up to 1 - r, r next to nothing)
+          t += mul_fixed(t, r);
+          q += ln2 + r;
+          if (fabsf(a.hi) < 0x1p20f) t += q + fixed_two(a);
+          else large += a.hi + (a.lo + (float)q * 0x1p-40f);
+        }
+        L = large + (float)t * 0x1p-40f;
+      }
     }
-    p.loss[n] = st ? __int_as_float(0x7fc00000) : none ? 0.0f : L;
-    p.row_status[n] = st;
+    if (tid == 0) {
+      p.loss[n] = st ? __int_as_float(0x7fc00000) : none ? 0.0f : L;
+      p.row_status[n] = st;
+    }
   }
   if (kGrad) {
     const float fill = st ? __int_as_float(0x7fc00000) : 0.0f;

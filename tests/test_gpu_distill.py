@@ -125,6 +125,43 @@ def test_absent_entries_and_rows_without_any(sd):
         assert (r.loss[0, 2:] == 0).all() and (r.grad[0, 2:] == 0).all() and (r.row_status == 0).all()
 
 
+@pytest.mark.parametrize("lse", [True, False])
+@pytest.mark.parametrize("T", [1.0, 0.7, 2.0])
+@pytest.mark.parametrize("V,K", [(200, 200), (1000, 1000), (32000, 64), (128256, 512)])
+def test_small_losses(sd, V, K, T, lse):
+    # A draft next to its teacher: a loss of some 1e-5 out of terms of some units.  The entries'
+    # weights are good to 2^-27, three logarithms to 2^-28, the rest of the sums to less: 2^-25
+    # in all.  The shares are off by 2^-22, which counts times |ln p / s|.  The other tokens' weights
+    # O are off by UNSURE of themselves; ln S goes with them by O / S, and with a log-sum-exp
+    # -r ln s_rest by -r more.
+    rng = np.random.default_rng(V + K)
+    T32 = float(np.float32(T))
+    y = 3.0 * rng.standard_normal((1, 3, V))
+    x = (y + 0.01 * rng.standard_normal(y.shape)).astype(np.float32)
+    ids = np.argsort(-y, axis=-1)[:, :, :K].astype(np.int32)
+    z = np.take_along_axis(y, ids, -1).astype(np.float32)
+    top = y.max(-1)
+    whole = (top / T32 + np.log(np.exp((y - top[..., None]) / T32).sum(-1))).astype(np.float32)
+    whole = whole if lse else None
+    got = sd.distill(cuda(x), cuda(ids), cuda(z), cuda(whole), None, T, grad=False)
+    for r in range(3):
+        row = x[0, r].astype(np.float64)
+        with np.errstate(divide="ignore"):
+            loss, _ = ref.distill(row, ids[0, r], z[0, r], None if whole is None else whole[0, r], T32)
+        if np.isinf(loss):  # (a rounded log-sum-exp leaves 2^-20 to tokens that do not exist)
+            assert float(got.loss[0, r]) == loss
+            continue
+        s = np.exp((row - row.max()) / T32)
+        s /= s.sum()
+        of = 1.0 - s[ids[0, r]].sum() if K < V else 0.0
+        p = np.exp(z[0, r].astype(np.float64) / T32 - (0.0 if whole is None else whole[0, r]))
+        p = p if lse else p / p.sum()
+        left = max(0.0, 1.0 - p.sum()) if lse else 0.0
+        ratio = np.abs(np.log(p / s[ids[0, r]]))
+        some = 2.0 ** -25 + 2.0 ** -22 * float((p * ratio).sum()) + abs(of - left) * UNSURE
+        assert abs(float(got.loss[0, r]) - loss) <= some + 2.0 ** -23 * abs(loss)
+
+
 def test_masked_tokens_and_certain_teachers(sd):
     x = normal(11, 1, 4, 700)
     x[0, :, 50:600] = -np.inf
