@@ -18,14 +18,14 @@
 // floating point; with them the kernel took 1790 us in place of 434), and the last few steps of
 // a row are 64-bit.
 //
-// Measured: 4096 rows of 128256 bfloat16, 64 entries, gradient out: 450 us, 4.7 TB/s, 69 % of the
-// measured copy rate; 4080 rows of 32003 bfloat16: 107 us, 64 %; 508 rows of 152064 float32: 146 us,
-// 62 %; 33 rows of 32000 float32: 10.3 us.  Of a CTA's 23000 clocks (three an SM) its share's
+// Measured: 4096 rows of 128256 bfloat16, 64 entries, gradient out: 446 us, 4.7 TB/s, 70 % of the
+// measured copy rate; 4080 rows of 32003 bfloat16: 103 us, 66 %; 508 rows of 152064 float32: 144 us,
+// 64 %; 33 rows of 32000 float32: 10.3 us.  Of a CTA's 23000 clocks (three an SM) its share's
 // arrival takes 7600, the sum 3300, the exchange 3000, the loss 2200, the gradient 5000: the
 // chain of those steps, which three CTAs overlap in part, is what keeps it from the copy rate.
 // Records that complete on an mbarrier, in place of the cluster's barrier: 1 % less, and 1 us more for
 // the smallest call.  The pairs of the loss cost 4 % (434 us with float32 terms, whose loss was off
-// by 2e-7; with the last steps in 64-bit floating point 485).
+// by 2e-7, in place of 450 at that time; with the last steps in 64-bit floating point 485).
 #include "draft_common.cuh"
 
 namespace specdec {
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
   }
   pdl_wait();
   pdl_launch_dependents();
-  cluster_arrive();  // all CTAs run before one writes to another (waited for below)
+  cluster_arrive_relaxed();  // all CTAs run before one writes to another (waited for below)
   __syncthreads();
 
   const uint8_t *row = reinterpret_cast<const uint8_t *>(p.x) +

@@ -24,14 +24,14 @@
 //
 // What bounds it is the instructions of exact weights, some 20 an element, beside an
 // HBM pass of 2 to 4 bytes an element (rows of 128256 bfloat16, two CTAs an SM):
-//   2304 flat rows, top-p 0.95, logits out: 817 us, 1.4 TB/s of reads and writes.  Of a CTA's
+//   2304 flat rows, top-p 0.95, logits out: 794 us, 1.5 TB/s of reads and writes.  Of a CTA's
 //     53000 clocks its share's arrival takes 8500, the histogram 8000, placing the bracket
 //     6000, the exact weights 19000, the list and exchanges 6500, the rows 6000.
-//   672 rows, no filter, 3 draws and probabilities: 206 us.  Of 41000 clocks arrival and
+//   672 rows, no filter, 3 draws and probabilities: 202 us.  Of 41000 clocks arrival and
 //     maximum 9000, weights 17000, draws 2700, probabilities 9300.
-//   256 rows, top-p 0.9, a draw and probabilities: 134 us (four waves of CTAs, the last a third full).  One row of 32000 float32 under
-//     top-k 40 and top-p: 15 us, a chain of exchanges and barriers (and of instructions that
-//     are not cached yet).
+//   256 rows, top-p 0.9, a draw and probabilities: 132 us (four waves of CTAs, the last a third
+//     full).  One row of 32000 float32 under top-k 40 and top-p: 14 us, a chain of exchanges and
+//     barriers (and of instructions that are not cached yet).
 // With threads of 512 a CTA 324 and 263 us in the place of 206 and 139: the kernel's code is
 // larger than the instruction cache's near levels, so that more warps in different places
 // cost more than they hide.
@@ -351,6 +351,7 @@ __device__ __forceinline__ void histogram(const Share &s, const uint8_t *buf, fl
       count_bin(base + 4 * min(__float_as_uint(y.y) - 0x4B000000u, rest));
     }
   }
+  __syncthreads();
   cluster_sync();
 }
 
@@ -556,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   int k = p.top_k ? p.top_k[b] : 0;
   float top_p = p.top_p ? p.top_p[b] : 1.0f;
   float min_p = p.min_p ? p.min_p[b] : 0.0f;
-  cluster_arrive();
+  cluster_arrive_relaxed();  // (all CTAs run before one writes to another)
   __syncthreads();
   share_edges<DT>(s, row, buf);
 
@@ -784,6 +785,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         }
       }
     }
+    __syncthreads();
     got = exchange(sm.ex, turn, rec, 3, rank, size);
     cut = cut_at(got[0][0]);
     Z = got[0][1];
@@ -854,7 +856,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         u64 in = 0;
         if (want > f.above && fits && !floored) {
           // the list: in place order, up to the one that reaches the mass
-          u64 rec2[kWords];
+          u64 rec2[kWords];  // (rank 0's counts)
           if (rank == 0) {
             const int all = collect(size, sm);
             constexpr int kEach = kList / kThreads;
@@ -877,12 +879,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
               }
               sum += wt[i];
             }
-            __syncthreads();
-            rec2[0] = sm.cut[0];
-            rec2[1] = sm.cut[1];
-            rec2[2] = sm.cut[2];
-            rec2[3] = in;
           }
+          __syncthreads();
+          rec2[0] = sm.cut[0];
+          rec2[1] = sm.cut[1];
+          rec2[2] = sm.cut[2];
+          rec2[3] = in;
           got = exchange(sm.ex, turn, rec2, 4, rank, size);
           in = got[0][3];
           if (want <= f.above + in) {
