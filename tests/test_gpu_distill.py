@@ -106,6 +106,14 @@ def test_clusters_of_every_size(sd, dtype, V, B):
     check(sd, x, 64, dtype=dtype, rows={(0, 0), (B // 2, 0), (B - 1, 0)})
 
 
+@pytest.mark.parametrize("V,B", [(50001, 80), (80000, 50), (100003, 40), (115000, 34), (130002, 30), (160001, 20),
+                                 (200000, 16), (240005, 13), (300000, 11)])
+def test_clusters_of_other_sizes(sd, V, B):
+    """3, 5, 6, 7, 8, 10, 12, 14 and 16 CTAs a float32 row."""
+    x = np.random.default_rng(V).standard_normal((B, 1, V)).astype(np.float32)
+    check(sd, x, 300, rows={(0, 0), (B - 1, 0)})
+
+
 @pytest.mark.parametrize("T", [0.01, 0.5, 4.0, 1000.0])
 @pytest.mark.parametrize("offset", [0.0, 300.0])
 def test_temperatures_and_offsets(sd, T, offset):

@@ -108,6 +108,26 @@ def test_clusters_of_every_size(sd, dtype, V, B, f):
     check(sd, x, [0.9] * B, dtype=dtype, rows=look, **flt)
 
 
+# float32 rows that take 3, 5, 6, 7, 8, 10, 12, 14 and 16 CTAs, the smaller numbers of them by
+# as many rows as leave no SM idle
+WIDE = [(50001, 80), (80000, 50), (100003, 40), (115000, 34), (130002, 30), (160001, 20), (200000, 16),
+        (240005, 13), (300000, 11)]
+
+
+@pytest.mark.parametrize("V,B", WIDE)
+@pytest.mark.parametrize("k", [1, 128, 129, 1024])
+def test_top_k_in_clusters_of_every_size(sd, V, B, k):
+    """The bound from groups of several lanes (up to 128) and of one thread's part."""
+    x = np.random.default_rng(V + k).standard_normal((B, 1, V)).astype(np.float32)
+    check(sd, x, [0.9] * B, rows={(0, 0), (B - 1, 0)}, k=[k] * B, p=[0.97] * B)
+
+
+@pytest.mark.parametrize("V,B", WIDE)
+def test_top_p_in_clusters_of_every_size(sd, V, B):
+    x = np.random.default_rng(V).standard_normal((B, 1, V)).astype(np.float32)
+    check(sd, x, [0.9] * B, rows={(0, 0), (B - 1, 0)}, p=[0.9, 0.5] * (B // 2) + [0.99] * (B % 2))
+
+
 def test_the_largest_vocabulary(sd):
     V = 1 << 19
     for dtype in ("f32", "bf16"):
