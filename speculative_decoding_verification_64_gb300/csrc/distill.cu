@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
             large += (float)mass * 0x1p-40f * ((a.hi - lse) + (a.lo + (float)ln * 0x1p-40f));
           }
           if (left > 0.0f) {
-            if (others > 0.0f) t += mul_fixed(r, ln2 - ln1 + ln);
+            if (others >= 0x1p-126f) t += mul_fixed(r, ln2 - ln1 + ln);
             else large = INFINITY;
           }
         } else {

@@ -70,6 +70,12 @@ using u64 = unsigned long long;
 
 __device__ const WeightTable g_table = make_table();
 
+// Values of bfloat16 rows that are counted one by one: magnitudes from 2^-14 up to 64, by
+// exponent, sign and mantissa (neighbouring values of one sign in different banks).
+constexpr int kMags = 20 * 128;
+constexpr uint32_t kFirstMag = 0x3880;  // the bits of 2^-14
+constexpr float kLeastMag = 0x1p-14f, kMostMag = 64.0f;
+
 struct SampleSmem {
   Exchange ex;
   Arrival in;
@@ -79,9 +85,11 @@ struct SampleSmem {
     u64 list[kList];
     uint16_t key[kKeys];
     uint32_t bin[kBins + 32];
+    alignas(8) uint32_t val[2 * kMags];
   };
   u64 mine[kMine];
   u64 red[2][kWarps];
+  u64 sums[kWarps][7];
   float redf[2][kWarps];
   double drop;         // T ln(min_p)
   float piece[64], whole;   // of the histogram's mass
@@ -479,6 +487,249 @@ __device__ __forceinline__ void place_bracket(float want, bool share, int size, 
   last = sm.bracket_last;
 }
 
+// Counts of the CTA's tokens by value (bfloat16); tokens of other magnitudes that weigh
+// anything go on the list.
+__device__ __forceinline__ void count_values(const Share &s, const uint8_t *buf, float least,
+                                             SampleSmem &sm) {
+  for (int i = threadIdx.x; i < 2 * kMags; i += kThreads) sm.val[i] = 0;
+  __syncthreads();
+  const uint32_t base = smem_addr(sm.val);
+  for (int v = threadIdx.x; v < s.nvec; v += kThreads) {
+    const uint4 q = *reinterpret_cast<const uint4 *>(buf + (size_t)v * 16);
+    const uint32_t a[4] = {q.x, q.y, q.z, q.w};
+    unsigned odd = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      // both halves as exponent, sign, mantissa
+      const uint32_t r = ((a[i] << 1) & 0xFF00FF00u) | ((a[i] >> 8) & 0x00800080u) | (a[i] & 0x007F007Fu);
+      const uint32_t j0 = (r & 0xFFFFu) - 2 * kFirstMag, j1 = (r >> 16) - 2 * kFirstMag;
+      if (j0 < 2u * kMags) count_bin(base + 4 * j0);
+      else odd |= 1u << (2 * i);
+      if (j1 < 2u * kMags) count_bin(base + 4 * j1);
+      else odd |= 2u << (2 * i);
+    }
+    while (odd) {
+      const int e = __ffs(odd) - 1;
+      odd &= odd - 1;
+      const float y = get_elem<SPECDEC_BF16>(buf + (size_t)v * 16 + 2 * e);
+      if (!(y >= least)) continue;
+      const int k = atomicAdd(&sm.n_mine, 1);
+      if (k < kMine) sm.mine[k] = place_of(y, s.first + v * 8 + e);
+    }
+  }
+}
+
+// top-p's cut of a bfloat16 row below 64 from counts of its values: a sum over the values in
+// place of one over the tokens.  Each CTA adds up the counts of all for its share of the
+// magnitudes, weighs them, and one exchange says whose share holds the cut; that CTA finds
+// the value and how many of its tokens are kept, and where that is not all, the CTA that
+// holds the last of them finds its index.  The least of top-p's and min-p's cut comes out, with the
+// kept mass and count.  False, and nothing found, where the cut is among tokens that are not
+// counted (near 0, below -64), or too many of those or of one value would have to be listed.
+// The same in every CTA.
+__device__ __noinline__ bool cut_by_values(const Share &s, const uint8_t *buf, const WeightOf &w,
+                                           float M, float top_p, float floor_value, int rank, int size,
+                                           int &turn, Cut &cut, u64 &Z, int &kept, SampleSmem &sm) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  count_values(s, buf, M - 60.0f / w.ch, sm);
+  __syncthreads();
+  cluster_sync();
+  const uint32_t vals = smem_addr(sm.val);
+  const int per = (kMags + size - 1) / size;
+  const int m0 = min(rank * per, kMags), m1 = min(m0 + per, kMags);
+  auto place = [&](int m) { return vals + 4u * (uint32_t)(m + (m & ~127)); };  // of +v; -v 128 further
+  auto counts = [&](int m) {  // of +v in the lower half, of -v in the upper
+    uint32_t p = 0, n = 0;
+#pragma unroll 4
+    for (int q = 0; q < size; ++q) {
+      const uint32_t at = cluster_addr(place(m), q);
+      p += remote_get32(at);
+      n += remote_get32(at + 512u);
+    }
+    return (u64)n << 32 | p;
+  };
+  auto magnitude = [](int m) { return __uint_as_float((kFirstMag + (uint32_t)m) << 16); };
+
+  // mass: of the positive values, the negative ones, tokens near 0, tokens below -64, and of
+  // all down to min-p's cut
+  u64 mass[5] = {0, 0, 0, 0, 0};
+  unsigned n[4] = {0, 0, 0, 0};  // tokens: positive, negative, near 0, down to min-p's cut
+#pragma unroll 1
+  for (int m = m0 + tid; m < m1; m += kThreads) {
+    const u64 c = counts(m);
+    if (!c) continue;
+    const float v = magnitude(m);
+    uint32_t a[2], b[2];
+    weight2(make_float2(v, -v), w, sm.table, a, b);
+    const uint32_t up = (uint32_t)c, down = (uint32_t)(c >> 32);
+    const u64 of_up = up * fixed_sum(a[0], b[0], 1), of_down = down * fixed_sum(a[1], b[1], 1);
+    mass[0] += of_up;
+    mass[1] += of_down;
+    n[0] += up;
+    n[1] += down;
+    if (v >= floor_value) {
+      mass[4] += of_up;
+      n[3] += up;
+    }
+    if (-v >= floor_value) {
+      mass[4] += of_down;
+      n[3] += down;
+    }
+  }
+#pragma unroll 1
+  for (int i = tid; i < min(sm.n_mine, kMine); i += kThreads) {
+    const float x = place_value(sm.mine[i]);
+    const u64 t = weight_fixed(x, w, sm.table);
+    const bool near = fabsf(x) < kLeastMag;
+    mass[2] += near ? t : 0;
+    mass[3] += near ? 0 : t;
+    n[2] += near;
+    if (x >= floor_value) {
+      mass[4] += t;
+      ++n[3];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 5; ++i) mass[i] = warp_sum_u64(mass[i]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) n[i] = __reduce_add_sync(kFull, n[i]);
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) sm.sums[warp][i] = mass[i];
+    sm.sums[warp][5] = (u64)n[0] << 32 | n[1];
+    sm.sums[warp][6] = (u64)n[2] << 32 | n[3];
+  }
+  __syncthreads();
+  u64 rec[kWords];
+  if (warp == 0) {
+#pragma unroll
+    for (int i = 0; i < 7; ++i) {
+      rec[i] = 0;
+#pragma unroll
+      for (int q = 0; q < kWarps; ++q) rec[i] += sm.sums[q][i];
+    }
+    rec[7] = (u64)(uint32_t)sm.n_mine;
+  }
+  const u64(*got)[kWords] = exchange(sm.ex, turn, rec, 8, rank, size);
+  u64 all[5] = {0, 0, 0, 0, 0};
+  int n_up = 0, n_near = 0, n_floor = 0;
+  bool fits = true;
+#pragma unroll 1
+  for (int q = 0; q < size; ++q) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) all[i] += got[q][i];
+    n_up += (int)(got[q][5] >> 32);
+    n_near += (int)(got[q][6] >> 32);
+    n_floor += (int)(uint32_t)got[q][6];
+    fits = fits && got[q][7] <= kMine;
+  }
+  if (!fits) return false;
+  const u64 want = max(share_at_least(top_p, all[0] + all[1] + all[2] + all[3]), 1ull);
+  if (want > all[4]) {  // min-p's cut comes first
+    cut = {floor_value, kAll};
+    Z = all[4];
+    kept = n_floor;
+    return true;
+  }
+  const bool up = want <= all[0];
+  u64 above = up ? 0 : all[0] + all[2];
+  int n_above = up ? 0 : n_up + n_near;
+  if (!up && (want <= above || want > above + all[1])) return false;
+  int owner = -1;
+#pragma unroll 1
+  for (int i = 0; i < size; ++i) {
+    const int q = up ? size - 1 - i : i;
+    const u64 here = got[q][up ? 0 : 1];
+    if (want <= above + here) {
+      owner = q;
+      break;
+    }
+    above += here;
+    n_above += (int)(up ? got[q][5] >> 32 : (uint32_t)got[q][5]);
+  }
+  if (rank == owner) {
+    bool found = false;
+    if (tid == 0) sm.cut[2] = 0;
+#pragma unroll 1
+    for (int i = 0; i < per && !found; i += kThreads) {
+      const int m = up ? m1 - 1 - i - tid : m0 + i + tid;
+      const bool mine = m >= m0 && m < m1;
+      const u64 c = mine ? counts(m) : 0;
+      const uint32_t here = up ? (uint32_t)c : (uint32_t)(c >> 32);
+      const float v = up ? magnitude(m) : -magnitude(m);
+      const u64 t = here ? weight_fixed(v, w, sm.table) : 0;
+      u64 whole, tokens;
+      const u64 before = above + cta_exscan(here * t, sm.red[0], whole);
+      const int n_before = n_above + (int)cta_exscan((u64)here, sm.red[1], tokens);
+      const bool hit = before < want && want <= before + here * t;
+      if (hit) {
+        const uint32_t keep = (uint32_t)((want - before + t - 1) / t);
+        sm.cut[0] = (u64)__float_as_uint(v) << 32 | (uint32_t)(n_before + (int)keep);
+        sm.cut[1] = before + keep * t;
+        sm.cut[2] = (u64)keep << 32 | here;
+      }
+      found = __syncthreads_or(hit);
+      above += whole;
+      n_above += (int)tokens;
+    }
+  }
+  __syncthreads();
+  rec[0] = sm.cut[0];
+  rec[1] = sm.cut[1];
+  rec[2] = sm.cut[2];
+  got = exchange(sm.ex, turn, rec, 3, rank, size);
+  const float value = __uint_as_float((uint32_t)(got[owner][0] >> 32));
+  const int count = (int)(uint32_t)got[owner][0];
+  const u64 sum = got[owner][1];
+  int keep = (int)(got[owner][2] >> 32);
+  cut = {value, kAll};
+  if (keep < (int)(uint32_t)got[owner][2]) {
+    // the last of `keep` tokens of this value, by index
+    const uint32_t at =
+        place((int)((__float_as_uint(value) >> 16 & 0x7FFFu) - kFirstMag)) + (up ? 0u : 512u);
+    int of = 0, here = 0;
+#pragma unroll 1
+    for (int q = 0; q < size; ++q) {
+      here = (int)remote_get32(cluster_addr(at, q));
+      of = q;
+      if (keep <= here) break;
+      keep -= here;
+    }
+    __syncthreads();  // (the list's last readers)
+    if (tid == 0) sm.n_mine = 0;
+    __syncthreads();
+    if (here > kMine) {
+      cluster_sync();  // (the counts' last readers)
+      return false;
+    }
+    if (rank == of) {
+      const uint32_t both_bits = (__float_as_uint(value) >> 16) * 0x10001u;
+      for (int v = tid; v < s.nvec; v += kThreads) {
+        const uint4 q = *reinterpret_cast<const uint4 *>(buf + (size_t)v * 16);
+        const uint32_t a[4] = {q.x ^ both_bits, q.y ^ both_bits, q.z ^ both_bits, q.w ^ both_bits};
+        unsigned same = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          same |= (e & 1 ? a[e >> 1] >> 16 : a[e >> 1] & 0xFFFFu) == 0 ? 1u << e : 0u;
+        while (same) {
+          const int e = __ffs(same) - 1;
+          same &= same - 1;
+          sm.mine[atomicAdd(&sm.n_mine, 1)] = place_of(value, s.first + v * 8 + e);
+        }
+      }
+      __syncthreads();
+      sort_down<kThreads>(sm.mine, here);
+    }
+    __syncthreads();
+    rec[0] = (u64)(uint32_t)place_index(sm.mine[keep - 1]);
+    got = exchange(sm.ex, turn, rec, 1, rank, size);
+    cut.index = (int)got[of][0];
+  }
+  Z = sum;
+  kept = count;
+  return true;
+}
+
 // The tokens from `lo` up, on the list.
 template <int DT>
 __device__ __forceinline__ void gather(const Share &s, const uint8_t *buf, const Cut &lo,
@@ -503,6 +754,25 @@ __device__ __forceinline__ void gather(const Share &s, const uint8_t *buf, const
       if (k < kMine) sm.mine[k] = place_of(y, at);
     }
   }
+}
+
+// The kept tokens' mass of each run, where they fit the list; the CTA's mass.
+template <int DT>
+__device__ __forceinline__ u64 weigh_few(const Share &s, const uint8_t *buf, const WeightOf &w,
+                                         const Cut &cut, u64 *steps, SampleSmem &sm) {
+  const int per = 32 * run_steps(s);
+  for (int i = threadIdx.x; i * per < s.nvec; i += kThreads) steps[i] = 0;
+  gather<DT>(s, buf, cut, sm);
+  __syncthreads();
+  u64 add = 0, mass;
+  for (int i = threadIdx.x; i < sm.n_mine; i += kThreads) {
+    const u64 q = sm.mine[i];
+    const u64 t = weight_fixed(place_value(q), w, sm.table);
+    atomicAdd(&steps[(place_index(q) - s.first) / Elem<DT>::kN / per], t);
+    add += t;
+  }
+  (void)cta_exscan(add, sm.red[0], mass);
+  return mass;
 }
 
 // All CTAs' lists, by rank 0, sorted.
@@ -797,7 +1067,27 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     int n_in;
     bool fits;
     if (floor_value > kLeast) cut = {floor_value, kAll};
-    if (top_p < 1.0f) {
+    bool found = false;
+    if (DT == SPECDEC_BF16 && top_p < 1.0f && M < kMostMag) {
+      found = cut_by_values(s, buf, w, M, top_p, floor_value, rank, size, turn, cut, Z, kept, sm);
+      __syncthreads();
+      if (tid == 0) sm.n_mine = 0;
+      __syncthreads();
+      if (found && p.S == 0) {
+        weighed = true;
+      } else if (found && kept <= kMine) {
+        mass = weigh_few<DT>(s, buf, w, cut, steps, sm);
+        rec[0] = mass;
+        got = exchange(sm.ex, turn, rec, 1, rank, size);
+#pragma unroll 1
+        for (int q = 0; q < rank; ++q) before += got[q][0];
+        weighed = true;
+      } else if (found && cut.index != kAll) {
+        weigh_row<DT, kBracket>(s, buf, w, cut, cut, steps, rank, size, turn, mass, before, n_in, fits, sm);
+        weighed = true;
+      }
+    }
+    if (top_p < 1.0f && !found) {
       // less than the wanted mass stands above H, all of it down to L: sums are exact, so that
       // this holds throughout, and halves end
       u64 L = (u64)max(order_key(M - 45.0f / ch), kLeastKey) << 32, H = over, lo, hi;
