@@ -11,8 +11,11 @@
 //   * With top-k: the k-th largest of the maxima of some hundred groups of tokens (its top 16
 //     bits) bounds the k-th logit from below, the few tokens that reach it are gathered by
 //     rank 0, sorted, weighed, cut and drawn from.
-//   * With top-p alone: a histogram of the logits, 1/64 octave of weight a bin, says about
-//     where the cut is.  A pass adds the weights of all places above a bracket around it, and
+//   * With top-p alone, bfloat16: the tokens of every value are counted (a row has some
+//     thousand values), each value is weighed once, and sums over the values name the one that
+//     top-p cuts, and how many of its tokens stay.
+//   * Float32, and bfloat16 rows of other magnitudes: a histogram of the logits, 1/64 octave of
+//     weight a bin, says about where the cut is.  A pass adds the weights of all places above a bracket around it, and
 //     in it; when the cut is inside and the bracket's tokens fit a list, they are sorted and
 //     the cut is found among them.  A bracket that missed is placed anew by what the pass
 //     found, and where that fails, between the places known to hold the cut, halves of them.
@@ -22,16 +25,17 @@
 // those of draft_weight.cuh, as good as 64-bit floating point for this.  The cluster's
 // CTAs exchange a record of a few words at each step.
 //
-// What bounds it is the instructions of exact weights, some 20 an element, beside an
-// HBM pass of 2 to 4 bytes an element (rows of 128256 bfloat16, two CTAs an SM):
-//   2304 flat rows, top-p 0.95, logits out: 794 us, 1.5 TB/s of reads and writes.  Of a CTA's
-//     53000 clocks its share's arrival takes 8500, the histogram 8000, placing the bracket
-//     6000, the exact weights 19000, the list and exchanges 6500, the rows 6000.
-//   672 rows, no filter, 3 draws and probabilities: 202 us.  Of 41000 clocks arrival and
+// What bounds it: the chain of passes over the share and of exchanges, two CTAs an SM, and
+// where all tokens are weighed some 23 instructions an element (rows of 128256 bfloat16, a read
+// and a write of HBM):
+//   2304 flat rows, top-p 0.95 and min-p, logits out: 556 us, 2.1 TB/s of reads and writes.  Of a
+//     CTA's 38000 clocks arrival and maximum take 11000, counting 9000, summing the counts 9000,
+//     the rows 6000.  By the histogram and exact weights of all tokens: 797.
+//   672 rows, no filter, 3 draws and probabilities: 204 us.  Of 41000 clocks arrival and
 //     maximum 9000, weights 17000, draws 2700, probabilities 9300.
-//   256 rows, top-p 0.9, a draw and probabilities: 132 us (four waves of CTAs, the last a third
-//     full).  One row of 32000 float32 under top-k 40 and top-p: 14 us, a chain of exchanges and
-//     barriers (and of instructions that are not cached yet).
+//   256 rows, top-p 0.9, a draw and probabilities: 122 us (four waves of CTAs, the last a third
+//     full; by the histogram 131).  One row of 32000 float32 under top-k 40 and top-p: 14 us, a
+//     chain of exchanges and barriers (and of instructions that are not cached yet).
 // With threads of 512 a CTA 324 and 263 us in the place of 206 and 139: the kernel's code is
 // larger than the instruction cache's near levels, so that more warps in different places
 // cost more than they hide.
@@ -48,7 +52,8 @@ constexpr int kFewK = 128;    // top-k up to which some 500 groups name the boun
 constexpr int kKeys = 4096;   // groups' maxima (256 of each of 16 CTAs)
 // The histogram's bins of a factor of two in weight, and its 24 octaves: a row's tail below
 // 2^-24 of its largest weight is 3 % of the mass at most for 2^19 tokens, and the exact pass
-// corrects the guess by what it found.  256 rows under top-p, 2304 flat ones: 134 and 817 us;
+// corrects the guess by what it found.  256 bfloat16 rows under top-p, 2304 flat ones, when
+// those came this way: 134 and 817 us;
 // with 128 bins an octave 140 and 849 (twice the bins to read from the other CTAs), with 32
 // 131 and 808, where flat rows of float32 bring brackets of twice the tokens.  With 16
 // octaves 206 us for the 256 rows: their tails' mass is missed, and a second bracket placed.
@@ -85,7 +90,7 @@ struct SampleSmem {
     u64 list[kList];
     uint16_t key[kKeys];
     uint32_t bin[kBins + 32];
-    alignas(8) uint32_t val[2 * kMags];
+    alignas(8) uint32_t val[2 * kMags + 32];
   };
   u64 mine[kMine];
   u64 red[2][kWarps];
@@ -487,34 +492,37 @@ __device__ __forceinline__ void place_bracket(float want, bool share, int size, 
   last = sm.bracket_last;
 }
 
-// Counts of the CTA's tokens by value (bfloat16); tokens of other magnitudes that weigh
-// anything go on the list.
+// Counts of the CTA's tokens by value (bfloat16); tokens of other magnitudes are counted in
+// places that nobody reads (no branch a token: 556 us for the 2304 rows, with one 648), and those
+// that weigh anything go on the list.
 __device__ __forceinline__ void count_values(const Share &s, const uint8_t *buf, float least,
                                              SampleSmem &sm) {
   for (int i = threadIdx.x; i < 2 * kMags; i += kThreads) sm.val[i] = 0;
   __syncthreads();
-  const uint32_t base = smem_addr(sm.val);
+  const uint32_t base = smem_addr(sm.val), rest = 2u * kMags + (threadIdx.x & 31);
+#pragma unroll 2
   for (int v = threadIdx.x; v < s.nvec; v += kThreads) {
     const uint4 q = *reinterpret_cast<const uint4 *>(buf + (size_t)v * 16);
     const uint32_t a[4] = {q.x, q.y, q.z, q.w};
-    unsigned odd = 0;
+    unsigned odd = 0;  // pairs with such a token
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       // both halves as exponent, sign, mantissa
       const uint32_t r = ((a[i] << 1) & 0xFF00FF00u) | ((a[i] >> 8) & 0x00800080u) | (a[i] & 0x007F007Fu);
       const uint32_t j0 = (r & 0xFFFFu) - 2 * kFirstMag, j1 = (r >> 16) - 2 * kFirstMag;
-      if (j0 < 2u * kMags) count_bin(base + 4 * j0);
-      else odd |= 1u << (2 * i);
-      if (j1 < 2u * kMags) count_bin(base + 4 * j1);
-      else odd |= 2u << (2 * i);
+      count_bin(base + 4 * min(j0, rest));
+      count_bin(base + 4 * min(j1, rest));
+      odd |= max(j0, j1) >= 2u * kMags ? 1u << i : 0u;
     }
     while (odd) {
-      const int e = __ffs(odd) - 1;
+      const int e0 = 2 * (__ffs(odd) - 1);
       odd &= odd - 1;
-      const float y = get_elem<SPECDEC_BF16>(buf + (size_t)v * 16 + 2 * e);
-      if (!(y >= least)) continue;
-      const int k = atomicAdd(&sm.n_mine, 1);
-      if (k < kMine) sm.mine[k] = place_of(y, s.first + v * 8 + e);
+      for (int e = e0; e < e0 + 2; ++e) {
+        const float y = get_elem<SPECDEC_BF16>(buf + (size_t)v * 16 + 2 * e);
+        if (!(y >= least) || (fabsf(y) >= kLeastMag && fabsf(y) < kMostMag)) continue;
+        const int k = atomicAdd(&sm.n_mine, 1);
+        if (k < kMine) sm.mine[k] = place_of(y, s.first + v * 8 + e);
+      }
     }
   }
 }
@@ -687,14 +695,16 @@ __device__ __noinline__ bool cut_by_values(const Share &s, const uint8_t *buf, c
     // the last of `keep` tokens of this value, by index
     const uint32_t at =
         place((int)((__float_as_uint(value) >> 16 & 0x7FFFu) - kFirstMag)) + (up ? 0u : 512u);
-    int of = 0, here = 0;
-#pragma unroll 1
-    for (int q = 0; q < size; ++q) {
-      here = (int)remote_get32(cluster_addr(at, q));
-      of = q;
-      if (keep <= here) break;
-      keep -= here;
+    int here = lane < size ? (int)remote_get32(cluster_addr(at, lane)) : 0, upto = here;
+#pragma unroll
+    for (int d = 1; d < kMaxCluster; d <<= 1) {
+      const int y = __shfl_up_sync(kFull, upto, d);
+      if (lane >= d) upto += y;
     }
+    // (the last CTA's sum is all of them: one lane reaches it)
+    const int of = __ffs(__ballot_sync(kFull, upto >= keep)) - 1;
+    keep -= __shfl_sync(kFull, upto - here, of);
+    here = __shfl_sync(kFull, here, of);
     __syncthreads();  // (the list's last readers)
     if (tid == 0) sm.n_mine = 0;
     __syncthreads();
