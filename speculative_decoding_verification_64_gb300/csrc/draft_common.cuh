@@ -550,7 +550,7 @@ __device__ __forceinline__ void store_like(const Share &s, uint8_t *row, int v, 
 // callers' (rows of 128256 bfloat16, us):
 //   sampling, 4 CTAs a row and 2 an SM: 140 / 207 / 849 for 256 rows under top-p, 672 rows
 //     without a filter, 2304 flat rows under top-p; 6 and 3: 162 / 195 / 977; 8 and 3: 216 /
-//     222 / 1461 (every CTA of a row has the same exchanges to wait for)
+//     222 / 1461 (every CTA of a row has the same exchanges to wait for), all by the histogram
 //   distillation (before its loss was held in pairs), 4 a row and 3 an SM: 434 for 4096 rows;
 //     5, 6 and 8 a row with 4 to 5 an SM: 463 to 500.  508 rows of 152064 float32: 138 with 10 a row and 3 an SM, 154 with 8
 //     and 2, 152 with 12 and 4, 208 with 16 and 5.

@@ -188,6 +188,33 @@ def test_flat_rows_and_rows_of_few_values(sd, dtype):
         check(sd, x, T, dtype=dtype, p=[p] * 6, m=[m] * 6)
 
 
+@pytest.mark.parametrize("V", [900, 30000, 128256])
+@pytest.mark.parametrize("kind", ["tiny", "low", "mixed", "few", "one", "high"])
+def test_values_that_are_counted_and_others(sd, V, kind):
+    """bfloat16 rows whose cut is at a value near 0, far below it, between those, at a value of
+    thousands of tokens, or above what is counted."""
+    rng = np.random.default_rng(V)
+    T = 1.0
+    if kind == "tiny":
+        x = rng.standard_normal((1, 1, V)) * 2.0 ** -16
+    elif kind == "low":
+        x, T = -64.0 - 400.0 * rng.random((1, 1, V)), 200.0
+        x[0, 0, rng.integers(0, V, 20)] = 1.0
+    elif kind == "mixed":
+        x = rng.choice([1.5, 2.0 ** -17, -2.0 ** -20, 0.0, -0.75, -3.0, -200.0], size=(1, 1, V))
+        T = 50.0
+    elif kind == "few":
+        x = rng.choice([0.5, 0.25, -0.125, -2.0], size=(1, 1, V))
+    elif kind == "one":
+        x = np.full((1, 1, V), -1.25)
+    else:
+        x, T = 30.0 + 60.0 * rng.random((1, 1, V)), 40.0
+    ps = [0.01, 0.15, 0.29, 0.43, 0.5, 0.57, 0.72, 0.86, 0.97, 0.99999]
+    n = len(ps)
+    check(sd, np.broadcast_to(x, (n, 1, V)), [T] * n, dtype="bf16", p=ps, seed=V)
+    check(sd, np.broadcast_to(x, (n, 1, V)), [T] * n, dtype="bf16", p=ps, m=[0.0, 0.9] * (n // 2), S=0)
+
+
 def test_zeros_of_both_signs_and_denormals(sd):
     x = np.zeros((1, 1, 6000))
     x[0, 0, ::2] = -0.0
