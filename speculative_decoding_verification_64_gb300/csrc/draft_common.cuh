@@ -203,62 +203,62 @@ __device__ __forceinline__ int place_index(unsigned long long p) {
   return (int)(0xFFFFFFFFu - (uint32_t)p);
 }
 
-// Ranks kE tokens a thread among list[0, n) and puts them there.
+// Sorts list[0, n) in kE chunks of one token a thread each: a token's rank in its own chunk is
+// counted, its rank in the others, once they are sorted, found by halves.
 template <int kThreads, int kE>
 __device__ __forceinline__ void sort_by_rank(unsigned long long *list, int n) {
+  const int tid = threadIdx.x;
   unsigned long long v[kE];
   int rank[kE];
 #pragma unroll
   for (int i = 0; i < kE; ++i) {
-    const int at = threadIdx.x + i * kThreads;
+    const int at = tid + i * kThreads, len = min(n - i * kThreads, kThreads);
     v[i] = at < n ? list[at] : 0ull;
     rank[i] = 0;
-  }
 #pragma unroll 4
-  for (int j = 0; j < n; ++j) {
-    const unsigned long long q = list[j];
-#pragma unroll
-    for (int i = 0; i < kE; ++i) rank[i] += q > v[i];
+    for (int j = 0; j < len; ++j) rank[i] += list[i * kThreads + j] > v[i];
   }
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kE; ++i)
-    if ((int)threadIdx.x + i * kThreads < n) list[rank[i]] = v[i];
+    if (tid + i * kThreads < n) list[i * kThreads + rank[i]] = v[i];
   __syncthreads();
-}
-
-// Sorts the CTA's list[0, n) downwards, all tokens of it different.  Up to four a thread
-// each token is compared with all others, which needs two barriers (17 tokens: 800 clocks,
-// 70 to 95 tokens: 2000 to 3000 beside another working CTA, where a bitonic network took
-// 6700); beyond that the network over the next power of two, its rest filled with 0 (below
-// every token).
-template <int kThreads>
-__device__ __noinline__ void sort_down(unsigned long long *list, int n) {
-  if (n <= kThreads) {
-    sort_by_rank<kThreads, 1>(list, n);
-    return;
-  }
-  if (n <= 4 * kThreads) {
-    sort_by_rank<kThreads, 4>(list, n);
-    return;
-  }
-  int len = 2;
-  while (len < n) len *= 2;
-  for (int i = n + threadIdx.x; i < len; i += kThreads) list[i] = 0ull;
-  __syncthreads();
-  for (int k = 2; k <= len; k *= 2) {
-    for (int j = k / 2; j > 0; j /= 2) {
-      for (int t = threadIdx.x; t < len / 2; t += kThreads) {
-        const int i = 2 * t - (t & (j - 1)), o = i + j;
-        const unsigned long long a = list[i], b = list[o];
-        if ((a < b) == ((i & k) == 0)) {
-          list[i] = b;
-          list[o] = a;
+  if constexpr (kE > 1) {
+#pragma unroll 1
+    for (int c = 0; c * kThreads < n; ++c) {
+      const int len = min(n - c * kThreads, kThreads);
+      int above[kE];  // tokens of the chunk that are larger
+#pragma unroll
+      for (int i = 0; i < kE; ++i) above[i] = 0;
+#pragma unroll 1
+      for (int step = kThreads; step > 0; step /= 2) {
+#pragma unroll
+        for (int i = 0; i < kE; ++i) {
+          const int at = above[i] + step;
+          if (at <= len && list[c * kThreads + at - 1] > v[i]) above[i] = at;
         }
       }
-      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kE; ++i) rank[i] += i == c ? 0 : above[i];
     }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kE; ++i)
+      if (tid + i * kThreads < n) list[rank[i]] = v[i];
+    __syncthreads();
   }
+}
+
+// Sorts the CTA's list[0, n) downwards, n <= 1024, all tokens of it different and none 0
+// (17 tokens: 800 clocks, 70 to 95 tokens: 2000 to 3000 beside another working CTA, where a
+// bitonic network took 6700; records of 512 entries of 1500 rows of 32000 128 us, each token
+// compared with all others 144).
+template <int kThreads>
+__device__ __noinline__ void sort_down(unsigned long long *list, int n) {
+  if (n <= kThreads)
+    sort_by_rank<kThreads, 1>(list, n);
+  else
+    sort_by_rank<kThreads, 1024 / kThreads>(list, n);
 }
 
 // m / T + ln s for s > 0, rounded about once: in units of 2^-40, where its parts are not

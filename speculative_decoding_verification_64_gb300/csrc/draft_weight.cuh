@@ -4,9 +4,10 @@
 //
 // With c = log2(e) / T as a pair of floats, x = (l - M) c is cut at the nearest multiple of
 // 2^-10: 2^x = 2^n 2^(j/1024) 2^f with |f| <= 2^-11.  2^(j/1024) comes from a table of
-// pairs, 2^f - 1 = f (ln 2 + f ln^2 2 / 2) with an error of 2^-37.  The difference l c - (M c + n + j / 1024) is one fused multiply-add, so that neither product
-// is rounded on its own; M c itself is first rounded to a multiple of 2^-10, which scales
-// all weights of a row alike.
+// pairs, 2^f - 1 = f (ln 2 + f ln^2 2 / 2) with an error of 2^-37.  The difference
+// l c - (M c + n + j / 1024) is one fused multiply-add, so that neither product is rounded on
+// its own; M c itself is first rounded to a multiple of 2^-10, which scales all weights of a
+// row alike.
 #pragma once
 
 #include "draft_common.cuh"

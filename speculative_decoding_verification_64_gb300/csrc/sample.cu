@@ -28,10 +28,10 @@
 // What bounds it: the chain of passes over the share and of exchanges, two CTAs an SM, and
 // where all tokens are weighed some 23 instructions an element (rows of 128256 bfloat16, a read
 // and a write of HBM):
-//   2304 flat rows, top-p 0.95 and min-p, logits out: 556 us, 2.1 TB/s of reads and writes.  Of a
+//   2304 flat rows, top-p 0.95 and min-p, logits out: 560 us, 2.1 TB/s of reads and writes.  Of a
 //     CTA's 38000 clocks arrival and maximum take 11000, counting 9000, summing the counts 9000,
 //     the rows 6000.  By the histogram and exact weights of all tokens: 797.
-//   672 rows, no filter, 3 draws and probabilities: 204 us.  Of 41000 clocks arrival and
+//   672 rows, no filter, 3 draws and probabilities: 206 us.  Of 41000 clocks arrival and
 //     maximum 9000, weights 17000, draws 2700, probabilities 9300.
 //   256 rows, top-p 0.9, a draw and probabilities: 122 us (four waves of CTAs, the last a third
 //     full; by the histogram 131).  One row of 32000 float32 under top-k 40 and top-p: 14 us, a
@@ -53,10 +53,10 @@ constexpr int kKeys = 4096;   // groups' maxima (256 of each of 16 CTAs)
 // The histogram's bins of a factor of two in weight, and its 24 octaves: a row's tail below
 // 2^-24 of its largest weight is 3 % of the mass at most for 2^19 tokens, and the exact pass
 // corrects the guess by what it found.  256 bfloat16 rows under top-p, 2304 flat ones, when
-// those came this way: 134 and 817 us;
-// with 128 bins an octave 140 and 849 (twice the bins to read from the other CTAs), with 32
-// 131 and 808, where flat rows of float32 bring brackets of twice the tokens.  With 16
-// octaves 206 us for the 256 rows: their tails' mass is missed, and a second bracket placed.
+// those came this way: 134 and 817 us; with 128 bins an octave 140 and 849 (twice the bins to
+// read from the other CTAs), with 32 131 and 808, where flat rows of float32 bring brackets of
+// twice the tokens.  With 16 octaves 206 us for the 256 rows: their tails' mass is missed, and
+// a second bracket placed.
 constexpr float kOctave = 64.0f;
 constexpr int kBins = 24 * 64;
 // A bracket reaches to either side of the place that the histogram names by this share of

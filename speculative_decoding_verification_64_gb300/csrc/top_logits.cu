@@ -82,7 +82,8 @@ __device__ __forceinline__ float group_maxima(const LaneData<DT> &d, int lane, f
   uint32_t w[kGroups / 2];
 #pragma unroll
   for (int k = 0; k < kGroups / 2; ++k) {
-    const uint32_t a = vector_max<DT>(d.v[k], k == 0 ? 0xFF800000u | __float_as_uint(d.edge) >> 16 : no_max<DT>());
+    const uint32_t edge = 0xFF800000u | __float_as_uint(d.edge) >> 16;
+    const uint32_t a = vector_max<DT>(d.v[k], k == 0 ? edge : no_max<DT>());
     const uint32_t b = vector_max<DT>(d.v[k + kGroups / 2], no_max<DT>());
     w[k] = max2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
   }
