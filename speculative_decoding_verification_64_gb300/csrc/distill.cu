@@ -19,7 +19,7 @@
 // a row are 64-bit.
 //
 // Measured: 4096 rows of 128256 bfloat16, 64 entries, gradient out: 446 us, 4.7 TB/s, 70 % of the
-// measured copy rate; 4080 rows of 32003 bfloat16: 103 us, 66 %; 508 rows of 152064 float32: 144 us,
+// measured copy rate; 4080 rows of 32003 bfloat16: 99 us, 69 %; 508 rows of 152064 float32: 144 us,
 // 64 %; 33 rows of 32000 float32: 10.3 us.  Of a CTA's 23000 clocks (three an SM) its share's
 // arrival takes 7600, the sum 3300, the exchange 3000, the loss 2200, the gradient 5000: the
 // chain of those steps, which three CTAs overlap in part, is what keeps it from the copy rate.

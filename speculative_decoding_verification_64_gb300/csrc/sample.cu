@@ -351,7 +351,7 @@ __device__ __forceinline__ void count_bin(uint32_t at) {
 // 2^23 + j.  Ends with the cluster's barrier.
 template <int DT>
 __device__ __forceinline__ void histogram(const Share &s, const uint8_t *buf, float M, float ch,
-                                          SampleSmem &sm) {
+                                          int size, SampleSmem &sm) {
   constexpr int kN = Elem<DT>::kN;
   for (int i = threadIdx.x; i < kBins; i += kThreads) sm.bin[i] = 0;
   __syncthreads();
@@ -369,7 +369,7 @@ __device__ __forceinline__ void histogram(const Share &s, const uint8_t *buf, fl
     }
   }
   __syncthreads();
-  cluster_sync();
+  cluster_sync(size);
 }
 
 // Where the mass of the cluster's histograms reaches `want` in their first bins (of weights
@@ -545,7 +545,7 @@ __device__ __noinline__ bool cut_by_values(const Share &s, const uint8_t *buf, c
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   count_values(s, buf, M - 60.0f / w.ch, sm);
   __syncthreads();
-  cluster_sync();
+  cluster_sync(size);
   const uint32_t vals = smem_addr(sm.val);
   const int per = (kMags + size - 1) / size;
   const int m0 = min(rank * per, kMags), m1 = min(m0 + per, kMags);
@@ -713,7 +713,7 @@ __device__ __noinline__ bool cut_by_values(const Share &s, const uint8_t *buf, c
     if (tid == 0) sm.n_mine = 0;
     __syncthreads();
     if (here > kMine) {
-      cluster_sync();  // (the counts' last readers)
+      cluster_sync(size);  // (the counts' last readers)
       return false;
     }
     if (rank == of) {
@@ -1112,7 +1112,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       float guess = top_p, hist_before;
       Found f;  // of the whole row
       u64 want;
-      histogram<DT>(s, buf, M, ch, sm);
+      histogram<DT>(s, buf, M, ch, size, sm);
       for (int tries = 0;; ++tries) {
         if (tries == kLimit) {
           st = SPECDEC_ROW_INTERNAL;
@@ -1213,7 +1213,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         const float unit = ex2_approx(-w.rest) / kFixed;
         guess = hist_before + ((float)want - (float)f.above) * unit;
         // (rank 0's list stands where its histogram was: it is made again)
-        if (tries < kTries - 1) histogram<DT>(s, buf, M, ch, sm);
+        if (tries < kTries - 1) histogram<DT>(s, buf, M, ch, size, sm);
         __syncthreads();
         if (tid == 0) sm.n_mine = 0;
         __syncthreads();
