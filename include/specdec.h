@@ -669,8 +669,9 @@ int specdec_top_logits(const void *logits, int dtype, long long request_stride,
  *   loss = sum_j p_j (ln p_j - ln s_id_j) + r (ln r - ln s_rest),
  * s_rest the mass of s outside the entries: the divergence KL(p || s), what the record
  * does not name taken as one token.  The gradient written is weight * d loss / d x.
- * r below 2^-20 (what a float32 lse leaves unsure) counts as 0 where s_rest is 0, and s_rest
- * is 0 below about 2^-126 (a larger r then makes the loss infinite).
+ * s_rest below 2^-126 counts as 0.  Where it is 0, so does an r below 2^-17 + 2^-22 |lse| (what
+ * the rounding of a float32 lse leaves over of a record of all tokens); a larger one makes the
+ * loss infinite.
  *
  *   logits       [B, R, V], float32 or bfloat16 (dtype)
  *   ids          int32 [B, R, K]; -1: no entry there.  No token twice

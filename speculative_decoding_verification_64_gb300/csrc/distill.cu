@@ -219,6 +219,7 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
   float m = -INFINITY;
   const unsigned long long(*got)[kWords] = nullptr;
   float coef = 0.0f, M = 0.0f, inv_s = 0.0f, left = 0.0f, inv_zs = 1.0f;
+  bool some_rest = false;  // s has mass outside the entries
   long long mass = 0;
   int st = 0;
   if (w != 0.0f) {
@@ -369,13 +370,16 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
     }
     inv_s = 1.0f / S;
     const float of = others * inv_s;
+    some_rest = of >= 0x1p-126f;
     float share = 1.0f;  // what is left of s outside the entries
     if (p.lse) {
-      // a log-sum-exp in float32 leaves about 2^-21 of the mass unsure: nothing is asked
-      // of a row that has nothing to give
+      // The shares of a record of all tokens add up to 1 but for its log-sum-exp's rounding, and
+      // that of the logits over T before their sum (three half steps of |lse|), and for a float32
+      // sum of them (exponents of some 7 units, exponentials, additions, the shares: 68 half steps
+      // of 1).  So much is not asked of a row that has nothing to give.
       left = fmaxf((float)((1ll << 40) - mass) * 0x1p-40f, 0.0f);
-      if (!(of > 0.0f) && left < 0x1p-20f) left = 0.0f;
-      share = of > 0.0f ? 1.0f - left / of : 0.0f;
+      if (!some_rest && left < fmaf(fabsf(lse), 0x1p-22f, 0x1p-17f)) left = 0.0f;
+      share = some_rest ? 1.0f - left / of : 0.0f;
     }
     coef = fminf(fmaxf(w * p.inv_t * share * inv_s, -3.0e38f), 3.0e38f);
   }
@@ -414,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
       const long long arg = tid == 0 ? S : tid == 1 ? O : r;
       float v = (float)arg * 0x1p-40f, low = (float)(arg - (long long)(float)arg) * 0x1p-40f;
       if (tid == 1 && O < kOne >> 10) {  // (few units: as float32 has it)
-        v = others;
+        v = fmaxf(others, 0x1p-126f);
         low = 0.0f;
       } else if (tid == 2 && !p.lse) {
         v = inv_zs;
@@ -433,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
             large += (float)mass * 0x1p-40f * ((a.hi - lse) + (a.lo + (float)ln * 0x1p-40f));
           }
           if (left > 0.0f) {
-            if (others >= 0x1p-126f) t += mul_fixed(r, ln2 - ln1 + ln);
+            if (some_rest) t += mul_fixed(r, ln2 - ln1 + ln);
             else large = INFINITY;
           }
         } else {

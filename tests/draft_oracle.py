@@ -96,8 +96,10 @@ def distill(x, ids, z, lse=None, T=1.0):
         rest = np.ones(len(x), dtype=bool)
         rest[ids] = False
         r, s = max(0.0, 1.0 - p.sum()), np.exp(log_s[rest]).sum()
-        if not s > 0 and r < 2.0 ** -20:
-            r = 0.0
+        if s < 2.0 ** -126:  # none, and r is what a float32 log-sum-exp leaves over
+            s = 0.0
+            if r < 2.0 ** -17 + 2.0 ** -22 * abs(float(lse)):
+                r = 0.0
         if r > 0:
             loss += r * (np.log(r) - np.log(s))
             target[rest] = r * np.exp(log_s[rest]) / s
