@@ -2,9 +2,10 @@
 // (specdec_distill).  With s = softmax(x / T) over the row and p_j the teacher's share of
 // entry j (token id_j):
 //     L = sum_j p_j (ln p_j - ln s_id_j) + r (ln r - ln s_rest)
-//     dL/dx_v = (s_v - p_v) / T at an entry's token, (s_v - r s_v / s_rest) / T elsewhere,
-// r = 1 - sum p_j and s_rest = the mass of s outside the entries when the teacher's
-// log-sum-exp is given; without it p = softmax over the entries and r = 0.
+//     dL/dx_v = (P s_v - p_v) / T at an entry's token, (P s_v - r s_v / s_rest) / T elsewhere,
+// r = max(0, 1 - sum p_j), P = r + sum p_j (1 but for records of more than 1) and s_rest = the
+// mass of s outside the entries when the teacher's log-sum-exp is given; without it p = softmax
+// over the entries, r = 0 and P = 1.
 //
 // A row is held in shared memory by a cluster of CTAs: it is read from HBM once, whatever
 // is computed from it, and the gradient is written once.  While the copies land, the
@@ -219,6 +220,7 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
   float m = -INFINITY;
   const unsigned long long(*got)[kWords] = nullptr;
   float coef = 0.0f, M = 0.0f, inv_s = 0.0f, left = 0.0f, inv_zs = 1.0f;
+  float whole = 1.0f;      // the shares' sum, r among them
   bool some_rest = false;  // s has mass outside the entries
   long long mass = 0;
   int st = 0;
@@ -379,7 +381,8 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
       // of 1).  So much is not asked of a row that has nothing to give.
       left = fmaxf((float)((1ll << 40) - mass) * 0x1p-40f, 0.0f);
       if (!some_rest && left < fmaf(fabsf(lse), 0x1p-22f, 0x1p-17f)) left = 0.0f;
-      share = some_rest ? 1.0f - left / of : 0.0f;
+      if (!(left > 0.0f)) whole = (float)mass * 0x1p-40f;
+      share = some_rest ? whole - left / of : 0.0f;
     }
     coef = fminf(fmaxf(w * p.inv_t * share * inv_s, -3.0e38f), 3.0e38f);
   }
@@ -478,9 +481,9 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
     }
     __syncthreads();
     if (!plain) {
-      const float k = w * p.inv_t;
+      const float k = w * p.inv_t, by = whole * inv_s;
       for (int j = tid; j < sm.entries; j += kThreads) {
-        const float y = k * (ex2_approx((at_x[j] - M) * c) * inv_s - at_p[j]);
+        const float y = k * (ex2_approx((at_x[j] - M) * c) * by - at_p[j]);
         put_elem<DT>(like ? out + (ptrdiff_t)(s.first + pos[j]) * es : buf + (size_t)pos[j] * es, y);
       }
     }

@@ -90,7 +90,7 @@ def distill(x, ids, z, lse=None, T=1.0):
         log_p = z - float(lse)
     p = np.exp(log_p)
     loss = float(sum(a * (b - c) for a, b, c in zip(p, log_p, log_s[ids]) if a > 0))
-    target = np.zeros(len(x))
+    target, whole = np.zeros(len(x)), p.sum()
     target[ids] = p
     if lse is not None:
         rest = np.ones(len(x), dtype=bool)
@@ -103,4 +103,5 @@ def distill(x, ids, z, lse=None, T=1.0):
         if r > 0:
             loss += r * (np.log(r) - np.log(s))
             target[rest] = r * np.exp(log_s[rest]) / s
-    return loss, (np.exp(log_s) - target) / T
+            whole += r
+    return loss, (whole * np.exp(log_s) - target) / T
