@@ -668,7 +668,9 @@ int specdec_top_logits(const void *logits, int dtype, long long request_stride,
  *   without            p = softmax of z / T over the entries, r = 0;
  *   loss = sum_j p_j (ln p_j - ln s_id_j) + r (ln r - ln s_rest),
  * s_rest the mass of s outside the entries: the divergence KL(p || s), what the record
- * does not name taken as one token.  The gradient written is weight * d loss / d x.
+ * does not name taken as one token.  The gradient written is weight * d loss / d x.  (A lse
+ * below that of the entries gives p of more than 1 in all; loss and gradient are those of the
+ * formula then, up to a p of 2^12.)
  * s_rest below 2^-126 counts as 0.  Where it is 0, so does an r below 2^-17 + 2^-22 |lse| (what
  * the rounding of a float32 lse leaves over of a record of all tokens); a larger one makes the
  * loss infinite.
@@ -683,8 +685,9 @@ int specdec_top_logits(const void *logits, int dtype, long long request_stride,
  *   loss         float32 [B, R], without the weight
  *   grad         [B, R, V] in dtype, or NULL: the loss alone
  *   row_status   int32 [B, R]: SPECDEC_ROW_BAD_TOKEN (an id outside [-1, V), a token
- *                twice), SPECDEC_ROW_NONFINITE (an unusable row, teacher or weight),
- *                SPECDEC_ROW_INTERNAL; such a row gets NaN in its loss and its gradient
+ *                twice), SPECDEC_ROW_NONFINITE (an unusable row, teacher or weight, a p
+ *                above 2^12), SPECDEC_ROW_INTERNAL; such a row gets NaN in its loss and its
+ *                gradient
  * A row of weight 0, or without an entry, gets loss 0, gradient 0 and status 0 whatever
  * it holds.  Limits: 1 <= K <= SPECDEC_MAX_TOPK, V <= SPECDEC_MAX_DRAFT_V.  B = 0 is a
  * no-op.

@@ -47,7 +47,8 @@ struct DistillSmem {
 
 constexpr float kTerm = 0x1p40f;  // units of the fixed-point sums
 constexpr float kMost = 0x1p12f;  // terms that they take (1024 of them); the larger are added
-                                  // in float32, where a loss with such a term ends anyway
+                                  // in float32, where a loss with such a term ends anyway (shares
+                                  // that large are refused)
 
 // Dynamic shared memory: DistillSmem, the share, one bit for each of its elements, and a
 // position, logit and teacher's share for each entry.
@@ -257,6 +258,7 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
       y.hi = l;
       const Two e = exp_two(y);
       pj[i] = (e.hi + e.lo) * inv_zs;
+      if (!(pj[i] <= kMost)) status |= SPECDEC_ROW_NONFINITE;
     }
 
     // the largest logit, as the copies land

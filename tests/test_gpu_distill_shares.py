@@ -1,5 +1,5 @@
 """specdec_distill on records whose shares add up to more than 1 (a log-sum-exp of another
-temperature, or of other logits): the gradient is that of the loss."""
+temperature, or of other logits): the gradient is that of the loss, shares beyond the sums are refused."""
 import numpy as np
 import pytest
 
@@ -65,3 +65,21 @@ def test_under_autograd(sd):
     d = floats([[1.0, 3.0, 0.0], [0.5, 1.0, -2.0]])
     g, = torch.autograd.grad(sd.distill_loss(t, ids, z, lse), t, d)
     assert torch.equal(g, sd.distill(t.detach(), ids, z, lse, d).grad)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [500, 70000])
+def test_shares_beyond_the_sums_are_refused(sd, V, dtype):
+    """A share of more than 2^12: SPECDEC_ROW_NONFINITE, up to it the loss and the gradient."""
+    x = normal(23, 1, 5, V)
+    ids = np.broadcast_to(np.array([V - 1, 2], dtype=np.int32), (1, 5, 2)).copy()
+    z = np.broadcast_to(np.array([0.0, -1.0], dtype=np.float32), (1, 5, 2)).copy()
+    lse = np.array([[-8.31, -8.33, -50.0, -1e3, -1e30]], dtype=np.float32)  # e^8.318 = 2^12
+    r = sd.distill(on_gpu(x, dtype), cuda(ids), cuda(z), cuda(lse))
+    assert r.row_status[0].tolist() == [0] + [sd.ROW_NONFINITE] * 4
+    assert r.loss[0, 1:].isnan().all() and r.grad[0, 1:].isnan().all()
+    check(sd, x[:, :1], ids[:, :1].copy(), z[:, :1].copy(), lse[:, :1].copy(), dtype=dtype)
+    # an absent entry's, and one of no probability, are not looked at
+    ids[0, :, 0], z[0, :, 1] = -1, -np.inf
+    r = sd.distill(on_gpu(x, dtype), cuda(ids), cuda(z), cuda(lse))
+    assert (r.row_status == 0).all()
