@@ -594,9 +594,11 @@ int specdec_attend(const void *q, const void *k_new, const void *v_new, int dtyp
  * Rows of logits stand in requests of R rows: row (b, r) at request_stride * b +
  * row_stride * r elements, its V elements one after another.  Rows may be slices (of a
  * padded vocabulary, of one position of a [B, gamma, V] array) and start anywhere an
- * element may.  Rows that a call writes follow the same rule with strides of their own,
- * may be the rows that it reads (same pointer and strides) and must not overlap them
- * otherwise.  A row is usable as in specdec_row_stats: no NaN or +infinity, one finite
+ * element may.  No two share an element, and all of them stand within 2^56 bytes; the
+ * stride of a single request or row is not used.  B * R < 2^27.  Rows that a call writes
+ * follow the same rule with strides of their own; they are the rows that it reads (same
+ * pointer and strides) or stand apart (neither within the span from the others' first to
+ * their last).  A row is usable as in specdec_row_stats: no NaN or +infinity, one finite
  * value, none above 2^100; -infinity takes a token out.  row_status is per row here.
  */
 

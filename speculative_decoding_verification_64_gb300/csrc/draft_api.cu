@@ -34,14 +34,18 @@ int rows_status(int dtype, int B, int R, int V, int most) {
 
 bool temperature_bad(float T) { return !(T >= 0x1p-20f && T <= 0x1p20f); }
 
+// More bytes than any address space has, and few enough for the kernels' offsets of 64 bits.
+constexpr __int128 kMostBytes = (__int128)1 << 56;
+
 // Strides under which the rows of V elements share none: rows of a request together, or
-// the requests' rows of one number together.
-bool strides_bad(int B, int R, int V, RowsAt at) {
-  if (at.request < 0 || at.row < 0 || at.request > LLONG_MAX / INT_MAX / 8 ||
-      at.row > LLONG_MAX / INT_MAX / 8)
-    return true;
-  const bool by_request = (R == 1 || at.row >= V) && (B <= 1 || at.request >= (R - 1) * at.row + V);
-  const bool by_row = (B <= 1 || at.request >= V) && (R == 1 || at.row >= (B - 1) * at.request + V);
+// the requests' rows of one number together.  A single row's or request's stride is not used.
+bool strides_bad(int B, int R, int V, RowsAt at, int es) {
+  const __int128 request = B > 1 ? at.request : 0, row = R > 1 ? at.row : 0;
+  if (request < 0 || row < 0) return true;
+  const __int128 requests = (B > 1 ? B - 1 : 0) * request, rows = (R - 1) * row;
+  if ((requests + rows + V) * es > kMostBytes) return true;
+  const bool by_request = (R == 1 || row >= V) && (B <= 1 || request >= rows + V);
+  const bool by_row = (B <= 1 || request >= V) && (R == 1 || row >= requests + V);
   return !by_request && !by_row;
 }
 
@@ -68,8 +72,8 @@ int distill_params(DistillParams &p, const void *logits, int dtype, RowsAt at, c
                    int B, int R, int V, int K, void *grad, RowsAt grad_at) {
   const int st = rows_status(dtype, B, R, V, SPECDEC_MAX_DRAFT_V);
   if (st != SPECDEC_OK) return st;
-  if (K < 1 || temperature_bad(temperature) || strides_bad(B, R, V, at) ||
-      (grad && strides_bad(B, R, V, grad_at)))
+  if (K < 1 || temperature_bad(temperature) || strides_bad(B, R, V, at, elem_bytes(dtype)) ||
+      (grad && strides_bad(B, R, V, grad_at, elem_bytes(dtype))))
     return SPECDEC_ERR_INVALID_ARG;
   if (K > SPECDEC_MAX_TOPK) return SPECDEC_ERR_UNSUPPORTED;
   if (B == 0) return SPECDEC_OK;
@@ -111,8 +115,8 @@ int specdec_sample(const void *logits, int dtype, long long request_stride, long
   SampleParams p = {};
   p.x_at = {request_stride, row_stride};
   p.rows_at = {rows_request_stride, rows_row_stride};
-  if (S < 0 || (flags & ~SPECDEC_SAMPLE_LOGITS) || strides_bad(B, R, V, p.x_at) ||
-      (rows && strides_bad(B, R, V, p.rows_at)))
+  if (S < 0 || (flags & ~SPECDEC_SAMPLE_LOGITS) || strides_bad(B, R, V, p.x_at, elem_bytes(dtype)) ||
+      (rows && strides_bad(B, R, V, p.rows_at, elem_bytes(dtype))))
     return SPECDEC_ERR_INVALID_ARG;
   if (S > SPECDEC_MAX_DRAWS) return SPECDEC_ERR_UNSUPPORTED;
   if (B == 0) return SPECDEC_OK;
@@ -158,7 +162,8 @@ int specdec_top_logits(const void *logits, int dtype, long long request_stride,
   if (st != SPECDEC_OK) return st;
   TopParams p = {};
   p.x_at = {request_stride, row_stride};
-  if (K < 1 || K > V || temperature_bad(temperature) || strides_bad(B, R, V, p.x_at))
+  if (K < 1 || K > V || temperature_bad(temperature) ||
+      strides_bad(B, R, V, p.x_at, elem_bytes(dtype)))
     return SPECDEC_ERR_INVALID_ARG;
   if (K > SPECDEC_MAX_TOPK) return SPECDEC_ERR_UNSUPPORTED;
   if (B == 0) return SPECDEC_OK;
