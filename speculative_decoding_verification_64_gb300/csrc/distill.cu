@@ -221,8 +221,6 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
   float m = -INFINITY;
   const unsigned long long(*got)[kWords] = nullptr;
   float coef = 0.0f, M = 0.0f, inv_s = 0.0f, left = 0.0f, inv_zs = 1.0f;
-  float whole = 1.0f;      // the shares' sum, r among them
-  bool some_rest = false;  // s has mass outside the entries
   long long mass = 0;
   int st = 0;
   if (w != 0.0f) {
@@ -258,7 +256,6 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
       y.hi = l;
       const Two e = exp_two(y);
       pj[i] = (e.hi + e.lo) * inv_zs;
-      if (!(pj[i] <= kMost)) status |= SPECDEC_ROW_NONFINITE;
     }
 
     // the largest logit, as the copies land
@@ -297,6 +294,7 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
         else
           large += x > -INFINITY ? t : INFINITY;
         at_mass += __float2ll_rn(fminf(pj[i], kMost) * kTerm);
+        if (pj[i] > kMost) status |= SPECDEC_ROW_NONFINITE;
       }
       const int k = atomicAdd(&sm.entries, 1);  // (their order decides nothing)
       pos[k] = at;
@@ -374,8 +372,8 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
     }
     inv_s = 1.0f / S;
     const float of = others * inv_s;
-    some_rest = of >= 0x1p-126f;
-    float share = 1.0f;  // what is left of s outside the entries
+    const bool some_rest = of >= 0x1p-126f;
+    float whole = 1.0f, share = 1.0f;  // the shares' sum, what is left of s outside the entries
     if (p.lse) {
       // The shares of a record of all tokens add up to 1 but for its log-sum-exp's rounding, and
       // that of the logits over T before their sum (three half steps of |lse|), and for a float32
@@ -385,8 +383,10 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
       if (!some_rest && left < fmaf(fabsf(lse), 0x1p-22f, 0x1p-17f)) left = 0.0f;
       if (!(left > 0.0f)) whole = (float)mass * 0x1p-40f;
       share = some_rest ? whole - left / of : 0.0f;
+      if (left > 0.0f && !some_rest) left = INFINITY;  // (the loss asks for no more than that)
     }
     coef = fminf(fmaxf(w * p.inv_t * share * inv_s, -3.0e38f), 3.0e38f);
+    inv_s *= whole;
   }
 
   if (rank == 0 && tid < 32 && p.loss) {
@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
             large += (float)mass * 0x1p-40f * ((a.hi - lse) + (a.lo + (float)ln * 0x1p-40f));
           }
           if (left > 0.0f) {
-            if (some_rest) t += mul_fixed(r, ln2 - ln1 + ln);
+            if (left < INFINITY) t += mul_fixed(r, ln2 - ln1 + ln);
             else large = INFINITY;
           }
         } else {
@@ -483,9 +483,9 @@ __global__ void __launch_bounds__(kThreads, 3) distill_kernel(const DistillParam
     }
     __syncthreads();
     if (!plain) {
-      const float k = w * p.inv_t, by = whole * inv_s;
+      const float k = w * p.inv_t;
       for (int j = tid; j < sm.entries; j += kThreads) {
-        const float y = k * (ex2_approx((at_x[j] - M) * c) * by - at_p[j]);
+        const float y = k * (ex2_approx((at_x[j] - M) * c) * inv_s - at_p[j]);
         put_elem<DT>(like ? out + (ptrdiff_t)(s.first + pos[j]) * es : buf + (size_t)pos[j] * es, y);
       }
     }
