@@ -1200,11 +1200,14 @@ def distill_loss(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor,
                  lse: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None,
                  temperature: float = 1.0, stream=None) -> torch.Tensor:
     """``weight`` times the divergences of ``distill``, float32 [B, R], under autograd (for the
-    logits).  The gradient is made with the loss, from one look at the logits, and holds for
-    rows whose incoming gradient is 1, as under ``.sum()``: a mean is cheaper as weights of
-    1 / n than as a division afterwards.  A malformed row's loss and gradient are NaN."""
+    logits and the weights).  The logits' gradient is made with the loss, from one look at
+    them, and holds for rows whose incoming gradient is 1, as under ``.sum()``: a mean is
+    cheaper as weights of 1 / n than as a division afterwards.  A weight's gradient is its
+    row's divergence, for which rows of weight 0 are looked at too where the weights require
+    one.  A malformed row's loss and gradients are NaN."""
     with _on(stream):
-        if torch.is_grad_enabled() and logits.requires_grad:
+        if torch.is_grad_enabled() and (logits.requires_grad or
+                                        (weight is not None and weight.requires_grad)):
             return _Distill.apply(logits, ids, teacher, lse, weight, temperature)
         loss = distill(logits, ids, teacher, lse, weight, temperature, grad=False).loss
         return loss if weight is None else loss * weight
@@ -1216,23 +1219,30 @@ class _Distill(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, logits, ids, teacher, lse, weight, temperature):
-        r = distill(logits, ids, teacher, lse, weight, temperature)
-        ctx.save_for_backward(logits, ids, teacher, lse, weight)
+        r = distill(logits, ids, teacher, lse, weight, temperature, grad=ctx.needs_input_grad[0])
+        loss = None
+        if ctx.needs_input_grad[4]:  # the rows of weight 0 have theirs too
+            alone = (weight == 0).float()
+            loss = r.loss + distill(logits, ids, teacher, lse, alone, temperature, grad=False).loss
+        ctx.save_for_backward(logits, ids, teacher, lse, weight, loss)
         ctx.temperature, ctx.grad = temperature, r.grad
         return r.loss if weight is None else r.loss * weight
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dloss):
-        logits, ids, teacher, lse, weight = ctx.saved_tensors
+        logits, ids, teacher, lse, weight, loss = ctx.saved_tensors
         dloss = dloss.contiguous()
+        dweight = None if loss is None else dloss * loss
         grad, ctx.grad = ctx.grad, None
-        if grad is None:
+        if not ctx.needs_input_grad[0]:
+            grad = None
+        elif grad is None:
             w = dloss if weight is None else dloss * weight
             grad = distill(logits, ids, teacher, lse, w, ctx.temperature).grad
         else:
             _distill_backward(logits, ids, teacher, lse, weight, ctx.temperature, dloss, grad)
-        return (grad,) + (None,) * 5
+        return grad, None, None, None, dweight, None
 
 
 def _distill_backward(logits, ids, teacher, lse, weight, temperature, dloss, grad):
