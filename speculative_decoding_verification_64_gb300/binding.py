@@ -1204,7 +1204,12 @@ def distill_loss(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor,
     them, and holds for rows whose incoming gradient is 1, as under ``.sum()``: a mean is
     cheaper as weights of 1 / n than as a division afterwards.  A weight's gradient is its
     row's divergence, for which rows of weight 0 are looked at too where the weights require
-    one.  A malformed row's loss and gradients are NaN."""
+    one.  A malformed row's loss and gradients are NaN.  The teacher is a constant: a ``teacher``
+    or ``lse`` that requires a gradient is refused."""
+    if torch.is_grad_enabled():
+        for name, t in (("teacher", teacher), ("lse", lse)):
+            if t is not None and t.requires_grad:
+                raise ValueError(f"distill_loss has no gradient for {name}: pass {name}.detach()")
     with _on(stream):
         if torch.is_grad_enabled() and (logits.requires_grad or
                                         (weight is not None and weight.requires_grad)):
