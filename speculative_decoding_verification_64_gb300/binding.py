@@ -1205,28 +1205,27 @@ def distill_loss(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor,
     cheaper as weights of 1 / n than as a division afterwards.  A weight's gradient is its
     row's divergence, for which rows of weight 0 are looked at too where the weights require
     one.  A malformed row's loss and gradients are NaN.  The teacher is a constant: a ``teacher``
-    or ``lse`` that requires a gradient is refused."""
-    if torch.is_grad_enabled():
+    or ``lse`` that requires a gradient is refused, and so are tangents (forward mode)."""
+    learn = torch.is_grad_enabled()
+    if learn:
         for name, t in (("teacher", teacher), ("lse", lse)):
             if t is not None and t.requires_grad:
                 raise ValueError(f"distill_loss has no gradient for {name}: pass {name}.detach()")
     with _on(stream):
-        if torch.is_grad_enabled() and (logits.requires_grad or
-                                        (weight is not None and weight.requires_grad)):
-            return _Distill.apply(logits, ids, teacher, lse, weight, temperature)
-        loss = distill(logits, ids, teacher, lse, weight, temperature, grad=False).loss
-        return loss if weight is None else loss * weight
+        return _Distill.apply(logits, ids, teacher, lse, weight, temperature, learn)
 
 
 class _Distill(torch.autograd.Function):
     """``distill`` under autograd.  The first backward turns the forward's gradient into its
-    own, in place; a second one (over a retained graph) makes it anew."""
+    own, in place; a second one (over a retained graph) makes it anew.  Calls without a gradient
+    to make come through here too: torch refuses tangents where no form of them is defined."""
 
     @staticmethod
-    def forward(ctx, logits, ids, teacher, lse, weight, temperature):
-        r = distill(logits, ids, teacher, lse, weight, temperature, grad=ctx.needs_input_grad[0])
+    def forward(ctx, logits, ids, teacher, lse, weight, temperature, learn):
+        r = distill(logits, ids, teacher, lse, weight, temperature,
+                    grad=learn and ctx.needs_input_grad[0])
         loss = None
-        if ctx.needs_input_grad[4]:  # the rows of weight 0 have theirs too
+        if learn and ctx.needs_input_grad[4]:  # the rows of weight 0 have theirs too
             alone = (weight == 0).float()
             loss = r.loss + distill(logits, ids, teacher, lse, alone, temperature, grad=False).loss
         ctx.save_for_backward(logits, ids, teacher, lse, weight, loss)
@@ -1247,7 +1246,7 @@ class _Distill(torch.autograd.Function):
             grad = distill(logits, ids, teacher, lse, w, ctx.temperature).grad
         else:
             _distill_backward(logits, ids, teacher, lse, weight, ctx.temperature, dloss, grad)
-        return grad, None, None, None, dweight, None
+        return grad, None, None, None, dweight, None, None
 
 
 def _distill_backward(logits, ids, teacher, lse, weight, temperature, dloss, grad):

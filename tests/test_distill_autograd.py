@@ -38,3 +38,40 @@ def test_the_teacher_has_no_gradient(sd, name, learn):
         assert not sd.distill_loss(**v).requires_grad
     v[name] = v[name].detach()
     assert sd.distill_loss(**v).requires_grad == learn
+
+
+@pytest.mark.parametrize("name", ["logits", "teacher", "lse", "weight"])
+@pytest.mark.parametrize("learn", [True, False])
+def test_tangents_are_refused(sd, name, learn):
+    import torch.autograd.forward_ad as forward_ad
+    v = inputs()
+    v["logits"].requires_grad_(learn)
+    with forward_ad.dual_level():
+        v[name] = forward_ad.make_dual(v[name], torch.ones_like(v[name]))
+        with pytest.raises(NotImplementedError, match="forward mode"):
+            sd.distill_loss(**v)
+        v[name] = forward_ad.unpack_dual(v[name]).primal
+        sd.distill_loss(**v)
+
+
+def test_functional_transforms_are_refused(sd):
+    v = inputs()
+    x = v.pop("logits")
+    with pytest.raises(RuntimeError):
+        torch.func.jvp(lambda x: sd.distill_loss(x, **v), (x,), (torch.ones_like(x),))
+    with pytest.raises(RuntimeError):
+        torch.func.grad(lambda x: sd.distill_loss(x, **v).sum())(x)
+
+
+@pytest.mark.parametrize("mode", [torch.no_grad, torch.inference_mode])
+def test_nothing_is_made_for_nobody(sd, monkeypatch, mode):
+    """No gradient where none is recorded, whatever requires one."""
+    v = inputs()
+    v["logits"].requires_grad_(True)
+    v["weight"].requires_grad_(True)
+    made = []
+    call = sd.distill
+    monkeypatch.setattr(sd, "distill", lambda *a, **kw: made.append(kw["grad"]) or call(*a, **kw))
+    with mode():
+        loss = sd.distill_loss(**v)
+    assert made == [False] and not loss.requires_grad
