@@ -1242,7 +1242,7 @@ class _Distill(torch.autograd.Function):
         if not ctx.needs_input_grad[0]:
             grad = None
         elif grad is None:
-            w = dloss if weight is None else dloss * weight
+            w = dloss if weight is None else torch.where(weight == 0, weight, dloss * weight)
             grad = distill(logits, ids, teacher, lse, w, ctx.temperature).grad
         else:
             _distill_backward(logits, ids, teacher, lse, weight, ctx.temperature, dloss, grad)

@@ -97,3 +97,16 @@ def test_learned_weights(sd):
     assert (a.grad - b.grad).abs().max() <= 2.0 ** -21 * alone.loss.abs().max()
     want = sd.distill(t.detach(), ids, z, lse, torch.softmax(b.detach(), 1) * (0.5 / 6)).grad
     assert (t.grad - want).abs().max() <= 2.0 ** -21 * want.abs().max()
+
+
+def test_rows_of_weight_0_under_any_gradient(sd):
+    """Nothing comes of them, the first time and over a retained graph, whatever comes in."""
+    x, record = case(35)
+    ids, z, lse = (cuda(a) for a in record)
+    t, w = on_gpu(x, "f32").requires_grad_(True), floats(W)
+    loss = sd.distill_loss(t, ids, z, lse, w)
+    d = floats([[1.0, float("inf"), 1.0], [1.0, 1.0, float("nan")]])
+    want = sd.distill(t.detach(), ids, z, lse, w).grad
+    for _ in range(3):
+        g, = torch.autograd.grad(loss, t, d, retain_graph=True)
+        assert torch.equal(g, want) and (g[0, 1] == 0).all() and (g[1, 2] == 0).all()
