@@ -1217,7 +1217,8 @@ def distill_loss(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor,
 
 class _Distill(torch.autograd.Function):
     """``distill`` under autograd.  The first backward turns the forward's gradient into its
-    own, in place; a second one (over a retained graph) makes it anew.  Calls without a gradient
+    own, in place; a second one (over a retained graph) makes it anew.  It is saved like the inputs,
+    so that hooks on saved tensors (offloading, checkpoints) have it too.  Calls without a gradient
     to make come through here too: torch refuses tangents where no form of them is defined."""
 
     @staticmethod
@@ -1228,24 +1229,25 @@ class _Distill(torch.autograd.Function):
         if learn and ctx.needs_input_grad[4]:  # the rows of weight 0 have theirs too
             alone = (weight == 0).float()
             loss = r.loss + distill(logits, ids, teacher, lse, alone, temperature, grad=False).loss
-        ctx.save_for_backward(logits, ids, teacher, lse, weight, loss)
-        ctx.temperature, ctx.grad = temperature, r.grad
+        ctx.save_for_backward(logits, ids, teacher, lse, weight, loss, r.grad)
+        ctx.temperature, ctx.spent = temperature, False
         return r.loss if weight is None else r.loss * weight
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dloss):
-        logits, ids, teacher, lse, weight, loss = ctx.saved_tensors
+        logits, ids, teacher, lse, weight, loss, grad = ctx.saved_tensors
         dloss = dloss.contiguous()
         dweight = None if loss is None else dloss * loss
-        grad, ctx.grad = ctx.grad, None
         if not ctx.needs_input_grad[0]:
             grad = None
-        elif grad is None:
+        elif ctx.spent:
             w = dloss if weight is None else torch.where(weight == 0, weight, dloss * weight)
             grad = distill(logits, ids, teacher, lse, w, ctx.temperature).grad
         else:
+            ctx.spent = True
             _distill_backward(logits, ids, teacher, lse, weight, ctx.temperature, dloss, grad)
+            grad = grad.data  # (the caller's: what becomes of it is no change of a saved tensor)
         return grad, None, None, None, dweight, None, None
 
 

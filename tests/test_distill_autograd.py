@@ -75,3 +75,47 @@ def test_nothing_is_made_for_nobody(sd, monkeypatch, mode):
     with mode():
         loss = sd.distill_loss(**v)
     assert made == [False] and not loss.requires_grad
+
+
+def test_hooks_on_saved_tensors_have_the_gradient(sd):
+    """Whatever is as large as the logits goes through them, and is gone with the graph."""
+    import gc
+    import weakref
+    v = inputs()
+    v["logits"].requires_grad_(True)
+    packed, held = [], []
+
+    def pack(t):
+        packed.append(tuple(t.shape))
+        t = t.detach().clone()
+        held.append(weakref.ref(t))
+        return t
+
+    with torch.autograd.graph.saved_tensors_hooks(pack, lambda t: t):
+        loss = sd.distill_loss(**v).sum()
+    assert packed.count((B, R, V)) == 2  # the logits, their gradient
+    node = loss.grad_fn.next_functions[0][0]
+    large = [k for k, t in vars(node).items() if torch.is_tensor(t)]
+    assert not large
+    g, = torch.autograd.grad(loss, v["logits"])
+    assert g.shape == (B, R, V)
+    del g, loss, node
+    gc.collect()
+    assert all(r() is None for r in held)
+
+
+def test_what_becomes_of_a_gradient_is_the_callers(sd):
+    """Changed in place, as clipping does, it does not stand in a retained graph's way."""
+    v = inputs()
+    x = v["logits"].requires_grad_(True)
+    loss = sd.distill_loss(**v).sum()
+    for _ in range(3):
+        g, = torch.autograd.grad(loss, x, retain_graph=True)
+        g.mul_(2.0)
+    for _ in range(3):
+        loss.backward(retain_graph=True)
+        x.grad.mul_(2.0)
+    with torch.no_grad():
+        v["weight"].add_(1.0)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()

@@ -110,3 +110,51 @@ def test_rows_of_weight_0_under_any_gradient(sd):
     for _ in range(3):
         g, = torch.autograd.grad(loss, t, d, retain_graph=True)
         assert torch.equal(g, want) and (g[0, 1] == 0).all() and (g[1, 2] == 0).all()
+
+
+@pytest.mark.parametrize("of_weights", [False, True])
+def test_offloaded_and_checkpointed(sd, of_weights):
+    """Saved tensors that go to the host and back, or are made again, give the same gradients."""
+    from torch.utils.checkpoint import checkpoint
+    x, record = case(36)
+    ids, z, lse = (cuda(a) for a in record)
+    d = floats([[1.0, 3.0, 0.0], [0.5, 1.0, -2.0]])
+
+    def leaves():
+        a = on_gpu(x, "f32").requires_grad_(True)
+        return (a, floats(W).requires_grad_(of_weights))
+
+    def step(a, w):
+        return sd.distill_loss(a * 1.5, ids, z, lse, w)
+
+    def gradients(loss, of, times=2):
+        of = of if of_weights else of[:1]
+        return [torch.autograd.grad(loss, of, d, retain_graph=i + 1 < times) for i in range(times)]
+
+    of = leaves()
+    want = gradients(step(*of), of)
+    of = leaves()
+    with torch.autograd.graph.save_on_cpu(pin_memory=True):
+        loss = step(*of)
+    off = gradients(loss, of)
+    of = leaves()
+    made = gradients(checkpoint(step, *of, use_reentrant=False), of, 1)
+    for got in (off, made):
+        for g, v in zip(got, want):
+            assert all(torch.equal(a, b) for a, b in zip(g, v))
+
+
+def test_gradients_that_are_changed_in_place(sd):
+    x, record = case(37)
+    ids, z, lse = (cuda(a) for a in record)
+    t = on_gpu(x, "f32").requires_grad_(True)
+    plain = sd.distill(t.detach(), ids, z, lse)
+    loss = sd.distill_loss(t, ids, z, lse).sum()
+    for _ in range(3):
+        g, = torch.autograd.grad(loss, t, retain_graph=True)
+        assert torch.equal(g, plain.grad)
+        g.zero_()
+    loss.backward(retain_graph=True)
+    t.grad.mul_(0.5)
+    loss.backward()
+    assert torch.equal(t.grad, plain.grad * 0.5 + plain.grad)
