@@ -615,9 +615,12 @@ int specdec_attend(const void *q, const void *k_new, const void *v_new, int dtyp
  * takes the first kept token, by index, with
  *     sum of w over the kept tokens up to it  >  uniforms[b, r, d] * sum over all kept,
  * the convention of the verify calls' final draw.  Several draws of a row are the i.i.d.
- * children of a tree node.  Weights carry about 2^-35 of themselves, to 2^-42 of the
- * largest, and their sums are exact: cuts and draws are those of 64-bit floating point but
- * for borders nearer than about 1e-10 of the mass, and no order of the work shows in them.
+ * children of a tree node.  Weights are whole multiples of 2^-42 of the largest, good to
+ * 2^-43 of it and about 2^-35 of themselves, and their sums are exact: cuts and draws are
+ * those of 64-bit floating point but for borders nearer than 2^-34 of the mass and V * 2^-43
+ * of the largest weight (1.5e-8 for 128256 tokens), and no order of the work shows in them.
+ * Tokens below 2^-43 of the largest (some 30 T under it) are kept where a filter keeps them,
+ * and never drawn.
  *
  *   logits      [B, R, V], float32 or bfloat16 (dtype)
  *   temperature float32 [B]: 0 or in [2^-20, 2^20]

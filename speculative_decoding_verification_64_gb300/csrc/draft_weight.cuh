@@ -1,6 +1,8 @@
-// Weights exp((l - M) / T) exact enough that sums over a whole vocabulary name the same
-// token as sums in 64-bit floating point do: each weight is a whole number of 2^-42 of the
-// largest one, good to about 2^-35 of itself, and sums of them are exact, in any order.
+// Weights exp((l - M) / T) for sums over a whole vocabulary that name a token: each weight is
+// a whole number of 2^-42 of the largest one, good to 2^-43 of that and about 2^-35 of itself, and
+// sums of them are exact, in any order.  A sum is that of 64-bit floating point to 2^-35 of
+// itself and 2^-43 a token; the latter shows where a long tail of tokens stands some 30 T below
+// the largest (each counts as 0 or as 2^-42): 1.5e-8 for 128256 tokens, 2^-24 for 2^19.
 //
 // With c = log2(e) / T as a pair of floats, x = (l - M) c is cut at the nearest multiple of
 // 2^-10: 2^x = 2^n 2^(j/1024) 2^f with |f| <= 2^-11.  2^(j/1024) comes from a table of

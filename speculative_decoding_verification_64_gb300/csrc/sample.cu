@@ -22,7 +22,7 @@
 //   * The draws of such rows: the passes leave the kept mass of every run of 32 to 128 vectors;
 //     a draw looks its run up, and a warp weighs that run once more.
 // Which token is cut last, or drawn, turns on sums over the vocabulary: weights and sums are
-// those of draft_weight.cuh, as good as 64-bit floating point for this.  The cluster's
+// those of draft_weight.cuh, in integers that no order of additions changes.  The cluster's
 // CTAs exchange a record of a few words at each step.
 //
 // What bounds it: the chain of passes over the share and of exchanges, two CTAs an SM, and
