@@ -15,6 +15,7 @@ import os
 from typing import Optional
 
 import torch
+from torch.autograd.forward_ad import unpack_dual
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libspecdec.so")
@@ -1206,27 +1207,31 @@ def distill_loss(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor,
     row's divergence, for which rows of weight 0 are looked at too where the weights require
     one.  A malformed row's loss and gradients are NaN.  The teacher is a constant: a ``teacher``
     or ``lse`` that requires a gradient is refused, and so are tangents (forward mode)."""
-    learn = torch.is_grad_enabled()
-    if learn:
+    if torch.is_grad_enabled():
         for name, t in (("teacher", teacher), ("lse", lse)):
             if t is not None and t.requires_grad:
                 raise ValueError(f"distill_loss has no gradient for {name}: pass {name}.detach()")
+    learn = torch.is_grad_enabled() and (logits.requires_grad or
+                                         (weight is not None and weight.requires_grad))
     with _on(stream):
-        return _Distill.apply(logits, ids, teacher, lse, weight, temperature, learn)
+        # (torch refuses tangents there, where no form of them is defined)
+        if learn or any(t is not None and unpack_dual(t).tangent is not None
+                        for t in (logits, teacher, lse, weight)):
+            return _Distill.apply(logits, ids, teacher, lse, weight, temperature)
+        loss = distill(logits, ids, teacher, lse, weight, temperature, grad=False).loss
+        return loss if weight is None else loss * weight
 
 
 class _Distill(torch.autograd.Function):
     """``distill`` under autograd.  The first backward turns the forward's gradient into its
     own, in place; a second one (over a retained graph) makes it anew.  It is saved like the inputs,
-    so that hooks on saved tensors (offloading, checkpoints) have it too.  Calls without a gradient
-    to make come through here too: torch refuses tangents where no form of them is defined."""
+    so that hooks on saved tensors (offloading, checkpoints) have it too."""
 
     @staticmethod
-    def forward(ctx, logits, ids, teacher, lse, weight, temperature, learn):
-        r = distill(logits, ids, teacher, lse, weight, temperature,
-                    grad=learn and ctx.needs_input_grad[0])
+    def forward(ctx, logits, ids, teacher, lse, weight, temperature):
+        r = distill(logits, ids, teacher, lse, weight, temperature, grad=ctx.needs_input_grad[0])
         loss = None
-        if learn and ctx.needs_input_grad[4]:  # the rows of weight 0 have theirs too
+        if ctx.needs_input_grad[4]:  # the rows of weight 0 have theirs too
             alone = (weight == 0).float()
             loss = r.loss + distill(logits, ids, teacher, lse, alone, temperature, grad=False).loss
         ctx.save_for_backward(logits, ids, teacher, lse, weight, loss, r.grad)
@@ -1248,7 +1253,7 @@ class _Distill(torch.autograd.Function):
             ctx.spent = True
             _distill_backward(logits, ids, teacher, lse, weight, ctx.temperature, dloss, grad)
             grad = grad.data  # (the caller's: what becomes of it is no change of a saved tensor)
-        return grad, None, None, None, dweight, None, None
+        return grad, None, None, None, dweight, None
 
 
 def _distill_backward(logits, ids, teacher, lse, weight, temperature, dloss, grad):
