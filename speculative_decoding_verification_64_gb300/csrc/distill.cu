@@ -19,9 +19,9 @@
 // floating point; with them the kernel took 1790 us in place of 434), and the last few steps of
 // a row are 64-bit.
 //
-// Measured: 4096 rows of 128256 bfloat16, 64 entries, gradient out: 446 us, 4.7 TB/s, 70 % of the
-// measured copy rate; 4080 rows of 32003 bfloat16: 99 us, 69 %; 508 rows of 152064 float32: 144 us,
-// 64 %; 33 rows of 32000 float32: 10.3 us.  Of a CTA's 23000 clocks (three an SM) its share's
+// Measured: 4096 rows of 128256 bfloat16, 64 entries, gradient out: 449 us, 4.7 TB/s, 70 % of the
+// measured copy rate, the loss alone 293; 4080 rows of 32003 bfloat16: 99 us, 70 %; 508 rows of
+// 152064 float32: 144 us, 64 %; 33 rows of 32000 float32: 10.3 us.  Of a CTA's 23000 clocks (three an SM) its share's
 // arrival takes 7600, the sum 3300, the exchange 3000, the loss 2200, the gradient 5000: the
 // chain of those steps, which three CTAs overlap in part, is what keeps it from the copy rate.
 // Records that complete on an mbarrier, in place of the cluster's barrier: 1 % less, and 1 us more for

@@ -553,12 +553,14 @@ __device__ __forceinline__ void store_like(const Share &s, uint8_t *row, int v, 
 // an SM (`per_sm`, which hides one CTA's waits behind another's work), more where the rows
 // leave SMs idle, none with less than 4 KB to do.  Measured with shares other than the
 // callers' (rows of 128256 bfloat16, us):
-//   sampling, 4 CTAs a row and 2 an SM: 140 / 207 / 849 for 256 rows under top-p, 672 rows
-//     without a filter, 2304 flat rows under top-p; 6 and 3: 162 / 195 / 977; 8 and 3: 216 /
-//     222 / 1461 (every CTA of a row has the same exchanges to wait for), all by the histogram
+//   sampling, 4 CTAs a row and 2 an SM: 122 / 207 / 560 for 256 rows under top-p, 672 rows
+//     without a filter, 2304 flat rows under top-p; 6 and 3: 163 / 252 / 821; 8 and 3: 151 /
+//     240 / 819 (every CTA of a row has the same exchanges to wait for, and fewer registers).
+//     float32, 256 rows under top-p and without a filter, 8 and 2: 218 / 115; 12 and 3: 340 /
+//     142; 16 and 3: 440 / 149
 //   distillation (before its loss was held in pairs), 4 a row and 3 an SM: 434 for 4096 rows;
-//     5, 6 and 8 a row with 4 to 5 an SM: 463 to 500.  508 rows of 152064 float32: 138 with 10 a row and 3 an SM, 154 with 8
-//     and 2, 152 with 12 and 4, 208 with 16 and 5.
+//     5, 6 and 8 a row with 4 to 5 an SM: 463 to 500.  508 rows of 152064 float32: 138 with 10 a
+//     row and 3 an SM, 154 with 8 and 2, 152 with 12 and 4, 208 with 16 and 5
 inline int cluster_for(long long rows, int V, int elem_bytes, int share_bytes, int per_sm) {
   int c = 1;
   while (c < kMaxCluster && (long long)V * elem_bytes > (long long)c * share_bytes)

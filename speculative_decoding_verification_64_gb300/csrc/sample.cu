@@ -15,10 +15,11 @@
 //     thousand values), each value is weighed once, and sums over the values name the one that
 //     top-p cuts, and how many of its tokens stay.
 //   * Float32, and bfloat16 rows of other magnitudes: a histogram of the logits, 1/64 octave of
-//     weight a bin, says about where the cut is.  A pass adds the weights of all places above a bracket around it, and
-//     in it; when the cut is inside and the bracket's tokens fit a list, they are sorted and
-//     the cut is found among them.  A bracket that missed is placed anew by what the pass
-//     found, and where that fails, between the places known to hold the cut, halves of them.
+//     weight a bin, says about where the cut is.  A pass adds the weights of all places above a
+//     bracket around it, and in it; when the cut is inside and the bracket's tokens fit a list,
+//     they are sorted and the cut is found among them.  A bracket that missed is placed anew by
+//     what the pass found, and where that fails, between the places known to hold the cut, halves
+//     of them.
 //   * The draws of such rows: the passes leave the kept mass of every run of 32 to 128 vectors;
 //     a draw looks its run up, and a warp weighs that run once more.
 // Which token is cut last, or drawn, turns on sums over the vocabulary: weights and sums are
@@ -36,9 +37,9 @@
 //   256 rows, top-p 0.9, a draw and probabilities: 122 us (four waves of CTAs, the last a third
 //     full; by the histogram 131).  One row of 32000 float32 under top-k 40 and top-p: 14 us, a
 //     chain of exchanges and barriers (and of instructions that are not cached yet).
-// With threads of 512 a CTA 324 and 263 us in the place of 206 and 139: the kernel's code is
-// larger than the instruction cache's near levels, so that more warps in different places
-// cost more than they hide.
+// With 512 threads a CTA 654, 226 and 133 us in their place: 64 registers a thread, some of them
+// spilled, and the kernel's code is larger than the instruction cache's near levels, so that more
+// warps in different places cost more than they hide.
 #include "draft_weight.cuh"
 
 namespace specdec {
@@ -46,17 +47,23 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kList = 1024;   // tokens that rank 0 can sort
+// Tokens that rank 0 can sort.  Of G groups' maxima the k-th largest lets some -G ln(1 - k / G)
+// tokens through: more than this from k = 650 for G = 1024, from 800 for 2048, and a cluster of 3
+// has 768 groups, which bound no larger k.  Halving passes follow there (top-k 500, 640, 768, 800 and
+// 1000: 64 rows of 102400 bfloat16, three CTAs each, 56, 80, 105, 335 and 568 us; 256 rows of 128256,
+// four CTAs, 180, 221, 257, 321 and 796).
+constexpr int kList = 1024;
 constexpr int kMine = 1024;   // tokens that a CTA can bring
 constexpr int kFewK = 128;    // top-k up to which some 500 groups name the bound
 constexpr int kKeys = 4096;   // groups' maxima (256 of each of 16 CTAs)
 // The histogram's bins of a factor of two in weight, and its 24 octaves: a row's tail below
 // 2^-24 of its largest weight is 3 % of the mass at most for 2^19 tokens, and the exact pass
-// corrects the guess by what it found.  256 bfloat16 rows under top-p, 2304 flat ones, when
-// those came this way: 134 and 817 us; with 128 bins an octave 140 and 849 (twice the bins to
-// read from the other CTAs), with 32 131 and 808, where flat rows of float32 bring brackets of
-// twice the tokens.  With 16 octaves 206 us for the 256 rows: their tails' mass is missed, and
-// a second bracket placed.
+// corrects the guess by what it found.  Float32 rows of 128256 under top-p, of few large tokens
+// (256, top-p 0.9), flat (576, 0.95 and min-p at T = 0.7) and flatter (256, 0.9 at T = 1): 218, 378 and
+// 1051 us; with 32 bins an octave 206, 351 and 1060, with 128 260, 468 (twice the bins to read
+// from the other CTAs) and 382 (the flattest rows' brackets fit the list then, where halving passes
+// follow with fewer).  With 16 octaves 320, 358 and 1020: tails' mass is missed, and a second
+// bracket placed.
 constexpr float kOctave = 64.0f;
 constexpr int kBins = 24 * 64;
 // A bracket reaches to either side of the place that the histogram names by this share of
@@ -498,7 +505,10 @@ __device__ __forceinline__ void place_bracket(float want, bool share, int size, 
 
 // Counts of the CTA's tokens by value (bfloat16); tokens of other magnitudes are counted in
 // places that nobody reads (no branch a token: 556 us for the 2304 rows, with one 648), and those
-// that weigh anything go on the list.
+// that weigh anything go on the list.  Those are looked at one by one, -infinity among them: 576 flat
+// rows of 128256 under top-p 0.95 take 228 us, half masked 460, masked but for 1000 tokens 336, and
+// rows of nothing but zeros, all of which are noted by one counter before the histogram has its
+// turn, 10.9 ms.
 __device__ __forceinline__ void count_values(const Share &s, const uint8_t *buf, float least,
                                              SampleSmem &sm) {
   for (int i = threadIdx.x; i < 2 * kMags; i += kThreads) sm.val[i] = 0;
